@@ -19,3 +19,8 @@ from ._lib import (  # noqa: F401
     mcc1d_selftest_wait, Mcc1dFwdTensors, fwd_tensors, mcc1d_fwd_ex, mcc1d_fwd_ex_workspace_size,
     PLAN_SMS, mcc1d_check_sm_count, mcc1d_device_sm_count,
 )
+from ._ssm import (  # noqa: F401
+    ScanArgs, ScanBwdArgs, ScanStepArgs, SelectiveScanGrads, ShortConvArgs, ShortConvBwdArgs, ShortConvGrads,
+    ShortConvStepArgs, selective_scan, selective_scan_backward, selective_scan_step, short_conv,
+    short_conv_backward, short_conv_step,
+)

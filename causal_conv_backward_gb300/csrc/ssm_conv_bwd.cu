@@ -1,0 +1,299 @@
+// ssm_conv_bwd.cu - gradients of the short convolution.
+//
+//   dpre(t)   = grad_y(t) d/dpre [pre sigmoid(pre)],   zero past the length
+//   grad_x(t) = sum over j of weight(W-1-j) dpre(t+j)  (+ grad_final_state)
+//   grad_weight(k) = sum over b, t of dpre(t) x(t-W+1+k),  grad_bias = sum of dpre
+//
+// pre is computed again from x rather than kept by the forward: that costs W
+// multiply-adds and saves the 2 bytes per element its copy would be read with.
+// A warp owns 32 V channels of one sequence and walks L rows, and W-1 more for
+// the look-ahead of grad_x, with the last W-1 rows of x and dpre in registers.
+// The weight sums stay in registers over the L rows, are added over the
+// block's 8 warps in shared memory and over blocks by a second kernel, each in
+// a fixed order: nothing depends on scheduling.
+#include "plan.h"
+#include "ssm.h"
+#include "ssm_common.cuh"
+
+namespace mcc1d {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kRows = 4;    // rows in flight per thread
+
+struct ConvBwdParams {
+    const uint16_t *gy, *x, *weight, *bias, *state, *gfs;
+    const int32_t *lengths;
+    uint16_t *gx, *gstate;
+    float *partial;
+    int64_t gs, gb, xs, xb, S, B, H, vecs, supers;
+    int32_t L, silu;
+};
+
+template <int DT, int V, int W>
+__global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvBwdParams p)
+{
+    constexpr int P = Vec<V>::P;
+    constexpr int Wm = W > 1 ? W - 1 : 1;
+    __shared__ float2 red[kWarps][W + 1][32][P];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t vec = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t part = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (part >= p.B * p.supers)
+        return;
+    const int64_t b = part / p.supers, super = part - b * p.supers;
+    const bool on = vec < p.vecs;
+    const int64_t h = on ? vec * V : 0;
+    const int64_t t0 = (super * kWarps + warp) * p.L;
+    const int64_t t1 = t0 + p.L < p.S ? t0 + p.L : p.S;
+
+    float2 aw[W + 1][P];    // grad_weight rows, then grad_bias
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+            aw[k][e] = make_float2(0.f, 0.f);
+
+    if (on && t0 < p.S) {
+        const int64_t len = clamped_length(p.lengths, b, p.S);
+        const uint16_t *x = p.x + b * p.xb + h, *gy = p.gy + b * p.gb + h;
+        const uint16_t *state = p.state ? p.state + b * (W - 1) * p.H + h : nullptr;
+        uint16_t *gx = p.gx + b * p.H + h;
+        const int64_t ys = p.B * p.H;
+        float2 w[W][P], bias[P], xw[Wm][P], dw[Wm][P];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const Vec<V> r = vload<V>(p.weight + k * p.H + h);
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                w[k][e] = unpack2<DT>(r.u[e]);
+        }
+        const Vec<V> rb = p.bias ? vload<V>(p.bias + h) : vzero<V>();
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+            bias[e] = unpack2<DT>(rb.u[e]);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int64_t t = t0 - (W - 1) + i;
+            Vec<V> r = vzero<V>();
+            if (t >= 0) {
+                if (t < len)
+                    r = vload<V>(x + t * p.xs);
+            } else if (state) {
+                r = vload<V>(state + (t + W - 1) * p.H);
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                xw[i][e] = unpack2<DT>(r.u[e]);
+                dw[i][e] = make_float2(0.f, 0.f);
+            }
+        }
+        // row r gives dpre(r) and, W-1 rows later than its own, grad_x(r-W+1)
+        const int64_t rend = t1 + W - 1;
+        const int64_t live = rend < len ? rend : len;
+        const int64_t first = t0 == 0 ? -(int64_t)(W - 1) : t0;   // first row of grad_x (below 0: the window's)
+        for (int64_t r0 = t0; r0 < rend; r0 += kRows) {
+            Vec<V> rx[kRows], rg[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const bool ok = r0 + i < live;
+                rx[i] = ok ? vload<V>(x + (r0 + i) * p.xs) : vzero<V>();
+                rg[i] = ok ? vload<V>(gy + (r0 + i) * p.gs) : vzero<V>();
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int64_t r = r0 + i, t = r - (W - 1);
+                const bool own = r < t1;
+                Vec<V> out;
+                Vec<V> fs = vzero<V>();
+                if (p.gfs && t >= len - (W - 1) && t < len && r < rend)
+                    fs = vload<V>(p.gfs + (b * (W - 1) + (t - (len - (W - 1)))) * p.H + h);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const float2 v = unpack2<DT>(rx[i].u[e]);
+                    float2 d = unpack2<DT>(rg[i].u[e]);
+                    if (p.silu) {
+                        float2 s = bias[e];
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k)
+                            s = fma2(w[k][e], xw[k][e], s);
+                        s = fma2(w[W - 1][e], v, s);
+                        const float sx = sigmoid(s.x), sy = sigmoid(s.y);
+                        d.x *= sx * fmaf(s.x, 1.f - sx, 1.f);
+                        d.y *= sy * fmaf(s.y, 1.f - sy, 1.f);
+                        if (r >= live)
+                            d = make_float2(0.f, 0.f);   // an infinite pre leaves nothing behind
+                    }
+                    if (own) {
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k)
+                            aw[k][e] = fma2(d, xw[k][e], aw[k][e]);
+                        aw[W - 1][e] = fma2(d, v, aw[W - 1][e]);
+                        aw[W][e] = add2(aw[W][e], d);
+                    }
+                    float2 g = unpack2<DT>(fs.u[e]);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+                        g = fma2(w[W - 1 - j][e], dw[j][e], g);
+                    g = fma2(w[0][e], d, g);
+                    out.u[e] = pack2<DT>(g);
+#pragma unroll
+                    for (int k = 0; k < W - 2; ++k) {
+                        xw[k][e] = xw[k + 1][e];
+                        dw[k][e] = dw[k + 1][e];
+                    }
+                    if (W > 1) {
+                        xw[W > 1 ? W - 2 : 0][e] = v;
+                        dw[W > 1 ? W - 2 : 0][e] = d;
+                    }
+                }
+                if (t >= first && t < t1) {
+                    if (t >= 0)
+                        vstore<V>(gx + t * ys, out);
+                    else if (p.gstate)
+                        vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+            red[warp][k][lane][e] = aw[k][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < (W + 1) * 32; i += kWarps * 32) {
+        const int k = i / 32, l = i & 31;
+        const int64_t v2 = (int64_t)blockIdx.x * 32 + l;
+        if (v2 >= p.vecs)
+            continue;
+        float *out = p.partial + (part * (W + 1) + k) * p.H + v2 * V;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            float2 s = red[0][k][l][e];
+#pragma unroll
+            for (int q = 1; q < kWarps; ++q)
+                s = add2(s, red[q][k][l][e]);
+            out[2 * e] = s.x;
+            if (V > 1)
+                out[2 * e + 1] = s.y;
+        }
+    }
+}
+
+// Sums column i of the [parts][cols] partials: 8 strided runs of parts, then
+// the runs in order.
+template <int DT>
+__global__ void __launch_bounds__(256) mcc1d_ssm_conv_bwd_sum(const float *partial, int64_t parts, int64_t cols,
+                                                             int64_t wcols, uint16_t *gw, uint16_t *gbias)
+{
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (i < cols)
+        for (int64_t r = q; r < parts; r += 8)
+            s += partial[r * cols + i];
+    red[q][lane] = s;
+    __syncthreads();
+    if (q == 0 && i < cols) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+            s += red[k][lane];
+        const uint16_t v = (uint16_t)pack2<DT>(make_float2(s, 0.f));
+        if (i < wcols)
+            gw[i] = v;
+        else if (gbias)
+            gbias[i - wcols] = v;
+    }
+}
+
+template <int DT>
+int32_t run_bwd(const ConvBwdParams &p, int V, int W, dim3 grid, cudaStream_t s)
+{
+    switch (W) {
+#define MCC1D_CASE(w)                                                              \
+    case w:                                                                        \
+        if (V == 1)                                                                \
+            mcc1d_ssm_conv_bwd<DT, 1, w><<<grid, kWarps * 32, 0, s>>>(p);          \
+        else                                                                       \
+            mcc1d_ssm_conv_bwd<DT, conv_vec(w), w><<<grid, kWarps * 32, 0, s>>>(p); \
+        break;
+        MCC1D_CASE(1) MCC1D_CASE(2) MCC1D_CASE(3) MCC1D_CASE(4)
+        MCC1D_CASE(5) MCC1D_CASE(6) MCC1D_CASE(7) MCC1D_CASE(8)
+#undef MCC1D_CASE
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+int bwd_vec(const mcc1d_short_conv_bwd_args &a)
+{
+    const int V = conv_vec((int)a.W);
+    const uintptr_t any = (uintptr_t)a.grad_y | (uintptr_t)a.x | (uintptr_t)a.weight | (uintptr_t)a.bias |
+                          (uintptr_t)a.state | (uintptr_t)a.grad_final_state | (uintptr_t)a.grad_x |
+                          (uintptr_t)a.grad_state;
+    const int64_t steps = a.H | a.grad_y_strides[0] | a.grad_y_strides[1] | a.x_strides[0] | a.x_strides[1];
+    return (any & (uintptr_t)(2 * V - 1)) == 0 && (steps & (V - 1)) == 0 ? V : 1;
+}
+
+}  // namespace
+
+ConvBwdPlan conv_bwd_plan(const mcc1d_short_conv_bwd_args &a)
+{
+    ConvBwdPlan p;
+    // 64 rows per warp re-read W-1 in 64; fewer where that leaves SMs idle
+    const int64_t wide = (a.H + 127) / 128 * a.B;
+    int64_t L = 64;
+    while (L > 8 && wide * ((a.S + 8 * L - 1) / (8 * L)) < 152 * 2)
+        L /= 2;
+    p.L = (int32_t)L;
+    p.supers = (a.S + kWarps * L - 1) / (kWarps * L);
+    p.parts = a.B * p.supers;
+    p.bytes = (uint64_t)p.parts * (uint64_t)((a.W + 1) * a.H) * 4u;
+    return p;
+}
+
+int32_t launch_short_conv_bwd(const mcc1d_short_conv_bwd_args &a, void *workspace, cudaStream_t stream)
+{
+    const ConvBwdPlan plan = conv_bwd_plan(a);
+    ConvBwdParams p;
+    p.gy = (const uint16_t *)a.grad_y;
+    p.x = (const uint16_t *)a.x;
+    p.weight = (const uint16_t *)a.weight;
+    p.bias = (const uint16_t *)a.bias;
+    p.state = (const uint16_t *)a.state;
+    p.gfs = (const uint16_t *)a.grad_final_state;
+    p.lengths = a.lengths;
+    p.gx = (uint16_t *)a.grad_x;
+    p.gstate = (uint16_t *)a.grad_state;
+    p.partial = (float *)workspace;
+    p.gs = a.grad_y_strides[0];
+    p.gb = a.grad_y_strides[1];
+    p.xs = a.x_strides[0];
+    p.xb = a.x_strides[1];
+    p.S = a.S;
+    p.B = a.B;
+    p.H = a.H;
+    p.supers = plan.supers;
+    p.L = plan.L;
+    p.silu = (a.flags & MCC1D_SILU) != 0;
+    const int V = bwd_vec(a);
+    p.vecs = a.H / V;
+    const int64_t gy = plan.parts < 32768 ? plan.parts : 32768;
+    const dim3 grid((unsigned)((p.vecs + 31) / 32), (unsigned)gy, (unsigned)((plan.parts + gy - 1) / gy));
+    const int32_t st = a.dtype == 0 ? run_bwd<0>(p, V, (int)a.W, grid, stream) : run_bwd<1>(p, V, (int)a.W, grid, stream);
+    if (st != kOk)
+        return st;
+    const int64_t cols = (a.W + 1) * a.H;
+    const unsigned blocks = (unsigned)((cols + 31) / 32);
+    if (a.dtype == 0)
+        mcc1d_ssm_conv_bwd_sum<0><<<blocks, 256, 0, stream>>>(p.partial, plan.parts, cols, a.W * a.H,
+                                                            (uint16_t *)a.grad_weight, (uint16_t *)a.grad_bias);
+    else
+        mcc1d_ssm_conv_bwd_sum<1><<<blocks, 256, 0, stream>>>(p.partial, plan.parts, cols, a.W * a.H,
+                                                            (uint16_t *)a.grad_weight, (uint16_t *)a.grad_bias);
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+}  // namespace mcc1d

@@ -1,0 +1,589 @@
+// ssm_scan.cu - the selective scan over prompts and for single tokens.
+//
+//   h(t)[n] = exp(dt A[n]) h(t-1)[n] + dt u B(t)[n],  y(t) = (C(t).h(t) + D u) z sigmoid(z)
+//
+// The call moves 8 bytes per (token, channel) and computes, for each of its N
+// states, one exponential and four multiply-adds: at N = 16 the special
+// function and fp32 pipes need more time than memory does, so the design
+// spends as few other instructions per state as it can. A channel's states
+// sit four to a lane (ssm_scan.cuh): enough warps for a few thousand channels
+// without cutting the sequence, and one shuffle-reduced sum per channel and
+// token.
+//
+// Where sequences and channels are too few to fill the machine the time axis
+// is cut into chunks: each chunk's state from a zero start and its sum of dt
+// (which fixes its decay exp(A sum dt)) are computed, the chunks are joined in
+// order, and the outputs are computed chunk by chunk from the joined states.
+#include "plan.h"
+#include "ssm_scan.cuh"
+
+namespace mcc1d {
+
+namespace {
+
+// What a pass leaves behind: outputs; a chunk's end state; or, for the
+// backward, also the states at tile starts and the gradient that reaches the
+// chunk's start from the outputs inside it.
+enum { kOutputs = 0, kSummary = 1, kSummaryGrad = 2 };
+
+template <int DT, int NL, int MODE>
+__global__ void __launch_bounds__(kScanThreads, 3) mcc1d_ssm_scan(const ScanParams p)
+{
+    using T = ScanTile<NL>;
+    constexpr int NP = T::NP, CB = T::CB, TT = scan_tile_rows(NL, MODE == kSummaryGrad);
+    constexpr int RP = TT / T::RG;
+    constexpr bool kY = MODE == kOutputs, kR = MODE == kSummaryGrad, kC = kY || kR;
+    __shared__ __align__(16) float2 sd[TT][CB];       // dt, dt u; then y in place of dt
+    __shared__ __align__(16) float sB[TT][NP];
+    __shared__ __align__(16) float sC[kC ? TT : 1][NP];
+    __shared__ __align__(16) float sg[kR ? TT : 1][CB];
+
+    const ScanWhere w = scan_where<NL>(p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = lane % NL, n0 = 4 * j;
+    const int cl = warp * T::CW + lane / NL;          // channel of the recurrence, within the block
+    const int64_t te = clamped_length(p.lengths, w.b, p.S);
+    // the thread's two channels and rows of a tile
+    const int pc = 2 * (threadIdx.x % T::CP), pr = threadIdx.x / T::CP;
+    const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
+    const int64_t ch = w.c0 + (on0 ? pc : 0);
+    const uint16_t *u = p.u + w.b * p.ub + ch, *delta = p.delta + w.b * p.db + ch;
+    const uint16_t *z = kC && p.z ? p.z + w.b * p.zb + ch : nullptr;
+    const uint16_t *gy = kR ? p.gy + w.b * p.gb + ch : nullptr;
+    const uint16_t *Bm = p.Bm + w.b * p.Bb + w.g * p.Bg, *Cm = kC ? p.Cm + w.b * p.Cb + w.g * p.Cg : nullptr;
+    const float bias0 = p.dbias && on0 ? p.dbias[ch] : 0.f, bias1 = p.dbias && on1 ? p.dbias[ch + 1] : 0.f;
+    const float D0 = kY && p.D && on0 ? p.D[ch] : 0.f, D1 = kY && p.D && on1 ? p.D[ch + 1] : 0.f;
+
+    // the lane's four states
+    const bool live = cl < w.nc;
+    const int64_t hc = w.c0 + (live ? cl : 0);
+    float2 A2[2], h[2], q[2], R[2];
+    {
+        const float4 a = load_states(p.A + hc * p.N, n0, p.N, p.vecA);
+        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kY) {
+            if (p.chunks > 1)
+                s = *reinterpret_cast<const float4 *>(p.e + ((w.chunk * p.B + w.b) * p.H + hc) * NP + n0);
+            else if (p.h0)
+                s = load_states(p.h0 + (w.b * p.H + hc) * p.N, n0, p.N, p.vecState);
+        }
+        h[0] = make_float2(s.x, s.y);
+        h[1] = make_float2(s.z, s.w);
+        q[0] = q[1] = make_float2(1.f, 1.f);
+        R[0] = R[1] = make_float2(0.f, 0.f);
+    }
+    float dtsum = 0.f;
+
+    uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
+    BcTile<NL, TT> bc;
+    const int64_t tile0 = w.chunk * p.tiles_per_chunk;
+    const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
+    auto load = [&](int64_t tile) {
+        const int64_t t0 = tile * TT;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+            const int64_t t = t0 + pr + r * T::RG;
+            const bool ok = t < te;
+            ru[r] = load_pair(u + t * p.us, ok && on0, ok && on1, p.pairs);
+            rd[r] = load_pair(delta + t * p.ds, ok && on0, ok && on1, p.pairs);
+            rz[r] = z ? load_pair(z + t * p.zs, ok && on0, ok && on1, p.pairs) : 0u;
+            rg[r] = kR ? load_pair(gy + t * p.gs, ok && on0, ok && on1, p.pairs) : 0u;
+        }
+        bc.load(p, Bm, Cm, t0, te);
+    };
+    if (tile0 * TT < te)
+        load(tile0);
+    for (int64_t tile = tile0; tile < tile1; ++tile) {
+        const int64_t t0 = tile * TT;
+        if (t0 >= te) {
+            // past the sequence's end: zeros, and the state stays
+            if (!kY)
+                break;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int64_t t = t0 + pr + r * T::RG;
+                if (t < p.S)
+                    store_pair(p.y + (t * p.B + w.b) * p.H + ch, 0u, on0, on1, p.pairs);
+            }
+            continue;
+        }
+        uint32_t cu[RP], cz[RP];
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+            const int64_t t = t0 + pr + r * T::RG;
+            const float2 uv = unpack2<DT>(ru[r]);
+            float2 dt = unpack2<DT>(rd[r]);
+            dt.x += bias0;
+            dt.y += bias1;
+            if (p.softplus) {
+                dt.x = softplus(dt.x);
+                dt.y = softplus(dt.y);
+            }
+            if (t >= te)
+                dt = make_float2(0.f, 0.f);
+            *reinterpret_cast<float4 *>(&sd[pr + r * T::RG][pc]) = make_float4(dt.x, dt.x * uv.x, dt.y, dt.y * uv.y);
+            if (kR) {
+                float2 g = unpack2<DT>(rg[r]);
+                if (z) {
+                    const float2 zv = unpack2<DT>(rz[r]);
+                    g.x *= zv.x * sigmoid(zv.x);
+                    g.y *= zv.y * sigmoid(zv.y);
+                }
+                *reinterpret_cast<float2 *>(&sg[pr + r * T::RG][pc]) = g;
+            }
+            cu[r] = ru[r];
+            cz[r] = rz[r];
+        }
+        bc.template put<DT>(sB, kC ? sC : nullptr);
+        __syncthreads();
+        if (tile + 1 < tile1 && t0 + TT < te)
+            load(tile + 1);
+        if (kR) {
+            if (live) {
+                const int64_t at = (tile * p.B + w.b) * p.H + hc;
+                *reinterpret_cast<float4 *>(p.cp + at * NP + n0) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+                if (j == 0)
+                    p.cpdt[at] = dtsum;
+            }
+        }
+#pragma unroll 2
+        for (int tb = 0; tb < TT; tb += NL) {
+            float yp[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const float2 dd = sd[tb + i][cl];
+                const float4 bv = *reinterpret_cast<const float4 *>(&sB[tb + i][n0]);
+                const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
+                float2 a0 = mul2(dt2, A2[0]), a1 = mul2(dt2, A2[1]);
+                a0 = make_float2(ex2(a0.x), ex2(a0.y));
+                a1 = make_float2(ex2(a1.x), ex2(a1.y));
+                h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
+                h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
+                if (!kY)
+                    dtsum += dd.x;
+                if (kC) {
+                    const float4 cv = *reinterpret_cast<const float4 *>(&sC[tb + i][n0]);
+                    const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
+                    if (kY) {
+                        const float2 s = fma2(h[0], c0, mul2(h[1], c1));
+                        yp[i] = s.x + s.y;
+                    } else {
+                        const float g = sg[tb + i][cl];
+                        const float2 g2 = make_float2(g, g);
+                        q[0] = mul2(q[0], a0);
+                        q[1] = mul2(q[1], a1);
+                        R[0] = fma2(q[0], mul2(g2, c0), R[0]);
+                        R[1] = fma2(q[1], mul2(g2, c1), R[1]);
+                    }
+                }
+            }
+            if (kY) {
+                lanes_sum<NL, NL>(yp, lane, 1);
+                sd[tb + j][cl].x = yp[0];
+            }
+        }
+        __syncthreads();
+        if (kY) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int64_t t = t0 + pr + r * T::RG;
+                const float4 s = *reinterpret_cast<const float4 *>(&sd[pr + r * T::RG][pc]);
+                const float2 uv = unpack2<DT>(cu[r]);
+                float2 y = make_float2(fmaf(D0, uv.x, s.x), fmaf(D1, uv.y, s.z));
+                if (z) {
+                    const float2 zv = unpack2<DT>(cz[r]);
+                    y.x *= zv.x * sigmoid(zv.x);
+                    y.y *= zv.y * sigmoid(zv.y);
+                }
+                if (t < p.S)
+                    store_pair(p.y + (t * p.B + w.b) * p.H + ch, t < te ? pack2<DT>(y) : 0u, on0, on1, p.pairs);
+            }
+        }
+    }
+    if (!live)
+        return;
+    const float4 out = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (kY) {
+        if (p.hT && w.chunk == p.chunks - 1)
+            store_states(p.hT + (w.b * p.H + hc) * p.N, n0, p.N, p.vecState, out);
+    } else {
+        const int64_t at = (w.chunk * p.B + w.b) * p.H + hc;
+        *reinterpret_cast<float4 *>(p.e + at * NP + n0) = out;
+        if (j == 0)
+            p.dts[at] = dtsum;
+        if (kR)
+            *reinterpret_cast<float4 *>(p.r + at * NP + n0) = make_float4(R[0].x, R[0].y, R[1].x, R[1].y);
+    }
+}
+
+// Joins the chunks: e[c] becomes the state that enters chunk c, r[c] the
+// gradient that enters it from the right. One thread per four states of a
+// channel; a batch of chunks is loaded ahead of the recurrence over them.
+template <bool GRAD>
+__global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, int NL)
+{
+    constexpr int K = 4;
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    const int64_t rows = p.B * p.H;
+    if (i >= rows * NL)
+        return;
+    const int64_t row = i / NL;
+    const int n0 = 4 * (int)(i - row * NL), NP = 4 * NL;
+    const float4 A = load_states(p.A + row % p.H * p.N, n0, p.N, p.vecA);
+    const float a[4] = {A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e};
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.h0)
+        s = load_states(p.h0 + row * p.N, n0, p.N, p.vecState);
+    for (int64_t c0 = 0; c0 < p.chunks; c0 += K) {
+        float4 v[K];
+        float d[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c0 + k < p.chunks) {
+                v[k] = *reinterpret_cast<const float4 *>(p.e + ((c0 + k) * rows + row) * NP + n0);
+                d[k] = p.dts[(c0 + k) * rows + row];
+            }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c0 + k < p.chunks) {
+                *reinterpret_cast<float4 *>(p.e + ((c0 + k) * rows + row) * NP + n0) = s;
+                s.x = fmaf(ex2(a[0] * d[k]), s.x, v[k].x);
+                s.y = fmaf(ex2(a[1] * d[k]), s.y, v[k].y);
+                s.z = fmaf(ex2(a[2] * d[k]), s.z, v[k].z);
+                s.w = fmaf(ex2(a[3] * d[k]), s.w, v[k].w);
+            }
+    }
+    if (!GRAD)
+        return;
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.gfs)
+        s = load_states(p.gfs + row * p.N, n0, p.N, p.vecState);
+    for (int64_t c0 = p.chunks - 1; c0 >= 0; c0 -= K) {
+        float4 v[K];
+        float d[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c0 - k >= 0) {
+                v[k] = *reinterpret_cast<const float4 *>(p.r + ((c0 - k) * rows + row) * NP + n0);
+                d[k] = p.dts[(c0 - k) * rows + row];
+            }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c0 - k >= 0) {
+                *reinterpret_cast<float4 *>(p.r + ((c0 - k) * rows + row) * NP + n0) = s;
+                s.x = fmaf(ex2(a[0] * d[k]), s.x, v[k].x);
+                s.y = fmaf(ex2(a[1] * d[k]), s.y, v[k].y);
+                s.z = fmaf(ex2(a[2] * d[k]), s.z, v[k].z);
+                s.w = fmaf(ex2(a[3] * d[k]), s.w, v[k].w);
+            }
+    }
+    if (p.gstate)
+        store_states(p.gstate + row * p.N, n0, p.N, p.vecState, s);
+}
+
+// One token: a row of states in, moved on by one step, and out.
+struct ScanStepParams {
+    const uint16_t *u, *delta, *z, *Bm, *Cm;
+    const float *A, *D, *dbias;
+    float *state;
+    const int32_t *slots;
+    uint16_t *y;
+    int64_t ub, db, zb, Bb, Bg, Cb, Cg, rows, B, H;
+    int32_t N, Hg, softplus, vecA, vecState;
+};
+
+template <int DT>
+__device__ __forceinline__ float load16(const uint16_t *p)
+{
+    return unpack2<DT>((uint32_t)__ldg(p)).x;
+}
+
+template <int DT, int NL>
+__global__ void __launch_bounds__(kScanThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
+{
+    const int j = threadIdx.x % NL, n0 = 4 * j;
+    const int64_t id = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) / NL;
+    const bool live = id < p.B * p.H;
+    const int64_t b = live ? id / p.H : 0, c = live ? id - b * p.H : 0;
+    const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
+    const bool on = live && slot >= 0 && slot < p.rows;
+    float part[1] = {0.f};
+    float uv = 0.f;
+    if (on) {
+        float *row = p.state + (slot * p.H + c) * p.N;
+        const float4 h = load_states(row, n0, p.N, p.vecState);
+        const float4 A = load_states(p.A + c * p.N, n0, p.N, p.vecA);
+        const int64_t g = c / p.Hg;
+        const uint16_t *B = p.Bm + b * p.Bb + g * p.Bg, *C = p.Cm + b * p.Cb + g * p.Cg;
+        float dt = load16<DT>(p.delta + b * p.db + c) + (p.dbias ? p.dbias[c] : 0.f);
+        if (p.softplus)
+            dt = softplus(dt);
+        uv = load16<DT>(p.u + b * p.ub + c);
+        const float du = dt * uv, dl = dt * kLog2e;
+        float4 o;
+        o.x = fmaf(ex2(dl * A.x), h.x, n0 < p.N ? du * load16<DT>(B + n0) : 0.f);
+        o.y = fmaf(ex2(dl * A.y), h.y, n0 + 1 < p.N ? du * load16<DT>(B + n0 + 1) : 0.f);
+        o.z = fmaf(ex2(dl * A.z), h.z, n0 + 2 < p.N ? du * load16<DT>(B + n0 + 2) : 0.f);
+        o.w = fmaf(ex2(dl * A.w), h.w, n0 + 3 < p.N ? du * load16<DT>(B + n0 + 3) : 0.f);
+        store_states(row, n0, p.N, p.vecState, o);
+        if (n0 < p.N)
+            part[0] = o.x * load16<DT>(C + n0);
+        if (n0 + 1 < p.N)
+            part[0] = fmaf(o.y, load16<DT>(C + n0 + 1), part[0]);
+        if (n0 + 2 < p.N)
+            part[0] = fmaf(o.z, load16<DT>(C + n0 + 2), part[0]);
+        if (n0 + 3 < p.N)
+            part[0] = fmaf(o.w, load16<DT>(C + n0 + 3), part[0]);
+    }
+    lanes_sum<1, NL>(part, threadIdx.x & 31, 1);
+    if (live && j == 0) {
+        float y = 0.f;
+        if (on) {
+            y = p.D ? fmaf(p.D[c], uv, part[0]) : part[0];
+            if (p.z) {
+                const float zv = load16<DT>(p.z + b * p.zb + c);
+                y *= zv * sigmoid(zv);
+            }
+        }
+        p.y[b * p.H + c] = (uint16_t)pack2<DT>(make_float2(y, 0.f));
+    }
+}
+
+bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+template <int DT, int MODE>
+int32_t run_scan(const ScanParams &p, int nl, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(p.blocks * p.B * p.chunks);
+    switch (nl) {
+    case 1: mcc1d_ssm_scan<DT, 1, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 2: mcc1d_ssm_scan<DT, 2, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 4: mcc1d_ssm_scan<DT, 4, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 8: mcc1d_ssm_scan<DT, 8, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
+    default: mcc1d_ssm_scan<DT, 16, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+template <int DT>
+int32_t run_step(const ScanStepParams &p, int nl, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)((p.B * p.H * nl + kScanThreads - 1) / kScanThreads);
+    switch (nl) {
+    case 1: mcc1d_ssm_scan_step<DT, 1><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 2: mcc1d_ssm_scan_step<DT, 2><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 4: mcc1d_ssm_scan_step<DT, 4><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 8: mcc1d_ssm_scan_step<DT, 8><<<grid, kScanThreads, 0, s>>>(p); break;
+    default: mcc1d_ssm_scan_step<DT, 16><<<grid, kScanThreads, 0, s>>>(p); break;
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+uint64_t take(uint64_t &off, uint64_t bytes)
+{
+    const uint64_t at = off;
+    off = (off + bytes + 255u) & ~(uint64_t)255u;
+    return at;
+}
+
+ScanPlan shape_plan(const mcc1d_scan_args &a, bool bwd)
+{
+    ScanPlan p = {};
+    p.nl = 1;
+    while (4 * p.nl < a.N)
+        p.nl *= 2;
+    p.np = 4 * p.nl;
+    p.cb = kScanThreads / p.nl;
+    p.tt = scan_tile_rows(p.nl, bwd);
+    const int64_t Hg = a.H / a.G;
+    p.blocks_per_group = (int32_t)((Hg + p.cb - 1) / p.cb);
+    p.blocks = a.G * p.blocks_per_group;
+    p.tiles = (a.S + p.tt - 1) / p.tt;
+    return p;
+}
+
+void cut(ScanPlan &p, int64_t chunks)
+{
+    if (chunks > p.tiles)
+        chunks = p.tiles;
+    if (chunks < 1)
+        chunks = 1;
+    p.tiles_per_chunk = (p.tiles + chunks - 1) / chunks;
+    p.chunks = (p.tiles + p.tiles_per_chunk - 1) / p.tiles_per_chunk;
+}
+
+}  // namespace
+
+ScanPlan scan_plan(const mcc1d_scan_args &a)
+{
+    ScanPlan p = shape_plan(a, false);
+    // One pass where it fills the machine about half; cutting the time axis
+    // computes the states twice, so it has to bring more than twice the blocks.
+    const int64_t rows = p.blocks * a.B;
+    cut(p, rows >= 152 ? 1 : (152 * 3 + rows - 1) / rows);
+    uint64_t off = 0;
+    const uint64_t ch = (uint64_t)(a.B * a.H);
+    if (p.chunks > 1) {
+        p.off_e = take(off, (uint64_t)p.chunks * ch * p.np * 4);
+        p.off_dt = take(off, (uint64_t)p.chunks * ch * 4);
+    }
+    p.bytes = off;
+    return p;
+}
+
+ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
+{
+    const mcc1d_scan_args &a = ba.fwd;
+    ScanPlan p = shape_plan(a, true);
+    const int64_t rows = p.blocks * a.B;
+    cut(p, (152 * 6 + rows - 1) / rows);
+    uint64_t off = 0;
+    const uint64_t ch = (uint64_t)(a.B * a.H);
+    p.off_e = take(off, (uint64_t)p.chunks * ch * p.np * 4);
+    p.off_r = take(off, (uint64_t)p.chunks * ch * p.np * 4);
+    p.off_dt = take(off, (uint64_t)p.chunks * ch * 4);
+    p.off_cp = take(off, (uint64_t)p.tiles * ch * p.np * 4);
+    p.off_cpdt = take(off, (uint64_t)p.tiles * ch * 4);
+    p.off_ga = take(off, (uint64_t)p.chunks * ch * p.np * 4);
+    p.off_gd = take(off, (uint64_t)p.chunks * ch * 8);
+    p.off_bc = take(off, (uint64_t)(a.S * a.B) * (uint64_t)p.blocks * 2u * p.np * 4);
+    p.bytes = off;
+    return p;
+}
+
+static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint8_t *ws)
+{
+    ScanParams p = {};
+    p.u = (const uint16_t *)a.u;
+    p.delta = (const uint16_t *)a.delta;
+    p.z = (const uint16_t *)a.z;
+    p.Bm = (const uint16_t *)a.B_;
+    p.Cm = (const uint16_t *)a.C;
+    p.A = a.A;
+    p.D = a.D;
+    p.dbias = a.delta_bias;
+    p.h0 = a.state;
+    p.lengths = a.lengths;
+    p.y = (uint16_t *)a.y;
+    p.hT = a.final_state;
+    p.us = a.u_strides[0], p.ub = a.u_strides[1];
+    p.ds = a.delta_strides[0], p.db = a.delta_strides[1];
+    p.zs = a.z ? a.z_strides[0] : 0, p.zb = a.z ? a.z_strides[1] : 0;
+    p.Bs = a.B_strides[0], p.Bb = a.B_strides[1], p.Bg = a.B_strides[2];
+    p.Cs = a.C_strides[0], p.Cb = a.C_strides[1], p.Cg = a.C_strides[2];
+    p.S = a.S;
+    p.B = a.B;
+    p.H = a.H;
+    p.N = (int32_t)a.N;
+    p.G = (int32_t)a.G;
+    p.Hg = (int32_t)(a.H / a.G);
+    p.blocks = pl.blocks;
+    p.blocks_per_group = pl.blocks_per_group;
+    p.tiles = pl.tiles;
+    p.tiles_per_chunk = pl.tiles_per_chunk;
+    p.chunks = pl.chunks;
+    p.softplus = (a.flags & MCC1D_SOFTPLUS) != 0;
+    const uintptr_t any = (uintptr_t)a.u | (uintptr_t)a.delta | (uintptr_t)a.z | (uintptr_t)a.y;
+    const int64_t steps = p.us | p.ub | p.ds | p.db | p.zs | p.zb | a.H | p.Hg;
+    p.pairs = (any & 3u) == 0 && (steps & 1) == 0;
+    const uintptr_t bca = (uintptr_t)a.B_ | (uintptr_t)a.C;
+    const int64_t bcs = p.Bs | p.Bb | p.Bg | p.Cs | p.Cb | p.Cg | a.N;
+    p.bcpairs = (bca & 3u) == 0 && (bcs & 1) == 0;
+    p.vecA = a.N % 4 == 0 && aligned(a.A, 16);
+    p.vecState = a.N % 4 == 0 && aligned(a.state, 16) && aligned(a.final_state, 16);
+    p.e = (float *)(ws + pl.off_e);
+    p.r = (float *)(ws + pl.off_r);
+    p.dts = (float *)(ws + pl.off_dt);
+    p.cp = (float *)(ws + pl.off_cp);
+    p.cpdt = (float *)(ws + pl.off_cpdt);
+    p.ga = (float *)(ws + pl.off_ga);
+    p.gd = (float *)(ws + pl.off_gd);
+    p.bc = (float *)(ws + pl.off_bc);
+    return p;
+}
+
+static int32_t join(const ScanParams &p, int nl, bool grad, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)((p.B * p.H * nl + 127) / 128);
+    if (grad)
+        mcc1d_ssm_scan_join<true><<<grid, 128, 0, s>>>(p, nl);
+    else
+        mcc1d_ssm_scan_join<false><<<grid, 128, 0, s>>>(p, nl);
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+int32_t launch_scan(const mcc1d_scan_args &a, const ScanPlan &pl, void *workspace, cudaStream_t stream)
+{
+    const ScanParams p = scan_params(a, pl, (uint8_t *)workspace);
+    if (p.chunks > 1) {
+        int32_t st = a.dtype == 0 ? run_scan<0, kSummary>(p, pl.nl, stream) : run_scan<1, kSummary>(p, pl.nl, stream);
+        if (st == kOk)
+            st = join(p, pl.nl, false, stream);
+        if (st != kOk)
+            return st;
+    }
+    return a.dtype == 0 ? run_scan<0, kOutputs>(p, pl.nl, stream) : run_scan<1, kOutputs>(p, pl.nl, stream);
+}
+
+int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *workspace, cudaStream_t stream)
+{
+    ScanParams p = scan_params(a.fwd, pl, (uint8_t *)workspace);
+    p.gy = (const uint16_t *)a.grad_y;
+    p.gs = a.grad_y_strides[0];
+    p.gb = a.grad_y_strides[1];
+    p.gfs = a.grad_final_state;
+    p.gu = (uint16_t *)a.grad_u;
+    p.gdelta = (uint16_t *)a.grad_delta;
+    p.gz = (uint16_t *)a.grad_z;
+    p.gstate = a.grad_state;
+    const uintptr_t any = (uintptr_t)a.grad_y | (uintptr_t)a.grad_u | (uintptr_t)a.grad_delta | (uintptr_t)a.grad_z |
+                          (uintptr_t)a.fwd.u | (uintptr_t)a.fwd.delta | (uintptr_t)a.fwd.z;
+    const int64_t steps = p.us | p.ub | p.ds | p.db | p.zs | p.zb | p.gs | p.gb | p.H | p.Hg;
+    p.pairs = (any & 3u) == 0 && (steps & 1) == 0;
+    p.vecState = a.fwd.N % 4 == 0 && aligned(a.fwd.state, 16) && aligned(a.grad_final_state, 16) &&
+                 aligned(a.grad_state, 16);
+    int32_t st = a.fwd.dtype == 0 ? run_scan<0, kSummaryGrad>(p, pl.nl, stream)
+                                  : run_scan<1, kSummaryGrad>(p, pl.nl, stream);
+    if (st == kOk)
+        st = join(p, pl.nl, true, stream);
+    if (st != kOk)
+        return st;
+    return launch_scan_bwd_main(p, pl, a, stream);
+}
+
+int32_t launch_scan_step(const mcc1d_scan_step_args &a, cudaStream_t stream)
+{
+    ScanStepParams p;
+    p.u = (const uint16_t *)a.u;
+    p.delta = (const uint16_t *)a.delta;
+    p.z = (const uint16_t *)a.z;
+    p.Bm = (const uint16_t *)a.B_;
+    p.Cm = (const uint16_t *)a.C;
+    p.A = a.A;
+    p.D = a.D;
+    p.dbias = a.delta_bias;
+    p.state = a.state;
+    p.slots = a.slots;
+    p.y = (uint16_t *)a.y;
+    p.ub = a.u_stride;
+    p.db = a.delta_stride;
+    p.zb = a.z_stride;
+    p.Bb = a.B_strides[0], p.Bg = a.B_strides[1];
+    p.Cb = a.C_strides[0], p.Cg = a.C_strides[1];
+    p.rows = a.cache_rows;
+    p.B = a.B;
+    p.H = a.H;
+    p.N = (int32_t)a.N;
+    p.Hg = (int32_t)(a.H / a.G);
+    p.softplus = (a.flags & MCC1D_SOFTPLUS) != 0;
+    p.vecA = a.N % 4 == 0 && aligned(a.A, 16);
+    p.vecState = a.N % 4 == 0 && aligned(a.state, 16);
+    int nl = 1;
+    while (4 * nl < a.N)
+        nl *= 2;
+    return a.dtype == 0 ? run_step<0>(p, nl, stream) : run_step<1>(p, nl, stream);
+}
+
+}  // namespace mcc1d
