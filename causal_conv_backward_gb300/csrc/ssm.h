@@ -29,18 +29,16 @@ int32_t launch_short_conv_step(const mcc1d_short_conv_step_args &a, cudaStream_t
 
 // ------------------------------------------------------------------ selective scan
 // A channel's N states are spread over NL = 1, 2, 4, 8 or 16 lanes of a warp,
-// four to a lane (NP = 4 NL >= N, padded with zeros); a block of 8 warps owns
-// CB = 256 / NL channels of one group and walks one time chunk in tiles of TT
-// rows.
+// four to a lane (NP = 4 NL >= N, padded with zeros). Blocks walk one time
+// chunk of their channels in tiles of TT rows.
 struct ScanPlan {
-    int32_t nl, np, cb, tt;
-    int32_t blocks_per_group;
-    int64_t blocks;           // G * blocks_per_group
+    int32_t nl, np, tt;
     int64_t tiles;            // ceil(S / tt)
     int64_t tiles_per_chunk;
     int64_t chunks;
     uint64_t off_e, off_r, off_dt, off_cp, off_cpdt, off_ga, off_gd, off_bc;   // workspace, in bytes
     uint64_t bytes;
+    int64_t most_blocks;      // of the largest grid
 };
 ScanPlan scan_plan(const mcc1d_scan_args &a);
 ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &a);

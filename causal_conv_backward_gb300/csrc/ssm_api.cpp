@@ -129,7 +129,7 @@ int32_t check(const mcc1d_scan_args *a, bool out)
     return kOk;
 }
 
-int32_t grid_ok(const ScanPlan &p, int64_t B) { return p.blocks * B <= kMaxGrid / p.chunks ? kOk : kErrShape; }
+int32_t grid_ok(const ScanPlan &p) { return p.most_blocks <= kMaxGrid ? kOk : kErrShape; }
 
 int32_t check(const mcc1d_scan_bwd_args *a)
 {
@@ -212,7 +212,7 @@ extern "C" int32_t mcc1d_scan_workspace_size(const mcc1d_scan_args *a, uint64_t 
     if (st != kOk)
         return st;
     const ScanPlan p = scan_plan(*a);
-    st = grid_ok(p, a->B);
+    st = grid_ok(p);
     if (st == kOk)
         *bytes_out = p.bytes;
     return st;
@@ -224,7 +224,7 @@ extern "C" int32_t mcc1d_scan(const mcc1d_scan_args *a, void *workspace, uint64_
     if (st != kOk)
         return st;
     const ScanPlan p = scan_plan(*a);
-    st = grid_ok(p, a->B);
+    st = grid_ok(p);
     if (st == kOk)
         st = check_workspace(workspace, workspace_bytes, p.bytes);
     if (st == kOk)
@@ -240,7 +240,7 @@ extern "C" int32_t mcc1d_scan_bwd_workspace_size(const mcc1d_scan_bwd_args *a, u
     if (st != kOk)
         return st;
     const ScanPlan p = scan_bwd_plan(*a);
-    st = grid_ok(p, a->fwd.B);
+    st = grid_ok(p);
     if (st == kOk)
         *bytes_out = p.bytes;
     return st;
@@ -253,7 +253,7 @@ extern "C" int32_t mcc1d_scan_bwd(const mcc1d_scan_bwd_args *a, void *workspace,
     if (st != kOk)
         return st;
     const ScanPlan p = scan_bwd_plan(*a);
-    st = grid_ok(p, a->fwd.B);
+    st = grid_ok(p);
     if (st == kOk)
         st = check_workspace(workspace, workspace_bytes, p.bytes);
     if (st == kOk)

@@ -26,33 +26,43 @@ namespace {
 // chunk's start from the outputs inside it.
 enum { kOutputs = 0, kSummary = 1, kSummaryGrad = 2 };
 
-template <int DT, int NL, int MODE>
-__global__ void __launch_bounds__(kScanThreads, 3) mcc1d_ssm_scan(const ScanParams p)
+template <int DT, int NL, int MODE, bool PAIRS>
+__global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParams p)
 {
-    using T = ScanTile<NL>;
-    constexpr int NP = T::NP, CB = T::CB, TT = scan_tile_rows(NL, MODE == kSummaryGrad);
-    constexpr int RP = TT / T::RG;
+    using T = ScanTile<NL, kFwdWarps>;
+    constexpr int NP = T::NP, CB = T::CB, TT = scan_tile_rows(NL), RG = T::RG, RP = TT / RG;
     constexpr bool kY = MODE == kOutputs, kR = MODE == kSummaryGrad, kC = kY || kR;
-    __shared__ __align__(16) float2 sd[TT][CB];       // dt, dt u; then y in place of dt
+    // dt and dt u come as equal pairs, ready for packed arithmetic
+    __shared__ __align__(16) float4 sd[TT][CB];
     __shared__ __align__(16) float sB[TT][NP];
     __shared__ __align__(16) float sC[kC ? TT : 1][NP];
-    __shared__ __align__(16) float sg[kR ? TT : 1][CB];
+    __shared__ __align__(16) float sy[kY ? TT : 1][CB][NL];  // a lane's part of y
+    __shared__ __align__(16) float sg[kR ? TT : 1][CB];      // the gradient of y
 
-    const ScanWhere w = scan_where<NL>(p);
+    const ScanWhere w = scan_where<NL, kFwdWarps>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = lane % NL, n0 = 4 * j;
     const int cl = warp * T::CW + lane / NL;          // channel of the recurrence, within the block
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
-    // the thread's two channels and rows of a tile
+    const int64_t tile0 = w.chunk * p.tiles_per_chunk;
+    const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
+    // the thread's two channels, and its first row of a tile (RG rows apart)
     const int pc = 2 * (threadIdx.x % T::CP), pr = threadIdx.x / T::CP;
     const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
-    const int64_t ch = w.c0 + (on0 ? pc : 0);
-    const uint16_t *u = p.u + w.b * p.ub + ch, *delta = p.delta + w.b * p.db + ch;
-    const uint16_t *z = kC && p.z ? p.z + w.b * p.zb + ch : nullptr;
-    const uint16_t *gy = kR ? p.gy + w.b * p.gb + ch : nullptr;
-    const uint16_t *Bm = p.Bm + w.b * p.Bb + w.g * p.Bg, *Cm = kC ? p.Cm + w.b * p.Cb + w.g * p.Cg : nullptr;
-    const float bias0 = p.dbias && on0 ? p.dbias[ch] : 0.f, bias1 = p.dbias && on1 ? p.dbias[ch + 1] : 0.f;
-    const float D0 = kY && p.D && on0 ? p.D[ch] : 0.f, D1 = kY && p.D && on1 ? p.D[ch + 1] : 0.f;
+    const int64_t ch = w.c0 + (on0 ? pc : 0), trow = tile0 * TT + pr;
+    const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
+    const uint16_t *z = kC && p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr;
+    const uint16_t *gy = kR ? p.gy + w.b * p.gb + ch + trow * p.gs : nullptr;
+    uint16_t *y = kY ? p.y + (trow * p.B + w.b) * p.H + ch : nullptr;
+    const int64_t ys = RG * p.B * p.H;
+    const uint16_t *Bm = p.Bm + w.b * p.Bb + w.g * p.Bg + tile0 * TT * p.Bs;
+    const uint16_t *Cm = p.Cm + w.b * p.Cb + w.g * p.Cg + tile0 * TT * p.Cs;
+    const int64_t us = RG * p.us, ds = RG * p.ds, zs = RG * p.zs, gs = RG * p.gs;
+    float2 bias = make_float2(0.f, 0.f), D = make_float2(0.f, 0.f);
+    if (p.dbias)
+        bias = make_float2(on0 ? p.dbias[ch] : 0.f, on1 ? p.dbias[ch + 1] : 0.f);
+    if (kY && p.D)
+        D = make_float2(on0 ? p.D[ch] : 0.f, on1 ? p.D[ch + 1] : 0.f);
 
     // the lane's four states
     const bool live = cl < w.nc;
@@ -77,129 +87,126 @@ __global__ void __launch_bounds__(kScanThreads, 3) mcc1d_ssm_scan(const ScanPara
     float dtsum = 0.f;
 
     uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
-    BcTile<NL, TT> bc;
-    const int64_t tile0 = w.chunk * p.tiles_per_chunk;
-    const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
-    auto load = [&](int64_t tile) {
-        const int64_t t0 = tile * TT;
+    BcTile<NL, kFwdWarps, TT, kC> bc;
+    auto load = [&](int rows) {
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-            const int64_t t = t0 + pr + r * T::RG;
-            const bool ok = t < te;
-            ru[r] = load_pair(u + t * p.us, ok && on0, ok && on1, p.pairs);
-            rd[r] = load_pair(delta + t * p.ds, ok && on0, ok && on1, p.pairs);
-            rz[r] = z ? load_pair(z + t * p.zs, ok && on0, ok && on1, p.pairs) : 0u;
-            rg[r] = kR ? load_pair(gy + t * p.gs, ok && on0, ok && on1, p.pairs) : 0u;
-        }
-        bc.load(p, Bm, Cm, t0, te);
-    };
-    if (tile0 * TT < te)
-        load(tile0);
-    for (int64_t tile = tile0; tile < tile1; ++tile) {
-        const int64_t t0 = tile * TT;
-        if (t0 >= te) {
-            // past the sequence's end: zeros, and the state stays
-            if (!kY)
-                break;
-#pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                const int64_t t = t0 + pr + r * T::RG;
-                if (t < p.S)
-                    store_pair(p.y + (t * p.B + w.b) * p.H + ch, 0u, on0, on1, p.pairs);
+            const bool ok = pr + r * RG < rows;
+            ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
+            rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
+            u += us;
+            delta += ds;
+            if (kC && p.z) {
+                rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
+                z += zs;
             }
-            continue;
+            if (kR) {
+                rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
+                gy += gs;
+            }
         }
+        bc.load(p, Bm, Cm, rows);
+        Bm += TT * p.Bs;
+        Cm += TT * p.Cs;
+    };
+    // rows of tile i before `end`, at most TT (none or fewer past it)
+    auto rows_before = [](int64_t end, int64_t i) { return (int)(end - i * TT < TT ? end - i * TT : TT); };
+    if (rows_before(te, tile0) > 0)
+        load(rows_before(te, tile0));
+    int64_t tile = tile0;
+    for (; tile < tile1; ++tile) {
+        const int rows = rows_before(te, tile);
+        if (rows <= 0)
+            break;
         uint32_t cu[RP], cz[RP];
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-            const int64_t t = t0 + pr + r * T::RG;
-            const float2 uv = unpack2<DT>(ru[r]);
-            float2 dt = unpack2<DT>(rd[r]);
-            dt.x += bias0;
-            dt.y += bias1;
-            if (p.softplus) {
-                dt.x = softplus(dt.x);
-                dt.y = softplus(dt.y);
-            }
-            if (t >= te)
+            const int row = pr + r * RG;
+            float2 dt = add2(unpack2<DT>(rd[r]), bias);
+            if (p.softplus)
+                dt = softplus2(dt);
+            if (row >= rows)
                 dt = make_float2(0.f, 0.f);
-            *reinterpret_cast<float4 *>(&sd[pr + r * T::RG][pc]) = make_float4(dt.x, dt.x * uv.x, dt.y, dt.y * uv.y);
+            const float2 du = mul2(dt, unpack2<DT>(ru[r]));
+            sd[row][pc] = make_float4(dt.x, dt.x, du.x, du.x);
+            sd[row][pc + 1] = make_float4(dt.y, dt.y, du.y, du.y);
             if (kR) {
                 float2 g = unpack2<DT>(rg[r]);
-                if (z) {
+                if (p.z) {
                     const float2 zv = unpack2<DT>(rz[r]);
-                    g.x *= zv.x * sigmoid(zv.x);
-                    g.y *= zv.y * sigmoid(zv.y);
+                    g = mul2(g, mul2(zv, sigmoid2(zv)));
                 }
-                *reinterpret_cast<float2 *>(&sg[pr + r * T::RG][pc]) = g;
+                *reinterpret_cast<float2 *>(&sg[row][pc]) = g;
             }
             cu[r] = ru[r];
             cz[r] = rz[r];
         }
-        bc.template put<DT>(sB, kC ? sC : nullptr);
+        bc.template put<DT>(p, sB, sC);
         __syncthreads();
-        if (tile + 1 < tile1 && t0 + TT < te)
-            load(tile + 1);
-        if (kR) {
-            if (live) {
-                const int64_t at = (tile * p.B + w.b) * p.H + hc;
-                *reinterpret_cast<float4 *>(p.cp + at * NP + n0) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-                if (j == 0)
-                    p.cpdt[at] = dtsum;
-            }
+        if (tile + 1 < tile1 && rows_before(te, tile + 1) > 0)
+            load(rows_before(te, tile + 1));
+        if (kR && live) {
+            const int64_t at = (tile * p.B + w.b) * p.H + hc;
+            *reinterpret_cast<float4 *>(p.cp + at * NP + n0) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+            if (j == 0)
+                p.cpdt[at] = dtsum;
         }
-#pragma unroll 2
-        for (int tb = 0; tb < TT; tb += NL) {
-            float yp[NL];
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const float2 dd = sd[tb + i][cl];
-                const float4 bv = *reinterpret_cast<const float4 *>(&sB[tb + i][n0]);
-                const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
-                float2 a0 = mul2(dt2, A2[0]), a1 = mul2(dt2, A2[1]);
-                a0 = make_float2(ex2(a0.x), ex2(a0.y));
-                a1 = make_float2(ex2(a1.x), ex2(a1.y));
-                h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
-                h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
-                if (!kY)
-                    dtsum += dd.x;
-                if (kC) {
-                    const float4 cv = *reinterpret_cast<const float4 *>(&sC[tb + i][n0]);
-                    const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
-                    if (kY) {
-                        const float2 s = fma2(h[0], c0, mul2(h[1], c1));
-                        yp[i] = s.x + s.y;
-                    } else {
-                        const float g = sg[tb + i][cl];
-                        const float2 g2 = make_float2(g, g);
-                        q[0] = mul2(q[0], a0);
-                        q[1] = mul2(q[1], a1);
-                        R[0] = fma2(q[0], mul2(g2, c0), R[0]);
-                        R[1] = fma2(q[1], mul2(g2, c1), R[1]);
-                    }
+#pragma unroll 8
+        for (int i = 0; i < TT; ++i) {
+            const float4 dd = sd[i][cl];
+            const float4 bv = *reinterpret_cast<const float4 *>(&sB[i][n0]);
+            const float2 dt2 = make_float2(dd.x, dd.y), du2 = make_float2(dd.z, dd.w);
+            const float2 a0 = decay2(dt2, A2[0]), a1 = decay2(dt2, A2[1]);
+            h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
+            h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
+            if (!kY)
+                dtsum += dd.x;
+            if (kC) {
+                const float4 cv = *reinterpret_cast<const float4 *>(&sC[i][n0]);
+                const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
+                if (kY) {
+                    const float2 s = fma2(h[0], c0, mul2(h[1], c1));
+                    sy[i][cl][j] = s.x + s.y;
+                } else {
+                    const float g = sg[i][cl];
+                    const float2 g2 = make_float2(g, g);
+                    q[0] = mul2(q[0], a0);
+                    q[1] = mul2(q[1], a1);
+                    R[0] = fma2(q[0], mul2(g2, c0), R[0]);
+                    R[1] = fma2(q[1], mul2(g2, c1), R[1]);
                 }
-            }
-            if (kY) {
-                lanes_sum<NL, NL>(yp, lane, 1);
-                sd[tb + j][cl].x = yp[0];
             }
         }
         __syncthreads();
         if (kY) {
+            const int all = rows_before(p.S, tile);
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                const int64_t t = t0 + pr + r * T::RG;
-                const float4 s = *reinterpret_cast<const float4 *>(&sd[pr + r * T::RG][pc]);
-                const float2 uv = unpack2<DT>(cu[r]);
-                float2 y = make_float2(fmaf(D0, uv.x, s.x), fmaf(D1, uv.y, s.z));
-                if (z) {
-                    const float2 zv = unpack2<DT>(cz[r]);
-                    y.x *= zv.x * sigmoid(zv.x);
-                    y.y *= zv.y * sigmoid(zv.y);
+            for (int r = 0; r < RP; ++r, y += ys) {
+                const int row = pr + r * RG;
+                const float *part = &sy[row][pc][0];
+                float2 v = make_float2(part[0], part[NL]);
+#pragma unroll
+                for (int k = 1; k < NL; ++k) {
+                    v.x += part[k];
+                    v.y += part[NL + k];
                 }
-                if (t < p.S)
-                    store_pair(p.y + (t * p.B + w.b) * p.H + ch, t < te ? pack2<DT>(y) : 0u, on0, on1, p.pairs);
+                v = fma2(D, unpack2<DT>(cu[r]), v);
+                if (p.z) {
+                    const float2 zv = unpack2<DT>(cz[r]);
+                    v = mul2(v, mul2(zv, sigmoid2(zv)));
+                }
+                if (row < all)
+                    store_pair<PAIRS>(y, row < rows ? pack2<DT>(v) : 0u, on0, on1);
             }
+        }
+    }
+    if (kY) {   // past the sequence's end: zeros, and the state stays
+        for (; tile < tile1; ++tile) {
+            const int all = rows_before(p.S, tile);
+#pragma unroll
+            for (int r = 0; r < RP; ++r, y += ys)
+                if (pr + r * RG < all)
+                    store_pair<PAIRS>(y, 0u, on0, on1);
         }
     }
     if (!live)
@@ -283,6 +290,8 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
         store_states(p.gstate + row * p.N, n0, p.N, p.vecState, s);
 }
 
+constexpr int kStepThreads = 256;
+
 // One token: a row of states in, moved on by one step, and out.
 struct ScanStepParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm;
@@ -301,10 +310,10 @@ __device__ __forceinline__ float load16(const uint16_t *p)
 }
 
 template <int DT, int NL>
-__global__ void __launch_bounds__(kScanThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
+__global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
 {
     const int j = threadIdx.x % NL, n0 = 4 * j;
-    const int64_t id = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) / NL;
+    const int64_t id = ((int64_t)blockIdx.x * kStepThreads + threadIdx.x) / NL;
     const bool live = id < p.B * p.H;
     const int64_t b = live ? id / p.H : 0, c = live ? id - b * p.H : 0;
     const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
@@ -353,30 +362,40 @@ __global__ void __launch_bounds__(kScanThreads) mcc1d_ssm_scan_step(const ScanSt
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-template <int DT, int MODE>
-int32_t run_scan(const ScanParams &p, int nl, cudaStream_t s)
+template <int DT, int MODE, int NL>
+int32_t run_nl(ScanParams p, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(p.blocks * p.B * p.chunks);
-    switch (nl) {
-    case 1: mcc1d_ssm_scan<DT, 1, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 2: mcc1d_ssm_scan<DT, 2, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 4: mcc1d_ssm_scan<DT, 4, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 8: mcc1d_ssm_scan<DT, 8, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
-    default: mcc1d_ssm_scan<DT, 16, MODE><<<grid, kScanThreads, 0, s>>>(p); break;
-    }
+    p.grid = scan_grid(p.H, p.G, ScanTile<NL, kFwdWarps>::CB);
+    const unsigned grid = (unsigned)(p.grid.blocks * p.B * p.chunks);
+    if (p.pairs)
+        mcc1d_ssm_scan<DT, NL, MODE, true><<<grid, 32 * kFwdWarps, 0, s>>>(p);
+    else
+        mcc1d_ssm_scan<DT, NL, MODE, false><<<grid, 32 * kFwdWarps, 0, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+template <int MODE>
+int32_t run_scan(const ScanParams &p, int dtype, int nl, cudaStream_t s)
+{
+    switch (nl) {
+    case 1: return dtype == 0 ? run_nl<0, MODE, 1>(p, s) : run_nl<1, MODE, 1>(p, s);
+    case 2: return dtype == 0 ? run_nl<0, MODE, 2>(p, s) : run_nl<1, MODE, 2>(p, s);
+    case 4: return dtype == 0 ? run_nl<0, MODE, 4>(p, s) : run_nl<1, MODE, 4>(p, s);
+    case 8: return dtype == 0 ? run_nl<0, MODE, 8>(p, s) : run_nl<1, MODE, 8>(p, s);
+    default: return dtype == 0 ? run_nl<0, MODE, 16>(p, s) : run_nl<1, MODE, 16>(p, s);
+    }
 }
 
 template <int DT>
 int32_t run_step(const ScanStepParams &p, int nl, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((p.B * p.H * nl + kScanThreads - 1) / kScanThreads);
+    const unsigned grid = (unsigned)((p.B * p.H * nl + kStepThreads - 1) / kStepThreads);
     switch (nl) {
-    case 1: mcc1d_ssm_scan_step<DT, 1><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 2: mcc1d_ssm_scan_step<DT, 2><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 4: mcc1d_ssm_scan_step<DT, 4><<<grid, kScanThreads, 0, s>>>(p); break;
-    case 8: mcc1d_ssm_scan_step<DT, 8><<<grid, kScanThreads, 0, s>>>(p); break;
-    default: mcc1d_ssm_scan_step<DT, 16><<<grid, kScanThreads, 0, s>>>(p); break;
+    case 1: mcc1d_ssm_scan_step<DT, 1><<<grid, kStepThreads, 0, s>>>(p); break;
+    case 2: mcc1d_ssm_scan_step<DT, 2><<<grid, kStepThreads, 0, s>>>(p); break;
+    case 4: mcc1d_ssm_scan_step<DT, 4><<<grid, kStepThreads, 0, s>>>(p); break;
+    case 8: mcc1d_ssm_scan_step<DT, 8><<<grid, kStepThreads, 0, s>>>(p); break;
+    default: mcc1d_ssm_scan_step<DT, 16><<<grid, kStepThreads, 0, s>>>(p); break;
     }
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
@@ -388,18 +407,14 @@ uint64_t take(uint64_t &off, uint64_t bytes)
     return at;
 }
 
-ScanPlan shape_plan(const mcc1d_scan_args &a, bool bwd)
+ScanPlan shape_plan(const mcc1d_scan_args &a)
 {
     ScanPlan p = {};
     p.nl = 1;
     while (4 * p.nl < a.N)
         p.nl *= 2;
     p.np = 4 * p.nl;
-    p.cb = kScanThreads / p.nl;
-    p.tt = scan_tile_rows(p.nl, bwd);
-    const int64_t Hg = a.H / a.G;
-    p.blocks_per_group = (int32_t)((Hg + p.cb - 1) / p.cb);
-    p.blocks = a.G * p.blocks_per_group;
+    p.tt = scan_tile_rows(p.nl);
     p.tiles = (a.S + p.tt - 1) / p.tt;
     return p;
 }
@@ -416,13 +431,22 @@ void cut(ScanPlan &p, int64_t chunks)
 
 }  // namespace
 
+ScanGrid scan_grid(int64_t H, int64_t G, int cb)
+{
+    ScanGrid g;
+    g.blocks_per_group = (int32_t)((H / G + cb - 1) / cb);
+    g.blocks = G * g.blocks_per_group;
+    return g;
+}
+
 ScanPlan scan_plan(const mcc1d_scan_args &a)
 {
-    ScanPlan p = shape_plan(a, false);
+    ScanPlan p = shape_plan(a);
     // One pass where it fills the machine about half; cutting the time axis
     // computes the states twice, so it has to bring more than twice the blocks.
-    const int64_t rows = p.blocks * a.B;
-    cut(p, rows >= 152 ? 1 : (152 * 3 + rows - 1) / rows);
+    const int64_t rows = scan_grid(a.H, a.G, 32 * kFwdWarps / p.nl).blocks * a.B;
+    cut(p, rows >= 152 * 2 ? 1 : (152 * 6 + rows - 1) / rows);
+    p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
     if (p.chunks > 1) {
@@ -436,9 +460,10 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
 ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
 {
     const mcc1d_scan_args &a = ba.fwd;
-    ScanPlan p = shape_plan(a, true);
-    const int64_t rows = p.blocks * a.B;
+    ScanPlan p = shape_plan(a);
+    const int64_t blocks = scan_grid(a.H, a.G, 32 * kBwdWarps / p.nl).blocks, rows = blocks * a.B;
     cut(p, (152 * 6 + rows - 1) / rows);
+    p.most_blocks = scan_grid(a.H, a.G, 32 * kFwdWarps / p.nl).blocks * a.B * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
     p.off_e = take(off, (uint64_t)p.chunks * ch * p.np * 4);
@@ -448,7 +473,7 @@ ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
     p.off_cpdt = take(off, (uint64_t)p.tiles * ch * 4);
     p.off_ga = take(off, (uint64_t)p.chunks * ch * p.np * 4);
     p.off_gd = take(off, (uint64_t)p.chunks * ch * 8);
-    p.off_bc = take(off, (uint64_t)(a.S * a.B) * (uint64_t)p.blocks * 2u * p.np * 4);
+    p.off_bc = take(off, (uint64_t)(a.S * a.B) * (uint64_t)blocks * 2u * p.np * 4);
     p.bytes = off;
     return p;
 }
@@ -479,8 +504,6 @@ static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint
     p.N = (int32_t)a.N;
     p.G = (int32_t)a.G;
     p.Hg = (int32_t)(a.H / a.G);
-    p.blocks = pl.blocks;
-    p.blocks_per_group = pl.blocks_per_group;
     p.tiles = pl.tiles;
     p.tiles_per_chunk = pl.tiles_per_chunk;
     p.chunks = pl.chunks;
@@ -491,6 +514,7 @@ static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint
     const uintptr_t bca = (uintptr_t)a.B_ | (uintptr_t)a.C;
     const int64_t bcs = p.Bs | p.Bb | p.Bg | p.Cs | p.Cb | p.Cg | a.N;
     p.bcpairs = (bca & 3u) == 0 && (bcs & 1) == 0;
+    p.bc8 = (bca & 15u) == 0 && (bcs & 7) == 0;
     p.vecA = a.N % 4 == 0 && aligned(a.A, 16);
     p.vecState = a.N % 4 == 0 && aligned(a.state, 16) && aligned(a.final_state, 16);
     p.e = (float *)(ws + pl.off_e);
@@ -518,13 +542,13 @@ int32_t launch_scan(const mcc1d_scan_args &a, const ScanPlan &pl, void *workspac
 {
     const ScanParams p = scan_params(a, pl, (uint8_t *)workspace);
     if (p.chunks > 1) {
-        int32_t st = a.dtype == 0 ? run_scan<0, kSummary>(p, pl.nl, stream) : run_scan<1, kSummary>(p, pl.nl, stream);
+        int32_t st = run_scan<kSummary>(p, a.dtype, pl.nl, stream);
         if (st == kOk)
             st = join(p, pl.nl, false, stream);
         if (st != kOk)
             return st;
     }
-    return a.dtype == 0 ? run_scan<0, kOutputs>(p, pl.nl, stream) : run_scan<1, kOutputs>(p, pl.nl, stream);
+    return run_scan<kOutputs>(p, a.dtype, pl.nl, stream);
 }
 
 int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *workspace, cudaStream_t stream)
@@ -544,8 +568,7 @@ int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *
     p.pairs = (any & 3u) == 0 && (steps & 1) == 0;
     p.vecState = a.fwd.N % 4 == 0 && aligned(a.fwd.state, 16) && aligned(a.grad_final_state, 16) &&
                  aligned(a.grad_state, 16);
-    int32_t st = a.fwd.dtype == 0 ? run_scan<0, kSummaryGrad>(p, pl.nl, stream)
-                                  : run_scan<1, kSummaryGrad>(p, pl.nl, stream);
+    int32_t st = run_scan<kSummaryGrad>(p, a.fwd.dtype, pl.nl, stream);
     if (st == kOk)
         st = join(p, pl.nl, true, stream);
     if (st != kOk)

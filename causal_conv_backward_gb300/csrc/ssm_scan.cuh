@@ -1,8 +1,8 @@
 // ssm_scan.cuh - what the selective scan's forward and backward kernels share:
 // their parameters, the tile loads and the sums over a channel's lanes.
 //
-// Layout of a block: 8 warps; a channel's N states sit on NL lanes, four to a
-// lane, so a warp owns 32/NL channels and the block CB = 256/NL, of one group
+// Layout of a block: NW warps; a channel's N states sit on NL lanes, four to a
+// lane, so a warp owns 32/NL channels and the block CB = 32 NW/NL, of one group
 // and one sequence. It walks one time chunk in tiles of TT rows. Loads, dt and
 // the gate are done once per (row, channel) by a thread that owns two adjacent
 // channels of RP rows of the tile; dt and dt*u reach the lanes of the
@@ -14,24 +14,30 @@
 
 namespace mcc1d {
 
-struct ScanParams;
-int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s);
+// Warps per block of the forward passes and of the backward. Small blocks share
+// out sequences of unequal length better; the backward's large ones halve its
+// partial sums of grad_B and grad_C.
+constexpr int kFwdWarps = 4, kBwdWarps = 8;
 
-constexpr int kScanThreads = 256;
-constexpr int kScanWarps = kScanThreads / 32;
-
-template <int NL>
+template <int NL, int NW>
 struct ScanTile {
+    static constexpr int THREADS = 32 * NW;
     static constexpr int NP = 4 * NL;              // states, padded
     static constexpr int CW = 32 / NL;             // channels per warp
-    static constexpr int CB = kScanWarps * CW;     // channels per block
+    static constexpr int CB = NW * CW;             // channels per block
     static constexpr int CP = CB / 2;              // channel pairs per row
-    static constexpr int RG = kScanThreads / CP;   // rows of one pass over a tile
+    static constexpr int RG = THREADS / CP;        // rows of one pass over a tile
 };
 
-// Rows per tile: 2048 (row, channel) elements, at most 64 rows (forward) or 32
-// (backward, whose shared memory per row is larger).
-__host__ __device__ constexpr int scan_tile_rows(int nl, bool bwd) { return 8 * nl < (bwd ? 32 : 64) ? 8 * nl : (bwd ? 32 : 64); }
+// Rows per tile: eight (row, channel) elements per thread, at most 32 rows.
+__host__ __device__ constexpr int scan_tile_rows(int nl) { return nl < 4 ? 8 * nl : 32; }
+
+// How blocks cover the channels.
+struct ScanGrid {
+    int64_t blocks;             // over all groups
+    int32_t blocks_per_group;
+};
+ScanGrid scan_grid(int64_t H, int64_t G, int cb);
 
 struct ScanParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm, *gy;
@@ -41,11 +47,15 @@ struct ScanParams {
     float *hT, *gstate;
     float *e, *r, *dts, *cp, *cpdt, *ga, *gd, *bc;
     int64_t us, ub, ds, db, zs, zb, Bs, Bb, Bg, Cs, Cb, Cg, gs, gb;
-    int64_t S, B, H, blocks, tiles, tiles_per_chunk, chunks;
-    int32_t N, G, Hg, blocks_per_group;
-    int32_t softplus, pairs, bcpairs;     // pairs: every [S,B,H] row starts on 4 bytes and Hg is even
+    int64_t S, B, H, tiles, tiles_per_chunk, chunks;
+    ScanGrid grid;                        // of the kernel launched
+    int32_t N, G, Hg;
+    int32_t softplus, pairs;              // pairs: every [S,B,H] row starts on 4 bytes and Hg is even
+    int32_t bcpairs, bc8;                 // rows of B and C start on 4 (16) bytes and N is even (a multiple of 8)
     int32_t vecA, vecState;               // rows of A (of the states) can be moved 16 bytes at a time
 };
+
+int32_t launch_scan_bwd_main(ScanParams p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s);
 
 // Where a block works.
 struct ScanWhere {
@@ -55,34 +65,36 @@ struct ScanWhere {
     int32_t nc;       // channels of the block inside the group
 };
 
-template <int NL>
+template <int NL, int NW>
 __device__ __forceinline__ ScanWhere scan_where(const ScanParams &p)
 {
     ScanWhere w;
     const int64_t i = blockIdx.x;
-    w.blk = (int32_t)(i % p.blocks);
-    const int64_t q = i / p.blocks;
+    w.blk = (int32_t)(i % p.grid.blocks);
+    const int64_t q = i / p.grid.blocks;
     w.b = q % p.B;
     w.chunk = q / p.B;
-    w.g = w.blk / p.blocks_per_group;
-    const int32_t in = (w.blk - w.g * p.blocks_per_group) * ScanTile<NL>::CB;
+    w.g = w.blk / p.grid.blocks_per_group;
+    const int32_t in = (w.blk - w.g * p.grid.blocks_per_group) * ScanTile<NL, NW>::CB;
     w.c0 = w.g * p.Hg + in;
-    w.nc = p.Hg - in < ScanTile<NL>::CB ? p.Hg - in : ScanTile<NL>::CB;
+    w.nc = p.Hg - in < ScanTile<NL, NW>::CB ? p.Hg - in : ScanTile<NL, NW>::CB;
     return w;
 }
 
-// Two adjacent channels of one row (the second only where `two`).
-__device__ __forceinline__ uint32_t load_pair(const uint16_t *p, bool one, bool two, bool wide)
+// Two adjacent 16-bit values, in one access (PAIRS: both are there) or two.
+template <bool PAIRS>
+__device__ __forceinline__ uint32_t load_pair(const uint16_t *p, bool one, bool two)
 {
-    if (wide)
+    if (PAIRS)
         return one ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
     const uint32_t lo = one ? __ldg(p) : 0u, hi = two ? __ldg(p + 1) : 0u;
     return lo | (hi << 16);
 }
 
-__device__ __forceinline__ void store_pair(uint16_t *p, uint32_t v, bool one, bool two, bool wide)
+template <bool PAIRS>
+__device__ __forceinline__ void store_pair(uint16_t *p, uint32_t v, bool one, bool two)
 {
-    if (wide) {
+    if (PAIRS) {
         if (one)
             *reinterpret_cast<uint32_t *>(p) = v;
         return;
@@ -123,9 +135,6 @@ __device__ __forceinline__ void store_states(float *row, int n0, int N, bool vec
         row[n0 + 3] = v.w;
 }
 
-// softplus(x) = log(1 + e^x); past 20 it is x to fp32's last bit.
-__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
-
 // Sums v[0..K-1] over NL lanes whose numbers 0..NL-1 are the lane bits from
 // `bit` up; K and NL are powers of two. Each exchange halves what a lane
 // carries on, so K values cost K (1 - 1/NL) shuffles where K >= NL, not
@@ -152,36 +161,89 @@ __device__ __forceinline__ void lanes_sum(float (&v)[K], int lane, int bit)
         v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step * bit);
 }
 
-// The rows of B and C of one tile, as pairs of states.
-template <int NL, int TT>
+// The rows of B and C of one tile on their way to shared memory. Rows whose
+// states start on 16 bytes and come in eights (p.bc8) move 16 bytes at a time,
+// others a pair or one at a time. Rows from `rows` on are zeros, as are states
+// past N. KC: C too, not B alone.
+template <int NL, int NW, int TT, bool KC>
 struct BcTile {
-    static constexpr int NP = 4 * NL;
-    static constexpr int TOTAL = TT * NP / 2;
-    static constexpr int N = (TOTAL + kScanThreads - 1) / kScanThreads;
-    uint32_t b[N], c[N];
+    static constexpr int NP = 4 * NL, THREADS = 32 * NW, TENSORS = KC ? 2 : 1;
+    static constexpr int PAIRS = TENSORS * TT * NP / 2, WORDS = (PAIRS + THREADS - 1) / THREADS;
+    static constexpr int EIGHTS = NP >= 8 ? PAIRS / 4 : 0, VECS = (EIGHTS + THREADS - 1) / THREADS;
+    static constexpr int N = WORDS > 4 * VECS ? WORDS : 4 * VECS;
+    uint32_t v[N];
 
-    __device__ __forceinline__ void load(const ScanParams &p, const uint16_t *B, const uint16_t *C, int64_t t0,
-                                         int64_t te)
+    template <bool BOTH>
+    __device__ __forceinline__ void load_pairs(const ScanParams &p, const uint16_t *B, const uint16_t *C, int rows)
     {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = threadIdx.x + i * kScanThreads, row = k / (NP / 2), n = 2 * (k % (NP / 2));
-            const bool on = k < TOTAL && t0 + row < te;
-            b[i] = load_pair(B + (t0 + row) * p.Bs + n, on && n < p.N, on && n + 1 < p.N, p.bcpairs);
-            c[i] = C ? load_pair(C + (t0 + row) * p.Cs + n, on && n < p.N, on && n + 1 < p.N, p.bcpairs) : 0u;
+        for (int i = 0; i < WORDS; ++i) {
+            const int k = threadIdx.x + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
+            const bool on = k < PAIRS && row < rows, c = k >= TT * NP / 2;
+            const uint16_t *src = c ? C + row * p.Cs + n : B + row * p.Bs + n;
+            v[i] = load_pair<BOTH>(src, on && n < p.N, on && n + 1 < p.N);
         }
     }
-    template <int DT>
-    __device__ __forceinline__ void put(float (*sB)[NP], float (*sC)[NP]) const
+    // The eight states of vector i: its tensor (C if true), row and first state.
+    __device__ __forceinline__ static bool place8(int i, int &row, int &n)
     {
+        const int k = threadIdx.x + i * THREADS, q = k % (EIGHTS / TENSORS);
+        row = q / (NP / 8);
+        n = 8 * (q % (NP / 8));
+        return k >= EIGHTS / TENSORS;
+    }
+    // B, C: the tile's first rows
+    __device__ __forceinline__ void load(const ScanParams &p, const uint16_t *B, const uint16_t *C, int rows)
+    {
+        if constexpr (VECS > 0) {
+            if (p.bc8) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = threadIdx.x + i * kScanThreads, row = k / (NP / 2), n = 2 * (k % (NP / 2));
-            if (k < TOTAL) {
-                *reinterpret_cast<float2 *>(&sB[row][n]) = unpack2<DT>(b[i]);
-                if (sC)
-                    *reinterpret_cast<float2 *>(&sC[row][n]) = unpack2<DT>(c[i]);
+                for (int i = 0; i < VECS; ++i) {
+                    int row, n;
+                    const bool c = place8(i, row, n);
+                    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+                    if (threadIdx.x + i * THREADS < EIGHTS && row < rows && n < p.N)
+                        r = __ldg(reinterpret_cast<const uint4 *>(c ? C + row * p.Cs + n : B + row * p.Bs + n));
+                    v[4 * i] = r.x;
+                    v[4 * i + 1] = r.y;
+                    v[4 * i + 2] = r.z;
+                    v[4 * i + 3] = r.w;
+                }
+                return;
             }
+        }
+        if (p.bcpairs)
+            load_pairs<true>(p, B, C, rows);
+        else
+            load_pairs<false>(p, B, C, rows);
+    }
+    template <int DT>
+    __device__ __forceinline__ void put(const ScanParams &p, float (*sB)[NP], float (*sC)[NP]) const
+    {
+        if constexpr (VECS > 0) {
+            if (p.bc8) {
+#pragma unroll
+                for (int i = 0; i < VECS; ++i) {
+                    int row, n;
+                    const bool c = place8(i, row, n);
+                    if (threadIdx.x + i * THREADS >= EIGHTS)
+                        break;
+                    float4 *dst = reinterpret_cast<float4 *>(KC && c ? &sC[row][n] : &sB[row][n]);
+                    const float2 e = unpack2<DT>(v[4 * i]), f = unpack2<DT>(v[4 * i + 1]);
+                    const float2 g = unpack2<DT>(v[4 * i + 2]), h = unpack2<DT>(v[4 * i + 3]);
+                    dst[0] = make_float4(e.x, e.y, f.x, f.y);
+                    dst[1] = make_float4(g.x, g.y, h.x, h.y);
+                }
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            const int k = threadIdx.x + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
+            if (k >= PAIRS)
+                break;
+            float *dst = KC && k >= TT * NP / 2 ? &sC[row][n] : &sB[row][n];
+            *reinterpret_cast<float2 *>(dst) = unpack2<DT>(v[i]);
         }
     }
 };

@@ -25,28 +25,28 @@ namespace mcc1d {
 
 namespace {
 
-constexpr int kSub = 4;
+constexpr int kSub = 4, kThreads = 32 * kBwdWarps;
 
 template <int NL>
 struct BwdShared {
-    using T = ScanTile<NL>;
-    static constexpr int TT = scan_tile_rows(NL, true);
+    using T = ScanTile<NL, kBwdWarps>;
+    static constexpr int TT = scan_tile_rows(NL);
     float4 sq[TT][T::CB];                         // dt, dt u, dy -> sum A q, sum g B, y; dt
-    float4 hs[TT / kSub][kScanThreads];           // states before each run of kSub rows
+    float4 hs[TT / kSub][kThreads];           // states before each run of kSub rows
     float sB[TT][T::NP], sC[TT][T::NP];
-    float bc[TT][kScanWarps][2 * T::NP];          // a warp's grad_B and grad_C
+    float bc[TT][kBwdWarps][2 * T::NP];          // a warp's grad_B and grad_C
 };
 
-template <int DT, int NL>
-__global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const ScanParams p)
+template <int DT, int NL, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanParams p)
 {
-    using T = ScanTile<NL>;
+    using T = ScanTile<NL, kBwdWarps>;
     using Sh = BwdShared<NL>;
     constexpr int NP = T::NP, CW = T::CW, TT = Sh::TT, RP = TT / T::RG;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
-    const ScanWhere w = scan_where<NL>(p);
+    const ScanWhere w = scan_where<NL, kBwdWarps>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = lane % NL, n0 = 4 * j, ci = lane / NL;
     const int cl = warp * CW + ci;
@@ -90,40 +90,36 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
                 const int64_t t = t0 + pr + r * T::RG;
                 if (t < p.S) {
                     const int64_t o = (t * p.B + w.b) * p.H + ch;
-                    store_pair(p.gu + o, 0u, on0, on1, p.pairs);
-                    store_pair(p.gdelta + o, 0u, on0, on1, p.pairs);
+                    store_pair<PAIRS>(p.gu + o, 0u, on0, on1);
+                    store_pair<PAIRS>(p.gdelta + o, 0u, on0, on1);
                     if (p.gz)
-                        store_pair(p.gz + o, 0u, on0, on1, p.pairs);
+                        store_pair<PAIRS>(p.gz + o, 0u, on0, on1);
                 }
             }
             continue;
         }
         uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
         {
-            BcTile<NL, TT> bc;
+            BcTile<NL, kBwdWarps, TT, true> bc;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
                 const int64_t t = t0 + pr + r * T::RG;
                 const bool ok = t < te;
-                ru[r] = load_pair(u + t * p.us, ok && on0, ok && on1, p.pairs);
-                rd[r] = load_pair(delta + t * p.ds, ok && on0, ok && on1, p.pairs);
-                rz[r] = z ? load_pair(z + t * p.zs, ok && on0, ok && on1, p.pairs) : 0u;
-                rg[r] = load_pair(gy + t * p.gs, ok && on0, ok && on1, p.pairs);
+                ru[r] = load_pair<PAIRS>(u + t * p.us, ok && on0, ok && on1);
+                rd[r] = load_pair<PAIRS>(delta + t * p.ds, ok && on0, ok && on1);
+                rz[r] = z ? load_pair<PAIRS>(z + t * p.zs, ok && on0, ok && on1) : 0u;
+                rg[r] = load_pair<PAIRS>(gy + t * p.gs, ok && on0, ok && on1);
             }
-            bc.load(p, Bm, Cm, t0, te);
-            bc.template put<DT>(sh.sB, sh.sC);
+            bc.load(p, Bm + t0 * p.Bs, Cm + t0 * p.Cs, (int)(te - t0 < TT ? te - t0 : TT));
+            bc.template put<DT>(p, sh.sB, sh.sC);
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
             const int64_t t = t0 + pr + r * T::RG;
             const float2 uv = unpack2<DT>(ru[r]);
-            float2 dt = unpack2<DT>(rd[r]), g = unpack2<DT>(rg[r]);
-            dt.x += bias0;
-            dt.y += bias1;
-            if (p.softplus) {
-                dt.x = softplus(dt.x);
-                dt.y = softplus(dt.y);
-            }
+            float2 dt = add2(unpack2<DT>(rd[r]), make_float2(bias0, bias1)), g = unpack2<DT>(rg[r]);
+            if (p.softplus)
+                dt = softplus2(dt);
             if (t >= te)
                 dt = make_float2(0.f, 0.f);
             if (z) {
@@ -155,9 +151,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
                 const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl]);
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
                 const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
-                float2 a0 = mul2(dt2, A2[0]), a1 = mul2(dt2, A2[1]);
-                a0 = make_float2(ex2(a0.x), ex2(a0.y));
-                a1 = make_float2(ex2(a1.x), ex2(a1.y));
+                const float2 a0 = decay2(dt2, A2[0]), a1 = decay2(dt2, A2[1]);
                 h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
                 h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
             }
@@ -177,9 +171,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
                 const float4 cv = *reinterpret_cast<const float4 *>(&sh.sC[s + i][n0]);
                 const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
-                const float2 a0 = mul2(dt2, A2[0]), a1 = mul2(dt2, A2[1]);
-                aa[i][0] = make_float2(ex2(a0.x), ex2(a0.y));
-                aa[i][1] = make_float2(ex2(a1.x), ex2(a1.y));
+                aa[i][0] = decay2(dt2, A2[0]);
+                aa[i][1] = decay2(dt2, A2[1]);
                 hh[i + 1][0] = fma2(aa[i][0], hh[i][0], mul2(du2, make_float2(bv.x, bv.y)));
                 hh[i + 1][1] = fma2(aa[i][1], hh[i][1], mul2(du2, make_float2(bv.z, bv.w)));
                 const float2 y = fma2(hh[i + 1][0], make_float2(cv.x, cv.y), mul2(hh[i + 1][1], make_float2(cv.z, cv.w)));
@@ -231,14 +224,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
         gA[0] = add2(gA[0], tA[0]);
         gA[1] = add2(gA[1], tA[1]);
         __syncthreads();
-        for (int i = threadIdx.x; i < TT * 2 * NP; i += kScanThreads) {
+        for (int i = threadIdx.x; i < TT * 2 * NP; i += kThreads) {
             const int row = i / (2 * NP), k = i % (2 * NP);
             float s = sh.bc[row][0][k];
 #pragma unroll
-            for (int q = 1; q < kScanWarps; ++q)
+            for (int q = 1; q < kBwdWarps; ++q)
                 s += sh.bc[row][q][k];
             if (t0 + row < te)
-                p.bc[(((t0 + row) * p.B + w.b) * p.blocks + w.blk) * (2 * NP) + k] = s;
+                p.bc[(((t0 + row) * p.B + w.b) * p.grid.blocks + w.blk) * (2 * NP) + k] = s;
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
@@ -255,7 +248,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
                 const float2 gz = make_float2(dy.x * fmaf(D0, uv.x, s0.z) * sx * fmaf(zv.x, 1.f - sx, 1.f),
                                               dy.y * fmaf(D1, uv.y, s1.z) * sy * fmaf(zv.y, 1.f - sy, 1.f));
                 if (p.gz && t < p.S)
-                    store_pair(p.gz + (t * p.B + w.b) * p.H + ch, t < te ? pack2<DT>(gz) : 0u, on0, on1, p.pairs);
+                    store_pair<PAIRS>(p.gz + (t * p.B + w.b) * p.H + ch, t < te ? pack2<DT>(gz) : 0u, on0, on1);
                 dy.x *= zv.x * sx;
                 dy.y *= zv.y * sy;
             }
@@ -271,8 +264,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) mcc1d_ssm_scan_bwd(const Scan
             }
             if (t < p.S) {
                 const int64_t o = (t * p.B + w.b) * p.H + ch;
-                store_pair(p.gu + o, t < te ? pack2<DT>(gu) : 0u, on0, on1, p.pairs);
-                store_pair(p.gdelta + o, t < te ? pack2<DT>(gr) : 0u, on0, on1, p.pairs);
+                store_pair<PAIRS>(p.gu + o, t < te ? pack2<DT>(gu) : 0u, on0, on1);
+                store_pair<PAIRS>(p.gdelta + o, t < te ? pack2<DT>(gr) : 0u, on0, on1);
             }
         }
         __syncthreads();   // bc is written again in the next tile
@@ -313,8 +306,8 @@ __global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_bc(const ScanParams p,
     const int64_t t = row / p.B, b = row - t * p.B;
     float s = 0.f;
     if (t < clamped_length(p.lengths, b, p.S)) {
-        const float *src = p.bc + (row * p.blocks + g * p.blocks_per_group) * (2 * NP) + k;
-        for (int m = 0; m < p.blocks_per_group; ++m)
+        const float *src = p.bc + (row * p.grid.blocks + g * p.grid.blocks_per_group) * (2 * NP) + k;
+        for (int m = 0; m < p.grid.blocks_per_group; ++m)
             s += src[(int64_t)m * 2 * NP];
     }
     (k < NP ? gB : gC)[q * p.N + n] = (uint16_t)pack2<DT>(make_float2(s, 0.f));
@@ -354,14 +347,21 @@ __global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_sum(const ScanParams p
     }
 }
 
+template <int DT, int NL, bool PAIRS>
+int32_t run_pairs(const ScanParams &p, cudaStream_t s)
+{
+    constexpr int bytes = (int)sizeof(BwdShared<NL>);
+    if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return kErrCuda;
+    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), kThreads, bytes, s>>>(p);
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
 template <int DT, int NL>
 int32_t run(const ScanParams &p, cudaStream_t s)
 {
-    constexpr int bytes = (int)sizeof(BwdShared<NL>);
-    if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return kErrCuda;
-    mcc1d_ssm_scan_bwd<DT, NL><<<(unsigned)(p.blocks * p.B * p.chunks), kScanThreads, bytes, s>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+    return p.pairs ? run_pairs<DT, NL, true>(p, s) : run_pairs<DT, NL, false>(p, s);
 }
 
 template <int DT>
@@ -378,8 +378,9 @@ int32_t run_nl(const ScanParams &p, int nl, cudaStream_t s)
 
 }  // namespace
 
-int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s)
+int32_t launch_scan_bwd_main(ScanParams p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s)
 {
+    p.grid = scan_grid(p.H, p.G, kThreads / pl.nl);
     const int32_t st = a.fwd.dtype == 0 ? run_nl<0>(p, pl.nl, s) : run_nl<1>(p, pl.nl, s);
     if (st != kOk)
         return st;
