@@ -26,23 +26,23 @@ namespace {
 // chunk's start from the outputs inside it.
 enum { kOutputs = 0, kSummary = 1, kSummaryGrad = 2 };
 
-template <int DT, int NL, int MODE, bool PAIRS>
-__global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParams p)
+template <class T, int DT, int MODE, bool PAIRS>
+__global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams p)
 {
-    using T = ScanTile<NL, kFwdWarps>;
-    constexpr int NP = T::NP, CB = T::CB, TT = scan_tile_rows(NL), RG = T::RG, RP = TT / RG;
+    constexpr int NP = T::NP, NL = T::NL, CB = T::CB, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
     constexpr bool kY = MODE == kOutputs, kR = MODE == kSummaryGrad, kC = kY || kR;
-    // dt and dt u come as equal pairs, ready for packed arithmetic
-    __shared__ __align__(16) float4 sd[TT][CB];
+    constexpr int U = TT < 8 ? TT : 8;                      // steps taken together
+    constexpr int YS = NL > 1 ? CB + 16 : CB;              // keeps the lanes of a channel on different banks
+    __shared__ __align__(16) float2 sd[TT][CB];            // dt, dt u
     __shared__ __align__(16) float sB[TT][NP];
     __shared__ __align__(16) float sC[kC ? TT : 1][NP];
-    __shared__ __align__(16) float sy[kY ? TT : 1][CB][NL];  // a lane's part of y
+    __shared__ __align__(16) float sy[kY ? TT : 1][NL][YS];  // a lane's part of y
     __shared__ __align__(16) float sg[kR ? TT : 1][CB];      // the gradient of y
 
-    const ScanWhere w = scan_where<NL, kFwdWarps>(p);
+    const ScanWhere w = scan_where<T>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = lane % NL, n0 = 4 * j;
-    const int cl = warp * T::CW + lane / NL;          // channel of the recurrence, within the block
+    const int j = T::state_lane(lane), n0 = 4 * j;
+    const int cl = (warp * T::CL + T::channel_lane(lane)) * K;   // first channel of the recurrence, within the block
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
     const int64_t tile0 = w.chunk * p.tiles_per_chunk;
     const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
@@ -64,14 +64,15 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
     if (kY && p.D)
         D = make_float2(on0 ? p.D[ch] : 0.f, on1 ? p.D[ch + 1] : 0.f);
 
-    // the lane's four states
-    const bool live = cl < w.nc;
-    const int64_t hc = w.c0 + (live ? cl : 0);
-    float2 A2[2], h[2], q[2], R[2];
-    {
+    // the lane's four states of each of its channels
+    float2 A2[K][2], h[K][2], q[K][2], R[K][2];
+    float dtsum[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t hc = w.c0 + (cl + k < w.nc ? cl + k : 0);
         const float4 a = load_states(p.A + hc * p.N, n0, p.N, p.vecA);
-        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
-        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+        A2[k][0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+        A2[k][1] = make_float2(a.z * kLog2e, a.w * kLog2e);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (kY) {
             if (p.chunks > 1)
@@ -79,15 +80,15 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
             else if (p.h0)
                 s = load_states(p.h0 + (w.b * p.H + hc) * p.N, n0, p.N, p.vecState);
         }
-        h[0] = make_float2(s.x, s.y);
-        h[1] = make_float2(s.z, s.w);
-        q[0] = q[1] = make_float2(1.f, 1.f);
-        R[0] = R[1] = make_float2(0.f, 0.f);
+        h[k][0] = make_float2(s.x, s.y);
+        h[k][1] = make_float2(s.z, s.w);
+        q[k][0] = q[k][1] = make_float2(1.f, 1.f);
+        R[k][0] = R[k][1] = make_float2(0.f, 0.f);
+        dtsum[k] = 0.f;
     }
-    float dtsum = 0.f;
 
     uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
-    BcTile<NL, kFwdWarps, TT, kC> bc;
+    BcTile<T, kC> bc;
     auto load = [&](int rows) {
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
@@ -128,8 +129,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
             if (row >= rows)
                 dt = make_float2(0.f, 0.f);
             const float2 du = mul2(dt, unpack2<DT>(ru[r]));
-            sd[row][pc] = make_float4(dt.x, dt.x, du.x, du.x);
-            sd[row][pc + 1] = make_float4(dt.y, dt.y, du.y, du.y);
+            *reinterpret_cast<float4 *>(&sd[row][pc]) = make_float4(dt.x, du.x, dt.y, du.y);
             if (kR) {
                 float2 g = unpack2<DT>(rg[r]);
                 if (p.z) {
@@ -145,35 +145,73 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
         __syncthreads();
         if (tile + 1 < tile1 && rows_before(te, tile + 1) > 0)
             load(rows_before(te, tile + 1));
-        if (kR && live) {
-            const int64_t at = (tile * p.B + w.b) * p.H + hc;
-            *reinterpret_cast<float4 *>(p.cp + at * NP + n0) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-            if (j == 0)
-                p.cpdt[at] = dtsum;
+        if (kR) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (cl + k < w.nc) {
+                    const int64_t at = (tile * p.B + w.b) * p.H + w.c0 + cl + k;
+                    *reinterpret_cast<float4 *>(p.cp + at * NP + n0) =
+                        make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
+                    if (j == 0)
+                        p.cpdt[at] = dtsum[k];
+                }
         }
-#pragma unroll 8
-        for (int i = 0; i < TT; ++i) {
-            const float4 dd = sd[i][cl];
-            const float4 bv = *reinterpret_cast<const float4 *>(&sB[i][n0]);
-            const float2 dt2 = make_float2(dd.x, dd.y), du2 = make_float2(dd.z, dd.w);
-            const float2 a0 = decay2(dt2, A2[0]), a1 = decay2(dt2, A2[1]);
-            h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
-            h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
-            if (!kY)
-                dtsum += dd.x;
-            if (kC) {
-                const float4 cv = *reinterpret_cast<const float4 *>(&sC[i][n0]);
-                const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
-                if (kY) {
-                    const float2 s = fma2(h[0], c0, mul2(h[1], c1));
-                    sy[i][cl][j] = s.x + s.y;
+        // a few steps at a time: their decays and inputs first, which depend on
+        // nothing before them, then the recurrence
+#pragma unroll 1
+        for (int tb = 0; tb < TT; tb += U) {
+            float2 a[U][K][2], b[U][K][2];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float2 dd[K];
+                if (K == 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sd[tb + i][cl]);
+                    dd[0] = make_float2(v.x, v.y);
+                    dd[K - 1] = make_float2(v.z, v.w);
                 } else {
-                    const float g = sg[i][cl];
-                    const float2 g2 = make_float2(g, g);
-                    q[0] = mul2(q[0], a0);
-                    q[1] = mul2(q[1], a1);
-                    R[0] = fma2(q[0], mul2(g2, c0), R[0]);
-                    R[1] = fma2(q[1], mul2(g2, c1), R[1]);
+                    dd[0] = sd[tb + i][cl];
+                }
+                const float4 bv = *reinterpret_cast<const float4 *>(&sB[tb + i][n0]);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float2 dt2 = make_float2(dd[k].x, dd[k].x), du2 = make_float2(dd[k].y, dd[k].y);
+                    a[i][k][0] = decay2(dt2, A2[k][0]);
+                    a[i][k][1] = decay2(dt2, A2[k][1]);
+                    b[i][k][0] = mul2(du2, make_float2(bv.x, bv.y));
+                    b[i][k][1] = mul2(du2, make_float2(bv.z, bv.w));
+                    if (!kY)
+                        dtsum[k] += dd[k].x;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float4 cv = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (kC)
+                    cv = *reinterpret_cast<const float4 *>(&sC[tb + i][n0]);
+                const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
+                float part[K];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    h[k][0] = fma2(a[i][k][0], h[k][0], b[i][k][0]);
+                    h[k][1] = fma2(a[i][k][1], h[k][1], b[i][k][1]);
+                    if (kY) {
+                        const float2 s = fma2(h[k][0], c0, mul2(h[k][1], c1));
+                        part[k] = s.x + s.y;
+                    }
+                    if (kR) {
+                        const float g = sg[tb + i][cl + k];
+                        const float2 g2 = make_float2(g, g);
+                        q[k][0] = mul2(q[k][0], a[i][k][0]);
+                        q[k][1] = mul2(q[k][1], a[i][k][1]);
+                        R[k][0] = fma2(q[k][0], mul2(g2, c0), R[k][0]);
+                        R[k][1] = fma2(q[k][1], mul2(g2, c1), R[k][1]);
+                    }
+                }
+                if (kY) {
+                    if (K == 2)
+                        *reinterpret_cast<float2 *>(&sy[tb + i][j][cl]) = make_float2(part[0], part[K - 1]);
+                    else
+                        sy[tb + i][j][cl] = part[0];
                 }
             }
         }
@@ -183,13 +221,10 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
 #pragma unroll
             for (int r = 0; r < RP; ++r, y += ys) {
                 const int row = pr + r * RG;
-                const float *part = &sy[row][pc][0];
-                float2 v = make_float2(part[0], part[NL]);
+                float2 v = *reinterpret_cast<const float2 *>(&sy[row][0][pc]);
 #pragma unroll
-                for (int k = 1; k < NL; ++k) {
-                    v.x += part[k];
-                    v.y += part[NL + k];
-                }
+                for (int k = 1; k < NL; ++k)
+                    v = add2(v, *reinterpret_cast<const float2 *>(&sy[row][k][pc]));
                 v = fma2(D, unpack2<DT>(cu[r]), v);
                 if (p.z) {
                     const float2 zv = unpack2<DT>(cz[r]);
@@ -209,19 +244,24 @@ __global__ void __launch_bounds__(32 * kFwdWarps) mcc1d_ssm_scan(const ScanParam
                     store_pair<PAIRS>(y, 0u, on0, on1);
         }
     }
-    if (!live)
-        return;
-    const float4 out = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    if (kY) {
-        if (p.hT && w.chunk == p.chunks - 1)
-            store_states(p.hT + (w.b * p.H + hc) * p.N, n0, p.N, p.vecState, out);
-    } else {
-        const int64_t at = (w.chunk * p.B + w.b) * p.H + hc;
-        *reinterpret_cast<float4 *>(p.e + at * NP + n0) = out;
-        if (j == 0)
-            p.dts[at] = dtsum;
-        if (kR)
-            *reinterpret_cast<float4 *>(p.r + at * NP + n0) = make_float4(R[0].x, R[0].y, R[1].x, R[1].y);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (cl + k >= w.nc)
+            break;
+        const int64_t hc = w.c0 + cl + k;
+        const float4 out = make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
+        if (kY) {
+            if (p.hT && w.chunk == p.chunks - 1)
+                store_states(p.hT + (w.b * p.H + hc) * p.N, n0, p.N, p.vecState, out);
+        } else {
+            const int64_t at = (w.chunk * p.B + w.b) * p.H + hc;
+            *reinterpret_cast<float4 *>(p.e + at * NP + n0) = out;
+            if (j == 0)
+                p.dts[at] = dtsum[k];
+            if (kR)
+                *reinterpret_cast<float4 *>(p.r + at * NP + n0) =
+                    make_float4(R[k][0].x, R[k][0].y, R[k][1].x, R[k][1].y);
+        }
     }
 }
 
@@ -318,7 +358,7 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
     const int64_t b = live ? id / p.H : 0, c = live ? id - b * p.H : 0;
     const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
     const bool on = live && slot >= 0 && slot < p.rows;
-    float part[1] = {0.f};
+    float part = 0.f;
     float uv = 0.f;
     if (on) {
         float *row = p.state + (slot * p.H + c) * p.N;
@@ -338,19 +378,21 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
         o.w = fmaf(ex2(dl * A.w), h.w, n0 + 3 < p.N ? du * load16<DT>(B + n0 + 3) : 0.f);
         store_states(row, n0, p.N, p.vecState, o);
         if (n0 < p.N)
-            part[0] = o.x * load16<DT>(C + n0);
+            part = o.x * load16<DT>(C + n0);
         if (n0 + 1 < p.N)
-            part[0] = fmaf(o.y, load16<DT>(C + n0 + 1), part[0]);
+            part = fmaf(o.y, load16<DT>(C + n0 + 1), part);
         if (n0 + 2 < p.N)
-            part[0] = fmaf(o.z, load16<DT>(C + n0 + 2), part[0]);
+            part = fmaf(o.z, load16<DT>(C + n0 + 2), part);
         if (n0 + 3 < p.N)
-            part[0] = fmaf(o.w, load16<DT>(C + n0 + 3), part[0]);
+            part = fmaf(o.w, load16<DT>(C + n0 + 3), part);
     }
-    lanes_sum<1, NL>(part, threadIdx.x & 31, 1);
+#pragma unroll
+    for (int step = 1; step < NL; step *= 2)
+        part += __shfl_xor_sync(0xFFFFFFFFu, part, step);
     if (live && j == 0) {
         float y = 0.f;
         if (on) {
-            y = p.D ? fmaf(p.D[c], uv, part[0]) : part[0];
+            y = p.D ? fmaf(p.D[c], uv, part) : part;
             if (p.z) {
                 const float zv = load16<DT>(p.z + b * p.zb + c);
                 y *= zv * sigmoid(zv);
@@ -362,27 +404,41 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-template <int DT, int MODE, int NL>
-int32_t run_nl(ScanParams p, cudaStream_t s)
+// Tiles of a forward pass.
+template <int NL>
+using OutTile = ScanTile<NL, 4, 1, (NL < 4 ? 8 * NL : 32)>;
+// Tiles of the backward's first pass have the backward's rows.
+template <int NL>
+using GradTile = ScanTile<NL, 4, 1, BwdTile<NL>::TT>;
+
+template <class T, int MODE>
+int32_t run_tile(ScanParams p, int dtype, cudaStream_t s)
 {
-    p.grid = scan_grid(p.H, p.G, ScanTile<NL, kFwdWarps>::CB);
+    p.grid = scan_grid(p.H, p.G, T::CB);
     const unsigned grid = (unsigned)(p.grid.blocks * p.B * p.chunks);
-    if (p.pairs)
-        mcc1d_ssm_scan<DT, NL, MODE, true><<<grid, 32 * kFwdWarps, 0, s>>>(p);
-    else
-        mcc1d_ssm_scan<DT, NL, MODE, false><<<grid, 32 * kFwdWarps, 0, s>>>(p);
+    if (dtype == 0) {
+        if (p.pairs)
+            mcc1d_ssm_scan<T, 0, MODE, true><<<grid, T::THREADS, 0, s>>>(p);
+        else
+            mcc1d_ssm_scan<T, 0, MODE, false><<<grid, T::THREADS, 0, s>>>(p);
+    } else {
+        if (p.pairs)
+            mcc1d_ssm_scan<T, 1, MODE, true><<<grid, T::THREADS, 0, s>>>(p);
+        else
+            mcc1d_ssm_scan<T, 1, MODE, false><<<grid, T::THREADS, 0, s>>>(p);
+    }
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
-template <int MODE>
+template <template <int> class Tile, int MODE>
 int32_t run_scan(const ScanParams &p, int dtype, int nl, cudaStream_t s)
 {
     switch (nl) {
-    case 1: return dtype == 0 ? run_nl<0, MODE, 1>(p, s) : run_nl<1, MODE, 1>(p, s);
-    case 2: return dtype == 0 ? run_nl<0, MODE, 2>(p, s) : run_nl<1, MODE, 2>(p, s);
-    case 4: return dtype == 0 ? run_nl<0, MODE, 4>(p, s) : run_nl<1, MODE, 4>(p, s);
-    case 8: return dtype == 0 ? run_nl<0, MODE, 8>(p, s) : run_nl<1, MODE, 8>(p, s);
-    default: return dtype == 0 ? run_nl<0, MODE, 16>(p, s) : run_nl<1, MODE, 16>(p, s);
+    case 1: return run_tile<Tile<1>, MODE>(p, dtype, s);
+    case 2: return run_tile<Tile<2>, MODE>(p, dtype, s);
+    case 4: return run_tile<Tile<4>, MODE>(p, dtype, s);
+    case 8: return run_tile<Tile<8>, MODE>(p, dtype, s);
+    default: return run_tile<Tile<16>, MODE>(p, dtype, s);
     }
 }
 
@@ -414,9 +470,20 @@ ScanPlan shape_plan(const mcc1d_scan_args &a)
     while (4 * p.nl < a.N)
         p.nl *= 2;
     p.np = 4 * p.nl;
-    p.tt = scan_tile_rows(p.nl);
-    p.tiles = (a.S + p.tt - 1) / p.tt;
     return p;
+}
+
+// Channels per block and rows per tile.
+template <template <int> class Tile>
+void tile_shape(int nl, int &cb, int &tt)
+{
+    switch (nl) {
+    case 1: cb = Tile<1>::CB, tt = Tile<1>::TT; break;
+    case 2: cb = Tile<2>::CB, tt = Tile<2>::TT; break;
+    case 4: cb = Tile<4>::CB, tt = Tile<4>::TT; break;
+    case 8: cb = Tile<8>::CB, tt = Tile<8>::TT; break;
+    default: cb = Tile<16>::CB, tt = Tile<16>::TT; break;
+    }
 }
 
 void cut(ScanPlan &p, int64_t chunks)
@@ -444,8 +511,11 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
     ScanPlan p = shape_plan(a);
     // One pass where it fills the machine about half; cutting the time axis
     // computes the states twice, so it has to bring more than twice the blocks.
-    const int64_t rows = scan_grid(a.H, a.G, 32 * kFwdWarps / p.nl).blocks * a.B;
-    cut(p, rows >= 152 * 2 ? 1 : (152 * 6 + rows - 1) / rows);
+    int cb;
+    tile_shape<OutTile>(p.nl, cb, p.tt);
+    p.tiles = (a.S + p.tt - 1) / p.tt;
+    const int64_t rows = scan_grid(a.H, a.G, cb).blocks * a.B, warps = rows * OutTile<4>::WARPS;
+    cut(p, warps >= 152 * 5 ? 1 : (152 * 12 + warps - 1) / warps);
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
@@ -461,9 +531,13 @@ ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
 {
     const mcc1d_scan_args &a = ba.fwd;
     ScanPlan p = shape_plan(a);
-    const int64_t blocks = scan_grid(a.H, a.G, 32 * kBwdWarps / p.nl).blocks, rows = blocks * a.B;
+    int cb, cb_first;
+    tile_shape<GradTile>(p.nl, cb_first, p.tt);
+    tile_shape<BwdTile>(p.nl, cb, p.tt);
+    p.tiles = (a.S + p.tt - 1) / p.tt;
+    const int64_t blocks = scan_grid(a.H, a.G, cb).blocks, rows = blocks * a.B;
     cut(p, (152 * 6 + rows - 1) / rows);
-    p.most_blocks = scan_grid(a.H, a.G, 32 * kFwdWarps / p.nl).blocks * a.B * p.chunks;
+    p.most_blocks = scan_grid(a.H, a.G, cb_first).blocks * a.B * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
     p.off_e = take(off, (uint64_t)p.chunks * ch * p.np * 4);
@@ -542,13 +616,13 @@ int32_t launch_scan(const mcc1d_scan_args &a, const ScanPlan &pl, void *workspac
 {
     const ScanParams p = scan_params(a, pl, (uint8_t *)workspace);
     if (p.chunks > 1) {
-        int32_t st = run_scan<kSummary>(p, a.dtype, pl.nl, stream);
+        int32_t st = run_scan<OutTile, kSummary>(p, a.dtype, pl.nl, stream);
         if (st == kOk)
             st = join(p, pl.nl, false, stream);
         if (st != kOk)
             return st;
     }
-    return run_scan<kOutputs>(p, a.dtype, pl.nl, stream);
+    return run_scan<OutTile, kOutputs>(p, a.dtype, pl.nl, stream);
 }
 
 int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *workspace, cudaStream_t stream)
@@ -568,7 +642,7 @@ int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *
     p.pairs = (any & 3u) == 0 && (steps & 1) == 0;
     p.vecState = a.fwd.N % 4 == 0 && aligned(a.fwd.state, 16) && aligned(a.grad_final_state, 16) &&
                  aligned(a.grad_state, 16);
-    int32_t st = run_scan<kSummaryGrad>(p, a.fwd.dtype, pl.nl, stream);
+    int32_t st = run_scan<GradTile, kSummaryGrad>(p, a.fwd.dtype, pl.nl, stream);
     if (st == kOk)
         st = join(p, pl.nl, true, stream);
     if (st != kOk)

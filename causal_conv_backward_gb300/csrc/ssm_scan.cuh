@@ -2,11 +2,12 @@
 // their parameters, the tile loads and the sums over a channel's lanes.
 //
 // Layout of a block: NW warps; a channel's N states sit on NL lanes, four to a
-// lane, so a warp owns 32/NL channels and the block CB = 32 NW/NL, of one group
-// and one sequence. It walks one time chunk in tiles of TT rows. Loads, dt and
-// the gate are done once per (row, channel) by a thread that owns two adjacent
-// channels of RP rows of the tile; dt and dt*u reach the lanes of the
-// recurrence through shared memory, and y comes back the same way.
+// lane, and a lane holds them for K channels, so a warp owns 32 K/NL channels
+// and the block CB = 32 K NW/NL, of one group and one sequence. It walks one
+// time chunk in tiles of TT rows. Loads, dt and the gate are done once per
+// (row, channel) by a thread that owns two adjacent channels of RP rows of the
+// tile; dt and dt u reach the lanes of the recurrence through shared memory,
+// and y comes back the same way.
 #pragma once
 
 #include "ssm.h"
@@ -14,23 +15,35 @@
 
 namespace mcc1d {
 
-// Warps per block of the forward passes and of the backward. Small blocks share
-// out sequences of unequal length better; the backward's large ones halve its
-// partial sums of grad_B and grad_C.
-constexpr int kFwdWarps = 4, kBwdWarps = 8;
-
-template <int NL, int NW>
+template <int NL_, int NW, int K_, int TT_>
 struct ScanTile {
+    static constexpr int NL = NL_, K = K_, TT = TT_, WARPS = NW;
     static constexpr int THREADS = 32 * NW;
     static constexpr int NP = 4 * NL;              // states, padded
-    static constexpr int CW = 32 / NL;             // channels per warp
-    static constexpr int CB = NW * CW;             // channels per block
+    static constexpr int CL = 32 / NL;             // lanes of one state
+    static constexpr int CB = NW * CL * K;         // channels per block
     static constexpr int CP = CB / 2;              // channel pairs per row
     static constexpr int RG = THREADS / CP;        // rows of one pass over a tile
+    static constexpr int RP = TT / RG;             // rows per thread
+    static_assert(RG >= 1 && RP >= 1 && RG * CP == THREADS && RP * RG == TT, "a tile is whole passes");
+
+    // A lane's number among a channel's NL, and its (first) channel / K in the
+    // warp. Shared-memory loads of 8 and 16 bytes run at their full rate only
+    // where lanes one apart, or two apart, read the same address (measured:
+    // 2.1 against 4.0 cycles for 16 bytes): the states take lane bit 0 and the
+    // bits above the channels', so that dt (same channel) repeats one apart
+    // and B and C (same states) two apart.
+    __device__ __forceinline__ static int state_lane(int lane)
+    {
+        return NL == 1 ? 0 : (lane & 1) | ((lane / (2 * CL)) << 1);
+    }
+    __device__ __forceinline__ static int channel_lane(int lane) { return NL == 1 ? lane : (lane >> 1) % CL; }
 };
 
-// Rows per tile: eight (row, channel) elements per thread, at most 32 rows.
-__host__ __device__ constexpr int scan_tile_rows(int nl) { return nl < 4 ? 8 * nl : 32; }
+// Tiles of the backward: 8 warps (fewer would write more partial sums of
+// grad_B and grad_C), eight (row, channel) elements per thread, at most 32 rows.
+template <int NL>
+using BwdTile = ScanTile<NL, 8, 1, (NL < 4 ? 8 * NL : 32)>;
 
 // How blocks cover the channels.
 struct ScanGrid {
@@ -65,7 +78,7 @@ struct ScanWhere {
     int32_t nc;       // channels of the block inside the group
 };
 
-template <int NL, int NW>
+template <class T>
 __device__ __forceinline__ ScanWhere scan_where(const ScanParams &p)
 {
     ScanWhere w;
@@ -75,9 +88,9 @@ __device__ __forceinline__ ScanWhere scan_where(const ScanParams &p)
     w.b = q % p.B;
     w.chunk = q / p.B;
     w.g = w.blk / p.grid.blocks_per_group;
-    const int32_t in = (w.blk - w.g * p.grid.blocks_per_group) * ScanTile<NL, NW>::CB;
+    const int32_t in = (w.blk - w.g * p.grid.blocks_per_group) * T::CB;
     w.c0 = w.g * p.Hg + in;
-    w.nc = p.Hg - in < ScanTile<NL, NW>::CB ? p.Hg - in : ScanTile<NL, NW>::CB;
+    w.nc = p.Hg - in < T::CB ? p.Hg - in : T::CB;
     return w;
 }
 
@@ -135,39 +148,13 @@ __device__ __forceinline__ void store_states(float *row, int n0, int N, bool vec
         row[n0 + 3] = v.w;
 }
 
-// Sums v[0..K-1] over NL lanes whose numbers 0..NL-1 are the lane bits from
-// `bit` up; K and NL are powers of two. Each exchange halves what a lane
-// carries on, so K values cost K (1 - 1/NL) shuffles where K >= NL, not
-// K log2 NL. Lane number j is left with v[0..] = the sums of values
-// j K/NL .. (K >= NL), or with v[0] = that of value j % K (K < NL).
-template <int K, int NL>
-__device__ __forceinline__ void lanes_sum(float (&v)[K], int lane, int bit)
-{
-    constexpr int M = K < NL ? K : NL;
-    int n = K;
-#pragma unroll
-    for (int step = M / 2; step >= 1; step /= 2) {
-        const bool up = (lane & (step * bit)) != 0;
-        n /= 2;
-#pragma unroll
-        for (int i = 0; i < K / 2; ++i)
-            if (i < n) {
-                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, step * bit);
-            }
-    }
-#pragma unroll
-    for (int step = M; step < NL; step *= 2)
-        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step * bit);
-}
-
 // The rows of B and C of one tile on their way to shared memory. Rows whose
 // states start on 16 bytes and come in eights (p.bc8) move 16 bytes at a time,
 // others a pair or one at a time. Rows from `rows` on are zeros, as are states
 // past N. KC: C too, not B alone.
-template <int NL, int NW, int TT, bool KC>
+template <class T, bool KC>
 struct BcTile {
-    static constexpr int NP = 4 * NL, THREADS = 32 * NW, TENSORS = KC ? 2 : 1;
+    static constexpr int NP = T::NP, TT = T::TT, THREADS = T::THREADS, TENSORS = KC ? 2 : 1;
     static constexpr int PAIRS = TENSORS * TT * NP / 2, WORDS = (PAIRS + THREADS - 1) / THREADS;
     static constexpr int EIGHTS = NP >= 8 ? PAIRS / 4 : 0, VECS = (EIGHTS + THREADS - 1) / THREADS;
     static constexpr int N = WORDS > 4 * VECS ? WORDS : 4 * VECS;

@@ -25,28 +25,54 @@ namespace mcc1d {
 
 namespace {
 
-constexpr int kSub = 4, kThreads = 32 * kBwdWarps;
+constexpr int kSub = 4, kBwdWarps = BwdTile<1>::WARPS, kThreads = 32 * kBwdWarps;
 
 template <int NL>
 struct BwdShared {
-    using T = ScanTile<NL, kBwdWarps>;
-    static constexpr int TT = scan_tile_rows(NL);
+    using T = BwdTile<NL>;
+    static constexpr int TT = T::TT;
     float4 sq[TT][T::CB];                         // dt, dt u, dy -> sum A q, sum g B, y; dt
     float4 hs[TT / kSub][kThreads];           // states before each run of kSub rows
     float sB[TT][T::NP], sC[TT][T::NP];
     float bc[TT][kBwdWarps][2 * T::NP];          // a warp's grad_B and grad_C
 };
 
+// Sums v[0..K-1] over NL lanes whose numbers 0..NL-1 are the lane bits from
+// `bit` up; K and NL are powers of two. Each exchange halves what a lane
+// carries on, so K values cost K (1 - 1/NL) shuffles where K >= NL, not
+// K log2 NL. Lane number j is left with v[0..] = the sums of values
+// j K/NL .. (K >= NL), or with v[0] = that of value j % K (K < NL).
+template <int K, int NL>
+__device__ __forceinline__ void lanes_sum(float (&v)[K], int lane, int bit)
+{
+    constexpr int M = K < NL ? K : NL;
+    int n = K;
+#pragma unroll
+    for (int step = M / 2; step >= 1; step /= 2) {
+        const bool up = (lane & (step * bit)) != 0;
+        n /= 2;
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i)
+            if (i < n) {
+                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, step * bit);
+            }
+    }
+#pragma unroll
+    for (int step = M; step < NL; step *= 2)
+        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step * bit);
+}
+
 template <int DT, int NL, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanParams p)
 {
-    using T = ScanTile<NL, kBwdWarps>;
+    using T = BwdTile<NL>;
     using Sh = BwdShared<NL>;
-    constexpr int NP = T::NP, CW = T::CW, TT = Sh::TT, RP = TT / T::RG;
+    constexpr int NP = T::NP, CW = T::CL, TT = Sh::TT, RP = T::RP;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
-    const ScanWhere w = scan_where<NL, kBwdWarps>(p);
+    const ScanWhere w = scan_where<T>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = lane % NL, n0 = 4 * j, ci = lane / NL;
     const int cl = warp * CW + ci;
@@ -100,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanPara
         }
         uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
         {
-            BcTile<NL, kBwdWarps, TT, true> bc;
+            BcTile<T, true> bc;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
                 const int64_t t = t0 + pr + r * T::RG;
