@@ -28,6 +28,12 @@ int32_t launch_short_conv_bwd(const mcc1d_short_conv_bwd_args &a, void *workspac
 int32_t launch_short_conv_step(const mcc1d_short_conv_step_args &a, cudaStream_t stream);
 
 // ------------------------------------------------------------------ selective scan
+// How blocks cover the channels.
+struct ScanGrid {
+    int64_t blocks;           // over all groups
+    int32_t blocks_per_group;
+};
+
 // A channel's N states are spread over NL = 1, 2, 4, 8 or 16 lanes of a warp,
 // four to a lane (NP = 4 NL >= N, padded with zeros). Blocks walk one time
 // chunk of their channels in tiles of TT rows.
@@ -39,6 +45,7 @@ struct ScanPlan {
     uint64_t off_e, off_r, off_dt, off_cp, off_cpdt, off_ga, off_gd, off_bc;   // workspace, in bytes
     uint64_t bytes;
     int64_t most_blocks;      // of the largest grid
+    ScanGrid grid;            // of the passes
 };
 ScanPlan scan_plan(const mcc1d_scan_args &a);
 ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &a);

@@ -407,14 +407,9 @@ bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 // Tiles of a forward pass.
 template <int NL>
 using OutTile = ScanTile<NL, 4, 1, (NL < 4 ? 8 * NL : 32)>;
-// Tiles of the backward's first pass have the backward's rows.
-template <int NL>
-using GradTile = ScanTile<NL, 4, 1, BwdTile<NL>::TT>;
-
 template <class T, int MODE>
-int32_t run_tile(ScanParams p, int dtype, cudaStream_t s)
+int32_t run_tile(const ScanParams &p, int dtype, cudaStream_t s)
 {
-    p.grid = scan_grid(p.H, p.G, T::CB);
     const unsigned grid = (unsigned)(p.grid.blocks * p.B * p.chunks);
     if (dtype == 0) {
         if (p.pairs)
@@ -473,6 +468,14 @@ ScanPlan shape_plan(const mcc1d_scan_args &a)
     return p;
 }
 
+ScanGrid scan_grid(int64_t H, int64_t G, int cb)
+{
+    ScanGrid g;
+    g.blocks_per_group = (int32_t)((H / G + cb - 1) / cb);
+    g.blocks = G * g.blocks_per_group;
+    return g;
+}
+
 // Channels per block and rows per tile.
 template <template <int> class Tile>
 void tile_shape(int nl, int &cb, int &tt)
@@ -498,14 +501,6 @@ void cut(ScanPlan &p, int64_t chunks)
 
 }  // namespace
 
-ScanGrid scan_grid(int64_t H, int64_t G, int cb)
-{
-    ScanGrid g;
-    g.blocks_per_group = (int32_t)((H / G + cb - 1) / cb);
-    g.blocks = G * g.blocks_per_group;
-    return g;
-}
-
 ScanPlan scan_plan(const mcc1d_scan_args &a)
 {
     ScanPlan p = shape_plan(a);
@@ -514,7 +509,8 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
     int cb;
     tile_shape<OutTile>(p.nl, cb, p.tt);
     p.tiles = (a.S + p.tt - 1) / p.tt;
-    const int64_t rows = scan_grid(a.H, a.G, cb).blocks * a.B, warps = rows * OutTile<4>::WARPS;
+    p.grid = scan_grid(a.H, a.G, cb);
+    const int64_t rows = p.grid.blocks * a.B, warps = rows * OutTile<4>::WARPS;
     cut(p, warps >= 152 * 5 ? 1 : (152 * 12 + warps - 1) / warps);
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
@@ -531,13 +527,13 @@ ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
 {
     const mcc1d_scan_args &a = ba.fwd;
     ScanPlan p = shape_plan(a);
-    int cb, cb_first;
-    tile_shape<GradTile>(p.nl, cb_first, p.tt);
+    int cb;
     tile_shape<BwdTile>(p.nl, cb, p.tt);
     p.tiles = (a.S + p.tt - 1) / p.tt;
-    const int64_t blocks = scan_grid(a.H, a.G, cb).blocks, rows = blocks * a.B;
-    cut(p, (152 * 6 + rows - 1) / rows);
-    p.most_blocks = scan_grid(a.H, a.G, cb_first).blocks * a.B * p.chunks;
+    p.grid = scan_grid(a.H, a.G, cb);
+    const int64_t rows = p.grid.blocks * a.B;
+    cut(p, (152 * 12 + rows - 1) / rows);
+    p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
     p.off_e = take(off, (uint64_t)p.chunks * ch * p.np * 4);
@@ -547,7 +543,7 @@ ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
     p.off_cpdt = take(off, (uint64_t)p.tiles * ch * 4);
     p.off_ga = take(off, (uint64_t)p.chunks * ch * p.np * 4);
     p.off_gd = take(off, (uint64_t)p.chunks * ch * 8);
-    p.off_bc = take(off, (uint64_t)(a.S * a.B) * (uint64_t)blocks * 2u * p.np * 4);
+    p.off_bc = take(off, (uint64_t)(a.S * a.B) * (uint64_t)p.grid.blocks * 2u * p.np * 4);
     p.bytes = off;
     return p;
 }
@@ -578,6 +574,7 @@ static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint
     p.N = (int32_t)a.N;
     p.G = (int32_t)a.G;
     p.Hg = (int32_t)(a.H / a.G);
+    p.grid = pl.grid;
     p.tiles = pl.tiles;
     p.tiles_per_chunk = pl.tiles_per_chunk;
     p.chunks = pl.chunks;
@@ -642,7 +639,7 @@ int32_t launch_scan_bwd(const mcc1d_scan_bwd_args &a, const ScanPlan &pl, void *
     p.pairs = (any & 3u) == 0 && (steps & 1) == 0;
     p.vecState = a.fwd.N % 4 == 0 && aligned(a.fwd.state, 16) && aligned(a.grad_final_state, 16) &&
                  aligned(a.grad_state, 16);
-    int32_t st = run_scan<GradTile, kSummaryGrad>(p, a.fwd.dtype, pl.nl, stream);
+    int32_t st = run_scan<BwdTile, kSummaryGrad>(p, a.fwd.dtype, pl.nl, stream);
     if (st == kOk)
         st = join(p, pl.nl, true, stream);
     if (st != kOk)

@@ -40,17 +40,10 @@ struct ScanTile {
     __device__ __forceinline__ static int channel_lane(int lane) { return NL == 1 ? lane : (lane >> 1) % CL; }
 };
 
-// Tiles of the backward: 8 warps (fewer would write more partial sums of
-// grad_B and grad_C), eight (row, channel) elements per thread, at most 32 rows.
+// Tiles of the backward, and of the pass before it: two channels per lane, so
+// that grad_B's and grad_C's sums over channels start inside the lane.
 template <int NL>
-using BwdTile = ScanTile<NL, 8, 1, (NL < 4 ? 8 * NL : 32)>;
-
-// How blocks cover the channels.
-struct ScanGrid {
-    int64_t blocks;             // over all groups
-    int32_t blocks_per_group;
-};
-ScanGrid scan_grid(int64_t H, int64_t G, int cb);
+using BwdTile = ScanTile<NL, 4, 2, (NL < 8 ? 4 * NL : 32)>;
 
 struct ScanParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm, *gy;
@@ -68,7 +61,7 @@ struct ScanParams {
     int32_t vecA, vecState;               // rows of A (of the states) can be moved 16 bytes at a time
 };
 
-int32_t launch_scan_bwd_main(ScanParams p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s);
+int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s);
 
 // Where a block works.
 struct ScanWhere {

@@ -25,206 +25,231 @@ namespace mcc1d {
 
 namespace {
 
-constexpr int kSub = 4, kBwdWarps = BwdTile<1>::WARPS, kThreads = 32 * kBwdWarps;
+constexpr int kSub = 2;          // rows whose states and decays sit in registers
+constexpr int kBlocksPerSM = 3;
+
+// Sums v[0..N-1] over L lanes, N and L powers of two. The lanes' numbers are
+// made of the lane bits FIRST (the lowest), 2 REST, 4 REST and so on. Each
+// exchange halves what a lane carries on, so N values cost N (1 - 1/L)
+// shuffles where N >= L, not N log2 L. Lane number j is left with v[0..] = the
+// sums of values j N/L .. (N >= L), or with v[0] = that of value j % N (N < L).
+template <int N, int L, int FIRST, int REST>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int lane)
+{
+    constexpr int M = N < L ? N : L;
+    int n = N;
+#pragma unroll
+    for (int step = M / 2; step >= 1; step /= 2) {
+        const int mask = step == 1 ? FIRST : step * REST;
+        const bool up = (lane & mask) != 0;
+        n /= 2;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            if (i < n) {
+                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, mask);
+            }
+    }
+#pragma unroll
+    for (int step = M; step < L; step *= 2)
+        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step == 1 ? FIRST : step * REST);
+}
 
 template <int NL>
 struct BwdShared {
     using T = BwdTile<NL>;
     static constexpr int TT = T::TT;
-    float4 sq[TT][T::CB];                         // dt, dt u, dy -> sum A q, sum g B, y; dt
-    float4 hs[TT / kSub][kThreads];           // states before each run of kSub rows
+    float4 sq[TT][T::CB];                         // dt, dt u, dy, dt; the first three then sum A log2e q, sum g B, y
+    float4 hs[TT / kSub][T::K][T::THREADS];       // states before each run of kSub rows
     float sB[TT][T::NP], sC[TT][T::NP];
-    float bc[TT][kBwdWarps][2 * T::NP];          // a warp's grad_B and grad_C
+    float bc[TT][T::WARPS][2 * T::NP];            // a warp's grad_B and grad_C
 };
 
-// Sums v[0..K-1] over NL lanes whose numbers 0..NL-1 are the lane bits from
-// `bit` up; K and NL are powers of two. Each exchange halves what a lane
-// carries on, so K values cost K (1 - 1/NL) shuffles where K >= NL, not
-// K log2 NL. Lane number j is left with v[0..] = the sums of values
-// j K/NL .. (K >= NL), or with v[0] = that of value j % K (K < NL).
-template <int K, int NL>
-__device__ __forceinline__ void lanes_sum(float (&v)[K], int lane, int bit)
-{
-    constexpr int M = K < NL ? K : NL;
-    int n = K;
-#pragma unroll
-    for (int step = M / 2; step >= 1; step /= 2) {
-        const bool up = (lane & (step * bit)) != 0;
-        n /= 2;
-#pragma unroll
-        for (int i = 0; i < K / 2; ++i)
-            if (i < n) {
-                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, step * bit);
-            }
-    }
-#pragma unroll
-    for (int step = M; step < NL; step *= 2)
-        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step * bit);
-}
-
 template <int DT, int NL, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanParams p)
+__global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_scan_bwd(const ScanParams p)
 {
     using T = BwdTile<NL>;
     using Sh = BwdShared<NL>;
-    constexpr int NP = T::NP, CW = T::CL, TT = Sh::TT, RP = T::RP;
+    constexpr int NP = T::NP, CL = T::CL, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
     const ScanWhere w = scan_where<T>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = lane % NL, n0 = 4 * j, ci = lane / NL;
-    const int cl = warp * CW + ci;
+    const int j = T::state_lane(lane), n0 = 4 * j, ci = T::channel_lane(lane);
+    const int cl = (warp * CL + ci) * K;
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
     const int pc = 2 * (threadIdx.x % T::CP), pr = threadIdx.x / T::CP;
     const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
     const int64_t ch = w.c0 + (on0 ? pc : 0);
-    const uint16_t *u = p.u + w.b * p.ub + ch, *delta = p.delta + w.b * p.db + ch;
-    const uint16_t *z = p.z ? p.z + w.b * p.zb + ch : nullptr, *gy = p.gy + w.b * p.gb + ch;
     const uint16_t *Bm = p.Bm + w.b * p.Bb + w.g * p.Bg, *Cm = p.Cm + w.b * p.Cb + w.g * p.Cg;
-    const float bias0 = p.dbias && on0 ? p.dbias[ch] : 0.f, bias1 = p.dbias && on1 ? p.dbias[ch + 1] : 0.f;
-    const float D0 = p.D && on0 ? p.D[ch] : 0.f, D1 = p.D && on1 ? p.D[ch + 1] : 0.f;
+    float2 bias = make_float2(0.f, 0.f), D = make_float2(0.f, 0.f);
+    if (p.dbias)
+        bias = make_float2(on0 ? p.dbias[ch] : 0.f, on1 ? p.dbias[ch + 1] : 0.f);
+    if (p.D)
+        D = make_float2(on0 ? p.D[ch] : 0.f, on1 ? p.D[ch + 1] : 0.f);
 
-    const bool live = cl < w.nc;
-    const int64_t hc = w.c0 + (live ? cl : 0);
-    const int64_t at = (w.chunk * p.B + w.b) * p.H + hc;
-    float2 A[2], A2[2], X[2], gA[2], hin[2];
-    {
-        const float4 a = load_states(p.A + hc * p.N, n0, p.N, p.vecA);
-        A[0] = make_float2(a.x, a.y);
-        A[1] = make_float2(a.z, a.w);
-        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
-        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
-        const float4 x = *reinterpret_cast<const float4 *>(p.r + at * NP + n0);
-        X[0] = make_float2(x.x, x.y);
-        X[1] = make_float2(x.z, x.w);
-        const float4 s = *reinterpret_cast<const float4 *>(p.e + at * NP + n0);
-        hin[0] = make_float2(s.x, s.y);
-        hin[1] = make_float2(s.z, s.w);
-        gA[0] = gA[1] = make_float2(0.f, 0.f);
+    float2 A2[K][2], X[K][2], gA[K][2];
+    int64_t hc[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        hc[k] = w.b * p.H + w.c0 + (cl + k < w.nc ? cl + k : 0);
+        const float4 a = load_states(p.A + (hc[k] - w.b * p.H) * p.N, n0, p.N, p.vecA);
+        A2[k][0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+        A2[k][1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+        const float4 x = *reinterpret_cast<const float4 *>(p.r + (w.chunk * p.B * p.H + hc[k]) * NP + n0);
+        X[k][0] = make_float2(x.x, x.y);
+        X[k][1] = make_float2(x.z, x.w);
+        gA[k][0] = gA[k][1] = make_float2(0.f, 0.f);
     }
     float2 gD = make_float2(0.f, 0.f), gbias = make_float2(0.f, 0.f);
 
     const int64_t tile0 = w.chunk * p.tiles_per_chunk;
     const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
     for (int64_t tile = tile1 - 1; tile >= tile0; --tile) {
-        const int64_t t0 = tile * TT;
-        if (t0 >= te) {
+        const int64_t t0 = tile * TT, trow = t0 + pr;
+        const int rows = (int)(te - t0 < TT ? te - t0 : TT), all = (int)(p.S - t0 < TT ? p.S - t0 : TT);
+        const int64_t o0 = (trow * p.B + w.b) * p.H + ch, os = RG * p.B * p.H;
+        if (rows <= 0) {
+            int64_t o = o0;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                const int64_t t = t0 + pr + r * T::RG;
-                if (t < p.S) {
-                    const int64_t o = (t * p.B + w.b) * p.H + ch;
+            for (int r = 0; r < RP; ++r, o += os)
+                if (pr + r * RG < all) {
                     store_pair<PAIRS>(p.gu + o, 0u, on0, on1);
                     store_pair<PAIRS>(p.gdelta + o, 0u, on0, on1);
                     if (p.gz)
                         store_pair<PAIRS>(p.gz + o, 0u, on0, on1);
                 }
-            }
             continue;
         }
         uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
         {
             BcTile<T, true> bc;
+            const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
+            const uint16_t *z = p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr, *gy = p.gy + w.b * p.gb + ch + trow * p.gs;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-                const int64_t t = t0 + pr + r * T::RG;
-                const bool ok = t < te;
-                ru[r] = load_pair<PAIRS>(u + t * p.us, ok && on0, ok && on1);
-                rd[r] = load_pair<PAIRS>(delta + t * p.ds, ok && on0, ok && on1);
-                rz[r] = z ? load_pair<PAIRS>(z + t * p.zs, ok && on0, ok && on1) : 0u;
-                rg[r] = load_pair<PAIRS>(gy + t * p.gs, ok && on0, ok && on1);
+                const bool ok = pr + r * RG < rows;
+                ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
+                rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
+                rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
+                u += RG * p.us;
+                delta += RG * p.ds;
+                gy += RG * p.gs;
+                if (p.z) {
+                    rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
+                    z += RG * p.zs;
+                }
             }
-            bc.load(p, Bm + t0 * p.Bs, Cm + t0 * p.Cs, (int)(te - t0 < TT ? te - t0 : TT));
+            bc.load(p, Bm + t0 * p.Bs, Cm + t0 * p.Cs, rows);
             bc.template put<DT>(p, sh.sB, sh.sC);
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-            const int64_t t = t0 + pr + r * T::RG;
-            const float2 uv = unpack2<DT>(ru[r]);
-            float2 dt = add2(unpack2<DT>(rd[r]), make_float2(bias0, bias1)), g = unpack2<DT>(rg[r]);
+            const int row = pr + r * RG;
+            float2 dt = add2(unpack2<DT>(rd[r]), bias), g = unpack2<DT>(rg[r]);
             if (p.softplus)
                 dt = softplus2(dt);
-            if (t >= te)
+            if (row >= rows)
                 dt = make_float2(0.f, 0.f);
-            if (z) {
+            if (p.z) {
                 const float2 zv = unpack2<DT>(rz[r]);
-                g.x *= zv.x * sigmoid(zv.x);
-                g.y *= zv.y * sigmoid(zv.y);
+                g = mul2(g, mul2(zv, sigmoid2(zv)));
             }
-            sh.sq[pr + r * T::RG][pc] = make_float4(dt.x, dt.x * uv.x, g.x, dt.x);
-            sh.sq[pr + r * T::RG][pc + 1] = make_float4(dt.y, dt.y * uv.y, g.y, dt.y);
+            const float2 du = mul2(dt, unpack2<DT>(ru[r]));
+            sh.sq[row][pc] = make_float4(dt.x, du.x, g.x, dt.x);
+            sh.sq[row][pc + 1] = make_float4(dt.y, du.y, g.y, dt.y);
         }
         // the state at the tile's start: from the chunk's zero start, and what entered the chunk
-        float2 h[2];
-        {
-            const int64_t ct = (tile * p.B + w.b) * p.H + hc;
+        float2 h[K][2];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t ct = tile * p.B * p.H + hc[k];
             const float4 s = *reinterpret_cast<const float4 *>(p.cp + ct * NP + n0);
+            const float4 e = *reinterpret_cast<const float4 *>(p.e + (w.chunk * p.B * p.H + hc[k]) * NP + n0);
             const float d = p.cpdt[ct];
-            h[0].x = fmaf(ex2(d * A2[0].x), hin[0].x, s.x);
-            h[0].y = fmaf(ex2(d * A2[0].y), hin[0].y, s.y);
-            h[1].x = fmaf(ex2(d * A2[1].x), hin[1].x, s.z);
-            h[1].y = fmaf(ex2(d * A2[1].y), hin[1].y, s.w);
+            h[k][0] = fma2(make_float2(ex2(d * A2[k][0].x), ex2(d * A2[k][0].y)), make_float2(e.x, e.y), make_float2(s.x, s.y));
+            h[k][1] = fma2(make_float2(ex2(d * A2[k][1].x), ex2(d * A2[k][1].y)), make_float2(e.z, e.w), make_float2(s.z, s.w));
         }
         __syncthreads();
+#pragma unroll 1
         for (int s = 0; s < TT; s += kSub) {
-            sh.hs[s / kSub][threadIdx.x] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                sh.hs[s / kSub][k][threadIdx.x] = make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
             if (s + kSub == TT)
                 break;
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
-                const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl]);
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
-                const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
-                const float2 a0 = decay2(dt2, A2[0]), a1 = decay2(dt2, A2[1]);
-                h[0] = fma2(a0, h[0], mul2(du2, make_float2(bv.x, bv.y)));
-                h[1] = fma2(a1, h[1], mul2(du2, make_float2(bv.z, bv.w)));
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl + k]);
+                    const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
+                    h[k][0] = fma2(decay2(dt2, A2[k][0]), h[k][0], mul2(du2, make_float2(bv.x, bv.y)));
+                    h[k][1] = fma2(decay2(dt2, A2[k][1]), h[k][1], mul2(du2, make_float2(bv.z, bv.w)));
+                }
             }
         }
-        float2 tA[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // the tile's part of grad_A: short sums first
+        float2 tA[K][2];   // the tile's part of grad_A: short sums first
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            tA[k][0] = tA[k][1] = make_float2(0.f, 0.f);
+#pragma unroll 1
         for (int s = TT - kSub; s >= 0; s -= kSub) {
-            float2 hh[kSub + 1][2], aa[kSub][2];
-            float ys[kSub], sa[kSub], sb[kSub];
-            {
-                const float4 v = sh.hs[s / kSub][threadIdx.x];
-                hh[0][0] = make_float2(v.x, v.y);
-                hh[0][1] = make_float2(v.z, v.w);
+            float2 hh[kSub + 1][K][2], aa[kSub][K][2];
+            float ys[K * kSub], sa[K * kSub], sb[K * kSub];     // of (step, channel)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float4 v = sh.hs[s / kSub][k][threadIdx.x];
+                hh[0][k][0] = make_float2(v.x, v.y);
+                hh[0][k][1] = make_float2(v.z, v.w);
             }
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
-                const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl]);
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
                 const float4 cv = *reinterpret_cast<const float4 *>(&sh.sC[s + i][n0]);
-                const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
-                aa[i][0] = decay2(dt2, A2[0]);
-                aa[i][1] = decay2(dt2, A2[1]);
-                hh[i + 1][0] = fma2(aa[i][0], hh[i][0], mul2(du2, make_float2(bv.x, bv.y)));
-                hh[i + 1][1] = fma2(aa[i][1], hh[i][1], mul2(du2, make_float2(bv.z, bv.w)));
-                const float2 y = fma2(hh[i + 1][0], make_float2(cv.x, cv.y), mul2(hh[i + 1][1], make_float2(cv.z, cv.w)));
-                ys[i] = y.x + y.y;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl + k]);
+                    const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
+                    aa[i][k][0] = decay2(dt2, A2[k][0]);
+                    aa[i][k][1] = decay2(dt2, A2[k][1]);
+                    hh[i + 1][k][0] = fma2(aa[i][k][0], hh[i][k][0], mul2(du2, make_float2(bv.x, bv.y)));
+                    hh[i + 1][k][1] = fma2(aa[i][k][1], hh[i][k][1], mul2(du2, make_float2(bv.z, bv.w)));
+                    const float2 y = fma2(hh[i + 1][k][0], make_float2(cv.x, cv.y),
+                                          mul2(hh[i + 1][k][1], make_float2(cv.z, cv.w)));
+                    ys[i * K + k] = y.x + y.y;
+                }
             }
 #pragma unroll
             for (int i = kSub - 1; i >= 0; --i) {
-                const float4 dd = sh.sq[s + i][cl];
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
                 const float4 cv = *reinterpret_cast<const float4 *>(&sh.sC[s + i][n0]);
-                const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y), dy2 = make_float2(dd.z, dd.z);
-                const float2 g0 = fma2(dy2, make_float2(cv.x, cv.y), X[0]), g1 = fma2(dy2, make_float2(cv.z, cv.w), X[1]);
-                const float2 b2 = fma2(g0, make_float2(bv.x, bv.y), mul2(g1, make_float2(bv.z, bv.w)));
-                sb[i] = b2.x + b2.y;
-                X[0] = mul2(aa[i][0], g0);
-                X[1] = mul2(aa[i][1], g1);
-                const float2 q0 = mul2(X[0], hh[i][0]), q1 = mul2(X[1], hh[i][1]);
-                const float2 a2 = fma2(A[0], q0, mul2(A[1], q1));
-                sa[i] = a2.x + a2.y;
-                tA[0] = fma2(dt2, q0, tA[0]);
-                tA[1] = fma2(dt2, q1, tA[1]);
-                const float2 v0 = mul2(g0, du2), v1 = mul2(g1, du2);
-                const float2 c0 = mul2(hh[i + 1][0], dy2), c1 = mul2(hh[i + 1][1], dy2);
+                float2 v0, v1, c0, c1;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float4 dd = sh.sq[s + i][cl + k];
+                    const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y), dy2 = make_float2(dd.z, dd.z);
+                    const float2 g0 = fma2(dy2, make_float2(cv.x, cv.y), X[k][0]);
+                    const float2 g1 = fma2(dy2, make_float2(cv.z, cv.w), X[k][1]);
+                    const float2 b2 = fma2(g0, make_float2(bv.x, bv.y), mul2(g1, make_float2(bv.z, bv.w)));
+                    sb[i * K + k] = b2.x + b2.y;
+                    X[k][0] = mul2(aa[i][k][0], g0);
+                    X[k][1] = mul2(aa[i][k][1], g1);
+                    const float2 q0 = mul2(X[k][0], hh[i][k][0]), q1 = mul2(X[k][1], hh[i][k][1]);
+                    const float2 a2 = fma2(A2[k][0], q0, mul2(A2[k][1], q1));
+                    sa[i * K + k] = a2.x + a2.y;
+                    tA[k][0] = fma2(dt2, q0, tA[k][0]);
+                    tA[k][1] = fma2(dt2, q1, tA[k][1]);
+                    v0 = k == 0 ? mul2(g0, du2) : fma2(g0, du2, v0);
+                    v1 = k == 0 ? mul2(g1, du2) : fma2(g1, du2, v1);
+                    c0 = k == 0 ? mul2(hh[i + 1][k][0], dy2) : fma2(hh[i + 1][k][0], dy2, c0);
+                    c1 = k == 0 ? mul2(hh[i + 1][k][1], dy2) : fma2(hh[i + 1][k][1], dy2, c1);
+                }
                 float v[8] = {v0.x, v0.y, v1.x, v1.y, c0.x, c0.y, c1.x, c1.y};
-                lanes_sum<8, CW>(v, lane, NL);
-                constexpr int KEEP = CW >= 8 ? 1 : 8 / CW;
+                lanes_sum<8, CL, NL == 1 ? 1 : 2, NL == 1 ? 1 : 2>(v, lane);
+                constexpr int KEEP = CL >= 8 ? 1 : 8 / CL;
                 if (ci < 8) {
                     const int k = (ci * KEEP) % 8;      // v[0..KEEP-1] are values k.. of the eight
                     float *o = &sh.bc[s + i][warp][(k / 4) * NP + n0 + k % 4];
@@ -233,71 +258,75 @@ __global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanPara
                         o[m] = v[m];
                 }
             }
-            lanes_sum<kSub, NL>(ys, lane, 1);
-            lanes_sum<kSub, NL>(sa, lane, 1);
-            lanes_sum<kSub, NL>(sb, lane, 1);
-            constexpr int OWN = NL >= kSub ? 1 : kSub / NL;
-            if (j < kSub) {
+            constexpr int N = K * kSub, OWN = NL >= N ? 1 : N / NL;
+            lanes_sum<N, NL, 1, CL>(ys, lane);
+            lanes_sum<N, NL, 1, CL>(sa, lane);
+            lanes_sum<N, NL, 1, CL>(sb, lane);
+            if (j < N) {
 #pragma unroll
                 for (int m = 0; m < OWN; ++m) {
-                    float *o = reinterpret_cast<float *>(&sh.sq[s + j * OWN + m][cl]);
+                    const int q = j * OWN + m;          // (step, channel)
+                    float *o = reinterpret_cast<float *>(&sh.sq[s + q / K][cl + q % K]);
                     *reinterpret_cast<float2 *>(o) = make_float2(sa[m], sb[m]);
                     o[2] = ys[m];
                 }
             }
             __syncwarp();
         }
-        gA[0] = add2(gA[0], tA[0]);
-        gA[1] = add2(gA[1], tA[1]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            gA[k][0] = add2(gA[k][0], tA[k][0]);
+            gA[k][1] = add2(gA[k][1], tA[k][1]);
+        }
         __syncthreads();
-        for (int i = threadIdx.x; i < TT * 2 * NP; i += kThreads) {
+        for (int i = threadIdx.x; i < TT * 2 * NP; i += T::THREADS) {
             const int row = i / (2 * NP), k = i % (2 * NP);
             float s = sh.bc[row][0][k];
 #pragma unroll
-            for (int q = 1; q < kBwdWarps; ++q)
+            for (int q = 1; q < T::WARPS; ++q)
                 s += sh.bc[row][q][k];
-            if (t0 + row < te)
+            if (row < rows)
                 p.bc[(((t0 + row) * p.B + w.b) * p.grid.blocks + w.blk) * (2 * NP) + k] = s;
         }
+        int64_t o = o0;
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            const int64_t t = t0 + pr + r * T::RG;
-            const float4 s0 = sh.sq[pr + r * T::RG][pc], s1 = sh.sq[pr + r * T::RG][pc + 1];
-            const float2 uv = unpack2<DT>(ru[r]);
-            float2 raw = unpack2<DT>(rd[r]);
-            raw.x += bias0;
-            raw.y += bias1;
+        for (int r = 0; r < RP; ++r, o += os) {
+            const int row = pr + r * RG;
+            const float4 s0 = sh.sq[row][pc], s1 = sh.sq[row][pc + 1];
+            const float2 uv = unpack2<DT>(ru[r]), raw = add2(unpack2<DT>(rd[r]), bias), sb = make_float2(s0.y, s1.y);
+            const bool in = row < rows;
             float2 dy = unpack2<DT>(rg[r]);
-            if (z) {
-                const float2 zv = unpack2<DT>(rz[r]);
-                const float sx = sigmoid(zv.x), sy = sigmoid(zv.y);
-                const float2 gz = make_float2(dy.x * fmaf(D0, uv.x, s0.z) * sx * fmaf(zv.x, 1.f - sx, 1.f),
-                                              dy.y * fmaf(D1, uv.y, s1.z) * sy * fmaf(zv.y, 1.f - sy, 1.f));
-                if (p.gz && t < p.S)
-                    store_pair<PAIRS>(p.gz + (t * p.B + w.b) * p.H + ch, t < te ? pack2<DT>(gz) : 0u, on0, on1);
-                dy.x *= zv.x * sx;
-                dy.y *= zv.y * sy;
+            if (p.z) {
+                const float2 zv = unpack2<DT>(rz[r]), sz = sigmoid2(zv), one = make_float2(1.f, 1.f);
+                if (p.gz && row < all) {
+                    // d/dz [z sz] = sz (1 + z (1 - sz))
+                    const float2 d = mul2(sz, fma2(zv, make_float2(1.f - sz.x, 1.f - sz.y), one));
+                    const float2 gz = mul2(mul2(dy, fma2(D, uv, make_float2(s0.z, s1.z))), d);
+                    store_pair<PAIRS>(p.gz + o, in ? pack2<DT>(gz) : 0u, on0, on1);
+                }
+                dy = mul2(dy, mul2(zv, sz));
             }
-            float2 gr = make_float2(fmaf(uv.x, s0.y, s0.x), fmaf(uv.y, s1.y, s1.x));
-            if (p.softplus) {
-                gr.x *= raw.x > 20.f ? 1.f : sigmoid(raw.x);
-                gr.y *= raw.y > 20.f ? 1.f : sigmoid(raw.y);
-            }
-            const float2 gu = make_float2(fmaf(s0.w, s0.y, D0 * dy.x), fmaf(s1.w, s1.y, D1 * dy.y));
-            if (t < te) {
+            constexpr float ln2 = 0.693147181f;
+            float2 gr = fma2(uv, sb, mul2(make_float2(s0.x, s1.x), make_float2(ln2, ln2)));
+            if (p.softplus)
+                gr = mul2(gr, sigmoid2(raw));
+            const float2 gu = fma2(make_float2(s0.w, s1.w), sb, mul2(D, dy));
+            if (in) {
                 gD = fma2(dy, uv, gD);
                 gbias = add2(gbias, gr);
             }
-            if (t < p.S) {
-                const int64_t o = (t * p.B + w.b) * p.H + ch;
-                store_pair<PAIRS>(p.gu + o, t < te ? pack2<DT>(gu) : 0u, on0, on1);
-                store_pair<PAIRS>(p.gdelta + o, t < te ? pack2<DT>(gr) : 0u, on0, on1);
+            if (row < all) {
+                store_pair<PAIRS>(p.gu + o, in ? pack2<DT>(gu) : 0u, on0, on1);
+                store_pair<PAIRS>(p.gdelta + o, in ? pack2<DT>(gr) : 0u, on0, on1);
             }
         }
         __syncthreads();   // bc is written again in the next tile
     }
-    if (live)
-        *reinterpret_cast<float4 *>(p.ga + at * NP + n0) = make_float4(gA[0].x, gA[0].y, gA[1].x, gA[1].y);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (cl + k < w.nc)
+            *reinterpret_cast<float4 *>(p.ga + (w.chunk * p.B * p.H + hc[k]) * NP + n0) =
+                make_float4(gA[k][0].x, gA[k][0].y, gA[k][1].x, gA[k][1].y);
     // grad_D and grad_delta_bias over the threads that share channels
     float4 *red = &sh.sq[0][0];
     __syncthreads();
@@ -305,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) mcc1d_ssm_scan_bwd(const ScanPara
     __syncthreads();
     if (pr == 0) {
         float4 s = red[pc / 2];
-        for (int k = 1; k < T::RG; ++k) {
+        for (int k = 1; k < RG; ++k) {
             const float4 v = red[k * T::CP + pc / 2];
             s.x += v.x;
             s.y += v.y;
@@ -380,7 +409,7 @@ int32_t run_pairs(const ScanParams &p, cudaStream_t s)
     if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
         return kErrCuda;
-    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), kThreads, bytes, s>>>(p);
+    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), BwdTile<NL>::THREADS, bytes, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
@@ -404,9 +433,8 @@ int32_t run_nl(const ScanParams &p, int nl, cudaStream_t s)
 
 }  // namespace
 
-int32_t launch_scan_bwd_main(ScanParams p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s)
+int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s)
 {
-    p.grid = scan_grid(p.H, p.G, kThreads / pl.nl);
     const int32_t st = a.fwd.dtype == 0 ? run_nl<0>(p, pl.nl, s) : run_nl<1>(p, pl.nl, s);
     if (st != kOk)
         return st;
