@@ -3,12 +3,12 @@ checks and marshalling over the C ABI of ``include/mcc1d_ssm.h``."""
 from __future__ import annotations
 
 import ctypes
+import struct
 from collections import namedtuple
 
 from ._lib import Mcc1dError, load as _load_lib
 
 SILU, SOFTPLUS = 1, 2
-MAX_W, MAX_N = 8, 64
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -46,13 +46,38 @@ ScanStepArgs = _struct("ScanStepArgs", "Mirror of ``mcc1d_scan_step_args``.", [
 ShortConvGrads = namedtuple("ShortConvGrads", "x weight bias state")
 SelectiveScanGrads = namedtuple("SelectiveScanGrads", "u delta A B C D z delta_bias state")
 
+
+
+def _packer(cls):
+    """struct.pack for the fields of ``cls``: the calls build their descriptor
+    as one bytes object, several times faster than filling a ctypes structure."""
+    def codes(c):
+        out = ""
+        for _, kind in c._fields_:
+            if hasattr(kind, "_fields_"):
+                out += codes(kind)
+            elif kind is _vp:
+                out += "P"
+            else:
+                n = getattr(kind, "_length_", 1)
+                out += ("q" if ctypes.sizeof(kind) // n == 8 else "i") * n
+        return out
+    s = struct.Struct("@" + codes(cls))
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_conv, _pack_conv_bwd, _pack_conv_step = (_packer(c) for c in (ShortConvArgs, ShortConvBwdArgs, ShortConvStepArgs))
+_pack_scan, _pack_scan_bwd, _pack_scan_step = (_packer(c) for c in (ScanArgs, ScanBwdArgs, ScanStepArgs))
+
 _lib = None
 _torch = None
+_raw_stream = None
 
 
 def _load():
     """The library with this module's prototypes, and torch."""
-    global _lib, _torch
+    global _lib, _torch, _raw_stream
     if _lib is None:
         import torch
         lib = _load_lib()
@@ -64,6 +89,9 @@ def _load():
         for name in ("short_conv_bwd", "scan", "scan_bwd"):
             f = getattr(lib, f"mcc1d_{name}_workspace_size")
             f.argtypes, f.restype = [_vp, size], _i32
+        # the current stream's handle without a Stream object around it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch, _lib = torch, lib
     return _lib
 
@@ -77,35 +105,46 @@ def _code(t, name):
     raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
 
 
-def _check(t, name, shape, dtype, device, dense=True):
-    """`t` has this shape, dtype and device, and is dense (or at least has
-    adjacent elements along its last axis)."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+def _refuse(t, name, shape, dtype, index):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if dense:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif shape[-1] > 1 and t.stride(-1) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(t, name, shape, dtype, index):
+    """The address of a dense tensor of this shape, dtype and device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, index)
+    return t.data_ptr()
+
+
+def _optional(t, name, shape, dtype, index):
+    return 0 if t is None else _dense(t, name, shape, dtype, index)
+
+
+def _rows(t, name, shape, dtype, index):
+    """The address of a tensor with adjacent elements along its last axis."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index)
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have adjacent elements along its last axis (stride 1, not {t.stride(-1)})")
+    return t.data_ptr()
 
 
 def _first(t, name, dims):
-    """Dims, dtype code and device of the leading tensor."""
+    """Shape, dtype code and device of the leading tensor."""
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape = t.shape
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have adjacent elements along its last axis (stride 1, not {t.stride(-1)})")
-    return t.shape, _code(t, name), t.device
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return shape, _code(t, name), t.get_device()
 
 
 def _flag(activation):
@@ -116,52 +155,42 @@ def _flag(activation):
     raise ValueError(f"activation must be 'silu' or None, not {activation!r}")
 
 
-def _optional(t, name, shape, dtype, device):
-    if t is not None:
-        _check(t, name, shape, dtype, device)
-
-
 # ------------------------------------------------------------------ streams and workspaces
-def _stream(stream, device):
-    """The stream's handle, and the torch stream to record tensors on where it
-    is not the current one (their memory must not be reused before it is done)."""
+def _stream(stream, index):
+    """The stream's handle, and the torch stream to record tensors on where one
+    was given (their memory must not be reused before it is done)."""
     if stream is None:
-        return _torch.cuda.current_stream(device).cuda_stream, None
+        return _raw_stream(index), None
     if isinstance(stream, int):
-        stream = _torch.cuda.ExternalStream(stream, device=device) if stream else _torch.cuda.default_stream(device)
+        stream = _torch.cuda.ExternalStream(stream, device=index) if stream else _torch.cuda.default_stream(index)
     return stream.cuda_stream, stream
 
 
 def _record(stream, *tensors):
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _call(name, args, handle):
-    st = getattr(_lib, name)(ctypes.byref(args), handle or None)
+    st = getattr(_lib, name)(args, handle)
     if st != 0:
         raise Mcc1dError(st, name)
 
 
 def _call_ws(name, args, handle, stream, device):
     """The two phases: sizes the workspace, takes it from torch, enqueues."""
-    n = ctypes.c_uint64(0)
-    st = getattr(_lib, name + "_workspace_size")(ctypes.byref(args), ctypes.byref(n))
+    n = ctypes.c_uint64()
+    st = getattr(_lib, name + "_workspace_size")(args, n)
     if st != 0:
         raise Mcc1dError(st, name + "_workspace_size")
-    ws = _torch.empty(n.value, dtype=_torch.uint8, device=device) if n.value else None
-    st = getattr(_lib, name)(ctypes.byref(args), _ptr(ws), n.value, handle or None)
+    n = n.value
+    ws = _torch.empty(n, dtype=_torch.uint8, device=device) if n else None
+    st = getattr(_lib, name)(args, ws.data_ptr() if n else 0, n, handle)
     if st != 0:
         raise Mcc1dError(st, name)
-    _record(stream, ws)
-
-
-def _strides(t, dims):
-    """Strides of the leading axes; those of axes of one element do not matter."""
-    st, sh = t.stride(), t.shape
-    return tuple(st[i] if sh[i] > 1 else 0 for i in range(dims))
+    if stream is not None:
+        _record(stream, ws)
 
 
 # ------------------------------------------------------------------ short convolution
@@ -176,22 +205,20 @@ def short_conv(x, weight, bias=None, *, activation="silu", lengths=None, state=N
     last W-1 rows, which continue the sequence in another call or in
     ``short_conv_step``."""
     _load()
-    (S, B, H), code, dev = _first(x, "x", 3)
-    W, dt = weight.shape[0], x.dtype
-    _check(weight, "weight", (W, H), dt, dev)
-    _optional(bias, "bias", (H,), dt, dev)
-    _optional(state, "state", (B, W - 1, H), dt, dev)
-    _optional(lengths, "lengths", (B,), _torch.int32, dev)
-    _optional(y, "y", (S, B, H), dt, dev)
-    flags = _flag(activation)
-    handle, stream = _stream(stream, dev)
+    shape, code, index = _first(x, "x", 3)
+    S, B, H = shape
+    W, dt, device = weight.shape[0], x.dtype, x.device
     if y is None:
-        y = _torch.empty((S, B, H), dtype=dt, device=dev)
-    final = _torch.empty((B, W - 1, H), dtype=dt, device=dev) if return_state else None
-    args = ShortConvArgs(x.data_ptr(), _strides(x, 2), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
-                         y.data_ptr(), _ptr(final), S, B, H, W, code, flags)
+        y = _torch.empty(shape, dtype=dt, device=device)
+    final = _torch.empty((B, W - 1, H), dtype=dt, device=device) if return_state else None
+    args = _pack_conv(x.data_ptr(), x.stride(0), x.stride(1), _dense(weight, "weight", (W, H), dt, index),
+                      _optional(bias, "bias", (H,), dt, index), _optional(state, "state", (B, W - 1, H), dt, index),
+                      _optional(lengths, "lengths", (B,), _torch.int32, index), _dense(y, "y", shape, dt, index),
+                      0 if final is None else final.data_ptr(), S, B, H, W, code, _flag(activation))
+    handle, stream = _stream(stream, index)
     _call("mcc1d_short_conv", args, handle)
-    _record(stream, x, weight, bias, state, lengths, y, final)
+    if stream is not None:
+        _record(stream, x, weight, bias, state, lengths, y, final)
     return (y, final) if return_state else y
 
 
@@ -202,37 +229,37 @@ def short_conv_backward(grad_y, x, weight, bias=None, *, activation="silu", leng
     ``ShortConvGrads(x, weight, bias, state)``; bias and state are None where
     the argument was."""
     _load()
-    (S, B, H), code, dev = _first(x, "x", 3)
-    W, dt = weight.shape[0], x.dtype
-    _check(weight, "weight", (W, H), dt, dev)
-    _check(grad_y, "grad_y", (S, B, H), dt, dev, dense=False)
-    _optional(bias, "bias", (H,), dt, dev)
-    _optional(state, "state", (B, W - 1, H), dt, dev)
-    _optional(lengths, "lengths", (B,), _torch.int32, dev)
-    _optional(grad_final_state, "grad_final_state", (B, W - 1, H), dt, dev)
-    flags = _flag(activation)
-    handle, stream = _stream(stream, dev)
-    gx = _torch.empty((S, B, H), dtype=dt, device=dev)
-    gw = _torch.empty((W, H), dtype=dt, device=dev)
-    gb = _torch.empty((H,), dtype=dt, device=dev) if bias is not None else None
-    gs = _torch.empty((B, W - 1, H), dtype=dt, device=dev) if state is not None else None
-    args = ShortConvBwdArgs(grad_y.data_ptr(), _strides(grad_y, 2), x.data_ptr(), _strides(x, 2), weight.data_ptr(),
-                            _ptr(bias), _ptr(state), _ptr(lengths), _ptr(grad_final_state), gx.data_ptr(),
-                            gw.data_ptr(), _ptr(gb), _ptr(gs), S, B, H, W, code, flags)
-    _call_ws("mcc1d_short_conv_bwd", args, handle, stream, dev)
-    _record(stream, grad_y, x, weight, bias, state, lengths, grad_final_state, gx, gw, gb, gs)
+    shape, code, index = _first(x, "x", 3)
+    S, B, H = shape
+    W, dt, device = weight.shape[0], x.dtype, x.device
+    gx = _torch.empty(shape, dtype=dt, device=device)
+    gw = _torch.empty((W, H), dtype=dt, device=device)
+    gb = _torch.empty((H,), dtype=dt, device=device) if bias is not None else None
+    gs = _torch.empty((B, W - 1, H), dtype=dt, device=device) if state is not None else None
+    args = _pack_conv_bwd(_rows(grad_y, "grad_y", shape, dt, index), grad_y.stride(0), grad_y.stride(1), x.data_ptr(),
+                          x.stride(0), x.stride(1), _dense(weight, "weight", (W, H), dt, index),
+                          _optional(bias, "bias", (H,), dt, index), _optional(state, "state", (B, W - 1, H), dt, index),
+                          _optional(lengths, "lengths", (B,), _torch.int32, index),
+                          _optional(grad_final_state, "grad_final_state", (B, W - 1, H), dt, index), gx.data_ptr(),
+                          gw.data_ptr(), 0 if gb is None else gb.data_ptr(), 0 if gs is None else gs.data_ptr(),
+                          S, B, H, W, code, _flag(activation))
+    handle, stream = _stream(stream, index)
+    _call_ws("mcc1d_short_conv_bwd", args, handle, stream, device)
+    if stream is not None:
+        _record(stream, grad_y, x, weight, bias, state, lengths, grad_final_state, gx, gw, gb, gs)
     return ShortConvGrads(gx, gw, gb, gs)
 
 
-def _cache(state, name, tail, dtype, device, B, slots):
-    """Rows of a cache [rows, *tail] that serves B sequences."""
+def _cache(state, tail, dtype, index, B, slots):
+    """Address and rows of a cache [rows, *tail] that serves B sequences, and
+    the address of the rows' slots."""
     rows = state.shape[0] if state.dim() else 0
-    _check(state, name, (rows, *tail), dtype, device)
+    at = _dense(state, "state", (rows, *tail), dtype, index)
     if slots is not None:
-        _check(slots, "slots", (B,), _torch.int32, device)
-    elif rows < B:
-        raise ValueError(f"{name} has {rows} rows for {B} sequences")
-    return rows
+        return at, rows, _dense(slots, "slots", (B,), _torch.int32, index)
+    if rows < B:
+        raise ValueError(f"state has {rows} rows for {B} sequences")
+    return at, rows, 0
 
 
 def short_conv_step(x, state, weight, bias=None, *, activation="silu", slots=None, y=None, stream=None):
@@ -241,44 +268,40 @@ def short_conv_step(x, state, weight, bias=None, *, activation="silu", slots=Non
     is moved on in place. A slot outside the cache marks a padding row: y is
     zero, no state changes. Two rows must not name one slot. Returns y [B,H]."""
     _load()
-    (B, H), code, dev = _first(x, "x", 2)
+    shape, code, index = _first(x, "x", 2)
+    B, H = shape
     W, dt = weight.shape[0], x.dtype
-    _check(weight, "weight", (W, H), dt, dev)
-    _optional(bias, "bias", (H,), dt, dev)
-    _optional(y, "y", (B, H), dt, dev)
-    rows = _cache(state, "state", (W - 1, H), dt, dev, B, slots)
-    flags = _flag(activation)
-    handle, stream = _stream(stream, dev)
     if y is None:
-        y = _torch.empty((B, H), dtype=dt, device=dev)
-    args = ShortConvStepArgs(x.data_ptr(), _strides(x, 1)[0], _ptr(state), weight.data_ptr(), _ptr(bias), _ptr(slots),
-                             y.data_ptr(), rows, B, H, W, code, flags)
+        y = _torch.empty(shape, dtype=dt, device=x.device)
+    cache, rows, at = _cache(state, (W - 1, H), dt, index, B, slots)
+    args = _pack_conv_step(x.data_ptr(), x.stride(0), cache, _dense(weight, "weight", (W, H), dt, index),
+                           _optional(bias, "bias", (H,), dt, index), at, _dense(y, "y", shape, dt, index), rows, B, H,
+                           W, code, _flag(activation))
+    handle, stream = _stream(stream, index)
     _call("mcc1d_short_conv_step", args, handle)
-    _record(stream, x, state, weight, bias, slots, y)
+    if stream is not None:
+        _record(stream, x, state, weight, bias, slots, y)
     return y
 
 
 # ------------------------------------------------------------------ selective scan
-def _scan_args(u, delta, A, B, C, D, z, delta_bias, softplus, lengths, state, y, final):
-    (S, nb, H), code, dev = _first(u, "u", 3)
+def _scan_fields(u, delta, A, B, C, D, z, delta_bias, softplus, lengths, state, y, final):
+    """The descriptor's fields, in order."""
+    shape, code, index = _first(u, "u", 3)
+    S, nb, H = shape
     dt, f32 = u.dtype, _torch.float32
     if A.dim() != 2 or B.dim() != 4:
         raise ValueError("A must be [H,N] and B, C [S,B,G,N]")
     N, G = A.shape[1], B.shape[2]
-    _check(A, "A", (H, N), f32, dev)
-    _check(delta, "delta", (S, nb, H), dt, dev, dense=False)
-    _check(B, "B", (S, nb, G, N), dt, dev, dense=False)
-    _check(C, "C", (S, nb, G, N), dt, dev, dense=False)
-    if z is not None:
-        _check(z, "z", (S, nb, H), dt, dev, dense=False)
-    _optional(D, "D", (H,), f32, dev)
-    _optional(delta_bias, "delta_bias", (H,), f32, dev)
-    _optional(lengths, "lengths", (nb,), _torch.int32, dev)
-    _optional(state, "state", (nb, H, N), f32, dev)
-    return ScanArgs(u.data_ptr(), _strides(u, 2), delta.data_ptr(), _strides(delta, 2), _ptr(z),
-                    _strides(z, 2) if z is not None else (0, 0), B.data_ptr(), _strides(B, 3), C.data_ptr(),
-                    _strides(C, 3), A.data_ptr(), _ptr(D), _ptr(delta_bias), _ptr(state), _ptr(lengths), _ptr(y),
-                    _ptr(final), S, nb, H, N, G, code, SOFTPLUS if softplus else 0)
+    bc = (S, nb, G, N)
+    return (u.data_ptr(), u.stride(0), u.stride(1), _rows(delta, "delta", shape, dt, index), delta.stride(0),
+            delta.stride(1), *((0, 0, 0) if z is None else (_rows(z, "z", shape, dt, index), z.stride(0), z.stride(1))),
+            _rows(B, "B", bc, dt, index), B.stride(0), B.stride(1), B.stride(2),
+            _rows(C, "C", bc, dt, index), C.stride(0), C.stride(1), C.stride(2), _dense(A, "A", (H, N), f32, index),
+            _optional(D, "D", (H,), f32, index), _optional(delta_bias, "delta_bias", (H,), f32, index),
+            _optional(state, "state", (nb, H, N), f32, index), _optional(lengths, "lengths", (nb,), _torch.int32, index),
+            _optional(y, "y", shape, dt, index), 0 if final is None else final.data_ptr(), S, nb, H, N, G, code,
+            SOFTPLUS if softplus else 0)
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, delta_softplus=False, lengths=None,
@@ -293,15 +316,16 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, delta_
     lengths[b] tokens: y is zero past the end, nothing is read there. Returns
     y, or (y, final_state) with ``return_state``."""
     _load()
-    S, nb, H = u.shape if u.dim() == 3 else (0, 0, 0)
-    _optional(y, "y", (S, nb, H), u.dtype, u.device)
-    if y is None and u.is_cuda:
-        y = _torch.empty((S, nb, H), dtype=u.dtype, device=u.device)
-    final = _torch.empty((nb, H, A.shape[-1]), dtype=_torch.float32, device=u.device) if return_state else None
-    args = _scan_args(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, y, final)
-    handle, stream = _stream(stream, u.device)
-    _call_ws("mcc1d_scan", args, handle, stream, u.device)
-    _record(stream, u, delta, A, B, C, D, z, delta_bias, lengths, state, y, final)
+    (S, nb, H), _, index = _first(u, "u", 3)
+    device = u.device
+    if y is None:
+        y = _torch.empty((S, nb, H), dtype=u.dtype, device=device)
+    final = _torch.empty((nb, H, A.shape[-1]), dtype=_torch.float32, device=device) if return_state else None
+    args = _pack_scan(*_scan_fields(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, y, final))
+    handle, stream = _stream(stream, index)
+    _call_ws("mcc1d_scan", args, handle, stream, device)
+    if stream is not None:
+        _record(stream, u, delta, A, B, C, D, z, delta_bias, lengths, state, y, final)
     return (y, final) if return_state else y
 
 
@@ -312,23 +336,25 @@ def selective_scan_backward(grad_y, u, delta, A, B, C, D=None, z=None, delta_bia
     ``SelectiveScanGrads(u, delta, A, B, C, D, z, delta_bias, state)`` with None
     where the argument was None; A, D, delta_bias and state are fp32."""
     _load()
-    fwd = _scan_args(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, None, None)
-    (S, nb, H), dev, dt, f32 = u.shape, u.device, u.dtype, _torch.float32
+    fwd = _scan_fields(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, None, None)
+    shape, device, index, dt, f32 = u.shape, u.device, u.get_device(), u.dtype, _torch.float32
+    S, nb, H = shape
     G, N = B.shape[2:]
-    _check(grad_y, "grad_y", (S, nb, H), dt, dev, dense=False)
-    _optional(grad_final_state, "grad_final_state", (nb, H, N), f32, dev)
-    handle, stream = _stream(stream, dev)
 
     def out(like, shape, dtype):
-        return _torch.empty(shape, dtype=dtype, device=dev) if like is not None else None
+        return _torch.empty(shape, dtype=dtype, device=device) if like is not None else None
 
-    g = SelectiveScanGrads(out(u, (S, nb, H), dt), out(u, (S, nb, H), dt), out(A, (H, N), f32),
-                           out(B, (S, nb, G, N), dt), out(C, (S, nb, G, N), dt), out(D, (H,), f32),
-                           out(z, (S, nb, H), dt), out(delta_bias, (H,), f32), out(state, (nb, H, N), f32))
-    args = ScanBwdArgs(fwd, grad_y.data_ptr(), _strides(grad_y, 2), _ptr(grad_final_state), _ptr(g.u), _ptr(g.delta),
-                       _ptr(g.z), _ptr(g.B), _ptr(g.C), _ptr(g.A), _ptr(g.D), _ptr(g.delta_bias), _ptr(g.state))
-    _call_ws("mcc1d_scan_bwd", args, handle, stream, dev)
-    _record(stream, grad_y, u, delta, A, B, C, D, z, delta_bias, lengths, state, grad_final_state, *g)
+    g = SelectiveScanGrads(out(u, shape, dt), out(u, shape, dt), out(A, (H, N), f32), out(B, (S, nb, G, N), dt),
+                           out(C, (S, nb, G, N), dt), out(D, (H,), f32), out(z, shape, dt),
+                           out(delta_bias, (H,), f32), out(state, (nb, H, N), f32))
+    at = SelectiveScanGrads(*[0 if t is None else t.data_ptr() for t in g])
+    args = _pack_scan_bwd(*fwd, _rows(grad_y, "grad_y", shape, dt, index), grad_y.stride(0), grad_y.stride(1),
+                          _optional(grad_final_state, "grad_final_state", (nb, H, N), f32, index), at.u, at.delta,
+                          at.z, at.B, at.C, at.A, at.D, at.delta_bias, at.state)
+    handle, stream = _stream(stream, index)
+    _call_ws("mcc1d_scan_bwd", args, handle, stream, device)
+    if stream is not None:
+        _record(stream, grad_y, u, delta, A, B, C, D, z, delta_bias, lengths, state, grad_final_state, *g)
     return g
 
 
@@ -340,28 +366,25 @@ def selective_scan_step(u, delta, state, A, B, C, D=None, z=None, delta_bias=Non
     the cache marks a padding row: y is zero, no state changes. Two rows must
     not name one slot. Returns y [B,H]."""
     _load()
-    (nb, H), code, dev = _first(u, "u", 2)
+    shape, code, index = _first(u, "u", 2)
+    nb, H = shape
     dt, f32 = u.dtype, _torch.float32
     if A.dim() != 2 or B.dim() != 3:
         raise ValueError("A must be [H,N] and B, C [B,G,N]")
     N, G = A.shape[1], B.shape[1]
-    _check(A, "A", (H, N), f32, dev)
-    _check(delta, "delta", (nb, H), dt, dev, dense=False)
-    _check(B, "B", (nb, G, N), dt, dev, dense=False)
-    _check(C, "C", (nb, G, N), dt, dev, dense=False)
-    if z is not None:
-        _check(z, "z", (nb, H), dt, dev, dense=False)
-    _optional(D, "D", (H,), f32, dev)
-    _optional(delta_bias, "delta_bias", (H,), f32, dev)
-    _optional(y, "y", (nb, H), dt, dev)
-    rows = _cache(state, "state", (H, N), f32, dev, nb, slots)
-    handle, stream = _stream(stream, dev)
+    bc = (nb, G, N)
     if y is None:
-        y = _torch.empty((nb, H), dtype=dt, device=dev)
-    args = ScanStepArgs(u.data_ptr(), _strides(u, 1)[0], delta.data_ptr(), _strides(delta, 1)[0], _ptr(z),
-                        _strides(z, 1)[0] if z is not None else 0, B.data_ptr(), _strides(B, 2), C.data_ptr(),
-                        _strides(C, 2), A.data_ptr(), _ptr(D), _ptr(delta_bias), state.data_ptr(), _ptr(slots),
-                        y.data_ptr(), rows, nb, H, N, G, code, SOFTPLUS if delta_softplus else 0)
+        y = _torch.empty(shape, dtype=dt, device=u.device)
+    cache, rows, at = _cache(state, (H, N), f32, index, nb, slots)
+    args = _pack_scan_step(u.data_ptr(), u.stride(0), _rows(delta, "delta", shape, dt, index), delta.stride(0),
+                           *((0, 0) if z is None else (_rows(z, "z", shape, dt, index), z.stride(0))),
+                           _rows(B, "B", bc, dt, index), B.stride(0), B.stride(1), _rows(C, "C", bc, dt, index),
+                           C.stride(0), C.stride(1), _dense(A, "A", (H, N), f32, index),
+                           _optional(D, "D", (H,), f32, index), _optional(delta_bias, "delta_bias", (H,), f32, index),
+                           cache, at, _dense(y, "y", shape, dt, index), rows, nb, H, N, G, code,
+                           SOFTPLUS if delta_softplus else 0)
+    handle, stream = _stream(stream, index)
     _call("mcc1d_scan_step", args, handle)
-    _record(stream, u, delta, state, A, B, C, D, z, delta_bias, slots, y)
+    if stream is not None:
+        _record(stream, u, delta, state, A, B, C, D, z, delta_bias, slots, y)
     return y

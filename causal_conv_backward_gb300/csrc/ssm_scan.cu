@@ -14,6 +14,8 @@
 // is cut into chunks: each chunk's state from a zero start and its sum of dt
 // (which fixes its decay exp(A sum dt)) are computed, the chunks are joined in
 // order, and the outputs are computed chunk by chunk from the joined states.
+#include <algorithm>
+
 #include "plan.h"
 #include "ssm_scan.cuh"
 
@@ -511,7 +513,8 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.grid = scan_grid(a.H, a.G, cb);
     const int64_t rows = p.grid.blocks * a.B, warps = rows * OutTile<4>::WARPS;
-    cut(p, warps >= 152 * 5 ? 1 : (152 * 12 + warps - 1) / warps);
+    const int64_t most = p.tiles / 4;     // a chunk of fewer tiles costs more launches than it saves
+    cut(p, warps >= 152 * 5 || most < 2 ? 1 : std::min((152 * 12 + warps - 1) / warps, most));
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);

@@ -18,6 +18,9 @@
 // recurrence back. Sums over a channel's states and over a warp's channels go
 // through shuffles, those over warps and blocks through memory, in a fixed
 // order.
+#include <atomic>
+
+#include "device.h"
 #include "plan.h"
 #include "ssm_scan.cuh"
 
@@ -406,9 +409,15 @@ template <int DT, int NL, bool PAIRS>
 int32_t run_pairs(const ScanParams &p, cudaStream_t s)
 {
     constexpr int bytes = (int)sizeof(BwdShared<NL>);
-    if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
-        return kErrCuda;
+    // once per context: a context created after a device reset starts without the attribute
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long ctx = current_context_id();
+    if (ctx == 0 || ready.load(std::memory_order_acquire) != ctx) {
+        if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 bytes) != cudaSuccess)
+            return kErrCuda;
+        ready.store(ctx, std::memory_order_release);
+    }
     mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), BwdTile<NL>::THREADS, bytes, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
