@@ -80,37 +80,52 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams 
             for (int e = 0; e < P; ++e)
                 win[i][e] = unpack2<DT>(r.u[e]);
         }
-        for (int64_t t = t0; t < te; t += kRows) {
-            Vec<V> in[kRows];
+        auto emit = [&](const Vec<V> &in, uint16_t *to) {
+            Vec<V> out;
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const float2 v = unpack2<DT>(in.u[e]);
+                float2 s = bias[e];
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+                    s = fma2(w[k][e], win[k][e], s);
+                s = fma2(w[W - 1][e], v, s);
+                if (p.silu)
+                    s = mul2(s, sigmoid2(s));
+                out.u[e] = pack2<DT>(s);
+#pragma unroll
+                for (int k = 0; k < W - 2; ++k)
+                    win[k][e] = win[k + 1][e];
+                if (W > 1)
+                    win[W > 1 ? W - 2 : 0][e] = v;
+            }
+            vstore<V>(to, out);
+        };
+        // whole batches of rows, the next one loaded before this one is used
+        const uint16_t *src = x + t0 * p.xs;
+        uint16_t *dst = y + t0 * ys;
+        int64_t left = te - t0;
+        Vec<V> in[kRows];
+        if (left >= kRows)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r, src += p.xs)
+                in[r] = vload<V>(src);
+        while (left >= kRows) {
+            Vec<V> cur[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
-                in[r] = t + r < te ? vload<V>(x + (t + r) * p.xs) : vzero<V>();
+                cur[r] = in[r];
+            left -= kRows;
+            if (left >= kRows)
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                Vec<V> out;
+                for (int r = 0; r < kRows; ++r, src += p.xs)
+                    in[r] = vload<V>(src);
 #pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const float2 v = unpack2<DT>(in[r].u[e]);
-                    float2 s = bias[e];
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-                        s = fma2(w[k][e], win[k][e], s);
-                    s = fma2(w[W - 1][e], v, s);
-                    if (p.silu) {
-                        s.x *= sigmoid(s.x);
-                        s.y *= sigmoid(s.y);
-                    }
-                    out.u[e] = pack2<DT>(s);
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k)
-                        win[k][e] = win[k + 1][e];
-                    if (W > 1)
-                        win[W > 1 ? W - 2 : 0][e] = v;
-                }
-                if (t + r < te)
-                    vstore<V>(y + (t + r) * ys, out);
-            }
+            for (int r = 0; r < kRows; ++r, dst += ys)
+                emit(cur[r], dst);
         }
+        for (; left > 0; --left, src += p.xs, dst += ys)
+            emit(vload<V>(src), dst);
     }
     for (int64_t t = t0 > te ? t0 : te; t < t1; ++t)
         vstore<V>(y + t * ys, vzero<V>());
@@ -163,10 +178,8 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_step(const StepParams
 #pragma unroll
         for (int k = 0; k < W; ++k)
             s = fma2(unpack2<DT>(wt[k].u[e]), unpack2<DT>(row[k].u[e]), s);
-        if (p.silu) {
-            s.x *= sigmoid(s.x);
-            s.y *= sigmoid(s.y);
-        }
+        if (p.silu)
+            s = mul2(s, sigmoid2(s));
         out.u[e] = pack2<DT>(s);
     }
     vstore<V>(y, out);

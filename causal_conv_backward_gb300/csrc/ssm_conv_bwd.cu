@@ -93,69 +93,102 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
         const int64_t rend = t1 + W - 1;
         const int64_t live = rend < len ? rend : len;
         const int64_t first = t0 == 0 ? -(int64_t)(W - 1) : t0;   // first row of grad_x (below 0: the window's)
-        for (int64_t r0 = t0; r0 < rend; r0 += kRows) {
-            Vec<V> rx[kRows], rg[kRows];
+        // One row: its x and grad_y, `own`: in this run of rows, so counted in the sums; `in`: before the
+        // length; gf: the final window's gradient where row r-W+1 of grad_x is in it. Returns grad_x(r-W+1).
+        auto row = [&](const Vec<V> &rx, const Vec<V> &rg, const Vec<V> &gf, bool own, bool in) {
+            Vec<V> out;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const bool ok = r0 + i < live;
-                rx[i] = ok ? vload<V>(x + (r0 + i) * p.xs) : vzero<V>();
-                rg[i] = ok ? vload<V>(gy + (r0 + i) * p.gs) : vzero<V>();
-            }
+            for (int e = 0; e < P; ++e) {
+                const float2 v = unpack2<DT>(rx.u[e]);
+                float2 d = unpack2<DT>(rg.u[e]);
+                if (p.silu) {
+                    float2 s = bias[e];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int64_t r = r0 + i, t = r - (W - 1);
-                const bool own = r < t1;
-                Vec<V> out;
-                Vec<V> fs = vzero<V>();
-                if (p.gfs && t >= len - (W - 1) && t < len && r < rend)
-                    fs = vload<V>(p.gfs + (b * (W - 1) + (t - (len - (W - 1)))) * p.H + h);
-#pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const float2 v = unpack2<DT>(rx[i].u[e]);
-                    float2 d = unpack2<DT>(rg[i].u[e]);
-                    if (p.silu) {
-                        float2 s = bias[e];
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-                            s = fma2(w[k][e], xw[k][e], s);
-                        s = fma2(w[W - 1][e], v, s);
-                        const float sx = sigmoid(s.x), sy = sigmoid(s.y);
-                        d.x *= sx * fmaf(s.x, 1.f - sx, 1.f);
-                        d.y *= sy * fmaf(s.y, 1.f - sy, 1.f);
-                        if (r >= live)
-                            d = make_float2(0.f, 0.f);   // an infinite pre leaves nothing behind
-                    }
-                    if (own) {
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-                            aw[k][e] = fma2(d, xw[k][e], aw[k][e]);
-                        aw[W - 1][e] = fma2(d, v, aw[W - 1][e]);
-                        aw[W][e] = add2(aw[W][e], d);
-                    }
-                    float2 g = unpack2<DT>(fs.u[e]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-                        g = fma2(w[W - 1 - j][e], dw[j][e], g);
-                    g = fma2(w[0][e], d, g);
-                    out.u[e] = pack2<DT>(g);
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k) {
-                        xw[k][e] = xw[k + 1][e];
-                        dw[k][e] = dw[k + 1][e];
-                    }
-                    if (W > 1) {
-                        xw[W > 1 ? W - 2 : 0][e] = v;
-                        dw[W > 1 ? W - 2 : 0][e] = d;
-                    }
+                    for (int k = 0; k < W - 1; ++k)
+                        s = fma2(w[k][e], xw[k][e], s);
+                    s = fma2(w[W - 1][e], v, s);
+                    // d/ds [s g(s)] = g (1 + s (1 - g)), g the sigmoid
+                    const float2 g = sigmoid2(s), one = make_float2(1.f, 1.f);
+                    d = mul2(d, mul2(g, fma2(s, fma2(g, make_float2(-1.f, -1.f), one), one)));
+                    if (!in)
+                        d = make_float2(0.f, 0.f);   // an infinite pre leaves nothing behind
                 }
-                if (t >= first && t < t1) {
-                    if (t >= 0)
-                        vstore<V>(gx + t * ys, out);
-                    else if (p.gstate)
-                        vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
+                if (own) {
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k)
+                        aw[k][e] = fma2(d, xw[k][e], aw[k][e]);
+                    aw[W - 1][e] = fma2(d, v, aw[W - 1][e]);
+                    aw[W][e] = add2(aw[W][e], d);
+                }
+                float2 o = fma2(w[0][e], d, unpack2<DT>(gf.u[e]));
+#pragma unroll
+                for (int k = W - 2; k >= 0; --k)
+                    o = fma2(w[W - 1 - k][e], dw[k][e], o);
+                out.u[e] = pack2<DT>(o);
+#pragma unroll
+                for (int k = 0; k < W - 2; ++k) {
+                    xw[k][e] = xw[k + 1][e];
+                    dw[k][e] = dw[k + 1][e];
+                }
+                if (W > 1) {
+                    xw[W > 1 ? W - 2 : 0][e] = v;
+                    dw[W > 1 ? W - 2 : 0][e] = d;
                 }
             }
+            return out;
+        };
+        auto edge = [&](int64_t r) {
+            const bool in = r < live;
+            const int64_t t = r - (W - 1);
+            Vec<V> gf = vzero<V>();
+            if (p.gfs && t >= len - (W - 1) && t < len)
+                gf = vload<V>(p.gfs + (b * (W - 1) + (t - (len - (W - 1)))) * p.H + h);
+            const Vec<V> out = row(in ? vload<V>(x + r * p.xs) : vzero<V>(), in ? vload<V>(gy + r * p.gs) : vzero<V>(), gf,
+                                   r < t1, in);
+            if (t < first)
+                return;
+            if (t >= 0)
+                vstore<V>(gx + t * ys, out);
+            else if (p.gstate)
+                vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
+        };
+        // the first W-1 rows and what is near the run's or the sequence's end go one by one; between them
+        // batches of rows, the next one loaded before this one is used
+        int64_t r = t0;
+        for (; r < t0 + W - 1 && r < rend; ++r)
+            edge(r);
+        const int64_t stop = t1 < len ? t1 : len;
+        int64_t left = stop - r;
+        const uint16_t *sx = x + r * p.xs, *sg = gy + r * p.gs;
+        uint16_t *to = gx + (r - (W - 1)) * ys;
+        Vec<V> rx[kRows], rg[kRows];
+        auto load = [&]() {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i, sx += p.xs, sg += p.gs) {
+                rx[i] = vload<V>(sx);
+                rg[i] = vload<V>(sg);
+            }
+        };
+        if (left >= kRows)
+            load();
+        while (left >= kRows) {
+            Vec<V> cx[kRows], cg[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                cx[i] = rx[i];
+                cg[i] = rg[i];
+            }
+            left -= kRows;
+            if (left >= kRows)
+                load();
+            // rows before the final window's: up to W-1 rows before the length no grad_final_state arrives
+#pragma unroll
+            for (int i = 0; i < kRows; ++i, to += ys)
+                vstore<V>(to, row(cx[i], cg[i], vzero<V>(), true, true));
+            r += kRows;
         }
+        for (; r < rend; ++r)
+            edge(r);
     }
 #pragma unroll
     for (int k = 0; k <= W; ++k)

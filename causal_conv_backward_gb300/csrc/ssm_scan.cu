@@ -332,17 +332,18 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
         store_states(p.gstate + row * p.N, n0, p.N, p.vecState, s);
 }
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 
-// One token: a row of states in, moved on by one step, and out.
+// One token: a row of states in, moved on by one step, and out. Four states to
+// a lane as above, so that neighbouring lanes move neighbouring 16 bytes.
 struct ScanStepParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm;
     const float *A, *D, *dbias;
     float *state;
     const int32_t *slots;
     uint16_t *y;
-    int64_t ub, db, zb, Bb, Bg, Cb, Cg, rows, B, H;
-    int32_t N, Hg, softplus, vecA, vecState;
+    int64_t ub, db, zb, Bb, Bg, Cb, Cg, rows;
+    int32_t B, H, N, Hg, softplus, vecA, vecState, vecB;   // vecB: rows of B and C start on 8 bytes
 };
 
 template <int DT>
@@ -351,42 +352,53 @@ __device__ __forceinline__ float load16(const uint16_t *p)
     return unpack2<DT>((uint32_t)__ldg(p)).x;
 }
 
+// Four states of B or C, zeros past N.
+template <int DT>
+__device__ __forceinline__ void load_four(const uint16_t *row, int n0, int N, bool vec, float2 (&v)[2])
+{
+    uint32_t lo = 0u, hi = 0u;
+    if (vec) {
+        if (n0 < N) {
+            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(row + n0));
+            lo = r.x;
+            hi = r.y;
+        }
+    } else {
+        lo = load_pair<false>(row + n0, n0 < N, n0 + 1 < N);
+        hi = load_pair<false>(row + n0 + 2, n0 + 2 < N, n0 + 3 < N);
+    }
+    v[0] = unpack2<DT>(lo);
+    v[1] = unpack2<DT>(hi);
+}
+
 template <int DT, int NL>
 __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
 {
     const int j = threadIdx.x % NL, n0 = 4 * j;
-    const int64_t id = ((int64_t)blockIdx.x * kStepThreads + threadIdx.x) / NL;
-    const bool live = id < p.B * p.H;
-    const int64_t b = live ? id / p.H : 0, c = live ? id - b * p.H : 0;
+    const int c = (int)(blockIdx.x * (kStepThreads / NL)) + (int)threadIdx.x / NL;
+    const int64_t b = blockIdx.y;
     const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
-    const bool on = live && slot >= 0 && slot < p.rows;
-    float part = 0.f;
-    float uv = 0.f;
+    const bool live = c < p.H, on = live && slot >= 0 && slot < p.rows;
+    float part = 0.f, uv = 0.f;
     if (on) {
         float *row = p.state + (slot * p.H + c) * p.N;
         const float4 h = load_states(row, n0, p.N, p.vecState);
-        const float4 A = load_states(p.A + c * p.N, n0, p.N, p.vecA);
-        const int64_t g = c / p.Hg;
-        const uint16_t *B = p.Bm + b * p.Bb + g * p.Bg, *C = p.Cm + b * p.Cb + g * p.Cg;
+        const float4 A = load_states(p.A + (int64_t)c * p.N, n0, p.N, p.vecA);
+        const int64_t g = p.Hg == p.H ? 0 : c / p.Hg;
+        float2 B[2], C[2];
+        load_four<DT>(p.Bm + b * p.Bb + g * p.Bg, n0, p.N, p.vecB, B);
+        load_four<DT>(p.Cm + b * p.Cb + g * p.Cg, n0, p.N, p.vecB, C);
         float dt = load16<DT>(p.delta + b * p.db + c) + (p.dbias ? p.dbias[c] : 0.f);
+        uv = load16<DT>(p.u + b * p.ub + c);
         if (p.softplus)
             dt = softplus(dt);
-        uv = load16<DT>(p.u + b * p.ub + c);
         const float du = dt * uv, dl = dt * kLog2e;
-        float4 o;
-        o.x = fmaf(ex2(dl * A.x), h.x, n0 < p.N ? du * load16<DT>(B + n0) : 0.f);
-        o.y = fmaf(ex2(dl * A.y), h.y, n0 + 1 < p.N ? du * load16<DT>(B + n0 + 1) : 0.f);
-        o.z = fmaf(ex2(dl * A.z), h.z, n0 + 2 < p.N ? du * load16<DT>(B + n0 + 2) : 0.f);
-        o.w = fmaf(ex2(dl * A.w), h.w, n0 + 3 < p.N ? du * load16<DT>(B + n0 + 3) : 0.f);
-        store_states(row, n0, p.N, p.vecState, o);
-        if (n0 < p.N)
-            part = o.x * load16<DT>(C + n0);
-        if (n0 + 1 < p.N)
-            part = fmaf(o.y, load16<DT>(C + n0 + 1), part);
-        if (n0 + 2 < p.N)
-            part = fmaf(o.z, load16<DT>(C + n0 + 2), part);
-        if (n0 + 3 < p.N)
-            part = fmaf(o.w, load16<DT>(C + n0 + 3), part);
+        const float2 du2 = make_float2(du, du), dl2 = make_float2(dl, dl);
+        float2 o0 = fma2(decay2(dl2, make_float2(A.x, A.y)), make_float2(h.x, h.y), mul2(du2, B[0]));
+        float2 o1 = fma2(decay2(dl2, make_float2(A.z, A.w)), make_float2(h.z, h.w), mul2(du2, B[1]));
+        store_states(row, n0, p.N, p.vecState, make_float4(o0.x, o0.y, o1.x, o1.y));
+        const float2 s = fma2(o0, C[0], mul2(o1, C[1]));
+        part = s.x + s.y;
     }
 #pragma unroll
     for (int step = 1; step < NL; step *= 2)
@@ -442,7 +454,8 @@ int32_t run_scan(const ScanParams &p, int dtype, int nl, cudaStream_t s)
 template <int DT>
 int32_t run_step(const ScanStepParams &p, int nl, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((p.B * p.H * nl + kStepThreads - 1) / kStepThreads);
+    const int per = kStepThreads / nl;
+    const dim3 grid((unsigned)((p.H + per - 1) / per), (unsigned)p.B);
     switch (nl) {
     case 1: mcc1d_ssm_scan_step<DT, 1><<<grid, kStepThreads, 0, s>>>(p); break;
     case 2: mcc1d_ssm_scan_step<DT, 2><<<grid, kStepThreads, 0, s>>>(p); break;
@@ -670,13 +683,14 @@ int32_t launch_scan_step(const mcc1d_scan_step_args &a, cudaStream_t stream)
     p.Bb = a.B_strides[0], p.Bg = a.B_strides[1];
     p.Cb = a.C_strides[0], p.Cg = a.C_strides[1];
     p.rows = a.cache_rows;
-    p.B = a.B;
-    p.H = a.H;
+    p.B = (int32_t)a.B;
+    p.H = (int32_t)a.H;
     p.N = (int32_t)a.N;
     p.Hg = (int32_t)(a.H / a.G);
     p.softplus = (a.flags & MCC1D_SOFTPLUS) != 0;
     p.vecA = a.N % 4 == 0 && aligned(a.A, 16);
     p.vecState = a.N % 4 == 0 && aligned(a.state, 16);
+    p.vecB = a.N % 4 == 0 && aligned(a.B_, 8) && aligned(a.C, 8) && ((p.Bb | p.Bg | p.Cb | p.Cg) & 3) == 0;
     int nl = 1;
     while (4 * nl < a.N)
         nl *= 2;
