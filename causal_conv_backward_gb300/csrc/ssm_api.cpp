@@ -158,8 +158,12 @@ int32_t check(const mcc1d_scan_step_args *a)
     if (!shape_ok(1, a->B, a->H) || !states_ok(a->B, a->H, a->N, a->G) || a->cache_rows < 1 ||
         (!a->slots && a->cache_rows < a->B))
         return kErrShape;
-    if (a->u_stride < 0 || a->delta_stride < 0 || (a->z && a->z_stride < 0) || !strides_ok(a->B_strides) ||
-        !strides_ok(a->C_strides) || !on2({a->u, a->delta, a->z, a->B_, a->C, a->y}) ||
+    const int64_t strides[7] = {a->u_stride,     a->delta_stride, a->z ? a->z_stride : 0, a->B_strides[0],
+                                a->B_strides[1], a->C_strides[0], a->C_strides[1]};
+    for (int64_t s : strides)
+        if (s < 0 || s > kMaxGrid)
+            return kErrInvalid;
+    if ( !on2({a->u, a->delta, a->z, a->B_, a->C, a->y}) ||
         !on4({a->A, a->D, a->delta_bias, a->state, a->slots}))
         return kErrInvalid;
     return kOk;

@@ -67,6 +67,109 @@ __device__ __forceinline__ void vstore(uint16_t *p, const Vec<V> &r)
         *p = (uint16_t)r.u[0];
 }
 
+// Asynchronous copy of V channels (4 or 8 bytes) from global to shared memory,
+// in the issuing thread's groups.
+template <int V>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint16_t *src)
+{
+    static_assert(V == 2 || V == 4, "4 or 8 bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(2 * V) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the N newest groups of this thread have arrived.
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int V>
+__device__ __forceinline__ Vec<V> vload_shared(const uint8_t *p)
+{
+    Vec<V> r;
+    if constexpr (V == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.u[0] = v.x;
+        r.u[1] = v.y;
+    } else {
+        r.u[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    return r;
+}
+
+// Rows of T tensors on their way to one thread: whole batches of R rows, STAGES
+// of them, copied asynchronously into shared memory, where the thread reads
+// back only what it copied itself (no barrier). Registers could not hold the
+// bytes that have to be in flight: at about 0.8 us of latency an SM needs
+// 36 KB. Single channels (V = 1) are too narrow to copy and wait in registers.
+template <int V, int T, int R, int STAGES>
+struct RowRing {
+    static constexpr int BYTES_PER_THREAD = V == 1 ? 0 : T * R * STAGES * 2 * V;
+    const uint16_t *src[T];
+    int64_t step[T];
+    int64_t left;          // rows not yet asked for
+    uint8_t *slots;        // of the block: slot (stage, row, tensor) of thread i at ((stage R + row) T + tensor) threads + i
+    int threads, next_in, next_out;
+    Vec<V> hold[V == 1 ? T * R : 1];
+
+    __device__ __forceinline__ uint8_t *slot(int stage, int row, int tensor) const
+    {
+        return slots + (((stage * R + row) * T + tensor) * threads + threadIdx.x) * (2 * V);
+    }
+    __device__ __forceinline__ void ask()
+    {
+        if constexpr (V > 1) {
+            if (left >= R) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        copy_async<V>(smem_u32(slot(next_in, r, t)), src[t]);
+                        src[t] += step[t];
+                    }
+                left -= R;
+            }
+            copy_commit();
+            next_in = next_in + 1 == STAGES ? 0 : next_in + 1;
+        } else if (left >= R) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    hold[r * T + t] = vload<V>(src[t]);
+                    src[t] += step[t];
+                }
+            left -= R;
+        }
+    }
+    __device__ __forceinline__ void start()
+    {
+        next_in = next_out = 0;
+#pragma unroll
+        for (int s = 0; s < (V > 1 ? STAGES - 1 : 1); ++s)
+            ask();
+    }
+    // The next batch; the one STAGES - 1 after it is asked for.
+    __device__ __forceinline__ void take(Vec<V> (&out)[R * T])
+    {
+        if constexpr (V > 1) {
+            ask();
+            copy_wait<STAGES - 1>();
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    out[r * T + t] = vload_shared<V>(slot(next_out, r, t));
+            next_out = next_out + 1 == STAGES ? 0 : next_out + 1;
+        } else {
+#pragma unroll
+            for (int i = 0; i < R * T; ++i)
+                out[i] = hold[i];
+            ask();
+        }
+    }
+};
+
 __device__ __forceinline__ float ex2(float x)
 {
     float r;

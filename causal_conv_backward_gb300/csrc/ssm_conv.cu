@@ -17,7 +17,8 @@ namespace mcc1d {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 8;    // rows in flight per thread
+constexpr int kRows = 4;     // rows of a batch
+constexpr int kStages = 4;   // batches, all but one in flight
 
 struct ConvParams {
     const uint16_t *x, *weight, *bias, *state;
@@ -42,6 +43,8 @@ template <int DT, int V, int W>
 __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams p)
 {
     constexpr int P = Vec<V>::P;
+    using Ring = RowRing<V, 1, kRows, kStages>;
+    __shared__ __align__(16) uint8_t slots[V == 1 ? 16 : kThreads * Ring::BYTES_PER_THREAD];
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (id >= p.B * p.vecs)
         return;
@@ -101,29 +104,24 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams 
             }
             vstore<V>(to, out);
         };
-        // whole batches of rows, the next one loaded before this one is used
         const uint16_t *src = x + t0 * p.xs;
         uint16_t *dst = y + t0 * ys;
         int64_t left = te - t0;
-        Vec<V> in[kRows];
-        if (left >= kRows)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r, src += p.xs)
-                in[r] = vload<V>(src);
-        while (left >= kRows) {
-            Vec<V> cur[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                cur[r] = in[r];
-            left -= kRows;
-            if (left >= kRows)
-#pragma unroll
-                for (int r = 0; r < kRows; ++r, src += p.xs)
-                    in[r] = vload<V>(src);
+        Ring ring;
+        ring.src[0] = src;
+        ring.step[0] = p.xs;
+        ring.left = left;
+        ring.slots = slots;
+        ring.threads = kThreads;
+        ring.start();
+        for (; left >= kRows; left -= kRows) {
+            Vec<V> in[kRows];
+            ring.take(in);
 #pragma unroll
             for (int r = 0; r < kRows; ++r, dst += ys)
-                emit(cur[r], dst);
+                emit(in[r], dst);
         }
+        src += (te - t0 - left) * p.xs;
         for (; left > 0; --left, src += p.xs, dst += ys)
             emit(vload<V>(src), dst);
     }

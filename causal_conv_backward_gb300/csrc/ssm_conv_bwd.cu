@@ -20,7 +20,8 @@ namespace mcc1d {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = 4;    // rows in flight per thread
+constexpr int kRows = 4;     // rows of a batch
+constexpr int kStages = 3;   // batches, all but one in flight
 
 struct ConvBwdParams {
     const uint16_t *gy, *x, *weight, *bias, *state, *gfs;
@@ -36,7 +37,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
 {
     constexpr int P = Vec<V>::P;
     constexpr int Wm = W > 1 ? W - 1 : 1;
-    __shared__ float2 red[kWarps][W + 1][32][P];
+    using Ring = RowRing<V, 2, kRows, kStages>;
+    union Shared {
+        uint8_t slots[V == 1 ? 16 : kWarps * 32 * Ring::BYTES_PER_THREAD];
+        float2 red[kWarps][W + 1][32][P];      // after the rows
+    };
+    __shared__ __align__(16) Shared shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t vec = (int64_t)blockIdx.x * 32 + lane;
     const int64_t part = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
@@ -153,48 +159,39 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
                 vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
         };
         // the first W-1 rows and what is near the run's or the sequence's end go one by one; between them
-        // batches of rows, the next one loaded before this one is used
+        // batches of rows
         int64_t r = t0;
         for (; r < t0 + W - 1 && r < rend; ++r)
             edge(r);
         const int64_t stop = t1 < len ? t1 : len;
         int64_t left = stop - r;
-        const uint16_t *sx = x + r * p.xs, *sg = gy + r * p.gs;
         uint16_t *to = gx + (r - (W - 1)) * ys;
-        Vec<V> rx[kRows], rg[kRows];
-        auto load = [&]() {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i, sx += p.xs, sg += p.gs) {
-                rx[i] = vload<V>(sx);
-                rg[i] = vload<V>(sg);
-            }
-        };
-        if (left >= kRows)
-            load();
-        while (left >= kRows) {
-            Vec<V> cx[kRows], cg[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                cx[i] = rx[i];
-                cg[i] = rg[i];
-            }
-            left -= kRows;
-            if (left >= kRows)
-                load();
+        Ring ring;
+        ring.src[0] = x + r * p.xs;
+        ring.src[1] = gy + r * p.gs;
+        ring.step[0] = p.xs;
+        ring.step[1] = p.gs;
+        ring.left = left;
+        ring.slots = shared.slots;
+        ring.threads = kWarps * 32;
+        ring.start();
+        for (; left >= kRows; left -= kRows, r += kRows) {
+            Vec<V> in[2 * kRows];
+            ring.take(in);
             // rows before the final window's: up to W-1 rows before the length no grad_final_state arrives
 #pragma unroll
             for (int i = 0; i < kRows; ++i, to += ys)
-                vstore<V>(to, row(cx[i], cg[i], vzero<V>(), true, true));
-            r += kRows;
+                vstore<V>(to, row(in[2 * i], in[2 * i + 1], vzero<V>(), true, true));
         }
         for (; r < rend; ++r)
             edge(r);
     }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
         for (int e = 0; e < P; ++e)
-            red[warp][k][lane][e] = aw[k][e];
+            shared.red[warp][k][lane][e] = aw[k][e];
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * 32; i += kWarps * 32) {
         const int k = i / 32, l = i & 31;
@@ -204,10 +201,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
         float *out = p.partial + (part * (W + 1) + k) * p.H + v2 * V;
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-            float2 s = red[0][k][l][e];
+            float2 s = shared.red[0][k][l][e];
 #pragma unroll
             for (int q = 1; q < kWarps; ++q)
-                s = add2(s, red[q][k][l][e]);
+                s = add2(s, shared.red[q][k][l][e]);
             out[2 * e] = s.x;
             if (V > 1)
                 out[2 * e + 1] = s.y;

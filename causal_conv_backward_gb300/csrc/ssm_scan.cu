@@ -342,7 +342,8 @@ struct ScanStepParams {
     float *state;
     const int32_t *slots;
     uint16_t *y;
-    int64_t ub, db, zb, Bb, Bg, Cb, Cg, rows;
+    uint32_t ub, db, zb, Bb, Bg, Cb, Cg;   // strides below 2^31: products of 32 bits by 32
+    int64_t rows;
     int32_t B, H, N, Hg, softplus, vecA, vecState, vecB;   // vecB: rows of B and C start on 8 bytes
 };
 
@@ -371,49 +372,74 @@ __device__ __forceinline__ void load_four(const uint16_t *row, int n0, int N, bo
     v[1] = unpack2<DT>(hi);
 }
 
+// A thread takes R rows of one channel: A is read once, all rows' loads are in
+// flight together, and what a row needs once per channel (dt, the gate, y) is
+// done by one lane each instead of by all NL.
+template <int NL>
+constexpr int kStepRows = NL < 4 ? NL : 4;
+
 template <int DT, int NL>
 __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
 {
-    const int j = threadIdx.x % NL, n0 = 4 * j;
+    constexpr int R = kStepRows<NL>;
+    const int j = threadIdx.x % NL, n0 = 4 * j, lane = threadIdx.x & 31;
     const int c = (int)(blockIdx.x * (kStepThreads / NL)) + (int)threadIdx.x / NL;
-    const int64_t b = blockIdx.y;
-    const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
-    const bool live = c < p.H, on = live && slot >= 0 && slot < p.rows;
-    float part = 0.f, uv = 0.f;
-    if (on) {
-        float *row = p.state + (slot * p.H + c) * p.N;
-        const float4 h = load_states(row, n0, p.N, p.vecState);
-        const float4 A = load_states(p.A + (int64_t)c * p.N, n0, p.N, p.vecA);
-        const int64_t g = p.Hg == p.H ? 0 : c / p.Hg;
-        float2 B[2], C[2];
-        load_four<DT>(p.Bm + b * p.Bb + g * p.Bg, n0, p.N, p.vecB, B);
-        load_four<DT>(p.Cm + b * p.Cb + g * p.Cg, n0, p.N, p.vecB, C);
-        float dt = load16<DT>(p.delta + b * p.db + c) + (p.dbias ? p.dbias[c] : 0.f);
-        uv = load16<DT>(p.u + b * p.ub + c);
-        if (p.softplus)
-            dt = softplus(dt);
-        const float du = dt * uv, dl = dt * kLog2e;
-        const float2 du2 = make_float2(du, du), dl2 = make_float2(dl, dl);
-        float2 o0 = fma2(decay2(dl2, make_float2(A.x, A.y)), make_float2(h.x, h.y), mul2(du2, B[0]));
-        float2 o1 = fma2(decay2(dl2, make_float2(A.z, A.w)), make_float2(h.z, h.w), mul2(du2, B[1]));
-        store_states(row, n0, p.N, p.vecState, make_float4(o0.x, o0.y, o1.x, o1.y));
-        const float2 s = fma2(o0, C[0], mul2(o1, C[1]));
-        part = s.x + s.y;
-    }
+    const bool live = c < p.H;
+    const int ch = live ? c : 0;
+    const int b0 = (int)blockIdx.y * R, rows = p.B - b0 < R ? p.B - b0 : R;
+    const uint32_t g = p.Hg == p.H ? 0 : ch / p.Hg, in_row = (uint32_t)(ch * p.N), row_size = (uint32_t)(p.H * p.N);
+    const uint16_t *Bg = p.Bm + (uint64_t)g * p.Bg, *Cg = p.Cm + (uint64_t)g * p.Cg;
+
+    float *at[R];
+    float4 h[R];
+    float2 B[R][2], C[R][2];
 #pragma unroll
-    for (int step = 1; step < NL; step *= 2)
-        part += __shfl_xor_sync(0xFFFFFFFFu, part, step);
-    if (live && j == 0) {
-        float y = 0.f;
-        if (on) {
-            y = p.D ? fmaf(p.D[c], uv, part) : part;
-            if (p.z) {
-                const float zv = load16<DT>(p.z + b * p.zb + c);
-                y *= zv * sigmoid(zv);
-            }
-        }
-        p.y[b * p.H + c] = (uint16_t)pack2<DT>(make_float2(y, 0.f));
+    for (int r = 0; r < R; ++r) {
+        const uint32_t b = b0 + (r < rows ? r : 0);
+        const int32_t slot = p.slots ? p.slots[b] : (int32_t)b;
+        const bool on = live && r < rows && slot >= 0 && slot < p.rows;
+        at[r] = on ? p.state + (uint64_t)(uint32_t)slot * row_size + in_row : nullptr;
+        h[r] = on ? load_states(at[r], n0, p.N, p.vecState) : make_float4(0.f, 0.f, 0.f, 0.f);
+        load_four<DT>(Bg + (uint64_t)b * p.Bb, n0, p.N, p.vecB, B[r]);
+        load_four<DT>(Cg + (uint64_t)b * p.Cb, n0, p.N, p.vecB, C[r]);
     }
+    const float4 A = load_states(p.A + in_row, n0, p.N, p.vecA);
+    // this lane's own row
+    const int own = j < R ? j : 0;
+    const bool mine = live && j < R && own < rows;
+    const uint32_t bm = b0 + (own < rows ? own : 0);
+    float dt = load16<DT>(p.delta + (uint64_t)bm * p.db + ch) + (p.dbias ? p.dbias[ch] : 0.f);
+    const float uv = load16<DT>(p.u + (uint64_t)bm * p.ub + ch);
+    const float zv = p.z ? load16<DT>(p.z + (uint64_t)bm * p.zb + ch) : 0.f;
+    const float D = p.D ? p.D[ch] : 0.f;
+    if (p.softplus)
+        dt = softplus(dt);
+    const float dl = dt * kLog2e, du = dt * uv;
+
+    float part[R], y = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float dlr = __shfl_sync(0xFFFFFFFFu, dl, r, NL), dur = __shfl_sync(0xFFFFFFFFu, du, r, NL);
+        const float2 dl2 = make_float2(dlr, dlr), du2 = make_float2(dur, dur);
+        const float2 o0 = fma2(decay2(dl2, make_float2(A.x, A.y)), make_float2(h[r].x, h[r].y), mul2(du2, B[r][0]));
+        const float2 o1 = fma2(decay2(dl2, make_float2(A.z, A.w)), make_float2(h[r].z, h[r].w), mul2(du2, B[r][1]));
+        if (at[r])
+            store_states(at[r], n0, p.N, p.vecState, make_float4(o0.x, o0.y, o1.x, o1.y));
+        const float2 s = fma2(o0, C[r][0], mul2(o1, C[r][1]));
+        part[r] = at[r] ? s.x + s.y : 0.f;
+    }
+    lanes_sum<R, NL, 1, 1>(part, lane);
+    bool there = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        there = r == own ? at[r] != nullptr : there;
+    if (there) {
+        y = fmaf(D, uv, part[0]);
+        if (p.z)
+            y *= zv * sigmoid(zv);
+    }
+    if (mine)
+        p.y[(uint64_t)bm * p.H + ch] = (uint16_t)pack2<DT>(make_float2(y, 0.f));
 }
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -455,7 +481,8 @@ template <int DT>
 int32_t run_step(const ScanStepParams &p, int nl, cudaStream_t s)
 {
     const int per = kStepThreads / nl;
-    const dim3 grid((unsigned)((p.H + per - 1) / per), (unsigned)p.B);
+    const int rows = nl < 4 ? nl : 4;
+    const dim3 grid((unsigned)((p.H + per - 1) / per), (unsigned)((p.B + rows - 1) / rows));
     switch (nl) {
     case 1: mcc1d_ssm_scan_step<DT, 1><<<grid, kStepThreads, 0, s>>>(p); break;
     case 2: mcc1d_ssm_scan_step<DT, 2><<<grid, kStepThreads, 0, s>>>(p); break;
@@ -677,11 +704,11 @@ int32_t launch_scan_step(const mcc1d_scan_step_args &a, cudaStream_t stream)
     p.state = a.state;
     p.slots = a.slots;
     p.y = (uint16_t *)a.y;
-    p.ub = a.u_stride;
-    p.db = a.delta_stride;
-    p.zb = a.z_stride;
-    p.Bb = a.B_strides[0], p.Bg = a.B_strides[1];
-    p.Cb = a.C_strides[0], p.Cg = a.C_strides[1];
+    p.ub = (uint32_t)a.u_stride;
+    p.db = (uint32_t)a.delta_stride;
+    p.zb = (uint32_t)a.z_stride;
+    p.Bb = (uint32_t)a.B_strides[0], p.Bg = (uint32_t)a.B_strides[1];
+    p.Cb = (uint32_t)a.C_strides[0], p.Cg = (uint32_t)a.C_strides[1];
     p.rows = a.cache_rows;
     p.B = (int32_t)a.B;
     p.H = (int32_t)a.H;

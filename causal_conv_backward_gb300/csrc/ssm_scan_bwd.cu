@@ -31,33 +31,6 @@ namespace {
 constexpr int kSub = 2;          // rows whose states and decays sit in registers
 constexpr int kBlocksPerSM = 3;
 
-// Sums v[0..N-1] over L lanes, N and L powers of two. The lanes' numbers are
-// made of the lane bits FIRST (the lowest), 2 REST, 4 REST and so on. Each
-// exchange halves what a lane carries on, so N values cost N (1 - 1/L)
-// shuffles where N >= L, not N log2 L. Lane number j is left with v[0..] = the
-// sums of values j N/L .. (N >= L), or with v[0] = that of value j % N (N < L).
-template <int N, int L, int FIRST, int REST>
-__device__ __forceinline__ void lanes_sum(float (&v)[N], int lane)
-{
-    constexpr int M = N < L ? N : L;
-    int n = N;
-#pragma unroll
-    for (int step = M / 2; step >= 1; step /= 2) {
-        const int mask = step == 1 ? FIRST : step * REST;
-        const bool up = (lane & mask) != 0;
-        n /= 2;
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-            if (i < n) {
-                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, mask);
-            }
-    }
-#pragma unroll
-    for (int step = M; step < L; step *= 2)
-        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], step == 1 ? FIRST : step * REST);
-}
-
 template <int NL>
 struct BwdShared {
     using T = BwdTile<NL>;

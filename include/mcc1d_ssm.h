@@ -32,7 +32,8 @@
  *    elements, outermost first, H always adjacent; B and C take strides for
  *    S, B and G, N adjacent. Strides may be zero and of any alignment; an
  *    input is read in place. Everything else, and every output, is dense.
- *    Negative strides are refused.
+ *    Negative strides are refused, as are strides of 2^31 elements and more in
+ *    mcc1d_scan_step.
  *  - `lengths` (int32 [B], on the device) or NULL: sequence b ends after
  *    lengths[b] tokens (values outside 0..S are taken as the nearer end).
  *    Tokens past the end are not read: their outputs and gradients are zero,
