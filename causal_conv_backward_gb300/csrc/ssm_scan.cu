@@ -28,45 +28,163 @@ namespace {
 // chunk's start from the outputs inside it.
 enum { kOutputs = 0, kSummary = 1, kSummaryGrad = 2 };
 
+template <class T, int MODE>
+struct ScanShared {
+    static constexpr bool kY = MODE == kOutputs, kR = MODE == kSummaryGrad, kC = kY || kR;
+    static constexpr int NL = T::NL, TT = T::TT, CB = T::CB;
+    // a lane's row of y: CL mod 32, so that the lanes of a warp are on 32 different banks
+    static constexpr int YS = CB + (T::CL * T::K + 32 * T::WARPS - CB % 32) % 32;
+    float2 sd[2][TT][CB];                    // dt, dt u
+    float sB[2][TT][T::NP];
+    float sC[2][kC ? TT : 1][T::NP];
+    float sy[2][kY ? TT : 1][NL][YS];        // a lane's part of y
+    float sg[2][kR ? TT : 1][CB];            // the gradient of y
+    uint2 raw[2][kY ? T::RP : 1][T::EL_THREADS];   // u and z of a tile, until its outputs are due
+};
+
+// Every thread of the block, from either role's code.
+__device__ __forceinline__ void block_barrier(int threads) { asm volatile("bar.sync 0, %0;" ::"r"(threads) : "memory"); }
+
 template <class T, int DT, int MODE, bool PAIRS>
-__global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams p)
+__global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1d_ssm_scan(const ScanParams p)
 {
-    constexpr int NP = T::NP, NL = T::NL, CB = T::CB, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
-    constexpr bool kY = MODE == kOutputs, kR = MODE == kSummaryGrad, kC = kY || kR;
-    constexpr int U = TT < 8 ? TT : 8;                      // steps taken together
-    constexpr int YS = NL > 1 ? CB + 16 : CB;              // keeps the lanes of a channel on different banks
-    __shared__ __align__(16) float2 sd[TT][CB];            // dt, dt u
-    __shared__ __align__(16) float sB[TT][NP];
-    __shared__ __align__(16) float sC[kC ? TT : 1][NP];
-    __shared__ __align__(16) float sy[kY ? TT : 1][NL][YS];  // a lane's part of y
-    __shared__ __align__(16) float sg[kR ? TT : 1][CB];      // the gradient of y
+    using Sh = ScanShared<T, MODE>;
+    constexpr int NP = T::NP, NL = T::NL, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
+    constexpr bool kY = Sh::kY, kR = Sh::kR, kC = Sh::kC;
+    constexpr int U = 4;                     // steps of the recurrence taken together
+    extern __shared__ __align__(16) unsigned char raw_shared[];
+    Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
     const ScanWhere w = scan_where<T>(p);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = T::state_lane(lane), n0 = 4 * j;
-    const int cl = (warp * T::CL + T::channel_lane(lane)) * K;   // first channel of the recurrence, within the block
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
     const int64_t tile0 = w.chunk * p.tiles_per_chunk;
     const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
-    // the thread's two channels, and its first row of a tile (RG rows apart)
-    const int pc = 2 * (threadIdx.x % T::CP), pr = threadIdx.x / T::CP;
-    const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
-    const int64_t ch = w.c0 + (on0 ? pc : 0), trow = tile0 * TT + pr;
-    const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
-    const uint16_t *z = kC && p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr;
-    const uint16_t *gy = kR ? p.gy + w.b * p.gb + ch + trow * p.gs : nullptr;
-    uint16_t *y = kY ? p.y + (trow * p.B + w.b) * p.H + ch : nullptr;
-    const int64_t ys = RG * p.B * p.H;
-    const uint16_t *Bm = p.Bm + w.b * p.Bb + w.g * p.Bg + tile0 * TT * p.Bs;
-    const uint16_t *Cm = p.Cm + w.b * p.Cb + w.g * p.Cg + tile0 * TT * p.Cs;
-    const int64_t us = RG * p.us, ds = RG * p.ds, zs = RG * p.zs, gs = RG * p.gs;
-    float2 bias = make_float2(0.f, 0.f), D = make_float2(0.f, 0.f);
-    if (p.dbias)
-        bias = make_float2(on0 ? p.dbias[ch] : 0.f, on1 ? p.dbias[ch + 1] : 0.f);
-    if (kY && p.D)
-        D = make_float2(on0 ? p.D[ch] : 0.f, on1 ? p.D[ch + 1] : 0.f);
+    // the chunk's tiles that hold tokens, and the rows of its i-th tile that do; all but the last are full
+    const int64_t live_end = (te + TT - 1) / TT < tile1 ? (te + TT - 1) / TT : tile1;
+    const int n_tiles = live_end > tile0 ? (int)(live_end - tile0) : 0;
+    const int last_rows = n_tiles > 0 ? (int)(te - (tile0 + n_tiles - 1) * TT < TT ? te - (tile0 + n_tiles - 1) * TT : TT) : 0;
+    auto rows_in = [&](int i) { return i < n_tiles - 1 ? TT : last_rows; };
+    const int warp = threadIdx.x >> 5;
 
-    // the lane's four states of each of its channels
+    if (warp >= T::WARPS) {
+        const int id = threadIdx.x - 32 * T::WARPS;
+        const int pc = 2 * (id % T::CP), pr = id / T::CP;
+        const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
+        const int64_t ch = w.c0 + (on0 ? pc : 0), trow = tile0 * TT + pr;
+        const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
+        const uint16_t *z = kC && p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr;
+        const uint16_t *gy = kR ? p.gy + w.b * p.gb + ch + trow * p.gs : nullptr;
+        uint16_t *y = kY ? p.y + (trow * p.B + w.b) * p.H + ch : nullptr;
+        const int64_t ys = RG * p.B * p.H;
+        const int64_t us = RG * p.us, ds = RG * p.ds, zs = RG * p.zs, gs = RG * p.gs;
+        float2 bias = make_float2(0.f, 0.f), D = make_float2(0.f, 0.f);
+        if (p.dbias)
+            bias = make_float2(on0 ? p.dbias[ch] : 0.f, on1 ? p.dbias[ch + 1] : 0.f);
+        if (kY && p.D)
+            D = make_float2(on0 ? p.D[ch] : 0.f, on1 ? p.D[ch + 1] : 0.f);
+
+        uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
+        BcTile<T, kC> bc;
+        bc.start(p, p.Bm + w.b * p.Bb + w.g * p.Bg + tile0 * TT * p.Bs, p.Cm + w.b * p.Cb + w.g * p.Cg + tile0 * TT * p.Cs, id, 1);
+        auto load = [&](int rows) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const bool ok = pr + r * RG < rows;
+                ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
+                rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
+                u += us;
+                delta += ds;
+                rz[r] = 0u;
+                if (kC && p.z) {
+                    rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
+                    z += zs;
+                }
+                if (kR) {
+                    rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
+                    gy += gs;
+                }
+            }
+            bc.load(p, rows);
+        };
+        // what the recurrence needs of tile i, whose rows are in registers; then the next tile's are asked for
+        auto before = [&](int i) {
+            const int buf = i & 1, rows = rows_in(i);
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int row = pr + r * RG;
+                float2 dt = add2(unpack2<DT>(rd[r]), bias);
+                if (p.softplus)
+                    dt = softplus2(dt);
+                if (row >= rows)
+                    dt = make_float2(0.f, 0.f);
+                const float2 du = mul2(dt, unpack2<DT>(ru[r]));
+                *reinterpret_cast<float4 *>(&sh.sd[buf][row][pc]) = make_float4(dt.x, du.x, dt.y, du.y);
+                if (kY)
+                    sh.raw[buf][r][id] = make_uint2(ru[r], rz[r]);
+                if (kR) {
+                    float2 g = unpack2<DT>(rg[r]);
+                    if (p.z) {
+                        const float2 zv = unpack2<DT>(rz[r]);
+                        g = mul2(g, mul2(zv, sigmoid2(zv)));
+                    }
+                    *reinterpret_cast<float2 *>(&sh.sg[buf][row][pc]) = g;
+                }
+            }
+            bc.template put<DT>(p, sh.sB[buf], sh.sC[buf]);
+            if (i + 1 < n_tiles)
+                load(rows_in(i + 1));
+        };
+        // the outputs of tile i
+        const int last_all = (int)(p.S - (live_end - 1) * TT < TT ? p.S - (live_end - 1) * TT : TT);
+        auto after = [&](int i) {
+            const int buf = i & 1, rows = rows_in(i), all = i < n_tiles - 1 ? TT : last_all;
+#pragma unroll
+            for (int r = 0; r < RP; ++r, y += ys) {
+                const int row = pr + r * RG;
+                const uint2 rv = sh.raw[buf][r][id];
+                float2 v = *reinterpret_cast<const float2 *>(&sh.sy[buf][row][0][pc]);
+#pragma unroll
+                for (int k = 1; k < NL; ++k)
+                    v = add2(v, *reinterpret_cast<const float2 *>(&sh.sy[buf][row][k][pc]));
+                v = fma2(D, unpack2<DT>(rv.x), v);
+                if (p.z) {
+                    const float2 zv = unpack2<DT>(rv.y);
+                    v = mul2(v, mul2(zv, sigmoid2(zv)));
+                }
+                if (row < all)
+                    store_pair<PAIRS>(y, row < rows ? pack2<DT>(v) : 0u, on0, on1);
+            }
+        };
+        if (n_tiles > 0) {
+            load(rows_in(0));
+            before(0);
+        }
+        block_barrier(T::THREADS);
+        for (int i = 0; i < n_tiles; ++i) {
+            if (kY && i > 0)
+                after(i - 1);
+            if (i + 1 < n_tiles)
+                before(i + 1);
+            block_barrier(T::THREADS);
+        }
+        if (kY) {
+            if (n_tiles > 0)
+                after(n_tiles - 1);
+            // past the sequence's end: zeros, and the state stays
+            for (int64_t tile = tile0 + n_tiles; tile < tile1; ++tile) {
+                const int all = (int)(p.S - tile * TT < TT ? p.S - tile * TT : TT);
+#pragma unroll
+                for (int r = 0; r < RP; ++r, y += ys)
+                    if (pr + r * RG < all)
+                        store_pair<PAIRS>(y, 0u, on0, on1);
+            }
+        }
+        return;
+    }
+
+    // the recurrence: a lane's four states of each of its channels
+    const int lane = threadIdx.x & 31, j = T::state_lane(lane), n0 = 4 * j;
+    const int cl = (warp * T::CL + T::channel_lane(lane)) * K;   // first channel, within the block
     float2 A2[K][2], h[K][2], q[K][2], R[K][2];
     float dtsum[K];
 #pragma unroll
@@ -88,70 +206,14 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
         R[k][0] = R[k][1] = make_float2(0.f, 0.f);
         dtsum[k] = 0.f;
     }
-
-    uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
-    BcTile<T, kC> bc;
-    auto load = [&](int rows) {
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            const bool ok = pr + r * RG < rows;
-            ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
-            rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
-            u += us;
-            delta += ds;
-            if (kC && p.z) {
-                rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
-                z += zs;
-            }
-            if (kR) {
-                rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
-                gy += gs;
-            }
-        }
-        bc.load(p, Bm, Cm, rows);
-        Bm += TT * p.Bs;
-        Cm += TT * p.Cs;
-    };
-    // rows of tile i before `end`, at most TT (none or fewer past it)
-    auto rows_before = [](int64_t end, int64_t i) { return (int)(end - i * TT < TT ? end - i * TT : TT); };
-    if (rows_before(te, tile0) > 0)
-        load(rows_before(te, tile0));
-    int64_t tile = tile0;
-    for (; tile < tile1; ++tile) {
-        const int rows = rows_before(te, tile);
-        if (rows <= 0)
-            break;
-        uint32_t cu[RP], cz[RP];
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            const int row = pr + r * RG;
-            float2 dt = add2(unpack2<DT>(rd[r]), bias);
-            if (p.softplus)
-                dt = softplus2(dt);
-            if (row >= rows)
-                dt = make_float2(0.f, 0.f);
-            const float2 du = mul2(dt, unpack2<DT>(ru[r]));
-            *reinterpret_cast<float4 *>(&sd[row][pc]) = make_float4(dt.x, du.x, dt.y, du.y);
-            if (kR) {
-                float2 g = unpack2<DT>(rg[r]);
-                if (p.z) {
-                    const float2 zv = unpack2<DT>(rz[r]);
-                    g = mul2(g, mul2(zv, sigmoid2(zv)));
-                }
-                *reinterpret_cast<float2 *>(&sg[row][pc]) = g;
-            }
-            cu[r] = ru[r];
-            cz[r] = rz[r];
-        }
-        bc.template put<DT>(p, sB, sC);
-        __syncthreads();
-        if (tile + 1 < tile1 && rows_before(te, tile + 1) > 0)
-            load(rows_before(te, tile + 1));
+    block_barrier(T::THREADS);
+    for (int tile = 0; tile < n_tiles; ++tile) {
+        const int buf = tile & 1;
         if (kR) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (cl + k < w.nc) {
-                    const int64_t at = (tile * p.B + w.b) * p.H + w.c0 + cl + k;
+                    const int64_t at = ((tile0 + tile) * p.B + w.b) * p.H + w.c0 + cl + k;
                     *reinterpret_cast<float4 *>(p.cp + at * NP + n0) =
                         make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
                     if (j == 0)
@@ -167,13 +229,13 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
             for (int i = 0; i < U; ++i) {
                 float2 dd[K];
                 if (K == 2) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&sd[tb + i][cl]);
+                    const float4 v = *reinterpret_cast<const float4 *>(&sh.sd[buf][tb + i][cl]);
                     dd[0] = make_float2(v.x, v.y);
                     dd[K - 1] = make_float2(v.z, v.w);
                 } else {
-                    dd[0] = sd[tb + i][cl];
+                    dd[0] = sh.sd[buf][tb + i][cl];
                 }
-                const float4 bv = *reinterpret_cast<const float4 *>(&sB[tb + i][n0]);
+                const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[buf][tb + i][n0]);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const float2 dt2 = make_float2(dd[k].x, dd[k].x), du2 = make_float2(dd[k].y, dd[k].y);
@@ -189,7 +251,7 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
             for (int i = 0; i < U; ++i) {
                 float4 cv = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (kC)
-                    cv = *reinterpret_cast<const float4 *>(&sC[tb + i][n0]);
+                    cv = *reinterpret_cast<const float4 *>(&sh.sC[buf][tb + i][n0]);
                 const float2 c0 = make_float2(cv.x, cv.y), c1 = make_float2(cv.z, cv.w);
                 float part[K];
 #pragma unroll
@@ -201,7 +263,7 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
                         part[k] = s.x + s.y;
                     }
                     if (kR) {
-                        const float g = sg[tb + i][cl + k];
+                        const float g = sh.sg[buf][tb + i][cl + k];
                         const float2 g2 = make_float2(g, g);
                         q[k][0] = mul2(q[k][0], a[i][k][0]);
                         q[k][1] = mul2(q[k][1], a[i][k][1]);
@@ -211,40 +273,13 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
                 }
                 if (kY) {
                     if (K == 2)
-                        *reinterpret_cast<float2 *>(&sy[tb + i][j][cl]) = make_float2(part[0], part[K - 1]);
+                        *reinterpret_cast<float2 *>(&sh.sy[buf][tb + i][j][cl]) = make_float2(part[0], part[K - 1]);
                     else
-                        sy[tb + i][j][cl] = part[0];
+                        sh.sy[buf][tb + i][j][cl] = part[0];
                 }
             }
         }
-        __syncthreads();
-        if (kY) {
-            const int all = rows_before(p.S, tile);
-#pragma unroll
-            for (int r = 0; r < RP; ++r, y += ys) {
-                const int row = pr + r * RG;
-                float2 v = *reinterpret_cast<const float2 *>(&sy[row][0][pc]);
-#pragma unroll
-                for (int k = 1; k < NL; ++k)
-                    v = add2(v, *reinterpret_cast<const float2 *>(&sy[row][k][pc]));
-                v = fma2(D, unpack2<DT>(cu[r]), v);
-                if (p.z) {
-                    const float2 zv = unpack2<DT>(cz[r]);
-                    v = mul2(v, mul2(zv, sigmoid2(zv)));
-                }
-                if (row < all)
-                    store_pair<PAIRS>(y, row < rows ? pack2<DT>(v) : 0u, on0, on1);
-            }
-        }
-    }
-    if (kY) {   // past the sequence's end: zeros, and the state stays
-        for (; tile < tile1; ++tile) {
-            const int all = rows_before(p.S, tile);
-#pragma unroll
-            for (int r = 0; r < RP; ++r, y += ys)
-                if (pr + r * RG < all)
-                    store_pair<PAIRS>(y, 0u, on0, on1);
-        }
+        block_barrier(T::THREADS);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -267,13 +302,13 @@ __global__ void __launch_bounds__(T::THREADS, 4) mcc1d_ssm_scan(const ScanParams
     }
 }
 
-// Joins the chunks: e[c] becomes the state that enters chunk c, r[c] the
-// gradient that enters it from the right. One thread per four states of a
-// channel; a batch of chunks is loaded ahead of the recurrence over them.
-template <bool GRAD>
+// Joins the chunks: e[c] becomes the state that enters chunk c (blockIdx.y = 0),
+// r[c] the gradient that enters it from the right (blockIdx.y = 1). One thread
+// per four states of a channel; a batch of chunks is loaded ahead of the
+// recurrence over them.
 __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, int NL)
 {
-    constexpr int K = 4;
+    constexpr int K = 8;
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
     const int64_t rows = p.B * p.H;
     if (i >= rows * NL)
@@ -282,53 +317,34 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
     const int n0 = 4 * (int)(i - row * NL), NP = 4 * NL;
     const float4 A = load_states(p.A + row % p.H * p.N, n0, p.N, p.vecA);
     const float a[4] = {A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e};
+    const bool back = blockIdx.y == 1;
+    float *const at = back ? p.r : p.e;
+    const float *const first = back ? p.gfs : p.h0;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.h0)
-        s = load_states(p.h0 + row * p.N, n0, p.N, p.vecState);
+    if (first)
+        s = load_states(first + row * p.N, n0, p.N, p.vecState);
     for (int64_t c0 = 0; c0 < p.chunks; c0 += K) {
         float4 v[K];
         float d[K];
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (c0 + k < p.chunks) {
-                v[k] = *reinterpret_cast<const float4 *>(p.e + ((c0 + k) * rows + row) * NP + n0);
-                d[k] = p.dts[(c0 + k) * rows + row];
+                const int64_t c = (back ? p.chunks - 1 - c0 - k : c0 + k) * rows + row;
+                v[k] = *reinterpret_cast<const float4 *>(at + c * NP + n0);
+                d[k] = p.dts[c];
             }
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (c0 + k < p.chunks) {
-                *reinterpret_cast<float4 *>(p.e + ((c0 + k) * rows + row) * NP + n0) = s;
+                const int64_t c = (back ? p.chunks - 1 - c0 - k : c0 + k) * rows + row;
+                *reinterpret_cast<float4 *>(at + c * NP + n0) = s;
                 s.x = fmaf(ex2(a[0] * d[k]), s.x, v[k].x);
                 s.y = fmaf(ex2(a[1] * d[k]), s.y, v[k].y);
                 s.z = fmaf(ex2(a[2] * d[k]), s.z, v[k].z);
                 s.w = fmaf(ex2(a[3] * d[k]), s.w, v[k].w);
             }
     }
-    if (!GRAD)
-        return;
-    s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.gfs)
-        s = load_states(p.gfs + row * p.N, n0, p.N, p.vecState);
-    for (int64_t c0 = p.chunks - 1; c0 >= 0; c0 -= K) {
-        float4 v[K];
-        float d[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (c0 - k >= 0) {
-                v[k] = *reinterpret_cast<const float4 *>(p.r + ((c0 - k) * rows + row) * NP + n0);
-                d[k] = p.dts[(c0 - k) * rows + row];
-            }
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (c0 - k >= 0) {
-                *reinterpret_cast<float4 *>(p.r + ((c0 - k) * rows + row) * NP + n0) = s;
-                s.x = fmaf(ex2(a[0] * d[k]), s.x, v[k].x);
-                s.y = fmaf(ex2(a[1] * d[k]), s.y, v[k].y);
-                s.z = fmaf(ex2(a[2] * d[k]), s.z, v[k].z);
-                s.w = fmaf(ex2(a[3] * d[k]), s.w, v[k].w);
-            }
-    }
-    if (p.gstate)
+    if (back && p.gstate)
         store_states(p.gstate + row * p.N, n0, p.N, p.vecState, s);
 }
 
@@ -444,25 +460,23 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-// Tiles of a forward pass.
-template <int NL>
-using OutTile = ScanTile<NL, 4, 1, (NL < 4 ? 8 * NL : 32)>;
+template <class T, int DT, int MODE, bool PAIRS>
+int32_t launch_tile(const ScanParams &p, cudaStream_t s)
+{
+    constexpr int bytes = (int)sizeof(ScanShared<T, MODE>);
+    static SharedReady ready;
+    if (!ready.set((const void *)mcc1d_ssm_scan<T, DT, MODE, PAIRS>, bytes))
+        return kErrCuda;
+    mcc1d_ssm_scan<T, DT, MODE, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), T::THREADS, bytes, s>>>(p);
+    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
 template <class T, int MODE>
 int32_t run_tile(const ScanParams &p, int dtype, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(p.grid.blocks * p.B * p.chunks);
-    if (dtype == 0) {
-        if (p.pairs)
-            mcc1d_ssm_scan<T, 0, MODE, true><<<grid, T::THREADS, 0, s>>>(p);
-        else
-            mcc1d_ssm_scan<T, 0, MODE, false><<<grid, T::THREADS, 0, s>>>(p);
-    } else {
-        if (p.pairs)
-            mcc1d_ssm_scan<T, 1, MODE, true><<<grid, T::THREADS, 0, s>>>(p);
-        else
-            mcc1d_ssm_scan<T, 1, MODE, false><<<grid, T::THREADS, 0, s>>>(p);
-    }
-    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+    if (dtype == 0)
+        return p.pairs ? launch_tile<T, 0, MODE, true>(p, s) : launch_tile<T, 0, MODE, false>(p, s);
+    return p.pairs ? launch_tile<T, 1, MODE, true>(p, s) : launch_tile<T, 1, MODE, false>(p, s);
 }
 
 template <template <int> class Tile, int MODE>
@@ -546,15 +560,16 @@ void cut(ScanPlan &p, int64_t chunks)
 ScanPlan scan_plan(const mcc1d_scan_args &a)
 {
     ScanPlan p = shape_plan(a);
-    // One pass where it fills the machine about half; cutting the time axis
-    // computes the states twice, so it has to bring more than twice the blocks.
+    // Cutting the time axis computes the states twice, so it has to bring more
+    // than twice the warps: at 256 blocks (2048 tokens x 4 x 2048) one pass takes
+    // 174 us and cut in chunks 187, at 128 (4096 x 2 x 2048) 319 against 186.
     int cb;
     tile_shape<OutTile>(p.nl, cb, p.tt);
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.grid = scan_grid(a.H, a.G, cb);
-    const int64_t rows = p.grid.blocks * a.B, warps = rows * OutTile<4>::WARPS;
+    const int64_t rows = p.grid.blocks * a.B;
     const int64_t most = p.tiles / 4;     // a chunk of fewer tiles costs more launches than it saves
-    cut(p, warps >= 152 * 5 || most < 2 ? 1 : std::min((152 * 12 + warps - 1) / warps, most));
+    cut(p, rows >= 190 || most < 2 ? 1 : std::min(152 * 6 / rows, most));
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
@@ -644,11 +659,8 @@ static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint
 
 static int32_t join(const ScanParams &p, int nl, bool grad, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((p.B * p.H * nl + 127) / 128);
-    if (grad)
-        mcc1d_ssm_scan_join<true><<<grid, 128, 0, s>>>(p, nl);
-    else
-        mcc1d_ssm_scan_join<false><<<grid, 128, 0, s>>>(p, nl);
+    const dim3 grid((unsigned)((p.B * p.H * nl + 127) / 128), grad ? 2 : 1);
+    mcc1d_ssm_scan_join<<<grid, 128, 0, s>>>(p, nl);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 

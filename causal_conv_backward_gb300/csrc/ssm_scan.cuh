@@ -1,31 +1,35 @@
 // ssm_scan.cuh - what the selective scan's forward and backward kernels share:
 // their parameters, the tile loads and the sums over a channel's lanes.
 //
-// Layout of a block: NW warps; a channel's N states sit on NL lanes, four to a
-// lane, and a lane holds them for K channels, so a warp owns 32 K/NL channels
-// and the block CB = 32 K NW/NL, of one group and one sequence. It walks one
-// time chunk in tiles of TT rows. Loads, dt and the gate are done once per
-// (row, channel) by a thread that owns two adjacent channels of RP rows of the
-// tile; dt and dt u reach the lanes of the recurrence through shared memory,
-// and y comes back the same way.
+// Layout of a block: NW recurrence warps; a channel's N states sit on NL lanes,
+// four to a lane, and a lane holds them for K channels, so a warp owns 32 K/NL
+// channels and the block CB = 32 K NW/NL, of one group and one sequence. It
+// walks one time chunk in tiles of TT rows. EW further warps do what is needed
+// once per (row, channel): the loads, dt and the gate for the tile after the
+// one the recurrence is in, and the outputs of the tile before it. A thread of
+// theirs owns two adjacent channels of RP rows of the tile. The two kinds meet
+// in shared memory, in two buffers, with one barrier per tile.
 #pragma once
 
+#include <atomic>
+
+#include "device.h"
 #include "ssm.h"
 #include "ssm_common.cuh"
 
 namespace mcc1d {
 
-template <int NL_, int NW, int K_, int TT_>
+template <int NL_, int NW, int EW, int K_, int TT_>
 struct ScanTile {
     static constexpr int NL = NL_, K = K_, TT = TT_, WARPS = NW;
-    static constexpr int THREADS = 32 * NW;
+    static constexpr int THREADS = 32 * (NW + EW), EL_THREADS = 32 * EW;
     static constexpr int NP = 4 * NL;              // states, padded
     static constexpr int CL = 32 / NL;             // lanes of one state
     static constexpr int CB = NW * CL * K;         // channels per block
     static constexpr int CP = CB / 2;              // channel pairs per row
-    static constexpr int RG = THREADS / CP;        // rows of one pass over a tile
+    static constexpr int RG = EL_THREADS / CP;     // rows of one pass over a tile
     static constexpr int RP = TT / RG;             // rows per thread
-    static_assert(RG >= 1 && RP >= 1 && RG * CP == THREADS && RP * RG == TT, "a tile is whole passes");
+    static_assert(RG >= 1 && RP >= 1 && RG * CP == EL_THREADS && RP * RG == TT, "a tile is whole passes");
 
     // A lane's number among a channel's NL, and its (first) channel / K in the
     // warp. Shared-memory loads of 8 and 16 bytes run at their full rate only
@@ -40,10 +44,22 @@ struct ScanTile {
     __device__ __forceinline__ static int channel_lane(int lane) { return NL == 1 ? lane : (lane >> 1) % CL; }
 };
 
-// Tiles of the backward, and of the pass before it: two channels per lane, so
-// that grad_B's and grad_C's sums over channels start inside the lane.
+// Tiles of the forward. Two channels per lane: B and C are read from shared
+// memory once for both, without which its bandwidth is the first limit (1024
+// tokens x 8 sequences x 2048 channels: 107 us, one channel per lane 124 us).
+// At N = 16 the element warps have as much to do for a tile as the recurrence
+// warps; fewer states shift that, as more do.
 template <int NL>
-using BwdTile = ScanTile<NL, 4, 2, (NL < 8 ? 4 * NL : 32)>;
+using OutTile = ScanTile<NL, 2, (NL < 4 ? 4 : NL == 4 ? 2 : 1), 2, (NL == 1 ? 8 : 16)>;
+// Tiles of the backward's first pass, with the rows and channels of its second.
+template <int NL>
+using BwdTile = ScanTile<NL, 4, (NL < 8 ? 4 : NL == 8 ? 2 : 1), 2, (NL < 4 ? 4 * NL : 16)>;
+// Tiles of the backward's second pass: the same rows and channels, and the
+// recurrence warps do the elements' part too, so that every warp has the
+// registers of a recurrence warp. Two channels per lane, so that grad_B's and
+// grad_C's sums over channels start inside the lane.
+template <int NL>
+using BwdMainTile = ScanTile<NL, 4, 4, 2, BwdTile<NL>::TT>;
 
 struct ScanParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm, *gy;
@@ -62,6 +78,22 @@ struct ScanParams {
 };
 
 int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1d_scan_bwd_args &a, cudaStream_t s);
+
+// A kernel's shared-memory limit, raised once per context: a context created
+// after a device reset starts without the attribute.
+struct SharedReady {
+    std::atomic<unsigned long long> ctx{0};
+    bool set(const void *kernel, int bytes)
+    {
+        const unsigned long long now = current_context_id();
+        if (now != 0 && ctx.load(std::memory_order_acquire) == now)
+            return true;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return false;
+        ctx.store(now != 0 ? now : current_context_id(), std::memory_order_release);
+        return true;
+    }
+};
 
 // Where a block works.
 struct ScanWhere {
@@ -174,43 +206,64 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N], int lane)
 // past N. KC: C too, not B alone.
 template <class T, bool KC>
 struct BcTile {
-    static constexpr int NP = T::NP, TT = T::TT, THREADS = T::THREADS, TENSORS = KC ? 2 : 1;
+    static constexpr int NP = T::NP, TT = T::TT, THREADS = T::EL_THREADS, TENSORS = KC ? 2 : 1;
     static constexpr int PAIRS = TENSORS * TT * NP / 2, WORDS = (PAIRS + THREADS - 1) / THREADS;
     static constexpr int EIGHTS = NP >= 8 ? PAIRS / 4 : 0, VECS = (EIGHTS + THREADS - 1) / THREADS;
     static constexpr int N = WORDS > 4 * VECS ? WORDS : 4 * VECS;
     uint32_t v[N];
+    int id;                                  // of the thread, among THREADS
+    const uint16_t *B_, *C_, *src[VECS > 0 ? VECS : 1];
+    int64_t Bstep, Cstep;
+    int row8[VECS > 0 ? VECS : 1];           // TT where there is nothing to load
 
     template <bool BOTH>
     __device__ __forceinline__ void load_pairs(const ScanParams &p, const uint16_t *B, const uint16_t *C, int rows)
     {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-            const int k = threadIdx.x + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
+            const int k = id + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
             const bool on = k < PAIRS && row < rows, c = k >= TT * NP / 2;
             const uint16_t *src = c ? C + row * p.Cs + n : B + row * p.Bs + n;
             v[i] = load_pair<BOTH>(src, on && n < p.N, on && n + 1 < p.N);
         }
     }
     // The eight states of vector i: its tensor (C if true), row and first state.
-    __device__ __forceinline__ static bool place8(int i, int &row, int &n)
+    __device__ __forceinline__ bool place8(int i, int &row, int &n) const
     {
-        const int k = threadIdx.x + i * THREADS, q = k % (EIGHTS / TENSORS);
+        const int k = id + i * THREADS, q = k % (EIGHTS / TENSORS);
         row = q / (NP / 8);
         n = 8 * (q % (NP / 8));
         return k >= EIGHTS / TENSORS;
     }
-    // B, C: the tile's first rows
-    __device__ __forceinline__ void load(const ScanParams &p, const uint16_t *B, const uint16_t *C, int rows)
+    // B, C: the first tile's first rows; dir: 1 where the tiles run forwards, -1 backwards.
+    __device__ __forceinline__ void start(const ScanParams &p, const uint16_t *B, const uint16_t *C, int thread, int dir)
+    {
+        id = thread;
+        B_ = B;
+        C_ = C;
+        Bstep = dir * TT * p.Bs;
+        Cstep = dir * TT * p.Cs;
+        if constexpr (VECS > 0) {
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                int row, n;
+                const bool c = place8(i, row, n), in = id + i * THREADS < EIGHTS && n < p.N;
+                src[i] = c ? C + row * p.Cs + n : B + row * p.Bs + n;
+                row8[i] = in ? row : TT;
+            }
+        }
+    }
+    // The next tile, of which `rows` rows hold tokens.
+    __device__ __forceinline__ void load(const ScanParams &p, int rows)
     {
         if constexpr (VECS > 0) {
             if (p.bc8) {
 #pragma unroll
                 for (int i = 0; i < VECS; ++i) {
-                    int row, n;
-                    const bool c = place8(i, row, n);
                     uint4 r = make_uint4(0u, 0u, 0u, 0u);
-                    if (threadIdx.x + i * THREADS < EIGHTS && row < rows && n < p.N)
-                        r = __ldg(reinterpret_cast<const uint4 *>(c ? C + row * p.Cs + n : B + row * p.Bs + n));
+                    if (row8[i] < rows)
+                        r = __ldg(reinterpret_cast<const uint4 *>(src[i]));
+                    src[i] += id + i * THREADS >= EIGHTS / TENSORS ? Cstep : Bstep;
                     v[4 * i] = r.x;
                     v[4 * i + 1] = r.y;
                     v[4 * i + 2] = r.z;
@@ -220,9 +273,11 @@ struct BcTile {
             }
         }
         if (p.bcpairs)
-            load_pairs<true>(p, B, C, rows);
+            load_pairs<true>(p, B_, C_, rows);
         else
-            load_pairs<false>(p, B, C, rows);
+            load_pairs<false>(p, B_, C_, rows);
+        B_ += Bstep;
+        C_ += Cstep;
     }
     template <int DT>
     __device__ __forceinline__ void put(const ScanParams &p, float (*sB)[NP], float (*sC)[NP]) const
@@ -233,7 +288,7 @@ struct BcTile {
                 for (int i = 0; i < VECS; ++i) {
                     int row, n;
                     const bool c = place8(i, row, n);
-                    if (threadIdx.x + i * THREADS >= EIGHTS)
+                    if (id + i * THREADS >= EIGHTS)
                         break;
                     float4 *dst = reinterpret_cast<float4 *>(KC && c ? &sC[row][n] : &sB[row][n]);
                     const float2 e = unpack2<DT>(v[4 * i]), f = unpack2<DT>(v[4 * i + 1]);
@@ -246,7 +301,7 @@ struct BcTile {
         }
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-            const int k = threadIdx.x + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
+            const int k = id + i * THREADS, q = k % (TT * NP / 2), row = q / (NP / 2), n = 2 * (q % (NP / 2));
             if (k >= PAIRS)
                 break;
             float *dst = KC && k >= TT * NP / 2 ? &sC[row][n] : &sB[row][n];

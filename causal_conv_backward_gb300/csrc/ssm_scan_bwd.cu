@@ -18,9 +18,6 @@
 // recurrence back. Sums over a channel's states and over a warp's channels go
 // through shuffles, those over warps and blocks through memory, in a fixed
 // order.
-#include <atomic>
-
-#include "device.h"
 #include "plan.h"
 #include "ssm_scan.cuh"
 
@@ -29,22 +26,27 @@ namespace mcc1d {
 namespace {
 
 constexpr int kSub = 2;          // rows whose states and decays sit in registers
-constexpr int kBlocksPerSM = 3;
+constexpr int kBlocksPerSM = 4;
 
 template <int NL>
 struct BwdShared {
-    using T = BwdTile<NL>;
+    using T = BwdMainTile<NL>;
     static constexpr int TT = T::TT;
     float4 sq[TT][T::CB];                         // dt, dt u, dy, dt; the first three then sum A log2e q, sum g B, y
-    float4 hs[TT / kSub][T::K][T::THREADS];       // states before each run of kSub rows
+    float4 hs[TT / kSub][T::K][T::EL_THREADS];       // states before each run of kSub rows
     float sB[TT][T::NP], sC[TT][T::NP];
-    float bc[TT][T::WARPS][2 * T::NP];            // a warp's grad_B and grad_C
+    // A warp's grad_B and grad_C of row s + i take the place of its own hs[s / kSub][i], which it has read by then.
+    static_assert(kSub <= T::K && 2 * T::NP <= 4 * 32, "a row of sums fits a warp's states of one channel");
+    __device__ __forceinline__ float *bc(int row, int warp)
+    {
+        return reinterpret_cast<float *>(&hs[row / kSub][row % kSub][32 * warp]);
+    }
 };
 
 template <int DT, int NL, bool PAIRS>
-__global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_scan_bwd(const ScanParams p)
+__global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc1d_ssm_scan_bwd(const ScanParams p)
 {
-    using T = BwdTile<NL>;
+    using T = BwdMainTile<NL>;
     using Sh = BwdShared<NL>;
     constexpr int NP = T::NP, CL = T::CL, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
     extern __shared__ __align__(16) unsigned char raw_shared[];
@@ -82,44 +84,49 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_
 
     const int64_t tile0 = w.chunk * p.tiles_per_chunk;
     const int64_t tile1 = tile0 + p.tiles_per_chunk < p.tiles ? tile0 + p.tiles_per_chunk : p.tiles;
-    for (int64_t tile = tile1 - 1; tile >= tile0; --tile) {
-        const int64_t t0 = tile * TT, trow = t0 + pr;
-        const int rows = (int)(te - t0 < TT ? te - t0 : TT), all = (int)(p.S - t0 < TT ? p.S - t0 : TT);
-        const int64_t o0 = (trow * p.B + w.b) * p.H + ch, os = RG * p.B * p.H;
-        if (rows <= 0) {
-            int64_t o = o0;
+    const int64_t live_end = (te + TT - 1) / TT < tile1 ? (te + TT - 1) / TT : tile1;   // past the tiles with tokens
+    const int64_t os = RG * p.B * p.H;
+    // past the sequence's end: zeros
+    for (int64_t tile = tile1 - 1; tile >= tile0 && tile >= live_end; --tile) {
+        int64_t o = ((tile * TT + pr) * p.B + w.b) * p.H + ch;
 #pragma unroll
-            for (int r = 0; r < RP; ++r, o += os)
-                if (pr + r * RG < all) {
-                    store_pair<PAIRS>(p.gu + o, 0u, on0, on1);
-                    store_pair<PAIRS>(p.gdelta + o, 0u, on0, on1);
-                    if (p.gz)
-                        store_pair<PAIRS>(p.gz + o, 0u, on0, on1);
-                }
-            continue;
-        }
-        uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
-        {
-            BcTile<T, true> bc;
-            const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
-            const uint16_t *z = p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr, *gy = p.gy + w.b * p.gb + ch + trow * p.gs;
-#pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                const bool ok = pr + r * RG < rows;
-                ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
-                rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
-                rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
-                u += RG * p.us;
-                delta += RG * p.ds;
-                gy += RG * p.gs;
-                if (p.z) {
-                    rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
-                    z += RG * p.zs;
-                }
+        for (int r = 0; r < RP; ++r, o += os)
+            if (tile * TT + pr + r * RG < p.S) {
+                store_pair<PAIRS>(p.gu + o, 0u, on0, on1);
+                store_pair<PAIRS>(p.gdelta + o, 0u, on0, on1);
+                if (p.gz)
+                    store_pair<PAIRS>(p.gz + o, 0u, on0, on1);
             }
-            bc.load(p, Bm + t0 * p.Bs, Cm + t0 * p.Cs, rows);
-            bc.template put<DT>(p, sh.sB, sh.sC);
+    }
+    auto load = [&](int64_t tile, uint32_t (&ru)[RP], uint32_t (&rd)[RP], uint32_t (&rz)[RP], uint32_t (&rg)[RP]) {
+        const int64_t trow = tile * TT + pr;
+        const int rows = (int)(te - tile * TT < TT ? te - tile * TT : TT);
+        const uint16_t *u = p.u + w.b * p.ub + ch + trow * p.us, *delta = p.delta + w.b * p.db + ch + trow * p.ds;
+        const uint16_t *z = p.z ? p.z + w.b * p.zb + ch + trow * p.zs : nullptr, *gy = p.gy + w.b * p.gb + ch + trow * p.gs;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+            const bool ok = pr + r * RG < rows;
+            ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
+            rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
+            rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
+            u += RG * p.us;
+            delta += RG * p.ds;
+            gy += RG * p.gs;
+            if (p.z) {
+                rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
+                z += RG * p.zs;
+            }
         }
+    };
+    BcTile<T, true> bc;
+    bc.start(p, Bm + (live_end - 1) * TT * p.Bs, Cm + (live_end - 1) * TT * p.Cs, threadIdx.x, -1);
+    for (int64_t tile = live_end - 1; tile >= tile0; --tile) {
+        const int64_t t0 = tile * TT;
+        const int rows = (int)(te - t0 < TT ? te - t0 : TT), all = (int)(p.S - t0 < TT ? p.S - t0 : TT);
+        uint32_t ru[RP], rd[RP], rz[RP], rg[RP];   // read again at the tile's end rather than held
+        load(tile, ru, rd, rz, rg);
+        bc.load(p, rows);
+        bc.template put<DT>(p, sh.sB, sh.sC);
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
             const int row = pr + r * RG;
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_
                 hh[0][k][0] = make_float2(v.x, v.y);
                 hh[0][k][1] = make_float2(v.z, v.w);
             }
+            __syncwarp();   // the warp's sums take the place of these
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_
                 constexpr int KEEP = CL >= 8 ? 1 : 8 / CL;
                 if (ci < 8) {
                     const int k = (ci * KEEP) % 8;      // v[0..KEEP-1] are values k.. of the eight
-                    float *o = &sh.bc[s + i][warp][(k / 4) * NP + n0 + k % 4];
+                    float *o = sh.bc(s + i, warp) + (k / 4) * NP + n0 + k % 4;
 #pragma unroll
                     for (int m = 0; m < KEEP; ++m)
                         o[m] = v[m];
@@ -255,22 +263,23 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_
             gA[k][1] = add2(gA[k][1], tA[k][1]);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < TT * 2 * NP; i += T::THREADS) {
+        for (int i = threadIdx.x; i < TT * 2 * NP; i += T::EL_THREADS) {
             const int row = i / (2 * NP), k = i % (2 * NP);
-            float s = sh.bc[row][0][k];
+            float s = sh.bc(row, 0)[k];
 #pragma unroll
             for (int q = 1; q < T::WARPS; ++q)
-                s += sh.bc[row][q][k];
+                s += sh.bc(row, q)[k];
             if (row < rows)
                 p.bc[(((t0 + row) * p.B + w.b) * p.grid.blocks + w.blk) * (2 * NP) + k] = s;
         }
-        int64_t o = o0;
+        int64_t o = ((t0 + pr) * p.B + w.b) * p.H + ch;
+        load(tile, ru, rd, rz, rg);
 #pragma unroll
         for (int r = 0; r < RP; ++r, o += os) {
             const int row = pr + r * RG;
+            const bool in = row < rows;
             const float4 s0 = sh.sq[row][pc], s1 = sh.sq[row][pc + 1];
             const float2 uv = unpack2<DT>(ru[r]), raw = add2(unpack2<DT>(rd[r]), bias), sb = make_float2(s0.y, s1.y);
-            const bool in = row < rows;
             float2 dy = unpack2<DT>(rg[r]);
             if (p.z) {
                 const float2 zv = unpack2<DT>(rz[r]), sz = sigmoid2(zv), one = make_float2(1.f, 1.f);
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, kBlocksPerSM) mcc1d_ssm_
                 store_pair<PAIRS>(p.gdelta + o, in ? pack2<DT>(gr) : 0u, on0, on1);
             }
         }
-        __syncthreads();   // bc is written again in the next tile
+        __syncthreads();   // hs is written again in the next tile
     }
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -382,16 +391,10 @@ template <int DT, int NL, bool PAIRS>
 int32_t run_pairs(const ScanParams &p, cudaStream_t s)
 {
     constexpr int bytes = (int)sizeof(BwdShared<NL>);
-    // once per context: a context created after a device reset starts without the attribute
-    static std::atomic<unsigned long long> ready{0};
-    const unsigned long long ctx = current_context_id();
-    if (ctx == 0 || ready.load(std::memory_order_acquire) != ctx) {
-        if (cudaFuncSetAttribute(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 bytes) != cudaSuccess)
-            return kErrCuda;
-        ready.store(ctx, std::memory_order_release);
-    }
-    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), BwdTile<NL>::THREADS, bytes, s>>>(p);
+    static SharedReady ready;
+    if (!ready.set((const void *)mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, bytes))
+        return kErrCuda;
+    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), BwdMainTile<NL>::EL_THREADS, bytes, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
