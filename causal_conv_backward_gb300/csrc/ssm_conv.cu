@@ -122,8 +122,14 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams 
                 emit(in[r], dst);
         }
         src += (te - t0 - left) * p.xs;
-        for (; left > 0; --left, src += p.xs, dst += ys)
-            emit(vload<V>(src), dst);
+        Vec<V> rest[kRows - 1];
+#pragma unroll
+        for (int r = 0; r < kRows - 1; ++r, src += p.xs)
+            rest[r] = r < left ? vload<V>(src) : vzero<V>();
+#pragma unroll
+        for (int r = 0; r < kRows - 1; ++r, dst += ys)
+            if (r < left)
+                emit(rest[r], dst);
     }
     for (int64_t t = t0 > te ? t0 : te; t < t1; ++t)
         vstore<V>(y + t * ys, vzero<V>());
@@ -253,7 +259,7 @@ int32_t launch_short_conv(const mcc1d_short_conv_args &a, cudaStream_t stream)
     p.vecs = a.H / V;
     const int64_t lanes = a.B * p.vecs, blocks = (lanes + kThreads - 1) / kThreads;
     // long runs of rows re-read fewer window rows; short ones give more threads
-    int64_t L = 32;
+    int64_t L = 128;
     while (L > 8 && blocks * ((a.S + L - 1) / L) < 152 * 8)
         L /= 2;
     while ((a.S + L - 1) / L > 65535)

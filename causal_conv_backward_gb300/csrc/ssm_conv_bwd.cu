@@ -22,6 +22,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRows = 4;     // rows of a batch
 constexpr int kStages = 3;   // batches, all but one in flight
+constexpr int kEdge = 2;     // rows that go one by one, loaded together
 
 struct ConvBwdParams {
     const uint16_t *gy, *x, *weight, *bias, *state, *gfs;
@@ -143,26 +144,39 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
             }
             return out;
         };
-        auto edge = [&](int64_t r) {
-            const bool in = r < live;
-            const int64_t t = r - (W - 1);
-            Vec<V> gf = vzero<V>();
-            if (p.gfs && t >= len - (W - 1) && t < len)
-                gf = vload<V>(p.gfs + (b * (W - 1) + (t - (len - (W - 1)))) * p.H + h);
-            const Vec<V> out = row(in ? vload<V>(x + r * p.xs) : vzero<V>(), in ? vload<V>(gy + r * p.gs) : vzero<V>(), gf,
-                                   r < t1, in);
-            if (t < first)
-                return;
-            if (t >= 0)
-                vstore<V>(gx + t * ys, out);
-            else if (p.gstate)
-                vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
+        // Rows r..end-1 with every check, kEdge of them loaded together.
+        auto edges = [&](int64_t r, int64_t end) {
+            for (; r < end; r += kEdge) {
+                Vec<V> ex[kEdge], eg[kEdge], gf[kEdge];
+#pragma unroll
+                for (int i = 0; i < kEdge; ++i) {
+                    const int64_t q = r + i, t = q - (W - 1);
+                    const bool in = q < live && q < end;
+                    ex[i] = in ? vload<V>(x + q * p.xs) : vzero<V>();
+                    eg[i] = in ? vload<V>(gy + q * p.gs) : vzero<V>();
+                    gf[i] = vzero<V>();
+                    if (p.gfs && t >= len - (W - 1) && t < len && q < end)
+                        gf[i] = vload<V>(p.gfs + (b * (W - 1) + (t - (len - (W - 1)))) * p.H + h);
+                }
+#pragma unroll
+                for (int i = 0; i < kEdge; ++i) {
+                    const int64_t q = r + i, t = q - (W - 1);
+                    if (q >= end)
+                        break;
+                    const Vec<V> out = row(ex[i], eg[i], gf[i], q < t1, q < live);
+                    if (t < first)
+                        continue;
+                    if (t >= 0)
+                        vstore<V>(gx + t * ys, out);
+                    else if (p.gstate)
+                        vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
+                }
+            }
         };
         // the first W-1 rows and what is near the run's or the sequence's end go one by one; between them
         // batches of rows
-        int64_t r = t0;
-        for (; r < t0 + W - 1 && r < rend; ++r)
-            edge(r);
+        int64_t r = t0 + W - 1 < rend ? t0 + W - 1 : rend;
+        edges(t0, r);
         const int64_t stop = t1 < len ? t1 : len;
         int64_t left = stop - r;
         uint16_t *to = gx + (r - (W - 1)) * ys;
@@ -183,8 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
             for (int i = 0; i < kRows; ++i, to += ys)
                 vstore<V>(to, row(in[2 * i], in[2 * i + 1], vzero<V>(), true, true));
         }
-        for (; r < rend; ++r)
-            edge(r);
+        edges(r, rend);
     }
     __syncthreads();
 #pragma unroll
@@ -272,10 +285,13 @@ int bwd_vec(const mcc1d_short_conv_bwd_args &a)
 ConvBwdPlan conv_bwd_plan(const mcc1d_short_conv_bwd_args &a)
 {
     ConvBwdPlan p;
-    // 64 rows per warp re-read W-1 in 64; fewer where that leaves SMs idle
+    // Every run of rows begins and ends with rows that go one by one: 64 rows per
+    // warp cost 371 us on 8192 x 8 x 4096, 128 334, 256 311 and 512 338. Fewer
+    // rows where that leaves less than a block per SM (at two blocks per SM
+    // 4096 x 2 x 2048 took 41 us, at one 36)
     const int64_t wide = (a.H + 127) / 128 * a.B;
-    int64_t L = 64;
-    while (L > 8 && wide * ((a.S + 8 * L - 1) / (8 * L)) < 152 * 2)
+    int64_t L = 256;
+    while (L > 8 && wide * ((a.S + 8 * L - 1) / (8 * L)) < 152)
         L /= 2;
     p.L = (int32_t)L;
     p.supers = (a.S + kWarps * L - 1) / (kWarps * L);

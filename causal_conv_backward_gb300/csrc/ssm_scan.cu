@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
     using Sh = ScanShared<T, MODE>;
     constexpr int NP = T::NP, NL = T::NL, TT = T::TT, RG = T::RG, RP = T::RP, K = T::K;
     constexpr bool kY = Sh::kY, kR = Sh::kR, kC = Sh::kC;
-    constexpr int U = 4;                     // steps of the recurrence taken together
+    constexpr int U = 2;                     // steps of the recurrence taken together
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
@@ -569,7 +569,7 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
     p.grid = scan_grid(a.H, a.G, cb);
     const int64_t rows = p.grid.blocks * a.B;
     const int64_t most = p.tiles / 4;     // a chunk of fewer tiles costs more launches than it saves
-    cut(p, rows >= 190 || most < 2 ? 1 : std::min(152 * 6 / rows, most));
+    cut(p, rows >= 190 || most < 2 ? 1 : std::min(152 * 8 / rows, most));
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);

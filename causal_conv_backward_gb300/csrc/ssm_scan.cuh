@@ -47,10 +47,10 @@ struct ScanTile {
 // Tiles of the forward. Two channels per lane: B and C are read from shared
 // memory once for both, without which its bandwidth is the first limit (1024
 // tokens x 8 sequences x 2048 channels: 107 us, one channel per lane 124 us).
-// At N = 16 the element warps have as much to do for a tile as the recurrence
-// warps; fewer states shift that, as more do.
+// At N = 16 the element warps are what a block alone on its SM waits for (222 us
+// with or without the recurrence on 4096 x 1 x 2048), so they are four.
 template <int NL>
-using OutTile = ScanTile<NL, 2, (NL < 4 ? 4 : NL == 4 ? 2 : 1), 2, (NL == 1 ? 8 : 16)>;
+using OutTile = ScanTile<NL, 2, (NL <= 4 ? 4 : NL == 8 ? 2 : 1), 2, (NL == 1 ? 8 : 16)>;
 // Tiles of the backward's first pass, with the rows and channels of its second.
 template <int NL>
 using BwdTile = ScanTile<NL, 4, (NL < 8 ? 4 : NL == 8 ? 2 : 1), 2, (NL < 4 ? 4 * NL : 16)>;

@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_bc(const ScanParams p,
     float s = 0.f;
     if (t < clamped_length(p.lengths, b, p.S)) {
         const float *src = p.bc + (row * p.grid.blocks + g * p.grid.blocks_per_group) * (2 * NP) + k;
+#pragma unroll 8
         for (int m = 0; m < p.grid.blocks_per_group; ++m)
             s += src[(int64_t)m * 2 * NP];
     }
