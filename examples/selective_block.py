@@ -104,7 +104,7 @@ class SelectiveBlock(torch.nn.Module):
         return self.out_proj(y)
 
 
-def train(block, steps=60, S=64, B=16, lag=5, lr=3e-3):
+def train(block, steps=60, S=64, B=16, lag=2, lr=1e-2):
     """Learns to give back its input of `lag` tokens ago; returns the losses."""
     g = torch.Generator(device="cuda").manual_seed(0)
     width = block.in_proj.in_features
