@@ -467,7 +467,7 @@ int32_t launch_tile(const ScanParams &p, cudaStream_t s)
     static SharedReady ready;
     if (!ready.set((const void *)mcc1d_ssm_scan<T, DT, MODE, PAIRS>, bytes))
         return kErrCuda;
-    mcc1d_ssm_scan<T, DT, MODE, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), T::THREADS, bytes, s>>>(p);
+    mcc1d_ssm_scan<T, DT, MODE, PAIRS><<<scan_launch_grid(p), T::THREADS, bytes, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
@@ -545,12 +545,30 @@ void tile_shape(int nl, int &cb, int &tt)
     }
 }
 
-void cut(ScanPlan &p, int64_t chunks)
+// Cuts the time axis into at most `most` chunks. The machine holds kSlots
+// blocks at once, and a chunk costs about kChunkTiles tiles besides its own
+// (setup, the join): the fewest waves of the fewest tiles, of more than
+// `waves_above` waves where that can be had. (The backward's two passes hold
+// different numbers of blocks, so two waves of one are ragged in the other:
+// 1024 x 8 x 2048 took 523 us in 512 blocks a pass and 453 in 1792.)
+void cut(ScanPlan &p, int64_t rows, int64_t most, int64_t waves_above)
 {
-    if (chunks > p.tiles)
-        chunks = p.tiles;
-    if (chunks < 1)
-        chunks = 1;
+    constexpr int64_t kSlots = 152 * 4, kChunkTiles = 2;
+    most = std::min(std::max<int64_t>(most, 1), p.tiles);
+    int64_t best = 0, chunks = 1;
+    auto consider = [&](int64_t c) {
+        if (c < 1 || c > most || (c < most && rows * c <= kSlots * waves_above))
+            return;
+        const int64_t cost = (rows * c + kSlots - 1) / kSlots * ((p.tiles + c - 1) / c + kChunkTiles);
+        if (best == 0 || cost < best) {
+            best = cost;
+            chunks = c;
+        }
+    };
+    for (int64_t c = 1; c <= 4; ++c)
+        consider(c);
+    for (int64_t waves = 1; waves <= 7; ++waves)
+        consider(std::min(kSlots * waves / rows, most));
     p.tiles_per_chunk = (p.tiles + chunks - 1) / chunks;
     p.chunks = (p.tiles + p.tiles_per_chunk - 1) / p.tiles_per_chunk;
 }
@@ -568,8 +586,7 @@ ScanPlan scan_plan(const mcc1d_scan_args &a)
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.grid = scan_grid(a.H, a.G, cb);
     const int64_t rows = p.grid.blocks * a.B;
-    const int64_t most = p.tiles / 4;     // a chunk of fewer tiles costs more launches than it saves
-    cut(p, rows >= 190 || most < 2 ? 1 : std::min(152 * 8 / rows, most));
+    cut(p, rows, rows >= 190 ? 1 : p.tiles / 4, 0);   // chunks of fewer than 4 tiles cost more launches than they save
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
@@ -590,7 +607,7 @@ ScanPlan scan_bwd_plan(const mcc1d_scan_bwd_args &ba)
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.grid = scan_grid(a.H, a.G, cb);
     const int64_t rows = p.grid.blocks * a.B;
-    cut(p, (152 * 12 + rows - 1) / rows);
+    cut(p, rows, p.tiles, 2);
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);

@@ -95,7 +95,12 @@ struct SharedReady {
     }
 };
 
-// Where a block works.
+inline dim3 scan_launch_grid(const ScanParams &p)
+{
+    return dim3((unsigned)p.grid.blocks, (unsigned)p.B, (unsigned)p.chunks);
+}
+
+// Where a block works: blockIdx = (channel block, sequence, chunk).
 struct ScanWhere {
     int64_t chunk, b;
     int32_t blk, g;
@@ -107,11 +112,9 @@ template <class T>
 __device__ __forceinline__ ScanWhere scan_where(const ScanParams &p)
 {
     ScanWhere w;
-    const int64_t i = blockIdx.x;
-    w.blk = (int32_t)(i % p.grid.blocks);
-    const int64_t q = i / p.grid.blocks;
-    w.b = q % p.B;
-    w.chunk = q / p.B;
+    w.blk = (int32_t)blockIdx.x;
+    w.b = blockIdx.y;
+    w.chunk = blockIdx.z;
     w.g = w.blk / p.grid.blocks_per_group;
     const int32_t in = (w.blk - w.g * p.grid.blocks_per_group) * T::CB;
     w.c0 = w.g * p.Hg + in;

@@ -395,7 +395,7 @@ int32_t run_pairs(const ScanParams &p, cudaStream_t s)
     static SharedReady ready;
     if (!ready.set((const void *)mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, bytes))
         return kErrCuda;
-    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<(unsigned)(p.grid.blocks * p.B * p.chunks), BwdMainTile<NL>::EL_THREADS, bytes, s>>>(p);
+    mcc1d_ssm_scan_bwd<DT, NL, PAIRS><<<scan_launch_grid(p), BwdMainTile<NL>::EL_THREADS, bytes, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
