@@ -119,7 +119,7 @@ int32_t check(const mcc1d_scan_args *a, bool out)
     if (!shape_ok(a->S, a->B, a->H) || !states_ok(a->B, a->H, a->N, a->G))
         return kErrShape;
     // a backward thread owns one value of the group sums over [S,B,G,2N]
-    if ((double)a->S * (double)a->B * (double)a->G * 128.0 > (double)kMaxGrid * 256.0)
+    if ((double)a->S * (double)a->B * (double)a->G * 128.0 > (double)(kMaxGrid / 2) * 256.0)
         return kErrShape;
     if (!strides_ok(a->u_strides) || !strides_ok(a->delta_strides) || (a->z && !strides_ok(a->z_strides)) ||
         !strides_ok(a->B_strides) || !strides_ok(a->C_strides) ||

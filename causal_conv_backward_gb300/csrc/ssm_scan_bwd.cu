@@ -118,6 +118,11 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
             }
         }
     };
+    // a thread's sums of grad_B and grad_C in the tile: column bk of rows brow, brow + BR, ..
+    constexpr int BR = T::EL_THREADS / (2 * NP), BN = TT > BR ? TT / BR : 1;
+    static_assert(BR >= 1 && (TT % BR == 0 || BR > TT), "a tile is whole passes");
+    const int bk = threadIdx.x % (2 * NP), brow = threadIdx.x / (2 * NP);
+    const int64_t bstep = (int64_t)p.B * p.grid.blocks * (2 * NP);
     BcTile<T, true> bc;
     bc.start(p, Bm + (live_end - 1) * TT * p.Bs, Cm + (live_end - 1) * TT * p.Cs, threadIdx.x, -1);
     for (int64_t tile = live_end - 1; tile >= tile0; --tile) {
@@ -263,17 +268,20 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
             gA[k][1] = add2(gA[k][1], tA[k][1]);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < TT * 2 * NP; i += T::EL_THREADS) {
-            const int row = i / (2 * NP), k = i % (2 * NP);
-            float s = sh.bc(row, 0)[k];
+        load(tile, ru, rd, rz, rg);
+        float *to = p.bc + (t0 + brow) * bstep + (w.b * p.grid.blocks + w.blk) * (2 * NP) + bk;
+#pragma unroll
+        for (int i = 0; i < BN; ++i, to += BR * bstep) {
+            const int row = brow + i * BR;
+            if (row >= rows)
+                break;
+            float s = sh.bc(row, 0)[bk];
 #pragma unroll
             for (int q = 1; q < T::WARPS; ++q)
-                s += sh.bc(row, q)[k];
-            if (row < rows)
-                p.bc[(((t0 + row) * p.B + w.b) * p.grid.blocks + w.blk) * (2 * NP) + k] = s;
+                s += sh.bc(row, q)[bk];
+            *to = s;
         }
         int64_t o = ((t0 + pr) * p.B + w.b) * p.H + ch;
-        load(tile, ru, rd, rz, rg);
 #pragma unroll
         for (int r = 0; r < RP; ++r, o += os) {
             const int row = pr + r * RG;
@@ -334,33 +342,34 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
     }
 }
 
-// grad_B and grad_C: the blocks of a group added up, one value per thread.
+// What is left to add up, in one launch. The first bc_blocks blocks: grad_B and
+// grad_C, the blocks of a group, one value per thread. The others: grad_A,
+// grad_D and grad_delta_bias, the (chunk, sequence) parts of every column, 8
+// strided runs of parts and then the runs in order.
 template <int DT>
-__global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_bc(const ScanParams p, int NP, uint16_t *gB, uint16_t *gC)
+__global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_sums(const ScanParams p, int NP, unsigned bc_blocks, uint16_t *gB,
+                                                              uint16_t *gC, float *gA, float *gD, float *gbias)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int k = (int)(i % (2 * NP)), n = k % NP;
-    const int64_t q = i / (2 * NP), row = q / p.G, g = q - row * p.G;   // row = t B + b
-    if (row >= p.S * p.B || n >= p.N)
-        return;
-    const int64_t t = row / p.B, b = row - t * p.B;
-    float s = 0.f;
-    if (t < clamped_length(p.lengths, b, p.S)) {
-        const float *src = p.bc + (row * p.grid.blocks + g * p.grid.blocks_per_group) * (2 * NP) + k;
+    if (blockIdx.x < bc_blocks) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const int k = (int)(i % (2 * NP)), n = k % NP;
+        const int64_t q = i / (2 * NP), row = q / p.G, g = q - row * p.G;   // row = t B + b
+        if (row >= p.S * p.B || n >= p.N)
+            return;
+        const int64_t t = row / p.B, b = row - t * p.B;
+        float s = 0.f;
+        if (t < clamped_length(p.lengths, b, p.S)) {
+            const float *src = p.bc + (row * p.grid.blocks + g * p.grid.blocks_per_group) * (2 * NP) + k;
 #pragma unroll 8
-        for (int m = 0; m < p.grid.blocks_per_group; ++m)
-            s += src[(int64_t)m * 2 * NP];
+            for (int m = 0; m < p.grid.blocks_per_group; ++m)
+                s += src[(int64_t)m * 2 * NP];
+        }
+        (k < NP ? gB : gC)[q * p.N + n] = (uint16_t)pack2<DT>(make_float2(s, 0.f));
+        return;
     }
-    (k < NP ? gB : gC)[q * p.N + n] = (uint16_t)pack2<DT>(make_float2(s, 0.f));
-}
-
-// grad_A, grad_D and grad_delta_bias: the (chunk, sequence) parts of every
-// column added up, 8 strided runs of parts and then the runs in order.
-__global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_sum(const ScanParams p, int NP, float *gA, float *gD, float *gbias)
-{
     __shared__ float red[8][32];
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + lane, parts = p.chunks * p.B, acols = p.H * NP, cols = acols + 2 * p.H;
+    const int64_t i = (int64_t)(blockIdx.x - bc_blocks) * 32 + lane, parts = p.chunks * p.B, acols = p.H * NP, cols = acols + 2 * p.H;
     float s = 0.f;
     if (i < cols) {
         const float *src = i < acols ? p.ga + i : p.gd + (i - acols);
@@ -424,14 +433,14 @@ int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1
     const int32_t st = a.fwd.dtype == 0 ? run_nl<0>(p, pl.nl, s) : run_nl<1>(p, pl.nl, s);
     if (st != kOk)
         return st;
-    const int64_t values = p.S * p.B * p.G * 2 * pl.np;
-    const unsigned grid = (unsigned)((values + 255) / 256);
+    const int64_t values = p.S * p.B * p.G * 2 * pl.np, cols = p.H * (pl.np + 2);
+    const unsigned bc_blocks = (unsigned)((values + 255) / 256), grid = bc_blocks + (unsigned)((cols + 31) / 32);
     if (a.fwd.dtype == 0)
-        mcc1d_ssm_scan_bwd_bc<0><<<grid, 256, 0, s>>>(p, pl.np, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C);
+        mcc1d_ssm_scan_bwd_sums<0><<<grid, 256, 0, s>>>(p, pl.np, bc_blocks, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C,
+                                                       a.grad_A, a.grad_D, a.grad_delta_bias);
     else
-        mcc1d_ssm_scan_bwd_bc<1><<<grid, 256, 0, s>>>(p, pl.np, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C);
-    const int64_t cols = p.H * (pl.np + 2);
-    mcc1d_ssm_scan_bwd_sum<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(p, pl.np, a.grad_A, a.grad_D, a.grad_delta_bias);
+        mcc1d_ssm_scan_bwd_sums<1><<<grid, 256, 0, s>>>(p, pl.np, bc_blocks, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C,
+                                                       a.grad_A, a.grad_D, a.grad_delta_bias);
     return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
