@@ -32,8 +32,11 @@ template <int NL>
 struct BwdShared {
     using T = BwdMainTile<NL>;
     static constexpr int TT = T::TT;
-    float4 sq[TT][T::CB];                         // dt, dt u, dy, dt; the first three then sum A log2e q, sum g B, y
+    // dt, dt u, dy, dt; the first three then sum A log2e q, sum g B, y. A lane's channels lie in planes of their
+    // own, so that the lanes of a warp read neighbouring 16 bytes.
+    float4 sq[TT][T::K][T::CB / T::K];
     float4 hs[TT / kSub][T::K][T::EL_THREADS];       // states before each run of kSub rows
+    static_assert(T::K == 2, "a thread's pair of channels is a lane's");
     float sB[TT][T::NP], sC[TT][T::NP];
     // A warp's grad_B and grad_C of row s + i take the place of its own hs[s / kSub][i], which it has read by then.
     static_assert(kSub <= T::K && 2 * T::NP <= 4 * 32, "a row of sums fits a warp's states of one channel");
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
     const ScanWhere w = scan_where<T>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = T::state_lane(lane), n0 = 4 * j, ci = T::channel_lane(lane);
-    const int cl = (warp * CL + ci) * K;
+    const int cw = warp * CL + ci, cl = cw * K;
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
     const int pc = 2 * (threadIdx.x % T::CP), pr = threadIdx.x / T::CP;
     const bool on0 = pc < w.nc, on1 = pc + 1 < w.nc;
@@ -145,8 +148,8 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                 g = mul2(g, mul2(zv, sigmoid2(zv)));
             }
             const float2 du = mul2(dt, unpack2<DT>(ru[r]));
-            sh.sq[row][pc] = make_float4(dt.x, du.x, g.x, dt.x);
-            sh.sq[row][pc + 1] = make_float4(dt.y, du.y, g.y, dt.y);
+            sh.sq[row][0][pc / 2] = make_float4(dt.x, du.x, g.x, dt.x);
+            sh.sq[row][1][pc / 2] = make_float4(dt.y, du.y, g.y, dt.y);
         }
         // the state at the tile's start: from the chunk's zero start, and what entered the chunk
         float2 h[K][2];
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[s + i][n0]);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl + k]);
+                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][k][cw]);
                     const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
                     h[k][0] = fma2(decay2(dt2, A2[k][0]), h[k][0], mul2(du2, make_float2(bv.x, bv.y)));
                     h[k][1] = fma2(decay2(dt2, A2[k][1]), h[k][1], mul2(du2, make_float2(bv.z, bv.w)));
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                 const float4 cv = *reinterpret_cast<const float4 *>(&sh.sC[s + i][n0]);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][cl + k]);
+                    const float2 dd = *reinterpret_cast<const float2 *>(&sh.sq[s + i][k][cw]);
                     const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y);
                     aa[i][k][0] = decay2(dt2, A2[k][0]);
                     aa[i][k][1] = decay2(dt2, A2[k][1]);
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                 float2 v0, v1, c0, c1;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const float4 dd = sh.sq[s + i][cl + k];
+                    const float4 dd = sh.sq[s + i][k][cw];
                     const float2 dt2 = make_float2(dd.x, dd.x), du2 = make_float2(dd.y, dd.y), dy2 = make_float2(dd.z, dd.z);
                     const float2 g0 = fma2(dy2, make_float2(cv.x, cv.y), X[k][0]);
                     const float2 g1 = fma2(dy2, make_float2(cv.z, cv.w), X[k][1]);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
 #pragma unroll
                 for (int m = 0; m < OWN; ++m) {
                     const int q = j * OWN + m;          // (step, channel)
-                    float *o = reinterpret_cast<float *>(&sh.sq[s + q / K][cl + q % K]);
+                    float *o = reinterpret_cast<float *>(&sh.sq[s + q / K][q % K][cw]);
                     *reinterpret_cast<float2 *>(o) = make_float2(sa[m], sb[m]);
                     o[2] = ys[m];
                 }
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
         for (int r = 0; r < RP; ++r, o += os) {
             const int row = pr + r * RG;
             const bool in = row < rows;
-            const float4 s0 = sh.sq[row][pc], s1 = sh.sq[row][pc + 1];
+            const float4 s0 = sh.sq[row][0][pc / 2], s1 = sh.sq[row][1][pc / 2];
             const float2 uv = unpack2<DT>(ru[r]), raw = add2(unpack2<DT>(rd[r]), bias), sb = make_float2(s0.y, s1.y);
             float2 dy = unpack2<DT>(rg[r]);
             if (p.z) {
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
             *reinterpret_cast<float4 *>(p.ga + (w.chunk * p.B * p.H + hc[k]) * NP + n0) =
                 make_float4(gA[k][0].x, gA[k][0].y, gA[k][1].x, gA[k][1].y);
     // grad_D and grad_delta_bias over the threads that share channels
-    float4 *red = &sh.sq[0][0];
+    float4 *red = &sh.sq[0][0][0];
     __syncthreads();
     red[pr * T::CP + pc / 2] = make_float4(gD.x, gbias.x, gD.y, gbias.y);
     __syncthreads();
