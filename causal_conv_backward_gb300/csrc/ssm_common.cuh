@@ -5,8 +5,22 @@
 #include <type_traits>
 
 #include "device_common.cuh"
+#include "plan.h"
 
 namespace mcc1d {
+
+// Launches a kernel and says whether this launch failed (an error that an
+// earlier call of the program left behind is not this call's).
+template <class... P, class... A>
+int32_t launch(void (*kernel)(P...), dim3 grid, int threads, int shared_bytes, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = (size_t)shared_bytes;
+    c.stream = stream;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...) == cudaSuccess ? kOk : kErrCuda;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -21,6 +35,16 @@ struct Vec {
 // Channels per thread of the short convolution over prompts: a tap costs V
 // registers of weights and of each window, so wide kernels take fewer.
 constexpr int conv_vec(int W) { return W <= 4 ? 4 : 2; }
+
+// As many of them as the addresses (their bits or'd) and the row steps in
+// elements (or'd) allow: 4, 2 or 1.
+inline int conv_vec_for(int W, uintptr_t addresses, int64_t steps)
+{
+    int V = conv_vec(W);
+    while (V > 1 && ((addresses & (uintptr_t)(2 * V - 1)) != 0 || (steps & (V - 1)) != 0))
+        V /= 2;
+    return V;
+}
 
 template <int V>
 __device__ __forceinline__ Vec<V> vzero()

@@ -6,8 +6,13 @@
 // One thread owns V adjacent channels of one sequence and walks L rows with
 // the last W-1 rows in registers, so x is read once but for W-1 rows per L.
 // The call moves 4 bytes per element against 2 W + 5 flops and two special
-// functions: it is bound by memory, and the rows of a batch are loaded
-// kRows ahead of their use to keep enough bytes in flight.
+// functions and is bound by memory; the rows travel through a ring in shared
+// memory (RowRing), three batches ahead of their use, since registers do not
+// hold the bytes that have to be in flight. Measured, bf16, W = 4: 162 us on
+// 8192 x 8 x 4096 (0.97 of the measured copy bandwidth), 46 us on
+// 4096 x 8 x 2048 (0.85; 57 with eight rows in registers); wider kernels run
+// into their arithmetic (W = 8: 67 us), rows that are not 8-byte aligned move
+// two bytes per lane (100 us).
 #include "plan.h"
 #include "ssm.h"
 #include "ssm_common.cuh"
@@ -198,30 +203,28 @@ template <int DT>
 int32_t run_fwd(const ConvParams &p, int V, int W, dim3 grid, cudaStream_t s)
 {
     switch (W) {
-#define MCC1D_CASE(w)                                                         \
-    case w:                                                                   \
-        if (V == 1)                                                           \
-            mcc1d_ssm_conv_fwd<DT, 1, w><<<grid, kThreads, 0, s>>>(p);        \
-        else                                                                  \
-            mcc1d_ssm_conv_fwd<DT, conv_vec(w), w><<<grid, kThreads, 0, s>>>(p); \
-        break;
+#define MCC1D_CASE(w)                                                            \
+    case w:                                                                      \
+        return V == 1 ? launch(mcc1d_ssm_conv_fwd<DT, 1, w>, grid, kThreads, 0, s, p)   \
+               : V == 2 ? launch(mcc1d_ssm_conv_fwd<DT, 2, w>, grid, kThreads, 0, s, p) \
+                        : launch(mcc1d_ssm_conv_fwd<DT, conv_vec(w), w>, grid, kThreads, 0, s, p);
         MCC1D_CASE(1) MCC1D_CASE(2) MCC1D_CASE(3) MCC1D_CASE(4)
         MCC1D_CASE(5) MCC1D_CASE(6) MCC1D_CASE(7) MCC1D_CASE(8)
 #undef MCC1D_CASE
     }
-    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+    return kErrShape;
 }
 
 template <int DT, int V>
 int32_t run_step(const StepParams &p, int W, dim3 grid, cudaStream_t s)
 {
     switch (W) {
-#define MCC1D_CASE(w) case w: mcc1d_ssm_conv_step<DT, V, w><<<grid, kThreads, 0, s>>>(p); break;
+#define MCC1D_CASE(w) case w: return launch(mcc1d_ssm_conv_step<DT, V, w>, grid, kThreads, 0, s, p);
         MCC1D_CASE(1) MCC1D_CASE(2) MCC1D_CASE(3) MCC1D_CASE(4)
         MCC1D_CASE(5) MCC1D_CASE(6) MCC1D_CASE(7) MCC1D_CASE(8)
 #undef MCC1D_CASE
     }
-    return cudaPeekAtLastError() == cudaSuccess ? kOk : kErrCuda;
+    return kErrShape;
 }
 
 }  // namespace
@@ -230,11 +233,10 @@ namespace {
 
 int fwd_vec(const mcc1d_short_conv_args &a)
 {
-    const int V = conv_vec((int)a.W);
     const uintptr_t any = (uintptr_t)a.x | (uintptr_t)a.weight | (uintptr_t)a.bias | (uintptr_t)a.state |
                           (uintptr_t)a.y | (uintptr_t)a.final_state;
     const int64_t steps = a.H | a.x_strides[0] | a.x_strides[1];
-    return (any & (uintptr_t)(2 * V - 1)) == 0 && (steps & (V - 1)) == 0 ? V : 1;
+    return conv_vec_for((int)a.W, any, steps);
 }
 
 }  // namespace
@@ -258,7 +260,8 @@ int32_t launch_short_conv(const mcc1d_short_conv_args &a, cudaStream_t stream)
     const int V = fwd_vec(a);
     p.vecs = a.H / V;
     const int64_t lanes = a.B * p.vecs, blocks = (lanes + kThreads - 1) / kThreads;
-    // long runs of rows re-read fewer window rows; short ones give more threads
+    // Long runs of rows re-read fewer window rows; short ones give more threads.
+    // 4096 x 8 x 2048: W = 4 48 us with runs of 32 rows, 46 with 128; W = 8 118 and 76.
     int64_t L = 128;
     while (L > 8 && blocks * ((a.S + L - 1) / L) < 152 * 8)
         L /= 2;

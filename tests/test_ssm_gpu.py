@@ -455,3 +455,26 @@ def test_refusals():
     with pytest.raises(ValueError):
         m.selective_scan_step(t["u"][0], t["delta"][0], t["state"][:1], t["A"], t["B"][0], t["C"][0])
     assert ctypes.sizeof(m.ScanArgs) > 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens agree with the same tokens run
+    alone from the carried window and state."""
+    S, H, N, last = 540_000, 4096, 4, 50
+    assert S * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(S, 1, H, generator=g, device="cuda", dtype=BF16)
+    w, b = rand(4, H, seed=2), rand(H, seed=3)
+    y = torch.empty(S, 1, H, device="cuda", dtype=BF16)     # too large for guards to be worth it
+    m.short_conv(x, w, b, y=y)
+    _, window = m.short_conv(x[:S - last], w, b, return_state=True, y=torch.empty_like(y[:S - last]))
+    assert torch.equal(window, x[S - last - 3:S - last].transpose(0, 1))
+    assert torch.equal(m.short_conv(x[S - last:], w, b, state=window), y[S - last:])
+    delta, A, Bm = x.sub_(1.0), -torch.exp(rand(H, N, dtype=F32)), rand(last, 1, 1, N).repeat(S // last, 1, 1, 1)
+    _, state = m.selective_scan(y[:S - last], delta[:S - last], A, Bm[:S - last], Bm[:S - last], delta_softplus=True,
+                                return_state=True, y=torch.empty_like(y[:S - last]))
+    tail = slice(S - last, S)
+    want, f = m.selective_scan(y[tail], delta[tail], A, Bm[tail], Bm[tail], delta_softplus=True, state=state, return_state=True)
+    got, f2 = m.selective_scan(y, delta, A, Bm, Bm, delta_softplus=True, return_state=True, y=torch.empty_like(y))
+    ref.check(got[tail], want.double(), N + 64, "y")
+    ref.check(f2, f.double(), N + 64, "state")
