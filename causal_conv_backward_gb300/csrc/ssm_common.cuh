@@ -11,16 +11,33 @@ namespace mcc1d {
 
 // Launches a kernel and says whether this launch failed (an error that an
 // earlier call of the program left behind is not this call's).
+// `after`: as a programmatic dependent of the call's kernel before it, whose
+// results it waits for itself (previous_done) once it is set up.
 template <class... P, class... A>
-int32_t launch(void (*kernel)(P...), dim3 grid, int threads, int shared_bytes, cudaStream_t stream, A &&...args)
+int32_t launch_as(bool after, void (*kernel)(P...), dim3 grid, int threads, int shared_bytes, cudaStream_t stream, A &&...args)
 {
     cudaLaunchConfig_t c = {};
     c.gridDim = grid;
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = (size_t)shared_bytes;
     c.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = after ? 1 : 0;
     return cudaLaunchKernelEx(&c, kernel, P(args)...) == cudaSuccess ? kOk : kErrCuda;
 }
+template <class... P, class... A>
+int32_t launch(void (*kernel)(P...), dim3 grid, int threads, int shared_bytes, cudaStream_t stream, A &&...args)
+{
+    return launch_as(false, kernel, grid, threads, shared_bytes, stream, args...);
+}
+
+// The kernel this one depends on has finished (at once where it was launched
+// plainly); the kernel that depends on this one may be set up.
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 

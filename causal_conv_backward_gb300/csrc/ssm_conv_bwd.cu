@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
         float2 red[kWarps][W + 1][32][P];      // after the rows
     };
     __shared__ __align__(16) Shared shared;
+    next_may_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t vec = (int64_t)blockIdx.x * 32 + lane;
     const int64_t part = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(256) mcc1d_ssm_conv_bwd_sum(const float *parti
                                                              int64_t wcols, uint16_t *gw, uint16_t *gbias)
 {
     __shared__ float red[8][32];
+    previous_done();
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
@@ -335,7 +337,7 @@ int32_t launch_short_conv_bwd(const mcc1d_short_conv_bwd_args &a, void *workspac
     const int64_t cols = (a.W + 1) * a.H;
     const unsigned blocks = (unsigned)((cols + 31) / 32);
     const auto sum = a.dtype == 0 ? mcc1d_ssm_conv_bwd_sum<0> : mcc1d_ssm_conv_bwd_sum<1>;
-    return launch(sum, blocks, 256, 0, stream, p.partial, plan.parts, cols, a.W * a.H, (uint16_t *)a.grad_weight,
+    return launch_as(true, sum, blocks, 256, 0, stream, p.partial, plan.parts, cols, a.W * a.H, (uint16_t *)a.grad_weight,
                   (uint16_t *)a.grad_bias);
 }
 

@@ -60,6 +60,11 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
+    // outputs after a join read its states; the passes before a join let it be set up
+    if (kY)
+        previous_done();
+    else
+        next_may_start();
     const ScanWhere w = scan_where<T>(p);
     const int64_t te = clamped_length(p.lengths, w.b, p.S);
     const int64_t tile0 = w.chunk * p.tiles_per_chunk;
@@ -322,6 +327,8 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
     const int n0 = 4 * (int)(i - row * NL), NP = 4 * NL;
     const float4 A = load_states(p.A + row % p.H * p.N, n0, p.N, p.vecA);
     const float a[4] = {A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e};
+    next_may_start();
+    previous_done();
     const bool back = blockIdx.y == 1;
     float *const at = back ? p.r : p.e;
     const float *const first = back ? p.gfs : p.h0;
@@ -475,7 +482,7 @@ int32_t launch_tile(const ScanParams &p, cudaStream_t s)
     static SharedReady ready;
     if (!ready.set((const void *)mcc1d_ssm_scan<T, DT, MODE, PAIRS>, bytes))
         return kErrCuda;
-    return launch(mcc1d_ssm_scan<T, DT, MODE, PAIRS>, scan_launch_grid(p), T::THREADS, bytes, s, p);
+    return launch_as(MODE == kOutputs && p.chunks > 1, mcc1d_ssm_scan<T, DT, MODE, PAIRS>, scan_launch_grid(p), T::THREADS, bytes, s, p);
 }
 
 template <class T, int MODE>
@@ -683,7 +690,7 @@ static ScanParams scan_params(const mcc1d_scan_args &a, const ScanPlan &pl, uint
 static int32_t join(const ScanParams &p, int nl, bool grad, cudaStream_t s)
 {
     const dim3 grid((unsigned)((p.B * p.H * nl + 127) / 128), grad ? 2 : 1);
-    return launch(mcc1d_ssm_scan_join, grid, 128, 0, s, p, nl);
+    return launch_as(true, mcc1d_ssm_scan_join, grid, 128, 0, s, p, nl);
 }
 
 int32_t launch_scan(const mcc1d_scan_args &a, const ScanPlan &pl, void *workspace, cudaStream_t stream)

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh &sh = *reinterpret_cast<Sh *>(raw_shared);
 
+    next_may_start();
+    previous_done();
     const ScanWhere w = scan_where<T>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = T::state_lane(lane), n0 = 4 * j, ci = T::channel_lane(lane);
@@ -362,6 +364,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) mcc1d_ssm_scan_bwd_sums(const ScanParams p, int NP, unsigned bc_blocks, uint16_t *gB,
                                                               uint16_t *gC, float *gA, float *gD, float *gbias)
 {
+    previous_done();
     if (blockIdx.x < bc_blocks) {
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
         const int k = (int)(i % (2 * NP)), n = k % NP;
@@ -416,7 +419,7 @@ int32_t run_pairs(const ScanParams &p, cudaStream_t s)
     static SharedReady ready;
     if (!ready.set((const void *)mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, bytes))
         return kErrCuda;
-    return launch(mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, scan_launch_grid(p), BwdMainTile<NL>::EL_THREADS, bytes, s, p);
+    return launch_as(true, mcc1d_ssm_scan_bwd<DT, NL, PAIRS>, scan_launch_grid(p), BwdMainTile<NL>::EL_THREADS, bytes, s, p);
 }
 
 template <int DT, int NL>
@@ -447,7 +450,7 @@ int32_t launch_scan_bwd_main(const ScanParams &p, const ScanPlan &pl, const mcc1
     const int64_t values = p.S * p.B * p.G * 2 * pl.np, cols = p.H * (pl.np + 2);
     const unsigned bc_blocks = (unsigned)((values + 255) / 256), grid = bc_blocks + (unsigned)((cols + 31) / 32);
     const auto sums = a.fwd.dtype == 0 ? mcc1d_ssm_scan_bwd_sums<0> : mcc1d_ssm_scan_bwd_sums<1>;
-    return launch(sums, grid, 256, 0, s, p, pl.np, bc_blocks, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C, a.grad_A, a.grad_D,
+    return launch_as(true, sums, grid, 256, 0, s, p, pl.np, bc_blocks, (uint16_t *)a.grad_B, (uint16_t *)a.grad_C, a.grad_A, a.grad_D,
                   a.grad_delta_bias);
 }
 
