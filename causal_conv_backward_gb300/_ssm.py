@@ -73,11 +73,12 @@ _pack_scan, _pack_scan_bwd, _pack_scan_step = (_packer(c) for c in (ScanArgs, Sc
 _lib = None
 _torch = None
 _raw_stream = None
+_current_device = None
 
 
 def _load():
     """The library with this module's prototypes, and torch."""
-    global _lib, _torch, _raw_stream
+    global _lib, _torch, _raw_stream, _current_device
     if _lib is None:
         import torch
         lib = _load_lib()
@@ -92,6 +93,7 @@ def _load():
         # the current stream's handle without a Stream object around it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch, _lib = torch, lib
     return _lib
 
@@ -144,7 +146,10 @@ def _first(t, name, dims):
     shape = t.shape
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have adjacent elements along its last axis (stride 1, not {t.stride(-1)})")
-    return shape, _code(t, name), t.get_device()
+    index = t.get_device()
+    if index != _current_device():
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
+    return shape, _code(t, name), index
 
 
 def _flag(activation):

@@ -237,14 +237,8 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
             float2 a[U][K][2], b[U][K][2];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                float2 dd[K];
-                if (K == 2) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&sh.sd[buf][tb + i][cl]);
-                    dd[0] = make_float2(v.x, v.y);
-                    dd[K - 1] = make_float2(v.z, v.w);
-                } else {
-                    dd[0] = sh.sd[buf][tb + i][cl];
-                }
+                const float4 both = *reinterpret_cast<const float4 *>(&sh.sd[buf][tb + i][cl]);
+                const float2 dd[K] = {make_float2(both.x, both.y), make_float2(both.z, both.w)};
                 const float4 bv = *reinterpret_cast<const float4 *>(&sh.sB[buf][tb + i][n0]);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
@@ -281,12 +275,8 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
                         R[k][1] = fma2(q[k][1], mul2(g2, c1), R[k][1]);
                     }
                 }
-                if (kY) {
-                    if (K == 2)
-                        *reinterpret_cast<float2 *>(&sh.sy[buf][tb + i][j][cl]) = make_float2(part[0], part[K - 1]);
-                    else
-                        sh.sy[buf][tb + i][j][cl] = part[0];
-                }
+                if (kY)
+                    *reinterpret_cast<float2 *>(&sh.sy[buf][tb + i][j][cl]) = make_float2(part[0], part[1]);
             }
         }
         block_barrier(T::THREADS);

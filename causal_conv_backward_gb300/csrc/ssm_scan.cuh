@@ -2,8 +2,8 @@
 // their parameters, the tile loads and the sums over a channel's lanes.
 //
 // Layout of a block: NW recurrence warps; a channel's N states sit on NL lanes,
-// four to a lane, and a lane holds them for K channels, so a warp owns 32 K/NL
-// channels and the block CB = 32 K NW/NL, of one group and one sequence. It
+// four to a lane, and a lane holds them for K = 2 channels, so a warp owns
+// 64/NL channels and the block CB = 64 NW/NL, of one group and one sequence. It
 // walks one time chunk in tiles of TT rows. EW further warps do what is needed
 // once per (row, channel): the loads, dt and the gate for the tile after the
 // one the recurrence is in, and the outputs of the tile before it. A thread of
@@ -19,9 +19,9 @@
 
 namespace mcc1d {
 
-template <int NL_, int NW, int EW, int K_, int TT_>
+template <int NL_, int NW, int EW, int TT_>
 struct ScanTile {
-    static constexpr int NL = NL_, K = K_, TT = TT_, WARPS = NW;
+    static constexpr int NL = NL_, K = 2, TT = TT_, WARPS = NW;
     static constexpr int THREADS = 32 * (NW + EW), EL_THREADS = 32 * EW;
     static constexpr int NP = 4 * NL;              // states, padded
     static constexpr int CL = 32 / NL;             // lanes of one state
@@ -44,22 +44,22 @@ struct ScanTile {
     __device__ __forceinline__ static int channel_lane(int lane) { return NL == 1 ? lane : (lane >> 1) % CL; }
 };
 
-// Tiles of the forward. Two channels per lane: B and C are read from shared
-// memory once for both, without which its bandwidth is the first limit (1024
-// tokens x 8 sequences x 2048 channels: 107 us, one channel per lane 124 us).
+// Tiles of the forward. B and C are read from shared memory once for a lane's
+// two channels, without which its bandwidth is the first limit (1024 tokens x 8
+// sequences x 2048 channels: 107 us, with one channel per lane 124 us).
 // At N = 16 the element warps are what a block alone on its SM waits for (222 us
 // with or without the recurrence on 4096 x 1 x 2048), so they are four.
 template <int NL>
-using OutTile = ScanTile<NL, 2, (NL <= 4 ? 4 : NL == 8 ? 2 : 1), 2, (NL == 1 ? 8 : 16)>;
+using OutTile = ScanTile<NL, 2, (NL <= 4 ? 4 : NL == 8 ? 2 : 1), (NL == 1 ? 8 : 16)>;
 // Tiles of the backward's first pass, with the rows and channels of its second.
 template <int NL>
-using BwdTile = ScanTile<NL, 4, (NL < 8 ? 4 : NL == 8 ? 2 : 1), 2, (NL < 4 ? 4 * NL : 16)>;
+using BwdTile = ScanTile<NL, 4, (NL < 8 ? 4 : NL == 8 ? 2 : 1), (NL < 4 ? 4 * NL : 16)>;
 // Tiles of the backward's second pass: the same rows and channels, and the
 // recurrence warps do the elements' part too, so that every warp has the
 // registers of a recurrence warp. Two channels per lane, so that grad_B's and
 // grad_C's sums over channels start inside the lane.
 template <int NL>
-using BwdMainTile = ScanTile<NL, 4, 4, 2, BwdTile<NL>::TT>;
+using BwdMainTile = ScanTile<NL, 4, 4, BwdTile<NL>::TT>;
 
 struct ScanParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm, *gy;

@@ -45,7 +45,6 @@ struct BwdShared {
     // own, so that the lanes of a warp read neighbouring 16 bytes.
     float4 sq[TT][T::K][T::CB / T::K];
     float4 hs[TT / kSub][T::K][T::EL_THREADS];       // states before each run of kSub rows
-    static_assert(T::K == 2, "a thread's pair of channels is a lane's");
     float sB[TT][T::NP], sC[TT][T::NP];
     // A warp's grad_B and grad_C of row s + i take the place of its own hs[s / kSub][i], which it has read by then.
     static_assert(kSub <= T::K && 2 * T::NP <= 4 * 32, "a row of sums fits a warp's states of one channel");
