@@ -581,15 +581,17 @@ void cut(ScanPlan &p, int64_t rows, int64_t most, int64_t waves_above)
 ScanPlan scan_plan(const mcc1d_scan_args &a)
 {
     ScanPlan p = shape_plan(a);
-    // Cutting the time axis computes the states twice, so it has to bring more
-    // than twice the warps: at 256 blocks (2048 tokens x 4 x 2048) one pass takes
-    // 174 us and cut in chunks 187, at 128 (4096 x 2 x 2048) 319 against 186.
+    // Cutting the time axis computes the states twice and costs two launches.
+    // One pass against chunks, us: 256 blocks (2048 x 8 x 1024) 146 and 163, 192
+    // (2048 x 6 x 1024) 140 and 125, 128 (2048 x 4 x 1024) 117 and 95; short
+    // sequences: 8 tiles (128 x 4 x 1024) 12.4 and 14.5, 16 tiles (256 x 2 x 1024)
+    // 18.8 and 14.6.
     int cb;
     tile_shape<OutTile>(p.nl, cb, p.tt);
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.grid = scan_grid(a.H, a.G, cb);
     const int64_t rows = p.grid.blocks * a.B;
-    cut(p, rows, rows >= 190 ? 1 : p.tiles / 4, 0);   // chunks of fewer than 4 tiles cost more launches than they save
+    cut(p, rows, rows >= 220 || p.tiles < 12 ? 1 : p.tiles / 2, 0);
     p.most_blocks = rows * p.chunks;
     uint64_t off = 0;
     const uint64_t ch = (uint64_t)(a.B * a.H);
