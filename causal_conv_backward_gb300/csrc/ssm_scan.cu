@@ -355,8 +355,9 @@ constexpr int kStepThreads = 128;
 // One token: a row of states in, moved on by one step, and out; the states'
 // 8 N bytes per channel are what moves. Four states to a lane as above, so that
 // neighbouring lanes move neighbouring 16 bytes. 256 rows of 4096 channels, N =
-// 16: 34 us, 0.62 of the measured copy bandwidth (56 us with one row per
-// thread, whose dt, gate and addresses all lanes of a channel worked out).
+// 16: 27 us, 0.77 of the measured copy bandwidth (56 us with one row per
+// thread, whose dt, gate and addresses all lanes of a channel worked out, 34
+// with branches around the loads).
 struct ScanStepParams {
     const uint16_t *u, *delta, *z, *Bm, *Cm;
     const float *A, *D, *dbias;
@@ -365,7 +366,7 @@ struct ScanStepParams {
     uint16_t *y;
     uint32_t ub, db, zb, Bb, Bg, Cb, Cg;   // strides below 2^31: products of 32 bits by 32
     int64_t rows;
-    int32_t B, H, N, Hg, softplus, vecA, vecState, vecB;   // vecB: rows of B and C start on 8 bytes
+    int32_t B, H, N, Hg, softplus;
 };
 
 template <int DT>
@@ -399,11 +400,16 @@ __device__ __forceinline__ void load_four(const uint16_t *row, int n0, int N, bo
 template <int NL>
 constexpr int kStepRows = NL < 4 ? NL : 4;
 
-template <int DT, int NL>
+// VEC: rows of the cache, A, B and C move four states at a time. Lanes past N
+// and rows that are not there read where others do, write nothing and add
+// nothing: loads without branches around them.
+template <int DT, int NL, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanStepParams p)
 {
     constexpr int R = kStepRows<NL>;
-    const int j = threadIdx.x % NL, n0 = 4 * j, lane = threadIdx.x & 31;
+    const int j = threadIdx.x % NL, lane = threadIdx.x & 31;
+    const bool states = 4 * j < p.N;
+    const int n0 = states ? 4 * j : 0;
     const int c = (int)(blockIdx.x * (kStepThreads / NL)) + (int)threadIdx.x / NL;
     const bool live = c < p.H;
     const int ch = live ? c : 0;
@@ -412,19 +418,20 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
     const uint16_t *Bg = p.Bm + (uint64_t)g * p.Bg, *Cg = p.Cm + (uint64_t)g * p.Cg;
 
     float *at[R];
+    bool on[R];
     float4 h[R];
     float2 B[R][2], C[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t b = b0 + (r < rows ? r : 0);
         const int32_t slot = p.slots ? p.slots[b] : (int32_t)b;
-        const bool on = live && r < rows && slot >= 0 && slot < p.rows;
-        at[r] = on ? p.state + (uint64_t)(uint32_t)slot * row_size + in_row : nullptr;
-        h[r] = on ? load_states(at[r], n0, p.N, p.vecState) : make_float4(0.f, 0.f, 0.f, 0.f);
-        load_four<DT>(Bg + (uint64_t)b * p.Bb, n0, p.N, p.vecB, B[r]);
-        load_four<DT>(Cg + (uint64_t)b * p.Cb, n0, p.N, p.vecB, C[r]);
+        on[r] = r < rows && slot >= 0 && slot < p.rows;
+        at[r] = p.state + (uint64_t)(uint32_t)(on[r] ? slot : 0) * row_size + in_row;
+        h[r] = load_states(at[r], n0, p.N, VEC);
+        load_four<DT>(Bg + (uint64_t)b * p.Bb, n0, p.N, VEC, B[r]);
+        load_four<DT>(Cg + (uint64_t)b * p.Cb, n0, p.N, VEC, C[r]);
     }
-    const float4 A = load_states(p.A + in_row, n0, p.N, p.vecA);
+    const float4 A = load_states(p.A + in_row, n0, p.N, VEC);
     // this lane's own row
     const int own = j < R ? j : 0;
     const bool mine = live && j < R && own < rows;
@@ -437,30 +444,26 @@ __global__ void __launch_bounds__(kStepThreads) mcc1d_ssm_scan_step(const ScanSt
         dt = softplus(dt);
     const float dl = dt * kLog2e, du = dt * uv;
 
-    float part[R], y = 0.f;
+    float part[R];
+    bool there = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const float dlr = __shfl_sync(0xFFFFFFFFu, dl, r, NL), dur = __shfl_sync(0xFFFFFFFFu, du, r, NL);
         const float2 dl2 = make_float2(dlr, dlr), du2 = make_float2(dur, dur);
         const float2 o0 = fma2(decay2(dl2, make_float2(A.x, A.y)), make_float2(h[r].x, h[r].y), mul2(du2, B[r][0]));
         const float2 o1 = fma2(decay2(dl2, make_float2(A.z, A.w)), make_float2(h[r].z, h[r].w), mul2(du2, B[r][1]));
-        if (at[r])
-            store_states(at[r], n0, p.N, p.vecState, make_float4(o0.x, o0.y, o1.x, o1.y));
+        if (on[r] && live && states)
+            store_states(at[r], n0, p.N, VEC, make_float4(o0.x, o0.y, o1.x, o1.y));
         const float2 s = fma2(o0, C[r][0], mul2(o1, C[r][1]));
-        part[r] = at[r] ? s.x + s.y : 0.f;
+        part[r] = states ? s.x + s.y : 0.f;
+        there = r == own ? on[r] : there;
     }
     lanes_sum<R, NL, 1, 1>(part, lane);
-    bool there = false;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        there = r == own ? at[r] != nullptr : there;
-    if (there) {
-        y = fmaf(D, uv, part[0]);
-        if (p.z)
-            y *= zv * sigmoid(zv);
-    }
+    float y = fmaf(D, uv, part[0]);
+    if (p.z)
+        y *= zv * sigmoid(zv);
     if (mine)
-        p.y[(uint64_t)bm * p.H + ch] = (uint16_t)pack2<DT>(make_float2(y, 0.f));
+        p.y[(uint64_t)bm * p.H + ch] = there ? (uint16_t)pack2<DT>(make_float2(y, 0.f)) : (uint16_t)0;
 }
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -495,18 +498,17 @@ int32_t run_scan(const ScanParams &p, int dtype, int nl, cudaStream_t s)
     }
 }
 
-template <int DT>
+template <int DT, bool VEC>
 int32_t run_step(const ScanStepParams &p, int nl, cudaStream_t s)
 {
-    const int per = kStepThreads / nl;
-    const int rows = nl < 4 ? nl : 4;
+    const int per = kStepThreads / nl, rows = nl < 4 ? nl : 4;
     const dim3 grid((unsigned)((p.H + per - 1) / per), (unsigned)((p.B + rows - 1) / rows));
     switch (nl) {
-    case 1: return launch(mcc1d_ssm_scan_step<DT, 1>, grid, kStepThreads, 0, s, p);
-    case 2: return launch(mcc1d_ssm_scan_step<DT, 2>, grid, kStepThreads, 0, s, p);
-    case 4: return launch(mcc1d_ssm_scan_step<DT, 4>, grid, kStepThreads, 0, s, p);
-    case 8: return launch(mcc1d_ssm_scan_step<DT, 8>, grid, kStepThreads, 0, s, p);
-    default: return launch(mcc1d_ssm_scan_step<DT, 16>, grid, kStepThreads, 0, s, p);
+    case 1: return launch(mcc1d_ssm_scan_step<DT, 1, VEC>, grid, kStepThreads, 0, s, p);
+    case 2: return launch(mcc1d_ssm_scan_step<DT, 2, VEC>, grid, kStepThreads, 0, s, p);
+    case 4: return launch(mcc1d_ssm_scan_step<DT, 4, VEC>, grid, kStepThreads, 0, s, p);
+    case 8: return launch(mcc1d_ssm_scan_step<DT, 8, VEC>, grid, kStepThreads, 0, s, p);
+    default: return launch(mcc1d_ssm_scan_step<DT, 16, VEC>, grid, kStepThreads, 0, s, p);
     }
 }
 
@@ -748,13 +750,14 @@ int32_t launch_scan_step(const mcc1d_scan_step_args &a, cudaStream_t stream)
     p.N = (int32_t)a.N;
     p.Hg = (int32_t)(a.H / a.G);
     p.softplus = (a.flags & MCC1D_SOFTPLUS) != 0;
-    p.vecA = a.N % 4 == 0 && aligned(a.A, 16);
-    p.vecState = a.N % 4 == 0 && aligned(a.state, 16);
-    p.vecB = a.N % 4 == 0 && aligned(a.B_, 8) && aligned(a.C, 8) && ((p.Bb | p.Bg | p.Cb | p.Cg) & 3) == 0;
+    const bool vec = a.N % 4 == 0 && aligned(a.A, 16) && aligned(a.state, 16) && aligned(a.B_, 8) && aligned(a.C, 8) &&
+                     ((p.Bb | p.Bg | p.Cb | p.Cg) & 3) == 0;
     int nl = 1;
     while (4 * nl < a.N)
         nl *= 2;
-    return a.dtype == 0 ? run_step<0>(p, nl, stream) : run_step<1>(p, nl, stream);
+    if (a.dtype == 0)
+        return vec ? run_step<0, true>(p, nl, stream) : run_step<0, false>(p, nl, stream);
+    return vec ? run_step<1, true>(p, nl, stream) : run_step<1, false>(p, nl, stream);
 }
 
 }  // namespace mcc1d
