@@ -96,49 +96,66 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
         uint32_t ru[RP], rd[RP], rz[RP], rg[RP];
         BcTile<T, kC> bc;
         bc.start(p, p.Bm + w.b * p.Bb + w.g * p.Bg + tile0 * TT * p.Bs, p.Cm + w.b * p.Cb + w.g * p.Cg + tile0 * TT * p.Cs, id, 1);
+        // Branches that are the same for every row stand outside the loops over rows, whose bodies interleave.
         auto load = [&](int rows) {
+            bool ok[RP];
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-                const bool ok = pr + r * RG < rows;
-                ru[r] = load_pair<PAIRS>(u, ok && on0, ok && on1);
-                rd[r] = load_pair<PAIRS>(delta, ok && on0, ok && on1);
+                ok[r] = pr + r * RG < rows;
+                ru[r] = load_pair<PAIRS>(u, ok[r] && on0, ok[r] && on1);
+                rd[r] = load_pair<PAIRS>(delta, ok[r] && on0, ok[r] && on1);
+                rz[r] = 0u;
                 u += us;
                 delta += ds;
-                rz[r] = 0u;
-                if (kC && p.z) {
-                    rz[r] = load_pair<PAIRS>(z, ok && on0, ok && on1);
-                    z += zs;
-                }
                 if (kR) {
-                    rg[r] = load_pair<PAIRS>(gy, ok && on0, ok && on1);
+                    rg[r] = load_pair<PAIRS>(gy, ok[r] && on0, ok[r] && on1);
                     gy += gs;
                 }
+            }
+            if (kC && p.z) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r, z += zs)
+                    rz[r] = load_pair<PAIRS>(z, ok[r] && on0, ok[r] && on1);
             }
             bc.load(p, rows);
         };
         // what the recurrence needs of tile i, whose rows are in registers; then the next tile's are asked for
         auto before = [&](int i) {
             const int buf = i & 1, rows = rows_in(i);
+            float2 dt[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r)
+                dt[r] = add2(unpack2<DT>(rd[r]), bias);
+            if (p.softplus) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    dt[r] = softplus2(dt[r]);
+            }
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
                 const int row = pr + r * RG;
-                float2 dt = add2(unpack2<DT>(rd[r]), bias);
-                if (p.softplus)
-                    dt = softplus2(dt);
                 if (row >= rows)
-                    dt = make_float2(0.f, 0.f);
-                const float2 du = mul2(dt, unpack2<DT>(ru[r]));
-                *reinterpret_cast<float4 *>(&sh.sd[buf][row][pc]) = make_float4(dt.x, du.x, dt.y, du.y);
+                    dt[r] = make_float2(0.f, 0.f);
+                const float2 du = mul2(dt[r], unpack2<DT>(ru[r]));
+                *reinterpret_cast<float4 *>(&sh.sd[buf][row][pc]) = make_float4(dt[r].x, du.x, dt[r].y, du.y);
                 if (kY)
                     sh.raw[buf][r][id] = make_uint2(ru[r], rz[r]);
-                if (kR) {
-                    float2 g = unpack2<DT>(rg[r]);
-                    if (p.z) {
+            }
+            if (kR) {
+                float2 g[RP];
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    g[r] = unpack2<DT>(rg[r]);
+                if (p.z) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
                         const float2 zv = unpack2<DT>(rz[r]);
-                        g = mul2(g, mul2(zv, sigmoid2(zv)));
+                        g[r] = mul2(g[r], mul2(zv, sigmoid2(zv)));
                     }
-                    *reinterpret_cast<float2 *>(&sh.sg[buf][row][pc]) = g;
                 }
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    *reinterpret_cast<float2 *>(&sh.sg[buf][pr + r * RG][pc]) = g[r];
             }
             bc.template put<DT>(p, sh.sB[buf], sh.sC[buf]);
             if (i + 1 < n_tiles)
@@ -148,21 +165,30 @@ __global__ void __launch_bounds__(T::THREADS, MODE == kSummaryGrad ? 3 : 4) mcc1
         const int last_all = (int)(p.S - (live_end - 1) * TT < TT ? p.S - (live_end - 1) * TT : TT);
         auto after = [&](int i) {
             const int buf = i & 1, rows = rows_in(i), all = i < n_tiles - 1 ? TT : last_all;
+            float2 v[RP];
+            uint2 rv[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int row = pr + r * RG;
+                rv[r] = sh.raw[buf][r][id];
+                v[r] = *reinterpret_cast<const float2 *>(&sh.sy[buf][row][0][pc]);
+#pragma unroll
+                for (int k = 1; k < NL; ++k)
+                    v[r] = add2(v[r], *reinterpret_cast<const float2 *>(&sh.sy[buf][row][k][pc]));
+                v[r] = fma2(D, unpack2<DT>(rv[r].x), v[r]);
+            }
+            if (p.z) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    const float2 zv = unpack2<DT>(rv[r].y);
+                    v[r] = mul2(v[r], mul2(zv, sigmoid2(zv)));
+                }
+            }
 #pragma unroll
             for (int r = 0; r < RP; ++r, y += ys) {
                 const int row = pr + r * RG;
-                const uint2 rv = sh.raw[buf][r][id];
-                float2 v = *reinterpret_cast<const float2 *>(&sh.sy[buf][row][0][pc]);
-#pragma unroll
-                for (int k = 1; k < NL; ++k)
-                    v = add2(v, *reinterpret_cast<const float2 *>(&sh.sy[buf][row][k][pc]));
-                v = fma2(D, unpack2<DT>(rv.x), v);
-                if (p.z) {
-                    const float2 zv = unpack2<DT>(rv.y);
-                    v = mul2(v, mul2(zv, sigmoid2(zv)));
-                }
                 if (row < all)
-                    store_pair<PAIRS>(y, row < rows ? pack2<DT>(v) : 0u, on0, on1);
+                    store_pair<PAIRS>(y, row < rows ? pack2<DT>(v[r]) : 0u, on0, on1);
             }
         };
         if (n_tiles > 0) {

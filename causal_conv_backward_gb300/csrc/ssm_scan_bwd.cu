@@ -145,21 +145,35 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
         load(tile, ru, rd, rz, rg);
         bc.load(p, rows);
         bc.template put<DT>(p, sh.sB, sh.sC);
+        {
+            // branches that are the same for every row stand outside the loops over rows
+            float2 dt[RP], g[RP];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            const int row = pr + r * RG;
-            float2 dt = add2(unpack2<DT>(rd[r]), bias), g = unpack2<DT>(rg[r]);
-            if (p.softplus)
-                dt = softplus2(dt);
-            if (row >= rows)
-                dt = make_float2(0.f, 0.f);
-            if (p.z) {
-                const float2 zv = unpack2<DT>(rz[r]);
-                g = mul2(g, mul2(zv, sigmoid2(zv)));
+            for (int r = 0; r < RP; ++r) {
+                dt[r] = add2(unpack2<DT>(rd[r]), bias);
+                g[r] = unpack2<DT>(rg[r]);
             }
-            const float2 du = mul2(dt, unpack2<DT>(ru[r]));
-            sh.sq[row][0][pc / 2] = make_float4(dt.x, du.x, g.x, dt.x);
-            sh.sq[row][1][pc / 2] = make_float4(dt.y, du.y, g.y, dt.y);
+            if (p.softplus) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    dt[r] = softplus2(dt[r]);
+            }
+            if (p.z) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    const float2 zv = unpack2<DT>(rz[r]);
+                    g[r] = mul2(g[r], mul2(zv, sigmoid2(zv)));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int row = pr + r * RG;
+                if (row >= rows)
+                    dt[r] = make_float2(0.f, 0.f);
+                const float2 du = mul2(dt[r], unpack2<DT>(ru[r]));
+                sh.sq[row][0][pc / 2] = make_float4(dt[r].x, du.x, g[r].x, dt[r].x);
+                sh.sq[row][1][pc / 2] = make_float4(dt[r].y, du.y, g[r].y, dt[r].y);
+            }
         }
         // the state at the tile's start: from the chunk's zero start, and what entered the chunk
         float2 h[K][2];
