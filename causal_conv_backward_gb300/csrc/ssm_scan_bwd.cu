@@ -308,36 +308,53 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                 s += sh.bc(row, q)[bk];
             *to = s;
         }
-        int64_t o = ((t0 + pr) * p.B + w.b) * p.H + ch;
+        const int64_t o = ((t0 + pr) * p.B + w.b) * p.H + ch;
+        const float2 one = make_float2(1.f, 1.f);
+        float2 dy[RP], slope[RP];
 #pragma unroll
-        for (int r = 0; r < RP; ++r, o += os) {
+        for (int r = 0; r < RP; ++r) {
+            dy[r] = unpack2<DT>(rg[r]);
+            slope[r] = one;
+        }
+        if (p.z) {
+            uint32_t gz[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                const int row = pr + r * RG;
+                const float2 y = make_float2(sh.sq[row][0][pc / 2].z, sh.sq[row][1][pc / 2].z);
+                const float2 zv = unpack2<DT>(rz[r]), sz = sigmoid2(zv);
+                // d/dz [z sz] = sz (1 + z (1 - sz))
+                const float2 d = mul2(sz, fma2(zv, make_float2(1.f - sz.x, 1.f - sz.y), one));
+                gz[r] = pack2<DT>(mul2(mul2(dy[r], fma2(D, unpack2<DT>(ru[r]), y)), d));
+                dy[r] = mul2(dy[r], mul2(zv, sz));
+            }
+            if (p.gz) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    if (pr + r * RG < all)
+                        store_pair<PAIRS>(p.gz + o + r * os, pr + r * RG < rows ? gz[r] : 0u, on0, on1);
+            }
+        }
+        if (p.softplus) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r)
+                slope[r] = sigmoid2(add2(unpack2<DT>(rd[r]), bias));
+        }
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
             const int row = pr + r * RG;
-            const bool in = row < rows;
             const float4 s0 = sh.sq[row][0][pc / 2], s1 = sh.sq[row][1][pc / 2];
-            const float2 uv = unpack2<DT>(ru[r]), raw = add2(unpack2<DT>(rd[r]), bias), sb = make_float2(s0.y, s1.y);
-            float2 dy = unpack2<DT>(rg[r]);
-            if (p.z) {
-                const float2 zv = unpack2<DT>(rz[r]), sz = sigmoid2(zv), one = make_float2(1.f, 1.f);
-                if (p.gz && row < all) {
-                    // d/dz [z sz] = sz (1 + z (1 - sz))
-                    const float2 d = mul2(sz, fma2(zv, make_float2(1.f - sz.x, 1.f - sz.y), one));
-                    const float2 gz = mul2(mul2(dy, fma2(D, uv, make_float2(s0.z, s1.z))), d);
-                    store_pair<PAIRS>(p.gz + o, in ? pack2<DT>(gz) : 0u, on0, on1);
-                }
-                dy = mul2(dy, mul2(zv, sz));
-            }
+            const float2 uv = unpack2<DT>(ru[r]), sb = make_float2(s0.y, s1.y);
             constexpr float ln2 = 0.693147181f;
-            float2 gr = fma2(uv, sb, mul2(make_float2(s0.x, s1.x), make_float2(ln2, ln2)));
-            if (p.softplus)
-                gr = mul2(gr, sigmoid2(raw));
-            const float2 gu = fma2(make_float2(s0.w, s1.w), sb, mul2(D, dy));
-            if (in) {
-                gD = fma2(dy, uv, gD);
-                gbias = add2(gbias, gr);
-            }
+            float2 gr = mul2(fma2(uv, sb, mul2(make_float2(s0.x, s1.x), make_float2(ln2, ln2))), slope[r]);
+            float2 gu = fma2(make_float2(s0.w, s1.w), sb, mul2(D, dy[r]));
+            if (row >= rows)
+                gr = gu = make_float2(0.f, 0.f);
+            gD = fma2(dy[r], uv, gD);      // past the end both are zeros
+            gbias = add2(gbias, gr);
             if (row < all) {
-                store_pair<PAIRS>(p.gu + o, in ? pack2<DT>(gu) : 0u, on0, on1);
-                store_pair<PAIRS>(p.gdelta + o, in ? pack2<DT>(gr) : 0u, on0, on1);
+                store_pair<PAIRS>(p.gu + o + r * os, pack2<DT>(gu), on0, on1);
+                store_pair<PAIRS>(p.gdelta + o + r * os, pack2<DT>(gr), on0, on1);
             }
         }
         __syncthreads();   // hs is written again in the next tile
