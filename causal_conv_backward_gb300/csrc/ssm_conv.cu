@@ -30,7 +30,7 @@ struct ConvParams {
     const int32_t *lengths;
     uint16_t *y, *final_state;
     int64_t xs, xb, S, B, H, vecs;   // vecs = H / V
-    int32_t L, silu;
+    int32_t L;
 };
 
 // Row t of a sequence behind its carried window: x for t >= 0, else the
@@ -44,7 +44,7 @@ __device__ __forceinline__ Vec<V> window_row(const uint16_t *x, int64_t xs, cons
     return state ? vload<V>(state + (t + W - 1) * H) : vzero<V>();
 }
 
-template <int DT, int V, int W>
+template <int DT, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams p)
 {
     constexpr int P = Vec<V>::P;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_fwd(const ConvParams 
                 for (int k = 0; k < W - 1; ++k)
                     s = fma2(w[k][e], win[k][e], s);
                 s = fma2(w[W - 1][e], v, s);
-                if (p.silu)
+                if (SILU)
                     s = mul2(s, sigmoid2(s));
                 out.u[e] = pack2<DT>(s);
 #pragma unroll
@@ -199,15 +199,15 @@ __global__ void __launch_bounds__(kThreads) mcc1d_ssm_conv_step(const StepParams
 
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-template <int DT>
+template <int DT, bool SILU>
 int32_t run_fwd(const ConvParams &p, int V, int W, dim3 grid, cudaStream_t s)
 {
     switch (W) {
 #define MCC1D_CASE(w)                                                            \
     case w:                                                                      \
-        return V == 1 ? launch(mcc1d_ssm_conv_fwd<DT, 1, w>, grid, kThreads, 0, s, p)   \
-               : V == 2 ? launch(mcc1d_ssm_conv_fwd<DT, 2, w>, grid, kThreads, 0, s, p) \
-                        : launch(mcc1d_ssm_conv_fwd<DT, conv_vec(w), w>, grid, kThreads, 0, s, p);
+        return V == 1 ? launch(mcc1d_ssm_conv_fwd<DT, 1, w, SILU>, grid, kThreads, 0, s, p)   \
+               : V == 2 ? launch(mcc1d_ssm_conv_fwd<DT, 2, w, SILU>, grid, kThreads, 0, s, p) \
+                        : launch(mcc1d_ssm_conv_fwd<DT, conv_vec(w), w, SILU>, grid, kThreads, 0, s, p);
         MCC1D_CASE(1) MCC1D_CASE(2) MCC1D_CASE(3) MCC1D_CASE(4)
         MCC1D_CASE(5) MCC1D_CASE(6) MCC1D_CASE(7) MCC1D_CASE(8)
 #undef MCC1D_CASE
@@ -256,7 +256,6 @@ int32_t launch_short_conv(const mcc1d_short_conv_args &a, cudaStream_t stream)
     p.S = a.S;
     p.B = a.B;
     p.H = a.H;
-    p.silu = (a.flags & MCC1D_SILU) != 0;
     const int V = fwd_vec(a);
     p.vecs = a.H / V;
     const int64_t lanes = a.B * p.vecs, blocks = (lanes + kThreads - 1) / kThreads;
@@ -269,7 +268,9 @@ int32_t launch_short_conv(const mcc1d_short_conv_args &a, cudaStream_t stream)
         L *= 2;
     p.L = (int32_t)L;
     const dim3 grid((unsigned)blocks, (unsigned)((a.S + L - 1) / L));
-    return a.dtype == 0 ? run_fwd<0>(p, V, (int)a.W, grid, stream) : run_fwd<1>(p, V, (int)a.W, grid, stream);
+    const bool silu = (a.flags & MCC1D_SILU) != 0;
+    const auto run = a.dtype == 0 ? (silu ? run_fwd<0, true> : run_fwd<0, false>) : (silu ? run_fwd<1, true> : run_fwd<1, false>);
+    return run(p, V, (int)a.W, grid, stream);
 }
 
 int32_t launch_short_conv_step(const mcc1d_short_conv_step_args &a, cudaStream_t stream)

@@ -34,10 +34,10 @@ struct ConvBwdParams {
     uint16_t *gx, *gstate;
     float *partial;
     int64_t gs, gb, xs, xb, S, B, H, vecs, supers;
-    int32_t L, silu;
+    int32_t L;
 };
 
-template <int DT, int V, int W>
+template <int DT, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvBwdParams p)
 {
     constexpr int P = Vec<V>::P;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
             for (int e = 0; e < P; ++e) {
                 const float2 v = unpack2<DT>(rx.u[e]);
                 float2 d = unpack2<DT>(rg.u[e]);
-                if (p.silu) {
+                if (SILU) {
                     float2 s = bias[e];
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k)
@@ -258,15 +258,15 @@ __global__ void __launch_bounds__(256) mcc1d_ssm_conv_bwd_sum(const float *parti
     }
 }
 
-template <int DT>
+template <int DT, bool SILU>
 int32_t run_bwd(const ConvBwdParams &p, int V, int W, dim3 grid, cudaStream_t s)
 {
     switch (W) {
 #define MCC1D_CASE(w)                                                            \
     case w:                                                                      \
-        return V == 1 ? launch(mcc1d_ssm_conv_bwd<DT, 1, w>, grid, kWarps * 32, 0, s, p)   \
-               : V == 2 ? launch(mcc1d_ssm_conv_bwd<DT, 2, w>, grid, kWarps * 32, 0, s, p) \
-                        : launch(mcc1d_ssm_conv_bwd<DT, conv_vec(w), w>, grid, kWarps * 32, 0, s, p);
+        return V == 1 ? launch(mcc1d_ssm_conv_bwd<DT, 1, w, SILU>, grid, kWarps * 32, 0, s, p)   \
+               : V == 2 ? launch(mcc1d_ssm_conv_bwd<DT, 2, w, SILU>, grid, kWarps * 32, 0, s, p) \
+                        : launch(mcc1d_ssm_conv_bwd<DT, conv_vec(w), w, SILU>, grid, kWarps * 32, 0, s, p);
         MCC1D_CASE(1) MCC1D_CASE(2) MCC1D_CASE(3) MCC1D_CASE(4)
         MCC1D_CASE(5) MCC1D_CASE(6) MCC1D_CASE(7) MCC1D_CASE(8)
 #undef MCC1D_CASE
@@ -326,12 +326,13 @@ int32_t launch_short_conv_bwd(const mcc1d_short_conv_bwd_args &a, void *workspac
     p.H = a.H;
     p.supers = plan.supers;
     p.L = plan.L;
-    p.silu = (a.flags & MCC1D_SILU) != 0;
     const int V = bwd_vec(a);
     p.vecs = a.H / V;
     const int64_t gy = plan.parts < 32768 ? plan.parts : 32768;
     const dim3 grid((unsigned)((p.vecs + 31) / 32), (unsigned)gy, (unsigned)((plan.parts + gy - 1) / gy));
-    const int32_t st = a.dtype == 0 ? run_bwd<0>(p, V, (int)a.W, grid, stream) : run_bwd<1>(p, V, (int)a.W, grid, stream);
+    const bool silu = (a.flags & MCC1D_SILU) != 0;
+    const auto run = a.dtype == 0 ? (silu ? run_bwd<0, true> : run_bwd<0, false>) : (silu ? run_bwd<1, true> : run_bwd<1, false>);
+    const int32_t st = run(p, V, (int)a.W, grid, stream);
     if (st != kOk)
         return st;
     const int64_t cols = (a.W + 1) * a.H;
