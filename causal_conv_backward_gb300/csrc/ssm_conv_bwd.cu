@@ -11,10 +11,10 @@
 // The weight sums stay in registers over the L rows, are added over the
 // block's 8 warps in shared memory and over blocks by a second kernel, each in
 // a fixed order: nothing depends on scheduling. 6 bytes per element move: bf16,
-// W = 4, 8192 x 8 x 4096 takes 312 us (0.76 of the measured copy bandwidth;
-// 779 with plain loads, 371 with runs of 64 rows), 4096 x 8 x 2048 96 us
-// (0.62). What is left over memory's time is instructions: 28 per element, at
-// two blocks of 128 registers per SM.
+// W = 4, 8192 x 8 x 4096 takes 288 us (0.83 of the measured copy bandwidth; 779
+// with plain loads, 371 with runs of 64 rows, 312 with the activation tested
+// per row), 4096 x 8 x 2048 88 us (0.67). What is left over memory's time is
+// instructions (21 per element) at two blocks of 128 registers per SM.
 #include "plan.h"
 #include "ssm.h"
 #include "ssm_common.cuh"
@@ -293,7 +293,8 @@ ConvBwdPlan conv_bwd_plan(const mcc1d_short_conv_bwd_args &a)
 {
     ConvBwdPlan p;
     // Every run of rows begins and ends with rows that go one by one: 64 rows per
-    // warp cost 371 us on 8192 x 8 x 4096, 128 334, 256 311 and 512 338. Fewer
+    // warp cost 371 us on 8192 x 8 x 4096, 128 334, 256 311 and 512 338 (measured
+    // before the last two changes to the rows' loop). Fewer
     // rows where that leaves less than a block per SM (at two blocks per SM
     // 4096 x 2 x 2048 took 41 us, at one 36)
     const int64_t wide = (a.H + 127) / 128 * a.B;

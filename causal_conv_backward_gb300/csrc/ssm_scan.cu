@@ -11,9 +11,9 @@
 // The design therefore spends as few other instructions per state as it can.
 // A channel's states sit four to a lane (ssm_scan.cuh): enough warps for a few
 // thousand channels without cutting the sequence. Measured, bf16, N = 16:
-// 691 us on 1024 x 32 x 4096 (48 cycles per 128 steps, issuing on 66 % of
-// cycles), 422 us on 4096 x 8 x 2048 (512 blocks on 152 SMs: four on some and
-// three on others), 465 us on 131072 x 1 x 384 (cut in chunks).
+// 690 us on 1024 x 32 x 4096 (48 cycles per 128 steps, issuing on 64 % of
+// cycles), 418 us on 4096 x 8 x 2048 (512 blocks on 152 SMs: four on some and
+// three on others), 461 us on 131072 x 1 x 384 (cut in chunks).
 //
 // Where sequences and channels are too few to fill the machine the time axis
 // is cut into chunks: each chunk's state from a zero start and its sum of dt

@@ -21,12 +21,13 @@
 //
 // 14 bytes per (token, channel) have to move, and about 21 N flops with 3 N
 // exponentials (the states are run through three times) are computed: it is
-// bound by instructions, 39 per 128 (channel, state) steps in the first pass
-// and 114 in this one, of which 63 are the run back, 9 the run forward and
-// 16 + 7 the sums over lanes. Four blocks of 128 registers per SM beat three of
-// 168 (2048 x 8 x 2048: 886 against 921 us), which is why the tile's rows are
-// read again at its end and the warps' sums take the place of the states they
-// have used. bf16, N = 16: 830 us on 2048 x 8 x 2048, 3185 on 1024 x 32 x 4096.
+// bound by instructions, about 38 per 128 (channel, state) steps in the first
+// pass and 114 in this one, of which 63 are the run back (16 of them its sums
+// over a channel's lanes, 7 those over a warp's channels) and 9 the run
+// forward. Four blocks of 128 registers per SM beat three of 168 (4096 x 8 x
+// 2048: 1706 against 1771 us), which is why the tile's rows are read again at
+// its end and the warps' sums take the place of the states they have used.
+// bf16, N = 16: 812 us on 2048 x 8 x 2048, 3105 on 1024 x 32 x 4096.
 #include "plan.h"
 #include "ssm_scan.cuh"
 
