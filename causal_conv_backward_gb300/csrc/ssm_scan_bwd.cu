@@ -85,11 +85,15 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
     int64_t hc[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        hc[k] = w.b * p.H + w.c0 + (cl + k < w.nc ? cl + k : 0);
-        const float4 a = load_states(p.A + (hc[k] - w.b * p.H) * p.N, n0, p.N, p.vecA);
+        const bool there = cl + k < w.nc;
+        hc[k] = w.b * p.H + w.c0 + (there ? cl + k : 0);
+        // A lane past the group's channels holds zeros: its steps are softplus(0), under which another channel's
+        // growing state or gradient would pass fp32, and infinity times its zero input is NaN in the group's sums.
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = there ? load_states(p.A + (hc[k] - w.b * p.H) * p.N, n0, p.N, p.vecA) : none;
         A2[k][0] = make_float2(a.x * kLog2e, a.y * kLog2e);
         A2[k][1] = make_float2(a.z * kLog2e, a.w * kLog2e);
-        const float4 x = *reinterpret_cast<const float4 *>(p.r + (w.chunk * p.B * p.H + hc[k]) * NP + n0);
+        const float4 x = there ? *reinterpret_cast<const float4 *>(p.r + (w.chunk * p.B * p.H + hc[k]) * NP + n0) : none;
         X[k][0] = make_float2(x.x, x.y);
         X[k][1] = make_float2(x.z, x.w);
         gA[k][0] = gA[k][1] = make_float2(0.f, 0.f);

@@ -1,0 +1,35 @@
+"""Values at the edges of the short convolution and the selective scan: what a
+mask, a padding lane or a padding row covers leaves nothing behind, whatever
+stands there, and finite results come out of large intermediate ones."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import causal_conv_backward_gb300 as m  # noqa: E402
+import ssm_reference as ref  # noqa: E402
+from test_ssm_gpu import BF16, F32, cuda_ready, guards, lens, rand, reference_scan, scan_inputs  # noqa: E402,F401
+
+SCAN_ARGS = ("u", "delta", "A", "B", "C", "D", "z", "delta_bias")
+INF = float("inf")
+
+
+# N = 4, 16, 64: one, four and sixteen lanes per channel, blocks of 256, 64 and 16 channels
+@pytest.mark.parametrize("N,H,G", [(4, 5, 1), (16, 5, 1), (16, 6, 2), (64, 3, 1)])
+def test_growing_states_leave_the_groups_other_channels_alone(N, H, G):
+    """A > 0 with small steps: every state grows a little, and lanes past the
+    group's last channel, whose steps are not small, add nothing."""
+    S, B = 40, 2
+    t, clean = scan_inputs(S, B, H, N, G, BF16, "Dzsp", "dense", None)
+    for d in (t, clean):
+        d["A"] = 60 + 0.1 * rand(H, N, dtype=F32, seed=30)
+        d["delta"] = (-6.9 + 0.1 * rand(S, B, H, dtype=F32, seed=31)).to(BF16)   # steps near 0.001
+    args = [t[k] for k in SCAN_ARGS]
+    gy, gf = rand(S, B, H, seed=20), rand(B, H, N, dtype=F32, seed=21)
+    leaves, ry, rf = reference_scan(clean, "p", None)
+    got = m.selective_scan_backward(gy, *args, delta_softplus=True, state=t["state"], grad_final_state=gf)
+    loss = (ry * ref.to64(gy)).sum() + (rf * ref.to64(gf)).sum()
+    names = [k for k in got._fields if leaves[k] is not None]
+    for k, want in zip(names, torch.autograd.grad(loss, [leaves[k] for k in names])):
+        terms = {"B": H // G + 64, "C": H // G + 64, "A": S * B, "D": S * B}.get(k, 4 * N + 64)
+        ref.check(getattr(got, k), want, terms, k)
