@@ -1,5 +1,9 @@
 """The short convolution and the selective scan on torch tensors: argument
-checks and marshalling over the C ABI of ``include/mcc1d_ssm.h``."""
+checks and marshalling over the C ABI of ``include/mcc1d_ssm.h``.
+
+``stream`` (a torch stream or its handle) takes a call off the current stream.
+The caller orders it after what made the inputs, and later users of the results
+after it; memory is not reused before both streams are done with it."""
 from __future__ import annotations
 
 import ctypes
@@ -162,8 +166,7 @@ def _flag(activation):
 
 # ------------------------------------------------------------------ streams and workspaces
 def _stream(stream, index):
-    """The stream's handle, and the torch stream to record tensors on where one
-    was given (their memory must not be reused before it is done)."""
+    """The stream's handle, and the torch stream where one was given."""
     if stream is None:
         return _raw_stream(index), None
     if isinstance(stream, int):
@@ -171,10 +174,27 @@ def _stream(stream, index):
     return stream.cuda_stream, stream
 
 
-def _record(stream, *tensors):
-    for t in tensors:
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`. A given stream's comes from its own pool:
+    the current stream may still be reading or writing what its pool hands out,
+    and nothing orders the given stream after that."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
+
+
+def _record(stream, index, used, made=()):
+    """After a call on a given stream: no tensor's memory is reused before that
+    stream is done with it, nor the outputs' before the current stream is."""
+    current = _torch.cuda.current_stream(index)
+    for t in used:
         if t is not None:
             t.record_stream(stream)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(current)
 
 
 def _call(name, args, handle):
@@ -190,12 +210,10 @@ def _call_ws(name, args, handle, stream, device):
     if st != 0:
         raise Mcc1dError(st, name + "_workspace_size")
     n = n.value
-    ws = _torch.empty(n, dtype=_torch.uint8, device=device) if n else None
+    ws = _empty(n, _torch.uint8, device, stream) if n else None
     st = getattr(_lib, name)(args, ws.data_ptr() if n else 0, n, handle)
     if st != 0:
         raise Mcc1dError(st, name)
-    if stream is not None:
-        _record(stream, ws)
 
 
 # ------------------------------------------------------------------ short convolution
@@ -213,17 +231,17 @@ def short_conv(x, weight, bias=None, *, activation="silu", lengths=None, state=N
     shape, code, index = _first(x, "x", 3)
     S, B, H = shape
     W, dt, device = weight.shape[0], x.dtype, x.device
+    handle, stream = _stream(stream, index)
     if y is None:
-        y = _torch.empty(shape, dtype=dt, device=device)
-    final = _torch.empty((B, W - 1, H), dtype=dt, device=device) if return_state else None
+        y = _empty(shape, dt, device, stream)
+    final = _empty((B, W - 1, H), dt, device, stream) if return_state else None
     args = _pack_conv(x.data_ptr(), x.stride(0), x.stride(1), _dense(weight, "weight", (W, H), dt, index),
                       _optional(bias, "bias", (H,), dt, index), _optional(state, "state", (B, W - 1, H), dt, index),
                       _optional(lengths, "lengths", (B,), _torch.int32, index), _dense(y, "y", shape, dt, index),
                       0 if final is None else final.data_ptr(), S, B, H, W, code, _flag(activation))
-    handle, stream = _stream(stream, index)
     _call("mcc1d_short_conv", args, handle)
     if stream is not None:
-        _record(stream, x, weight, bias, state, lengths, y, final)
+        _record(stream, index, (x, weight, bias, state, lengths), (y, final))
     return (y, final) if return_state else y
 
 
@@ -237,10 +255,11 @@ def short_conv_backward(grad_y, x, weight, bias=None, *, activation="silu", leng
     shape, code, index = _first(x, "x", 3)
     S, B, H = shape
     W, dt, device = weight.shape[0], x.dtype, x.device
-    gx = _torch.empty(shape, dtype=dt, device=device)
-    gw = _torch.empty((W, H), dtype=dt, device=device)
-    gb = _torch.empty((H,), dtype=dt, device=device) if bias is not None else None
-    gs = _torch.empty((B, W - 1, H), dtype=dt, device=device) if state is not None else None
+    handle, stream = _stream(stream, index)
+    gx = _empty(shape, dt, device, stream)
+    gw = _empty((W, H), dt, device, stream)
+    gb = _empty((H,), dt, device, stream) if bias is not None else None
+    gs = _empty((B, W - 1, H), dt, device, stream) if state is not None else None
     args = _pack_conv_bwd(_rows(grad_y, "grad_y", shape, dt, index), grad_y.stride(0), grad_y.stride(1), x.data_ptr(),
                           x.stride(0), x.stride(1), _dense(weight, "weight", (W, H), dt, index),
                           _optional(bias, "bias", (H,), dt, index), _optional(state, "state", (B, W - 1, H), dt, index),
@@ -248,10 +267,9 @@ def short_conv_backward(grad_y, x, weight, bias=None, *, activation="silu", leng
                           _optional(grad_final_state, "grad_final_state", (B, W - 1, H), dt, index), gx.data_ptr(),
                           gw.data_ptr(), 0 if gb is None else gb.data_ptr(), 0 if gs is None else gs.data_ptr(),
                           S, B, H, W, code, _flag(activation))
-    handle, stream = _stream(stream, index)
     _call_ws("mcc1d_short_conv_bwd", args, handle, stream, device)
     if stream is not None:
-        _record(stream, grad_y, x, weight, bias, state, lengths, grad_final_state, gx, gw, gb, gs)
+        _record(stream, index, (grad_y, x, weight, bias, state, lengths, grad_final_state), (gx, gw, gb, gs))
     return ShortConvGrads(gx, gw, gb, gs)
 
 
@@ -276,16 +294,16 @@ def short_conv_step(x, state, weight, bias=None, *, activation="silu", slots=Non
     shape, code, index = _first(x, "x", 2)
     B, H = shape
     W, dt = weight.shape[0], x.dtype
+    handle, stream = _stream(stream, index)
     if y is None:
-        y = _torch.empty(shape, dtype=dt, device=x.device)
+        y = _empty(shape, dt, x.device, stream)
     cache, rows, at = _cache(state, (W - 1, H), dt, index, B, slots)
     args = _pack_conv_step(x.data_ptr(), x.stride(0), cache, _dense(weight, "weight", (W, H), dt, index),
                            _optional(bias, "bias", (H,), dt, index), at, _dense(y, "y", shape, dt, index), rows, B, H,
                            W, code, _flag(activation))
-    handle, stream = _stream(stream, index)
     _call("mcc1d_short_conv_step", args, handle)
     if stream is not None:
-        _record(stream, x, state, weight, bias, slots, y)
+        _record(stream, index, (x, state, weight, bias, slots), (y,))
     return y
 
 
@@ -323,14 +341,14 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, delta_
     _load()
     (S, nb, H), _, index = _first(u, "u", 3)
     device = u.device
-    if y is None:
-        y = _torch.empty((S, nb, H), dtype=u.dtype, device=device)
-    final = _torch.empty((nb, H, A.shape[-1]), dtype=_torch.float32, device=device) if return_state else None
-    args = _pack_scan(*_scan_fields(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, y, final))
     handle, stream = _stream(stream, index)
+    if y is None:
+        y = _empty((S, nb, H), u.dtype, device, stream)
+    final = _empty((nb, H, A.shape[-1]), _torch.float32, device, stream) if return_state else None
+    args = _pack_scan(*_scan_fields(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lengths, state, y, final))
     _call_ws("mcc1d_scan", args, handle, stream, device)
     if stream is not None:
-        _record(stream, u, delta, A, B, C, D, z, delta_bias, lengths, state, y, final)
+        _record(stream, index, (u, delta, A, B, C, D, z, delta_bias, lengths, state), (y, final))
     return (y, final) if return_state else y
 
 
@@ -345,9 +363,10 @@ def selective_scan_backward(grad_y, u, delta, A, B, C, D=None, z=None, delta_bia
     shape, device, index, dt, f32 = u.shape, u.device, u.get_device(), u.dtype, _torch.float32
     S, nb, H = shape
     G, N = B.shape[2:]
+    handle, stream = _stream(stream, index)
 
     def out(like, shape, dtype):
-        return _torch.empty(shape, dtype=dtype, device=device) if like is not None else None
+        return _empty(shape, dtype, device, stream) if like is not None else None
 
     g = SelectiveScanGrads(out(u, shape, dt), out(u, shape, dt), out(A, (H, N), f32), out(B, (S, nb, G, N), dt),
                            out(C, (S, nb, G, N), dt), out(D, (H,), f32), out(z, shape, dt),
@@ -356,10 +375,9 @@ def selective_scan_backward(grad_y, u, delta, A, B, C, D=None, z=None, delta_bia
     args = _pack_scan_bwd(*fwd, _rows(grad_y, "grad_y", shape, dt, index), grad_y.stride(0), grad_y.stride(1),
                           _optional(grad_final_state, "grad_final_state", (nb, H, N), f32, index), at.u, at.delta,
                           at.z, at.B, at.C, at.A, at.D, at.delta_bias, at.state)
-    handle, stream = _stream(stream, index)
     _call_ws("mcc1d_scan_bwd", args, handle, stream, device)
     if stream is not None:
-        _record(stream, grad_y, u, delta, A, B, C, D, z, delta_bias, lengths, state, grad_final_state, *g)
+        _record(stream, index, (grad_y, u, delta, A, B, C, D, z, delta_bias, lengths, state, grad_final_state), g)
     return g
 
 
@@ -378,8 +396,9 @@ def selective_scan_step(u, delta, state, A, B, C, D=None, z=None, delta_bias=Non
         raise ValueError("A must be [H,N] and B, C [B,G,N]")
     N, G = A.shape[1], B.shape[1]
     bc = (nb, G, N)
+    handle, stream = _stream(stream, index)
     if y is None:
-        y = _torch.empty(shape, dtype=dt, device=u.device)
+        y = _empty(shape, dt, u.device, stream)
     cache, rows, at = _cache(state, (H, N), f32, index, nb, slots)
     args = _pack_scan_step(u.data_ptr(), u.stride(0), _rows(delta, "delta", shape, dt, index), delta.stride(0),
                            *((0, 0) if z is None else (_rows(z, "z", shape, dt, index), z.stride(0))),
@@ -388,8 +407,7 @@ def selective_scan_step(u, delta, state, A, B, C, D=None, z=None, delta_bias=Non
                            _optional(D, "D", (H,), f32, index), _optional(delta_bias, "delta_bias", (H,), f32, index),
                            cache, at, _dense(y, "y", shape, dt, index), rows, nb, H, N, G, code,
                            SOFTPLUS if delta_softplus else 0)
-    handle, stream = _stream(stream, index)
     _call("mcc1d_scan_step", args, handle)
     if stream is not None:
-        _record(stream, u, delta, state, A, B, C, D, z, delta_bias, slots, y)
+        _record(stream, index, (u, delta, state, A, B, C, D, z, delta_bias, slots), (y,))
     return y
