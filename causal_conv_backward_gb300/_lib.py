@@ -231,6 +231,35 @@ def mcc1d_fwd(x, weight, mask_or_null, y, stream, S, B, H, W, dtype, device_stat
         raise Mcc1dError(st, "mcc1d_fwd")
 
 
+class _On:
+    """A convenience call's stream: the current one, or `given` (a torch stream
+    or its handle), which the caller orders after what made the inputs. A given
+    stream's calls take memory from its own pool: the current stream may still
+    be using what its pool hands out, and nothing orders the given one after
+    that. Nor is any tensor's memory reused before both are done with it."""
+
+    def __init__(self, torch, given, device):
+        self.torch, self.current = torch, torch.cuda.current_stream(device)
+        if isinstance(given, int):
+            given = torch.cuda.ExternalStream(given, device=device) if given else torch.cuda.default_stream(device)
+        self.given, self.stream = given, given if given is not None else self.current
+
+    def empty(self, shape, dtype, device):
+        if self.given is None:
+            return self.torch.empty(shape, dtype=dtype, device=device)
+        with self.torch.cuda.stream(self.given):
+            return self.torch.empty(shape, dtype=dtype, device=device)
+
+    def record(self, used, made):
+        if self.given is None:
+            return
+        for t in (*used, *made):
+            if t is not None:
+                t.record_stream(self.given)
+        for t in made:
+            t.record_stream(self.current)
+
+
 def forward(x, weight, mask=None, *, y=None, stream=None):
     """Convenience forward on torch CUDA tensors x [S,B,H], weight [W,H]
     (1 <= W <= 8), mask [B,S] or None; inputs may be strided views (they go
@@ -240,20 +269,18 @@ def forward(x, weight, mask=None, *, y=None, stream=None):
     W = weight.shape[0]
     if mask is not None and mask.dtype == torch.bool:
         mask = mask.view(torch.uint8)
+    on = _On(torch, stream, x.device)
     if y is None:
-        y = torch.empty((S, B, H), dtype=x.dtype, device=x.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
+        y = on.empty((S, B, H), x.dtype, x.device)
     dense = x.is_contiguous() and weight.is_contiguous() and (mask is None or mask.is_contiguous())
     if dense:
-        mcc1d_fwd(x, weight, mask, y, stream, S, B, H, W, dtype_code(x.dtype))
+        mcc1d_fwd(x, weight, mask, y, on.stream, S, B, H, W, dtype_code(x.dtype))
     else:
         t = fwd_tensors(x, weight, mask, y)
         nb = mcc1d_fwd_ex_workspace_size(t, S, B, H, W, x.dtype)
-        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=x.device)
-        if isinstance(stream, torch.cuda.Stream):
-            ws.record_stream(stream)   # not reused before the call has run on `stream`
-        mcc1d_fwd_ex(t, S, B, H, W, x.dtype, ws, nb, stream)
+        ws = on.empty(max(nb, 1), torch.uint8, x.device)
+        mcc1d_fwd_ex(t, S, B, H, W, x.dtype, ws, nb, on.stream)
+    on.record((x, weight, mask), (y,))
     return y
 
 
@@ -353,12 +380,11 @@ def backward(gradY, x, weight, mask=None, *, gradX=None, gradWeight=None, worksp
             raise ValueError("gradY, x and weight must be CUDA tensors")
     if mask is not None and mask.dtype == torch.bool:
         mask = mask.view(torch.uint8)
+    on = _On(torch, stream, gradY.device)
     if gradX is None:
-        gradX = torch.empty((S, B, H), dtype=gradY.dtype, device=gradY.device)
+        gradX = on.empty((S, B, H), gradY.dtype, gradY.device)
     if gradWeight is None:
-        gradWeight = torch.empty((W, H), dtype=weight.dtype, device=weight.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(gradY.device)
+        gradWeight = on.empty((W, H), weight.dtype, weight.device)
     dense = (W == 3 and all(t.is_contiguous() for t in (gradY, x, weight))
              and (mask is None or mask.is_contiguous()))
     if dense:
@@ -367,12 +393,11 @@ def backward(gradY, x, weight, mask=None, *, gradX=None, gradWeight=None, worksp
         desc = tensors(gradY, x, weight, mask, gradX, gradWeight)
         nbytes = mcc1d_bwd_ex_workspace_size(desc, S, B, H, W, code)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=gradY.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)   # not reused before the call has run on `stream`
+        workspace = on.empty(nbytes, torch.uint8, gradY.device)
     wsb = workspace.numel() * workspace.element_size()
     if dense:
-        mcc1d_bwd(gradY, x, weight, mask, gradX, gradWeight, workspace, stream, S, B, H, W, code, wsb)
+        mcc1d_bwd(gradY, x, weight, mask, gradX, gradWeight, workspace, on.stream, S, B, H, W, code, wsb)
     else:
-        mcc1d_bwd_ex(desc, S, B, H, W, code, workspace, wsb, stream)
+        mcc1d_bwd_ex(desc, S, B, H, W, code, workspace, wsb, on.stream)
+    on.record((gradY, x, weight, mask, workspace), (gradX, gradWeight))
     return gradX, gradWeight
