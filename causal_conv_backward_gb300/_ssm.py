@@ -171,6 +171,8 @@ def _stream(stream, index):
         return _raw_stream(index), None
     if isinstance(stream, int):
         stream = _torch.cuda.ExternalStream(stream, device=index) if stream else _torch.cuda.default_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on cuda:{stream.device.index}, the tensors on cuda:{index}")
     return stream.cuda_stream, stream
 
 

@@ -136,3 +136,11 @@ def test_a_given_output_is_recorded_on_the_stream(fake, name):
     y, side = Tensor(args[0].shape, "bf16"), Stream("side")
     assert outputs(getattr(_ssm, name)(*args, y=y, stream=side, **kw))[0] is y
     assert side in y.recorded
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_of_another_device_is_refused(fake, name):
+    args, kw = calls()[name]
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        getattr(_ssm, name)(*args, stream=Stream("there", index=1), **kw)
+    assert not fake.made and not any(t.recorded for t in args if isinstance(t, Tensor))
