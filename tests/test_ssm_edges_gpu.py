@@ -33,3 +33,41 @@ def test_growing_states_leave_the_groups_other_channels_alone(N, H, G):
     for k, want in zip(names, torch.autograd.grad(loss, [leaves[k] for k in names])):
         terms = {"B": H // G + 64, "C": H // G + 64, "A": S * B, "D": S * B}.get(k, 4 * N + 64)
         ref.check(getattr(got, k), want, terms, k)
+
+
+@pytest.mark.parametrize("H,W", [(64, 4), (66, 6), (33, 4)])
+@pytest.mark.parametrize("activation", ["silu", None])
+def test_conv_sequence_without_tokens_adds_nothing(H, W, activation):
+    """Whatever the window of a length of zero holds, the weights' gradients
+    are those of the other sequences."""
+    S, B = 21, 3
+    x, w, b, gy = rand(S, B, H, seed=1), rand(W, H, scale=0.5, seed=2), rand(H, seed=3), rand(S, B, H, seed=4)
+    state, ln = rand(B, W - 1, H, seed=5), lens([21, 0, 13])
+    clean = m.short_conv_backward(gy, x, w, b, activation=activation, lengths=ln, state=state)
+    state[1, :, ::2], state[1, :, 1::2] = INF, float("nan")
+    got = m.short_conv_backward(gy, x, w, b, activation=activation, lengths=ln, state=state)
+    for k in ("x", "weight", "bias", "state"):
+        assert torch.equal(getattr(got, k), getattr(clean, k)), k
+
+
+@pytest.mark.parametrize("H,W", [(64, 4), (66, 6), (33, 4)])
+def test_conv_infinite_last_token_meets_its_own_taps_only(H, W):
+    """Without an activation x(n-1) reaches one row of grad_weight; the rows
+    past the length give the same result as no rows there."""
+    S, n = 40, 21
+    x, w, gy = rand(S, 1, H, seed=1), rand(W, H, scale=0.5, seed=2), rand(S, 1, H, seed=4)
+    x[n - 1, 0, 3] = INF
+    got = m.short_conv_backward(gy, x, w, activation=None, lengths=lens([n]))
+    want = m.short_conv_backward(gy[:n], x[:n], w, activation=None)
+    assert want.weight.isinf().sum() == 1 and torch.isfinite(want.weight[:W - 1]).all()
+    assert torch.equal(got.weight, want.weight)
+    assert torch.equal(got.x[:n], want.x) and not got.x[n:].any()
+
+
+@pytest.mark.parametrize("bad", [INF, float("nan")])
+def test_conv_gradient_past_the_end_is_zero_for_any_weight(bad):
+    S, H, W, n = 40, 64, 4, 21
+    x, w, gy = rand(S, 1, H, seed=1), rand(W, H, scale=0.5, seed=2), rand(S, 1, H, seed=4)
+    w[:, 5] = bad
+    got = m.short_conv_backward(gy, x, w, lengths=lens([n]))
+    assert not got.x[n:].any()
