@@ -36,6 +36,7 @@ namespace mcc1d {
 namespace {
 
 constexpr int kSub = 2;          // rows whose states and decays sit in registers
+static_assert(kSub == 2, "a run that is walked back has at most its last row past the tokens");
 constexpr int kBlocksPerSM = 4;
 
 template <int NL>
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
         for (int k = 0; k < K; ++k)
             tA[k][0] = tA[k][1] = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int s = TT - kSub; s >= 0; s -= kSub) {
+        for (int s = (rows - 1) / kSub * kSub; s >= 0; s -= kSub) {   // from the run of the last token
             float2 hh[kSub + 1][K][2], aa[kSub][K][2];
             float ys[K * kSub], sa[K * kSub], sb[K * kSub];     // of (step, channel)
 #pragma unroll
@@ -261,8 +262,12 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
                     const float2 q0 = mul2(X[k][0], hh[i][k][0]), q1 = mul2(X[k][1], hh[i][k][1]);
                     const float2 a2 = fma2(A2[k][0], q0, mul2(A2[k][1], q1));
                     sa[i * K + k] = a2.x + a2.y;
-                    tA[k][0] = fma2(dt2, q0, tA[k][0]);
-                    tA[k][1] = fma2(dt2, q1, tA[k][1]);
+                    // A run's last row may be past the last token: its dt is 0, but the state it starts from, which
+                    // no token's grad_A has in it, may be infinite. (817 us on 2048 x 8 x 2048, 810 without the test.)
+                    if (i < kSub - 1 || s + i < rows) {
+                        tA[k][0] = fma2(dt2, q0, tA[k][0]);
+                        tA[k][1] = fma2(dt2, q1, tA[k][1]);
+                    }
                     v0 = k == 0 ? mul2(g0, du2) : fma2(g0, du2, v0);
                     v1 = k == 0 ? mul2(g1, du2) : fma2(g1, du2, v1);
                     c0 = k == 0 ? mul2(hh[i + 1][k][0], dy2) : fma2(hh[i + 1][k][0], dy2, c0);

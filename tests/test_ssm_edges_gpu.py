@@ -71,3 +71,20 @@ def test_conv_gradient_past_the_end_is_zero_for_any_weight(bad):
     w[:, 5] = bad
     got = m.short_conv_backward(gy, x, w, lengths=lens([n]))
     assert not got.x[n:].any()
+
+
+@pytest.mark.parametrize("S,lengths", [(20, None), (21, None), (48, [37])])
+def test_infinite_last_input_leaves_grad_A_finite(S, lengths):
+    """grad_A sums g(t) a(t) h(t-1): the state after the last token is not in
+    it, though it stands in the rows that fill the last tile."""
+    H, N = 6, 16
+    t, clean = scan_inputs(S, 1, H, N, 1, BF16, "Dp", "dense", None)
+    n = S if lengths is None else lengths[0]
+    for d in (t, clean):
+        d["u"][n - 1, 0, 2] = INF
+    gy = rand(S, 1, H, seed=20)
+    leaves, ry, _ = reference_scan(clean, "p", lengths)
+    want = torch.autograd.grad((ry[:n] * ref.to64(gy)[:n]).sum(), leaves["A"])[0]
+    assert torch.isfinite(want).all()
+    got = m.selective_scan_backward(gy, *[t[k] for k in SCAN_ARGS], delta_softplus=True, lengths=lens(lengths))
+    ref.check(got.A, want, S, "A")
