@@ -232,6 +232,17 @@ __device__ __forceinline__ float2 decay2(float2 dt2, float2 A2)
     return make_float2(ex2(x.x), ex2(x.y));
 }
 
+// exp(dt A) h + b for two states, from A log2 e and the dt of many tokens. The
+// growth goes in as two factors, neither of them infinite: alone it may pass
+// fp32 where no state does (an h of zero stays zero); token by token it does
+// not arise.
+__device__ __forceinline__ float2 grown(float2 h, float dt, float2 A2, float2 b)
+{
+    const float2 x = mul2(make_float2(0.5f * dt, 0.5f * dt), A2);
+    const float2 f = make_float2(ex2(fminf(x.x, 127.f)), ex2(fminf(x.y, 127.f)));
+    return fma2(f, mul2(f, h), b);
+}
+
 __device__ __forceinline__ float rcp(float x)
 {
     float r;

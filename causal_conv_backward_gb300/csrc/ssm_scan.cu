@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
     const int64_t row = i / NL;
     const int n0 = 4 * (int)(i - row * NL), NP = 4 * NL;
     const float4 A = load_states(p.A + row % p.H * p.N, n0, p.N, p.vecA);
-    const float a[4] = {A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e};
+    const float2 a0 = make_float2(A.x * kLog2e, A.y * kLog2e), a1 = make_float2(A.z * kLog2e, A.w * kLog2e);
     next_may_start();
     previous_done();
     const bool back = blockIdx.y == 1;
@@ -366,10 +366,9 @@ __global__ void __launch_bounds__(128) mcc1d_ssm_scan_join(const ScanParams p, i
             if (c0 + k < p.chunks) {
                 const int64_t c = (back ? p.chunks - 1 - c0 - k : c0 + k) * rows + row;
                 *reinterpret_cast<float4 *>(at + c * NP + n0) = s;
-                s.x = fmaf(ex2(a[0] * d[k]), s.x, v[k].x);
-                s.y = fmaf(ex2(a[1] * d[k]), s.y, v[k].y);
-                s.z = fmaf(ex2(a[2] * d[k]), s.z, v[k].z);
-                s.w = fmaf(ex2(a[3] * d[k]), s.w, v[k].w);
+                const float2 lo = grown(make_float2(s.x, s.y), d[k], a0, make_float2(v[k].x, v[k].y));
+                const float2 hi = grown(make_float2(s.z, s.w), d[k], a1, make_float2(v[k].z, v[k].w));
+                s = make_float4(lo.x, lo.y, hi.x, hi.y);
             }
     }
     if (back && p.gstate)

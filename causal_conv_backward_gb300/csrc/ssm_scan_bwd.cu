@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(BwdMainTile<NL>::EL_THREADS, kBlocksPerSM) mcc
             const float4 s = *reinterpret_cast<const float4 *>(p.cp + ct * NP + n0);
             const float4 e = *reinterpret_cast<const float4 *>(p.e + (w.chunk * p.B * p.H + hc[k]) * NP + n0);
             const float d = p.cpdt[ct];
-            h[k][0] = fma2(make_float2(ex2(d * A2[k][0].x), ex2(d * A2[k][0].y)), make_float2(e.x, e.y), make_float2(s.x, s.y));
-            h[k][1] = fma2(make_float2(ex2(d * A2[k][1].x), ex2(d * A2[k][1].y)), make_float2(e.z, e.w), make_float2(s.z, s.w));
+            h[k][0] = grown(make_float2(e.x, e.y), d, A2[k][0], make_float2(s.x, s.y));
+            h[k][1] = grown(make_float2(e.z, e.w), d, A2[k][1], make_float2(s.z, s.w));
         }
         __syncthreads();
 #pragma unroll 1

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 import causal_conv_backward_gb300 as m  # noqa: E402
 import ssm_reference as ref  # noqa: E402
 from test_ssm_gpu import BF16, F32, cuda_ready, guards, lens, rand, reference_scan, scan_inputs  # noqa: E402,F401
+from test_ssm_long_gpu import leaf, scan64, scan_bwd_chunks  # noqa: E402
 
 SCAN_ARGS = ("u", "delta", "A", "B", "C", "D", "z", "delta_bias")
 INF = float("inf")
@@ -88,3 +89,54 @@ def test_infinite_last_input_leaves_grad_A_finite(S, lengths):
     assert torch.isfinite(want).all()
     got = m.selective_scan_backward(gy, *[t[k] for k in SCAN_ARGS], delta_softplus=True, lengths=lens(lengths))
     ref.check(got.A, want, S, "A")
+
+
+@pytest.mark.parametrize("N", [4, 16, 64])
+def test_empty_states_stay_empty_through_any_growth(N):
+    """Zero inputs first (padding on the left), with A > 0 and steps so large
+    that the growth over a chunk is past fp32: the states stay zero until the
+    first input, and what follows is as if it stood alone."""
+    S, H, first, G = 260, 10, 215, 1
+    t, clean = scan_inputs(S, 1, H, N, G, BF16, "Dzp", "dense", None)
+    for d in (t, clean):
+        d["A"] = 1 + 0.1 * rand(H, N, dtype=F32, seed=30)
+        d["u"][:first] = 0
+        d["delta"][:first] = 30.0        # e^(30 A) per token
+        d["delta"][first:] = -4.0
+    args = [t[k] for k in SCAN_ARGS]
+    alone = {k: v[first:] if v is not None and k in ("u", "delta", "B", "C", "z") else v for k, v in clean.items()}
+    leaves, ry, rf = reference_scan(alone, "p", None)
+    y, final = m.selective_scan(*args, delta_softplus=True, return_state=True)
+    assert not y[:first].any()
+    ref.check(y[first:], ry, N + 64, "y")
+    ref.check(final, rf, N + 64, "final state")
+    gy = rand(S, 1, H, seed=20)
+    got = m.selective_scan_backward(gy, *args, delta_softplus=True)
+    names = ("u", "delta", "B", "C", "z")
+    for k, want in zip(names, torch.autograd.grad((ry * ref.to64(gy[first:])).sum(), [leaves[k] for k in names])):
+        ref.check(getattr(got, k)[first:], want, {"B": H + 64, "C": H + 64}.get(k, 4 * N + 64), k)
+
+
+def test_empty_states_stay_empty_in_chunks_of_several_tiles():
+    """The same where the first input stands in a chunk's second tile."""
+    S, B, H, N, first = 450, 128, 7, 16, 215
+    tiles, chunks = scan_bwd_chunks(S, B, H, N, 1)
+    per = -(-tiles // chunks)
+    assert first // 16 % per > 0
+    t, clean = scan_inputs(S, B, H, N, 1, BF16, "Dzbsp", "dense", None)
+    t["A"] = 1 + 0.1 * rand(H, N, dtype=F32, seed=30)
+    t["u"][:first] = 0
+    t["delta"][:first] = 30.0
+    t["delta"][first:] = -4.0
+    t["state"].zero_()
+    args, cut = [t[k] for k in SCAN_ARGS], ("u", "delta", "B", "C", "z")
+    leaves = {k: leaf(v[first:] if k in cut else v) for k, v in t.items()}
+    ry, rf = scan64(leaves, None)
+    y, final = m.selective_scan(*args, delta_softplus=True, return_state=True)
+    assert not y[:first].any()
+    ref.check(y[first:], ry, N + S, "y")
+    ref.check(final, rf, N + S, "final state")
+    gy = rand(S, B, H, seed=20)
+    got = m.selective_scan_backward(gy, *args, delta_softplus=True)
+    for k, want in zip(cut, torch.autograd.grad((ry * gy[first:].double()).sum(), [leaves[k] for k in cut])):
+        ref.check(getattr(got, k)[first:], want, {"B": H + S, "C": H + S}.get(k, 4 * N + S), k)
