@@ -226,9 +226,9 @@ def short_conv(x, weight, bias=None, *, activation="silu", lengths=None, state=N
     [H] or None. ``activation``: "silu" or None. ``state`` [B,W-1,H] holds the
     W-1 rows before the sequence (zeros without it). ``lengths`` (int32 [B])
     ends sequence b after lengths[b] tokens; y is zero past the end, and x is
-    not read there. Returns y, or (y, final_state) with ``return_state``: the
-    last W-1 rows, which continue the sequence in another call or in
-    ``short_conv_step``."""
+    not read there. A given ``y`` is dense and overlaps no input. Returns y, or
+    (y, final_state) with ``return_state``: the last W-1 rows, which continue
+    the sequence in another call or in ``short_conv_step``."""
     _load()
     shape, code, index = _first(x, "x", 3)
     S, B, H = shape
@@ -291,7 +291,8 @@ def short_conv_step(x, state, weight, bias=None, *, activation="silu", slots=Non
     """``short_conv`` of one token per sequence: x [B,H]; ``state`` is a cache
     [rows,W-1,H] whose row b (or slots[b], int32) holds sequence b's window and
     is moved on in place. A slot outside the cache marks a padding row: y is
-    zero, no state changes. Two rows must not name one slot. Returns y [B,H]."""
+    zero, no state changes. Two rows must not name one slot. A given ``y`` is
+    dense and overlaps nothing else. Returns y [B,H]."""
     _load()
     shape, code, index = _first(x, "x", 2)
     B, H = shape
@@ -338,8 +339,9 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, delta_
     an adjacent last axis; H/G channels share a group's B and C; N <= 64); A
     [H,N], D [H], delta_bias [H] and ``state`` [B,H,N], the state before the
     sequence, are fp32. ``lengths`` (int32 [B]) ends sequence b after
-    lengths[b] tokens: y is zero past the end, nothing is read there. Returns
-    y, or (y, final_state) with ``return_state``."""
+    lengths[b] tokens: y is zero past the end, nothing is read there. A given
+    ``y`` is dense and overlaps no input. Returns y, or (y, final_state) with
+    ``return_state``."""
     _load()
     (S, nb, H), _, index = _first(u, "u", 3)
     device = u.device
@@ -389,7 +391,8 @@ def selective_scan_step(u, delta, state, A, B, C, D=None, z=None, delta_bias=Non
     [B,G,N]; ``state`` is an fp32 cache [rows,H,N] whose row b (or slots[b],
     int32) holds sequence b's state and is moved on in place. A slot outside
     the cache marks a padding row: y is zero, no state changes. Two rows must
-    not name one slot. Returns y [B,H]."""
+    not name one slot. A given ``y`` is dense and overlaps nothing else. Returns
+    y [B,H]."""
     _load()
     shape, code, index = _first(u, "u", 2)
     nb, H = shape

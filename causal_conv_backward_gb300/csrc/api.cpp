@@ -504,7 +504,7 @@ extern "C" const char *mcc1d_status_string(int32_t status)
     switch (status) {
     case kOk: return "MCC1D_OK";
     case kErrNull: return "MCC1D_ERR_PARAM_NULLPTR: a required pointer is null";
-    case kErrInvalid: return "MCC1D_ERR_PARAM_INVALID: unsupported dtype or flag, a negative stride, or a misaligned pointer";
+    case kErrInvalid: return "MCC1D_ERR_PARAM_INVALID: unsupported dtype or flag, a negative stride, a misaligned pointer, or (mcc1d_ssm.h) an output that overlaps an input or another output";
     case kErrShape: return "MCC1D_ERR_INNER_TILING_ERROR: shape outside B 1..32, B*S 1..524288, H 384..24576 (H%64==0), W==3 (mcc1d_ssm.h: outside that header's limits)";
     case kErrWorkspace: return "MCC1D_ERR_WORKSPACE: workspace smaller than the _workspace_size call reported";
     case kErrCuda: return "MCC1D_ERR_CUDA: a CUDA runtime call failed";

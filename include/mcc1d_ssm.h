@@ -46,7 +46,7 @@
  *    updates cache row b.
  *  - Pointers are DEVICE pointers owned by the caller. Tensors may have the
  *    alignment of their element; aligned rows move faster. Outputs must not
- *    overlap inputs or each other (except the in-place `state`). The library
+ *    overlap inputs or each other (a step's `state` is both). The library
  *    allocates nothing and keeps nothing between calls; what a call needs is
  *    in `workspace` (256-byte aligned is best, 16 required), sized by the
  *    *_workspace_size call, whose contents on entry are ignored.
@@ -58,7 +58,8 @@
  *
  * Errors (nothing is enqueued): MCC1D_ERR_PARAM_NULLPTR for a null descriptor
  * or a required null pointer; MCC1D_ERR_PARAM_INVALID for a dtype, flag,
- * negative stride or an element-misaligned pointer;
+ * negative stride, an element-misaligned pointer, or an output (or the
+ * workspace) that overlaps an input or another output;
  * MCC1D_ERR_INNER_TILING_ERROR for a shape outside the limits;
  * MCC1D_ERR_WORKSPACE for a workspace below the reported size;
  * MCC1D_ERR_DEVICE as in mcc1d.h; MCC1D_ERR_CUDA if a launch failed.

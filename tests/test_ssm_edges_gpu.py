@@ -140,3 +140,24 @@ def test_empty_states_stay_empty_in_chunks_of_several_tiles():
     got = m.selective_scan_backward(gy, *args, delta_softplus=True)
     for k, want in zip(cut, torch.autograd.grad((ry * gy[first:].double()).sum(), [leaves[k] for k in cut])):
         ref.check(getattr(got, k)[first:], want, {"B": H + S, "C": H + S}.get(k, 4 * N + S), k)
+
+
+def test_given_outputs():
+    """On an input they are refused; beside one, in the same buffer, they are not."""
+    S, B, H, W = 20, 2, 64, 4
+    two = torch.cat([rand(1, S, B, H, seed=1), torch.zeros(1, S, B, H, dtype=BF16, device="cuda")])
+    x, y, w, win = two[0], two[1], rand(W, H, seed=2), rand(B, W - 1, H, seed=3)
+    want = m.short_conv(x, w)
+    for bad in (x, two.view(-1)[H:H + S * B * H].view(S, B, H)):
+        with pytest.raises(m.Mcc1dError):
+            m.short_conv(x, w, y=bad)
+    assert m.short_conv(x, w, y=y) is y and torch.equal(y, want)
+    with pytest.raises(m.Mcc1dError):
+        m.short_conv_step(x[0], win, w, y=x[0])
+    with pytest.raises(m.Mcc1dError):
+        m.short_conv_step(x[0], win, w, y=win[0, :B])
+    t, _ = scan_inputs(S, B, H, 16, 1, BF16, "Dzbp", "dense", None)
+    for k in ("u", "delta", "z"):
+        with pytest.raises(m.Mcc1dError):
+            m.selective_scan(*[t[k] for k in SCAN_ARGS], delta_softplus=True, y=t[k])
+    assert torch.equal(x, two[0]) and torch.equal(m.short_conv(x, w), want)
