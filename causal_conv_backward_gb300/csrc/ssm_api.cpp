@@ -252,9 +252,6 @@ int32_t check(const mcc1d_scan_args *a, bool out)
         return kErrInvalid;
     if (!shape_ok(a->S, a->B, a->H) || !states_ok(a->B, a->H, a->N, a->G))
         return kErrShape;
-    // a backward thread owns one value of the group sums over [S,B,G,2N]
-    if ((double)a->S * (double)a->B * (double)a->G * 128.0 > (double)(kMaxGrid / 2) * 256.0)
-        return kErrShape;
     if (!strides_ok(a->u_strides) || !strides_ok(a->delta_strides) || (a->z && !strides_ok(a->z_strides)) ||
         !strides_ok(a->B_strides) || !strides_ok(a->C_strides) ||
         !on2({a->u, a->delta, a->z, a->B_, a->C, out ? a->y : nullptr}) ||
@@ -276,6 +273,10 @@ int32_t check(const mcc1d_scan_bwd_args *a)
         return kErrNull;
     if ((a->grad_z && !a->fwd.z) || (a->grad_D && !a->fwd.D) || (a->grad_delta_bias && !a->fwd.delta_bias))
         return kErrNull;
+    // a thread, of 256 to a block, owns one value of the group sums over [S,B,G] of two padded rows of states
+    const mcc1d_scan_args &f = a->fwd;
+    if ((double)f.S * (double)f.B * (double)f.G * (2.0 * scan_bwd_plan(*a).np) > (double)(kMaxGrid / 2) * 256.0)
+        return kErrShape;
     if (!strides_ok(a->grad_y_strides) ||
         !on2({a->grad_y, a->grad_u, a->grad_delta, a->grad_z, a->grad_B, a->grad_C}) ||
         !on4({a->grad_final_state, a->grad_A, a->grad_D, a->grad_delta_bias, a->grad_state}))

@@ -54,7 +54,8 @@
  *    without waiting. Results are deterministic: no floating-point atomics,
  *    every sum in an order that depends on the shape only.
  *  - Limits: 1 <= S <= 2^31 - 4096, 1 <= B <= 65535, 1 <= H <= 2^20,
- *    H % G == 0, and B*H*N and a grid's blocks below 2^31.
+ *    H % G == 0, and B*H*N and a grid's blocks below 2^31 (the backward's
+ *    sums: S*B*G times N, padded to 4 times a power of two, below 2^37).
  *
  * Errors (nothing is enqueued): MCC1D_ERR_PARAM_NULLPTR for a null descriptor
  * or a required null pointer; MCC1D_ERR_PARAM_INVALID for a dtype, flag,

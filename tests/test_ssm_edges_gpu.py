@@ -161,3 +161,18 @@ def test_given_outputs():
         with pytest.raises(m.Mcc1dError):
             m.selective_scan(*[t[k] for k in SCAN_ARGS], delta_softplus=True, y=t[k])
     assert torch.equal(x, two[0]) and torch.equal(m.short_conv(x, w), want)
+
+
+def test_scan_of_more_than_2_31_group_rows():
+    """One channel per group, S B G above 2^31; inputs constant over time, so
+    that the last tokens are at the fixed point of h = a h + dt u B."""
+    S, H = (1 << 19) + 3, 4096
+    u, delta, Bm, Cm = rand(1, 1, H, seed=1), rand(1, 1, H, scale=0.5, seed=2), rand(1, 1, H, 1, seed=3), rand(1, 1, H, 1, seed=4)
+    A = -1 - rand(H, 1, dtype=F32, seed=5).abs()
+    y = torch.empty(S, 1, H, dtype=BF16, device="cuda")
+    m.selective_scan(u.expand(S, 1, H), delta.expand(S, 1, H), A, Bm.expand(S, 1, H, 1), Cm.expand(S, 1, H, 1), delta_softplus=True, y=y)
+    dt = torch.logaddexp(delta.double(), torch.zeros_like(delta).double())
+    a, b, c = torch.exp(dt * A[:, 0].double()), dt * u.double() * Bm[..., 0].double(), Cm[..., 0].double()
+    t = torch.arange(1, 41, device="cuda").double().view(-1, 1, 1)
+    ref.check(y[:40], (1 - a ** t) / (1 - a) * b * c, 40, "first tokens")
+    ref.check(y[-40:], (b / (1 - a) * c).expand(40, 1, H), 40, "last tokens")
