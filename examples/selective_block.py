@@ -12,6 +12,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -25,6 +26,7 @@ class ShortConv(torch.autograd.Function):
         return mcc.short_conv(x, weight, bias)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         g = mcc.short_conv_backward(grad_y.contiguous(), *ctx.saved_tensors)
         return g.x, g.weight, g.bias
@@ -37,6 +39,7 @@ class SelectiveScan(torch.autograd.Function):
         return mcc.selective_scan(u, delta, A, B, C, D, z, delta_bias, delta_softplus=True)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         g = mcc.selective_scan_backward(grad_y.contiguous(), *ctx.saved_tensors, delta_softplus=True)
         return g.u, g.delta, g.A, g.B, g.C, g.D, g.z, g.delta_bias
