@@ -1,6 +1,11 @@
 """The short convolution and the selective scan on torch tensors: argument
 checks and marshalling over the C ABI of ``include/mcc1d_ssm.h``.
 
+Like ``forward`` and ``backward`` of the masked convolution, the calls record
+nothing for autograd: results do not require a gradient, whatever the inputs
+do, and gradients come from the ``_backward`` calls.
+``examples/selective_block.py`` puts the pairs into ``autograd.Function``s.
+
 ``stream`` (a torch stream or its handle) takes a call off the current stream.
 The caller orders it after what made the inputs, and later users of the results
 after it; memory is not reused before both streams are done with it."""
