@@ -106,12 +106,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
             }
         }
         // row r gives dpre(r) and, W-1 rows later than its own, grad_x(r-W+1)
-        const int64_t stop = t1 < len ? t1 : len;      // past the run's tokens
-        const int64_t rend = stop + W - 1;
+        const int64_t rend = t1 + W - 1;
+        const int64_t live = rend < len ? rend : len;
         const int64_t first = t0 == 0 ? -(int64_t)(W - 1) : t0;   // first row of grad_x (below 0: the window's)
-        // One row: its x and grad_y; `own`: one of the run's tokens, so counted in the sums (a row past the length
-        // must not be: zero times an infinite x of the window is NaN); `in`: before the length; gf: the final
-        // window's gradient where row r-W+1 of grad_x is in it. Returns grad_x(r-W+1).
+        // One row: its x and grad_y, `own`: in this run of rows, so counted in the sums; `in`: before the
+        // length; gf: the final window's gradient where row r-W+1 of grad_x is in it. Returns grad_x(r-W+1).
         auto row = [&](const Vec<V> &rx, const Vec<V> &rg, const Vec<V> &gf, bool own, bool in) {
             Vec<V> out;
 #pragma unroll
@@ -127,8 +126,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
                     // d/ds [s g(s)] = g (1 + s (1 - g)), g the sigmoid
                     const float2 g = sigmoid2(s), one = make_float2(1.f, 1.f);
                     d = mul2(d, mul2(g, fma2(s, fma2(g, make_float2(-1.f, -1.f), one), one)));
-                    if (!in)
-                        d = make_float2(0.f, 0.f);   // an infinite pre leaves nothing behind
+                }
+                if (!in) {   // an infinite pre, or an infinite x before it, leaves nothing behind
+                    d = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k)
+                        xw[k][e] = make_float2(0.f, 0.f);
                 }
                 if (own) {
 #pragma unroll
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
 #pragma unroll
                 for (int i = 0; i < kEdge; ++i) {
                     const int64_t q = r + i, t = q - (W - 1);
-                    const bool in = q < len && q < end;
+                    const bool in = q < live && q < end;
                     ex[i] = in ? vload<V>(x + q * p.xs) : vzero<V>();
                     eg[i] = in ? vload<V>(gy + q * p.gs) : vzero<V>();
                     gf[i] = vzero<V>();
@@ -173,11 +176,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
                     const int64_t q = r + i, t = q - (W - 1);
                     if (q >= end)
                         break;
-                    const Vec<V> out = row(ex[i], eg[i], gf[i], q < stop, q < len);
+                    const Vec<V> out = row(ex[i], eg[i], gf[i], q < t1, q < live);
                     if (t < first)
                         continue;
                     if (t >= 0)
-                        vstore<V>(gx + t * ys, out);
+                        vstore<V>(gx + t * ys, t < len ? out : vzero<V>());   // whatever the weights are
                     else if (p.gstate)
                         vstore<V>(p.gstate + (b * (W - 1) + t + W - 1) * p.H + h, out);
                 }
@@ -187,6 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
         // batches of rows
         int64_t r = t0 + W - 1 < rend ? t0 + W - 1 : rend;
         edges(t0, r);
+        const int64_t stop = t1 < len ? t1 : len;
         int64_t left = stop - r;
         uint16_t *to = gx + (r - (W - 1)) * ys;
         Ring ring;
@@ -207,8 +211,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvB
                 vstore<V>(to, row(in[2 * i], in[2 * i + 1], vzero<V>(), true, true));
         }
         edges(r, rend);
-        for (int64_t t = t0 > len ? t0 : len; t < t1; ++t)
-            vstore<V>(gx + t * ys, vzero<V>());
     }
     __syncthreads();
 #pragma unroll
