@@ -11,10 +11,12 @@
 // The weight sums stay in registers over the L rows, are added over the
 // block's 8 warps in shared memory and over blocks by a second kernel, each in
 // a fixed order: nothing depends on scheduling. 6 bytes per element move: bf16,
-// W = 4, 8192 x 8 x 4096 takes 288 us (0.83 of the measured copy bandwidth; 779
+// W = 4, 8192 x 8 x 4096 takes 289 us (0.82 of the measured copy bandwidth; 779
 // with plain loads, 371 with runs of 64 rows, 312 with the activation tested
-// per row), 4096 x 8 x 2048 88 us (0.67). What is left over memory's time is
-// instructions (21 per element) at two blocks of 128 registers per SM.
+// per row), 4096 x 8 x 2048 89 us (0.67), with W = 8 152. What is left over
+// memory's time is instructions (21 per element) at two blocks of 128 registers
+// per SM; at the smaller size it is first of all the 256 blocks, two on 104 of
+// the SMs and one on 48.
 #include "plan.h"
 #include "ssm.h"
 #include "ssm_common.cuh"
@@ -39,8 +41,8 @@ struct ConvBwdParams {
 
 // SILU: with the activation. Single channels (V = 1) take it from p.silu: there
 // the branch keeps the next rows' loads ahead of the arithmetic (odd rows,
-// 4096 x 8 x 2047: 212 us against 258), elsewhere it keeps rows from
-// interleaving.
+// 4096 x 8 x 2047: 212 us against 258 when the two were compared, 214 now),
+// elsewhere it keeps rows from interleaving.
 template <int DT, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kWarps * 32, 2) mcc1d_ssm_conv_bwd(const ConvBwdParams p)
 {
@@ -297,10 +299,12 @@ ConvBwdPlan conv_bwd_plan(const mcc1d_short_conv_bwd_args &a)
 {
     ConvBwdPlan p;
     // Every run of rows begins and ends with rows that go one by one: 64 rows per
-    // warp cost 371 us on 8192 x 8 x 4096, 128 334, 256 311 and 512 338 (measured
-    // before the last two changes to the rows' loop). Fewer
-    // rows where that leaves less than a block per SM (at two blocks per SM
-    // 4096 x 2 x 2048 took 41 us, at one 36)
+    // warp cost 342 us on 8192 x 8 x 4096, 128 310, 256 289 and 512 314. Fewer
+    // rows where that leaves less than a block per SM: 4096 x 2 x 2048 takes 33 us
+    // with 64 rows (256 blocks), 35 with 128 (128 blocks), 56 with 256. Between
+    // one block per SM and two, SMs hold unequal numbers of them and shorter runs
+    // do not pay for that: 4096 x 8 x 2048 takes 89 us with 256 rows (256 blocks)
+    // and 95 with 128.
     const int64_t wide = (a.H + 127) / 128 * a.B;
     int64_t L = 256;
     while (L > 8 && wide * ((a.S + 8 * L - 1) / (8 * L)) < 152)

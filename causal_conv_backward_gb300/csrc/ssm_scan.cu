@@ -13,7 +13,7 @@
 // thousand channels without cutting the sequence. Measured, bf16, N = 16:
 // 690 us on 1024 x 32 x 4096 (48 cycles per 128 steps, issuing on 64 % of
 // cycles), 418 us on 4096 x 8 x 2048 (512 blocks on 152 SMs: four on some and
-// three on others), 461 us on 131072 x 1 x 384 (cut in chunks).
+// three on others), 463 us on 131072 x 1 x 384 (cut in chunks).
 //
 // Where sequences and channels are too few to fill the machine the time axis
 // is cut into chunks: each chunk's state from a zero start and its sum of dt
@@ -576,11 +576,16 @@ void tile_shape(int nl, int &cb, int &tt)
 }
 
 // Cuts the time axis into at most `most` chunks. The machine holds kSlots
-// blocks at once, and a chunk costs about kChunkTiles tiles besides its own
-// (setup, the join): the fewest waves of the fewest tiles, of more than
-// `waves_above` waves where that can be had. (The backward's two passes hold
-// different numbers of blocks, so two waves of one are ragged in the other:
-// 1024 x 8 x 2048 took 523 us in 512 blocks a pass and 453 in 1792.)
+// blocks at once (four per SM; the backward's first pass three), and a chunk
+// costs about kChunkTiles tiles besides its own (setup, the join): the fewest
+// waves of the fewest tiles, of more than `waves_above` waves where that can be
+// had. The backward asks for more than two, since its passes hold different
+// numbers of blocks and two waves of one are ragged in the other: 1024 x 8 x
+// 2048 takes 503 us in 512 blocks a pass, 434 in 1024 and 429 in the 1792 that
+// it gets. Where `most` chunks make no more than two waves they are taken
+// without comparing costs: 509 x 2 x 768 takes 39 us in 32 chunks, 42 in 16 and
+// 64 in 8. In between the rule can miss: 2048 x 2 x 1024 takes 127 us in the
+// 43 chunks that it gets and 124 in 32.
 void cut(ScanPlan &p, int64_t rows, int64_t most, int64_t waves_above)
 {
     constexpr int64_t kSlots = 152 * 4, kChunkTiles = 2;

@@ -25,9 +25,10 @@
 // pass and 114 in this one, of which 63 are the run back (16 of them its sums
 // over a channel's lanes, 7 those over a warp's channels) and 9 the run
 // forward. Four blocks of 128 registers per SM beat three of 168 (4096 x 8 x
-// 2048: 1706 against 1771 us), which is why the tile's rows are read again at
+// 2048: 1608 against 1632 us), which is why the tile's rows are read again at
 // its end and the warps' sums take the place of the states they have used.
-// bf16, N = 16: 812 us on 2048 x 8 x 2048, 3105 on 1024 x 32 x 4096.
+// bf16, N = 16: 813 us on 2048 x 8 x 2048, 3095 on 1024 x 32 x 4096; N = 4, 8
+// and 32 on 2048 x 8 x 2048: 445, 539 and 1491.
 #include "plan.h"
 #include "ssm_scan.cuh"
 
