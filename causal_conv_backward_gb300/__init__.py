@@ -24,3 +24,7 @@ from ._ssm import (  # noqa: F401
     ShortConvStepArgs, selective_scan, selective_scan_backward, selective_scan_step, short_conv,
     short_conv_backward, short_conv_step,
 )
+from ._norm import (  # noqa: F401
+    GatedNormArgs, GatedNormBwdArgs, GatedNormGrads, ResidualNormArgs, ResidualNormBwdArgs, ResidualNormGrads,
+    gated_norm, gated_norm_backward, residual_norm, residual_norm_backward,
+)

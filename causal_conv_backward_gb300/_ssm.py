@@ -67,6 +67,8 @@ def _packer(cls):
                 out += codes(kind)
             elif kind is _vp:
                 out += "P"
+            elif kind is ctypes.c_double:
+                out += "d"
             else:
                 n = getattr(kind, "_length_", 1)
                 out += ("q" if ctypes.sizeof(kind) // n == 8 else "i") * n

@@ -1,0 +1,271 @@
+// norm_common.cuh - rows of values spread over threads: addresses, loads,
+// sums, and the choice of threads per row.
+//
+// All four kernels move each input and output once and do some ten operations
+// a value, so HBM bounds them: a row stays in registers from its load to its
+// store, and threads hold 16-byte vectors, E values each.
+#pragma once
+
+#include "norm.h"
+#include "ssm_common.cuh"
+
+namespace mcc1d {
+
+// r / d and r % d for r < 2^31 by one multiplication: with l = ceil(log2 d) and
+// m = floor(2^(31+l) / d) + 1, floor(r m / 2^(31+l)) is the quotient (the excess
+// r (m d - 2^(31+l)) / (d 2^(31+l)) is at most r / 2^(31+l) <= 1/d' for d' >= d).
+struct Divisor {
+    uint32_t d;
+    uint32_t shift;
+    uint64_t m;
+    Divisor() = default;
+    explicit Divisor(int64_t by) : d((uint32_t)by)
+    {
+        uint32_t l = 0;
+        while (((uint64_t)1 << l) < d)
+            ++l;
+        shift = 31 + l;
+        m = ((uint64_t)1 << shift) / d + 1;
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t r) const { return (uint32_t)((r * m) >> shift); }
+};
+
+// The address of row r = (s B + b) H + h of a tensor with these strides.
+struct RowAddress {
+    int64_t s, b, h;
+};
+struct RowOrder {
+    Divisor B, H;
+    __device__ __forceinline__ int64_t at(const RowAddress &a, uint32_t r) const
+    {
+        const uint32_t q = H.quotient(r), s = B.quotient(q);
+        return s * a.s + (q - s * B.d) * a.b + (r - q * H.d) * a.h;
+    }
+};
+
+// A row of up to V x NV x TPR values over TPR threads: vector j of thread t
+// starts at value (j TPR + t) V.
+template <int V_, int NV_, int TPR_>
+struct RowShape {
+    static constexpr int V = V_, NV = NV_, TPR = TPR_, E = V_ * NV_;
+    static constexpr int THREADS = TPR_ > 32 ? TPR_ : 256, ROWS = THREADS / TPR_;
+};
+
+template <class R>
+__device__ __forceinline__ int thread_of_row() { return threadIdx.x % R::TPR; }
+
+// ------------------------------------------------------------------ loads and stores
+// 16-bit values of type DT (0, 1), or fp32 (2); zero past the row's end.
+template <int DT>
+struct Element {
+    typedef uint16_t type;
+};
+template <>
+struct Element<2> {
+    typedef float type;
+};
+
+// One thread's share of a row as it came from memory.
+template <int DT, class R>
+struct Share {
+    static constexpr int WORDS = R::V == 1 ? 1 : (DT == 2 ? 8 : 4);
+    uint32_t u[R::NV * WORDS];
+};
+
+template <int DT, class R>
+__device__ __forceinline__ Share<DT, R> load_share(const void *base, int64_t at, int D)
+{
+    Share<DT, R> r;
+    const typename Element<DT>::type *p = static_cast<const typename Element<DT>::type *>(base) + at;
+    constexpr int W = Share<DT, R>::WORDS;
+#pragma unroll
+    for (int j = 0; j < R::NV; ++j) {
+        const int i = (j * R::TPR + thread_of_row<R>()) * R::V;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            r.u[j * W + w] = 0u;
+        if (i < D) {
+            if constexpr (R::V == 1 && DT == 2) {
+                r.u[j] = __float_as_uint(__ldg(p + i));
+            } else if constexpr (R::V == 1) {
+                r.u[j] = __ldg(p + i);
+            } else {
+#pragma unroll
+                for (int w = 0; w < W; w += 4) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + i) + w / 4);
+                    r.u[j * W + w] = v.x, r.u[j * W + w + 1] = v.y, r.u[j * W + w + 2] = v.z, r.u[j * W + w + 3] = v.w;
+                }
+            }
+        }
+    }
+    return r;
+}
+
+template <int DT, class R>
+__device__ __forceinline__ void values(const Share<DT, R> &r, float (&x)[R::E])
+{
+    constexpr int W = Share<DT, R>::WORDS;
+#pragma unroll
+    for (int j = 0; j < R::NV; ++j) {
+        if constexpr (DT == 2) {
+#pragma unroll
+            for (int e = 0; e < R::V; ++e)
+                x[j * R::V + e] = __uint_as_float(r.u[j * W + e]);
+        } else if constexpr (R::V == 1) {
+            x[j] = unpack2<DT>(r.u[j]).x;
+        } else {
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float2 v = unpack2<DT>(r.u[j * W + w]);
+                x[j * R::V + 2 * w] = v.x, x[j * R::V + 2 * w + 1] = v.y;
+            }
+        }
+    }
+}
+
+template <int DT, class R>
+__device__ __forceinline__ void load_values(const void *base, int64_t at, int D, float (&x)[R::E])
+{
+    values<DT, R>(load_share<DT, R>(base, at, D), x);
+}
+
+template <int DT, class R>
+__device__ __forceinline__ void store_values(void *base, int64_t at, int D, const float (&x)[R::E])
+{
+    typename Element<DT>::type *p = static_cast<typename Element<DT>::type *>(base) + at;
+#pragma unroll
+    for (int j = 0; j < R::NV; ++j) {
+        const int i = (j * R::TPR + thread_of_row<R>()) * R::V;
+        if (i >= D)
+            continue;
+        const float *v = x + j * R::V;
+        if constexpr (R::V == 1 && DT == 2) {
+            p[i] = v[0];
+        } else if constexpr (R::V == 1) {
+            p[i] = (uint16_t)pack2<DT>(make_float2(v[0], 0.f));
+        } else if constexpr (DT == 2) {
+            float4 *q = reinterpret_cast<float4 *>(p + i);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(p + i) = make_uint4(pack2<DT>(make_float2(v[0], v[1])), pack2<DT>(make_float2(v[2], v[3])),
+                                                           pack2<DT>(make_float2(v[4], v[5])), pack2<DT>(make_float2(v[6], v[7])));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ sums over a row
+// N sums over the threads of a row, the same for each of them. `turn` flips
+// between calls, so that one barrier a call is enough.
+template <class R, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*shared)[2][3][16], int &turn)
+{
+#pragma unroll
+    for (int d = (R::TPR < 32 ? R::TPR : 32) / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], d);
+    if constexpr (R::TPR > 32) {
+        constexpr int WARPS = R::TPR / 32;
+        if (threadIdx.x % 32 == 0)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                (*shared)[turn][k][threadIdx.x / 32] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                s += (*shared)[turn][k][w];
+            v[k] = s;
+        }
+        turn ^= 1;
+    }
+}
+
+// 1 / sqrt(v), to the last bits: the instruction's result and one Newton step
+// (not at 0 and infinity, where the step would make NaN of them).
+__device__ __forceinline__ float inverse_root(float v)
+{
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    if (r > 0.f && r < INFINITY)
+        r = r * fmaf(-0.5f * v * r, r, 1.5f);
+    return r;
+}
+
+// ------------------------------------------------------------------ which threads
+// Threads for rows of D values: up to 1024 a warp or less, so that sums need
+// shuffles only; above, a block. Rows that cannot be read in 16-byte vectors
+// are read value by value.
+template <class F>
+int32_t with_row_shape(int64_t D, bool vectors, F &&f)
+{
+    if (vectors) {
+        if (D <= 64)
+            return f(RowShape<8, 1, 8>());
+        if (D <= 128)
+            return f(RowShape<8, 1, 16>());
+        if (D <= 256)
+            return f(RowShape<8, 1, 32>());
+        if (D <= 1024)
+            return f(RowShape<8, 4, 32>());
+        if (D <= 2048)
+            return f(RowShape<8, 2, 128>());
+        if (D <= 4096)
+            return f(RowShape<8, 2, 256>());
+        return f(RowShape<8, 4, 512>());
+    }
+    if (D <= 128)
+        return f(RowShape<1, 4, 32>());
+    if (D <= 512)
+        return f(RowShape<1, 16, 32>());
+    if (D <= 2048)
+        return f(RowShape<1, 16, 128>());
+    return f(RowShape<1, 32, 512>());
+}
+
+// Whether rows of D values can be read in vectors of eight: addresses (or'd) on
+// 16 bytes, steps in elements (or'd) and the row itself multiples of eight.
+inline bool vectors_for(int64_t D, uintptr_t addresses, int64_t steps)
+{
+    return D % 8 == 0 && (addresses & 15u) == 0 && (steps & 7) == 0;
+}
+
+// ------------------------------------------------------------------ sums over rows
+// Each thread's sums over its rows, joined over the block's rows of threads and
+// written to part [blocks][D]: one barrier per use of `shared`.
+template <class R>
+__device__ __forceinline__ void store_part(const float (&x)[R::E], float *part, int D, float (*shared)[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1])
+{
+    float sum[R::E];
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+        sum[e] = x[e];
+    if constexpr (R::ROWS > 1) {
+        __syncthreads();
+        const int row = threadIdx.x / R::TPR, t = thread_of_row<R>();
+#pragma unroll
+        for (int e = 0; e < R::E; ++e)
+            (*shared)[(row * R::E + e) * R::TPR + t] = x[e];
+        __syncthreads();
+        if (row > 0)
+            return;
+        for (int k = 1; k < R::ROWS; ++k)
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                sum[e] += (*shared)[(k * R::E + e) * R::TPR + t];
+    }
+    float *to = part + (int64_t)blockIdx.x * D;
+#pragma unroll
+    for (int j = 0; j < R::NV; ++j)
+#pragma unroll
+        for (int e = 0; e < R::V; ++e) {
+            const int i = (j * R::TPR + thread_of_row<R>()) * R::V + e;
+            if (i < D)
+                to[i] = sum[j * R::V + e];
+        }
+}
+
+}  // namespace mcc1d

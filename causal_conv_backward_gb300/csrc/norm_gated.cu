@@ -1,0 +1,235 @@
+// norm_gated.cu - the gated norm and its gradients, and the sums over rows of
+// both norms' weights.
+#include <algorithm>
+
+#include "norm_common.cuh"
+
+namespace mcc1d {
+
+namespace {
+
+struct GatedParams {
+    const void *x, *z, *weight, *grad_y;
+    void *y, *grad_x, *grad_z;
+    float *part;
+    RowAddress xs, zs, gs;
+    RowOrder order;
+    uint32_t rows;
+    int32_t D;
+    float eps, inv_D;
+};
+
+template <int DT, class R>
+__global__ void __launch_bounds__(R::THREADS) gated_norm_kernel(const __grid_constant__ GatedParams p)
+{
+    __shared__ float shared[2][3][16];
+    int turn = 0;
+    const uint32_t row = blockIdx.x * R::ROWS + threadIdx.x / R::TPR;
+    const bool there = row < p.rows;
+    const uint32_t r = there ? row : p.rows - 1;
+    float x[R::E], w[R::E], z[R::E];
+    const auto xr = load_share<DT, R>(p.x, p.order.at(p.xs, r), p.D);
+    Share<DT, R> zr;
+    if (p.z)
+        zr = load_share<DT, R>(p.z, p.order.at(p.zs, r), p.D);
+    load_values<DT, R>(p.weight, 0, p.D, w);
+    values<DT, R>(xr, x);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+        s[0] = fmaf(x[e], x[e], s[0]);
+    row_sums<R>(s, &shared, turn);
+    const float rms = inverse_root(fmaf(s[0], p.inv_D, p.eps));
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+        x[e] = x[e] * rms * w[e];
+    if (p.z) {
+        values<DT, R>(zr, z);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e)
+            x[e] *= z[e] * sigmoid(z[e]);
+    }
+    if (there)
+        store_values<DT, R>(p.y, (int64_t)row * p.D, p.D, x);
+}
+
+// With n = x r, r = 1/rms(x), g = grad_y silu(z):
+//   grad_weight = sum of g n over the rows,  grad_z = grad_y n weight silu'(z),
+//   grad_x = r (g weight - n mean(g weight n))
+template <int DT, class R>
+__global__ void __launch_bounds__(R::THREADS) gated_norm_bwd_kernel(const __grid_constant__ GatedParams p)
+{
+    __shared__ float shared[2][3][16];
+    __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
+    int turn = 0;
+    float w[R::E], gw[R::E];
+    load_values<DT, R>(p.weight, 0, p.D, w);
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+        gw[e] = 0.f;
+    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += gridDim.x * R::ROWS) {
+        const uint32_t row = first + threadIdx.x / R::TPR;
+        const bool there = row < p.rows;
+        const uint32_t r = there ? row : p.rows - 1;
+        float x[R::E], g[R::E];
+        Share<DT, R> zr;
+        const auto xr = load_share<DT, R>(p.x, p.order.at(p.xs, r), p.D);
+        const auto gr = load_share<DT, R>(p.grad_y, p.order.at(p.gs, r), p.D);
+        if (p.z)
+            zr = load_share<DT, R>(p.z, p.order.at(p.zs, r), p.D);
+        values<DT, R>(xr, x);
+        float s[2] = {0.f, 0.f};
+        if (p.z) {
+            float z[R::E];
+            values<DT, R>(zr, z);
+            values<DT, R>(gr, g);
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                g[e] *= z[e] * sigmoid(z[e]);
+        } else {
+            values<DT, R>(gr, g);
+        }
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            s[0] = fmaf(x[e], x[e], s[0]);
+            s[1] = fmaf(g[e] * w[e], x[e], s[1]);
+        }
+        row_sums<R>(s, &shared, turn);
+        const float rms = inverse_root(fmaf(s[0], p.inv_D, p.eps));
+        const float along = s[1] * p.inv_D * rms;      // mean(g weight n)
+        if (there) {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                const float n = x[e] * rms;
+                gw[e] = fmaf(g[e], n, gw[e]);
+                g[e] = rms * fmaf(-n, along, g[e] * w[e]);
+                x[e] = n;
+            }
+            store_values<DT, R>(p.grad_x, (int64_t)row * p.D, p.D, g);
+            if (p.grad_z) {
+                float z[R::E];
+                values<DT, R>(zr, z);
+                values<DT, R>(gr, g);
+#pragma unroll
+                for (int e = 0; e < R::E; ++e) {
+                    const float sig = sigmoid(z[e]);
+                    g[e] *= x[e] * w[e] * sig * fmaf(z[e], 1.f - sig, 1.f);
+                }
+                store_values<DT, R>(p.grad_z, (int64_t)row * p.D, p.D, g);
+            }
+        }
+    }
+    store_part<R>(gw, p.part, p.D, &joined);
+}
+
+// out[c] = sum of part[p][c]: 32 columns to a block of 8 warps, each warp its
+// share of the parts, the warps' sums joined in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const __grid_constant__ ColumnSums s, int32_t parts, int32_t columns)
+{
+    __shared__ float joined[8][32];
+    previous_done();
+    if (!s.out[blockIdx.y])
+        return;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (c < columns) {
+        const float *part = s.part[blockIdx.y] + c;
+        int p = warp;
+        for (; p + 24 < parts; p += 32)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                a[k] += part[(int64_t)(p + 8 * k) * columns];
+        for (; p < parts; p += 8)
+            a[0] += part[(int64_t)p * columns];
+    }
+    joined[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
+    __syncthreads();
+    if (warp > 0 || c >= columns)
+        return;
+    float sum = joined[0][lane];
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+        sum += joined[k][lane];
+    if (s.type[blockIdx.y] == 2)
+        static_cast<float *>(s.out[blockIdx.y])[c] = sum;
+    else
+        static_cast<uint16_t *>(s.out[blockIdx.y])[c] =
+            (uint16_t)(s.type[blockIdx.y] == 0 ? pack2<0>(make_float2(sum, 0.f)) : pack2<1>(make_float2(sum, 0.f)));
+}
+
+GatedParams gated_params(const mcc1d_gated_norm_args &a)
+{
+    GatedParams p = {};
+    p.x = a.x, p.z = a.z, p.weight = a.weight, p.y = a.y;
+    p.xs = {a.x_strides[0], a.x_strides[1], a.x_strides[2]};
+    p.zs = {a.z_strides[0], a.z_strides[1], a.z_strides[2]};
+    p.order.B = Divisor(a.B), p.order.H = Divisor(a.H);
+    p.rows = (uint32_t)(a.S * a.B * a.H), p.D = (int32_t)a.D;
+    p.eps = (float)a.eps, p.inv_D = (float)(1.0 / (double)a.D);
+    return p;
+}
+
+bool vectors(const mcc1d_gated_norm_args &a, uintptr_t more, int64_t more_steps)
+{
+    const int64_t zs = a.z ? a.z_strides[0] | a.z_strides[1] | a.z_strides[2] : 0;
+    return vectors_for(a.D, (uintptr_t)a.x | (uintptr_t)a.z | (uintptr_t)a.weight | more,
+                       a.x_strides[0] | a.x_strides[1] | a.x_strides[2] | zs | more_steps);
+}
+
+}  // namespace
+
+// Blocks of a backward over this many rows: two waves of the SMs' threads, so
+// that the partial sums of D columns stay small beside the rows.
+int64_t norm_bwd_blocks(int64_t rows, int64_t columns, bool vec)
+{
+    int64_t blocks = 0;
+    with_row_shape(columns, vec, [&](auto shape) {
+        typedef decltype(shape) R;
+        blocks = std::min<int64_t>((rows + R::ROWS - 1) / R::ROWS, 152 * (1024 / R::THREADS));
+        return 0;
+    });
+    return blocks;
+}
+
+bool gated_norm_vectors(const mcc1d_gated_norm_bwd_args &a)
+{
+    return vectors(a.fwd, (uintptr_t)a.grad_y | (uintptr_t)a.grad_x | (uintptr_t)a.grad_z,
+                   a.grad_y_strides[0] | a.grad_y_strides[1] | a.grad_y_strides[2]);
+}
+
+int32_t launch_gated_norm(const mcc1d_gated_norm_args &a, cudaStream_t stream)
+{
+    const GatedParams p = gated_params(a);
+    return with_row_shape(a.D, vectors(a, (uintptr_t)a.y, 0), [&](auto shape) {
+        typedef decltype(shape) R;
+        const dim3 grid((unsigned)((p.rows + R::ROWS - 1) / R::ROWS));
+        return a.dtype == 0 ? launch(gated_norm_kernel<0, R>, grid, R::THREADS, 0, stream, p)
+                            : launch(gated_norm_kernel<1, R>, grid, R::THREADS, 0, stream, p);
+    });
+}
+
+int32_t launch_gated_norm_bwd(const mcc1d_gated_norm_bwd_args &a, float *workspace, cudaStream_t stream)
+{
+    GatedParams p = gated_params(a.fwd);
+    p.grad_y = a.grad_y, p.grad_x = a.grad_x, p.grad_z = a.grad_z, p.part = workspace;
+    p.gs = {a.grad_y_strides[0], a.grad_y_strides[1], a.grad_y_strides[2]};
+    const bool vec = gated_norm_vectors(a);
+    const int64_t blocks = norm_bwd_blocks(p.rows, a.fwd.D, vec);
+    const int32_t st = with_row_shape(a.fwd.D, vec, [&](auto shape) {
+        typedef decltype(shape) R;
+        return a.fwd.dtype == 0 ? launch(gated_norm_bwd_kernel<0, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p)
+                                : launch(gated_norm_bwd_kernel<1, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p);
+    });
+    if (st != kOk)
+        return st;
+    const ColumnSums s = {{workspace}, {a.grad_weight}, {a.fwd.dtype}};
+    return launch_column_sums(s, blocks, a.fwd.D, 1, stream);
+}
+
+int32_t launch_column_sums(const ColumnSums &s, int64_t parts, int64_t columns, int sums, cudaStream_t stream)
+{
+    return launch_as(true, column_sums_kernel, dim3((unsigned)((columns + 31) / 32), (unsigned)sums), 256, 0, stream, s, (int32_t)parts,
+                     (int32_t)columns);
+}
+
+}  // namespace mcc1d

@@ -1,0 +1,137 @@
+// norm_residual_bwd.cu - the residual norm's gradients.
+//
+// With rh = 1/rms(h), q = grad_y weight, the gradient of h is
+//   gh = grad_h + rh (q - h rh^2 mean(q h));
+// it is grad_residual, and through the branch, gm = gh scale, t = gm post_weight:
+//   grad_x = r (t - x r^2 mean(t x)),  or gm without the branch's norm.
+// Sums over the rows: grad_weight of grad_y h rh, grad_scale of gh m,
+// grad_post_weight of gm x r. h is made again from x and the residual, which
+// reads as much as a saved h would and keeps it unrounded.
+#include "norm_residual.cuh"
+
+namespace mcc1d {
+
+namespace {
+
+template <int DT, int RT, class R>
+__global__ void __launch_bounds__(R::THREADS) residual_norm_bwd_kernel(const __grid_constant__ ResidualParams p)
+{
+    __shared__ float shared[2][3][16];
+    __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
+    int turn = 0;
+    float w[R::E], gw[R::E], gs[R::E], gp[R::E];
+    Branch<DT, R> b;
+    b.weights(p);
+    load_values<DT, R>(p.weight, 0, p.D, w);
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+        gw[e] = gs[e] = gp[e] = 0.f;
+    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += gridDim.x * R::ROWS) {
+        const uint32_t row = first + threadIdx.x / R::TPR;
+        const bool there = row < p.rows;
+        const uint32_t at = there ? row : p.rows - 1;
+        float x[R::E], h[R::E], g[R::E];
+        const auto xr = load_share<DT, R>(p.x, p.order.at(p.xs, at), p.D);
+        const auto rr = load_share<RT, R>(p.residual, p.order.at(p.rs, at), p.D);
+        const auto gr = load_share<DT, R>(p.grad_y, p.order.at(p.gs, at), p.D);
+        Share<RT, R> hr;
+        if (p.grad_h)
+            hr = load_share<RT, R>(p.grad_h, p.order.at(p.ghs, at), p.D);
+        values<DT, R>(xr, x);
+        values<RT, R>(rr, h);
+        b.sum(p, x, h, &shared, turn);
+        values<DT, R>(gr, g);
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            s[0] = fmaf(h[e], h[e], s[0]);
+            s[1] = fmaf(g[e] * w[e], h[e], s[1]);
+        }
+        row_sums<R>(s, &shared, turn);
+        const float rh = inverse_root(fmaf(s[0], p.inv_D, p.eps));
+        const float along = s[1] * p.inv_D * rh;
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            const float n = h[e] * rh;
+            if (there)
+                gw[e] = fmaf(g[e], n, gw[e]);
+            g[e] = rh * fmaf(-n, along, g[e] * w[e]);
+        }
+        if (p.grad_h) {
+            float gh[R::E];
+            values<RT, R>(hr, gh);
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                g[e] += gh[e];
+        }
+        if (there)
+            store_values<RT, R>(p.grad_residual, (int64_t)row * p.D, p.D, g);
+        if (p.scale) {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                const float m = p.post_weight ? x[e] * b.r * b.pw[e] : x[e];
+                if (there)
+                    gs[e] = fmaf(g[e], m, gs[e]);
+                g[e] *= b.s[e];
+            }
+        }
+        if (p.post_weight) {
+            float t[1] = {0.f};
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                x[e] *= b.r;
+                if (there)
+                    gp[e] = fmaf(g[e], x[e], gp[e]);
+                g[e] *= b.pw[e];
+                t[0] = fmaf(g[e], x[e], t[0]);
+            }
+            row_sums<R>(t, &shared, turn);
+            const float back = t[0] * p.inv_D;
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                g[e] = b.r * fmaf(-x[e], back, g[e]);
+        }
+        if (there)
+            store_values<DT, R>(p.grad_x, (int64_t)row * p.D, p.D, g);
+    }
+    store_part<R>(gw, p.part, p.D, &joined);
+    if (p.part_post)
+        store_part<R>(gp, p.part_post, p.D, &joined);
+    if (p.part_scale)
+        store_part<R>(gs, p.part_scale, p.D, &joined);
+}
+
+}  // namespace
+
+bool residual_norm_vectors(const mcc1d_residual_norm_bwd_args &a)
+{
+    return residual_vectors(a.fwd, (uintptr_t)a.grad_y | (uintptr_t)a.grad_h | (uintptr_t)a.grad_x | (uintptr_t)a.grad_residual,
+                            a.grad_y_strides[0] | a.grad_y_strides[1] | (a.grad_h ? a.grad_h_strides[0] | a.grad_h_strides[1] : 0));
+}
+
+int32_t launch_residual_norm_bwd(const mcc1d_residual_norm_bwd_args &a, float *workspace, cudaStream_t stream)
+{
+    const mcc1d_residual_norm_args &f = a.fwd;
+    ResidualParams p = residual_params(f);
+    p.grad_y = a.grad_y, p.grad_h = a.grad_h, p.grad_x = a.grad_x, p.grad_residual = a.grad_residual;
+    p.gs = {0, a.grad_y_strides[0], a.grad_y_strides[1]};
+    p.ghs = {0, a.grad_h_strides[0], a.grad_h_strides[1]};
+    const bool vec = residual_norm_vectors(a);
+    const int64_t blocks = norm_bwd_blocks(p.rows, f.H, vec);
+    p.part = workspace;
+    p.part_post = a.grad_post_weight ? workspace + blocks * f.H : nullptr;
+    p.part_scale = a.grad_scale ? workspace + 2 * blocks * f.H : nullptr;
+    const int32_t st = with_row_shape(f.H, vec, [&](auto shape) {
+        typedef decltype(shape) R;
+        const auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)blocks), R::THREADS, 0, stream, p); };
+        if (f.flags & MCC1D_WIDE)
+            return f.dtype == 0 ? go(residual_norm_bwd_kernel<0, 2, R>) : go(residual_norm_bwd_kernel<1, 2, R>);
+        return f.dtype == 0 ? go(residual_norm_bwd_kernel<0, 0, R>) : go(residual_norm_bwd_kernel<1, 1, R>);
+    });
+    if (st != kOk)
+        return st;
+    const ColumnSums s = {{p.part, p.part_post, p.part_scale}, {a.grad_weight, a.grad_post_weight, a.grad_scale}, {f.dtype, f.dtype, 2}};
+    return launch_column_sums(s, blocks, f.H, 3, stream);
+}
+
+}  // namespace mcc1d
