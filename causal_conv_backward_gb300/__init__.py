@@ -28,3 +28,6 @@ from ._norm import (  # noqa: F401
     GatedNormArgs, GatedNormBwdArgs, GatedNormGrads, ResidualNormArgs, ResidualNormBwdArgs, ResidualNormGrads,
     gated_norm, gated_norm_backward, residual_norm, residual_norm_backward,
 )
+from ._delta import (  # noqa: F401
+    DeltaArgs, DeltaBwdArgs, DeltaStepArgs, GatedDeltaGrads, gated_delta, gated_delta_backward, gated_delta_step,
+)

@@ -83,11 +83,11 @@ struct Region {
 private:
     bool meets(uintptr_t lo, uintptr_t hi, int k, uintptr_t from) const
     {
+        if (k >= axes || k >= 3)
+            return from < hi && from + row > lo;
         uint64_t inner = row;       // from an index of axis k to the end of its last row
         for (int j = k + 1; j < axes; ++j)
             inner += (uint64_t)(axis[j].count - 1) * axis[j].step;
-        if (k == axes)
-            return from < hi && from + row > lo;
         if (from >= hi)
             return false;
         const uint64_t first = lo >= from + inner ? (lo - from - inner) / axis[k].step + 1 : 0;

@@ -1,0 +1,65 @@
+// delta_common.cuh - what the gated delta rule's kernels share: parameters,
+// the gates of a token, and vectors of q and k divided by their lengths.
+#pragma once
+
+#include "delta.h"
+#include "norm_common.cuh"
+
+namespace mcc1d {
+
+struct DeltaParams {
+    const uint16_t *q, *k, *v, *delta, *beta, *grad_y;
+    const float *A, *delta_bias, *state, *grad_final;
+    const int32_t *lengths;
+    uint16_t *y, *grad_v;
+    float *final_state, *grad_state;
+    int64_t q_s[3], k_s[3], v_s[3], delta_s[2], beta_s[2], gy_s[3];
+    int64_t S;
+    int32_t B, H, G, K, V;
+    float scale;
+    int32_t flags;
+    // written down for the gradients
+    float *u, *states;
+};
+
+inline DeltaParams delta_params(const mcc1d_delta_args &a)
+{
+    DeltaParams p = {};
+    p.q = static_cast<const uint16_t *>(a.q), p.k = static_cast<const uint16_t *>(a.k), p.v = static_cast<const uint16_t *>(a.v);
+    p.delta = static_cast<const uint16_t *>(a.delta), p.beta = static_cast<const uint16_t *>(a.beta);
+    p.A = a.A, p.delta_bias = a.delta ? a.delta_bias : nullptr, p.state = a.state, p.lengths = a.lengths;
+    p.y = static_cast<uint16_t *>(a.y), p.final_state = a.final_state;
+    for (int i = 0; i < 3; ++i)
+        p.q_s[i] = a.q_strides[i], p.k_s[i] = a.k_strides[i], p.v_s[i] = a.v_strides[i];
+    for (int i = 0; i < 2; ++i)
+        p.delta_s[i] = a.delta_strides[i], p.beta_s[i] = a.beta_strides[i];
+    p.S = a.S, p.B = (int32_t)a.B, p.H = (int32_t)a.H, p.G = (int32_t)a.G, p.K = (int32_t)a.K, p.V = (int32_t)a.V;
+    p.scale = (float)a.scale, p.flags = a.flags;
+    return p;
+}
+
+// One 16-bit value.
+template <int DT>
+__device__ __forceinline__ float value(const uint16_t *p) { return unpack2<DT>(__ldg(p)).x; }
+
+// A token's gates from its raw delta and beta.
+struct Gates {
+    float raw, dt, log2a, b;    // log2 of the decay
+};
+__device__ __forceinline__ Gates gates_of(int flags, bool decays, float delta, float bias, float A, float beta)
+{
+    Gates g;
+    g.raw = delta + bias;
+    g.dt = flags & MCC1D_SOFTPLUS ? softplus(g.raw) : g.raw;
+    g.log2a = decays ? g.dt * (A * kLog2e) : 0.f;
+    g.b = flags & MCC1D_SIGMOID ? sigmoid(beta) : beta;
+    return g;
+}
+
+// What q or k is multiplied by, from its squared length.
+__device__ __forceinline__ float unit_factor(int flags, float squares)
+{
+    return flags & MCC1D_QK_NORM ? inverse_root(squares + (float)kUnitEps) : 1.f;
+}
+
+}  // namespace mcc1d
