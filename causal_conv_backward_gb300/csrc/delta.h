@@ -25,7 +25,24 @@ struct DeltaBwdPlan {
 };
 DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
 
-int32_t launch_delta(const mcc1d_delta_args &a, cudaStream_t stream);
+// What the products of a chunk need beside q, k and v, for each (b, h, chunk):
+// T and P T as fp16 terms in the panels that the tensor cores read, and the
+// factors of its tokens (delta_prepare.cu).
+constexpr int kPanelBytes = kChunk * 128;
+enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
+       kFactorT, kFactors };
+constexpr int kChunkBytes = 4 * kPanelBytes + kFactors * kChunk * 4;
+
+struct DeltaPlan {
+    bool tokens;                           // token by token, no workspace
+    int64_t chunks;                        // ceil(S / kChunk)
+    uint64_t bytes;
+};
+DeltaPlan delta_plan(const mcc1d_delta_args &a);
+
+int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream);
+int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream);
+int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, cudaStream_t stream);
 int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream);
 

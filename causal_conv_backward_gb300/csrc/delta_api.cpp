@@ -33,7 +33,8 @@ int32_t check(const mcc1d_delta_args *a, bool out)
         !strides_ok(a->beta_strides) || !on2({a->q, a->k, a->v, a->delta, a->beta, out ? a->y : nullptr}) ||
         !on4({a->A, a->delta_bias, a->state, a->lengths, out ? a->final_state : nullptr}))
         return kErrInvalid;
-    return kOk;
+    // blocks are chunks of sequences and heads
+    return (double)((a->S + kChunk - 1) / kChunk) * (double)a->B * (double)a->H <= (double)kMaxGrid ? kOk : kErrShape;
 }
 
 int32_t check(const mcc1d_delta_bwd_args *a)
@@ -50,8 +51,7 @@ int32_t check(const mcc1d_delta_bwd_args *a)
     if (!strides_ok(a->grad_y_strides) || !on2({a->grad_y, a->grad_q, a->grad_k, a->grad_v, a->grad_delta, a->grad_beta}) ||
         !on4({a->grad_final_state, a->grad_A, a->grad_delta_bias, a->grad_state}))
         return kErrInvalid;
-    // blocks are chunks of sequences and heads
-    return (double)((f.S + kChunk - 1) / kChunk) * (double)f.B * (double)f.H <= (double)kMaxGrid ? kOk : kErrShape;
+    return kOk;
 }
 
 int32_t check(const mcc1d_delta_step_args *a)
@@ -121,20 +121,22 @@ extern "C" int32_t mcc1d_delta_workspace_size(const mcc1d_delta_args *a, uint64_
         return kErrNull;
     const int32_t st = check(a, true);
     if (st == kOk)
-        *bytes_out = 0;
+        *bytes_out = delta_plan(*a).bytes;
     return st;
 }
 
 extern "C" int32_t mcc1d_delta(const mcc1d_delta_args *a, void *workspace, uint64_t workspace_bytes, void *stream)
 {
     int32_t st = check(a, true);
+    if (st != kOk)
+        return st;
+    const uint64_t bytes = delta_plan(*a).bytes;
+    st = check_workspace(workspace, workspace_bytes, bytes);
     if (st == kOk)
-        st = check_workspace(workspace, workspace_bytes, 0);
-    if (st == kOk)
-        st = check_apart(*a, workspace, 0);
+        st = check_apart(*a, workspace, bytes);
     if (st == kOk)
         st = check_current_device();
-    return st == kOk ? launch_delta(*a, static_cast<cudaStream_t>(stream)) : st;
+    return st == kOk ? launch_delta(*a, workspace, static_cast<cudaStream_t>(stream)) : st;
 }
 
 extern "C" int32_t mcc1d_delta_bwd_workspace_size(const mcc1d_delta_bwd_args *a, uint64_t *bytes_out)

@@ -470,6 +470,4 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     return launch_column_sums(s, parts, f.H, 2, stream);
 }
 
-int32_t launch_delta(const mcc1d_delta_args &a, cudaStream_t stream) { return launch_delta_tokens(a, nullptr, nullptr, stream); }
-
 }  // namespace mcc1d
