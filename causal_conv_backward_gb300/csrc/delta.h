@@ -26,11 +26,13 @@ struct DeltaBwdPlan {
 DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
 
 // What the products of a chunk need beside q, k and v, for each (b, h, chunk):
-// T and P T as fp16 terms in the panels that the tensor cores read, and the
-// factors of its tokens (delta_prepare.cu).
+// T and P T as fp16 terms in the panels that the tensor cores read, the factors
+// of its tokens, and in the row kFactorEnd its decay and the most that a row's
+// R and U can be of its v and state (delta_prepare.cu).
 constexpr int kPanelBytes = kChunk * 128;
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
        kFactorT, kFactors };
+enum { kEndDecay, kEndOfV, kEndOfState, kEndOfR };      // in that row
 constexpr int kChunkBytes = 4 * kPanelBytes + kFactors * kChunk * 4;
 
 struct DeltaPlan {

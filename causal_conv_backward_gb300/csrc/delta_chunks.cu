@@ -1,22 +1,23 @@
 // delta_chunks.cu - the gated delta rule over prompts, a chunk of 64 tokens at
 // a time, on the tensor cores.
 //
-// A block has one head's state [V,K], up to 128 rows of it, a row to a thread:
-// everything that goes along a row (decays, sums, scales, rounding to two fp16
-// terms) stays in the thread, and the state itself in its registers, in fp32.
-// With the factors of delta_prepare.cu, every chunk is
+// A block has one head's state [V,K], up to 128 rows of it, a row to two
+// threads that share its columns: everything that goes along a row (decays,
+// sums, scales, rounding to two fp16 terms) stays in them, and the state itself
+// in their registers, in fp32. With the factors of delta_prepare.cu, a chunk is
 //   X = S K^T        R = b V - e^c X          (A: the state, from tensor memory)
 //   U = R T^T        Y = e^c S Q^T + R (PT)^T
 //   S = e^c(end) S + (U e^(c(end)-c)) K
 // with tokens along the columns. Operands in tensor memory are two fp16 terms of
-// fp32 rows scaled by a power of two, 22 bits; K and Q are exact in fp16 (bf16
-// rows scaled by a power of two), so those products take two terms and those
+// fp32 rows scaled by a power of two, 22 bits; K and Q are exact in fp16 (rows
+// scaled by a power of two), so those products take two terms and those
 // with T and P T three. Sums are fp32.
 //
 // The chunks of one head follow on one another, X - R - U - S, and bound the
-// kernel: products of 64 tokens and the conversions between them. The products
-// for Y run in the gaps. Warps 0 to 3 hold the rows, warp 4 issues the products,
-// warps 5 to 7 bring tiles two chunks ahead.
+// kernel: the products' latency and the conversions between them, for which a
+// scheduler has two warps of rows. Y is taken in the gaps and leaves through
+// warps of its own. Warps 0 to 7 hold the rows, 8 to 11 write Y, 12 issues the
+// products, 13 to 15 bring the next chunk's tiles.
 #include "delta_common.cuh"
 #include "tensor_core.cuh"
 
@@ -24,102 +25,160 @@ namespace mcc1d {
 
 namespace {
 
-constexpr int kC = kChunk, kRowThreads = 128, kLoadThreads = 96, kThreads = kRowThreads + 32 + kLoadThreads, kStages = 2;
+constexpr int kC = kChunk, kRows = 128, kLoadThreads = 96, kThreads = 512, kStages = 2;
+// Registers by warpgroup: rows, rows, Y, the rest; together what the block has.
+constexpr int kRegRows = 168, kRegY = 96, kRegRest = 80;
+static_assert(2 * kRegRows + kRegY + kRegRest == 4 * 128, "65536 registers");
 
 struct ChunkParams {
     DeltaParams d;
     const uint8_t *prepared;
     int64_t chunks;
     int32_t tiles;            // of 128 rows of V
-    bool vectors_q, vectors_k, vectors_v;
+    bool vectors_q, vectors_k, vectors_v, vectors_s;
+    bool pairs_y;             // two rows of y are one word
 };
 
 template <int KP>
 struct Stage {
     static constexpr int kPanels = KP / 64 * kPanelBytes;
     static constexpr int K = 0, Q = kPanels, kPrepared = 2 * kPanels;
-    static constexpr int V = kPrepared + (kChunkBytes + 1023) / 1024 * 1024;
-    static constexpr int kBytes = V + kC * kRowThreads * 2;
+    static constexpr int V = kPrepared + (kChunkBytes + 1023) / 1024 * 1024;      // [token pair][row] of two values
+    static constexpr int kBytes = V + kC * kRows * 2;
     static_assert(kBytes % 1024 == 0, "panels on 1024 bytes");
 };
 
 // Columns of tensor memory: sums, then operands (pairs of fp16).
 enum { kX = 0, kU = 64, kQS = 128, kPR = 192, kSHi = 256, kSLo = 320, kRHi = 384, kRLo = 416, kUHi = 448, kULo = 480, kColumns = 512 };
 
-struct Barriers {
-    uint64_t full[kStages], empty[kStages], factors[kStages], x, r, u, v, y, s, end;
-    uint32_t tmem;
+struct ChunkShared {
+    uint64_t full[kStages], empty[kStages], factors[kStages], x, r, u, v, y, s, end, out;
+    float of_s[2][kRows], of_r[2][kRows];       // of the last two chunks: what rows' terms are multiplied by
+    float most[2][kRows], most_v[2][kRows], sum_u[2][kRows];      // of the halves of a row
+    uint32_t tmem, failed;
 };
 
-// Eight 16-bit values, from `live` of them.
-__device__ __forceinline__ uint4 eight(const uint16_t *from, bool vectors, int live)
+// A wait of a whole warp; false where it gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity)
 {
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (vectors) {
-        if (live > 0)
-            r = __ldg(reinterpret_cast<const uint4 *>(from));
-    } else if (live > 0) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded_inline(smem_u32(&bar), parity));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t &bar)
+{
+    __syncwarp();
+    if (threadIdx.x % 32 == 0)
+        mbar_arrive(smem_u32(&bar));
+}
+
+// Eight 16-bit values to shared memory, `live` of them from global memory and
+// zeros behind: as an asynchronous copy where addresses allow 16 bytes.
+template <bool VECTORS>
+__device__ __forceinline__ void bring_eight(uint32_t to, const uint16_t *from, int live)
+{
+    if constexpr (VECTORS) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live > 0 ? 16 : 0) : "memory");
+    } else {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             w[i] = i < live ? __ldg(from + i) : 0u;
-        r = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(w[0] | w[1] << 16), "r"(w[2] | w[3] << 16), "r"(w[4] | w[5] << 16),
+                     "r"(w[6] | w[7] << 16)
+                     : "memory");
     }
-    return r;
 }
 
-template <int DT>
-__device__ __forceinline__ uint4 as_half(uint4 v, float scale)
+// A chunk's rows of q or k on their way to panels. A loading thread has one
+// piece of every STEPth row, so that little is left to compute per piece.
+template <int KP, bool VECTORS>
+__device__ __forceinline__ void bring_rows(uint32_t panels, const uint16_t *from, int64_t step, int K, int n, int thread)
 {
-    if constexpr (DT == 1) {
-        return v;
-    } else {
-        const float2 s = make_float2(scale, scale);
-        return make_uint4(pack_half2(mul2(unpack2<0>(v.x), s)), pack_half2(mul2(unpack2<0>(v.y), s)), pack_half2(mul2(unpack2<0>(v.z), s)),
-                          pack_half2(mul2(unpack2<0>(v.w), s)));
+    constexpr int PIECES = KP / 8, STEP = kLoadThreads / PIECES;
+    static_assert(kLoadThreads % PIECES == 0, "whole rows");
+    const int piece = thread % PIECES, live = K - 8 * piece;
+    int t = thread / PIECES;
+    panels += (piece / 8) * kPanelBytes;
+    const uint16_t *row = from + t * step + 8 * piece;
+#pragma unroll 2
+    for (; t < kC; t += STEP, row += STEP * step) {
+        const bool there = t < n && live > 0;
+        bring_eight<VECTORS>(panels + panel_at(t, piece % 8), there ? row : from, there ? live : 0);
     }
 }
-
-// Pieces of eight values of 64 rows, in the order that the loading threads
-// share: all loads of a thread first, so that they are in flight together.
-template <int PIECES>
-struct Pieces {
-    static constexpr int N = (kC * PIECES + kLoadThreads - 1) / kLoadThreads;
-    uint4 v[N];
-    __device__ __forceinline__ void load(const uint16_t *from, int64_t step, int width, bool vectors, int n, int thread)
-    {
+// Pieces made scaled fp16 where they are, by the thread that brought them.
+template <int DT, int KP>
+__device__ __forceinline__ void make_half(uint8_t *panels, const float *scales, int thread)
+{
+    constexpr int PIECES = KP / 8, STEP = kLoadThreads / PIECES, N = (kC + STEP - 1) / STEP, BATCH = 4;
+    const int piece = thread % PIECES, t0 = thread / PIECES;
+    panels += (piece / 8) * kPanelBytes;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int e = thread + j * kLoadThreads, t = e / PIECES, piece = e % PIECES;
-            v[j] = eight(from + t * step + 8 * piece, vectors, t < n ? width - 8 * piece : 0);
+    for (int j = 0; j < N; j += BATCH) {
+        uint4 v[BATCH];
+        float s[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const int t = t0 + (j + e) * STEP;
+            if (t < kC)
+                v[e] = *reinterpret_cast<const uint4 *>(panels + panel_at(t, piece % 8)), s[e] = scales[t];
+        }
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const int t = t0 + (j + e) * STEP;
+            const float2 f = make_float2(s[e], s[e]);
+            if (t < kC)
+                *reinterpret_cast<uint4 *>(panels + panel_at(t, piece % 8)) =
+                    make_uint4(pack_half2(mul2(unpack2<DT>(v[e].x), f)), pack_half2(mul2(unpack2<DT>(v[e].y), f)),
+                               pack_half2(mul2(unpack2<DT>(v[e].z), f)), pack_half2(mul2(unpack2<DT>(v[e].w), f)));
         }
     }
-};
+}
 
-// A chunk's rows of q or k as panels.
-template <int DT, int KP>
-__device__ __forceinline__ void put_rows(const Pieces<KP / 8> &r, const float *scales, uint8_t *panels, int thread)
+// A chunk's rows of v: pieces of two tokens side by side, then exchanged to
+// pairs of tokens by the thread that brought them.
+constexpr int kPiecesV = kRows / 8, kStepV = kLoadThreads / kPiecesV;
+template <bool VECTORS>
+__device__ __forceinline__ void bring_values(uint32_t to, const uint16_t *from, int64_t step, int V, int n, int thread)
 {
-    constexpr int PIECES = KP / 8;
-#pragma unroll
-    for (int j = 0; j < Pieces<PIECES>::N; ++j) {
-        const int e = thread + j * kLoadThreads, t = e / PIECES, piece = e % PIECES;
-        if (t < kC)
-            *reinterpret_cast<uint4 *>(panels + (piece / 8) * kPanelBytes + panel_at(t, piece % 8)) =
-                as_half<DT>(r.v[j], DT == 0 ? scales[t] : 1.f);
+    const int piece = thread % kPiecesV, live = V - 8 * piece;
+    int t = 2 * (thread / kPiecesV);
+    to += 32 * thread;
+    const uint16_t *row = from + t * step + 8 * piece;
+#pragma unroll 2
+    for (; t < kC; t += 2 * kStepV, row += 2 * kStepV * step, to += 32 * kLoadThreads) {
+        const bool one = t < n && live > 0, two = t + 1 < n && live > 0;
+        bring_eight<VECTORS>(to, one ? row : from, one ? live : 0);
+        bring_eight<VECTORS>(to + 16, two ? row + step : from, two ? live : 0);
+    }
+}
+__device__ __forceinline__ void pair_values(uint8_t *v, int thread)
+{
+#pragma unroll 3
+    for (int e = thread; e < kC / 2 * kPiecesV; e += kLoadThreads) {
+        uint4 *at = reinterpret_cast<uint4 *>(v + 32 * e);
+        const uint4 x = at[0], y = at[1];
+        at[0] = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
+        at[1] = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410), __byte_perm(x.w, y.w, 0x7632));
     }
 }
 
-// Half of a thread's row of 64 values as terms: columns `hi` and `lo` on.
-__device__ __forceinline__ void put_terms(const float *x, float scale, uint32_t hi, uint32_t lo)
+// Scaled values of a row as terms in N / 2 columns from `hi` and `lo` on.
+template <int N>
+__device__ __forceinline__ void put_terms(const float *x, uint32_t hi, uint32_t lo)
 {
-    uint32_t h[16], l[16];
-    const float2 s = make_float2(scale, scale);
+    uint32_t h[N / 2], l[N / 2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        two_terms(mul2(make_float2(x[2 * e], x[2 * e + 1]), s), h[e], l[e]);
+    for (int e = 0; e < N / 2; ++e)
+        two_terms(make_float2(x[2 * e], x[2 * e + 1]), h[e], l[e]);
     tmem_store(hi, h);
     tmem_store(lo, l);
+}
+// What is stored is there for the products that are issued after an arrival.
+__device__ __forceinline__ void terms_done(uint64_t &bar)
+{
+    tmem_wait_stores();
+    tmem_fence_before();
+    warp_arrive(bar);
 }
 
 template <int N>
@@ -132,276 +191,388 @@ __device__ __forceinline__ float most_of(const float (&x)[N])
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// ------------------------------------------------------------------ the rows
+template <int DT, int KP>
+__device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh, const uint8_t *stages, int item, int b, int v0, int64_t n,
+                                          int64_t chunks)
+{
+    typedef Stage<KP> St;
+    constexpr int HK = KP / 2, HC = kC / 2;
+    const DeltaParams &p = cp.d;
+    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, half = warp / 4, row = v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, VK = (int64_t)p.V * p.K;
+    const bool mine = row < p.V;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+    float s[HK];             // the state times `scale_s`, a power of two
+    {
+        const float *from = p.state + item * VK + (int64_t)row * p.K + half * HK;
+#pragma unroll
+        for (int k = 0; k < HK; ++k)
+            s[k] = p.state && mine && half * HK + k < p.K ? from[k] : 0.f;
+    }
+    float scale_s;
+    // Scales come from bounds, so that no thread waits for its row's other half
+    // where the products wait for it: terms keep 22 bits of a row up to 2^17 below
+    // its bound. The state's largest value is known a phase late, the sum of a
+    // row's |U| in time.
+    sh.most[half][r] = most_of(s);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    scale_s = scale_for(fmaxf(sh.most[0][r], sh.most[1][r]));
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < HK; ++k)
+        s[k] *= scale_s;
+    const uint32_t terms_s = lanes + kSHi + HK / 2 * half, terms_r = lanes + kRHi + HC / 2 * half, terms_u = lanes + kUHi + HC / 2 * half;
+    if (chunks > 0) {
+        sh.of_s[0][r] = inverse_scale(scale_s);
+#pragma unroll
+        for (int c = 0; c < HK; c += 32)
+            put_terms<32>(s + c, terms_s + c / 2, terms_s + (kSLo - kSHi) + c / 2);
+        terms_done(sh.s);
+    }
+    bool ok = true;          // no wait gave up
+    for (int64_t i = 0;; ++i) {
+        const uint32_t parity = (uint32_t)(i & 1);
+        if (!ok)
+#pragma unroll
+            for (int k = 0; k < HK; ++k)
+                s[k] = __uint_as_float(0x7FFFFFFFu);
+        float *to = i == chunks ? (p.final_state ? p.final_state + item * VK : nullptr) : p.states ? p.states + (i * BH + item) * VK : nullptr;
+        if (to && mine) {
+            const float of = inverse_scale(scale_s);
+            to += (int64_t)row * p.K + half * HK;
+            if (cp.vectors_s) {
+#pragma unroll
+                for (int k = 0; k < HK; k += 4)
+                    if (half * HK + k < p.K)
+                        *reinterpret_cast<float4 *>(to + k) = make_float4(s[k] * of, s[k + 1] * of, s[k + 2] * of, s[k + 3] * of);
+            } else {
+#pragma unroll
+                for (int k = 0; k < HK; ++k)
+                    if (half * HK + k < p.K)
+                        to[k] = s[k] * of;
+            }
+        }
+        if (i >= chunks)
+            break;
+        const uint8_t *stage = stages + (i % kStages) * St::kBytes;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
+        const uint32_t *v = reinterpret_cast<const uint32_t *>(stage + St::V) + half * (HC / 2) * kRows + r;
+        f += half * HC;
+        // the products wait for the chunk's tiles too, but this thread reads some itself
+        ok = warp_wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1);
+        float most_v = 0.f;
+#pragma unroll 4
+        for (int t = 0; t < HC / 2; ++t) {
+            const float2 x = unpack2<DT>(v[t * kRows]);
+            most_v = fmaxf(most_v, fmaxf(fabsf(x.x), fabsf(x.y)));
+        }
+        sh.most[half][r] = most_of(s);
+        sh.most_v[half][r] = most_v;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (sh.failed) {         // all rows leave together; theirs are NaN
+            ok = false;
+            i = chunks - 1;
+            continue;
+        }
+        const float of_s = inverse_scale(scale_s), most_s = fmaxf(sh.most[0][r], sh.most[1][r]) * of_s;
+        const float bound_r = fmaf(ends[kEndOfV], fmaxf(sh.most_v[0][r], sh.most_v[1][r]), ends[kEndOfState] * most_s);
+        const float scale_r = scale_for(bound_r), of_r = inverse_scale(scale_r);
+        const float scale_u = scale_for(bound_r * ends[kEndOfR]), of_u = inverse_scale(scale_u), end = ends[kEndDecay];
+        if (half == 0)
+            sh.of_r[parity][r] = of_r;
+        ok = ok && warp_wait(sh.x, parity);
+        tmem_fence_after();
+        const float2 mx = make_float2(-of_s * scale_r, -of_s * scale_r), mv = make_float2(scale_r, scale_r);
+#pragma unroll 1
+        for (int t0 = 0; t0 < HC; t0 += 16) {
+            uint32_t raw[16];
+            float x[16];
+            tmem_load(lanes + kX + HC * half + t0, raw);
+            tmem_wait(raw);
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) {
+                const float2 bt = *reinterpret_cast<const float2 *>(f + kFactorB * kC + t0 + t), ft = *reinterpret_cast<const float2 *>(f + kFactorX * kC + t0 + t);
+                const float2 a = fma2(mul2(ft, mx), make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])),
+                                      mul2(mul2(bt, mv), unpack2<DT>(v[(t0 + t) / 2 * kRows])));
+                x[t] = a.x, x[t + 1] = a.y;
+            }
+            put_terms<16>(x, terms_r + t0 / 2, terms_r + (kRLo - kRHi) + t0 / 2);
+        }
+        terms_done(sh.r);
+        ok = ok && warp_wait(sh.u, parity);
+        tmem_fence_after();
+        float2 sum_u = make_float2(0.f, 0.f);
+        const float2 mu = make_float2(of_r * scale_u, of_r * scale_u);
+#pragma unroll 1
+        for (int t0 = 0; t0 < HC; t0 += 16) {
+            uint32_t raw[16];
+            float x[16];
+            tmem_load(lanes + kU + HC * half + t0, raw);
+            tmem_wait(raw);
+            if (p.u && mine) {
+                const int64_t at = i * kC + half * HC + t0, step = BH * p.V;
+                float *to_u = p.u + (at * BH + item) * p.V + row;
+#pragma unroll
+                for (int t = 0; t < 16; ++t, to_u += step)
+                    if (at + t < n)
+                        *to_u = __uint_as_float(raw[t]) * (of_r * f[kFactorT * kC + t0 + t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) {
+                const float2 ft = *reinterpret_cast<const float2 *>(f + kFactorU * kC + t0 + t);
+                const float2 a = mul2(mul2(ft, mu), make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])));
+                sum_u = add2(sum_u, make_float2(fabsf(a.x), fabsf(a.y)));
+                x[t] = a.x, x[t + 1] = a.y;
+            }
+            put_terms<16>(x, terms_u + t0 / 2, terms_u + (kULo - kUHi) + t0 / 2);
+        }
+        sh.sum_u[half][r] = sum_u.x + sum_u.y;
+        terms_done(sh.v);
+        warp_arrive(sh.empty[i % kStages]);
+        asm volatile("bar.sync 1, 256;" ::: "memory");     // for sum_u, while the products run
+        // |S| <= e^c(end) |S| + sum of |U k|, and no |k| is above 2^16 as an operand
+        const float before = scale_s;
+        scale_s = scale_for(fmaf(fabsf(end), most_s, (sh.sum_u[0][r] + sh.sum_u[1][r]) * of_u * 65536.f));
+        const float2 keep = make_float2(end * inverse_scale(before) * scale_s, end * inverse_scale(before) * scale_s);
+        const float2 add = make_float2(of_u * scale_s, of_u * scale_s);
+        if (half == 0)
+            sh.of_s[parity ^ 1][r] = inverse_scale(scale_s);
+        ok = ok && warp_wait(sh.end, parity);
+        tmem_fence_after();
+        if (!ok)
+            sh.failed = 1;
+#pragma unroll
+        for (int c = 0; c < HK; c += 32) {
+            uint32_t raw[32];
+            tmem_load(lanes + kX + HK * half + c, raw);
+            tmem_wait(raw);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                const float2 o = fma2(add, make_float2(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), mul2(keep, make_float2(s[c + k], s[c + k + 1])));
+                s[c + k] = o.x, s[c + k + 1] = o.y;
+            }
+            if (i + 1 < chunks)
+                put_terms<32>(s + c, terms_s + c / 2, terms_s + (kSLo - kSHi) + c / 2);
+        }
+        if (i + 1 < chunks)
+            terms_done(sh.s);
+    }
+}
+
+// ------------------------------------------------------------------ Y
+template <int DT, int KP>
+__device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, const uint8_t *stages, int item, int v0, int64_t n, int64_t chunks)
+{
+    typedef Stage<KP> St;
+    const DeltaParams &p = cp.d;
+    const int r = threadIdx.x % kRows, row = v0 + r;
+    const int64_t step = (int64_t)p.B * p.H * p.V;
+    const bool mine = row < p.V;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (threadIdx.x / 32 % 4)) << 16);
+    uint16_t *to = p.y + (int64_t)item * p.V + row;
+    const bool odd = r & 1;
+    uint16_t *pair = odd ? to + step - 1 : to;
+    int64_t i = 0;
+    for (; i < chunks; ++i) {
+        const uint8_t *stage = stages + (i % kStages) * St::kBytes;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
+        if (!warp_wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1) || !warp_wait(sh.y, (uint32_t)(i & 1)))
+            break;
+        tmem_fence_after();
+        const float2 of_s = make_float2(sh.of_s[i & 1][r], sh.of_s[i & 1][r]), of_r = make_float2(sh.of_r[i & 1][r], sh.of_r[i & 1][r]);
+        const int live = (int)(n - i * kC < kC ? n - i * kC : kC), rows = (int)(p.S - i * kC < kC ? p.S - i * kC : kC);
+        const bool whole = cp.pairs_y && rows == kC && live == kC;
+#pragma unroll 1
+        for (int t0 = 0; t0 < kC; t0 += 8) {
+            uint32_t a[8], c[8];
+            tmem_load(lanes + kQS + t0, a);
+            tmem_load(lanes + kPR + t0, c);
+            tmem_wait(a), tmem_wait(c);
+#pragma unroll
+            for (int t = 0; t < 8; t += 2) {
+                const int at = t0 + t;
+                const float2 fq = *reinterpret_cast<const float2 *>(f + kFactorQ * kC + at), fp = *reinterpret_cast<const float2 *>(f + kFactorP * kC + at);
+                const float2 y = fma2(mul2(fp, of_r), make_float2(__uint_as_float(c[t]), __uint_as_float(c[t + 1])),
+                                      mul2(mul2(fq, of_s), make_float2(__uint_as_float(a[t]), __uint_as_float(a[t + 1]))));
+                const uint32_t both = pack2<DT>(y);
+                if (whole) {        // two rows of one token: even lanes the first, odd lanes the second
+                    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, both, 1);
+                    if (mine)
+                        *reinterpret_cast<uint32_t *>(pair) = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
+                } else {
+                    if (mine && at < rows)
+                        to[0] = at < live ? (uint16_t)both : (uint16_t)0;
+                    if (mine && at + 1 < rows)
+                        to[step] = at + 1 < live ? (uint16_t)(both >> 16) : (uint16_t)0;
+                }
+                to += 2 * step, pair += 2 * step;
+            }
+        }
+        tmem_fence_before();
+        warp_arrive(sh.out);
+        warp_arrive(sh.empty[i % kStages]);
+    }
+    if (mine)
+        for (int64_t t = i * kC; t < p.S; ++t, to += step)
+            *to = i < chunks ? 0x7FFF : 0;          // NaN where a wait gave up
+}
+
+// ------------------------------------------------------------------ products
+// One thread's. `y`: those of Y too.
+template <int KP>
+__device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t stages, int64_t chunks, bool y)
+{
+    typedef Stage<KP> St;
+    constexpr uint32_t by_rows = mma_kind(kC, false), by_columns = mma_kind(KP, true);
+    const uint32_t tmem = sh.tmem;
+    const auto with_state = [&](uint32_t d, uint32_t panels) {
+#pragma unroll
+        for (int j = 0; j < KP / 16; ++j) {
+            const uint64_t k = desc_rows(panels + (j / 4) * kPanelBytes) + 2 * (j % 4);
+            mma_ts(tmem + d, tmem + kSHi + 8 * j, k, by_rows, j > 0);
+            mma_ts(tmem + d, tmem + kSLo + 8 * j, k, by_rows, true);
+        }
+    };
+    const auto with_r = [&](uint32_t d, uint32_t panels) {
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t hi = desc_rows(panels) + 2 * j, lo = desc_rows(panels + kPanelBytes) + 2 * j;
+            mma_ts(tmem + d, tmem + kRHi + 8 * j, hi, by_rows, j > 0);
+            mma_ts(tmem + d, tmem + kRHi + 8 * j, lo, by_rows, true);
+            mma_ts(tmem + d, tmem + kRLo + 8 * j, hi, by_rows, true);
+        }
+    };
+    const auto wait = [](uint64_t &bar, uint32_t parity) { return mbar_wait_bounded_inline(smem_u32(&bar), parity); };
+    for (int64_t i = 0; i < chunks; ++i) {
+        const uint32_t parity = (uint32_t)(i & 1), stage = stages + (uint32_t)(i % kStages) * St::kBytes;
+        if (!wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1) || !wait(sh.s, parity))
+            break;
+        tmem_fence_after();
+        with_state(kX, stage + St::K);
+        mma_commit(smem_u32(&sh.x));
+        if (!wait(sh.r, parity))
+            break;
+        tmem_fence_after();
+        with_r(kU, stage + St::kPrepared);
+        mma_commit(smem_u32(&sh.u));
+        if (y) {
+            if (!wait(sh.out, parity ^ 1))         // the Y before this one has been read
+                break;
+            tmem_fence_after();
+            with_state(kQS, stage + St::Q);
+            with_r(kPR, stage + St::kPrepared + 2 * kPanelBytes);
+            mma_commit(smem_u32(&sh.y));
+        }
+        if (!wait(sh.v, parity))
+            break;
+        tmem_fence_after();
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t k = desc_columns(stage + St::K, kPanelBytes) + (uint64_t)(2048 * j >> 4);
+            mma_ts(tmem + kX, tmem + kUHi + 8 * j, k, by_columns, j > 0);
+            mma_ts(tmem + kX, tmem + kULo + 8 * j, k, by_columns, true);
+        }
+        mma_commit(smem_u32(&sh.end));
+        mma_commit(smem_u32(&sh.empty[i % kStages]));
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+template <int DT, int KP>
+__device__ __forceinline__ void bring_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, int item, int b, int h, int v0, int64_t n,
+                                            int64_t chunks)
+{
+    typedef Stage<KP> St;
+    const DeltaParams &p = cp.d;
+    const int thread = threadIdx.x - (kThreads - kLoadThreads), g = h / (p.H / p.G);
+    for (int64_t i = 0; i < chunks; ++i) {
+        const int64_t t0 = i * kC;
+        const int live = (int)(n - t0 < kC ? n - t0 : kC);
+        uint8_t *stage = stages + (i % kStages) * St::kBytes;
+        if (!warp_wait(sh.empty[i % kStages], (uint32_t)(i / kStages + 1) & 1))
+            break;
+        if (thread == 0) {
+            const uint32_t bar = smem_u32(&sh.factors[i % kStages]);
+            mbar_arrive_expect_tx(bar, kChunkBytes);
+            bulk_g2s(smem_u32(stage + St::kPrepared), cp.prepared + (item * cp.chunks + i) * kChunkBytes, kChunkBytes, bar);
+        }
+        const uint16_t *k = p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], *q = p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
+        const uint16_t *v = p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0;
+        const uint32_t at = smem_u32(stage);
+        if (cp.vectors_k)
+            bring_rows<KP, true>(at + St::K, k, p.k_s[0], p.K, live, thread);
+        else
+            bring_rows<KP, false>(at + St::K, k, p.k_s[0], p.K, live, thread);
+        if (cp.vectors_v)
+            bring_values<true>(at + St::V, v, p.v_s[0], p.V - v0, live, thread);
+        else
+            bring_values<false>(at + St::V, v, p.v_s[0], p.V - v0, live, thread);
+        if (!p.y) {
+        } else if (cp.vectors_q)
+            bring_rows<KP, true>(at + St::Q, q, p.q_s[0], p.K, live, thread);
+        else
+            bring_rows<KP, false>(at + St::Q, q, p.q_s[0], p.K, live, thread);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        pair_values(stage + St::V, thread);
+        if (!warp_wait(sh.factors[i % kStages], (uint32_t)(i / kStages) & 1))
+            break;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
+        make_half<DT, KP>(stage + St::K, f + kFactorScaleK * kC, thread);
+        if (p.y)
+            make_half<DT, KP>(stage + St::Q, f + kFactorScaleQ * kC, thread);
+        shared_to_async();
+        warp_arrive(sh.full[i % kStages]);
+    }
+}
+
 template <int DT, int KP>
 __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_constant__ ChunkParams cp)
 {
-    typedef Stage<KP> St;
     extern __shared__ uint8_t raw_shared[];
-    __shared__ Barriers bars;
+    __shared__ ChunkShared sh;
     uint8_t *stages = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
     const DeltaParams &p = cp.d;
-    const int tid = threadIdx.x, warp = tid / 32;
-    const int item = blockIdx.x / cp.tiles, v0 = (blockIdx.x % cp.tiles) * kRowThreads;
-    const int b = item / p.H, h = item % p.H, g = h / (p.H / p.G);
+    const int tid = threadIdx.x, warp = tid / 32, group = warp / 4;
+    const int item = blockIdx.x / cp.tiles, v0 = (blockIdx.x % cp.tiles) * kRows, b = item / p.H, h = item % p.H;
     const int64_t n = clamped_length(p.lengths, b, p.S), chunks = (n + kC - 1) / kC;
-    const int64_t BH = (int64_t)p.B * p.H, VK = (int64_t)p.V * p.K;
 
     if (tid == 0) {
+        sh.failed = 0;
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&bars.full[i]), kLoadThreads);
-            mbar_init(smem_u32(&bars.factors[i]), 1);
-            mbar_init(smem_u32(&bars.empty[i]), kRowThreads + 1);
+            mbar_init(smem_u32(&sh.full[i]), kLoadThreads / 32);
+            mbar_init(smem_u32(&sh.empty[i]), 8 + (p.y ? 4 : 0) + 1);
+            mbar_init(smem_u32(&sh.factors[i]), 1);
         }
-        mbar_init(smem_u32(&bars.x), 1), mbar_init(smem_u32(&bars.u), 1), mbar_init(smem_u32(&bars.y), 1), mbar_init(smem_u32(&bars.end), 1);
-        mbar_init(smem_u32(&bars.r), kRowThreads), mbar_init(smem_u32(&bars.v), kRowThreads), mbar_init(smem_u32(&bars.s), kRowThreads);
+        mbar_init(smem_u32(&sh.x), 1), mbar_init(smem_u32(&sh.u), 1), mbar_init(smem_u32(&sh.y), 1), mbar_init(smem_u32(&sh.end), 1);
+        mbar_init(smem_u32(&sh.r), 8), mbar_init(smem_u32(&sh.v), 8), mbar_init(smem_u32(&sh.s), 8), mbar_init(smem_u32(&sh.out), 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 4)
-        tmem_alloc(smem_u32(&bars.tmem), kColumns);
+    if (warp == 12)
+        tmem_alloc(smem_u32(&sh.tmem), kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = bars.tmem;
 
-    if (warp < 4) {
-        const int row = v0 + tid;
-        const bool mine = row < p.V;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        float s[KP];
-        {
-            const float *from = p.state ? p.state + item * VK + (int64_t)row * p.K : nullptr;
-#pragma unroll
-            for (int k = 0; k < KP; ++k)
-                s[k] = from && mine && k < p.K ? from[k] : 0.f;
-        }
-        float of_s = 1.f;      // what the state's terms are multiplied by
-        const auto put_state = [&]() {
-            const float scale = scale_for(most_of(s));
-            of_s = inverse_scale(scale);
-#pragma unroll
-            for (int c = 0; c < KP / 32; ++c)
-                put_terms(s + 32 * c, scale, lanes + kSHi + 16 * c, lanes + kSLo + 16 * c);
-            tmem_wait_stores();
-            tmem_fence_before();
-            mbar_arrive(smem_u32(&bars.s));
-        };
-        const auto write_state = [&](float *to) {
-            if (mine)
-#pragma unroll
-                for (int k = 0; k < KP; ++k)
-                    if (k < p.K)
-                        to[(int64_t)row * p.K + k] = s[k];
-        };
-        int64_t i = 0;
-        if (chunks > 0)
-            put_state();
-        for (; i < chunks; ++i) {
-            const uint32_t parity = (uint32_t)(i & 1);
-            const uint8_t *stage = stages + (i % kStages) * St::kBytes;
-            const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
-            const uint16_t *v = reinterpret_cast<const uint16_t *>(stage + St::V) + tid;
-            const int live = (int)(n - i * kC < kC ? n - i * kC : kC);
-            if (p.states)
-                write_state(p.states + (i * BH + item) * VK);
-            // the tiles of this chunk (the products wait for them too, but this thread reads some itself)
-            bool ok = mbar_wait_bounded_inline(smem_u32(&bars.full[i % kStages]), (uint32_t)(i / kStages) & 1);
-            ok = ok && mbar_wait_bounded_inline(smem_u32(&bars.x), parity);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
-            tmem_fence_after();
-            float r[kC], of_r;
-            {
-                uint32_t x[2][32];
-                tmem_load(lanes + kX, x[0]);
-                tmem_load(lanes + kX + 32, x[1]);
-                tmem_wait(x[0]), tmem_wait(x[1]);
-#pragma unroll
-                for (int t = 0; t < kC; t += 4) {
-                    const float4 bt = *reinterpret_cast<const float4 *>(f + kFactorB * kC + t), ft = *reinterpret_cast<const float4 *>(f + kFactorX * kC + t);
-                    const float bs[4] = {bt.x, bt.y, bt.z, bt.w}, fs[4] = {ft.x, ft.y, ft.z, ft.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        r[t + e] = fmaf(-fs[e] * of_s, __uint_as_float(x[(t + e) / 32][(t + e) % 32]), bs[e] * unpack2<DT>(v[(t + e) * kRowThreads]).x);
-                }
-                const float scale = scale_for(most_of(r));
-                of_r = inverse_scale(scale);
-                put_terms(r, scale, lanes + kRHi, lanes + kRLo);
-                put_terms(r + 32, scale, lanes + kRHi + 16, lanes + kRLo + 16);
-                tmem_wait_stores();
-                tmem_fence_before();
-                mbar_arrive(smem_u32(&bars.r));
-            }
-            float of_u;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_inline(smem_u32(&bars.u), parity)))
-                break;
-            tmem_fence_after();
-            {
-                uint32_t x[2][32];
-                tmem_load(lanes + kU, x[0]);
-                tmem_load(lanes + kU + 32, x[1]);
-                tmem_wait(x[0]), tmem_wait(x[1]);
-                if (p.u) {
-                    float *to = p.u + (i * kC * BH + item) * p.V + row;
-#pragma unroll
-                    for (int t = 0; t < kC; ++t)
-                        if (mine && t < live)
-                            to[t * BH * p.V] = __uint_as_float(x[t / 32][t % 32]) * (of_r * f[kFactorT * kC + t]);
-                }
-#pragma unroll
-                for (int t = 0; t < kC; t += 4) {
-                    const float4 ft = *reinterpret_cast<const float4 *>(f + kFactorU * kC + t);
-                    const float fs[4] = {ft.x, ft.y, ft.z, ft.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        r[t + e] = __uint_as_float(x[(t + e) / 32][(t + e) % 32]) * (fs[e] * of_r);
-                }
-                const float scale = scale_for(most_of(r));
-                of_u = inverse_scale(scale);
-                put_terms(r, scale, lanes + kUHi, lanes + kULo);
-                put_terms(r + 32, scale, lanes + kUHi + 16, lanes + kULo + 16);
-                tmem_wait_stores();
-                tmem_fence_before();
-                mbar_arrive(smem_u32(&bars.v));
-            }
-            const float end = f[kFactorEnd * kC];
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_inline(smem_u32(&bars.y), parity)))
-                break;
-            tmem_fence_after();
-            if (p.y) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t a[32], c[32];
-                    tmem_load(lanes + kQS + 32 * half, a);
-                    tmem_load(lanes + kPR + 32 * half, c);
-                    tmem_wait(a), tmem_wait(c);
-                    uint16_t *to = p.y + ((i * kC + 32 * half) * BH + item) * p.V + row;
-                    const int64_t rows = p.S - (i * kC + 32 * half);
-#pragma unroll
-                    for (int t = 0; t < 32; ++t) {
-                        const float yq = __uint_as_float(a[t]) * (of_s * f[kFactorQ * kC + 32 * half + t]);
-                        const float y = fmaf(__uint_as_float(c[t]), of_r * f[kFactorP * kC + 32 * half + t], yq);
-                        if (mine && t < rows)
-                            to[t * BH * p.V] = t + 32 * half < live ? (uint16_t)pack2<DT>(make_float2(y, 0.f)) : (uint16_t)0;
-                    }
-                }
-            }
-            mbar_arrive(smem_u32(&bars.empty[i % kStages]));
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded_inline(smem_u32(&bars.end), parity)))
-                break;
-            tmem_fence_after();
-#pragma unroll
-            for (int c = 0; c < KP / 32; ++c) {
-                uint32_t x[32];
-                tmem_load(lanes + kX + 32 * c, x);
-                tmem_wait(x);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    s[32 * c + k] = fmaf(of_u, __uint_as_float(x[k]), end * s[32 * c + k]);
-            }
-            if (i + 1 < chunks)
-                put_state();
-        }
-        // a wait that gave up leaves NaN behind
-        const bool failed = i < chunks;
-        if (failed)
-#pragma unroll
-            for (int k = 0; k < KP; ++k)
-                s[k] = __uint_as_float(0x7FFFFFFFu);
-        if (p.final_state)
-            write_state(p.final_state + item * VK);
-        if (p.y && mine) {
-            for (int64_t t = i * kC; t < p.S; ++t)
-                p.y[(t * BH + item) * p.V + row] = failed ? 0x7FFF : 0;
-        }
-    } else if (warp == 4) {
-        if (tid % 32 == 0) {
-            constexpr uint32_t rows64 = mma_kind(kC, false), columns = mma_kind(KP, true);
-            for (int64_t i = 0; i < chunks; ++i) {
-                const uint32_t parity = (uint32_t)(i & 1), stage = smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes;
-                bool ok = mbar_wait_bounded_inline(smem_u32(&bars.full[i % kStages]), (uint32_t)(i / kStages) & 1);
-                ok = ok && mbar_wait_bounded_inline(smem_u32(&bars.s), parity);
-                if (!ok)
-                    break;
-                tmem_fence_after();
-#pragma unroll
-                for (int j = 0; j < KP / 16; ++j) {
-                    const uint64_t k = desc_rows(stage + St::K + (j / 4) * kPanelBytes) + 2 * (j % 4);
-                    mma_ts(tmem + kX, tmem + kSHi + 8 * j, k, rows64, j > 0);
-                    mma_ts(tmem + kX, tmem + kSLo + 8 * j, k, rows64, true);
-                }
-                mma_commit(smem_u32(&bars.x));
-#pragma unroll
-                for (int j = 0; j < KP / 16; ++j) {
-                    const uint64_t q = desc_rows(stage + St::Q + (j / 4) * kPanelBytes) + 2 * (j % 4);
-                    mma_ts(tmem + kQS, tmem + kSHi + 8 * j, q, rows64, j > 0);
-                    mma_ts(tmem + kQS, tmem + kSLo + 8 * j, q, rows64, true);
-                }
-                if (!mbar_wait_bounded_inline(smem_u32(&bars.r), parity))
-                    break;
-                tmem_fence_after();
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    const uint32_t d = tmem + (which ? kPR : kU), at = stage + St::kPrepared + which * 2 * kPanelBytes;
-#pragma unroll
-                    for (int j = 0; j < kC / 16; ++j) {
-                        const uint64_t hi = desc_rows(at) + 2 * j, lo = desc_rows(at + kPanelBytes) + 2 * j;
-                        mma_ts(d, tmem + kRHi + 8 * j, hi, rows64, j > 0);
-                        mma_ts(d, tmem + kRHi + 8 * j, lo, rows64, true);
-                        mma_ts(d, tmem + kRLo + 8 * j, hi, rows64, true);
-                    }
-                    mma_commit(smem_u32(which ? &bars.y : &bars.u));
-                }
-                if (!mbar_wait_bounded_inline(smem_u32(&bars.v), parity))
-                    break;
-                tmem_fence_after();
-#pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t k = desc_columns(stage + St::K, kPanelBytes) + (uint64_t)(2048 * j >> 4);
-                    mma_ts(tmem + kX, tmem + kUHi + 8 * j, k, columns, j > 0);
-                    mma_ts(tmem + kX, tmem + kULo + 8 * j, k, columns, true);
-                }
-                mma_commit(smem_u32(&bars.end));
-                mma_commit(smem_u32(&bars.empty[i % kStages]));
-            }
-        }
+    if (group < 2) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegRows));
+        hold_rows<DT, KP>(cp, sh, stages, item, b, v0, n, chunks);
+    } else if (group == 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegY));
+        if (p.y)
+            write_y<DT, KP>(cp, sh, stages, item, v0, n, chunks);
     } else {
-        const int thread = tid - kRowThreads - 32;
-        for (int64_t i = 0; i < chunks; ++i) {
-            const int64_t t0 = i * kC;
-            const int live = (int)(n - t0 < kC ? n - t0 : kC);
-            uint8_t *stage = stages + (i % kStages) * St::kBytes;
-            const uint32_t full = smem_u32(&bars.full[i % kStages]), ready = smem_u32(&bars.factors[i % kStages]);
-            Pieces<KP / 8> k, q;
-            Pieces<kRowThreads / 8> v;
-            k.load(p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], p.K, cp.vectors_k, live, thread);
-            q.load(p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2], p.q_s[0], p.K, cp.vectors_q, live, thread);
-            v.load(p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], p.V - v0, cp.vectors_v, live, thread);
-            if (!mbar_wait_bounded_inline(smem_u32(&bars.empty[i % kStages]), (uint32_t)(i / kStages + 1) & 1))
-                break;
-            if (thread == 0) {
-                mbar_arrive_expect_tx(ready, kChunkBytes);
-                bulk_g2s(smem_u32(stage + St::kPrepared), cp.prepared + (item * cp.chunks + i) * kChunkBytes, kChunkBytes, ready);
-            }
-#pragma unroll
-            for (int j = 0; j < Pieces<kRowThreads / 8>::N; ++j) {
-                const int e = thread + j * kLoadThreads;
-                if (e < kC * kRowThreads / 8)
-                    *reinterpret_cast<uint4 *>(stage + St::V + 16 * e) = v.v[j];
-            }
-            if (!mbar_wait_bounded_inline(ready, (uint32_t)(i / kStages) & 1))
-                break;
-            const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
-            put_rows<DT, KP>(k, f + kFactorScaleK * kC, stage + St::K, thread);
-            put_rows<DT, KP>(q, f + kFactorScaleQ * kC, stage + St::Q, thread);
-            shared_to_async();
-            mbar_arrive(full);
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
+        if (warp > 12)
+            bring_tiles<DT, KP>(cp, sh, stages, item, b, h, v0, n, chunks);
+        else if (tid % 32 == 0)
+            issue_products<KP>(sh, smem_u32(stages), chunks, p.y != nullptr);
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == 12) {
         tmem_fence_after();
-        tmem_free(tmem, kColumns);
+        tmem_free(sh.tmem, kColumns);
     }
 }
 
@@ -431,9 +602,11 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, 
     p.d = delta_params(a);
     p.prepared = prepared;
     p.chunks = (a.S + kChunk - 1) / kChunk;
-    p.tiles = (int32_t)((a.V + kRowThreads - 1) / kRowThreads);
+    p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
     const auto vectors = [](int64_t n, const void *at, const int64_t (&s)[3]) { return vectors_for(n, (uintptr_t)at, s[0] | s[1] | s[2]); };
     p.vectors_q = vectors(a.K, a.q, a.q_strides), p.vectors_k = vectors(a.K, a.k, a.k_strides), p.vectors_v = vectors(a.V, a.v, a.v_strides);
+    p.pairs_y = a.V % 2 == 0 && ((uintptr_t)a.y & 3u) == 0;
+    p.vectors_s = a.K % 4 == 0 && ((uintptr_t)a.final_state & 15u) == 0;
     if (a.dtype == 0)
         return a.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
     return a.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);

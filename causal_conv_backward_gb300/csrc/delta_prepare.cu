@@ -31,7 +31,7 @@ struct PrepareShared {
     uint16_t q[kC][RS], k[kC][RS];
     float kk[kC][kRow], qk[kC][kRow];
     float L[kC][kRow], T[kC][kRow], P[kC][kRow], X[kC][kRow];
-    float ch[kC], cl[kC], b[kC], fq[kC], fk[kC], mq[kC], mk[kC];
+    float ch[kC], cl[kC], b[kC], fq[kC], fk[kC], lk[kC], mq[kC], mk[kC], of_v[kC], of_s[kC], of_r[kC];
 };
 
 template <int DT>
@@ -96,18 +96,23 @@ __device__ __forceinline__ void small_product(float (*to)[kRow], int r0, int c0,
     }
 }
 
-// Row t of a matrix as two panels, scaled; four threads to a row, 16 values each. Returns 1 / scale.
-__device__ __forceinline__ float store_terms(const float *row, uint8_t *hi, uint8_t *lo, int t, int part)
+// Row t of a matrix as two panels, scaled; four threads to a row, 16 values each.
+// Returns 1 / scale and the sum of the row's magnitudes.
+__device__ __forceinline__ float2 store_terms(const float *row, uint8_t *hi, uint8_t *lo, int t, int part)
 {
-    float x[16], most = 0.f;
+    float x[16], most = 0.f, sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
         const float4 v = *reinterpret_cast<const float4 *>(row + 16 * part + j);
         x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
         most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        sum += (fabsf(v.x) + fabsf(v.y)) + (fabsf(v.z) + fabsf(v.w));
     }
-    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    }
     const float scale = scale_for(most);
 #pragma unroll
     for (int piece = 0; piece < 2; ++piece) {
@@ -119,7 +124,7 @@ __device__ __forceinline__ float store_terms(const float *row, uint8_t *hi, uint
         *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    return inverse_scale(scale);
+    return make_float2(inverse_scale(scale), sum);
 }
 
 template <int DT, int KP>
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_prepare_kernel(const __grid
         return;
     const int n = (int)(length - t0 < kC ? length - t0 : kC);
 
-    // q, k, their factors, and the scale that makes fp16 of bf16 values without loss
+    // q, k, their factors, and the scale that makes rows of about one size of them in fp16, without loss
     for (int i = warp; i < kC; i += kThreads / 32) {
         const uint16_t *qp = p.q + (t0 + i) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
         const uint16_t *kp = p.k + (t0 + i) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2];
@@ -159,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, 2) delta_prepare_kernel(const __grid
             }
         if (lane == 0) {
             sh.fq[i] = unit_factor(p.flags, sums[0]), sh.fk[i] = unit_factor(p.flags, sums[1]);
-            sh.mq[i] = DT == 0 ? scale_for(most[0]) : 1.f, sh.mk[i] = DT == 0 ? scale_for(most[1]) : 1.f;
+            sh.lk[i] = sqrtf(sums[1]) * sh.fk[i];
+            sh.mq[i] = scale_for(most[0]), sh.mk[i] = scale_for(most[1]);
         }
     }
     __syncthreads();
@@ -258,21 +264,36 @@ __global__ void __launch_bounds__(kThreads, 2) delta_prepare_kernel(const __grid
         }
         __syncthreads();
         const int t = tid / 4, part = tid % 4;
-        const float of_t = store_terms(sh.T[t], out, out + kPanelBytes, t, part);
-        const float of_p = store_terms(sh.X[t], out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
+        const float2 of_t = store_terms(sh.T[t], out, out + kPanelBytes, t, part);
+        const float2 of_p = store_terms(sh.X[t], out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
         if (part == 0) {
             const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f));
             const float el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
-            const float k = sh.fk[t] * inverse_scale(sh.mk[t]), q = sh.fq[t] * p.scale * inverse_scale(sh.mq[t]);
+            // a row of zeros adds nothing, and must not lower the others' scale
+            const float k = sh.lk[t] != 0.f ? sh.fk[t] * inverse_scale(sh.mk[t]) : 0.f, q = sh.fq[t] * p.scale * inverse_scale(sh.mq[t]);
             factors[kFactorB * kC + t] = sh.b[t];
             factors[kFactorX * kC + t] = sh.b[t] * ec * k;
-            factors[kFactorU * kC + t] = of_t * el * k;
+            factors[kFactorU * kC + t] = of_t.x * el * k;
             factors[kFactorQ * kC + t] = ec * q;
-            factors[kFactorP * kC + t] = of_p;
-            factors[kFactorT * kC + t] = of_t;
+            factors[kFactorP * kC + t] = of_p.x;
+            factors[kFactorT * kC + t] = of_t.x;
             factors[kFactorScaleK * kC + t] = sh.mk[t];
             factors[kFactorScaleQ * kC + t] = sh.mq[t];
-            factors[kFactorEnd * kC + t] = ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
+            sh.of_v[t] = fabsf(sh.b[t]);
+            sh.of_s[t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
+            sh.of_r[t] = of_t.y * el * fabsf(k);
+        }
+        __syncthreads();
+        if (warp < 3) {
+            const float *x = warp == 0 ? sh.of_v : warp == 1 ? sh.of_s : sh.of_r;
+            float most = fmaxf(x[lane], x[lane + 32]);
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2)
+                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            if (lane == 0)
+                factors[kFactorEnd * kC + kEndOfV + warp] = most;
+        } else if (tid == 96) {
+            factors[kFactorEnd * kC + kEndDecay] = ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
         }
     }
 }
