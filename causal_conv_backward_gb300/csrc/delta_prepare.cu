@@ -23,59 +23,40 @@ struct PrepareParams {
     DeltaParams d;
     uint8_t *out;
     int64_t chunks;
+    bool vectors_q, vectors_k;
 };
 
+// Rows of 16-bit values eight longer, so that eight of them start on different
+// banks. What the tokens' rows take is T and X later on.
 template <int KP>
 struct PrepareShared {
-    static constexpr int RS = KP + 8;                       // of 16-bit rows, so that eight of them start on different banks
-    uint16_t q[kC][RS], k[kC][RS];
-    float kk[kC][kRow], qk[kC][kRow];
-    float L[kC][kRow], T[kC][kRow], P[kC][kRow], X[kC][kRow];
-    float ch[kC], cl[kC], b[kC], fq[kC], fk[kC], lk[kC], mq[kC], mk[kC], of_v[kC], of_s[kC], of_r[kC];
+    static constexpr int RS = KP + 8;
+    union {
+        uint16_t qk[2][kC][RS];
+        struct {
+            float T[kC][kRow], X[kC][kRow];
+        };
+    };
+    float L[kC][kRow], P[kC][kRow];
+    float ch[kC], cl[kC], b[kC], f[2][kC], m[2][kC], lk[kC], of_v[kC], of_s[kC], of_r[kC];
 };
 
 template <int DT>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     if constexpr (DT == 0)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// out (16 rows from r0, columns from c0, `NB` of eight) = rows x columns products over KP values.
-template <int DT, int KP, int NB>
-__device__ __forceinline__ void token_products(const uint16_t (*rows)[KP + 8], const uint16_t (*cols)[KP + 8], const float *fr, const float *fc,
-                                               float scale, float (*out)[kRow], int r0, int c0)
+// Four 8 x 8 matrices of 16-bit values, the rows' addresses from eight lanes each.
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at)
 {
-    const int lane = threadIdx.x % 32, g = lane / 4, p = 2 * (lane % 4);
-    float acc[NB][4];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-        acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-    for (int at = 0; at < KP; at += 16) {
-        const uint32_t a[4] = {*reinterpret_cast<const uint32_t *>(&rows[r0 + g][at + p]), *reinterpret_cast<const uint32_t *>(&rows[r0 + g + 8][at + p]),
-                               *reinterpret_cast<const uint32_t *>(&rows[r0 + g][at + p + 8]),
-                               *reinterpret_cast<const uint32_t *>(&rows[r0 + g + 8][at + p + 8])};
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const uint32_t b[2] = {*reinterpret_cast<const uint32_t *>(&cols[c0 + 8 * n + g][at + p]),
-                                   *reinterpret_cast<const uint32_t *>(&cols[c0 + 8 * n + g][at + p + 8])};
-            mma16816<DT>(acc[n], a, b);
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = r0 + g + 8 * (e / 2), c = c0 + 8 * n + p + e % 2;
-            out[r][c] = acc[n][e] * (fr[r] * scale) * fc[c];
-        }
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
 // to[r0+i][c0+j] = sign * sum over m < N of a[ar+i][ac+m] b[br+m][bc+j], N x N, by `threads` threads.
@@ -128,56 +109,50 @@ __device__ __forceinline__ float2 store_terms(const float *row, uint8_t *hi, uin
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kThreads, 2) delta_prepare_kernel(const __grid_constant__ PrepareParams pp)
+__global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid_constant__ PrepareParams pp)
 {
     extern __shared__ __align__(16) uint8_t raw_shared[];
-    PrepareShared<KP> &sh = *reinterpret_cast<PrepareShared<KP> *>(raw_shared);
+    typedef PrepareShared<KP> Shared;
+    Shared &sh = *reinterpret_cast<Shared *>(raw_shared);
     const DeltaParams &p = pp.d;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int g = blockIdx.x % p.G, b = (blockIdx.x / p.G) % p.B, per = p.H / p.G;
-    const int64_t chunk = blockIdx.x / p.G / p.B, t0 = chunk * kC;
+    const int h = blockIdx.x % p.H, b = (blockIdx.x / p.H) % p.B, g = h / (p.H / p.G);
+    const int64_t chunk = blockIdx.x / p.H / p.B, t0 = chunk * kC;
     const int64_t length = clamped_length(p.lengths, b, p.S);
     if (length <= t0)
         return;
     const int n = (int)(length - t0 < kC ? length - t0 : kC);
+    const int64_t item = (int64_t)b * p.H + h;
+    uint8_t *out = pp.out + (item * pp.chunks + chunk) * kChunkBytes;
+    float *factors = reinterpret_cast<float *>(out + 4 * kPanelBytes);
 
-    // q, k, their factors, and the scale that makes rows of about one size of them in fp16, without loss
-    for (int i = warp; i < kC; i += kThreads / 32) {
-        const uint16_t *qp = p.q + (t0 + i) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
-        const uint16_t *kp = p.k + (t0 + i) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2];
-        float sums[2] = {0.f, 0.f}, most[2] = {0.f, 0.f};
+    // rows of q and k, all of a thread's loads in flight together
+    constexpr int PIECES = KP / 8, STEP = kThreads / PIECES, N = kC / STEP;
+    {
+        const int piece = tid % PIECES, first = tid / PIECES;
+        uint4 x[2][N];
 #pragma unroll
-        for (int j = 0; j < KP / 32; ++j) {
-            const int at = j * 32 + lane;
-            const uint16_t q = i < n && at < p.K ? __ldg(qp + at) : 0, k = i < n && at < p.K ? __ldg(kp + at) : 0;
-            sh.q[i][at] = q, sh.k[i][at] = k;
-            const float qv = unpack2<DT>(q).x, kv = unpack2<DT>(k).x;
-            sums[0] = fmaf(qv, qv, sums[0]), sums[1] = fmaf(kv, kv, sums[1]);
-            most[0] = fmaxf(most[0], fabsf(qv)), most[1] = fmaxf(most[1], fabsf(kv));
-        }
+        for (int w = 0; w < 2; ++w) {
+            const int64_t step = w ? p.k_s[0] : p.q_s[0];
+            const uint16_t *from = w ? p.k + b * p.k_s[1] + g * p.k_s[2] : p.q + b * p.q_s[1] + g * p.q_s[2];
+            from += (t0 + first) * step + 8 * piece;
+            const bool vectors = w ? pp.vectors_k : pp.vectors_q;
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2)
+            for (int j = 0; j < N; ++j, from += STEP * step) {
+                const int live = first + j * STEP < n ? p.K - 8 * piece : 0;
+                x[w][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (vectors) {
+                    if (live > 0)
+                        x[w][j] = __ldg(reinterpret_cast<const uint4 *>(from));
+                } else {
+                    uint32_t *e = reinterpret_cast<uint32_t *>(&x[w][j]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                sums[e] += __shfl_xor_sync(0xFFFFFFFFu, sums[e], d);
-                most[e] = fmaxf(most[e], __shfl_xor_sync(0xFFFFFFFFu, most[e], d));
+                    for (int i = 0; i < 8; ++i)
+                        if (i < live)
+                            e[i / 2] |= (uint32_t)__ldg(from + i) << (16 * (i % 2));
+                }
             }
-        if (lane == 0) {
-            sh.fq[i] = unit_factor(p.flags, sums[0]), sh.fk[i] = unit_factor(p.flags, sums[1]);
-            sh.lk[i] = sqrtf(sums[1]) * sh.fk[i];
-            sh.mq[i] = scale_for(most[0]), sh.mk[i] = scale_for(most[1]);
         }
-    }
-    __syncthreads();
-    // eight warps: 16 rows of one product and half of its columns each, two products
-    token_products<DT, KP, 4>(sh.k, sh.k, sh.fk, sh.fk, 1.f, sh.kk, 16 * (warp % 4), 32 * (warp / 4));
-    token_products<DT, KP, 4>(sh.q, sh.k, sh.fq, sh.fk, p.scale, sh.qk, 16 * (warp % 4), 32 * (warp / 4));
-
-    for (int h = g * per; h < (g + 1) * per; ++h) {
-        const int64_t item = (int64_t)b * p.H + h;
-        uint8_t *out = pp.out + (item * pp.chunks + chunk) * kChunkBytes;
-        float *factors = reinterpret_cast<float *>(out + 4 * kPanelBytes);
-        __syncthreads();
         // gates, and the running sum of log2 a in two parts whose differences are
         // exact in the first: multiples of 2^-9 below 2^14
         if (tid < kC) {
@@ -190,111 +165,174 @@ __global__ void __launch_bounds__(kThreads, 2) delta_prepare_kernel(const __grid
             const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f), hi = rintf(l * 512.f) * (1.f / 512.f);
             sh.ch[tid] = hi, sh.cl[tid] = l - hi, sh.b[tid] = gate.b;
         }
-        __syncthreads();
-        if (warp < 2) {
-            float *c = warp == 0 ? sh.ch : sh.cl;
-            const float x = c[2 * lane], y = c[2 * lane + 1] + x;
-            float s = y;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const float o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-                if (lane >= d)
-                    s += o;
-            }
-            const float o = __shfl_up_sync(0xFFFFFFFFu, s, 1), before = lane > 0 ? o : 0.f;
-            c[2 * lane] = before + x;
-            c[2 * lane + 1] = before + y;
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                *reinterpret_cast<uint4 *>(&sh.qk[w][first + j * STEP][8 * piece]) = x[w][j];
+    }
+    __syncthreads();
+    if (warp < 2) {
+        float *c = warp == 0 ? sh.ch : sh.cl;
+        const float x = c[2 * lane], y = c[2 * lane + 1] + x;
+        float s = y;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const float o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+            if (lane >= d)
+                s += o;
         }
-        __syncthreads();
-        for (int e = tid; e < kC * kC; e += kThreads) {
-            const int t = e / kC, i = e % kC;
-            const float D = i <= t ? ex2(fminf((sh.ch[t] - sh.ch[i]) + (sh.cl[t] - sh.cl[i]), 127.f)) : 0.f;
-            sh.L[t][i] = i < t ? sh.b[t] * D * sh.kk[t][i] : 0.f;
-            sh.P[t][i] = i <= t ? D * sh.qk[t][i] : 0.f;
-            sh.T[t][i] = 0.f;
-        }
-        __syncthreads();
-        if (warp < 4 && lane < 16) {         // the diagonal blocks, a column to a thread
-            float x[16];
-            const int o = 16 * warp;
+        const float o = __shfl_up_sync(0xFFFFFFFFu, s, 1), before = lane > 0 ? o : 0.f;
+        c[2 * lane] = before + x;
+        c[2 * lane + 1] = before + y;
+    }
+    {   // lengths, and the scale that makes rows of about one size of them in fp16, without loss: two threads to a row
+        const int w = tid / 128, t = tid % 128 / 2, half = tid % 2;
+        float sum = 0.f, most = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = i == lane ? 1.f : 0.f;
+        for (int j = 0; j < KP / 16; ++j) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sh.qk[w][t][(2 * j + half) * 8]);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int m = 0; m < i; ++m)
-                    s = fmaf(-sh.L[o + i][o + m], x[m], s);
-                x[i] = s;
-                sh.T[o + i][o + lane] = s;
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack2<DT>(u[e]);
+                sum = fmaf(x.x, x.x, fmaf(x.y, x.y, sum));
+                most = fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y)));
             }
         }
-        __syncthreads();
-        // the corners below them, 16 wide and then 32 wide
-        small_product<16>(sh.X, 32 * (tid / 128), 0, sh.L, 32 * (tid / 128) + 16, 32 * (tid / 128), sh.T, 32 * (tid / 128), 32 * (tid / 128), 1.f,
-                          tid % 128, 128);
-        __syncthreads();
-        small_product<16>(sh.T, 32 * (tid / 128) + 16, 32 * (tid / 128), sh.T, 32 * (tid / 128) + 16, 32 * (tid / 128) + 16, sh.X, 32 * (tid / 128), 0,
-                          -1.f, tid % 128, 128);
-        __syncthreads();
-        small_product<32>(sh.X, 0, 0, sh.L, 32, 0, sh.T, 0, 0, 1.f, tid, kThreads);
-        __syncthreads();
-        small_product<32>(sh.T, 32, 0, sh.T, 32, 32, sh.X, 0, 0, -1.f, tid, kThreads);
-        __syncthreads();
-        {   // P T, four rows and four columns to a thread
-            const int r = 4 * (tid / 16), c = 4 * (tid % 16);
-            float s[4][4] = {};
-            if (c <= r + 3)
-                for (int m = c; m < r + 4; m += 4) {
-                    float4 x[4], y[4];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        if (half == 0) {
+            const float f = unit_factor(p.flags, sum);
+            sh.f[w][t] = f, sh.m[w][t] = scale_for(most);
+            if (w == 1)
+                sh.lk[t] = sqrtf(sum) * f;
+        }
+    }
+    __syncthreads();
+    {   // 16 rows and 32 columns of both products to a warp
+        const int r0 = 16 * (warp % 4), c0 = 32 * (warp / 4), row = lane / 4, col = 2 * (lane % 4);
+        float kk[4][4] = {}, qk[4][4] = {};
+        if (c0 <= r0 + 15) {
+            constexpr int RS = Shared::RS;
+            const uint32_t q = smem_u32(&sh.qk[0][r0 + lane % 16][8 * (lane / 16)]), k = q + kC * RS * 2;
+            const uint32_t c = smem_u32(&sh.qk[1][c0 + lane % 8 + 8 * (lane / 16)][8 * (lane / 8 % 2)]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = *reinterpret_cast<const float4 *>(&sh.P[r + i][m]), y[i] = *reinterpret_cast<const float4 *>(&sh.T[m + i][c]);
+            for (int at = 0; at < KP; at += 16) {
+                uint32_t aq[4], ak[4], x[4], y[4];
+                load_matrices(aq, q + 2 * at);
+                load_matrices(ak, k + 2 * at);
+                load_matrices(x, c + 2 * at);
+                load_matrices(y, c + 2 * at + 16 * RS * 2);
+                mma16816<DT>(kk[0], ak, x[0], x[1]), mma16816<DT>(kk[1], ak, x[2], x[3]);
+                mma16816<DT>(kk[2], ak, y[0], y[1]), mma16816<DT>(kk[3], ak, y[2], y[3]);
+                mma16816<DT>(qk[0], aq, x[0], x[1]), mma16816<DT>(qk[1], aq, x[2], x[3]);
+                mma16816<DT>(qk[2], aq, y[0], y[1]), mma16816<DT>(qk[3], aq, y[2], y[3]);
+            }
+        }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int half = 0; half < 2; ++half) {
+            const int t = r0 + row + 8 * half;
+            const float th = sh.ch[t], tl = sh.cl[t], lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            s[i][0] = fmaf(xs[k], y[k].x, s[i][0]), s[i][1] = fmaf(xs[k], y[k].y, s[i][1]);
-                            s[i][2] = fmaf(xs[k], y[k].z, s[i][2]), s[i][3] = fmaf(xs[k], y[k].w, s[i][3]);
-                        }
+            for (int j = 0; j < 4; ++j) {
+                float l[2], x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = c0 + 8 * j + col + e;
+                    const float D = i <= t ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) * sh.f[1][i] : 0.f;
+                    l[e] = i < t ? kk[j][2 * half + e] * (D * lt) : 0.f;
+                    x[e] = i <= t ? qk[j][2 * half + e] * (D * pt) : 0.f;
+                }
+                *reinterpret_cast<float2 *>(&sh.L[t][c0 + 8 * j + col]) = make_float2(l[0], l[1]);
+                *reinterpret_cast<float2 *>(&sh.P[t][c0 + 8 * j + col]) = make_float2(x[0], x[1]);
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < kC * kC / 4; e += kThreads)
+        *reinterpret_cast<float4 *>(&sh.T[e / (kC / 4)][4 * (e % (kC / 4))]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (warp < 4 && lane < 16) {         // the diagonal blocks, a column to a thread
+        float x[16];
+        const int o = 16 * warp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                s = fmaf(-sh.L[o + i][o + m], x[m], s);
+            x[i] = s;
+            sh.T[o + i][o + lane] = s;
+        }
+    }
+    __syncthreads();
+    // the corners below them, 16 wide and then 32 wide
+    small_product<16>(sh.X, 32 * (tid / 128), 0, sh.L, 32 * (tid / 128) + 16, 32 * (tid / 128), sh.T, 32 * (tid / 128), 32 * (tid / 128), 1.f,
+                      tid % 128, 128);
+    __syncthreads();
+    small_product<16>(sh.T, 32 * (tid / 128) + 16, 32 * (tid / 128), sh.T, 32 * (tid / 128) + 16, 32 * (tid / 128) + 16, sh.X, 32 * (tid / 128), 0,
+                      -1.f, tid % 128, 128);
+    __syncthreads();
+    small_product<32>(sh.X, 0, 0, sh.L, 32, 0, sh.T, 0, 0, 1.f, tid, kThreads);
+    __syncthreads();
+    small_product<32>(sh.T, 32, 0, sh.T, 32, 32, sh.X, 0, 0, -1.f, tid, kThreads);
+    __syncthreads();
+    {   // P T, four rows and four columns to a thread
+        const int r = 4 * (tid / 16), c = 4 * (tid % 16);
+        float s[4][4] = {};
+        if (c <= r + 3)
+            for (int m = c; m < r + 4; m += 4) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = *reinterpret_cast<const float4 *>(&sh.P[r + i][m]), y[i] = *reinterpret_cast<const float4 *>(&sh.T[m + i][c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        s[i][0] = fmaf(xs[k], y[k].x, s[i][0]), s[i][1] = fmaf(xs[k], y[k].y, s[i][1]);
+                        s[i][2] = fmaf(xs[k], y[k].z, s[i][2]), s[i][3] = fmaf(xs[k], y[k].w, s[i][3]);
                     }
                 }
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4 *>(&sh.X[r + i][c]) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
-        }
-        __syncthreads();
-        const int t = tid / 4, part = tid % 4;
-        const float2 of_t = store_terms(sh.T[t], out, out + kPanelBytes, t, part);
-        const float2 of_p = store_terms(sh.X[t], out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
-        if (part == 0) {
-            const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f));
-            const float el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
-            // a row of zeros adds nothing, and must not lower the others' scale
-            const float k = sh.lk[t] != 0.f ? sh.fk[t] * inverse_scale(sh.mk[t]) : 0.f, q = sh.fq[t] * p.scale * inverse_scale(sh.mq[t]);
-            factors[kFactorB * kC + t] = sh.b[t];
-            factors[kFactorX * kC + t] = sh.b[t] * ec * k;
-            factors[kFactorU * kC + t] = of_t.x * el * k;
-            factors[kFactorQ * kC + t] = ec * q;
-            factors[kFactorP * kC + t] = of_p.x;
-            factors[kFactorT * kC + t] = of_t.x;
-            factors[kFactorScaleK * kC + t] = sh.mk[t];
-            factors[kFactorScaleQ * kC + t] = sh.mq[t];
-            sh.of_v[t] = fabsf(sh.b[t]);
-            sh.of_s[t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
-            sh.of_r[t] = of_t.y * el * fabsf(k);
-        }
-        __syncthreads();
-        if (warp < 3) {
-            const float *x = warp == 0 ? sh.of_v : warp == 1 ? sh.of_s : sh.of_r;
-            float most = fmaxf(x[lane], x[lane + 32]);
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(&sh.X[r + i][c]) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+    }
+    __syncthreads();
+    const int t = tid / 4, part = tid % 4;
+    const float2 of_t = store_terms(sh.T[t], out, out + kPanelBytes, t, part);
+    const float2 of_p = store_terms(sh.X[t], out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
+    if (part == 0) {
+        const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f));
+        const float el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
+        // a row of zeros adds nothing, and must not lower the others' scale
+        const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f, q = sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
+        factors[kFactorB * kC + t] = sh.b[t];
+        factors[kFactorX * kC + t] = sh.b[t] * ec * k;
+        factors[kFactorU * kC + t] = of_t.x * el * k;
+        factors[kFactorQ * kC + t] = ec * q;
+        factors[kFactorP * kC + t] = of_p.x;
+        factors[kFactorT * kC + t] = of_t.x;
+        factors[kFactorScaleK * kC + t] = sh.m[1][t];
+        factors[kFactorScaleQ * kC + t] = sh.m[0][t];
+        sh.of_v[t] = fabsf(sh.b[t]);
+        sh.of_s[t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
+        sh.of_r[t] = of_t.y * el * fabsf(k);
+    }
+    __syncthreads();
+    if (warp < 3) {
+        const float *x = warp == 0 ? sh.of_v : warp == 1 ? sh.of_s : sh.of_r;
+        float most = fmaxf(x[lane], x[lane + 32]);
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-            if (lane == 0)
-                factors[kFactorEnd * kC + kEndOfV + warp] = most;
-        } else if (tid == 96) {
-            factors[kFactorEnd * kC + kEndDecay] = ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
-        }
+        for (int d = 16; d > 0; d /= 2)
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        if (lane == 0)
+            factors[kFactorEnd * kC + kEndOfV + warp] = most;
+    } else if (tid == 96) {
+        factors[kFactorEnd * kC + kEndDecay] = ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
     }
 }
 
@@ -304,7 +342,7 @@ int32_t prepare(const PrepareParams &p, cudaStream_t stream)
     constexpr int bytes = (int)sizeof(PrepareShared<KP>);
     if (cudaFuncSetAttribute(delta_prepare_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_prepare_kernel<DT, KP>, dim3((unsigned)(p.chunks * p.d.B * p.d.G)), kThreads, bytes, stream, p);
+    return launch(delta_prepare_kernel<DT, KP>, dim3((unsigned)(p.chunks * p.d.B * p.d.H)), kThreads, bytes, stream, p);
 }
 
 }  // namespace
@@ -314,6 +352,8 @@ int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaS
     PrepareParams p = {};
     p.d = delta_params(a);
     p.out = prepared, p.chunks = (a.S + kChunk - 1) / kChunk;
+    p.vectors_q = vectors_for(a.K, (uintptr_t)a.q, a.q_strides[0] | a.q_strides[1] | a.q_strides[2]);
+    p.vectors_k = vectors_for(a.K, (uintptr_t)a.k, a.k_strides[0] | a.k_strides[1] | a.k_strides[2]);
     if (a.dtype == 0)
         return a.K <= 64 ? prepare<0, 64>(p, stream) : prepare<0, 128>(p, stream);
     return a.K <= 64 ? prepare<1, 64>(p, stream) : prepare<1, 128>(p, stream);

@@ -178,4 +178,13 @@ __device__ __forceinline__ void two_terms(float2 v, uint32_t &hi, uint32_t &lo)
     lo = pack_half2(sub2(v, __half22float2(c.h)));
 }
 
+// A tile of a described tensor [batch,head,token,value] to shared memory (128-byte
+// aligned), completing on an mbarrier; `x` is a multiple of eight.
+__device__ __forceinline__ void tile_g2s(uint32_t dst, const void *map, int x, int token, int head, int batch, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map),
+                 "r"(x), "r"(token), "r"(head), "r"(batch), "r"(bar)
+                 : "memory");
+}
+
 }  // namespace mcc1d
