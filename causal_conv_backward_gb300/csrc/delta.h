@@ -14,13 +14,22 @@ constexpr int kMaxKey = 128, kMaxValue = 1024;
 constexpr int kChunk = 64;                 // tokens whose products are taken together
 constexpr double kUnitEps = 1e-6;          // under the root of |q|^2, |k|^2
 
-// Workspace of the backward, in bytes from its start; all fp32. T = S B H V
-// values per token, states [chunks][B H][V K].
+// What a pass over the tokens writes down for the gradients: u(t) or du(t)
+// [S,B,H,Vp], and the states (or their gradients) at chunks' ends [chunks][B H][V,Kp].
+struct DeltaKept {
+    float *u, *states;
+    int32_t Vp, Kp;                        // V and K to a multiple of four
+};
+
+// Workspace of the backward, in bytes from its start.
 struct DeltaBwdPlan {
+    bool tokens;                           // token by token
     int64_t chunks;                        // ceil(S / kChunk)
-    uint64_t off_u, off_du;                // u(t) and its gradient, [S,B,H,V]
+    int32_t Vp, Kp;
+    uint64_t off_u, off_du;                // u(t) and its gradient
     uint64_t off_s, off_g;                 // states before each chunk, gradients of those after it
     uint64_t off_sums;                     // grad_A, grad_delta_bias of each (chunk, sequence): [2][chunks B][H]
+    uint64_t off_prepared;
     uint64_t bytes;
 };
 DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
@@ -44,14 +53,14 @@ DeltaPlan delta_plan(const mcc1d_delta_args &a);
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream);
-int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, cudaStream_t stream);
+int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream);
 int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream);
 
 // Token by token (delta_tokens.cu): the forward, with u(t) and the states at
 // chunk starts written down where the pointers are given; and the states'
 // gradients backwards, with du(t), those at chunk ends and grad_v.
-int32_t launch_delta_tokens(const mcc1d_delta_args &a, float *u, float *states, cudaStream_t stream);
-int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, float *du, float *grads, cudaStream_t stream);
+int32_t launch_delta_tokens(const mcc1d_delta_args &a, const DeltaKept &kept, cudaStream_t stream);
+int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, const DeltaKept &kept, cudaStream_t stream);
 
 }  // namespace mcc1d

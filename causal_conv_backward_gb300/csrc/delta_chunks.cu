@@ -212,11 +212,12 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
 #pragma unroll
             for (int k = 0; k < HK; ++k)
                 s[k] = __uint_as_float(0x7FFFFFFFu);
-        float *to = i == chunks ? (p.final_state ? p.final_state + item * VK : nullptr) : p.states ? p.states + (i * BH + item) * VK : nullptr;
+        float *to = i == chunks ? p.final_state : p.kept.states;
         if (to && mine) {
             const float of = inverse_scale(scale_s);
-            to += (int64_t)row * p.K + part * HK;
-            if (cp.vectors_s) {
+            to += i == chunks ? item * VK + (int64_t)row * p.K : ((i * BH + item) * p.V + row) * p.kept.Kp;
+            to += part * HK;
+            if (cp.vectors_s || i < chunks) {
 #pragma unroll
                 for (int k = 0; k < HK; k += 4)
                     if (part * HK + k < p.K)
@@ -285,9 +286,9 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
             float x[16];
             tmem_load(lanes + kU + HC * part + t0, raw);
             tmem_wait(raw);
-            if (p.u && mine) {
-                const int64_t at = i * kC + part * HC + t0, step = BH * p.V;
-                float *to_u = p.u + (at * BH + item) * p.V + row;
+            if (p.kept.u && mine) {
+                const int64_t at = i * kC + part * HC + t0, step = BH * p.kept.Vp;
+                float *to_u = p.kept.u + (at * BH + item) * p.kept.Vp + row;
 #pragma unroll
                 for (int t = 0; t < 16; ++t, to_u += step)
                     if (at + t < n)
@@ -605,10 +606,11 @@ DeltaPlan delta_plan(const mcc1d_delta_args &a)
     return p;
 }
 
-int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, cudaStream_t stream)
+int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream)
 {
     ChunkParams p = {};
     p.d = delta_params(a);
+    p.d.kept = kept;
     p.prepared = prepared;
     p.chunks = (a.S + kChunk - 1) / kChunk;
     p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
@@ -625,10 +627,10 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream)
 {
     if (delta_plan(a).tokens)
-        return launch_delta_tokens(a, nullptr, nullptr, stream);
+        return launch_delta_tokens(a, DeltaKept(), stream);
     uint8_t *prepared = static_cast<uint8_t *>(workspace);
     const int32_t st = launch_delta_prepare(a, prepared, stream);
-    return st == kOk ? launch_delta_chunks(a, prepared, stream) : st;
+    return st == kOk ? launch_delta_chunks(a, prepared, DeltaKept(), stream) : st;
 }
 
 }  // namespace mcc1d

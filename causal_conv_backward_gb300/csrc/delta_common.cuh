@@ -18,8 +18,7 @@ struct DeltaParams {
     int32_t B, H, G, K, V;
     float scale;
     int32_t flags;
-    // written down for the gradients
-    float *u, *states;
+    DeltaKept kept;
 };
 
 inline DeltaParams delta_params(const mcc1d_delta_args &a)

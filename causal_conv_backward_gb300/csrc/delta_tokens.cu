@@ -81,7 +81,7 @@ __device__ __forceinline__ void load_rows(const DeltaParams &p, const float *fro
         }
 }
 template <int J>
-__device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int row0, int l8, const float (&s)[kRR][4 * J])
+__device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int step, int row0, int l8, const float (&s)[kRR][4 * J])
 {
 #pragma unroll
     for (int r = 0; r < kRR; ++r)
@@ -89,7 +89,7 @@ __device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int 
         for (int e = 0; e < 4 * J; ++e) {
             const int row = row0 + 4 * r, at = (e / 4) * 32 + l8 * 4 + e % 4;
             if (row < p.V && at < p.K)
-                to[row * p.K + at] = s[r][e];
+                to[row * step + at] = s[r][e];
         }
 }
 
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_
     load_rows<J>(p, p.state ? p.state + item * VK : nullptr, row0, l8, s);
     for (int64_t t0 = 0; t0 < n; t0 += kGroup) {
         const int live = (int)(n - t0 < kGroup ? n - t0 : kGroup);
-        if (p.states && t0 % kChunk == 0)
-            store_rows<J>(p, p.states + ((t0 / kChunk) * p.B * p.H + item) * VK, row0, l8, s);
+        if (p.kept.states && t0 % kChunk == 0)
+            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.V * p.kept.Kp, p.kept.Kp, row0, l8, s);
         __syncthreads();
         stage<DT, 32 * J>(p, sh, p.v, p.v_s, b, h, first, t0, live);
         __syncthreads();
@@ -157,14 +157,14 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_
                 if (l8 == 0 && row0 + 4 * r < p.V) {
                     if (p.y)
                         p.y[out + row0 + 4 * r] = (uint16_t)pack2<DT>(make_float2(fmaf(u, kq, a * x[kRR + r]), 0.f));
-                    if (p.u)
-                        p.u[out + row0 + 4 * r] = u;
+                    if (p.kept.u)
+                        p.kept.u[((t0 + i) * p.B * p.H + item) * p.kept.Vp + row0 + 4 * r] = u;
                 }
             }
         }
     }
     if (p.final_state)
-        store_rows<J>(p, p.final_state + item * VK, row0, l8, s);
+        store_rows<J>(p, p.final_state + item * VK, p.K, row0, l8, s);
     if (p.y)
         for (int64_t t = n + warp; t < p.S; t += kWarps)
             for (int j = lane; j < kRowsPerBlock; j += 32)
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_bwd_kernel(const __g
     for (int64_t t0 = (n - 1) / kGroup * kGroup; n > 0 && t0 >= 0; t0 -= kGroup) {
         const int live = (int)(n - t0 < kGroup ? n - t0 : kGroup);
         if ((t0 + kGroup) % kChunk == 0 || t0 + kGroup >= n)
-            store_rows<J>(p, p.states + ((t0 / kChunk) * p.B * p.H + item) * VK, row0, l8, s);
+            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.V * p.kept.Kp, p.kept.Kp, row0, l8, s);
         __syncthreads();
         stage<DT, 32 * J>(p, sh, p.grad_y, p.gy_s, b, h, first, t0, live);
         __syncthreads();
@@ -215,13 +215,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_bwd_kernel(const __g
                     s[r][e] = a * fmaf(-gm, k[e], fmaf(gy, q[e], s[r][e]));
                 if (l8 == 0 && row0 + 4 * r < p.V) {
                     p.grad_v[out + row0 + 4 * r] = (uint16_t)pack2<DT>(make_float2(gm, 0.f));
-                    p.u[out + row0 + 4 * r] = du;
+                    p.kept.u[((t0 + i) * p.B * p.H + item) * p.kept.Vp + row0 + 4 * r] = du;
                 }
             }
         }
     }
     if (p.grad_state)
-        store_rows<J>(p, p.grad_state + item * VK, row0, l8, s);
+        store_rows<J>(p, p.grad_state + item * VK, p.K, row0, l8, s);
     for (int64_t t = n + warp; t < p.S; t += kWarps)
         for (int j = lane; j < kRowsPerBlock; j += 32)
             if (first + j < p.V)
@@ -235,20 +235,20 @@ dim3 token_grid(const DeltaParams &p)
 
 }  // namespace
 
-int32_t launch_delta_tokens(const mcc1d_delta_args &a, float *u, float *states, cudaStream_t stream)
+int32_t launch_delta_tokens(const mcc1d_delta_args &a, const DeltaKept &kept, cudaStream_t stream)
 {
     DeltaParams p = delta_params(a);
-    p.u = u, p.states = states;
+    p.kept = kept;
     const auto go = [&](auto kernel) { return launch(kernel, token_grid(p), kWarps * 32, 0, stream, p); };
     if (a.dtype == 0)
         return a.K <= 64 ? go(delta_tokens_kernel<0, 2>) : go(delta_tokens_kernel<0, 4>);
     return a.K <= 64 ? go(delta_tokens_kernel<1, 2>) : go(delta_tokens_kernel<1, 4>);
 }
 
-int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, float *du, float *grads, cudaStream_t stream)
+int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, const DeltaKept &kept, cudaStream_t stream)
 {
     DeltaParams p = delta_params(a.fwd);
-    p.u = du, p.states = grads;
+    p.kept = kept;
     p.grad_y = static_cast<const uint16_t *>(a.grad_y), p.grad_v = static_cast<uint16_t *>(a.grad_v);
     p.grad_final = a.grad_final_state, p.grad_state = a.grad_state;
     for (int i = 0; i < 3; ++i)
