@@ -15,17 +15,18 @@ constexpr int kChunk = 64;                 // tokens whose products are taken to
 constexpr double kUnitEps = 1e-6;          // under the root of |q|^2, |k|^2
 
 // What a pass over the tokens writes down for the gradients: u(t) or du(t)
-// [S,B,H,Vp], and the states (or their gradients) at chunks' ends [chunks][B H][V,Kp].
+// [S,B,H,Vp], and the states (or their gradients) at chunks' ends
+// [chunks][B H][K,Vp].
 struct DeltaKept {
     float *u, *states;
-    int32_t Vp, Kp;                        // V and K to a multiple of four
+    int32_t Vp;                            // V to a multiple of four
 };
 
 // Workspace of the backward, in bytes from its start.
 struct DeltaBwdPlan {
     bool tokens;                           // token by token
     int64_t chunks;                        // ceil(S / kChunk)
-    int32_t Vp, Kp;
+    int32_t Vp;
     uint64_t off_u, off_du;                // u(t) and its gradient
     uint64_t off_s, off_g;                 // states before each chunk, gradients of those after it
     uint64_t off_sums;                     // grad_A, grad_delta_bias of each (chunk, sequence): [2][chunks B][H]
@@ -36,12 +37,14 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
 
 // What the products of a chunk need beside q, k and v, for each (b, h, chunk):
 // T and P T as fp16 terms in the panels that the tensor cores read, the factors
-// of its tokens, and in the row kFactorEnd its decay and the most that a row's
-// R and U can be of its v and state (delta_prepare.cu).
+// of its tokens, and in the row kFactorEnd what is one value (delta_prepare.cu).
 constexpr int kPanelBytes = kChunk * 128;
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
        kFactorT, kFactors };
-enum { kEndDecay, kEndOfV, kEndOfState, kEndOfR };      // in that row
+// In that row: the chunk's decay; what bounds a row's R (of its v and state), U
+// (of R), and backwards the state's part of du and of du as an operand, grad_y's
+// part of that; the largest factor of q.
+enum { kEndDecay, kEndOfV, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
 constexpr int kChunkBytes = 4 * kPanelBytes + kFactors * kChunk * 4;
 
 struct DeltaPlan {
@@ -53,6 +56,7 @@ DeltaPlan delta_plan(const mcc1d_delta_args &a);
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream);
+int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream);
 int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream);
 int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream);

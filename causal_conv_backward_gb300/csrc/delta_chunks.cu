@@ -19,17 +19,13 @@
 // warps of its own. Warps 0 to 7 hold the rows, 8 to 11 write Y, 12 issues the
 // products, 13 copies the tokens of the chunk after the next, 14 to 19 make
 // panels of the next one's.
-#include "delta_common.cuh"
-#include "tensor_core.cuh"
-#include "tensor_map.h"
+#include "delta_chunks.cuh"
 
 namespace mcc1d {
 
 namespace {
 
-constexpr int kC = kChunk, kRows = 128, kParts = 4, kStages = 2;
-constexpr int kRowWarps = 4 * kParts, kLoadWarps = 6, kLoadThreads = 32 * kLoadWarps, kThreads = 32 * (kRowWarps + 4 + 2 + kLoadWarps);
-constexpr int kProductWarp = kRowWarps + 4, kCopyWarp = kProductWarp + 1;
+constexpr int kStages = 2;
 // Registers by warpgroup: rows (four), Y, and two for the rest.
 constexpr int kRegRows = 80, kRegY = 64, kRegRest = 56, kRegLaunch = 72;
 static_assert(kParts * kRegRows + kRegY + 2 * kRegRest <= kThreads / 128 * kRegLaunch, "what the block is launched with");
@@ -63,36 +59,6 @@ struct ChunkShared {
     float most[kParts][kRows], most_v[kParts][kRows], sum_u[kParts][kRows];      // of the parts of a row
     uint32_t tmem, failed;
 };
-
-// A wait of a whole warp; false where it gave up.
-__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity)
-{
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded_inline(smem_u32(&bar), parity));
-}
-__device__ __forceinline__ void warp_arrive(uint64_t &bar)
-{
-    __syncwarp();
-    if (threadIdx.x % 32 == 0)
-        mbar_arrive(smem_u32(&bar));
-}
-
-// Piece `piece` of a token's row: eight 16-bit values, from the copied rows in
-// shared memory or, where they could not be copied, from global memory one by
-// one; zeros behind the row's and the sequence's end.
-__device__ __forceinline__ uint4 piece_of(const uint8_t *copied, const uint16_t *row, bool vectors, int live)
-{
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (live > 0 && vectors)
-        r = *reinterpret_cast<const uint4 *>(copied);
-    if (live > 0 && !vectors) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(&r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live)
-                w[i / 2] |= (uint32_t)__ldg(row + i) << (16 * (i % 2));
-    }
-    return r;
-}
 
 // A chunk's rows of q or k as scaled fp16 in panels. A thread has one piece of
 // every STEPth row.
@@ -128,42 +94,6 @@ __device__ __forceinline__ void pair_values(uint8_t *pairs, const uint8_t *copie
         to[0] = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
         to[1] = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410), __byte_perm(x.w, y.w, 0x7632));
     }
-}
-
-// Scaled values of a row as terms in N / 2 columns from `hi` and `lo` on.
-template <int N>
-__device__ __forceinline__ void put_terms(const float *x, uint32_t hi, uint32_t lo)
-{
-    uint32_t h[N / 2], l[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e)
-        two_terms(make_float2(x[2 * e], x[2 * e + 1]), h[e], l[e]);
-    tmem_store(hi, h);
-    tmem_store(lo, l);
-}
-// What is stored is there for the products that are issued after an arrival.
-__device__ __forceinline__ void terms_done(uint64_t &bar)
-{
-    tmem_wait_stores();
-    tmem_fence_before();
-    warp_arrive(bar);
-}
-
-template <int N>
-__device__ __forceinline__ float most_of(const float (&x)[N])
-{
-    float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        m[i % 4] = fmaxf(m[i % 4], fabsf(x[i]));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-
-__device__ __forceinline__ void rows_meet() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory"); }
-__device__ __forceinline__ float most_of_parts(const float (&x)[kParts][kRows], int r)
-{
-    static_assert(kParts == 4, "four parts of a row");
-    return fmaxf(fmaxf(x[0][r], x[1][r]), fmaxf(x[2][r], x[3][r]));
 }
 
 // ------------------------------------------------------------------ the rows
@@ -212,23 +142,16 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
 #pragma unroll
             for (int k = 0; k < HK; ++k)
                 s[k] = __uint_as_float(0x7FFFFFFFu);
-        float *to = i == chunks ? p.final_state : p.kept.states;
-        if (to && mine) {
+        if (i < chunks && p.kept.states && mine) {
             const float of = inverse_scale(scale_s);
-            to += i == chunks ? item * VK + (int64_t)row * p.K : ((i * BH + item) * p.V + row) * p.kept.Kp;
-            to += part * HK;
-            if (cp.vectors_s || i < chunks) {
+            float *to = p.kept.states + ((i * BH + item) * p.K + part * HK) * p.kept.Vp + row;
 #pragma unroll
-                for (int k = 0; k < HK; k += 4)
-                    if (part * HK + k < p.K)
-                        *reinterpret_cast<float4 *>(to + k) = make_float4(s[k] * of, s[k + 1] * of, s[k + 2] * of, s[k + 3] * of);
-            } else {
-#pragma unroll
-                for (int k = 0; k < HK; ++k)
-                    if (part * HK + k < p.K)
-                        to[k] = s[k] * of;
-            }
+            for (int k = 0; k < HK; ++k, to += p.kept.Vp)
+                if (part * HK + k < p.K)
+                    *to = s[k] * of;
         }
+        if (i >= chunks && p.final_state && mine)
+            write_row<HK>(p.final_state + item * VK + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
         if (i >= chunks)
             break;
         const uint8_t *stage = stages + (i % kStages) * St::kBytes;
@@ -614,9 +537,9 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, 
     p.prepared = prepared;
     p.chunks = (a.S + kChunk - 1) / kChunk;
     p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
-    p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides);
-    p.vectors_k = token_tiles(&p.map_k, a.k, a.S, a.B, a.G, a.K, a.k_strides);
-    p.vectors_v = token_tiles(&p.map_v, a.v, a.S, a.B, a.H, a.V, a.v_strides);
+    p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides, false);
+    p.vectors_k = token_tiles(&p.map_k, a.k, a.S, a.B, a.G, a.K, a.k_strides, false);
+    p.vectors_v = token_tiles(&p.map_v, a.v, a.S, a.B, a.H, a.V, a.v_strides, false);
     p.pairs_y = a.V % 2 == 0 && ((uintptr_t)a.y & 3u) == 0;
     p.vectors_s = a.K % 4 == 0 && ((uintptr_t)a.final_state & 15u) == 0;
     if (a.dtype == 0)

@@ -1,0 +1,538 @@
+// delta_chunks_bwd.cu - the gradients of the gated delta rule's states, from
+// the last chunk to the first, on the tensor cores.
+//
+// A block has up to 128 rows of one head's gradient G [V,K] of the state after
+// the chunk, as delta_chunks.cu has the state. With the factors of
+// delta_prepare.cu, D0 = e^(c(end)-c) G K^T, every chunk is
+//   dU through the later tokens: dR = D0 T + grad_y (P T)    (tokens along the columns)
+//   grad_v = b dR
+//   G = e^c(end) G + grad_y^T (e^c Q) - (dR b e^c) K
+// grad_y is exact in fp16 (a chunk's values scaled by a power of two) and is
+// multiplied from shared memory; e^c Q is two fp16 terms there. The chain is
+// G - D0 - dR - G; the products with grad_y run in its gaps. Warps 0 to 15 hold
+// the rows, 16 to 19 write dR and grad_v, 20 issues the products, 21 copies the
+// tiles, 22 to 27 make operands of them where they lie.
+#include "delta_chunks.cuh"
+
+namespace mcc1d {
+
+namespace {
+
+constexpr int kStages = 2;
+// Registers by warpgroup: rows (four), the ones that write, and two for the rest.
+constexpr int kRegRows = 72, kRegOut = 112, kRegRest = 48, kRegLaunch = 72;
+static_assert(kParts * kRegRows + kRegOut + 2 * kRegRest <= kThreads / 128 * kRegLaunch && kRegRows == kRegLaunch, "what the block is launched with");
+
+struct BackParams {
+    CUtensorMap map_q, map_k, map_y;    // where rows can be copied as tiles
+    DeltaParams d;
+    const uint8_t *prepared;
+    int64_t chunks;
+    int32_t tiles;            // of 128 rows of V
+    bool vectors_q, vectors_k, vectors_y, vectors_s;
+    bool pairs_v;             // two rows of grad_v are one word
+};
+
+template <int KP>
+struct Stage {
+    static constexpr int kPanels = KP / 64 * kPanelBytes;
+    static constexpr int K = 0, QHi = kPanels, QLo = 2 * kPanels, Y = 3 * kPanels, kPrepared = Y + kRows / 64 * kPanelBytes;
+    static constexpr int kBytes = kPrepared + (kChunkBytes + 1023) / 1024 * 1024;
+    static_assert(kBytes % 1024 == 0, "panels on 1024 bytes");
+};
+
+// Columns of tensor memory: sums, then operands (pairs of fp16). D0 and dR
+// follow on one another and share theirs; G's update is summed over X and U.
+enum { kX = 0, kU = 64, kYP = 128, kYQ = 192, kGHi = 320, kGLo = 384, kWHi = 448, kWLo = 480, kColumns = 512 };
+
+struct BackShared {
+    uint64_t full[kStages], empty[kStages], tiles[kStages], x, r, u, v, s, end, out;
+    float of_u[2][kRows];                       // of the last two chunks: what a row's sums are multiplied by
+    float of_out[4][kC], of_p[4];               // of the last four chunks: b, and the factor of grad_y (P T)
+    float of_y[4], of_yq[4], most_y[4];         // grad_y's factor, that of grad_y Q, the largest |grad_y|
+    float most[kParts][kRows], sum_r[kParts][kRows];
+    float most_of_warps[2][kLoadWarps];
+    uint32_t tmem, failed;
+};
+
+// ------------------------------------------------------------------ the rows
+template <int DT, int KP>
+__device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, const uint8_t *stages, int item, int v0, int64_t chunks)
+{
+    typedef Stage<KP> St;
+    constexpr int HK = KP / kParts, HC = kC / kParts, UNIT = HK < 32 ? HK : 32;
+    static_assert(HC == 16, "sixteen tokens to a thread");
+    const DeltaParams &p = cp.d;
+    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, VK = (int64_t)p.V * p.K;
+    const bool mine = row < p.V;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+    float s[HK];             // the gradient times `scale_s`, a power of two
+    {
+        const float *from = p.grad_final + item * VK + (int64_t)row * p.K + part * HK;
+#pragma unroll
+        for (int k = 0; k < HK; ++k)
+            s[k] = p.grad_final && mine && part * HK + k < p.K ? from[k] : 0.f;
+    }
+    // scales come from bounds, as in delta_chunks.cu
+    sh.most[part][r] = most_of(s);
+    rows_meet();
+    float scale_s = scale_for(most_of_parts(sh.most, r));
+    rows_meet();
+#pragma unroll
+    for (int k = 0; k < HK; ++k)
+        s[k] *= scale_s;
+    const uint32_t terms_s = lanes + kGHi + HK / 2 * part, terms_w = lanes + kWHi + HC / 2 * part;
+    if (chunks > 0) {
+#pragma unroll
+        for (int c = 0; c < HK; c += UNIT)
+            put_terms<UNIT>(s + c, terms_s + c / 2, terms_s + (kGLo - kGHi) + c / 2);
+        terms_done(sh.s);
+    }
+    bool ok = true;          // no wait gave up
+    for (int64_t i = 0;; ++i) {          // the chunks counted from the last
+        const uint32_t parity = (uint32_t)(i & 1);
+        if (!ok)
+#pragma unroll
+            for (int k = 0; k < HK; ++k)
+                s[k] = __uint_as_float(0x7FFFFFFFu);
+        if (i < chunks && mine) {
+            const float of = inverse_scale(scale_s);
+            float *to = p.kept.states + (((chunks - 1 - i) * BH + item) * p.K + part * HK) * p.kept.Vp + row;
+#pragma unroll
+            for (int k = 0; k < HK; ++k, to += p.kept.Vp)
+                if (part * HK + k < p.K)
+                    *to = s[k] * of;
+        }
+        if (i >= chunks) {
+            if (p.grad_state && mine)
+                write_row<HK>(p.grad_state + item * VK + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
+            break;
+        }
+        const uint8_t *stage = stages + (i % kStages) * St::kBytes;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
+        f += part * HC;
+        ok = warp_wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1);
+        sh.most[part][r] = most_of(s);
+        rows_meet();
+        if (sh.failed) {         // all rows leave together; theirs are NaN
+            ok = false;
+            i = chunks - 1;
+            continue;
+        }
+        const float of_s = inverse_scale(scale_s), most_s = most_of_parts(sh.most, r) * of_s, most_y = sh.most_y[i & 3];
+        const float scale_u = scale_for(ends[kEndOfGrad] * most_s), of_u = inverse_scale(scale_u);
+        const float scale_r = scale_for(fmaf(ends[kEndDuOfGrad], most_s, ends[kEndDuOfY] * most_y)), of_r = inverse_scale(scale_r);
+        const float of_yp = sh.of_y[i & 3] * f[kFactorP * kC], of_yq = sh.of_yq[i & 3], end = ends[kEndDecay];
+        if (part == 0)
+            sh.of_u[parity][r] = of_u;
+        ok = ok && warp_wait(sh.x, parity);
+        tmem_fence_after();
+        uint32_t raw[HC];
+        float x[HC];
+        tmem_load(lanes + kX + HC * part, raw);
+        tmem_wait(raw);
+        {
+            const float2 m = make_float2(of_s * scale_u, of_s * scale_u);
+#pragma unroll
+            for (int t = 0; t < HC; t += 2) {
+                const float2 ft = *reinterpret_cast<const float2 *>(f + kFactorU * kC + t);
+                const float2 a = mul2(mul2(ft, m), make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])));
+                x[t] = a.x, x[t + 1] = a.y;
+            }
+        }
+        put_terms<HC>(x, terms_w, terms_w + (kWLo - kWHi));
+        terms_done(sh.r);
+        ok = ok && warp_wait(sh.u, parity);
+        tmem_fence_after();
+        float2 sum = make_float2(0.f, 0.f);
+        {
+            uint32_t yp[HC];
+            tmem_load(lanes + kU + HC * part, raw);
+            tmem_load(lanes + kYP + HC * part, yp);
+            tmem_wait(raw), tmem_wait(yp);
+            const float2 mu = make_float2(-of_u * scale_r, -of_u * scale_r), my = make_float2(-of_yp * scale_r, -of_yp * scale_r);
+#pragma unroll
+            for (int t = 0; t < HC; t += 2) {
+                const float2 ft = *reinterpret_cast<const float2 *>(f + kFactorX * kC + t);
+                const float2 a = mul2(ft, fma2(mu, make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])),
+                                               mul2(my, make_float2(__uint_as_float(yp[t]), __uint_as_float(yp[t + 1])))));
+                sum = add2(sum, make_float2(fabsf(a.x), fabsf(a.y)));
+                x[t] = a.x, x[t + 1] = a.y;
+            }
+        }
+        sh.sum_r[part][r] = sum.x + sum.y;
+        put_terms<HC>(x, terms_w, terms_w + (kWLo - kWHi));
+        terms_done(sh.v);
+        warp_arrive(sh.empty[i % kStages]);
+        rows_meet();     // for sum_r, while the products run
+        // |G| <= e^c(end) |G| + sum of |dR k| + 64 |grad_y| |q|, and no |k|, |q| is above 2^16 as an operand
+        const float before = scale_s;
+        scale_s = scale_for(fmaf(fabsf(end), most_s, ((sh.sum_r[0][r] + sh.sum_r[1][r]) + (sh.sum_r[2][r] + sh.sum_r[3][r])) * of_r * 65536.f) +
+                            most_y * (kC * 65536.f) * (of_yq / sh.of_y[i & 3]));
+        const float2 keep = make_float2(end * inverse_scale(before) * scale_s, end * inverse_scale(before) * scale_s);
+        const float2 add = make_float2(of_r * scale_s, of_r * scale_s), add_y = make_float2(of_yq * scale_s, of_yq * scale_s);
+        ok = ok && warp_wait(sh.end, parity);
+        tmem_fence_after();
+        if (!ok)
+            sh.failed = 1;
+#pragma unroll
+        for (int c = 0; c < HK; c += 16) {
+            uint32_t yq[16];
+            tmem_load(lanes + kX + HK * part + c, raw);
+            tmem_load(lanes + kYQ + HK * part + c, yq);
+            tmem_wait(raw), tmem_wait(yq);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                float2 o = fma2(add, make_float2(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), mul2(keep, make_float2(s[c + k], s[c + k + 1])));
+                o = fma2(add_y, make_float2(__uint_as_float(yq[k]), __uint_as_float(yq[k + 1])), o);
+                s[c + k] = o.x, s[c + k + 1] = o.y;
+            }
+            if (i + 1 < chunks)
+                put_terms<16>(s + c, terms_s + c / 2, terms_s + (kGLo - kGHi) + c / 2);
+        }
+        if (i + 1 < chunks)
+            terms_done(sh.s);
+    }
+}
+
+// ------------------------------------------------------------------ dR and grad_v
+template <int DT>
+__device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh, int item, int v0, int64_t n, int64_t chunks)
+{
+    const DeltaParams &p = cp.d;
+    const int r = threadIdx.x % kRows, row = v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, step = BH * p.V, step_u = BH * p.kept.Vp;
+    const bool mine = row < p.V, odd = r & 1;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (threadIdx.x / 32 % 4)) << 16);
+    // tokens of no chunk
+    uint16_t *to = p.grad_v + (int64_t)item * p.V + row;
+    if (mine)
+        for (int64_t t = chunks * kC; t < p.S; ++t)
+            to[t * step] = 0;
+    int64_t i = 0;
+    for (; i < chunks; ++i) {
+        if (!warp_wait(sh.u, (uint32_t)(i & 1)))
+            break;
+        tmem_fence_after();
+        const int64_t t0 = (chunks - 1 - i) * kC;
+        const float of_u = sh.of_u[i & 1][r], of_p = sh.of_p[i & 3];
+        const float *bt = sh.of_out[i & 3];
+        const int live = (int)(n - t0 < kC ? n - t0 : kC), rows = (int)(p.S - t0 < kC ? p.S - t0 : kC);
+        const bool whole = cp.pairs_v && rows == kC && live == kC;
+        uint32_t dr[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t y[16];
+            tmem_load(lanes + kU + 16 * c, dr[c]);
+            tmem_load(lanes + kYP + 16 * c, y);
+            tmem_wait(dr[c]), tmem_wait(y);
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+                dr[c][t] = __float_as_uint(fmaf(of_u, __uint_as_float(dr[c][t]), of_p * __uint_as_float(y[t])));
+        }
+        tmem_fence_before();
+        warp_arrive(sh.out);
+        float *to_u = p.kept.u + (t0 * BH + item) * p.kept.Vp + row;
+        uint16_t *at = to + t0 * step, *pair = odd ? at + step - 1 : at;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (whole) {
+#pragma unroll
+                for (int t = 0; t < 16; t += 2, to_u += 2 * step_u, pair += 2 * step) {
+                    const float a = __uint_as_float(dr[c][t]), e = __uint_as_float(dr[c][t + 1]);
+                    if (mine)
+                        to_u[0] = a, to_u[step_u] = e;
+                    const uint32_t both = pack2<DT>(make_float2(a * bt[16 * c + t], e * bt[16 * c + t + 1]));
+                    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, both, 1);
+                    if (mine)       // two rows of one token: even lanes the first, odd lanes the second
+                        *reinterpret_cast<uint32_t *>(pair) = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 16; ++t, to_u += step_u, at += step) {
+                    const float a = __uint_as_float(dr[c][t]);
+                    const bool there = 16 * c + t < live;
+                    if (mine && there)
+                        *to_u = a;
+                    if (mine && 16 * c + t < rows)
+                        *at = there ? (uint16_t)pack2<DT>(make_float2(a * bt[16 * c + t], 0.f)) : (uint16_t)0;
+                }
+            }
+        }
+    }
+    if (mine && i < chunks)         // a wait gave up
+        for (int64_t t = 0; t < (chunks - i) * kC && t < p.S; ++t)
+            to[t * step] = 0x7FFF;
+}
+
+// ------------------------------------------------------------------ products
+template <int KP>
+__device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, int64_t chunks)
+{
+    typedef Stage<KP> St;
+    constexpr uint32_t by_rows = mma_kind(kC, false), by_columns = mma_kind(KP, true), tokens_by_columns = mma_kind(kC, true);
+    constexpr uint32_t y_tokens = mma_kind(kC, true, true), y_keys = mma_kind(KP, true, true);
+    const uint32_t tmem = sh.tmem;
+    const auto wait = [](uint64_t &bar, uint32_t parity) { return mbar_wait_bounded_inline(smem_u32(&bar), parity); };
+    for (int64_t i = 0; i < chunks; ++i) {
+        const uint32_t parity = (uint32_t)(i & 1), stage = stages + (uint32_t)(i % kStages) * St::kBytes;
+        if (!wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1) || !wait(sh.s, parity))
+            break;
+        tmem_fence_after();
+#pragma unroll
+        for (int j = 0; j < KP / 16; ++j) {
+            const uint64_t k = desc_rows(stage + St::K + (j / 4) * kPanelBytes) + 2 * (j % 4);
+            mma_ts(tmem + kX, tmem + kGHi + 8 * j, k, by_rows, j > 0);
+            mma_ts(tmem + kX, tmem + kGLo + 8 * j, k, by_rows, true);
+        }
+        mma_commit(smem_u32(&sh.x));
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t step = (uint64_t)(2048 * j >> 4), y = desc_columns(stage + St::Y, kPanelBytes) + step;
+            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + 2 * kPanelBytes, kPanelBytes) + step, y_tokens, j > 0);
+            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + 3 * kPanelBytes, kPanelBytes) + step, y_tokens, true);
+        }
+        if (!wait(sh.r, parity))
+            break;
+        tmem_fence_after();
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t step = (uint64_t)(2048 * j >> 4), hi = desc_columns(stage + St::kPrepared, kPanelBytes) + step;
+            const uint64_t lo = desc_columns(stage + St::kPrepared + kPanelBytes, kPanelBytes) + step;
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, hi, tokens_by_columns, j > 0);
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, lo, tokens_by_columns, true);
+            mma_ts(tmem + kU, tmem + kWLo + 8 * j, hi, tokens_by_columns, true);
+        }
+        mma_commit(smem_u32(&sh.u));
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t step = (uint64_t)(2048 * j >> 4), y = desc_columns(stage + St::Y, kPanelBytes) + step;
+            mma_ss(tmem + kYQ, y, desc_columns(stage + St::QHi, kPanelBytes) + step, y_keys, j > 0);
+            mma_ss(tmem + kYQ, y, desc_columns(stage + St::QLo, kPanelBytes) + step, y_keys, true);
+        }
+        if (!wait(sh.v, parity) || !wait(sh.out, parity))
+            break;
+        tmem_fence_after();
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j) {
+            const uint64_t k = desc_columns(stage + St::K, kPanelBytes) + (uint64_t)(2048 * j >> 4);
+            mma_ts(tmem + kX, tmem + kWHi + 8 * j, k, by_columns, j > 0);
+            mma_ts(tmem + kX, tmem + kWLo + 8 * j, k, by_columns, true);
+        }
+        mma_commit(smem_u32(&sh.end));
+        mma_commit(smem_u32(&sh.empty[i % kStages]));
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+template <int KP>
+__device__ __forceinline__ void copy_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, int item, int b, int h, int v0, int64_t chunks)
+{
+    typedef Stage<KP> St;
+    const DeltaParams &p = cp.d;
+    const int g = h / (p.H / p.G);
+    const bool k = cp.vectors_k, q = cp.vectors_q, y = cp.vectors_y;
+    for (int64_t i = 0; i < chunks; ++i) {
+        if (!warp_wait(sh.empty[i % kStages], (uint32_t)(i / kStages + 1) & 1))
+            break;
+        if (threadIdx.x % 32 == 0) {
+            const int64_t chunk = chunks - 1 - i;
+            const uint32_t stage = smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes, bar = smem_u32(&sh.tiles[i % kStages]);
+            const int t0 = (int)(chunk * kC), values = p.V - v0 > 64 ? 2 : 1;
+            mbar_arrive_expect_tx(bar, kChunkBytes + ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (y ? values : 0)) * kPanelBytes);
+            bulk_g2s(stage + St::kPrepared, cp.prepared + (item * cp.chunks + chunk) * kChunkBytes, kChunkBytes, bar);
+            for (int j = 0; j < KP / 64; ++j) {
+                if (k)
+                    tile_g2s(stage + St::K + j * kPanelBytes, &cp.map_k, 64 * j, t0, g, b, bar);
+                if (q)
+                    tile_g2s(stage + St::QHi + j * kPanelBytes, &cp.map_q, 64 * j, t0, g, b, bar);
+            }
+            for (int j = 0; y && j < values; ++j)
+                tile_g2s(stage + St::Y + j * kPanelBytes, &cp.map_y, v0 + 64 * j, t0, h, b, bar);
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ uint4 scaled_half(const float2 (&x)[4], float by)
+{
+    const float2 f = make_float2(by, by);
+    return make_uint4(pack_half2(mul2(x[0], f)), pack_half2(mul2(x[1], f)), pack_half2(mul2(x[2], f)), pack_half2(mul2(x[3], f)));
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4 &v, float2 (&x)[4])
+{
+    x[0] = unpack2<DT>(v.x), x[1] = unpack2<DT>(v.y), x[2] = unpack2<DT>(v.z), x[3] = unpack2<DT>(v.w);
+}
+
+template <int DT, int KP>
+__device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, int b, int h, int v0, int64_t n, int64_t chunks)
+{
+    typedef Stage<KP> St;
+    const DeltaParams &p = cp.d;
+    const int thread = threadIdx.x - (kThreads - kLoadThreads), g = h / (p.H / p.G);
+    for (int64_t i = 0; i < chunks; ++i) {
+        const int64_t t0 = (chunks - 1 - i) * kC;
+        const int live = (int)(n - t0 < kC ? n - t0 : kC);
+        uint8_t *stage = stages + (i % kStages) * St::kBytes;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
+        if (!warp_wait(sh.tiles[i % kStages], (uint32_t)(i / kStages) & 1))
+            break;
+        // grad_y: its largest value first
+        constexpr int PIECES_Y = kRows / 8, STEP_Y = kLoadThreads / PIECES_Y, PIECES = KP / 8, STEP = kLoadThreads / PIECES;
+        const uint16_t *gy = p.grad_y + t0 * p.gy_s[0] + b * p.gy_s[1] + h * p.gy_s[2] + v0;
+        const int piece_y = thread % PIECES_Y, live_y = p.V - v0 - 8 * piece_y;
+        uint8_t *panel_y = stage + St::Y + (piece_y / 8) * kPanelBytes;
+        float most = 0.f;
+#pragma unroll 2
+        for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
+            uint8_t *at = panel_y + panel_at(t, piece_y % 8);
+            float2 x[4];
+            unpack8<DT>(piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                most = fmaxf(most, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2)
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        if (thread % 32 == 0)
+            sh.most_of_warps[i & 1][thread / 32] = most;
+        asm volatile("bar.sync 2, %0;" ::"n"(kLoadThreads) : "memory");
+        most = sh.most_of_warps[i & 1][0];
+#pragma unroll
+        for (int w = 1; w < kLoadWarps; ++w)
+            most = fmaxf(most, sh.most_of_warps[i & 1][w]);
+        const float scale_y = scale_for(most);
+        const float scale_q = scale_for(f[kFactorEnd * kC + kEndMostQ] * 32768.f);       // rows of q are below 2^15 as operands
+        if (thread == 0) {
+            sh.of_y[i & 3] = inverse_scale(scale_y), sh.of_yq[i & 3] = inverse_scale(scale_y) * inverse_scale(scale_q), sh.most_y[i & 3] = most;
+            sh.of_p[i & 3] = inverse_scale(scale_y) * f[kFactorP * kC];
+        }
+        if (thread < kC)
+            sh.of_out[i & 3][thread] = f[kFactorB * kC + thread];
+#pragma unroll 2
+        for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
+            uint8_t *at = panel_y + panel_at(t, piece_y % 8);
+            float2 x[4];
+            unpack8<DT>(piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
+            *reinterpret_cast<uint4 *>(at) = scaled_half(x, scale_y);
+        }
+        const int piece = thread % PIECES, live_k = p.K - 8 * piece;
+        const uint16_t *k = p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] + 8 * piece, *q = p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2] + 8 * piece;
+        const int panel = (piece / 8) * kPanelBytes;
+#pragma unroll 1
+        for (int t = thread / PIECES; t < kC; t += STEP) {
+            const uint32_t off = panel + panel_at(t, piece % 8);
+            float2 x[4];
+            unpack8<DT>(piece_of(stage + St::K + off, k + t * p.k_s[0], cp.vectors_k, t < live ? live_k : 0), x);
+            *reinterpret_cast<uint4 *>(stage + St::K + off) = scaled_half(x, f[kFactorScaleK * kC + t]);
+            unpack8<DT>(piece_of(stage + St::QHi + off, q + t * p.q_s[0], cp.vectors_q, t < live ? live_k : 0), x);
+            const float by = f[kFactorScaleQ * kC + t], of = f[kFactorQ * kC + t] * scale_q;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                two_terms(mul2(mul2(x[e], make_float2(by, by)), make_float2(of, of)), hi[e], lo[e]);
+            *reinterpret_cast<uint4 *>(stage + St::QHi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(stage + St::QLo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        shared_to_async();
+        warp_arrive(sh.full[i % kStages]);
+    }
+}
+
+template <int DT, int KP>
+__global__ void __launch_bounds__(kThreads, 1) delta_chunks_bwd_kernel(const __grid_constant__ BackParams cp)
+{
+    extern __shared__ uint8_t raw_shared[];
+    __shared__ BackShared sh;
+    uint8_t *stages = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
+    const DeltaParams &p = cp.d;
+    const int tid = threadIdx.x, warp = tid / 32, group = warp / 4;
+    const int item = blockIdx.x / cp.tiles, v0 = (blockIdx.x % cp.tiles) * kRows, b = item / p.H, h = item % p.H;
+    const int64_t n = clamped_length(p.lengths, b, p.S), chunks = (n + kC - 1) / kC;
+
+    if (tid == 0) {
+        sh.failed = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), kLoadWarps);
+            mbar_init(smem_u32(&sh.empty[i]), kRowWarps + 1);
+            mbar_init(smem_u32(&sh.tiles[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.x), 1), mbar_init(smem_u32(&sh.u), 1), mbar_init(smem_u32(&sh.end), 1);
+        mbar_init(smem_u32(&sh.r), kRowWarps), mbar_init(smem_u32(&sh.v), kRowWarps), mbar_init(smem_u32(&sh.s), kRowWarps);
+        mbar_init(smem_u32(&sh.out), 4);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kProductWarp)
+        tmem_alloc(smem_u32(&sh.tmem), kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+
+    if (group < kParts) {
+        hold_rows<DT, KP>(cp, sh, stages, item, v0, chunks);
+    } else if (group == kParts) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegOut));
+        write_rows<DT>(cp, sh, item, v0, n, chunks);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
+        if (warp > kCopyWarp)
+            make_tiles<DT, KP>(cp, sh, stages, b, h, v0, n, chunks);
+        else if (warp == kCopyWarp)
+            copy_tiles<KP>(cp, sh, stages, item, b, h, v0, chunks);
+        else if (tid % 32 == 0)
+            issue_products<KP>(sh, smem_u32(stages), chunks);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kProductWarp) {
+        tmem_fence_after();
+        tmem_free(sh.tmem, kColumns);
+    }
+}
+
+template <int DT, int KP>
+int32_t chunks_of(const BackParams &p, cudaStream_t stream)
+{
+    constexpr int bytes = kStages * Stage<KP>::kBytes + 1024;
+    // the registers of the warps that write come out of what the block starts
+    // with: an increase past that would wait for ever
+    static const bool fits = [] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, delta_chunks_bwd_kernel<DT, KP>) == cudaSuccess && fa.numRegs == kRegLaunch;
+    }();
+    if (!fits)
+        return kErrCuda;
+    if (cudaFuncSetAttribute(delta_chunks_bwd_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return kErrCuda;
+    return launch(delta_chunks_bwd_kernel<DT, KP>, dim3((unsigned)((int64_t)p.d.B * p.d.H * p.tiles)), kThreads, bytes, stream, p);
+}
+
+}  // namespace
+
+int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream)
+{
+    const mcc1d_delta_args &f = a.fwd;
+    BackParams p = {};
+    p.d = delta_params(f);
+    p.d.kept = kept;
+    p.d.grad_y = static_cast<const uint16_t *>(a.grad_y), p.d.grad_v = static_cast<uint16_t *>(a.grad_v);
+    p.d.grad_final = a.grad_final_state, p.d.grad_state = a.grad_state;
+    for (int i = 0; i < 3; ++i)
+        p.d.gy_s[i] = a.grad_y_strides[i];
+    p.prepared = prepared;
+    p.chunks = (f.S + kChunk - 1) / kChunk;
+    p.tiles = (int32_t)((f.V + kRows - 1) / kRows);
+    p.vectors_q = token_tiles(&p.map_q, f.q, f.S, f.B, f.G, f.K, f.q_strides, true);
+    p.vectors_k = token_tiles(&p.map_k, f.k, f.S, f.B, f.G, f.K, f.k_strides, true);
+    p.vectors_y = token_tiles(&p.map_y, a.grad_y, f.S, f.B, f.H, f.V, a.grad_y_strides, true);
+    p.vectors_s = f.K % 4 == 0 && ((uintptr_t)a.grad_state & 15u) == 0;
+    p.pairs_v = f.V % 2 == 0 && ((uintptr_t)a.grad_v & 3u) == 0;
+    if (f.dtype == 0)
+        return f.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
+    return f.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);
+}
+
+}  // namespace mcc1d

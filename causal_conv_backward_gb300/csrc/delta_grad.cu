@@ -24,8 +24,8 @@ constexpr int kC = kChunk, kVT = 32, kThreads = 256, kTri = kC + 4, kVS = kVT + 
 
 struct GradParams {
     DeltaParams d;
-    const float *u, *du, *s, *g;   // [S,B,H,Vp], [chunks][B H][V,Kp]
-    int32_t Kp, Vp;
+    const float *u, *du, *s, *g;   // [S,B,H,Vp], [chunks][B H][K,Vp]
+    int32_t Vp;
     bool vectors_gy, vectors_v;
     uint16_t *grad_q, *grad_k, *grad_delta, *grad_beta;
     float *sum_A, *sum_bias;       // [chunks B][H]
@@ -35,8 +35,7 @@ struct GradParams {
 // four columns (or the other way round) of a fragment lie on different banks.
 template <int KP>
 struct GradTile {
-    static constexpr int KS = KP + 8;
-    float u[kC][kVS], du[kC][kVS], s[kVT][KS], g[kVT][KS];
+    float u[kC][kVS], du[kC][kVS], s[KP][kVS], g[KP][kVS];
     uint16_t gy[kC][kRaw], v[kC][kRaw];
 };
 template <int KP>
@@ -127,15 +126,15 @@ __device__ __forceinline__ void bring(const GradParams &gp, GradTile<KP> &tile, 
         copy16(&tile.u[t][at], gp.u + from, bytes);
         copy16(&tile.du[t][at], gp.du + from, bytes);
     }
-    const int64_t first = ((chunk * BH + item) * p.V + v0) * gp.Kp;
+    const int64_t first = (chunk * BH + item) * p.K * gp.Vp + v0;
 #pragma unroll 2
-    for (int e = tid; e < kVT * KP / 4; e += kThreads) {
-        const int j = e / (KP / 4), at = 4 * (e % (KP / 4));
-        const bool live = v0 + j < p.V && at < p.K;
-        const int64_t from = live ? first + (int64_t)j * gp.Kp + at : 0;
-        const int bytes = live ? min(4, p.K - at) * 4 : 0;
-        copy16(&tile.s[j][at], gp.s + from, bytes);
-        copy16(&tile.g[j][at], gp.g + from, bytes);
+    for (int e = tid; e < KP * kVT / 4; e += kThreads) {
+        const int k = e / (kVT / 4), at = 4 * (e % (kVT / 4));
+        const bool live = k < p.K && v0 + at < gp.Vp;
+        const int64_t from = live ? first + (int64_t)k * gp.Vp + at : 0;
+        const int bytes = live ? max(0, min(4, p.V - v0 - at)) * 4 : 0;
+        copy16(&tile.s[k][at], gp.s + from, bytes);
+        copy16(&tile.g[k][at], gp.g + from, bytes);
     }
     // 16-bit rows: eight values to a thread, 64 rows
     const int t = tid / 4, at = 8 * (tid % 4), live = t < n ? p.V - v0 - at : 0;
@@ -261,15 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
                 for (int j = 0; j < NK; ++j) {
                     const int at = k0 + 8 * j + fg;
-                    const Terms s0 = terms(x.s[v + ft][at]), s1 = terms(x.s[v + ft + 4][at]);
+                    const Terms s0 = terms(x.s[at][v + ft]), s1 = terms(x.s[at][v + ft + 4]);
                     mma_exact_a(qs[j], gy, s0, s1);
                     mma_terms(ks[j], duh, dul, s0, s1);
-                    const Terms g0 = terms(x.g[v + ft][at]), g1 = terms(x.g[v + ft + 4][at]);
+                    const Terms g0 = terms(x.g[at][v + ft]), g1 = terms(x.g[at][v + ft + 4]);
                     mma_terms(ke[j], uh, ul, g0, g1);
                 }
             }
             for (int e = tid; e < kVT * KP; e += kThreads)
-                gs = fmaf(x.s[e / KP][e % KP], x.g[e / KP][e % KP], gs);
+                gs = fmaf(x.s[e / kVT][e % kVT], x.g[e / kVT][e % kVT], gs);
 #pragma unroll
             for (int j = 0; j < 8; ++j)           // du.v: four threads to a token
                 dv = fmaf(x.du[tid / 4][8 * (tid % 4) + j], unpack2<DT>(x.v[tid / 4][8 * (tid % 4) + j]).x, dv);
@@ -518,14 +517,14 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a)
     const mcc1d_delta_args &f = a.fwd;
     DeltaBwdPlan p = {};
     p.chunks = (f.S + kChunk - 1) / kChunk;
-    p.Kp = (int32_t)((f.K + 3) / 4 * 4), p.Vp = (int32_t)((f.V + 3) / 4 * 4);
+    p.Vp = (int32_t)((f.V + 3) / 4 * 4);
     p.tokens = delta_plan(f).tokens;
     const auto take = [&](uint64_t bytes) {
         const uint64_t at = p.bytes;
         p.bytes += (bytes + 255) / 256 * 256;
         return at;
     };
-    const uint64_t tokens = (uint64_t)(f.S * f.B * f.H) * p.Vp, states = (uint64_t)(p.chunks * f.B * f.H * f.V) * p.Kp;
+    const uint64_t tokens = (uint64_t)(f.S * f.B * f.H) * p.Vp, states = (uint64_t)(p.chunks * f.B * f.H * f.K) * p.Vp;
     p.off_u = take(4 * tokens), p.off_du = take(4 * tokens);
     p.off_s = take(4 * states), p.off_g = take(4 * states);
     p.off_sums = take(4 * (uint64_t)(2 * p.chunks * f.B * f.H));
@@ -541,7 +540,7 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     const auto at = [&](uint64_t off) { return reinterpret_cast<float *>(ws + off); };
     mcc1d_delta_args in = f;
     in.y = nullptr, in.final_state = nullptr;
-    const DeltaKept kept = {at(plan.off_u), at(plan.off_s), plan.Vp, plan.Kp}, back = {at(plan.off_du), at(plan.off_g), plan.Vp, plan.Kp};
+    const DeltaKept kept = {at(plan.off_u), at(plan.off_s), plan.Vp}, back = {at(plan.off_du), at(plan.off_g), plan.Vp};
     int32_t st;
     if (plan.tokens) {
         st = launch_delta_tokens(in, kept, stream);
@@ -551,7 +550,7 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
             st = launch_delta_chunks(in, ws + plan.off_prepared, kept, stream);
     }
     if (st == kOk)
-        st = launch_delta_tokens_bwd(a, back, stream);
+        st = plan.tokens ? launch_delta_tokens_bwd(a, back, stream) : launch_delta_chunks_bwd(a, ws + plan.off_prepared, back, stream);
     if (st != kOk)
         return st;
     GradParams p = {};
@@ -559,7 +558,7 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     p.d.grad_y = static_cast<const uint16_t *>(a.grad_y);
     for (int i = 0; i < 3; ++i)
         p.d.gy_s[i] = a.grad_y_strides[i];
-    p.u = kept.u, p.du = back.u, p.s = kept.states, p.g = back.states, p.Kp = plan.Kp, p.Vp = plan.Vp;
+    p.u = kept.u, p.du = back.u, p.s = kept.states, p.g = back.states, p.Vp = plan.Vp;
     const auto vectors = [&](const void *x, const int64_t (&s)[3]) { return vectors_for(f.V, (uintptr_t)x, s[0] | s[1] | s[2]); };
     p.vectors_gy = vectors(a.grad_y, a.grad_y_strides), p.vectors_v = vectors(f.v, f.v_strides);
     p.grad_q = static_cast<uint16_t *>(a.grad_q), p.grad_k = static_cast<uint16_t *>(a.grad_k);

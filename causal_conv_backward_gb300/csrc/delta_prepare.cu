@@ -38,7 +38,8 @@ struct PrepareShared {
         };
     };
     float L[kC][kRow], P[kC][kRow];
-    float ch[kC], cl[kC], b[kC], f[2][kC], m[2][kC], lk[kC], of_v[kC], of_s[kC], of_r[kC];
+    float ch[kC], cl[kC], b[kC], f[2][kC], m[2][kC], lk[kC], ends[8][kC], most_p[kThreads / 32];
+    bool zero_q[kC];
 };
 
 template <int DT>
@@ -77,24 +78,9 @@ __device__ __forceinline__ void small_product(float (*to)[kRow], int r0, int c0,
     }
 }
 
-// Row t of a matrix as two panels, scaled; four threads to a row, 16 values each.
-// Returns 1 / scale and the sum of the row's magnitudes.
-__device__ __forceinline__ float2 store_terms(const float *row, uint8_t *hi, uint8_t *lo, int t, int part)
+// 16 values of row t of a matrix as two panels.
+__device__ __forceinline__ void store_terms(const float (&x)[16], float scale, uint8_t *hi, uint8_t *lo, int t, int part)
 {
-    float x[16], most = 0.f, sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(row + 16 * part + j);
-        x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
-        most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        sum += (fabsf(v.x) + fabsf(v.y)) + (fabsf(v.z) + fabsf(v.w));
-    }
-#pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    }
-    const float scale = scale_for(most);
 #pragma unroll
     for (int piece = 0; piece < 2; ++piece) {
         uint32_t h[4], l[4];
@@ -105,7 +91,13 @@ __device__ __forceinline__ float2 store_terms(const float *row, uint8_t *hi, uin
         *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    return make_float2(inverse_scale(scale), sum);
+}
+__device__ __forceinline__ float most_of_warp(float x)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2)
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+    return x;
 }
 
 template <int DT, int KP>
@@ -207,6 +199,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
             sh.f[w][t] = f, sh.m[w][t] = scale_for(most);
             if (w == 1)
                 sh.lk[t] = sqrtf(sum) * f;
+            else
+                sh.zero_q[t] = most == 0.f;
         }
     }
     __syncthreads();
@@ -302,37 +296,75 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
             *reinterpret_cast<float4 *>(&sh.X[r + i][c]) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     }
     __syncthreads();
+    // T by rows, P T as a whole scaled to fp16's range; four threads to a row
     const int t = tid / 4, part = tid % 4;
-    const float2 of_t = store_terms(sh.T[t], out, out + kPanelBytes, t, part);
-    const float2 of_p = store_terms(sh.X[t], out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
+    float xt[16], xp[16], most_t = 0.f, sum_t = 0.f, most_p = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sh.T[t][16 * part + j]), w = *reinterpret_cast<const float4 *>(&sh.X[t][16 * part + j]);
+        xt[j] = v.x, xt[j + 1] = v.y, xt[j + 2] = v.z, xt[j + 3] = v.w;
+        xp[j] = w.x, xp[j + 1] = w.y, xp[j + 2] = w.z, xp[j + 3] = w.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        most_t = fmaxf(most_t, fabsf(xt[j])), sum_t += fabsf(xt[j]);
+        most_p = fmaxf(most_p, fabsf(xp[j]));
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+        most_t = fmaxf(most_t, __shfl_xor_sync(0xFFFFFFFFu, most_t, d));
+        sum_t += __shfl_xor_sync(0xFFFFFFFFu, sum_t, d);
+    }
+    most_p = most_of_warp(most_p);
+    if (lane == 0)
+        sh.most_p[warp] = most_p;
+    const float scale_t = scale_for(most_t), of_t = inverse_scale(scale_t);
+    store_terms(xt, scale_t, out, out + kPanelBytes, t, part);
+    const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
+    // a row of zeros adds nothing, and must not lower the others' scale
+    const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
+    const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
+    const float fx = sh.b[t] * ec * k;
+    __syncthreads();
+    most_p = sh.most_p[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w)
+        most_p = fmaxf(most_p, sh.most_p[w]);
+    const float scale_p = scale_for(most_p);
+    store_terms(xp, scale_p, out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
     if (part == 0) {
-        const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f));
-        const float el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
-        // a row of zeros adds nothing, and must not lower the others' scale
-        const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f, q = sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
         factors[kFactorB * kC + t] = sh.b[t];
-        factors[kFactorX * kC + t] = sh.b[t] * ec * k;
-        factors[kFactorU * kC + t] = of_t.x * el * k;
+        factors[kFactorX * kC + t] = fx;
+        factors[kFactorU * kC + t] = of_t * el * k;
         factors[kFactorQ * kC + t] = ec * q;
-        factors[kFactorP * kC + t] = of_p.x;
-        factors[kFactorT * kC + t] = of_t.x;
+        factors[kFactorP * kC + t] = inverse_scale(scale_p);
+        factors[kFactorT * kC + t] = of_t;
         factors[kFactorScaleK * kC + t] = sh.m[1][t];
         factors[kFactorScaleQ * kC + t] = sh.m[0][t];
-        sh.of_v[t] = fabsf(sh.b[t]);
-        sh.of_s[t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
-        sh.of_r[t] = of_t.y * el * fabsf(k);
+        float (*ends)[kC] = sh.ends;
+        ends[0][t] = fabsf(sh.b[t]);
+        ends[1][t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
+        ends[2][t] = sum_t * el * fabsf(k);
+        ends[3][t] = el * sh.lk[t] * sqrtf((float)p.K) * of_t;
+        ends[4][t] = el * sh.lk[t] * sqrtf((float)p.K);
+        ends[5][t] = most_t;
+        ends[6][t] = fabsf(fx);
+        ends[7][t] = fabsf(ec * q);
     }
     __syncthreads();
-    if (warp < 3) {
-        const float *x = warp == 0 ? sh.of_v : warp == 1 ? sh.of_s : sh.of_r;
-        float most = fmaxf(x[lane], x[lane + 32]);
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2)
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+    {
+        const float most = most_of_warp(fmaxf(sh.ends[warp][lane], sh.ends[warp][lane + 32]));
         if (lane == 0)
-            factors[kFactorEnd * kC + kEndOfV + warp] = most;
-    } else if (tid == 96) {
-        factors[kFactorEnd * kC + kEndDecay] = ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
+            sh.most_p[warp] = most;
+    }
+    __syncthreads();
+    if (tid < 8) {
+        const float *e = sh.most_p, of[8] = {ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), e[0], e[1], e[2], e[3],
+                                             e[4] * (kC * e[5]) * e[6], kC * most_p * e[6], e[7]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (tid == j)
+                factors[kFactorEnd * kC + j] = of[j];
     }
 }
 

@@ -81,7 +81,7 @@ __device__ __forceinline__ void load_rows(const DeltaParams &p, const float *fro
         }
 }
 template <int J>
-__device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int step, int row0, int l8, const float (&s)[kRR][4 * J])
+__device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int step_row, int step_key, int row0, int l8, const float (&s)[kRR][4 * J])
 {
 #pragma unroll
     for (int r = 0; r < kRR; ++r)
@@ -89,7 +89,7 @@ __device__ __forceinline__ void store_rows(const DeltaParams &p, float *to, int 
         for (int e = 0; e < 4 * J; ++e) {
             const int row = row0 + 4 * r, at = (e / 4) * 32 + l8 * 4 + e % 4;
             if (row < p.V && at < p.K)
-                to[row * step + at] = s[r][e];
+                to[row * step_row + at * step_key] = s[r][e];
         }
 }
 
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_
     for (int64_t t0 = 0; t0 < n; t0 += kGroup) {
         const int live = (int)(n - t0 < kGroup ? n - t0 : kGroup);
         if (p.kept.states && t0 % kChunk == 0)
-            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.V * p.kept.Kp, p.kept.Kp, row0, l8, s);
+            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.K * p.kept.Vp, 1, p.kept.Vp, row0, l8, s);
         __syncthreads();
         stage<DT, 32 * J>(p, sh, p.v, p.v_s, b, h, first, t0, live);
         __syncthreads();
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_
         }
     }
     if (p.final_state)
-        store_rows<J>(p, p.final_state + item * VK, p.K, row0, l8, s);
+        store_rows<J>(p, p.final_state + item * VK, p.K, 1, row0, l8, s);
     if (p.y)
         for (int64_t t = n + warp; t < p.S; t += kWarps)
             for (int j = lane; j < kRowsPerBlock; j += 32)
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_bwd_kernel(const __g
     for (int64_t t0 = (n - 1) / kGroup * kGroup; n > 0 && t0 >= 0; t0 -= kGroup) {
         const int live = (int)(n - t0 < kGroup ? n - t0 : kGroup);
         if ((t0 + kGroup) % kChunk == 0 || t0 + kGroup >= n)
-            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.V * p.kept.Kp, p.kept.Kp, row0, l8, s);
+            store_rows<J>(p, p.kept.states + ((t0 / kChunk) * p.B * p.H + item) * p.K * p.kept.Vp, 1, p.kept.Vp, row0, l8, s);
         __syncthreads();
         stage<DT, 32 * J>(p, sh, p.grad_y, p.gy_s, b, h, first, t0, live);
         __syncthreads();
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_bwd_kernel(const __g
         }
     }
     if (p.grad_state)
-        store_rows<J>(p, p.grad_state + item * VK, p.K, row0, l8, s);
+        store_rows<J>(p, p.grad_state + item * VK, p.K, 1, row0, l8, s);
     for (int64_t t = n + warp; t < p.S; t += kWarps)
         for (int j = lane; j < kRowsPerBlock; j += 32)
             if (first + j < p.V)

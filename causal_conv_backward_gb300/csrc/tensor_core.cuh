@@ -115,10 +115,10 @@ __device__ __forceinline__ uint64_t desc_columns(uint32_t smem, uint32_t next)
     return kDescSwizzled | (uint64_t)(1024 >> 4) << 32 | (uint64_t)(next >> 4) << 16 | (smem >> 4);
 }
 
-// fp16 operands, fp32 sums, M = 128; B by columns where its rows run along the sum.
-__device__ constexpr uint32_t mma_kind(int N, bool b_columns)
+// fp16 operands, fp32 sums, M = 128; A or B by columns where its rows run along the sum.
+__device__ constexpr uint32_t mma_kind(int N, bool b_columns, bool a_columns = false)
 {
-    return 1u << 4 | (b_columns ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 | (128u / 16) << 24;
+    return 1u << 4 | (a_columns ? 1u << 15 : 0u) | (b_columns ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 | (128u / 16) << 24;
 }
 
 // D (+)= A B^T over 16 values of the sum, A in tensor memory (8 columns of
@@ -130,6 +130,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+// The same with A in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
         : "memory");
 }
 // The barrier gets one arrival when all of this thread's products so far are done.

@@ -25,7 +25,7 @@ Encode encoder()
 
 }  // namespace
 
-bool token_tiles(CUtensorMap *map, const void *at, int64_t S, int64_t B, int64_t heads, int64_t n, const int64_t (&strides)[3])
+bool token_tiles(CUtensorMap *map, const void *at, int64_t S, int64_t B, int64_t heads, int64_t n, const int64_t (&strides)[3], bool panels)
 {
     if (((uintptr_t)at & 15u) || n % 8)
         return false;
@@ -41,7 +41,7 @@ bool token_tiles(CUtensorMap *map, const void *at, int64_t S, int64_t B, int64_t
     const cuuint32_t box[4] = {64, 64, 1, 1}, every[4] = {1, 1, 1, 1};
     const Encode encode = encoder();
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(at), dims, steps, box, every, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                            panels ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace mcc1d
