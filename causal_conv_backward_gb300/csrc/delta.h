@@ -30,7 +30,7 @@ struct DeltaBwdPlan {
     uint64_t off_u, off_du;                // u(t) and its gradient
     uint64_t off_s, off_g;                 // states before each chunk, gradients of those after it
     uint64_t off_sums;                     // grad_A, grad_delta_bias of each (chunk, sequence): [2][chunks B][H]
-    uint64_t off_prepared;
+    uint64_t off_forward, off_grads;       // the forward's own, gradients at the ends of segments
     uint64_t bytes;
 };
 DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
@@ -50,14 +50,21 @@ constexpr int kChunkBytes = 4 * kPanelBytes + kFactors * kChunk * 4;
 struct DeltaPlan {
     bool tokens;                           // token by token, no workspace
     int64_t chunks;                        // ceil(S / kChunk)
-    uint64_t bytes;
+    int32_t segments;                      // of the time axis that are taken at once
+    uint64_t off_prepared, off_states, off_turns, bytes;
 };
 DeltaPlan delta_plan(const mcc1d_delta_args &a);
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream);
-int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream);
-int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream);
+int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const DeltaPlan &plan, const uint8_t *forward, float *grads, const DeltaKept &kept,
+                                cudaStream_t stream);
+int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, uint8_t *workspace, const DeltaKept &kept, cudaStream_t stream);
+// States at the ends of segments, from empty states, become those with which the
+// next segments begin: states [segments-1][heads][V,K] in place, s(j) = s(j-1)
+// turns(j) + s(j), turns [segments-1][heads][K,K] from j = 1 on. `back`: the
+// segments from the last one, with the turns transposed. (delta_join.cu)
+int32_t launch_delta_join(float *states, const float *turns, int64_t heads, int32_t V, int32_t K, int32_t segments, bool back, cudaStream_t stream);
 int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStream_t stream);
 int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream);
 

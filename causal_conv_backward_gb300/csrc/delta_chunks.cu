@@ -19,6 +19,8 @@
 // warps of its own. Warps 0 to 7 hold the rows, 8 to 11 write Y, 12 issues the
 // products, 13 copies the tokens of the chunk after the next, 14 to 19 make
 // panels of the next one's.
+#include <utility>
+
 #include "delta_chunks.cuh"
 
 namespace mcc1d {
@@ -38,6 +40,7 @@ struct ChunkParams {
     int32_t tiles;            // of 128 rows of V
     bool vectors_q, vectors_k, vectors_v, vectors_s;
     bool pairs_y;             // two rows of y are one word
+    Segments seg;
 };
 
 template <int KP>
@@ -98,22 +101,21 @@ __device__ __forceinline__ void pair_values(uint8_t *pairs, const uint8_t *copie
 
 // ------------------------------------------------------------------ the rows
 template <int DT, int KP>
-__device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh, const uint8_t *stages, int item, int b, int v0, int64_t n,
-                                          int64_t chunks)
+__device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh, const uint8_t *stages, const Part &pt, int64_t n)
 {
     typedef Stage<KP> St;
     constexpr int HK = KP / kParts, HC = kC / kParts, UNIT = HK < 32 ? HK : 32;
     const DeltaParams &p = cp.d;
-    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = v0 + r;
-    const int64_t BH = (int64_t)p.B * p.H, VK = (int64_t)p.V * p.K;
-    const bool mine = row < p.V;
+    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = pt.v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, chunks = pt.chunks, item = pt.item;
+    const bool mine = row < pt.rows;
     const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (warp % 4)) << 16);
     float s[HK];             // the state times `scale_s`, a power of two
     {
-        const float *from = p.state + item * VK + (int64_t)row * p.K + part * HK;
+        const float *from = pt.from + (int64_t)row * p.K + part * HK;
 #pragma unroll
         for (int k = 0; k < HK; ++k)
-            s[k] = p.state && mine && part * HK + k < p.K ? from[k] : 0.f;
+            s[k] = pt.from && mine && part * HK + k < p.K ? from[k] : pt.unit && row == part * HK + k ? 1.f : 0.f;
     }
     float scale_s;
     // Scales come from bounds, so that no thread waits for its row's other parts
@@ -144,14 +146,14 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
                 s[k] = __uint_as_float(0x7FFFFFFFu);
         if (i < chunks && p.kept.states && mine) {
             const float of = inverse_scale(scale_s);
-            float *to = p.kept.states + ((i * BH + item) * p.K + part * HK) * p.kept.Vp + row;
+            float *to = p.kept.states + (((pt.first + i) * BH + item) * p.K + part * HK) * p.kept.Vp + row;
 #pragma unroll
             for (int k = 0; k < HK; ++k, to += p.kept.Vp)
                 if (part * HK + k < p.K)
                     *to = s[k] * of;
         }
-        if (i >= chunks && p.final_state && mine)
-            write_row<HK>(p.final_state + item * VK + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
+        if (i >= chunks && pt.to && mine)
+            write_row<HK>(pt.to + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
         if (i >= chunks)
             break;
         const uint8_t *stage = stages + (i % kStages) * St::kBytes;
@@ -210,7 +212,7 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
             tmem_load(lanes + kU + HC * part + t0, raw);
             tmem_wait(raw);
             if (p.kept.u && mine) {
-                const int64_t at = i * kC + part * HC + t0, step = BH * p.kept.Vp;
+                const int64_t at = (pt.first + i) * kC + part * HC + t0, step = BH * p.kept.Vp;
                 float *to_u = p.kept.u + (at * BH + item) * p.kept.Vp + row;
 #pragma unroll
                 for (int t = 0; t < 16; ++t, to_u += step)
@@ -261,14 +263,14 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
 
 // ------------------------------------------------------------------ Y
 template <int DT>
-__device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, int item, int v0, int64_t n, int64_t chunks)
+__device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, const Part &pt, int64_t n)
 {
     const DeltaParams &p = cp.d;
-    const int r = threadIdx.x % kRows, row = v0 + r;
-    const int64_t step = (int64_t)p.B * p.H * p.V;
+    const int r = threadIdx.x % kRows, row = pt.v0 + r;
+    const int64_t step = (int64_t)p.B * p.H * p.V, chunks = pt.chunks;
     const bool mine = row < p.V;
     const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (threadIdx.x / 32 % 4)) << 16);
-    uint16_t *to = p.y + (int64_t)item * p.V + row;
+    uint16_t *to = p.y + pt.first * kC * step + (int64_t)pt.item * p.V + row;
     const bool odd = r & 1;
     uint16_t *pair = odd ? to + step - 1 : to;         // whole chunks come first
     int64_t i = 0;
@@ -278,7 +280,8 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
         const float *fq = sh.of_y[i & 3], *fp = fq + kC;
         tmem_fence_after();
         const float2 of_s = make_float2(sh.of_s[i & 1][r], sh.of_s[i & 1][r]), of_r = make_float2(sh.of_r[i & 1][r], sh.of_r[i & 1][r]);
-        const int live = (int)(n - i * kC < kC ? n - i * kC : kC), rows = (int)(p.S - i * kC < kC ? p.S - i * kC : kC);
+        const int64_t t1 = (pt.first + i) * kC;
+        const int live = (int)(n - t1 < kC ? n - t1 : kC), rows = (int)(p.S - t1 < kC ? p.S - t1 : kC);
         const bool whole = cp.pairs_y && rows == kC && live == kC;
 #pragma unroll 1
         for (int t0 = 0; t0 < kC; t0 += 16) {
@@ -312,9 +315,9 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
         tmem_fence_before();
         warp_arrive(sh.out);
     }
-    if (mine)
-        for (int64_t t = i * kC; t < p.S; ++t, to += step)
-            *to = i < chunks ? 0x7FFF : 0;          // NaN where a wait gave up
+    if (mine)          // tokens behind the sequence; NaN where a wait gave up
+        for (int64_t t = (pt.first + i) * kC, end = pt.last ? p.S : (pt.first + chunks) * kC; t < end; ++t, to += step)
+            *to = i < chunks ? 0x7FFF : 0;
 }
 
 // ------------------------------------------------------------------ products
@@ -381,18 +384,19 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t stages,
 // One warp: a chunk's rows as tiles of 64 tokens and 64 values, and its prepared
 // panels and factors.
 template <int KP>
-__device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, int item, int b, int h, int v0, int64_t chunks)
+__device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, const Part &pt)
 {
     typedef Stage<KP> St;
     const DeltaParams &p = cp.d;
-    const int lane = threadIdx.x % 32, g = h / (p.H / p.G);
+    const int lane = threadIdx.x % 32, b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
+    const int64_t chunks = pt.chunks;
     const uint32_t copied = smem_u32(stages) + kStages * St::kBytes, bar = smem_u32(&sh.rows);
-    const bool k = cp.vectors_k, q = cp.vectors_q && p.y, v = cp.vectors_v;
+    const bool k = cp.vectors_k, q = cp.vectors_q && p.y, v = cp.vectors_v && !pt.unit;
     for (int64_t i = 0; i < chunks; ++i) {
         if (!warp_wait(sh.rows_free, (uint32_t)(i + 1) & 1))
             break;
         if (lane == 0) {
-            const int t0 = (int)(i * kC);
+            const int t0 = (int)((pt.first + i) * kC);
             const int values = p.V - v0 > 64 ? 2 : 1;
             mbar_arrive_expect_tx(bar, ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (v ? values : 0)) * kPanelBytes);
             for (int j = 0; j < KP / 64; ++j) {
@@ -410,7 +414,7 @@ __device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &s
         if (lane == 0) {
             const uint32_t ready = smem_u32(&sh.factors[i % kStages]);
             mbar_arrive_expect_tx(ready, kChunkBytes);
-            bulk_g2s(smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes + St::kPrepared, cp.prepared + (item * cp.chunks + i) * kChunkBytes, kChunkBytes,
+            bulk_g2s(smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes + St::kPrepared, cp.prepared + (pt.item * cp.chunks + pt.first + i) * kChunkBytes, kChunkBytes,
                      ready);
         }
         __syncwarp();
@@ -419,14 +423,15 @@ __device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &s
 
 // The other loading warps: rows to panels and pairs.
 template <int DT, int KP>
-__device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, int b, int h, int v0, int64_t n, int64_t chunks)
+__device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, const Part &pt, int64_t n)
 {
     typedef Stage<KP> St;
     const DeltaParams &p = cp.d;
-    const int thread = threadIdx.x - (kThreads - kLoadThreads), g = h / (p.H / p.G);
+    const int thread = threadIdx.x - (kThreads - kLoadThreads), b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
+    const int64_t chunks = pt.chunks;
     const uint8_t *copied = stages + kStages * St::kBytes;
     for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t t0 = i * kC;
+        const int64_t t0 = (pt.first + i) * kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC);
         uint8_t *stage = stages + (i % kStages) * St::kBytes;
         const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
@@ -434,8 +439,8 @@ __device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &s
             break;
         make_panels<DT, KP>(stage + St::K, copied, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k,
                             live, thread);
-        pair_values(stage + St::V, copied + 2 * St::kPanels, p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], p.V - v0, cp.vectors_v,
-                    live, thread);
+        pair_values(stage + St::V, copied + 2 * St::kPanels, p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], pt.unit ? 0 : p.V - v0,
+                    cp.vectors_v, live, thread);
         if (p.y) {
             make_panels<DT, KP>(stage + St::Q, copied + St::kPanels, p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2], p.q_s[0], f + kFactorScaleQ * kC, p.K,
                                 cp.vectors_q, live, thread);
@@ -456,8 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
     uint8_t *stages = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
     const DeltaParams &p = cp.d;
     const int tid = threadIdx.x, warp = tid / 32, group = warp / 4;
-    const int item = blockIdx.x / cp.tiles, v0 = (blockIdx.x % cp.tiles) * kRows, b = item / p.H, h = item % p.H;
-    const int64_t n = clamped_length(p.lengths, b, p.S), chunks = (n + kC - 1) / kC;
+    int64_t n;
+    Part pt;
+    if (!part_of(cp.seg, p, cp.tiles, p.state, p.final_state, pt, n))
+        return;
 
     if (tid == 0) {
         sh.failed = 0;
@@ -479,19 +486,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
 
     if (group < kParts) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegRows));
-        hold_rows<DT, KP>(cp, sh, stages, item, b, v0, n, chunks);
+        hold_rows<DT, KP>(cp, sh, stages, pt, n);
     } else if (group == kParts) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegY));
         if (p.y)
-            write_y<DT>(cp, sh, item, v0, n, chunks);
+            write_y<DT>(cp, sh, pt, n);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
         if (warp > kCopyWarp)
-            make_tiles<DT, KP>(cp, sh, stages, b, h, v0, n, chunks);
+            make_tiles<DT, KP>(cp, sh, stages, pt, n);
         else if (warp == kCopyWarp)
-            copy_tiles<KP>(cp, sh, stages, item, b, h, v0, chunks);
+            copy_tiles<KP>(cp, sh, stages, pt);
         else if (tid % 32 == 0)
-            issue_products<KP>(sh, smem_u32(stages), chunks, p.y != nullptr);
+            issue_products<KP>(sh, smem_u32(stages), pt.chunks, p.y != nullptr);
     }
     tmem_fence_before();
     __syncthreads();
@@ -515,45 +522,99 @@ int32_t chunks_of(const ChunkParams &p, cudaStream_t stream)
         return kErrCuda;
     if (cudaFuncSetAttribute(delta_chunks_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_chunks_kernel<DT, KP>, dim3((unsigned)((int64_t)p.d.B * p.d.H * p.tiles)), kThreads, bytes, stream, p);
+    return launch(delta_chunks_kernel<DT, KP>, dim3((unsigned)blocks_of(p.seg, p.d, p.tiles)), kThreads, bytes, stream, p);
 }
 
 }  // namespace
+
+// Segments of the time axis: where heads are few, their chunks are shared out.
+// A first pass takes every segment but the last from an empty state (the first
+// from its own), and what becomes of any state on its way through it, K rows
+// from the unit matrix; a join passes the states on; a second pass takes all
+// segments at once. In units of a chunk's time, with waves of 152 blocks and two
+// units for each join, the shortest division is taken, if it saves a fifth: 65536
+// tokens of 6 heads of 64 take 3160 us in one piece and 400 us in 25.
+static int64_t waves(int64_t blocks) { return (blocks + kNumSMs - 1) / kNumSMs; }
+
+int32_t delta_segments(int64_t chunks, int64_t heads, int64_t tiles)
+{
+    int64_t best = 1, time = chunks * waves(heads * tiles) * 4 / 5;
+    for (int64_t n = 2; n <= 64 && n * 2 <= chunks; ++n) {
+        const int64_t per = (chunks + n - 1) / n;
+        const int64_t t = per * (waves((n - 1) * heads * (tiles + 1)) + waves(n * heads * tiles)) + 2 * n;
+        if (t < time)
+            best = n, time = t;
+    }
+    return (int32_t)best;
+}
 
 DeltaPlan delta_plan(const mcc1d_delta_args &a)
 {
     DeltaPlan p = {};
     p.chunks = (a.S + kChunk - 1) / kChunk;
     p.tokens = a.S < 32;
-    p.bytes = p.tokens ? 0 : (uint64_t)(p.chunks * a.B * a.H) * kChunkBytes;
+    if (p.tokens)
+        return p;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t at = p.bytes;
+        p.bytes += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    p.off_prepared = take((uint64_t)(p.chunks * a.B * a.H) * kChunkBytes);
+    p.segments = delta_segments(p.chunks, a.B * a.H, (a.V + kRows - 1) / kRows);
+    if (p.segments > 1) {
+        const uint64_t joins = (uint64_t)(p.segments - 1) * a.B * a.H * a.K * 4;
+        p.off_states = take(joins * a.V), p.off_turns = take(joins * a.K);
+    }
     return p;
 }
 
-int32_t launch_delta_chunks(const mcc1d_delta_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream)
+int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, uint8_t *workspace, const DeltaKept &kept, cudaStream_t stream)
 {
     ChunkParams p = {};
     p.d = delta_params(a);
-    p.d.kept = kept;
-    p.prepared = prepared;
-    p.chunks = (a.S + kChunk - 1) / kChunk;
+    p.prepared = workspace + plan.off_prepared;
+    p.chunks = plan.chunks;
     p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
     p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides, false);
     p.vectors_k = token_tiles(&p.map_k, a.k, a.S, a.B, a.G, a.K, a.k_strides, false);
     p.vectors_v = token_tiles(&p.map_v, a.v, a.S, a.B, a.H, a.V, a.v_strides, false);
     p.pairs_y = a.V % 2 == 0 && ((uintptr_t)a.y & 3u) == 0;
     p.vectors_s = a.K % 4 == 0 && ((uintptr_t)a.final_state & 15u) == 0;
-    if (a.dtype == 0)
-        return a.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
-    return a.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);
+    const auto go = [&]() {
+        if (a.dtype == 0)
+            return a.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
+        return a.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);
+    };
+    p.seg.count = plan.segments, p.seg.per = (plan.chunks + plan.segments - 1) / plan.segments;
+    if (plan.segments > 1) {
+        ChunkParams first = p;
+        first.seg.states = reinterpret_cast<float *>(workspace + plan.off_states);
+        first.seg.turns = reinterpret_cast<float *>(workspace + plan.off_turns);
+        first.seg.ends = true;
+        first.d.y = nullptr;
+        first.vectors_s = a.K % 4 == 0;
+        std::swap(p, first);
+        int32_t st = go();
+        std::swap(p, first);
+        if (st == kOk)
+            st = launch_delta_join(first.seg.states, first.seg.turns, a.B * a.H, (int32_t)a.V, (int32_t)a.K, plan.segments, false, stream);
+        if (st != kOk)
+            return st;
+        p.seg.states = first.seg.states;
+    }
+    p.d.kept = kept;
+    return go();
 }
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream)
 {
-    if (delta_plan(a).tokens)
+    const DeltaPlan plan = delta_plan(a);
+    if (plan.tokens)
         return launch_delta_tokens(a, DeltaKept(), stream);
-    uint8_t *prepared = static_cast<uint8_t *>(workspace);
-    const int32_t st = launch_delta_prepare(a, prepared, stream);
-    return st == kOk ? launch_delta_chunks(a, prepared, DeltaKept(), stream) : st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int32_t st = launch_delta_prepare(a, ws + plan.off_prepared, stream);
+    return st == kOk ? launch_delta_chunks(a, plan, ws, DeltaKept(), stream) : st;
 }
 
 }  // namespace mcc1d

@@ -16,6 +16,71 @@ constexpr int kC = kChunk, kRows = 128, kParts = 4;
 constexpr int kRowWarps = 4 * kParts, kLoadWarps = 6, kLoadThreads = 32 * kLoadWarps, kThreads = 32 * (kRowWarps + 4 + 2 + kLoadWarps);
 constexpr int kProductWarp = kRowWarps + 4, kCopyWarp = kProductWarp + 1;
 
+// How the time axis is cut (delta_chunks.cu). With `ends` the pass is the one
+// over all segments but the last, from empty states, that leaves `states` and,
+// in a forward, `turns`; without, the segments begin with `states`.
+struct Segments {
+    int32_t count;            // 1: not at all
+    int64_t per;              // chunks
+    float *states, *turns;    // [count-1][heads][V,K], [count-1][heads][K,K]
+    bool ends;
+};
+// A block's part: chunks, rows of V (or of the unit matrix), and where its rows'
+// states come from and go to.
+struct Part {
+    int item, v0, rows;
+    int64_t first, chunks;    // of its sequence
+    const float *from;
+    float *to;
+    bool unit, last;
+};
+inline int64_t blocks_of(const Segments &g, const DeltaParams &p, int32_t tiles)
+{
+    const int64_t heads = (int64_t)p.B * p.H;
+    return g.ends ? (g.count - 1) * heads * (tiles + (g.turns ? 1 : 0)) : g.count * heads * tiles;
+}
+// False where there is nothing to do.
+__device__ __forceinline__ bool part_of(const Segments &g, const DeltaParams &p, int tiles, const float *state, float *final_state, Part &pt, int64_t &n)
+{
+    const int all = tiles + (g.ends && g.turns ? 1 : 0), heads = p.B * p.H;
+    const int tile = blockIdx.x % all, segment = blockIdx.x / all / heads;
+    pt.item = blockIdx.x / all % heads;
+    pt.unit = tile == tiles;
+    if (pt.unit && segment == 0)
+        return false;
+    n = clamped_length(p.lengths, pt.item / p.H, p.S);
+    const int64_t chunks = (n + kChunk - 1) / kChunk;
+    pt.first = segment * g.per < chunks ? segment * g.per : chunks;
+    pt.chunks = chunks - pt.first < g.per ? chunks - pt.first : g.per;
+    pt.v0 = pt.unit ? 0 : tile * kRows;
+    pt.rows = pt.unit ? p.K : p.V;
+    pt.last = segment == g.count - 1;
+    const int64_t VK = (int64_t)p.V * p.K, KK = (int64_t)p.K * p.K, at = (int64_t)segment * heads + pt.item;
+    pt.from = segment == 0 ? (state ? state + pt.item * VK : nullptr) : !g.ends ? g.states + (at - heads) * VK : nullptr;
+    pt.to = pt.unit ? g.turns + at * KK : g.ends ? g.states + at * VK : pt.last && final_state ? final_state + pt.item * VK : nullptr;
+    return true;
+}
+
+// The same backwards: the pass from empty gradients leaves out the first segment
+// and puts the gradient that leaves segment j to states [j-1]; segment j of the
+// other begins with states [j].
+__device__ __forceinline__ void part_of_back(const Segments &g, const DeltaParams &p, int tiles, Part &pt, int64_t &n)
+{
+    const int heads = p.B * p.H, segment = blockIdx.x / tiles / heads + (g.ends ? 1 : 0);
+    pt.item = blockIdx.x / tiles % heads;
+    n = clamped_length(p.lengths, pt.item / p.H, p.S);
+    const int64_t chunks = (n + kChunk - 1) / kChunk;
+    pt.first = segment * g.per < chunks ? segment * g.per : chunks;
+    pt.chunks = chunks - pt.first < g.per ? chunks - pt.first : g.per;
+    pt.v0 = (blockIdx.x % tiles) * kRows;
+    pt.rows = p.V;
+    pt.unit = false;
+    pt.last = segment == g.count - 1;
+    const int64_t VK = (int64_t)p.V * p.K, at = (int64_t)segment * heads + pt.item;
+    pt.from = pt.last ? (p.grad_final ? p.grad_final + pt.item * VK : nullptr) : g.ends ? nullptr : g.states + at * VK;
+    pt.to = g.ends ? g.states + (at - heads) * VK : segment == 0 && p.grad_state ? p.grad_state + pt.item * VK : nullptr;
+}
+
 // A wait of a whole warp; false where it gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity)
 {

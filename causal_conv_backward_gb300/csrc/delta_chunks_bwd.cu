@@ -31,6 +31,7 @@ struct BackParams {
     int32_t tiles;            // of 128 rows of V
     bool vectors_q, vectors_k, vectors_y, vectors_s;
     bool pairs_v;             // two rows of grad_v are one word
+    Segments seg;
 };
 
 template <int KP>
@@ -57,22 +58,22 @@ struct BackShared {
 
 // ------------------------------------------------------------------ the rows
 template <int DT, int KP>
-__device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, const uint8_t *stages, int item, int v0, int64_t chunks)
+__device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, const uint8_t *stages, const Part &pt)
 {
     typedef Stage<KP> St;
     constexpr int HK = KP / kParts, HC = kC / kParts, UNIT = HK < 32 ? HK : 32;
     static_assert(HC == 16, "sixteen tokens to a thread");
     const DeltaParams &p = cp.d;
-    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = v0 + r;
-    const int64_t BH = (int64_t)p.B * p.H, VK = (int64_t)p.V * p.K;
+    const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = pt.v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, chunks = pt.chunks;
     const bool mine = row < p.V;
     const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (warp % 4)) << 16);
     float s[HK];             // the gradient times `scale_s`, a power of two
     {
-        const float *from = p.grad_final + item * VK + (int64_t)row * p.K + part * HK;
+        const float *from = pt.from + (int64_t)row * p.K + part * HK;
 #pragma unroll
         for (int k = 0; k < HK; ++k)
-            s[k] = p.grad_final && mine && part * HK + k < p.K ? from[k] : 0.f;
+            s[k] = pt.from && mine && part * HK + k < p.K ? from[k] : 0.f;
     }
     // scales come from bounds, as in delta_chunks.cu
     sh.most[part][r] = most_of(s);
@@ -96,17 +97,17 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
 #pragma unroll
             for (int k = 0; k < HK; ++k)
                 s[k] = __uint_as_float(0x7FFFFFFFu);
-        if (i < chunks && mine) {
+        if (i < chunks && mine && !cp.seg.ends) {
             const float of = inverse_scale(scale_s);
-            float *to = p.kept.states + (((chunks - 1 - i) * BH + item) * p.K + part * HK) * p.kept.Vp + row;
+            float *to = p.kept.states + (((pt.first + chunks - 1 - i) * BH + pt.item) * p.K + part * HK) * p.kept.Vp + row;
 #pragma unroll
             for (int k = 0; k < HK; ++k, to += p.kept.Vp)
                 if (part * HK + k < p.K)
                     *to = s[k] * of;
         }
         if (i >= chunks) {
-            if (p.grad_state && mine)
-                write_row<HK>(p.grad_state + item * VK + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
+            if (pt.to && mine)
+                write_row<HK>(pt.to + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
             break;
         }
         const uint8_t *stage = stages + (i % kStages) * St::kBytes;
@@ -198,24 +199,24 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
 
 // ------------------------------------------------------------------ dR and grad_v
 template <int DT>
-__device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh, int item, int v0, int64_t n, int64_t chunks)
+__device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh, const Part &pt, int64_t n)
 {
     const DeltaParams &p = cp.d;
-    const int r = threadIdx.x % kRows, row = v0 + r;
-    const int64_t BH = (int64_t)p.B * p.H, step = BH * p.V, step_u = BH * p.kept.Vp;
+    const int r = threadIdx.x % kRows, row = pt.v0 + r;
+    const int64_t BH = (int64_t)p.B * p.H, step = BH * p.V, step_u = BH * p.kept.Vp, chunks = pt.chunks, item = pt.item;
     const bool mine = row < p.V, odd = r & 1;
     const uint32_t lanes = sh.tmem + ((uint32_t)(32 * (threadIdx.x / 32 % 4)) << 16);
     // tokens of no chunk
     uint16_t *to = p.grad_v + (int64_t)item * p.V + row;
-    if (mine)
-        for (int64_t t = chunks * kC; t < p.S; ++t)
+    if (mine && pt.last)
+        for (int64_t t = (pt.first + chunks) * kC; t < p.S; ++t)
             to[t * step] = 0;
     int64_t i = 0;
     for (; i < chunks; ++i) {
         if (!warp_wait(sh.u, (uint32_t)(i & 1)))
             break;
         tmem_fence_after();
-        const int64_t t0 = (chunks - 1 - i) * kC;
+        const int64_t t0 = (pt.first + chunks - 1 - i) * kC;
         const float of_u = sh.of_u[i & 1][r], of_p = sh.of_p[i & 3];
         const float *bt = sh.of_out[i & 3];
         const int live = (int)(n - t0 < kC ? n - t0 : kC), rows = (int)(p.S - t0 < kC ? p.S - t0 : kC);
@@ -262,13 +263,13 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
         }
     }
     if (mine && i < chunks)         // a wait gave up
-        for (int64_t t = 0; t < (chunks - i) * kC && t < p.S; ++t)
+        for (int64_t t = pt.first * kC; t < (pt.first + chunks - i) * kC && t < p.S; ++t)
             to[t * step] = 0x7FFF;
 }
 
 // ------------------------------------------------------------------ products
 template <int KP>
-__device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, int64_t chunks)
+__device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, int64_t chunks, bool out)
 {
     typedef Stage<KP> St;
     constexpr uint32_t by_rows = mma_kind(kC, false), by_columns = mma_kind(KP, true), tokens_by_columns = mma_kind(kC, true);
@@ -311,7 +312,7 @@ __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, 
             mma_ss(tmem + kYQ, y, desc_columns(stage + St::QHi, kPanelBytes) + step, y_keys, j > 0);
             mma_ss(tmem + kYQ, y, desc_columns(stage + St::QLo, kPanelBytes) + step, y_keys, true);
         }
-        if (!wait(sh.v, parity) || !wait(sh.out, parity))
+        if (!wait(sh.v, parity) || (out && !wait(sh.out, parity)))
             break;
         tmem_fence_after();
 #pragma unroll
@@ -327,21 +328,22 @@ __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, 
 
 // ------------------------------------------------------------------ tiles
 template <int KP>
-__device__ __forceinline__ void copy_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, int item, int b, int h, int v0, int64_t chunks)
+__device__ __forceinline__ void copy_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, const Part &pt)
 {
     typedef Stage<KP> St;
     const DeltaParams &p = cp.d;
-    const int g = h / (p.H / p.G);
+    const int b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
+    const int64_t chunks = pt.chunks;
     const bool k = cp.vectors_k, q = cp.vectors_q, y = cp.vectors_y;
     for (int64_t i = 0; i < chunks; ++i) {
         if (!warp_wait(sh.empty[i % kStages], (uint32_t)(i / kStages + 1) & 1))
             break;
         if (threadIdx.x % 32 == 0) {
-            const int64_t chunk = chunks - 1 - i;
+            const int64_t chunk = pt.first + chunks - 1 - i;
             const uint32_t stage = smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes, bar = smem_u32(&sh.tiles[i % kStages]);
             const int t0 = (int)(chunk * kC), values = p.V - v0 > 64 ? 2 : 1;
             mbar_arrive_expect_tx(bar, kChunkBytes + ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (y ? values : 0)) * kPanelBytes);
-            bulk_g2s(stage + St::kPrepared, cp.prepared + (item * cp.chunks + chunk) * kChunkBytes, kChunkBytes, bar);
+            bulk_g2s(stage + St::kPrepared, cp.prepared + (pt.item * cp.chunks + chunk) * kChunkBytes, kChunkBytes, bar);
             for (int j = 0; j < KP / 64; ++j) {
                 if (k)
                     tile_g2s(stage + St::K + j * kPanelBytes, &cp.map_k, 64 * j, t0, g, b, bar);
@@ -367,13 +369,14 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float2 (&x)[4])
 }
 
 template <int DT, int KP>
-__device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, int b, int h, int v0, int64_t n, int64_t chunks)
+__device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh, uint8_t *stages, const Part &pt, int64_t n)
 {
     typedef Stage<KP> St;
     const DeltaParams &p = cp.d;
-    const int thread = threadIdx.x - (kThreads - kLoadThreads), g = h / (p.H / p.G);
+    const int thread = threadIdx.x - (kThreads - kLoadThreads), b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
+    const int64_t chunks = pt.chunks;
     for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t t0 = (chunks - 1 - i) * kC;
+        const int64_t t0 = (pt.first + chunks - 1 - i) * kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC);
         uint8_t *stage = stages + (i % kStages) * St::kBytes;
         const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
@@ -450,8 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_bwd_kernel(const __g
     uint8_t *stages = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
     const DeltaParams &p = cp.d;
     const int tid = threadIdx.x, warp = tid / 32, group = warp / 4;
-    const int item = blockIdx.x / cp.tiles, v0 = (blockIdx.x % cp.tiles) * kRows, b = item / p.H, h = item % p.H;
-    const int64_t n = clamped_length(p.lengths, b, p.S), chunks = (n + kC - 1) / kC;
+    int64_t n;
+    Part pt;
+    part_of_back(cp.seg, p, cp.tiles, pt, n);
 
     if (tid == 0) {
         sh.failed = 0;
@@ -472,18 +476,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_bwd_kernel(const __g
     tmem_fence_after();
 
     if (group < kParts) {
-        hold_rows<DT, KP>(cp, sh, stages, item, v0, chunks);
+        hold_rows<DT, KP>(cp, sh, stages, pt);
     } else if (group == kParts) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegOut));
-        write_rows<DT>(cp, sh, item, v0, n, chunks);
+        if (!cp.seg.ends)
+            write_rows<DT>(cp, sh, pt, n);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
         if (warp > kCopyWarp)
-            make_tiles<DT, KP>(cp, sh, stages, b, h, v0, n, chunks);
+            make_tiles<DT, KP>(cp, sh, stages, pt, n);
         else if (warp == kCopyWarp)
-            copy_tiles<KP>(cp, sh, stages, item, b, h, v0, chunks);
+            copy_tiles<KP>(cp, sh, stages, pt);
         else if (tid % 32 == 0)
-            issue_products<KP>(sh, smem_u32(stages), chunks);
+            issue_products<KP>(sh, smem_u32(stages), pt.chunks, !cp.seg.ends);
     }
     tmem_fence_before();
     __syncthreads();
@@ -507,12 +512,13 @@ int32_t chunks_of(const BackParams &p, cudaStream_t stream)
         return kErrCuda;
     if (cudaFuncSetAttribute(delta_chunks_bwd_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_chunks_bwd_kernel<DT, KP>, dim3((unsigned)((int64_t)p.d.B * p.d.H * p.tiles)), kThreads, bytes, stream, p);
+    return launch(delta_chunks_bwd_kernel<DT, KP>, dim3((unsigned)blocks_of(p.seg, p.d, p.tiles)), kThreads, bytes, stream, p);
 }
 
 }  // namespace
 
-int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const uint8_t *prepared, const DeltaKept &kept, cudaStream_t stream)
+int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const DeltaPlan &plan, const uint8_t *forward, float *grads, const DeltaKept &kept,
+                                cudaStream_t stream)
 {
     const mcc1d_delta_args &f = a.fwd;
     BackParams p = {};
@@ -522,17 +528,35 @@ int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const uint8_t *pr
     p.d.grad_final = a.grad_final_state, p.d.grad_state = a.grad_state;
     for (int i = 0; i < 3; ++i)
         p.d.gy_s[i] = a.grad_y_strides[i];
-    p.prepared = prepared;
-    p.chunks = (f.S + kChunk - 1) / kChunk;
+    p.prepared = forward + plan.off_prepared;
+    p.chunks = plan.chunks;
     p.tiles = (int32_t)((f.V + kRows - 1) / kRows);
     p.vectors_q = token_tiles(&p.map_q, f.q, f.S, f.B, f.G, f.K, f.q_strides, true);
     p.vectors_k = token_tiles(&p.map_k, f.k, f.S, f.B, f.G, f.K, f.k_strides, true);
     p.vectors_y = token_tiles(&p.map_y, a.grad_y, f.S, f.B, f.H, f.V, a.grad_y_strides, true);
     p.vectors_s = f.K % 4 == 0 && ((uintptr_t)a.grad_state & 15u) == 0;
     p.pairs_v = f.V % 2 == 0 && ((uintptr_t)a.grad_v & 3u) == 0;
-    if (f.dtype == 0)
-        return f.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
-    return f.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);
+    p.seg.count = plan.segments, p.seg.per = (plan.chunks + plan.segments - 1) / plan.segments;
+    const auto go = [&]() {
+        if (f.dtype == 0)
+            return f.K <= 64 ? chunks_of<0, 64>(p, stream) : chunks_of<0, 128>(p, stream);
+        return f.K <= 64 ? chunks_of<1, 64>(p, stream) : chunks_of<1, 128>(p, stream);
+    };
+    if (plan.segments > 1) {
+        p.seg.states = grads;
+        p.seg.ends = true;
+        const bool vectors = p.vectors_s;
+        p.vectors_s = f.K % 4 == 0;
+        int32_t st = go();
+        if (st == kOk)
+            st = launch_delta_join(grads, reinterpret_cast<const float *>(forward + plan.off_turns), f.B * f.H, (int32_t)f.V, (int32_t)f.K, plan.segments, true,
+                                   stream);
+        if (st != kOk)
+            return st;
+        p.seg.ends = false;
+        p.vectors_s = vectors;
+    }
+    return go();
 }
 
 }  // namespace mcc1d

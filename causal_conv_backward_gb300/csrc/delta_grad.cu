@@ -75,17 +75,27 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c += (a) (b), a exact or of two terms
+// c += (a) (b), a exact or of two terms, the small products first
 __device__ __forceinline__ void mma_exact_a(float (&c)[4], const uint32_t (&a)[4], const Terms &b0, const Terms &b1)
 {
-    mma1688(c, a, b0.hi, b1.hi);
     mma1688(c, a, b0.lo, b1.lo);
+    mma1688(c, a, b0.hi, b1.hi);
+}
+// The tensor cores cut their sums off where fp32 would round: long sums are
+// taken eight products at a time and added outside.
+__device__ __forceinline__ void add4(float (&c)[4], const float (&x)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const float2 s = add2(make_float2(c[e], c[e + 1]), make_float2(x[e], x[e + 1]));
+        c[e] = s.x, c[e + 1] = s.y;
+    }
 }
 __device__ __forceinline__ void mma_terms(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const Terms &b0, const Terms &b1)
 {
-    mma1688(c, hi, b0.hi, b1.hi);
     mma1688(c, hi, b0.lo, b1.lo);
     mma1688(c, lo, b0.hi, b1.hi);
+    mma1688(c, hi, b0.hi, b1.hi);
 }
 // The 16 x 8 fragment at rows r.., columns c.. of a row-major matrix.
 template <int STRIDE>
@@ -254,17 +264,21 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const Terms u0 = terms(x.u[c0 + 8 * j + fg][v + ft]), u1 = terms(x.u[c0 + 8 * j + fg][v + ft + 4]);
-                        mma_exact_a(P[j], gy, u0, u1);
-                        mma_terms(L[j], duh, dul, u0, u1);
+                        float x[4] = {}, y[4] = {};
+                        mma_exact_a(x, gy, u0, u1);
+                        mma_terms(y, duh, dul, u0, u1);
+                        add4(P[j], x), add4(L[j], y);
                     }
 #pragma unroll
                 for (int j = 0; j < NK; ++j) {
                     const int at = k0 + 8 * j + fg;
                     const Terms s0 = terms(x.s[at][v + ft]), s1 = terms(x.s[at][v + ft + 4]);
-                    mma_exact_a(qs[j], gy, s0, s1);
-                    mma_terms(ks[j], duh, dul, s0, s1);
+                    float x4[4] = {}, y4[4] = {}, z4[4] = {};
+                    mma_exact_a(x4, gy, s0, s1);
+                    mma_terms(y4, duh, dul, s0, s1);
                     const Terms g0 = terms(x.g[at][v + ft]), g1 = terms(x.g[at][v + ft + 4]);
-                    mma_terms(ke[j], uh, ul, g0, g1);
+                    mma_terms(z4, uh, ul, g0, g1);
+                    add4(qs[j], x4), add4(ks[j], y4), add4(ke[j], z4);
                 }
             }
             for (int e = tid; e < kVT * KP; e += kThreads)
@@ -528,7 +542,9 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a)
     p.off_u = take(4 * tokens), p.off_du = take(4 * tokens);
     p.off_s = take(4 * states), p.off_g = take(4 * states);
     p.off_sums = take(4 * (uint64_t)(2 * p.chunks * f.B * f.H));
-    p.off_prepared = take(p.tokens ? 0 : (uint64_t)(p.chunks * f.B * f.H) * kChunkBytes);
+    const DeltaPlan forward = delta_plan(f);
+    p.off_forward = take(forward.bytes);
+    p.off_grads = take(4 * (uint64_t)(forward.segments > 1 ? forward.segments - 1 : 0) * (uint64_t)(f.B * f.H * f.V * f.K));
     return p;
 }
 
@@ -544,13 +560,16 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     int32_t st;
     if (plan.tokens) {
         st = launch_delta_tokens(in, kept, stream);
-    } else {
-        st = launch_delta_prepare(in, ws + plan.off_prepared, stream);
         if (st == kOk)
-            st = launch_delta_chunks(in, ws + plan.off_prepared, kept, stream);
+            st = launch_delta_tokens_bwd(a, back, stream);
+    } else {
+        const DeltaPlan forward = delta_plan(f);
+        st = launch_delta_prepare(in, ws + plan.off_forward + forward.off_prepared, stream);
+        if (st == kOk)
+            st = launch_delta_chunks(in, forward, ws + plan.off_forward, kept, stream);
+        if (st == kOk)
+            st = launch_delta_chunks_bwd(a, forward, ws + plan.off_forward, at(plan.off_grads), back, stream);
     }
-    if (st == kOk)
-        st = plan.tokens ? launch_delta_tokens_bwd(a, back, stream) : launch_delta_chunks_bwd(a, ws + plan.off_prepared, back, stream);
     if (st != kOk)
         return st;
     GradParams p = {};
