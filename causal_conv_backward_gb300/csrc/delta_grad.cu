@@ -10,218 +10,270 @@
 //   gb(t) = du(t).v(t) - e^c(t) (du(t) S).k'(t) + sum over i of L'(t,i) (k'(t).k'(i))
 // and what each token's decay multiplies, summed, is the gradient of log a.
 //
-// All products are on the tensor cores with fp32 operands as two tf32 terms
-// (22 bits, any range; grad_y, q and k are exact in one), by mma.sync: the sums
-// behind grad_A and grad_delta_bias run over all tokens, and would show less.
-// They bound the kernel: 84 per eight values of V, 48 per eight tokens, a warp.
+// All products are on the tensor cores, of fp16 operands: two terms (22 bits) of
+// fp32 rows scaled by a power of two, q and k exact in one. A tile of 64 values
+// of V at a time, the rows of grad_y and du are multiplied with those of S and u,
+// the rows of u with those of G; then the tokens' own products follow. A thread
+// has one token's row, of grad_y (P', gq') or of du and u (L', gk'), and a quarter
+// of the columns; sums over tiles and heads are fp32 in its registers. What
+// bounds the kernel is reading u, du, S and G, 4 bytes a value, and their rounding.
 #include "delta_common.cuh"
+#include "tensor_core.cuh"
 
 namespace mcc1d {
 
 namespace {
 
-constexpr int kC = kChunk, kVT = 32, kThreads = 256, kTri = kC + 4, kVS = kVT + 4, kRaw = kVT + 8;
+constexpr int kC = kChunk, kVT = 64, kThreads = 512, kQuarters = 4;
 
 struct GradParams {
     DeltaParams d;
     const float *u, *du, *s, *g;   // [S,B,H,Vp], [chunks][B H][K,Vp]
     int32_t Vp;
-    bool vectors_gy, vectors_v;
+    bool vectors_q, vectors_k, vectors_gy, vectors_v, pairs;
     uint16_t *grad_q, *grad_k, *grad_delta, *grad_beta;
     float *sum_A, *sum_bias;       // [chunks B][H]
 };
 
-// Strides are 4 or 8 over a multiple of 32 words, so that the eight rows and
-// four columns (or the other way round) of a fragment lie on different banks.
+// Operands in shared memory. Panels of rows along V: grad_y, du, u (64 rows each,
+// one after the other), S and G (a row to a key); later rows along the tokens:
+// P' and L' (64 rows each), and the two that are taken by columns.
 template <int KP>
-struct GradTile {
-    float u[kC][kVS], du[kC][kVS], s[KP][kVS], g[KP][kVS];
-    uint16_t gy[kC][kRaw], v[kC][kRaw];
+struct Panels {
+    static constexpr int kRows = 3 * kPanelBytes;                   // of grad_y, du, u
+    static constexpr int kKeys = KP * 128;
+    static constexpr int A = 0, ALo = kRows, S = 2 * kRows, SLo = S + kKeys, G = S + 2 * kKeys, GLo = S + 3 * kKeys, QK = S + 4 * kKeys;
+    static constexpr int kQK = 2 * kPanelBytes;                     // rows of q, then of k, 64 keys of them
+    static constexpr int kBytes = QK + KP / 64 * kQK;
+    static constexpr int X = A, XLo = ALo, PC = S, PCLo = S + kPanelBytes, LC = S + 2 * kPanelBytes, LCLo = S + 3 * kPanelBytes;
 };
-template <int KP>
+
 struct GradShared {
-    static constexpr int KS = KP + 8;
-    float q[kC][KS], k[kC][KS];        // as they are, not divided by their lengths
-    union {
-        GradTile<KP> tile[2];
-        struct {
-            float P[kC][kTri], PT[kC][kTri], M[kC][kTri];
-        };
-    };
-    float ch[kC], cl[kC], b[kC], dt[kC], raw[kC], fq[kC], fk[kC], gc[kC], gb[kC], dv[kC], dot[8];
-    float sq[2][kC], sk[2][kC], se[2][kC], row[2][kC], low[2][kC], col[4][kC];     // of the warps that share a row or column
+    uint64_t done;
+    uint32_t tmem;
+    float of_rows[3 * kC], of_s[128], of_g[128];                     // what operands are multiplied by
+    float ch[kC], cl[kC], b[kC], dt[kC], raw[kC], fq[kC], fk[kC];    // fq, fk: of q, k as they are
+    float xq[kC], xk[kC];                                           // of q, k as operands
+    float gc[kC], gb[kC], dv[kC], dot[kThreads / 32];
+    float dots[3][kQuarters][kC], row[2][kQuarters][kC], low[kQuarters][kC], col[4][kC];
+    float most[kQuarters][2 * kC], most_of_warps[kThreads / 32];
 };
 
-// A value as two tf32 terms, 22 bits.
-struct Terms {
-    uint32_t hi, lo;
-};
-__device__ __forceinline__ uint32_t tf32(float x)
-{
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ Terms terms(float x)
-{
-    Terms t;
-    t.hi = tf32(x);
-    t.lo = tf32(x - __uint_as_float(t.hi));
-    return t;
-}
-__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// c += (a) (b), a exact or of two terms, the small products first
-__device__ __forceinline__ void mma_exact_a(float (&c)[4], const uint32_t (&a)[4], const Terms &b0, const Terms &b1)
-{
-    mma1688(c, a, b0.lo, b1.lo);
-    mma1688(c, a, b0.hi, b1.hi);
-}
-// The tensor cores cut their sums off where fp32 would round: long sums are
-// taken eight products at a time and added outside.
-__device__ __forceinline__ void add4(float (&c)[4], const float (&x)[4])
+// Columns of tensor memory: [grad_y; du] S, [grad_y; du] u, [du; u] G, [q; k] k;
+// then [P'; L'] k in G's place and the column products in S's.
+enum { kDS = 0, kDU = 128, kDG = 192, kDK = 320, kColumns = 512 };
+
+// Eight values of a workspace row, zeros past its end.
+__device__ __forceinline__ void load8(const float *from, int live, float (&x)[8])
 {
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-        const float2 s = add2(make_float2(c[e], c[e + 1]), make_float2(x[e], x[e + 1]));
-        c[e] = s.x, c[e + 1] = s.y;
+    for (int e = 0; e < 8; e += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < live)
+            v = __ldg(reinterpret_cast<const float4 *>(from + e));
+        x[e] = v.x, x[e + 1] = e + 1 < live ? v.y : 0.f, x[e + 2] = e + 2 < live ? v.z : 0.f, x[e + 3] = e + 3 < live ? v.w : 0.f;
     }
 }
-__device__ __forceinline__ void mma_terms(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const Terms &b0, const Terms &b1)
+template <int DT>
+__device__ __forceinline__ void load8(const uint16_t *from, bool vectors, int live, float (&x)[8])
 {
-    mma1688(c, hi, b0.lo, b1.lo);
-    mma1688(c, lo, b0.hi, b1.hi);
-    mma1688(c, hi, b0.hi, b1.hi);
-}
-// The 16 x 8 fragment at rows r.., columns c.. of a row-major matrix.
-template <int STRIDE>
-__device__ __forceinline__ void fragment(const float (*m)[STRIDE], int r, int c, uint32_t (&hi)[4], uint32_t (&lo)[4])
-{
-    const int g = threadIdx.x % 32 / 4, t = threadIdx.x % 4;
+    if (vectors) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (live > 0)
+            v = __ldg(reinterpret_cast<const uint4 *>(from));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const Terms x = terms(m[r + g + 8 * (e % 2)][c + t + 4 * (e / 2)]);
-        hi[e] = x.hi, lo[e] = x.lo;
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<DT>(u[e]);
+            x[2 * e] = f.x, x[2 * e + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = e < live ? value<DT>(from + e) : 0.f;
     }
 }
-
-__device__ __forceinline__ float sum4(float x)
+__device__ __forceinline__ float most8(const float (&x)[8])
 {
-    x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-    return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+    return fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
+                 fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
+}
+// The N threads that share a row.
+template <int N>
+__device__ __forceinline__ float most_of_lanes(float x)
+{
+#pragma unroll
+    for (int d = 1; d < N; d *= 2)
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+    return x;
+}
+template <int N>
+__device__ __forceinline__ float sum_of_lanes(float x)
+{
+#pragma unroll
+    for (int d = 1; d < N; d *= 2)
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+    return x;
+}
+__device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, uint32_t at, const float *x, float scale)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        two_terms(make_float2(x[2 * e] * scale, x[2 * e + 1] * scale), h[e], l[e]);
+    *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// A row's eight values (of its 64, over eight threads) as terms; 1 / its scale.
+__device__ __forceinline__ float put_row(uint8_t *hi, uint8_t *lo, int row, int piece, const float (&x)[8])
+{
+    const float scale = scale_for(most_of_lanes<8>(most8(x)));
+    put8(hi, lo, panel_at(row, piece), x, scale);
+    return inverse_scale(scale);
 }
 
-__device__ __forceinline__ void copy16(void *to, const void *from, int bytes)
+// Sums of 16 values over the warp's lanes: lane l has that of value l / 2.
+__device__ __forceinline__ float sums16(float (&x)[16])
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int d = 16, n = 8; n > 0; d /= 2, n /= 2) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            const float give = upper ? x[e] : x[e + n], keep = upper ? x[e + n] : x[e];
+            x[e] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, d);
+        }
+    }
+    return x[0] + __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
 }
 
-// Values v0.. of a chunk's rows: u, du, grad_y, v, and of the states' rows.
-template <int DT, int KP>
-__device__ __forceinline__ void bring(const GradParams &gp, GradTile<KP> &tile, int64_t chunk, int64_t item, int b, int h, int n, int v0)
+// Adds A B^T, all of two terms but A's second times B's second, over 64 values
+// of the sum, by one thread.
+__device__ __forceinline__ void three_products(uint32_t d, uint32_t a, uint32_t a_lo, uint32_t b, uint32_t b_lo, uint32_t kind)
 {
-    const DeltaParams &p = gp.d;
-    const int64_t BH = (int64_t)p.B * p.H, t0 = chunk * kC;
-    const int tid = threadIdx.x;
-#pragma unroll 2
-    for (int e = tid; e < kC * kVT / 4; e += kThreads) {
-        const int t = e / (kVT / 4), at = 4 * (e % (kVT / 4));
-        const bool live = t < n && v0 + at < gp.Vp;
-        const int64_t from = live ? ((t0 + t) * BH + item) * gp.Vp + v0 + at : 0;
-        const int bytes = live ? max(0, min(4, p.V - v0 - at)) * 4 : 0;
-        copy16(&tile.u[t][at], gp.u + from, bytes);
-        copy16(&tile.du[t][at], gp.du + from, bytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        mma_ss(d, desc_rows(a) + 2 * j, desc_rows(b_lo) + 2 * j, kind, j > 0);
+        mma_ss(d, desc_rows(a_lo) + 2 * j, desc_rows(b) + 2 * j, kind, true);
+        mma_ss(d, desc_rows(a) + 2 * j, desc_rows(b) + 2 * j, kind, true);
     }
-    const int64_t first = (chunk * BH + item) * p.K * gp.Vp + v0;
-#pragma unroll 2
-    for (int e = tid; e < KP * kVT / 4; e += kThreads) {
-        const int k = e / (kVT / 4), at = 4 * (e % (kVT / 4));
-        const bool live = k < p.K && v0 + at < gp.Vp;
-        const int64_t from = live ? first + (int64_t)k * gp.Vp + at : 0;
-        const int bytes = live ? max(0, min(4, p.V - v0 - at)) * 4 : 0;
-        copy16(&tile.s[k][at], gp.s + from, bytes);
-        copy16(&tile.g[k][at], gp.g + from, bytes);
-    }
-    // 16-bit rows: eight values to a thread, 64 rows
-    const int t = tid / 4, at = 8 * (tid % 4), live = t < n ? p.V - v0 - at : 0;
-    const uint16_t *gy = p.grad_y + (t0 + t) * p.gy_s[0] + b * p.gy_s[1] + h * p.gy_s[2] + v0 + at;
-    const uint16_t *v = p.v + (t0 + t) * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0 + at;
-    if (gp.vectors_gy)
-        copy16(&tile.gy[t][at], live > 0 ? gy : p.grad_y, live > 0 ? 16 : 0);
-    else
-        for (int i = 0; i < 8; ++i)
-            tile.gy[t][at + i] = i < live ? __ldg(gy + i) : (uint16_t)0;
-    if (gp.vectors_v)
-        copy16(&tile.v[t][at], live > 0 ? v : p.v, live > 0 ? 16 : 0);
-    else
-        for (int i = 0; i < 8; ++i)
-            tile.v[t][at + i] = i < live ? __ldg(v + i) : (uint16_t)0;
-    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <int DT, int KP>
 __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ GradParams gp)
 {
-    extern __shared__ __align__(16) uint8_t raw_shared[];
-    typedef GradShared<KP> Shared;
-    Shared &sh = *reinterpret_cast<Shared *>(raw_shared);
-    constexpr int NK = KP / 16;        // eights of keys of a warp
+    extern __shared__ uint8_t raw_shared[];
+    __shared__ GradShared sh;
+    typedef Panels<KP> Pn;
+    uint8_t *panels = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
+    const uint32_t at_panels = smem_u32(panels);
+    constexpr int KC = KP / kQuarters, UNIT = 16, IC = kC / kQuarters;        // a thread's keys and other tokens
     const DeltaParams &p = gp.d;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, fg = lane / 4, ft = lane % 4;
-    // a warp has 16 tokens, half of the other tokens and half of the keys
-    const int r0 = 16 * (warp % 4), part = warp / 4, c0 = 32 * part, k0 = KP / 2 * part;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, quarter = warp / 4;
+    const int r = 32 * (warp % 4) + lane, t = r % kC;             // its row of a product, and token
+    const bool of_du = r >= kC;                                   // a whole warp's
     const int g = blockIdx.x % p.G, b = (blockIdx.x / p.G) % p.B, per = p.H / p.G;
     const int64_t chunk = blockIdx.x / p.G / p.B, t0 = chunk * kC;
     const int64_t length = clamped_length(p.lengths, b, p.S);
     const int there = (int)(p.S - t0 < kC ? p.S - t0 : kC);                            // rows to write
     const int n = (int)(length <= t0 ? 0 : length - t0 < kC ? length - t0 : kC);       // tokens that are there
-    const int tiles = (p.V + kVT - 1) / kVT;
+    const int64_t BH = (int64_t)p.B * p.H;
+    const int prow = tid / 8, piece = tid % 8;                    // of the rows on their way to panels
 
-    // q, k and what they are multiplied by
-    for (int i = warp; i < kC; i += kThreads / 32) {
-        const uint16_t *qp = p.q + (t0 + i) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
-        const uint16_t *kp = p.k + (t0 + i) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2];
-        float sums[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < KP / 32; ++j) {
-            const int at = j * 32 + lane;
-            const float q = i < n && at < p.K ? value<DT>(qp + at) : 0.f, k = i < n && at < p.K ? value<DT>(kp + at) : 0.f;
-            sums[0] = fmaf(q, q, sums[0]);
-            sums[1] = fmaf(k, k, sums[1]);
-            sh.q[i][at] = q, sh.k[i][at] = k;
+    if (n == 0) {
+        for (int e = tid; e < kC * per; e += kThreads) {
+            const int i = e / per, h = g * per + e % per;
+            if (i < there) {
+                const int64_t at = ((t0 + i) * p.B + b) * p.H + h;
+                gp.grad_beta[at] = 0;
+                if (gp.grad_delta)
+                    gp.grad_delta[at] = 0;
+            }
+            if (i == 0)
+                gp.sum_A[(chunk * p.B + b) * p.H + h] = gp.sum_bias[(chunk * p.B + b) * p.H + h] = 0.f;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) {
-            sums[0] += __shfl_xor_sync(0xFFFFFFFFu, sums[0], d);
-            sums[1] += __shfl_xor_sync(0xFFFFFFFFu, sums[1], d);
+        for (int e = tid; e < there * p.K; e += kThreads) {
+            const int64_t at = (((t0 + e / p.K) * p.B + b) * p.G + g) * p.K + e % p.K;
+            gp.grad_q[at] = gp.grad_k[at] = 0;
         }
-        if (lane == 0)
-            sh.fq[i] = unit_factor(p.flags, sums[0]), sh.fk[i] = unit_factor(p.flags, sums[1]);
+        return;
     }
-    float gq[NK][4], gk[NK][4];        // of q', k', over the heads that share them
+    if (tid == 0) {
+        mbar_init(smem_u32(&sh.done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    if (warp == 0)
+        tmem_alloc(smem_u32(&sh.tmem), kColumns);
+    // q and k: as operands, and what they are multiplied by
 #pragma unroll
-    for (int j = 0; j < NK; ++j)
+    for (int w = 0; w < 2; ++w) {
+        const uint16_t *from = w ? p.k + (t0 + prow) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] : p.q + (t0 + prow) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
+        float x[KP / 64][8], sum = 0.f, most = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            gq[j][e] = gk[j][e] = 0.f;
+        for (int j = 0; j < KP / 64; ++j) {
+            const int at = 64 * j + 8 * piece;
+            load8<DT>(from + at, w ? gp.vectors_k : gp.vectors_q, prow < n ? p.K - at : 0, x[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum = fmaf(x[j][e], x[j][e], sum);
+            most = fmaxf(most, most8(x[j]));
+        }
+        sum = sum_of_lanes<8>(sum);
+        const float scale = scale_for(most_of_lanes<8>(most)), f = unit_factor(p.flags, sum);
+#pragma unroll
+        for (int j = 0; j < KP / 64; ++j) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = pack_half2(make_float2(x[j][2 * e] * scale, x[j][2 * e + 1] * scale));
+            *reinterpret_cast<uint4 *>(panels + Pn::QK + j * Pn::kQK + w * kPanelBytes + panel_at(prow, piece)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (piece == 0) {
+            if (w)
+                sh.fk[prow] = f, sh.xk[prow] = f * inverse_scale(scale);
+            else
+                sh.fq[prow] = f * p.scale, sh.xq[prow] = f * p.scale * inverse_scale(scale);
+        }
+    }
+    shared_to_async();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem, lanes = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+    constexpr uint32_t by_tokens = mma_kind(kC, false), by_keys = mma_kind(KP, false), keys_by_columns = mma_kind(KP, true), both_by_columns = mma_kind(KP, true, true);
+    uint32_t parity = 0;
+    bool ok = true;          // no wait gave up
+    if (tid == 0)            // q.k and k.k, exact; done with the first products that are waited for
+#pragma unroll
+        for (int j = 0; j < KP / 16; ++j) {
+            const uint32_t at = at_panels + Pn::QK + (j / 4) * Pn::kQK;
+            mma_ss(tmem + kDK, desc_rows(at) + 2 * (j % 4), desc_rows(at + kPanelBytes) + 2 * (j % 4), by_tokens, j > 0);
+        }
+    float acc[KC];           // of gq' or gk', over tiles and the heads that share them
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+        acc[c] = 0.f;
+    // this thread's keys of q (or k) as an operand
+    const auto own = [&](int c, float2 (&x)[4]) {      // eight from c on
+        const int at = quarter * KC + c;
+        const uint4 v = *reinterpret_cast<const uint4 *>(panels + Pn::QK + (at / 64) * Pn::kQK + (of_du ? kPanelBytes : 0) + panel_at(t, at % 64 / 8));
+        x[0] = unpack2<1>(v.x), x[1] = unpack2<1>(v.y), x[2] = unpack2<1>(v.z), x[3] = unpack2<1>(v.w);
+    };
 
-    for (int h = g * per; h < (g + 1) * per && n > 0; ++h) {
+    for (int h = g * per; h < (g + 1) * per; ++h) {
         const int64_t item = (int64_t)b * p.H + h;
         __syncthreads();
-        bring<DT, KP>(gp, sh.tile[0], chunk, item, b, h, n, 0);
         // gates, and the running sum of log2 a in two parts whose differences are
         // exact in the first: multiples of 2^-9 below 2^14
         if (tid < kC) {
-            const int64_t t = t0 + tid;
+            const int64_t at = t0 + tid;
             Gates gate = {0.f, 0.f, 0.f, 0.f};
             if (tid < n)
-                gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + t * p.delta_s[0] + b * p.delta_s[1] + h) : 0.f,
+                gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + at * p.delta_s[0] + b * p.delta_s[1] + h) : 0.f,
                                 p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
-                                value<DT>(p.beta + t * p.beta_s[0] + b * p.beta_s[1] + h));
+                                value<DT>(p.beta + at * p.beta_s[0] + b * p.beta_s[1] + h));
             const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f), hi = rintf(l * 512.f) * (1.f / 512.f);
             sh.ch[tid] = hi, sh.cl[tid] = l - hi, sh.b[tid] = gate.b, sh.dt[tid] = gate.dt, sh.raw[tid] = gate.raw;
         }
@@ -241,186 +293,228 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
             c[2 * lane + 1] = before + y;
         }
 
-        float P[4][4] = {}, L[4][4] = {}, qs[NK][4] = {}, ks[NK][4] = {}, ke[NK][4] = {}, gs = 0.f, dv = 0.f;
-        const bool low = c0 <= r0 + 15;        // some of the other tokens are not after the warp's
-        for (int tile = 0; tile < tiles; ++tile) {
-            if (tile + 1 < tiles) {
-                bring<DT, KP>(gp, sh.tile[(tile + 1) % 2], chunk, item, b, h, n, (tile + 1) * kVT);
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
+        float PL[IC], gs = 0.f, dv = 0.f, dot_s = 0.f, dot_g = 0.f;       // P' or L'; sums of S G, du.v, and along the row's q or k
+#pragma unroll
+        for (int c = 0; c < IC; ++c)
+            PL[c] = 0.f;
+        for (int v0 = 0; v0 < p.V; v0 += kVT) {
+            {
+                float x[8], y[8];
+                const int at = v0 + 8 * piece, live = prow < n ? p.V - at : 0;
+                const int64_t from = ((t0 + prow) * BH + item) * gp.Vp + at;
+                const float *s = gp.s + ((chunk * BH + item) * p.K + prow) * gp.Vp + at, *gr = gp.g + (s - gp.s);
+                float xs[KP / 64][8], xg[KP / 64][8];
+#pragma unroll
+                for (int j = 0; j < KP / 64; ++j) {
+                    const int there_k = prow + 64 * j < p.K ? p.V - at : 0;
+                    load8(s + (int64_t)64 * j * gp.Vp, there_k, xs[j]);
+                    load8(gr + (int64_t)64 * j * gp.Vp, there_k, xg[j]);
+                }
+                load8(gp.du + from, live, x);
+                load8<DT>(p.v + (t0 + prow) * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + at, gp.vectors_v, live, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dv = fmaf(x[e], y[e], dv);
+                const float of_du_row = put_row(panels + Pn::A, panels + Pn::ALo, kC + prow, piece, x);
+                load8(gp.u + from, live, x);
+                load8<DT>(p.grad_y + (t0 + prow) * p.gy_s[0] + b * p.gy_s[1] + h * p.gy_s[2] + at, gp.vectors_gy, live, y);
+#pragma unroll
+                for (int j = 0; j < KP / 64; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        gs = fmaf(xs[j][e], xg[j][e], gs);
+                    const float of = put_row(panels + Pn::S, panels + Pn::SLo, 64 * j + prow, piece, xs[j]);
+                    const float og = put_row(panels + Pn::G, panels + Pn::GLo, 64 * j + prow, piece, xg[j]);
+                    if (piece == 0)
+                        sh.of_s[64 * j + prow] = of, sh.of_g[64 * j + prow] = og;
+                }
+                const float of_u_row = put_row(panels + Pn::A, panels + Pn::ALo, 2 * kC + prow, piece, x);
+                const float of_y_row = put_row(panels + Pn::A, panels + Pn::ALo, prow, piece, y);
+                if (piece == 0)
+                    sh.of_rows[prow] = of_y_row, sh.of_rows[kC + prow] = of_du_row, sh.of_rows[2 * kC + prow] = of_u_row;
             }
+            shared_to_async();
+            tmem_fence_before();
             __syncthreads();
-            const GradTile<KP> &x = sh.tile[tile % 2];
-#pragma unroll 1
-            for (int v = 0; v < kVT; v += 8) {
-                uint32_t gy[4], duh[4], dul[4], uh[4], ul[4];
+            tmem_fence_after();
+            if (tid == 0) {
+                three_products(tmem + kDS, at_panels + Pn::A, at_panels + Pn::ALo, at_panels + Pn::S, at_panels + Pn::SLo, by_keys);
+                three_products(tmem + kDU, at_panels + Pn::A, at_panels + Pn::ALo, at_panels + Pn::A + 2 * kPanelBytes, at_panels + Pn::ALo + 2 * kPanelBytes,
+                               by_tokens);
+                three_products(tmem + kDG, at_panels + Pn::A + kPanelBytes, at_panels + Pn::ALo + kPanelBytes, at_panels + Pn::G, at_panels + Pn::GLo, by_keys);
+                mma_commit(smem_u32(&sh.done));
+            }
+            ok = ok && mbar_wait_bounded(smem_u32(&sh.done), parity);
+            parity ^= 1;
+            tmem_fence_after();
+            __syncwarp();
+            const float of_row = sh.of_rows[r], bt = sh.b[t];
+            const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
+            const float add = (of_du ? -ec : ec) * of_row, to_acc = of_du ? bt : 1.f, add_g = of_du ? el * sh.of_rows[kC + r] : 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    gy[e] = __float_as_uint(unpack2<DT>(x.gy[r0 + fg + 8 * (e % 2)][v + ft + 4 * (e / 2)]).x);
-                fragment<kVS>(x.du, r0, v, duh, dul);
-                fragment<kVS>(x.u, r0, v, uh, ul);
-                if (low)
+            for (int c = 0; c < KC; c += UNIT) {
+                uint32_t d[UNIT];
+                tmem_load(lanes + kDS + quarter * KC + c, d);
+                tmem_wait(d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const Terms u0 = terms(x.u[c0 + 8 * j + fg][v + ft]), u1 = terms(x.u[c0 + 8 * j + fg][v + ft + 4]);
-                        float x[4] = {}, y[4] = {};
-                        mma_exact_a(x, gy, u0, u1);
-                        mma_terms(y, duh, dul, u0, u1);
-                        add4(P[j], x), add4(L[j], y);
+                for (int e = 0; e < UNIT; e += 8) {
+                    float2 x[4];
+                    own(c + e, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float y = __uint_as_float(d[e + i]) * (add * sh.of_s[quarter * KC + c + e + i]);
+                        dot_s = fmaf(y, i % 2 ? x[i / 2].y : x[i / 2].x, dot_s);
+                        acc[c + e + i] = fmaf(to_acc, y, acc[c + e + i]);
                     }
-#pragma unroll
-                for (int j = 0; j < NK; ++j) {
-                    const int at = k0 + 8 * j + fg;
-                    const Terms s0 = terms(x.s[at][v + ft]), s1 = terms(x.s[at][v + ft + 4]);
-                    float x4[4] = {}, y4[4] = {}, z4[4] = {};
-                    mma_exact_a(x4, gy, s0, s1);
-                    mma_terms(y4, duh, dul, s0, s1);
-                    const Terms g0 = terms(x.g[at][v + ft]), g1 = terms(x.g[at][v + ft + 4]);
-                    mma_terms(z4, uh, ul, g0, g1);
-                    add4(qs[j], x4), add4(ks[j], y4), add4(ke[j], z4);
                 }
             }
-            for (int e = tid; e < kVT * KP; e += kThreads)
-                gs = fmaf(x.s[e / kVT][e % kVT], x.g[e / kVT][e % kVT], gs);
+            if (of_du)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)           // du.v: four threads to a token
-                dv = fmaf(x.du[tid / 4][8 * (tid % 4) + j], unpack2<DT>(x.v[tid / 4][8 * (tid % 4) + j]).x, dv);
-            __syncthreads();
-        }
+                for (int c = 0; c < KC; c += UNIT) {
+                    uint32_t d[UNIT];
+                    tmem_load(lanes + kDG + quarter * KC + c, d);
+                    tmem_wait(d);
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2)
-            gs += __shfl_xor_sync(0xFFFFFFFFu, gs, d);
-        if (lane == 0)
-            sh.dot[warp] = gs;
-        dv = sum4(dv);
-        if (tid % 4 == 0)
-            sh.dv[tid / 4] = dv;
-        const float last_h = sh.ch[kC - 1], last_l = sh.cl[kC - 1];
-        // the states' parts, and what they say about the decays
+                    for (int e = 0; e < UNIT; e += 8) {
+                        float2 x[4];
+                        own(c + e, x);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int t = r0 + fg + 8 * half;
-            const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((last_h - sh.ch[t]) + (last_l - sh.cl[t]), 127.f));
-            const float bt = sh.b[t];
-            float sq = 0.f, sk = 0.f, se = 0.f;
-#pragma unroll
-            for (int j = 0; j < NK; ++j)
-#pragma unroll
-                for (int e = 2 * half; e < 2 * half + 2; ++e) {
-                    const int at = k0 + 8 * j + 2 * ft + e % 2;
-                    const float q = sh.q[t][at], k = sh.k[t][at], x = ec * qs[j][e], y = -ec * ks[j][e], z = el * ke[j][e];
-                    sq = fmaf(x, q, sq);
-                    sk = fmaf(y, k, sk);
-                    se = fmaf(z, k, se);
-                    gq[j][e] += x;
-                    gk[j][e] += fmaf(bt, y, z);
-                }
-            sq = sum4(sq), sk = sum4(sk), se = sum4(se);
-            if (ft == 0) {
-                sh.sq[part][t] = sq * (sh.fq[t] * p.scale);
-                sh.sk[part][t] = sk * sh.fk[t];
-                sh.se[part][t] = se * sh.fk[t];
-            }
-        }
-        {   // k.k, q.k in the place of the states' parts: exact in one term each
-            float kk[4][4] = {}, qk[4][4] = {};
-            if (low)
-#pragma unroll 2
-                for (int at = 0; at < KP; at += 8) {
-                    uint32_t aq[4], ak[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        aq[e] = __float_as_uint(sh.q[r0 + fg + 8 * (e % 2)][at + ft + 4 * (e / 2)]);
-                        ak[e] = __float_as_uint(sh.k[r0 + fg + 8 * (e % 2)][at + ft + 4 * (e / 2)]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t x = __float_as_uint(sh.k[c0 + 8 * j + fg][at + ft]), y = __float_as_uint(sh.k[c0 + 8 * j + fg][at + ft + 4]);
-                        mma1688(kk[j], ak, x, y);
-                        mma1688(qk[j], aq, x, y);
-                    }
-                }
-            float col[4][2] = {};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = r0 + fg + 8 * half;
-                const float th = sh.ch[t], tl = sh.cl[t], bt = sh.b[t], fkt = sh.fk[t], fqt = sh.fq[t] * p.scale;
-                float row = 0.f, lowrow = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = c0 + 8 * j + 2 * ft + e, x = 2 * half + e;
-                        const float fki = sh.fk[i];
-                        const float D = i <= t ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) : 0.f;
-                        const float pd = i <= t ? P[j][x] * D : 0.f, ld = i < t ? -L[j][x] * D : 0.f, lk = ld * (kk[j][x] * fkt * fki);
-                        const float E = fmaf(pd, qk[j][x] * fqt * fki, bt * lk);
-                        row += E, lowrow += lk, col[j][e] += E;
-                        sh.P[t][i] = pd * fki;
-                        sh.PT[i][t] = pd * fqt;
-                        if (i <= t) {
-                            sh.M[t][i] = bt * ld * fki;
-                            sh.M[i][t] = bt * ld * fkt;
+                        for (int i = 0; i < 8; ++i) {
+                            const float y = __uint_as_float(d[e + i]) * (add_g * sh.of_g[quarter * KC + c + e + i]);
+                            dot_g = fmaf(y, i % 2 ? x[i / 2].y : x[i / 2].x, dot_g);
+                            acc[c + e + i] += y;
                         }
                     }
-                row = sum4(row), lowrow = sum4(lowrow);
-                if (ft == 0)
-                    sh.row[part][t] = row, sh.low[part][t] = lowrow;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float c = col[j][e];
-#pragma unroll
-                    for (int d = 4; d < 32; d *= 2)
-                        c += __shfl_xor_sync(0xFFFFFFFFu, c, d);
-                    if (fg == 0)
-                        sh.col[warp % 4][c0 + 8 * j + 2 * ft + e] = c;
                 }
-        }
-        __syncthreads();
-        // the tokens' own products, of two terms and q or k as they are
-#pragma unroll 1
-        for (int i = 0; i < kC; i += 8) {
-            uint32_t ph[4], pl[4], th[4], tl[4], mh[4], ml[4];
-            fragment<kTri>(sh.P, r0, i, ph, pl);
-            fragment<kTri>(sh.PT, r0, i, th, tl);
-            fragment<kTri>(sh.M, r0, i, mh, ml);
+            {
+                uint32_t d[IC];
+                tmem_load(lanes + kDU + quarter * IC, d);
+                tmem_wait(d);
+                const float f = of_du ? -of_row : of_row;
 #pragma unroll
-            for (int j = 0; j < NK; ++j) {
-                const int at = k0 + 8 * j + fg;
-                const uint32_t q0 = __float_as_uint(sh.q[i + ft][at]), q1 = __float_as_uint(sh.q[i + ft + 4][at]);
-                const uint32_t x0 = __float_as_uint(sh.k[i + ft][at]), x1 = __float_as_uint(sh.k[i + ft + 4][at]);
-                mma1688(gq[j], ph, x0, x1);
-                mma1688(gq[j], pl, x0, x1);
-                mma1688(gk[j], th, q0, q1);
-                mma1688(gk[j], tl, q0, q1);
-                mma1688(gk[j], mh, x0, x1);
-                mma1688(gk[j], ml, x0, x1);
+                for (int c = 0; c < IC; ++c)
+                    PL[c] = fmaf(__uint_as_float(d[c]), f * sh.of_rows[2 * kC + quarter * IC + c], PL[c]);
             }
+            tmem_fence_before();
+            __syncthreads();
+        }
+        gs = sum_of_lanes<32>(gs);
+        if (lane == 0)
+            sh.dot[warp] = gs;
+        dv = sum_of_lanes<8>(dv);
+        if (piece == 0)
+            sh.dv[prow] = dv;
+        if (of_du) {
+            sh.dots[1][quarter][t] = dot_s * sh.xk[t];
+            sh.dots[2][quarter][t] = dot_g * sh.xk[t];
+        } else {
+            sh.dots[0][quarter][t] = dot_s * sh.xq[t];
+        }
+        // P' and L', with the decays; by rows for the products with k, by columns
+        // with what the row's own token is multiplied by
+        {
+            uint32_t d[IC];
+            tmem_load(lanes + kDK + quarter * IC, d);
+            tmem_wait(d);
+            float E[IC], by_row[IC], row = 0.f, low = 0.f, most_row = 0.f, most_col = 0.f;
+            const float th = sh.ch[t], tl = sh.cl[t], f = of_du ? sh.xk[t] : sh.xq[t], bt = of_du ? sh.b[t] : 1.f;
+#pragma unroll
+            for (int c = 0; c < IC; ++c) {
+                const int i = quarter * IC + c;
+                const bool in = of_du ? i < t : i <= t;
+                const float D = in ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) : 0.f, x = in ? PL[c] * D : 0.f;
+                const float xi = sh.xk[i], lk = x * (__uint_as_float(d[c]) * f * xi);
+                E[c] = bt * lk;
+                low += lk, row += E[c];
+                by_row[c] = bt * x * xi;
+                PL[c] = bt * x * f;
+                most_row = fmaxf(most_row, fabsf(by_row[c]));
+                most_col = fmaxf(most_col, fabsf(PL[c]));
+            }
+            sh.row[of_du][quarter][t] = row;
+            if (of_du)
+                sh.low[quarter][t] = low;
+            const float col = sums16(E);
+            if (lane % 2 == 0)
+                sh.col[warp % 4][quarter * IC + lane / 2] = col;
+            most_col = most_of_lanes<32>(most_col);
+            if (lane == 0)
+                sh.most_of_warps[warp] = most_col;
+            sh.most[quarter][r] = most_row;
+            tmem_fence_before();
+            __syncthreads();
+            tmem_fence_after();
+            most_row = fmaxf(fmaxf(sh.most[0][r], sh.most[1][r]), fmaxf(sh.most[2][r], sh.most[3][r]));
+            most_col = sh.most_of_warps[0];
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w)
+                most_col = fmaxf(most_col, sh.most_of_warps[w]);
+            const float scale_row = scale_for(most_row), scale_col = scale_for(most_col);
+            uint8_t *hi = panels + (of_du ? Pn::LC : Pn::PC), *lo = panels + (of_du ? Pn::LCLo : Pn::PCLo);
+#pragma unroll
+            for (int e = 0; e < IC / 8; ++e) {
+                put8(panels + Pn::X, panels + Pn::XLo, panel_at(r, quarter * (IC / 8) + e), by_row + 8 * e, scale_row);
+                put8(hi, lo, panel_at(t, quarter * (IC / 8) + e), PL + 8 * e, scale_col);
+            }
+            shared_to_async();
+            tmem_fence_before();
+            __syncthreads();
+            tmem_fence_after();
+            if (tid == 0) {
+                const uint32_t qk = at_panels + Pn::QK;
+#pragma unroll
+                for (int j = 0; j < kC / 16; ++j) {
+                    const uint64_t step = (uint64_t)(2048 * j >> 4);
+                    const uint64_t q = desc_columns(qk, Pn::kQK) + step, k = desc_columns(qk + kPanelBytes, Pn::kQK) + step;
+                    mma_ss(tmem + kDG, desc_rows(at_panels + Pn::XLo) + 2 * j, k, keys_by_columns, j > 0);
+                    mma_ss(tmem + kDG, desc_rows(at_panels + Pn::X) + 2 * j, k, keys_by_columns, true);
+                    // 128 columns to the product, of the panel before too: the second half's rows are read
+                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::PCLo - kPanelBytes, kPanelBytes) + step, q, both_by_columns, j > 0);
+                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::LCLo - kPanelBytes, kPanelBytes) + step, k, both_by_columns, true);
+                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::PC - kPanelBytes, kPanelBytes) + step, q, both_by_columns, true);
+                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::LC - kPanelBytes, kPanelBytes) + step, k, both_by_columns, true);
+                }
+                mma_commit(smem_u32(&sh.done));
+            }
+            ok = ok && mbar_wait_bounded(smem_u32(&sh.done), parity);
+            parity ^= 1;
+            tmem_fence_after();
+            __syncwarp();
+            const float of_x = inverse_scale(scale_row), of_c = of_du ? inverse_scale(scale_col) : 0.f;
+#pragma unroll
+            for (int c = 0; c < KC; c += UNIT) {
+                uint32_t x[UNIT], y[UNIT];
+                tmem_load(lanes + kDG + quarter * KC + c, x);
+                tmem_load(lanes + kDS + quarter * KC + c, y);
+                tmem_wait(x), tmem_wait(y);
+#pragma unroll
+                for (int e = 0; e < UNIT; ++e) {
+                    acc[c + e] = fmaf(of_x, __uint_as_float(x[e]), acc[c + e]);
+                    if (of_du)
+                        acc[c + e] = fmaf(of_c, __uint_as_float(y[e]), acc[c + e]);
+                }
+            }
+            tmem_fence_before();
         }
         if (warp == 0) {
             const float A = p.delta ? __ldg(p.A + h) : 0.f;
+            const auto four = [](const float (&x)[kQuarters][kC], int i) { return (x[0][i] + x[1][i]) + (x[2][i] + x[3][i]); };
             float x[2], all_e = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float se = sh.se[0][t] + sh.se[1][t], sk = sh.sk[0][t] + sh.sk[1][t];
-                x[e] = (sh.row[0][t] + sh.row[1][t]) - ((sh.col[0][t] + sh.col[1][t]) + (sh.col[2][t] + sh.col[3][t]));
-                x[e] += (sh.sq[0][t] + sh.sq[1][t]) + sh.b[t] * sk - se;
-                sh.gb[t] = sh.dv[t] + sk + (sh.low[0][t] + sh.low[1][t]);
+                const int i = 2 * lane + e;
+                const float se = four(sh.dots[2], i), sk = four(sh.dots[1], i);
+                x[e] = (four(sh.row[0], i) + four(sh.row[1], i)) - ((sh.col[0][i] + sh.col[1][i]) + (sh.col[2][i] + sh.col[3][i]));
+                x[e] += four(sh.dots[0], i) + sh.b[i] * sk - se;
+                sh.gb[i] = sh.dv[i] + sk + four(sh.low, i);
                 all_e += se;
             }
-#pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                all_e += __shfl_xor_sync(0xFFFFFFFFu, all_e, d);
+            all_e = sum_of_lanes<32>(all_e);
             if (lane == 31) {
                 float s = 0.f;
                 for (int w = 0; w < kThreads / 32; ++w)
                     s += sh.dot[w];
-                x[1] += fmaf(s, ex2(fminf(last_h + last_l, 127.f)), all_e);
+                x[1] += fmaf(s, ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), all_e);
             }
             const float y = x[0] + x[1];
             float s = y;      // sums to the end
@@ -451,74 +545,68 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
                 sa = fmaf(gl, sh.dt[i], sa);
                 sb += graw;
             }
-#pragma unroll
-            for (int d = 16; d > 0; d /= 2) {
-                sa += __shfl_xor_sync(0xFFFFFFFFu, sa, d);
-                sb += __shfl_xor_sync(0xFFFFFFFFu, sb, d);
-            }
+            sa = sum_of_lanes<32>(sa), sb = sum_of_lanes<32>(sb);
             if (lane == 0) {
                 gp.sum_A[(chunk * p.B + b) * p.H + h] = sa;
                 gp.sum_bias[(chunk * p.B + b) * p.H + h] = sb;
             }
         }
     }
-    __syncthreads();
-    if (n == 0)
-        for (int e = tid; e < kC * per; e += kThreads) {
-            const int i = e / per, h = g * per + e % per;
-            if (i < there) {
-                const int64_t at = ((t0 + i) * p.B + b) * p.H + h;
-                gp.grad_beta[at] = 0;
-                if (gp.grad_delta)
-                    gp.grad_delta[at] = 0;
-            }
-            if (i == 0)
-                gp.sum_A[(chunk * p.B + b) * p.H + h] = gp.sum_bias[(chunk * p.B + b) * p.H + h] = 0.f;
-        }
     // through the division by the lengths: (g - x (x.g)) f for a unit vector x
-    const bool norm = p.flags & MCC1D_QK_NORM;
+    float dot = 0.f;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int t = r0 + fg + 8 * half;
-        float dq = 0.f, dk = 0.f;
+    for (int c = 0; c < KC; c += 8) {
+        float2 x[4];
+        own(c, x);
 #pragma unroll
-        for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int at = k0 + 8 * j + 2 * ft + e;
-                dq = fmaf(gq[j][2 * half + e], sh.q[t][at], dq);
-                dk = fmaf(gk[j][2 * half + e], sh.k[t][at], dk);
-            }
-        dq = sum4(dq), dk = sum4(dk);
-        if (ft == 0)
-            sh.sq[part][t] = dq, sh.sk[part][t] = dk;
+        for (int i = 0; i < 8; ++i)
+            dot = fmaf(acc[c + i], i % 2 ? x[i / 2].y : x[i / 2].x, dot);
     }
     __syncthreads();
+    sh.most[quarter][r] = dot;
+    __syncthreads();
+    const float f = of_du ? sh.fk[t] : sh.fq[t], fx = of_du ? sh.xk[t] : sh.xq[t];
+    dot = (sh.most[0][r] + sh.most[1][r]) + (sh.most[2][r] + sh.most[3][r]);
+    // q' is scale times a unit vector
+    const float unit = of_du ? 1.f : p.scale != 0.f ? 1.f / (p.scale * p.scale) : 0.f;
+    const float back = p.flags & MCC1D_QK_NORM ? -dot * fx * fx * unit : 0.f;
+    if (t < there) {
+        uint16_t *to = (of_du ? gp.grad_k : gp.grad_q) + (((t0 + t) * p.B + b) * p.G + g) * p.K;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int t = r0 + fg + 8 * half;
-        if (t >= there)
-            continue;
-        const float fq = sh.fq[t], fk = sh.fk[t];
-        const float dq = norm ? (sh.sq[0][t] + sh.sq[1][t]) * fq * fq : 0.f, dk = norm ? (sh.sk[0][t] + sh.sk[1][t]) * fk * fk : 0.f;
-        const int64_t to = (((t0 + t) * p.B + b) * p.G + g) * p.K;
+        for (int c = 0; c < KC; c += 8) {
+            float2 x[4];
+            own(c, x);
 #pragma unroll
-        for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int at = k0 + 8 * j + 2 * ft + e;
-                if (at < p.K) {
-                    gp.grad_q[to + at] = (uint16_t)pack2<DT>(make_float2(fmaf(-sh.q[t][at], dq, gq[j][2 * half + e]) * (fq * p.scale), 0.f));
-                    gp.grad_k[to + at] = (uint16_t)pack2<DT>(make_float2(fmaf(-sh.k[t][at], dk, gk[j][2 * half + e]) * fk, 0.f));
+            for (int i = 0; i < 4; ++i) {
+                const int at = quarter * KC + c + 2 * i;
+                float2 v = make_float2(fmaf(back, x[i].x, acc[c + 2 * i]) * f, fmaf(back, x[i].y, acc[c + 2 * i + 1]) * f);
+                if (!ok)
+                    v.x = v.y = __uint_as_float(0x7FFFFFFFu);
+                const uint32_t both = pack2<DT>(v);
+                if (gp.pairs) {
+                    if (at < p.K)
+                        *reinterpret_cast<uint32_t *>(to + at) = both;
+                } else {
+                    if (at < p.K)
+                        to[at] = (uint16_t)both;
+                    if (at + 1 < p.K)
+                        to[at + 1] = (uint16_t)(both >> 16);
                 }
             }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tmem_fence_after();
+        tmem_free(tmem, kColumns);
     }
 }
 
 template <int DT, int KP>
 int32_t grad(const GradParams &p, int64_t blocks, cudaStream_t stream)
 {
-    constexpr int bytes = (int)sizeof(GradShared<KP>);
+    constexpr int bytes = Panels<KP>::kBytes + 1024;
     if (cudaFuncSetAttribute(delta_grad_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
     return launch(delta_grad_kernel<DT, KP>, dim3((unsigned)blocks), kThreads, bytes, stream, p);
@@ -578,8 +666,10 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     for (int i = 0; i < 3; ++i)
         p.d.gy_s[i] = a.grad_y_strides[i];
     p.u = kept.u, p.du = back.u, p.s = kept.states, p.g = back.states, p.Vp = plan.Vp;
-    const auto vectors = [&](const void *x, const int64_t (&s)[3]) { return vectors_for(f.V, (uintptr_t)x, s[0] | s[1] | s[2]); };
-    p.vectors_gy = vectors(a.grad_y, a.grad_y_strides), p.vectors_v = vectors(f.v, f.v_strides);
+    const auto vectors = [](int64_t n, const void *x, const int64_t (&s)[3]) { return vectors_for(n, (uintptr_t)x, s[0] | s[1] | s[2]); };
+    p.vectors_gy = vectors(f.V, a.grad_y, a.grad_y_strides), p.vectors_v = vectors(f.V, f.v, f.v_strides);
+    p.vectors_q = vectors(f.K, f.q, f.q_strides), p.vectors_k = vectors(f.K, f.k, f.k_strides);
+    p.pairs = f.K % 2 == 0 && (((uintptr_t)a.grad_q | (uintptr_t)a.grad_k) & 3u) == 0;
     p.grad_q = static_cast<uint16_t *>(a.grad_q), p.grad_k = static_cast<uint16_t *>(a.grad_k);
     p.grad_delta = f.delta ? static_cast<uint16_t *>(a.grad_delta) : nullptr, p.grad_beta = static_cast<uint16_t *>(a.grad_beta);
     const int64_t parts = plan.chunks * f.B;
