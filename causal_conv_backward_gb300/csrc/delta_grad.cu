@@ -30,7 +30,7 @@ struct GradParams {
     DeltaParams d;
     const float *u, *du, *s, *g;   // [S,B,H,Vp], [chunks][B H][K,Vp]
     int32_t Vp;
-    bool vectors_q, vectors_k, vectors_gy, vectors_v, pairs;
+    bool vectors_q, vectors_k, vectors_gy, vectors_v, vectors_out;
     uint16_t *grad_q, *grad_k, *grad_delta, *grad_beta;
     float *sum_A, *sum_bias;       // [chunks B][H]
 };
@@ -66,6 +66,11 @@ enum { kDS = 0, kDU = 128, kDG = 192, kDK = 320, kColumns = 512 };
 // Eight values of a workspace row, zeros past its end.
 __device__ __forceinline__ void load8(const float *from, int live, float (&x)[8])
 {
+    if (live >= 8) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(from)), w = __ldg(reinterpret_cast<const float4 *>(from) + 1);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -130,6 +135,26 @@ __device__ __forceinline__ float put_row(uint8_t *hi, uint8_t *lo, int row, int 
     const float scale = scale_for(most_of_lanes<8>(most8(x)));
     put8(hi, lo, panel_at(row, piece), x, scale);
     return inverse_scale(scale);
+}
+
+// The rows of a tile of V, asked for ahead of their use (64 values of a row are
+// two lines of 128 bytes; a thread of every four asks).
+__device__ __forceinline__ void ask_ahead(const GradParams &gp, int64_t chunk, int64_t item, int v0, int row, int piece, int n)
+{
+    const DeltaParams &p = gp.d;
+    const int at = v0 + 8 * piece;
+    if (piece % 4 || at >= p.V)
+        return;
+    const auto ask = [](const float *x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); };
+    const int64_t BH = (int64_t)p.B * p.H;
+    if (row < n) {
+        const int64_t from = ((chunk * kC + row) * BH + item) * gp.Vp + at;
+        ask(gp.u + from), ask(gp.du + from);
+    }
+    for (int k = row; k < p.K; k += kC) {
+        const int64_t from = ((chunk * BH + item) * p.K + k) * gp.Vp + at;
+        ask(gp.s + from), ask(gp.g + from);
+    }
 }
 
 // Sums of 16 values over the warp's lanes: lane l has that of value l / 2.
@@ -207,34 +232,44 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     if (warp == 0)
         tmem_alloc(smem_u32(&sh.tmem), kColumns);
     // q and k: as operands, and what they are multiplied by
+    {
+        float x[2][KP / 64][8];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const uint16_t *from = w ? p.k + (t0 + prow) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] : p.q + (t0 + prow) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
-        float x[KP / 64][8], sum = 0.f, most = 0.f;
+        for (int w = 0; w < 2; ++w) {
+            const uint16_t *from = w ? p.k + (t0 + prow) * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] : p.q + (t0 + prow) * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2];
 #pragma unroll
-        for (int j = 0; j < KP / 64; ++j) {
-            const int at = 64 * j + 8 * piece;
-            load8<DT>(from + at, w ? gp.vectors_k : gp.vectors_q, prow < n ? p.K - at : 0, x[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum = fmaf(x[j][e], x[j][e], sum);
-            most = fmaxf(most, most8(x[j]));
+            for (int j = 0; j < KP / 64; ++j) {
+                const int at = 64 * j + 8 * piece;
+                load8<DT>(from + at, w ? gp.vectors_k : gp.vectors_q, prow < n ? p.K - at : 0, x[w][j]);
+            }
         }
-        sum = sum_of_lanes<8>(sum);
-        const float scale = scale_for(most_of_lanes<8>(most)), f = unit_factor(p.flags, sum);
+        ask_ahead(gp, chunk, (int64_t)b * p.H + g * per, 0, prow, piece, n);
 #pragma unroll
-        for (int j = 0; j < KP / 64; ++j) {
-            uint32_t h[4];
+        for (int w = 0; w < 2; ++w) {
+            float sum = 0.f, most = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                h[e] = pack_half2(make_float2(x[j][2 * e] * scale, x[j][2 * e + 1] * scale));
-            *reinterpret_cast<uint4 *>(panels + Pn::QK + j * Pn::kQK + w * kPanelBytes + panel_at(prow, piece)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-        if (piece == 0) {
-            if (w)
-                sh.fk[prow] = f, sh.xk[prow] = f * inverse_scale(scale);
-            else
-                sh.fq[prow] = f * p.scale, sh.xq[prow] = f * p.scale * inverse_scale(scale);
+            for (int j = 0; j < KP / 64; ++j) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum = fmaf(x[w][j][e], x[w][j][e], sum);
+                most = fmaxf(most, most8(x[w][j]));
+            }
+            sum = sum_of_lanes<8>(sum);
+            const float scale = scale_for(most_of_lanes<8>(most)), f = unit_factor(p.flags, sum);
+#pragma unroll
+            for (int j = 0; j < KP / 64; ++j) {
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = pack_half2(make_float2(x[w][j][2 * e] * scale, x[w][j][2 * e + 1] * scale));
+                *reinterpret_cast<uint4 *>(panels + Pn::QK + j * Pn::kQK + w * kPanelBytes + panel_at(prow, piece)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            if (piece == 0) {
+                if (w)
+                    sh.fk[prow] = f, sh.xk[prow] = f * inverse_scale(scale);
+                else
+                    sh.fq[prow] = f * p.scale, sh.xq[prow] = f * p.scale * inverse_scale(scale);
+            }
         }
     }
     shared_to_async();
@@ -264,34 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 
     for (int h = g * per; h < (g + 1) * per; ++h) {
         const int64_t item = (int64_t)b * p.H + h;
-        __syncthreads();
-        // gates, and the running sum of log2 a in two parts whose differences are
-        // exact in the first: multiples of 2^-9 below 2^14
-        if (tid < kC) {
-            const int64_t at = t0 + tid;
-            Gates gate = {0.f, 0.f, 0.f, 0.f};
-            if (tid < n)
-                gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + at * p.delta_s[0] + b * p.delta_s[1] + h) : 0.f,
-                                p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
-                                value<DT>(p.beta + at * p.beta_s[0] + b * p.beta_s[1] + h));
-            const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f), hi = rintf(l * 512.f) * (1.f / 512.f);
-            sh.ch[tid] = hi, sh.cl[tid] = l - hi, sh.b[tid] = gate.b, sh.dt[tid] = gate.dt, sh.raw[tid] = gate.raw;
-        }
-        __syncthreads();
-        if (warp < 2) {
-            float *c = warp == 0 ? sh.ch : sh.cl;
-            const float x = c[2 * lane], y = c[2 * lane + 1] + x;
-            float s = y;
+        float raw_delta[2] = {0.f, 0.f}, raw_beta[2] = {0.f, 0.f};      // of the first warp's tokens
+        if (warp == 0)
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const float o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-                if (lane >= d)
-                    s += o;
+            for (int e = 0; e < 2; ++e) {
+                const int64_t at = t0 + 2 * lane + e;
+                if (2 * lane + e < n) {
+                    if (p.delta)
+                        raw_delta[e] = value<DT>(p.delta + at * p.delta_s[0] + b * p.delta_s[1] + h);
+                    raw_beta[e] = value<DT>(p.beta + at * p.beta_s[0] + b * p.beta_s[1] + h);
+                }
             }
-            const float o = __shfl_up_sync(0xFFFFFFFFu, s, 1), before = lane > 0 ? o : 0.f;
-            c[2 * lane] = before + x;
-            c[2 * lane + 1] = before + y;
-        }
+        __syncthreads();
 
         float PL[IC], gs = 0.f, dv = 0.f, dot_s = 0.f, dot_g = 0.f;       // P' or L'; sums of S G, du.v, and along the row's q or k
 #pragma unroll
@@ -333,10 +352,40 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
                 if (piece == 0)
                     sh.of_rows[prow] = of_y_row, sh.of_rows[kC + prow] = of_du_row, sh.of_rows[2 * kC + prow] = of_u_row;
             }
+            if (warp == 0 && v0 == 0) {
+                // gates, and the running sum of log2 a in two parts whose differences are
+                // exact in the first: multiples of 2^-9 below 2^14
+                float hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * lane + e;
+                    Gates gate = {0.f, 0.f, 0.f, 0.f};
+                    if (i < n)
+                        gate = gates_of(p.flags, p.delta != nullptr, raw_delta[e], p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
+                                        raw_beta[e]);
+                    const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f);
+                    hi[e] = rintf(l * 512.f) * (1.f / 512.f), lo[e] = l - hi[e];
+                    sh.b[i] = gate.b, sh.dt[i] = gate.dt, sh.raw[i] = gate.raw;
+                }
+                float x = hi[0] + hi[1], y = lo[0] + lo[1];
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const float ox = __shfl_up_sync(0xFFFFFFFFu, x, d), oy = __shfl_up_sync(0xFFFFFFFFu, y, d);
+                    if (lane >= d)
+                        x += ox, y += oy;
+                }
+                sh.ch[2 * lane] = x - hi[1], sh.ch[2 * lane + 1] = x;
+                const float before = __shfl_up_sync(0xFFFFFFFFu, y, 1);
+                sh.cl[2 * lane] = (lane > 0 ? before : 0.f) + lo[0], sh.cl[2 * lane + 1] = y;
+            }
             shared_to_async();
             tmem_fence_before();
             __syncthreads();
             tmem_fence_after();
+            if (v0 + kVT < p.V)
+                ask_ahead(gp, chunk, item, v0 + kVT, prow, piece, n);
+            else if (h + 1 < (g + 1) * per)
+                ask_ahead(gp, chunk, item + 1, 0, prow, piece, n);
             if (tid == 0) {
                 three_products(tmem + kDS, at_panels + Pn::A, at_panels + Pn::ALo, at_panels + Pn::S, at_panels + Pn::SLo, by_keys);
                 three_products(tmem + kDU, at_panels + Pn::A, at_panels + Pn::ALo, at_panels + Pn::A + 2 * kPanelBytes, at_panels + Pn::ALo + 2 * kPanelBytes,
@@ -576,22 +625,23 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         for (int c = 0; c < KC; c += 8) {
             float2 x[4];
             own(c, x);
+            const int at = quarter * KC + c;
+            uint32_t u[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = quarter * KC + c + 2 * i;
                 float2 v = make_float2(fmaf(back, x[i].x, acc[c + 2 * i]) * f, fmaf(back, x[i].y, acc[c + 2 * i + 1]) * f);
                 if (!ok)
                     v.x = v.y = __uint_as_float(0x7FFFFFFFu);
-                const uint32_t both = pack2<DT>(v);
-                if (gp.pairs) {
-                    if (at < p.K)
-                        *reinterpret_cast<uint32_t *>(to + at) = both;
-                } else {
-                    if (at < p.K)
-                        to[at] = (uint16_t)both;
-                    if (at + 1 < p.K)
-                        to[at + 1] = (uint16_t)(both >> 16);
-                }
+                u[i] = pack2<DT>(v);
+            }
+            if (gp.vectors_out) {
+                if (at < p.K)
+                    *reinterpret_cast<uint4 *>(to + at) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (at + i < p.K)
+                        to[at + i] = (uint16_t)(u[i / 2] >> (16 * (i % 2)));
             }
         }
     }
@@ -669,7 +719,7 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
     const auto vectors = [](int64_t n, const void *x, const int64_t (&s)[3]) { return vectors_for(n, (uintptr_t)x, s[0] | s[1] | s[2]); };
     p.vectors_gy = vectors(f.V, a.grad_y, a.grad_y_strides), p.vectors_v = vectors(f.V, f.v, f.v_strides);
     p.vectors_q = vectors(f.K, f.q, f.q_strides), p.vectors_k = vectors(f.K, f.k, f.k_strides);
-    p.pairs = f.K % 2 == 0 && (((uintptr_t)a.grad_q | (uintptr_t)a.grad_k) & 3u) == 0;
+    p.vectors_out = vectors_for(f.K, (uintptr_t)a.grad_q | (uintptr_t)a.grad_k, 0);
     p.grad_q = static_cast<uint16_t *>(a.grad_q), p.grad_k = static_cast<uint16_t *>(a.grad_k);
     p.grad_delta = f.delta ? static_cast<uint16_t *>(a.grad_delta) : nullptr, p.grad_beta = static_cast<uint16_t *>(a.grad_beta);
     const int64_t parts = plan.chunks * f.B;
