@@ -54,6 +54,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// A value as two tf32 terms, 22 bits, and their products.
+__device__ __forceinline__ void tf32_terms(float x, uint32_t &hi, uint32_t &lo)
+{
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // Four 8 x 8 matrices of 16-bit values, the rows' addresses from eight lanes each.
 __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at)
 {
@@ -217,11 +229,13 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
                 load_matrices(aq, q + 2 * at);
                 load_matrices(ak, k + 2 * at);
                 load_matrices(x, c + 2 * at);
-                load_matrices(y, c + 2 * at + 16 * RS * 2);
                 mma16816<DT>(kk[0], ak, x[0], x[1]), mma16816<DT>(kk[1], ak, x[2], x[3]);
-                mma16816<DT>(kk[2], ak, y[0], y[1]), mma16816<DT>(kk[3], ak, y[2], y[3]);
                 mma16816<DT>(qk[0], aq, x[0], x[1]), mma16816<DT>(qk[1], aq, x[2], x[3]);
-                mma16816<DT>(qk[2], aq, y[0], y[1]), mma16816<DT>(qk[3], aq, y[2], y[3]);
+                if (c0 + 16 <= r0) {
+                    load_matrices(y, c + 2 * at + 16 * RS * 2);
+                    mma16816<DT>(kk[2], ak, y[0], y[1]), mma16816<DT>(kk[3], ak, y[2], y[3]);
+                    mma16816<DT>(qk[2], aq, y[0], y[1]), mma16816<DT>(qk[3], aq, y[2], y[3]);
+                }
             }
         }
 #pragma unroll
@@ -230,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
             const float th = sh.ch[t], tl = sh.cl[t], lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                if (c0 + 8 * j > r0 + 15)          // above the diagonal: read by nothing
+                    continue;
                 float l[2], x[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -244,10 +260,10 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
         }
     }
     __syncthreads();
-    for (int e = tid; e < kC * kC / 4; e += kThreads)
-        *reinterpret_cast<float4 *>(&sh.T[e / (kC / 4)][4 * (e % (kC / 4))]) = make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncthreads();
-    if (warp < 4 && lane < 16) {         // the diagonal blocks, a column to a thread
+    if (warp >= 4) {                     // zeros beside them, above the diagonal, that the wider products read
+        const int e = tid - 128, o = 32 * (e / 64), i = e % 64 / 4, j = 16 + 4 * (e % 4);
+        *reinterpret_cast<float4 *>(&sh.T[o + i][o + j]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else if (lane < 16) {              // the diagonal blocks, a column to a thread
         float x[16];
         const int o = 16 * warp;
 #pragma unroll
@@ -272,28 +288,34 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
     __syncthreads();
     small_product<32>(sh.T, 32, 0, sh.T, 32, 32, sh.X, 0, 0, -1.f, tid, kThreads);
     __syncthreads();
-    {   // P T, four rows and four columns to a thread
-        const int r = 4 * (tid / 16), c = 4 * (tid % 16);
-        float s[4][4] = {};
-        if (c <= r + 3)
-            for (int m = c; m < r + 4; m += 4) {
-                float4 x[4], y[4];
+    {   // P T on the tensor cores, two tf32 terms to a value: 16 rows and every other
+        // eight columns to a warp, tokens from the column's to the row's
+        const int r0 = 16 * (warp % 4), row = lane / 4, col = lane % 4;
+        float acc[4][4] = {};
+        for (int m = 0; m < r0 + 16; m += 8) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = *reinterpret_cast<const float4 *>(&sh.P[r + i][m]), y[i] = *reinterpret_cast<const float4 *>(&sh.T[m + i][c]);
+            for (int e = 0; e < 4; ++e)
+                tf32_terms(sh.P[r0 + row + 8 * (e % 2)][m + col + 4 * (e / 2)], ah[e], al[e]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        s[i][0] = fmaf(xs[k], y[k].x, s[i][0]), s[i][1] = fmaf(xs[k], y[k].y, s[i][1]);
-                        s[i][2] = fmaf(xs[k], y[k].z, s[i][2]), s[i][3] = fmaf(xs[k], y[k].w, s[i][3]);
-                    }
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int c = 8 * (2 * j + warp / 4);
+                if (c > m)
+                    continue;
+                uint32_t bh[2], bl[2];
+                tf32_terms(sh.T[m + col][c + row], bh[0], bl[0]);
+                tf32_terms(sh.T[m + col + 4][c + row], bh[1], bl[1]);
+                mma1688(acc[j], ah, bl[0], bl[1]);
+                mma1688(acc[j], al, bh[0], bh[1]);
+                mma1688(acc[j], ah, bh[0], bh[1]);
             }
+        }
+        // X holds what the last corner was made of: others are past it
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4 *>(&sh.X[r + i][c]) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float2 *>(&sh.X[r0 + row + 8 * e][8 * (2 * j + warp / 4) + 2 * col]) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
     }
     __syncthreads();
     // T by rows, P T as a whole scaled to fp16's range; four threads to a row
@@ -307,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
+        if (16 * part + j > t)         // never written
+            xt[j] = 0.f;
         most_t = fmaxf(most_t, fabsf(xt[j])), sum_t += fabsf(xt[j]);
         most_p = fmaxf(most_p, fabsf(xp[j]));
     }
