@@ -39,7 +39,7 @@ _ready = None
 def _load():
     """The library with this module's prototypes."""
     global _ready
-    lib = _base._load()
+    lib = _base._lib if _base._lib is not None else _base._load()
     if _ready is not lib:
         size, u64 = ctypes.POINTER(ctypes.c_uint64), ctypes.c_uint64
         for name, args in (("delta", [_vp, u64]), ("delta_bwd", [_vp, u64]), ("delta_step", [])):
@@ -49,7 +49,6 @@ def _load():
             f = getattr(lib, f"mcc1d_{name}_workspace_size")
             f.argtypes, f.restype = [_vp, size], _i32
         _ready = lib
-    return lib
 
 
 def _flags(delta_softplus, beta_sigmoid, qk_norm):
@@ -70,8 +69,7 @@ def _fields(q, k, v, delta, beta, A, delta_bias, softplus, sigmoid, norm, scale,
     dt, f32 = q.dtype, _base._torch.float32
     if delta is not None and A is None:
         raise ValueError("delta needs A")
-    return (q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _rows(k, "k", q.shape, dt, index), k.stride(0), k.stride(1),
-            k.stride(2), _rows(v, "v", (S, B, H, V), dt, index), v.stride(0), v.stride(1), v.stride(2),
+    return (q.data_ptr(), *q.stride()[:3], _rows(k, "k", q.shape, dt, index), *k.stride()[:3], _rows(v, "v", (S, B, H, V), dt, index), *v.stride()[:3],
             *((0, 0, 0) if delta is None else (_rows(delta, "delta", (S, B, H), dt, index), delta.stride(0), delta.stride(1))),
             _rows(beta, "beta", (S, B, H), dt, index), beta.stride(0), beta.stride(1), _optional(A, "A", (H,), f32, index),
             _optional(delta_bias, "delta_bias", (H,), f32, index), _optional(state, "state", (B, H, V, K), f32, index),
@@ -123,7 +121,7 @@ def gated_delta_backward(grad_y, q, k, v, delta, beta, A=None, delta_bias=None, 
     if delta_bias is not None and delta is None:
         raise ValueError("delta_bias needs delta")
     handle, stream = _stream(stream, index)
-    at = _rows(grad_y, "grad_y", (S, B, H, V), dt, index), grad_y.stride(0), grad_y.stride(1), grad_y.stride(2)
+    at = _rows(grad_y, "grad_y", (S, B, H, V), dt, index), *grad_y.stride()[:3]
     at_final = _optional(grad_final_state, "grad_final_state", (B, H, V, K), f32, index)
 
     def out(like, shape, dtype):
@@ -155,8 +153,8 @@ def gated_delta_step(q, k, v, delta, beta, state, A=None, delta_bias=None, *, de
     cache, rows, at = _cache(state, (H, V, K), f32, index, B, slots)
     if y is None:
         y = _empty((B, H, V), dt, q.device, stream)
-    args = _pack_step(q.data_ptr(), q.stride(0), q.stride(1), _rows(k, "k", q.shape, dt, index), k.stride(0), k.stride(1),
-                      _rows(v, "v", (B, H, V), dt, index), v.stride(0), v.stride(1),
+    args = _pack_step(q.data_ptr(), *q.stride()[:2], _rows(k, "k", q.shape, dt, index), *k.stride()[:2],
+                      _rows(v, "v", (B, H, V), dt, index), *v.stride()[:2],
                       *((0, 0) if delta is None else (_rows(delta, "delta", (B, H), dt, index), delta.stride(0))),
                       _rows(beta, "beta", (B, H), dt, index), beta.stride(0), _optional(A, "A", (H,), f32, index),
                       _optional(delta_bias, "delta_bias", (H,), f32, index), cache, at, _dense(y, "y", (B, H, V), dt, index),

@@ -41,7 +41,7 @@ _ready = None
 def _load():
     """The library with this module's prototypes."""
     global _ready
-    lib = _base._load()
+    lib = _base._lib if _base._lib is not None else _base._load()
     if _ready is not lib:
         size, u64 = ctypes.POINTER(ctypes.c_uint64), ctypes.c_uint64
         for name, args in (("gated_norm", []), ("gated_norm_bwd", [_vp, u64]), ("residual_norm", []),
@@ -52,29 +52,29 @@ def _load():
             f = getattr(lib, f"mcc1d_{name}_workspace_size")
             f.argtypes, f.restype = [_vp, size], _i32
         _ready = lib
-    return lib
 
 
 def _leading(t, name, least, most):
-    """Shape (filled up on the left with ones), dtype code and device of the leading tensor."""
-    if not least <= t.dim() <= most:
-        raise ValueError(f"{name} must have {least} to {most} dimensions, not {t.dim()}")
-    shape, code, index = _first(t, name, t.dim())
-    return (1,) * (most - len(shape)) + tuple(shape), code, index
+    """Shape, the same filled up on the left with ones, dtype code and device of the leading tensor."""
+    n = t.dim()
+    if not least <= n <= most:
+        raise ValueError(f"{name} must have {least} to {most} dimensions, not {n}")
+    shape, code, index = _first(t, name, n)
+    return shape, (1,) * (most - n) + tuple(shape), code, index
 
 
 def _steps(t, most):
     """The strides of all axes but the last, filled up on the left with zeros."""
-    n = t.dim()
-    return (0,) * (most - n) + tuple(t.stride(i) for i in range(n - 1))
+    s = t.stride()
+    return (0,) * (most - len(s)) + s[:-1]
 
 
 # ------------------------------------------------------------------ behind the mixer
-def _gated_fields(x, z, weight, y, eps):
-    (S, B, H, D), code, index = _leading(x, "x", 2, 4)
+def _gated_fields(x, z, weight, y, eps, lead):
+    shape, (S, B, H, D), code, index = lead
     dt = x.dtype
-    return (x.data_ptr(), *_steps(x, 4), *((0, 0, 0, 0) if z is None else (_rows(z, "z", x.shape, dt, index), *_steps(z, 4))),
-            _dense(weight, "weight", (D,), dt, index), _optional(y, "y", x.shape, dt, index), S, B, H, D, eps, code, 0)
+    return (x.data_ptr(), *_steps(x, 4), *((0, 0, 0, 0) if z is None else (_rows(z, "z", shape, dt, index), *_steps(z, 4))),
+            _dense(weight, "weight", (D,), dt, index), 0 if y is None else _dense(y, "y", shape, dt, index), S, B, H, D, eps, code, 0)
 
 
 def gated_norm(x, z, weight, *, eps=1e-6, y=None, stream=None):
@@ -83,13 +83,13 @@ def gated_norm(x, z, weight, *, eps=1e-6, y=None, stream=None):
     axis), with weight [D]; z like x, or None for no gate. A given ``y`` is dense
     and overlaps no input. Returns y."""
     _load()
-    index = _leading(x, "x", 2, 4)[2]
-    handle, stream = _stream(stream, index)
+    lead = _leading(x, "x", 2, 4)
+    handle, stream = _stream(stream, lead[3])
     if y is None:
-        y = _empty(x.shape, x.dtype, x.device, stream)
-    _call("mcc1d_gated_norm", _pack_gated(*_gated_fields(x, z, weight, y, eps)), handle)
+        y = _empty(lead[0], x.dtype, x.device, stream)
+    _call("mcc1d_gated_norm", _pack_gated(*_gated_fields(x, z, weight, y, eps, lead)), handle)
     if stream is not None:
-        _record(stream, index, (x, z, weight), (y,))
+        _record(stream, lead[3], (x, z, weight), (y,))
     return y
 
 
@@ -97,8 +97,9 @@ def gated_norm_backward(grad_y, x, z, weight, *, eps=1e-6, stream=None):
     """Gradients of ``gated_norm`` (same arguments) for grad_y like x. Returns
     ``GatedNormGrads(x, z, weight)``; z is None where the argument was."""
     _load()
-    fwd = _gated_fields(x, z, weight, None, eps)
-    shape, device, index, dt = x.shape, x.device, x.get_device(), x.dtype
+    lead = _leading(x, "x", 2, 4)
+    fwd = _gated_fields(x, z, weight, None, eps, lead)
+    shape, device, index, dt = lead[0], x.device, lead[3], x.dtype
     handle, stream = _stream(stream, index)
     at = _rows(grad_y, "grad_y", shape, dt, index)
     gx = _empty(shape, dt, device, stream)
@@ -121,14 +122,13 @@ def _stream_type(residual, dt):
     return dt, 0
 
 
-def _residual_fields(x, residual, weight, post_weight, scale, y, h, eps):
-    (S, B, H), code, index = _leading(x, "x", 2, 3)
-    dt = x.dtype
-    rt, flag = _stream_type(residual, dt)
-    return (x.data_ptr(), *_steps(x, 3), _rows(residual, "residual", x.shape, rt, index), *_steps(residual, 3),
-            _dense(weight, "weight", (H,), dt, index), _optional(post_weight, "post_weight", (H,), dt, index),
-            _optional(scale, "scale", (H,), _base._torch.float32, index), _optional(y, "y", x.shape, dt, index),
-            _optional(h, "h", x.shape, rt, index), S, B, H, eps, code, flag)
+def _residual_fields(x, residual, weight, post_weight, scale, y, h, eps, lead, rt, flag):
+    shape, (S, B, H), code, index = lead
+    dt, row = x.dtype, (H,)
+    return (x.data_ptr(), *_steps(x, 3), _rows(residual, "residual", shape, rt, index), *_steps(residual, 3),
+            _dense(weight, "weight", row, dt, index), _optional(post_weight, "post_weight", row, dt, index),
+            _optional(scale, "scale", row, _base._torch.float32, index), _optional(y, "y", shape, dt, index),
+            _optional(h, "h", shape, rt, index), S, B, H, eps, code, flag)
 
 
 def residual_norm(x, residual, weight, *, post_weight=None, scale=None, eps=1e-6, y=None, h=None, stream=None):
@@ -139,16 +139,17 @@ def residual_norm(x, residual, weight, *, post_weight=None, scale=None, eps=1e-6
     scale [H] is fp32. Given ``y`` and ``h`` are dense and overlap no input.
     Returns (y, h): what the next block reads, and the residual behind it."""
     _load()
-    index = _leading(x, "x", 2, 3)[2]
-    rt = _stream_type(residual, x.dtype)[0]
-    handle, stream = _stream(stream, index)
+    lead = _leading(x, "x", 2, 3)
+    rt, flag = _stream_type(residual, x.dtype)
+    handle, stream = _stream(stream, lead[3])
     if y is None:
-        y = _empty(x.shape, x.dtype, x.device, stream)
+        y = _empty(lead[0], x.dtype, x.device, stream)
     if h is None:
-        h = _empty(x.shape, rt, x.device, stream)
-    _call("mcc1d_residual_norm", _pack_residual(*_residual_fields(x, residual, weight, post_weight, scale, y, h, eps)), handle)
+        h = _empty(lead[0], rt, x.device, stream)
+    _call("mcc1d_residual_norm", _pack_residual(*_residual_fields(x, residual, weight, post_weight, scale, y, h, eps, lead, rt, flag)),
+          handle)
     if stream is not None:
-        _record(stream, index, (x, residual, weight, post_weight, scale), (y, h))
+        _record(stream, lead[3], (x, residual, weight, post_weight, scale), (y, h))
     return y, h
 
 
@@ -158,8 +159,10 @@ def residual_norm_backward(grad_y, grad_h, x, residual, weight, *, post_weight=N
     ``ResidualNormGrads(x, residual, weight, post_weight, scale)`` with None where
     the argument was None."""
     _load()
-    fwd = _residual_fields(x, residual, weight, post_weight, scale, None, None, eps)
-    shape, device, index, dt, rt = x.shape, x.device, x.get_device(), x.dtype, residual.dtype
+    lead = _leading(x, "x", 2, 3)
+    rt, flag = _stream_type(residual, x.dtype)
+    fwd = _residual_fields(x, residual, weight, post_weight, scale, None, None, eps, lead, rt, flag)
+    shape, device, index, dt = lead[0], x.device, lead[3], x.dtype
     handle, stream = _stream(stream, index)
     at = _rows(grad_y, "grad_y", shape, dt, index), *_steps(grad_y, 3)
     at_h = (0, 0, 0) if grad_h is None else (_rows(grad_h, "grad_h", shape, rt, index), *_steps(grad_h, 3))

@@ -13,7 +13,8 @@ constexpr int64_t kMaxNormRow = 16384;
 
 // Column sums over the rows go through partial sums of each block:
 // [sums][blocks][columns] fp32 in the workspace.
-int64_t norm_bwd_blocks(int64_t rows, int64_t columns, bool vectors);
+constexpr int kGatedThreads = 768, kResidualThreads = 512;      // of a backward, on an SM: what its registers allow
+int64_t norm_bwd_blocks(int64_t rows, int64_t columns, bool vectors, int threads);
 bool gated_norm_vectors(const mcc1d_gated_norm_bwd_args &a);
 bool residual_norm_vectors(const mcc1d_residual_norm_bwd_args &a);
 inline uint64_t norm_bwd_bytes(int64_t blocks, int64_t columns, int sums) { return 4ull * sums * blocks * columns; }

@@ -122,12 +122,12 @@ int32_t check_apart(const mcc1d_residual_norm_bwd_args &a, const void *ws, uint6
 uint64_t bytes_of(const mcc1d_gated_norm_bwd_args &a)
 {
     const int64_t rows = a.fwd.S * a.fwd.B * a.fwd.H;
-    return norm_bwd_bytes(norm_bwd_blocks(rows, a.fwd.D, gated_norm_vectors(a)), a.fwd.D, 1);
+    return norm_bwd_bytes(norm_bwd_blocks(rows, a.fwd.D, gated_norm_vectors(a), kGatedThreads), a.fwd.D, 1);
 }
 
 uint64_t bytes_of(const mcc1d_residual_norm_bwd_args &a)
 {
-    return norm_bwd_bytes(norm_bwd_blocks(a.fwd.S * a.fwd.B, a.fwd.H, residual_norm_vectors(a)), a.fwd.H, 3);
+    return norm_bwd_bytes(norm_bwd_blocks(a.fwd.S * a.fwd.B, a.fwd.H, residual_norm_vectors(a), kResidualThreads), a.fwd.H, 3);
 }
 
 template <class A>

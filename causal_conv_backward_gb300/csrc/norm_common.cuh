@@ -158,7 +158,7 @@ __device__ __forceinline__ void store_values(void *base, int64_t at, int D, cons
 // N sums over the threads of a row, the same for each of them. `turn` flips
 // between calls, so that one barrier a call is enough.
 template <class R, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*shared)[2][3][16], int &turn)
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*shared)[2][3][32], int &turn)
 {
 #pragma unroll
     for (int d = (R::TPR < 32 ? R::TPR : 32) / 2; d > 0; d /= 2)
@@ -224,6 +224,34 @@ int32_t with_row_shape(int64_t D, bool vectors, F &&f)
     if (D <= 2048)
         return f(RowShape<1, 16, 128>());
     return f(RowShape<1, 32, 512>());
+}
+
+// The backwards hold sums and the next row too: half as many values to a thread.
+template <class F>
+int32_t with_row_shape_bwd(int64_t D, bool vectors, F &&f)
+{
+    if (vectors) {
+        if (D <= 64)
+            return f(RowShape<8, 1, 8>());
+        if (D <= 128)
+            return f(RowShape<8, 1, 16>());
+        if (D <= 256)
+            return f(RowShape<8, 1, 32>());
+        if (D <= 1024)
+            return f(RowShape<8, 1, 128>());
+        if (D <= 2048)
+            return f(RowShape<8, 1, 256>());
+        if (D <= 4096)
+            return f(RowShape<8, 1, 512>());
+        return f(RowShape<8, 2, 1024>());
+    }
+    if (D <= 128)
+        return f(RowShape<1, 4, 32>());
+    if (D <= 1024)
+        return f(RowShape<1, 8, 128>());
+    if (D <= 4096)
+        return f(RowShape<1, 8, 512>());
+    return f(RowShape<1, 16, 1024>());
 }
 
 // Whether rows of D values can be read in vectors of eight: addresses (or'd) on

@@ -22,7 +22,7 @@ struct GatedParams {
 template <int DT, class R>
 __global__ void __launch_bounds__(R::THREADS) gated_norm_kernel(const __grid_constant__ GatedParams p)
 {
-    __shared__ float shared[2][3][16];
+    __shared__ float shared[2][3][32];
     int turn = 0;
     const uint32_t row = blockIdx.x * R::ROWS + threadIdx.x / R::TPR;
     const bool there = row < p.rows;
@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(R::THREADS) gated_norm_kernel(const __grid_con
 //   grad_weight = sum of g n over the rows,  grad_z = grad_y n weight silu'(z),
 //   grad_x = r (g weight - n mean(g weight n))
 template <int DT, class R>
-__global__ void __launch_bounds__(R::THREADS) gated_norm_bwd_kernel(const __grid_constant__ GatedParams p)
+__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREADS : 1) gated_norm_bwd_kernel(const __grid_constant__ GatedParams p)
 {
-    __shared__ float shared[2][3][16];
+    __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
     int turn = 0;
     float w[R::E], gw[R::E];
@@ -67,16 +67,24 @@ __global__ void __launch_bounds__(R::THREADS) gated_norm_bwd_kernel(const __grid
 #pragma unroll
     for (int e = 0; e < R::E; ++e)
         gw[e] = 0.f;
-    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += gridDim.x * R::ROWS) {
+    // rows one ahead of their use
+    Share<DT, R> xn, gn, zn;
+    const auto ask = [&](uint32_t first) {
+        const uint32_t row = first + threadIdx.x / R::TPR, at = row < p.rows ? row : p.rows - 1;
+        xn = load_share<DT, R>(p.x, p.order.at(p.xs, at), p.D);
+        gn = load_share<DT, R>(p.grad_y, p.order.at(p.gs, at), p.D);
+        if (p.z)
+            zn = load_share<DT, R>(p.z, p.order.at(p.zs, at), p.D);
+    };
+    const uint32_t step = gridDim.x * R::ROWS;
+    ask(blockIdx.x * R::ROWS);
+    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += step) {
         const uint32_t row = first + threadIdx.x / R::TPR;
         const bool there = row < p.rows;
-        const uint32_t r = there ? row : p.rows - 1;
         float x[R::E], g[R::E];
-        Share<DT, R> zr;
-        const auto xr = load_share<DT, R>(p.x, p.order.at(p.xs, r), p.D);
-        const auto gr = load_share<DT, R>(p.grad_y, p.order.at(p.gs, r), p.D);
-        if (p.z)
-            zr = load_share<DT, R>(p.z, p.order.at(p.zs, r), p.D);
+        const Share<DT, R> xr = xn, gr = gn, zr = zn;
+        if (p.rows - first > step)
+            ask(first + step);
         values<DT, R>(xr, x);
         float s[2] = {0.f, 0.f};
         if (p.z) {
@@ -178,14 +186,14 @@ bool vectors(const mcc1d_gated_norm_args &a, uintptr_t more, int64_t more_steps)
 
 }  // namespace
 
-// Blocks of a backward over this many rows: two waves of the SMs' threads, so
+// Blocks of a backward over this many rows: one wave of `threads` to an SM, so
 // that the partial sums of D columns stay small beside the rows.
-int64_t norm_bwd_blocks(int64_t rows, int64_t columns, bool vec)
+int64_t norm_bwd_blocks(int64_t rows, int64_t columns, bool vec, int threads)
 {
     int64_t blocks = 0;
-    with_row_shape(columns, vec, [&](auto shape) {
+    with_row_shape_bwd(columns, vec, [&](auto shape) {
         typedef decltype(shape) R;
-        blocks = std::min<int64_t>((rows + R::ROWS - 1) / R::ROWS, 152 * (1024 / R::THREADS));
+        blocks = std::min<int64_t>((rows + R::ROWS - 1) / R::ROWS, kNumSMs * std::max(1, threads / R::THREADS));
         return 0;
     });
     return blocks;
@@ -214,8 +222,8 @@ int32_t launch_gated_norm_bwd(const mcc1d_gated_norm_bwd_args &a, float *workspa
     p.grad_y = a.grad_y, p.grad_x = a.grad_x, p.grad_z = a.grad_z, p.part = workspace;
     p.gs = {a.grad_y_strides[0], a.grad_y_strides[1], a.grad_y_strides[2]};
     const bool vec = gated_norm_vectors(a);
-    const int64_t blocks = norm_bwd_blocks(p.rows, a.fwd.D, vec);
-    const int32_t st = with_row_shape(a.fwd.D, vec, [&](auto shape) {
+    const int64_t blocks = norm_bwd_blocks(p.rows, a.fwd.D, vec, kGatedThreads);
+    const int32_t st = with_row_shape_bwd(a.fwd.D, vec, [&](auto shape) {
         typedef decltype(shape) R;
         return a.fwd.dtype == 0 ? launch(gated_norm_bwd_kernel<0, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p)
                                 : launch(gated_norm_bwd_kernel<1, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p);

@@ -9,7 +9,7 @@ namespace {
 template <int DT, int RT, class R>
 __global__ void __launch_bounds__(R::THREADS) residual_norm_kernel(const __grid_constant__ ResidualParams p)
 {
-    __shared__ float shared[2][3][16];
+    __shared__ float shared[2][3][32];
     int turn = 0;
     const uint32_t row = blockIdx.x * R::ROWS + threadIdx.x / R::TPR;
     const bool there = row < p.rows;

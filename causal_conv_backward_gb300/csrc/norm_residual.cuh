@@ -44,17 +44,18 @@ inline bool residual_vectors(const mcc1d_residual_norm_args &a, uintptr_t more, 
 template <int DT, class R>
 struct Branch {
     float r;          // 1 / rms(x), or 1
-    float s[R::E], pw[R::E];
+    Share<2, R> s;
+    Share<DT, R> pw;
 
     __device__ __forceinline__ void weights(const ResidualParams &p)
     {
         if (p.post_weight)
-            load_values<DT, R>(p.post_weight, 0, p.D, pw);
+            pw = load_share<DT, R>(p.post_weight, 0, p.D);
         if (p.scale)
-            load_values<2, R>(p.scale, 0, p.D, s);
+            s = load_share<2, R>(p.scale, 0, p.D);
     }
     // h in place of the residual
-    __device__ __forceinline__ void sum(const ResidualParams &p, const float (&x)[R::E], float (&h)[R::E], float (*shared)[2][3][16], int &turn)
+    __device__ __forceinline__ void sum(const ResidualParams &p, const float (&x)[R::E], float (&h)[R::E], float (*shared)[2][3][32], int &turn)
     {
         r = 1.f;
         if (p.post_weight) {
@@ -65,11 +66,28 @@ struct Branch {
             row_sums<R>(v, shared, turn);
             r = inverse_root(fmaf(v[0], p.inv_D, p.eps));
         }
+        float m[R::E];
+        branch(p, x, m);
+        if (p.scale) {
+            float f[R::E];
+            values<2, R>(s, f);
 #pragma unroll
-        for (int e = 0; e < R::E; ++e) {
-            const float m = p.post_weight ? x[e] * r * pw[e] : x[e];
-            h[e] = p.scale ? fmaf(m, s[e], h[e]) : h[e] + m;
+            for (int e = 0; e < R::E; ++e)
+                h[e] = fmaf(m[e], f[e], h[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                h[e] += m[e];
         }
+    }
+    // m of x, once r is known
+    __device__ __forceinline__ void branch(const ResidualParams &p, const float (&x)[R::E], float (&m)[R::E]) const
+    {
+        if (p.post_weight)
+            values<DT, R>(pw, m);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e)
+            m[e] = p.post_weight ? x[e] * r * m[e] : x[e];
     }
 };
 

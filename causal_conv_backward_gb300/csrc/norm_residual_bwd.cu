@@ -14,33 +14,44 @@ namespace mcc1d {
 namespace {
 
 template <int DT, int RT, class R>
-__global__ void __launch_bounds__(R::THREADS) residual_norm_bwd_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREADS : 1) residual_norm_bwd_kernel(const __grid_constant__ ResidualParams p)
 {
-    __shared__ float shared[2][3][16];
+    __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
     int turn = 0;
-    float w[R::E], gw[R::E], gs[R::E], gp[R::E];
+    float gw[R::E], gs[R::E], gp[R::E];
     Branch<DT, R> b;
     b.weights(p);
-    load_values<DT, R>(p.weight, 0, p.D, w);
+    const auto wr = load_share<DT, R>(p.weight, 0, p.D);
 #pragma unroll
     for (int e = 0; e < R::E; ++e)
         gw[e] = gs[e] = gp[e] = 0.f;
-    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += gridDim.x * R::ROWS) {
+    // rows one ahead of their use
+    Share<DT, R> xn, gn;
+    Share<RT, R> rn, hn;
+    const auto ask = [&](uint32_t first) {
+        const uint32_t row = first + threadIdx.x / R::TPR, at = row < p.rows ? row : p.rows - 1;
+        xn = load_share<DT, R>(p.x, p.order.at(p.xs, at), p.D);
+        rn = load_share<RT, R>(p.residual, p.order.at(p.rs, at), p.D);
+        gn = load_share<DT, R>(p.grad_y, p.order.at(p.gs, at), p.D);
+        if (p.grad_h)
+            hn = load_share<RT, R>(p.grad_h, p.order.at(p.ghs, at), p.D);
+    };
+    const uint32_t step = gridDim.x * R::ROWS;
+    ask(blockIdx.x * R::ROWS);
+    for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += step) {
         const uint32_t row = first + threadIdx.x / R::TPR;
         const bool there = row < p.rows;
-        const uint32_t at = there ? row : p.rows - 1;
-        float x[R::E], h[R::E], g[R::E];
-        const auto xr = load_share<DT, R>(p.x, p.order.at(p.xs, at), p.D);
-        const auto rr = load_share<RT, R>(p.residual, p.order.at(p.rs, at), p.D);
-        const auto gr = load_share<DT, R>(p.grad_y, p.order.at(p.gs, at), p.D);
-        Share<RT, R> hr;
-        if (p.grad_h)
-            hr = load_share<RT, R>(p.grad_h, p.order.at(p.ghs, at), p.D);
+        float x[R::E], h[R::E], g[R::E], w[R::E];
+        const Share<DT, R> xr = xn, gr = gn;
+        const Share<RT, R> rr = rn, hr = hn;
+        if (p.rows - first > step)
+            ask(first + step);
         values<DT, R>(xr, x);
         values<RT, R>(rr, h);
         b.sum(p, x, h, &shared, turn);
         values<DT, R>(gr, g);
+        values<DT, R>(wr, w);
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
@@ -67,22 +78,25 @@ __global__ void __launch_bounds__(R::THREADS) residual_norm_bwd_kernel(const __g
         if (there)
             store_values<RT, R>(p.grad_residual, (int64_t)row * p.D, p.D, g);
         if (p.scale) {
+            float m[R::E], f[R::E];
+            b.branch(p, x, m);
+            values<2, R>(b.s, f);
 #pragma unroll
             for (int e = 0; e < R::E; ++e) {
-                const float m = p.post_weight ? x[e] * b.r * b.pw[e] : x[e];
                 if (there)
-                    gs[e] = fmaf(g[e], m, gs[e]);
-                g[e] *= b.s[e];
+                    gs[e] = fmaf(g[e], m[e], gs[e]);
+                g[e] *= f[e];
             }
         }
         if (p.post_weight) {
-            float t[1] = {0.f};
+            float t[1] = {0.f}, pw[R::E];
+            values<DT, R>(b.pw, pw);
 #pragma unroll
             for (int e = 0; e < R::E; ++e) {
                 x[e] *= b.r;
                 if (there)
                     gp[e] = fmaf(g[e], x[e], gp[e]);
-                g[e] *= b.pw[e];
+                g[e] *= pw[e];
                 t[0] = fmaf(g[e], x[e], t[0]);
             }
             row_sums<R>(t, &shared, turn);
@@ -117,11 +131,11 @@ int32_t launch_residual_norm_bwd(const mcc1d_residual_norm_bwd_args &a, float *w
     p.gs = {0, a.grad_y_strides[0], a.grad_y_strides[1]};
     p.ghs = {0, a.grad_h_strides[0], a.grad_h_strides[1]};
     const bool vec = residual_norm_vectors(a);
-    const int64_t blocks = norm_bwd_blocks(p.rows, f.H, vec);
+    const int64_t blocks = norm_bwd_blocks(p.rows, f.H, vec, kResidualThreads);
     p.part = workspace;
     p.part_post = a.grad_post_weight ? workspace + blocks * f.H : nullptr;
     p.part_scale = a.grad_scale ? workspace + 2 * blocks * f.H : nullptr;
-    const int32_t st = with_row_shape(f.H, vec, [&](auto shape) {
+    const int32_t st = with_row_shape_bwd(f.H, vec, [&](auto shape) {
         typedef decltype(shape) R;
         const auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)blocks), R::THREADS, 0, stream, p); };
         if (f.flags & MCC1D_WIDE)
