@@ -39,6 +39,7 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
 // T and P T as fp16 terms in the panels that the tensor cores read, the factors
 // of its tokens, and in the row kFactorEnd what is one value (delta_prepare.cu).
 constexpr int kPanelBytes = kChunk * 128;
+enum { kPanelT, kPanelPT, kPanelTLo, kPanelPTLo };            // T and P T meet the same rows
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
        kFactorT, kFactors };
 // In that row: the chunk's decay; what bounds a row's R (of its v and state), U

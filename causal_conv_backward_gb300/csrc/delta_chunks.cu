@@ -1,7 +1,7 @@
 // delta_chunks.cu - the gated delta rule over prompts, a chunk of 64 tokens at
 // a time, on the tensor cores.
 //
-// A block has one head's state [V,K], up to 128 rows of it, a row to two
+// A block has one head's state [V,K], up to 128 rows of it, a row to four
 // threads that share its columns: everything that goes along a row (decays,
 // sums, scales, rounding to two fp16 terms) stays in them, and the state itself
 // in their registers, in fp32. With the factors of delta_prepare.cu, a chunk is
@@ -14,10 +14,10 @@
 // with T and P T three. Sums are fp32.
 //
 // The chunks of one head follow on one another, X - R - U - S, and bound the
-// kernel: the products' latency and the conversions between them, for which a
-// scheduler has two warps of rows. Y is taken in the gaps and leaves through
-// warps of its own. Warps 0 to 7 hold the rows, 8 to 11 write Y, 12 issues the
-// products, 13 copies the tokens of the chunk after the next, 14 to 19 make
+// kernel: the products' time and the conversions between them, for which a
+// scheduler has four warps of rows. Y is taken in the gaps and leaves through
+// warps of its own. Warps 0 to 15 hold the rows, 16 to 19 write Y, 20 issues the
+// products, 21 copies the tokens of the chunk after the next, 22 to 27 make
 // panels of the next one's.
 #include <utility>
 
@@ -27,7 +27,7 @@ namespace mcc1d {
 
 namespace {
 
-constexpr int kStages = 2;
+constexpr int kTiles = 3, kPrepareds = 2;      // chunks whose tokens, and whose prepared panels, are there or on their way
 // Registers by warpgroup: rows (four), Y, and two for the rest.
 constexpr int kRegRows = 80, kRegY = 64, kRegRest = 56, kRegLaunch = 72;
 static_assert(kParts * kRegRows + kRegY + 2 * kRegRest <= kThreads / 128 * kRegLaunch, "what the block is launched with");
@@ -43,67 +43,64 @@ struct ChunkParams {
     Segments seg;
 };
 
+// Tokens: 64 keys of K's rows, then of Q's, then the next 64 keys; V as it is, 64
+// values of its rows, then the next 64.
 template <int KP>
-struct Stage {
+struct Tile {
     static constexpr int kPanels = KP / 64 * kPanelBytes;
-    static constexpr int K = 0, Q = kPanels, kPrepared = 2 * kPanels;
-    static constexpr int V = kPrepared + (kChunkBytes + 1023) / 1024 * 1024;      // [token pair][row] of two values
-    static constexpr int kBytes = V + kC * kRows * 2;
-    static_assert(kBytes % 1024 == 0, "panels on 1024 bytes");
+    static constexpr int K = 0, Q = kPanelBytes, V = 2 * kPanels, kBytes = V + kRows / 64 * kPanelBytes;
+    static constexpr int kAll = kTiles * kBytes;
 };
+constexpr int kPreparedBytes = (kChunkBytes + 1023) / 1024 * 1024;
 
-// Columns of tensor memory: sums, then operands (pairs of fp16).
-enum { kX = 0, kU = 64, kQS = 128, kPR = 192, kSHi = 256, kSLo = 320, kRHi = 384, kRLo = 416, kUHi = 448, kULo = 480, kColumns = 512 };
+// Columns of tensor memory: sums, then operands (pairs of fp16). The state's
+// update is summed over X and U.
+enum { kUpdate = 0, kX = 0, kU = 64, kQS = 128, kPR = 192, kSHi = 256, kSLo = 320, kWHi = 384, kWLo = 416, kVHi = 448, kVLo = 480, kColumns = 512 };
 
 struct ChunkShared {
-    uint64_t full[kStages], empty[kStages], factors[kStages], rows, rows_free, x, r, u, v, y, s, end, out;
+    uint64_t tiles[kTiles], full[kTiles], tile_free[kTiles], prepared[kPrepareds], prepared_free[kPrepareds], x, r, u, v, y, s, end, out;
     float of_s[2][kRows], of_r[2][kRows];       // of the last two chunks: what rows' terms are multiplied by
     float of_y[4][2 * kC];                      // the factors of Y of the last four chunks
     float most[kParts][kRows], most_v[kParts][kRows], sum_u[kParts][kRows];      // of the parts of a row
     uint32_t tmem, failed;
 };
 
-// A chunk's rows of q or k as scaled fp16 in panels. A thread has one piece of
-// every STEPth row.
+// A chunk's rows of q or k made scaled fp16 where they lie in their panels (or
+// come from global memory). A thread has one piece of every STEPth row.
 template <int DT, int KP>
-__device__ __forceinline__ void make_panels(uint8_t *panels, const uint8_t *copied, const uint16_t *from, int64_t step, const float *scales, int K, bool vectors,
-                                            int n, int thread)
+__device__ __forceinline__ void make_panels(uint8_t *panels, const uint16_t *from, int64_t step, const float *scales, int K, bool vectors, int n, int thread)
 {
     constexpr int PIECES = KP / 8, STEP = kLoadThreads / PIECES;
     static_assert(kLoadThreads % PIECES == 0, "whole rows");
     const int piece = thread % PIECES, live = K - 8 * piece;
-    panels += (piece / 8) * kPanelBytes;
+    panels += (piece / 8) * 2 * kPanelBytes;
 #pragma unroll 2
     for (int t = thread / PIECES; t < kC; t += STEP) {
-        const uint4 v = piece_of(copied + (piece / 8) * kPanelBytes + t * 128 + 16 * (piece % 8), from + t * step + 8 * piece, vectors, t < n ? live : 0);
+        uint8_t *at = panels + panel_at(t, piece % 8);
+        const uint4 v = piece_of(at, from + t * step + 8 * piece, vectors, t < n ? live : 0);
         const float2 f = make_float2(scales[t], scales[t]);
-        *reinterpret_cast<uint4 *>(panels + panel_at(t, piece % 8)) =
-            make_uint4(pack_half2(mul2(unpack2<DT>(v.x), f)), pack_half2(mul2(unpack2<DT>(v.y), f)), pack_half2(mul2(unpack2<DT>(v.z), f)),
-                       pack_half2(mul2(unpack2<DT>(v.w), f)));
+        *reinterpret_cast<uint4 *>(at) = make_uint4(pack_half2(mul2(unpack2<DT>(v.x), f)), pack_half2(mul2(unpack2<DT>(v.y), f)),
+                                                    pack_half2(mul2(unpack2<DT>(v.z), f)), pack_half2(mul2(unpack2<DT>(v.w), f)));
     }
 }
 
-// A chunk's rows of v as pairs of tokens.
-__device__ __forceinline__ void pair_values(uint8_t *pairs, const uint8_t *copied, const uint16_t *from, int64_t step, int V, bool vectors, int n, int thread)
+// A chunk's rows of v where they were not copied, and zeros behind their end.
+__device__ __forceinline__ void fill_values(uint8_t *values, const uint16_t *from, int64_t step, int V, bool vectors, int n, int thread)
 {
     constexpr int PIECES = kRows / 8;
     const int piece = thread % PIECES, live = V - 8 * piece;
-#pragma unroll 2
-    for (int t = 2 * (thread / PIECES); t < kC; t += 2 * (kLoadThreads / PIECES)) {
-        const uint8_t *at = copied + (piece / 8) * kPanelBytes + t * 128 + 16 * (piece % 8);
-        const uint4 x = piece_of(at, from + t * step + 8 * piece, vectors, t < n ? live : 0);
-        const uint4 y = piece_of(at + 128, from + (t + 1) * step + 8 * piece, vectors, t + 1 < n ? live : 0);
-        uint4 *to = reinterpret_cast<uint4 *>(pairs + t / 2 * kRows * 4 + 32 * piece);
-        to[0] = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
-        to[1] = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410), __byte_perm(x.w, y.w, 0x7632));
-    }
+#pragma unroll 1
+    for (int t = thread / PIECES + (vectors && live > 0 ? n / (kLoadThreads / PIECES) * (kLoadThreads / PIECES) : 0); t < kC; t += kLoadThreads / PIECES)
+        if (!vectors || t >= n || live <= 0)
+            *reinterpret_cast<uint4 *>(values + (piece / 8) * kPanelBytes + t * 128 + 16 * (piece % 8)) =
+                piece_of(nullptr, from + t * step + 8 * piece, false, t < n && !vectors ? live : 0);
 }
 
 // ------------------------------------------------------------------ the rows
 template <int DT, int KP>
-__device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh, const uint8_t *stages, const Part &pt, int64_t n)
+__device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh, const uint8_t *tiles, const Part &pt, int64_t n)
 {
-    typedef Stage<KP> St;
+    typedef Tile<KP> Tl;
     constexpr int HK = KP / kParts, HC = kC / kParts, UNIT = HK < 32 ? HK : 32;
     const DeltaParams &p = cp.d;
     const int warp = threadIdx.x / 32, r = threadIdx.x % kRows, part = warp / 4, row = pt.v0 + r;
@@ -129,7 +126,7 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
 #pragma unroll
     for (int k = 0; k < HK; ++k)
         s[k] *= scale_s;
-    const uint32_t terms_s = lanes + kSHi + HK / 2 * part, terms_r = lanes + kRHi + HC / 2 * part, terms_u = lanes + kUHi + HC / 2 * part;
+    const uint32_t terms_s = lanes + kSHi + HK / 2 * part, terms_w = lanes + kWHi + HC / 2 * part, terms_v = lanes + kVHi + HC / 2 * part;
     if (chunks > 0) {
         sh.of_s[0][r] = inverse_scale(scale_s);
 #pragma unroll
@@ -156,16 +153,18 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
             write_row<HK>(pt.to + (int64_t)row * p.K, part * HK, p.K, cp.vectors_s, s, inverse_scale(scale_s));
         if (i >= chunks)
             break;
-        const uint8_t *stage = stages + (i % kStages) * St::kBytes;
-        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
-        const uint32_t *v = reinterpret_cast<const uint32_t *>(stage + St::V) + part * (HC / 2) * kRows + r;
+        const uint8_t *prepared = tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes;
+        const float *f = reinterpret_cast<const float *>(prepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(tiles + (i % kTiles) * Tl::kBytes + Tl::V + (r / 64) * kPanelBytes) + part * HC * 64 + r % 64;
         f += part * HC;
         // the products wait for the chunk's tiles too, but this thread reads some itself
-        ok = warp_wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1);
+        ok = warp_wait(sh.full[i % kTiles], (uint32_t)(i / kTiles) & 1);
         float most_v = 0.f;
+        uint32_t pairs[HC / 2];      // of tokens
 #pragma unroll
-        for (int t = 0; t < HC / 2; ++t) {
-            const float2 x = unpack2<DT>(v[t * kRows]);
+        for (int t = 0; t < HC; t += 2) {
+            pairs[t / 2] = v[t * 64] | (uint32_t)v[(t + 1) * 64] << 16;
+            const float2 x = unpack2<DT>(pairs[t / 2]);
             most_v = fmaxf(most_v, fmaxf(fabsf(x.x), fabsf(x.y)));
         }
         sh.most[part][r] = most_of(s);
@@ -195,10 +194,10 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
             for (int t = 0; t < 16; t += 2) {
                 const float2 bt = *reinterpret_cast<const float2 *>(f + kFactorB * kC + t0 + t), ft = *reinterpret_cast<const float2 *>(f + kFactorX * kC + t0 + t);
                 const float2 a = fma2(mul2(ft, mx), make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])),
-                                      mul2(mul2(bt, mv), unpack2<DT>(v[(t0 + t) / 2 * kRows])));
+                                      mul2(mul2(bt, mv), unpack2<DT>(pairs[(t0 + t) / 2])));
                 x[t] = a.x, x[t + 1] = a.y;
             }
-            put_terms<16>(x, terms_r + t0 / 2, terms_r + (kRLo - kRHi) + t0 / 2);
+            put_terms<16>(x, terms_w + t0 / 2, terms_w + (kWLo - kWHi) + t0 / 2);
         }
         terms_done(sh.r);
         ok = ok && warp_wait(sh.u, parity);
@@ -226,11 +225,12 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
                 sum_u = add2(sum_u, make_float2(fabsf(a.x), fabsf(a.y)));
                 x[t] = a.x, x[t + 1] = a.y;
             }
-            put_terms<16>(x, terms_u + t0 / 2, terms_u + (kULo - kUHi) + t0 / 2);
+            put_terms<16>(x, terms_v + t0 / 2, terms_v + (kVLo - kVHi) + t0 / 2);
         }
         sh.sum_u[part][r] = sum_u.x + sum_u.y;
         terms_done(sh.v);
-        warp_arrive(sh.empty[i % kStages]);
+        warp_arrive(sh.tile_free[i % kTiles]);
+        warp_arrive(sh.prepared_free[i % kPrepareds]);
         rows_meet();     // for sum_u, while the products run
         // |S| <= e^c(end) |S| + sum of |U k|, and no |k| is above 2^16 as an operand
         const float before = scale_s;
@@ -246,7 +246,7 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
 #pragma unroll
         for (int c = 0; c < HK; c += UNIT) {
             uint32_t raw[UNIT];
-            tmem_load(lanes + kX + HK * part + c, raw);
+            tmem_load(lanes + kUpdate + HK * part + c, raw);
             tmem_wait(raw);
 #pragma unroll
             for (int k = 0; k < UNIT; k += 2) {
@@ -285,11 +285,14 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
         const bool whole = cp.pairs_y && rows == kC && live == kC;
 #pragma unroll 1
         for (int t0 = 0; t0 < kC; t0 += 16) {
-            uint32_t a[16], c[16];
+            uint32_t a[16], c[16], y[8];
             tmem_load(lanes + kQS + t0, a);
             tmem_load(lanes + kPR + t0, c);
             tmem_wait(a), tmem_wait(c);
-            uint32_t y[8];
+            if (t0 == kC - 16) {
+                tmem_fence_before();
+                warp_arrive(sh.out);
+            }
 #pragma unroll
             for (int t = 0; t < 16; t += 2) {
                 const float2 q = *reinterpret_cast<const float2 *>(fq + t0 + t), pr = *reinterpret_cast<const float2 *>(fp + t0 + t);
@@ -312,8 +315,6 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
             }
         }
         to += kC * step;
-        tmem_fence_before();
-        warp_arrive(sh.out);
     }
     if (mine)          // tokens behind the sequence; NaN where a wait gave up
         for (int64_t t = (pt.first + i) * kC, end = pt.last ? p.S : (pt.first + chunks) * kC; t < end; ++t, to += step)
@@ -323,15 +324,16 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
 // ------------------------------------------------------------------ products
 // One thread's. `y`: those of Y too.
 template <int KP>
-__device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t stages, int64_t chunks, bool y)
+__device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, int64_t chunks, bool y)
 {
-    typedef Stage<KP> St;
+    typedef Tile<KP> Tl;
     constexpr uint32_t by_rows = mma_kind(kC, false), by_columns = mma_kind(KP, true);
     const uint32_t tmem = sh.tmem;
+    const auto wait = [](uint64_t &bar, uint32_t parity) { return mbar_wait_bounded_inline(smem_u32(&bar), parity); };
     const auto with_state = [&](uint32_t d, uint32_t panels) {
 #pragma unroll
         for (int j = 0; j < KP / 16; ++j) {
-            const uint64_t k = desc_rows(panels + (j / 4) * kPanelBytes) + 2 * (j % 4);
+            const uint64_t k = desc_rows(panels + (j / 4) * 2 * kPanelBytes) + 2 * (j % 4);
             mma_ts(tmem + d, tmem + kSHi + 8 * j, k, by_rows, j > 0);
             mma_ts(tmem + d, tmem + kSLo + 8 * j, k, by_rows, true);
         }
@@ -339,31 +341,33 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t stages,
     const auto with_r = [&](uint32_t d, uint32_t panels) {
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t hi = desc_rows(panels) + 2 * j, lo = desc_rows(panels + kPanelBytes) + 2 * j;
-            mma_ts(tmem + d, tmem + kRHi + 8 * j, hi, by_rows, j > 0);
-            mma_ts(tmem + d, tmem + kRHi + 8 * j, lo, by_rows, true);
-            mma_ts(tmem + d, tmem + kRLo + 8 * j, hi, by_rows, true);
+            const uint64_t hi = desc_rows(panels) + 2 * j, lo = desc_rows(panels + (kPanelTLo - kPanelT) * kPanelBytes) + 2 * j;
+            mma_ts(tmem + d, tmem + kWHi + 8 * j, hi, by_rows, j > 0);
+            mma_ts(tmem + d, tmem + kWHi + 8 * j, lo, by_rows, true);
+            mma_ts(tmem + d, tmem + kWLo + 8 * j, hi, by_rows, true);
         }
     };
-    const auto wait = [](uint64_t &bar, uint32_t parity) { return mbar_wait_bounded_inline(smem_u32(&bar), parity); };
     for (int64_t i = 0; i < chunks; ++i) {
-        const uint32_t parity = (uint32_t)(i & 1), stage = stages + (uint32_t)(i % kStages) * St::kBytes;
-        if (!wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1) || !wait(sh.s, parity))
+        const uint32_t parity = (uint32_t)(i & 1), tile = tiles + (uint32_t)(i % kTiles) * Tl::kBytes;
+        const uint32_t prepared = tiles + Tl::kAll + (uint32_t)(i % kPrepareds) * kPreparedBytes;
+        if (!wait(sh.full[i % kTiles], (uint32_t)(i / kTiles) & 1) || !wait(sh.s, parity))
             break;
         tmem_fence_after();
-        with_state(kX, stage + St::K);
+        with_state(kX, tile + Tl::K);
         mma_commit(smem_u32(&sh.x));
-        if (!wait(sh.r, parity))
-            break;
-        tmem_fence_after();
-        with_r(kU, stage + St::kPrepared);
-        mma_commit(smem_u32(&sh.u));
-        if (y) {
+        if (y) {                   // while X becomes R, and U an operand
             if (!wait(sh.out, parity ^ 1))         // the Y before this one has been read
                 break;
             tmem_fence_after();
-            with_state(kQS, stage + St::Q);
-            with_r(kPR, stage + St::kPrepared + 2 * kPanelBytes);
+            with_state(kQS, tile + Tl::Q);
+        }
+        if (!wait(sh.r, parity))
+            break;
+        tmem_fence_after();
+        with_r(kU, prepared + kPanelT * kPanelBytes);
+        mma_commit(smem_u32(&sh.u));
+        if (y) {
+            with_r(kPR, prepared + kPanelPT * kPanelBytes);
             mma_commit(smem_u32(&sh.y));
         }
         if (!wait(sh.v, parity))
@@ -371,85 +375,87 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t stages,
         tmem_fence_after();
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t k = desc_columns(stage + St::K, kPanelBytes) + (uint64_t)(2048 * j >> 4);
-            mma_ts(tmem + kX, tmem + kUHi + 8 * j, k, by_columns, j > 0);
-            mma_ts(tmem + kX, tmem + kULo + 8 * j, k, by_columns, true);
+            const uint64_t k = desc_columns(tile + Tl::K, 2 * kPanelBytes) + (uint64_t)(2048 * j >> 4);
+            mma_ts(tmem + kUpdate, tmem + kVHi + 8 * j, k, by_columns, j > 0);
+            mma_ts(tmem + kUpdate, tmem + kVLo + 8 * j, k, by_columns, true);
         }
         mma_commit(smem_u32(&sh.end));
-        mma_commit(smem_u32(&sh.empty[i % kStages]));
+        mma_commit(smem_u32(&sh.tile_free[i % kTiles]));
+        mma_commit(smem_u32(&sh.prepared_free[i % kPrepareds]));
     }
 }
 
 // ------------------------------------------------------------------ tiles
-// One warp: a chunk's rows as tiles of 64 tokens and 64 values, and its prepared
-// panels and factors.
+// One warp: a chunk's rows as tiles of 64 tokens and 64 values, up to three chunks
+// ahead, and its prepared panels and factors.
 template <int KP>
-__device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, const Part &pt)
+__device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *tiles, const Part &pt)
 {
-    typedef Stage<KP> St;
+    typedef Tile<KP> Tl;
     const DeltaParams &p = cp.d;
-    const int lane = threadIdx.x % 32, b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
+    const int b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
     const int64_t chunks = pt.chunks;
-    const uint32_t copied = smem_u32(stages) + kStages * St::kBytes, bar = smem_u32(&sh.rows);
     const bool k = cp.vectors_k, q = cp.vectors_q && p.y, v = cp.vectors_v && !pt.unit;
+    int64_t next = 0;          // whose tokens are to be asked for
     for (int64_t i = 0; i < chunks; ++i) {
-        if (!warp_wait(sh.rows_free, (uint32_t)(i + 1) & 1))
-            break;
-        if (lane == 0) {
-            const int t0 = (int)((pt.first + i) * kC);
-            const int values = p.V - v0 > 64 ? 2 : 1;
-            mbar_arrive_expect_tx(bar, ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (v ? values : 0)) * kPanelBytes);
-            for (int j = 0; j < KP / 64; ++j) {
-                if (k)
-                    tile_g2s(copied + j * kPanelBytes, &cp.map_k, 64 * j, t0, g, b, bar);
-                if (q)
-                    tile_g2s(copied + St::kPanels + j * kPanelBytes, &cp.map_q, 64 * j, t0, g, b, bar);
+        for (; next < chunks && next < i + kTiles; ++next) {
+            if (next > i && !__all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&sh.tile_free[next % kTiles]), (uint32_t)(next / kTiles + 1) & 1)))
+                break;         // not free yet, and not what is waited for
+            if (!warp_wait(sh.tile_free[next % kTiles], (uint32_t)(next / kTiles + 1) & 1))
+                return;
+            if (threadIdx.x % 32 == 0) {
+                const uint32_t tile = smem_u32(tiles) + (uint32_t)(next % kTiles) * Tl::kBytes, bar = smem_u32(&sh.tiles[next % kTiles]);
+                const int t0 = (int)((pt.first + next) * kC), values = p.V - v0 > 64 ? 2 : 1;
+                mbar_arrive_expect_tx(bar, ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (v ? values : 0)) * kPanelBytes);
+                for (int j = 0; j < KP / 64; ++j) {
+                    if (k)
+                        tile_g2s(tile + Tl::K + 2 * j * kPanelBytes, &cp.map_k, 64 * j, t0, g, b, bar);
+                    if (q)
+                        tile_g2s(tile + Tl::Q + 2 * j * kPanelBytes, &cp.map_q, 64 * j, t0, g, b, bar);
+                }
+                for (int j = 0; v && j < values; ++j)
+                    tile_g2s(tile + Tl::V + j * kPanelBytes, &cp.map_v, v0 + 64 * j, t0, h, b, bar);
             }
-            for (int j = 0; v && j < values; ++j)
-                tile_g2s(copied + 2 * St::kPanels + j * kPanelBytes, &cp.map_v, v0 + 64 * j, t0, h, b, bar);
+            __syncwarp();
         }
-        __syncwarp();
-        if (!warp_wait(sh.empty[i % kStages], (uint32_t)(i / kStages + 1) & 1))
-            break;
-        if (lane == 0) {
-            const uint32_t ready = smem_u32(&sh.factors[i % kStages]);
+        if (!warp_wait(sh.prepared_free[i % kPrepareds], (uint32_t)(i / kPrepareds + 1) & 1))
+            return;
+        if (threadIdx.x % 32 == 0) {
+            const uint32_t ready = smem_u32(&sh.prepared[i % kPrepareds]);
             mbar_arrive_expect_tx(ready, kChunkBytes);
-            bulk_g2s(smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes + St::kPrepared, cp.prepared + (pt.item * cp.chunks + pt.first + i) * kChunkBytes, kChunkBytes,
-                     ready);
+            bulk_g2s(smem_u32(tiles) + Tl::kAll + (uint32_t)(i % kPrepareds) * kPreparedBytes, cp.prepared + (pt.item * cp.chunks + pt.first + i) * kChunkBytes,
+                     kChunkBytes, ready);
         }
         __syncwarp();
     }
 }
 
-// The other loading warps: rows to panels and pairs.
+// The other loading warps: rows to operands.
 template <int DT, int KP>
-__device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *stages, const Part &pt, int64_t n)
+__device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &sh, uint8_t *tiles, const Part &pt, int64_t n)
 {
-    typedef Stage<KP> St;
+    typedef Tile<KP> Tl;
     const DeltaParams &p = cp.d;
     const int thread = threadIdx.x - (kThreads - kLoadThreads), b = pt.item / p.H, h = pt.item % p.H, g = h / (p.H / p.G), v0 = pt.v0;
     const int64_t chunks = pt.chunks;
-    const uint8_t *copied = stages + kStages * St::kBytes;
     for (int64_t i = 0; i < chunks; ++i) {
         const int64_t t0 = (pt.first + i) * kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC);
-        uint8_t *stage = stages + (i % kStages) * St::kBytes;
-        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
-        if (!warp_wait(sh.rows, (uint32_t)(i & 1)) || !warp_wait(sh.factors[i % kStages], (uint32_t)(i / kStages) & 1))
+        uint8_t *tile = tiles + (i % kTiles) * Tl::kBytes;
+        const float *f = reinterpret_cast<const float *>(tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes + 4 * kPanelBytes);
+        if (!warp_wait(sh.tiles[i % kTiles], (uint32_t)(i / kTiles) & 1) || !warp_wait(sh.prepared[i % kPrepareds], (uint32_t)(i / kPrepareds) & 1))
             break;
-        make_panels<DT, KP>(stage + St::K, copied, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k,
-                            live, thread);
-        pair_values(stage + St::V, copied + 2 * St::kPanels, p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], pt.unit ? 0 : p.V - v0,
-                    cp.vectors_v, live, thread);
+        make_panels<DT, KP>(tile + Tl::K, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k, live, thread);
         if (p.y) {
-            make_panels<DT, KP>(stage + St::Q, copied + St::kPanels, p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2], p.q_s[0], f + kFactorScaleQ * kC, p.K,
-                                cp.vectors_q, live, thread);
+            make_panels<DT, KP>(tile + Tl::Q, p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2], p.q_s[0], f + kFactorScaleQ * kC, p.K, cp.vectors_q, live,
+                                thread);
             if (thread < 2 * kC)
                 sh.of_y[i & 3][thread] = f[kFactorQ * kC + thread];
         }
+        if (live < kC || !cp.vectors_v || pt.unit || p.V - v0 < kRows)
+            fill_values(tile + Tl::V, p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], pt.unit ? 0 : p.V - v0, cp.vectors_v, live, thread);
         shared_to_async();
-        warp_arrive(sh.rows_free);
-        warp_arrive(sh.full[i % kStages]);
+        warp_arrive(sh.full[i % kTiles]);
     }
 }
 
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
 {
     extern __shared__ uint8_t raw_shared[];
     __shared__ ChunkShared sh;
-    uint8_t *stages = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
+    uint8_t *tiles = raw_shared + (1024 - smem_u32(raw_shared) % 1024) % 1024;
     const DeltaParams &p = cp.d;
     const int tid = threadIdx.x, warp = tid / 32, group = warp / 4;
     int64_t n;
@@ -468,12 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
 
     if (tid == 0) {
         sh.failed = 0;
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), kLoadWarps);
-            mbar_init(smem_u32(&sh.empty[i]), kRowWarps + 1);
-            mbar_init(smem_u32(&sh.factors[i]), 1);
-        }
-        mbar_init(smem_u32(&sh.rows), 1), mbar_init(smem_u32(&sh.rows_free), kLoadWarps);
+        for (int i = 0; i < kTiles; ++i)
+            mbar_init(smem_u32(&sh.tiles[i]), 1), mbar_init(smem_u32(&sh.full[i]), kLoadWarps), mbar_init(smem_u32(&sh.tile_free[i]), kRowWarps + 1);
+        for (int i = 0; i < kPrepareds; ++i)
+            mbar_init(smem_u32(&sh.prepared[i]), 1), mbar_init(smem_u32(&sh.prepared_free[i]), kRowWarps + 1);
         mbar_init(smem_u32(&sh.x), 1), mbar_init(smem_u32(&sh.u), 1), mbar_init(smem_u32(&sh.y), 1), mbar_init(smem_u32(&sh.end), 1);
         mbar_init(smem_u32(&sh.r), kRowWarps), mbar_init(smem_u32(&sh.v), kRowWarps), mbar_init(smem_u32(&sh.s), kRowWarps), mbar_init(smem_u32(&sh.out), 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
 
     if (group < kParts) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegRows));
-        hold_rows<DT, KP>(cp, sh, stages, pt, n);
+        hold_rows<DT, KP>(cp, sh, tiles, pt, n);
     } else if (group == kParts) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegY));
         if (p.y)
@@ -494,11 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
         if (warp > kCopyWarp)
-            make_tiles<DT, KP>(cp, sh, stages, pt, n);
+            make_tiles<DT, KP>(cp, sh, tiles, pt, n);
         else if (warp == kCopyWarp)
-            copy_tiles<KP>(cp, sh, stages, pt);
+            copy_tiles<KP>(cp, sh, tiles, pt);
         else if (tid % 32 == 0)
-            issue_products<KP>(sh, smem_u32(stages), pt.chunks, p.y != nullptr);
+            issue_products<KP>(sh, smem_u32(tiles), pt.chunks, p.y != nullptr);
     }
     tmem_fence_before();
     __syncthreads();
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const __grid_
 template <int DT, int KP>
 int32_t chunks_of(const ChunkParams &p, cudaStream_t stream)
 {
-    constexpr int bytes = kStages * Stage<KP>::kBytes + kC * (2 * KP + kRows) * 2 + 1024;
+    constexpr int bytes = Tile<KP>::kAll + kPrepareds * kPreparedBytes + 1024;
     // the rows' registers come out of what the block starts with: an increase
     // past that would wait for ever
     static const bool fits = [] {
@@ -576,8 +580,8 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, ui
     p.prepared = workspace + plan.off_prepared;
     p.chunks = plan.chunks;
     p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
-    p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides, false);
-    p.vectors_k = token_tiles(&p.map_k, a.k, a.S, a.B, a.G, a.K, a.k_strides, false);
+    p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides, true);
+    p.vectors_k = token_tiles(&p.map_k, a.k, a.S, a.B, a.G, a.K, a.k_strides, true);
     p.vectors_v = token_tiles(&p.map_v, a.v, a.S, a.B, a.H, a.V, a.v_strides, false);
     p.pairs_y = a.V % 2 == 0 && ((uintptr_t)a.y & 3u) == 0;
     p.vectors_s = a.K % 4 == 0 && ((uintptr_t)a.final_state & 15u) == 0;

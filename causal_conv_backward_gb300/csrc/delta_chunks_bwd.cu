@@ -291,16 +291,16 @@ __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, 
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
             const uint64_t step = (uint64_t)(2048 * j >> 4), y = desc_columns(stage + St::Y, kPanelBytes) + step;
-            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + 2 * kPanelBytes, kPanelBytes) + step, y_tokens, j > 0);
-            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + 3 * kPanelBytes, kPanelBytes) + step, y_tokens, true);
+            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + kPanelPT * kPanelBytes, kPanelBytes) + step, y_tokens, j > 0);
+            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + kPanelPTLo * kPanelBytes, kPanelBytes) + step, y_tokens, true);
         }
         if (!wait(sh.r, parity))
             break;
         tmem_fence_after();
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t step = (uint64_t)(2048 * j >> 4), hi = desc_columns(stage + St::kPrepared, kPanelBytes) + step;
-            const uint64_t lo = desc_columns(stage + St::kPrepared + kPanelBytes, kPanelBytes) + step;
+            const uint64_t step = (uint64_t)(2048 * j >> 4), hi = desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step;
+            const uint64_t lo = desc_columns(stage + St::kPrepared + kPanelTLo * kPanelBytes, kPanelBytes) + step;
             mma_ts(tmem + kU, tmem + kWHi + 8 * j, hi, tokens_by_columns, j > 0);
             mma_ts(tmem + kU, tmem + kWHi + 8 * j, lo, tokens_by_columns, true);
             mma_ts(tmem + kU, tmem + kWLo + 8 * j, hi, tokens_by_columns, true);

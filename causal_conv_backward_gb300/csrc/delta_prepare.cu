@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
     if (lane == 0)
         sh.most_p[warp] = most_p;
     const float scale_t = scale_for(most_t), of_t = inverse_scale(scale_t);
-    store_terms(xt, scale_t, out, out + kPanelBytes, t, part);
+    store_terms(xt, scale_t, out + kPanelT * kPanelBytes, out + kPanelTLo * kPanelBytes, t, part);
     const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
     // a row of zeros adds nothing, and must not lower the others' scale
     const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid
     for (int w = 1; w < kThreads / 32; ++w)
         most_p = fmaxf(most_p, sh.most_p[w]);
     const float scale_p = scale_for(most_p);
-    store_terms(xp, scale_p, out + 2 * kPanelBytes, out + 3 * kPanelBytes, t, part);
+    store_terms(xp, scale_p, out + kPanelPT * kPanelBytes, out + kPanelPTLo * kPanelBytes, t, part);
     if (part == 0) {
         factors[kFactorB * kC + t] = sh.b[t];
         factors[kFactorX * kC + t] = fx;

@@ -20,7 +20,25 @@ struct DeltaStepParams {
     int32_t H, G, K, V, flags;
     float scale;
     int32_t tiles;       // blocks along V
+    bool fours;          // four keys of q and k are one load
 };
+
+// Four 16-bit values, `live` of them there.
+template <int DT>
+__device__ __forceinline__ void four(const uint16_t *from, bool fours, int live, float *x)
+{
+    if (fours) {
+        uint2 v = make_uint2(0u, 0u);
+        if (live > 0)
+            v = __ldg(reinterpret_cast<const uint2 *>(from));
+        const float2 a = unpack2<DT>(v.x), b = unpack2<DT>(v.y);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = i < live ? value<DT>(from + i) : 0.f;
+    }
+}
 
 // Eight lanes share a row of the state, each with J groups of four adjacent
 // keys 32 apart; a warp has RR times four rows, a block four warps.
@@ -65,16 +83,17 @@ __global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __gri
     const uint16_t *qp = p.q + b * p.q_s[0] + g * p.q_s[1], *kp = p.k + b * p.k_s[0] + g * p.k_s[1];
     float q[4 * J], k[4 * J], sums[3] = {0.f, 0.f, 0.f};       // q.q, k.k, k.q
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < J; ++j) {
+        const int at = j * 32 + l8 * 4;
+        four<DT>(qp + at, p.fours, p.K - at, &q[4 * j]);
+        four<DT>(kp + at, p.fours, p.K - at, &k[4 * j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = j * 32 + l8 * 4 + i, e = 4 * j + i;
-            q[e] = at < p.K ? value<DT>(qp + at) : 0.f;
-            k[e] = at < p.K ? value<DT>(kp + at) : 0.f;
+        for (int e = 4 * j; e < 4 * j + 4; ++e) {
             sums[0] = fmaf(q[e], q[e], sums[0]);
             sums[1] = fmaf(k[e], k[e], sums[1]);
             sums[2] = fmaf(q[e], k[e], sums[2]);
         }
+    }
     const Gates gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + b * p.delta_s + h) : 0.f,
                                 p.delta && p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
                                 value<DT>(p.beta + b * p.beta_s + h));
@@ -132,10 +151,9 @@ __global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __gri
     }
 }
 
-template <int DT, int J>
+template <int DT, int J, int RR>
 int32_t step(const DeltaStepParams &q, int64_t items, bool whole, cudaStream_t stream)
 {
-    constexpr int RR = 2;
     DeltaStepParams p = q;
     p.tiles = (p.V + 4 * RR * kStepWarps - 1) / (4 * RR * kStepWarps);
     const dim3 grid((unsigned)(items * p.tiles));
@@ -157,9 +175,18 @@ int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream)
     p.H = (int32_t)a.H, p.G = (int32_t)a.G, p.K = (int32_t)a.K, p.V = (int32_t)a.V, p.flags = a.flags, p.scale = (float)a.scale;
     const bool whole = a.K % 4 == 0 && ((uintptr_t)a.state & 15u) == 0;
     const int64_t items = a.B * a.H;
+    p.fours = a.K % 4 == 0 && (((uintptr_t)a.q | (uintptr_t)a.k) & 7u) == 0 && ((a.q_strides[0] | a.q_strides[1] | a.k_strides[0] | a.k_strides[1]) & 3) == 0;
+    // eight rows to a warp where that still makes four blocks for each SM
+    const bool tall = items * ((a.V + 31) / 32) >= 4 * kNumSMs;
     const auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        return a.K <= 32 ? step<DT, 1>(p, items, whole, stream) : a.K <= 64 ? step<DT, 2>(p, items, whole, stream) : step<DT, 4>(p, items, whole, stream);
+        const auto rows = [&](auto rr) {
+            constexpr int RR = decltype(rr)::value;
+            return a.K <= 32   ? step<DT, 1, RR>(p, items, whole, stream)
+                   : a.K <= 64 ? step<DT, 2, RR>(p, items, whole, stream)
+                               : step<DT, 4, RR>(p, items, whole, stream);
+        };
+        return tall ? rows(std::integral_constant<int, 2>()) : rows(std::integral_constant<int, 1>());
     };
     return a.dtype == 0 ? go(std::integral_constant<int, 0>()) : go(std::integral_constant<int, 1>());
 }

@@ -54,6 +54,12 @@ struct RowShape {
 template <class R>
 __device__ __forceinline__ int thread_of_row() { return threadIdx.x % R::TPR; }
 
+// Two neighbours of a thread's values, for packed arithmetic.
+template <int N>
+__device__ __forceinline__ float2 pair(const float (&x)[N], int e) { return make_float2(x[e], x[e + 1]); }
+template <int N>
+__device__ __forceinline__ void put(float (&x)[N], int e, float2 v) { x[e] = v.x, x[e + 1] = v.y; }
+
 // ------------------------------------------------------------------ loads and stores
 // 16-bit values of type DT (0, 1), or fp32 (2); zero past the row's end.
 template <int DT>

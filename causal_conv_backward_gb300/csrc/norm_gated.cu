@@ -20,7 +20,7 @@ struct GatedParams {
 };
 
 template <int DT, class R>
-__global__ void __launch_bounds__(R::THREADS) gated_norm_kernel(const __grid_constant__ GatedParams p)
+__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) gated_norm_kernel(const __grid_constant__ GatedParams p)
 {
     __shared__ float shared[2][3][32];
     int turn = 0;

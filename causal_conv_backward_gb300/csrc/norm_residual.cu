@@ -7,7 +7,7 @@ namespace {
 
 // RT: the residual stream's type.
 template <int DT, int RT, class R>
-__global__ void __launch_bounds__(R::THREADS) residual_norm_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) residual_norm_kernel(const __grid_constant__ ResidualParams p)
 {
     __shared__ float shared[2][3][32];
     int turn = 0;

@@ -59,10 +59,11 @@ struct Branch {
     {
         r = 1.f;
         if (p.post_weight) {
-            float v[1] = {0.f};
+            float2 v2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                v[0] = fmaf(x[e], x[e], v[0]);
+            for (int e = 0; e < R::E; e += 2)
+                v2 = fma2(pair(x, e), pair(x, e), v2);
+            float v[1] = {v2.x + v2.y};
             row_sums<R>(v, shared, turn);
             r = inverse_root(fmaf(v[0], p.inv_D, p.eps));
         }
@@ -72,22 +73,27 @@ struct Branch {
             float f[R::E];
             values<2, R>(s, f);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                h[e] = fmaf(m[e], f[e], h[e]);
+            for (int e = 0; e < R::E; e += 2)
+                put(h, e, fma2(pair(m, e), pair(f, e), pair(h, e)));
         } else {
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                h[e] += m[e];
+            for (int e = 0; e < R::E; e += 2)
+                put(h, e, add2(pair(h, e), pair(m, e)));
         }
     }
     // m of x, once r is known
     __device__ __forceinline__ void branch(const ResidualParams &p, const float (&x)[R::E], float (&m)[R::E]) const
     {
-        if (p.post_weight)
+        if (p.post_weight) {
             values<DT, R>(pw, m);
 #pragma unroll
-        for (int e = 0; e < R::E; ++e)
-            m[e] = p.post_weight ? x[e] * r * m[e] : x[e];
+            for (int e = 0; e < R::E; e += 2)
+                put(m, e, mul2(mul2(pair(x, e), make_float2(r, r)), pair(m, e)));
+        } else {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e)
+                m[e] = x[e];
+        }
     }
 };
 

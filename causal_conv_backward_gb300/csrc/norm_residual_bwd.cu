@@ -52,28 +52,28 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
         b.sum(p, x, h, &shared, turn);
         values<DT, R>(gr, g);
         values<DT, R>(wr, w);
-        float s[2] = {0.f, 0.f};
+        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < R::E; ++e) {
-            s[0] = fmaf(h[e], h[e], s[0]);
-            s[1] = fmaf(g[e] * w[e], h[e], s[1]);
+        for (int e = 0; e < R::E; e += 2) {
+            s2[0] = fma2(pair(h, e), pair(h, e), s2[0]);
+            s2[1] = fma2(mul2(pair(g, e), pair(w, e)), pair(h, e), s2[1]);
         }
+        float s[2] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y};
         row_sums<R>(s, &shared, turn);
         const float rh = inverse_root(fmaf(s[0], p.inv_D, p.eps));
-        const float along = s[1] * p.inv_D * rh;
+        const float along = s[1] * p.inv_D * rh, in = there ? 1.f : 0.f;      // rows that are not there add nothing
 #pragma unroll
-        for (int e = 0; e < R::E; ++e) {
-            const float n = h[e] * rh;
-            if (there)
-                gw[e] = fmaf(g[e], n, gw[e]);
-            g[e] = rh * fmaf(-n, along, g[e] * w[e]);
+        for (int e = 0; e < R::E; e += 2) {
+            const float2 n = mul2(pair(h, e), make_float2(rh, rh));
+            put(gw, e, fma2(mul2(pair(g, e), make_float2(in, in)), n, pair(gw, e)));
+            put(g, e, mul2(make_float2(rh, rh), fma2(n, make_float2(-along, -along), mul2(pair(g, e), pair(w, e)))));
         }
         if (p.grad_h) {
             float gh[R::E];
             values<RT, R>(hr, gh);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                g[e] += gh[e];
+            for (int e = 0; e < R::E; e += 2)
+                put(g, e, add2(pair(g, e), pair(gh, e)));
         }
         if (there)
             store_values<RT, R>(p.grad_residual, (int64_t)row * p.D, p.D, g);
@@ -82,28 +82,28 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
             b.branch(p, x, m);
             values<2, R>(b.s, f);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e) {
-                if (there)
-                    gs[e] = fmaf(g[e], m[e], gs[e]);
-                g[e] *= f[e];
+            for (int e = 0; e < R::E; e += 2) {
+                put(gs, e, fma2(mul2(pair(g, e), make_float2(in, in)), pair(m, e), pair(gs, e)));
+                put(g, e, mul2(pair(g, e), pair(f, e)));
             }
         }
         if (p.post_weight) {
-            float t[1] = {0.f}, pw[R::E];
+            float pw[R::E];
             values<DT, R>(b.pw, pw);
+            float2 t2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e) {
-                x[e] *= b.r;
-                if (there)
-                    gp[e] = fmaf(g[e], x[e], gp[e]);
-                g[e] *= pw[e];
-                t[0] = fmaf(g[e], x[e], t[0]);
+            for (int e = 0; e < R::E; e += 2) {
+                put(x, e, mul2(pair(x, e), make_float2(b.r, b.r)));
+                put(gp, e, fma2(mul2(pair(g, e), make_float2(in, in)), pair(x, e), pair(gp, e)));
+                put(g, e, mul2(pair(g, e), pair(pw, e)));
+                t2 = fma2(pair(g, e), pair(x, e), t2);
             }
+            float t[1] = {t2.x + t2.y};
             row_sums<R>(t, &shared, turn);
             const float back = t[0] * p.inv_D;
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                g[e] = b.r * fmaf(-x[e], back, g[e]);
+            for (int e = 0; e < R::E; e += 2)
+                put(g, e, mul2(make_float2(b.r, b.r), fma2(pair(x, e), make_float2(-back, -back), pair(g, e))));
         }
         if (there)
             store_values<DT, R>(p.grad_x, (int64_t)row * p.D, p.D, g);

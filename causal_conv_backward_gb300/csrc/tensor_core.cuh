@@ -152,6 +152,20 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
 // are ordered after it.
 __device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Whether a barrier's phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------ two terms
 // The power of two that takes a largest magnitude to 2^14..2^15 (1 for zero,
 // infinity and NaN), and its reciprocal. A value times it is hi + lo, two fp16
