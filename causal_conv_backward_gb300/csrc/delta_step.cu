@@ -2,7 +2,10 @@
 //
 // The state, 4 V K bytes a head, is read and written once; everything else is
 // small beside it. Both products with the state come out of one pass before it
-// changes: S(t) q' = a S(t-1) q' + u (k'.q').
+// changes: S(t) q' = a S(t-1) q' + u (k'.q'). States are read and written past the
+// caches' order (256 x 16 heads of 128 x 128: 86 us without, 80 with; the copy
+// bandwidth would take 79). Loading four values of q and k at once, which leaves
+// more blocks in flight, took 93 us.
 #include "delta_common.cuh"
 
 namespace mcc1d {
@@ -20,25 +23,7 @@ struct DeltaStepParams {
     int32_t H, G, K, V, flags;
     float scale;
     int32_t tiles;       // blocks along V
-    bool fours;          // four keys of q and k are one load
 };
-
-// Four 16-bit values, `live` of them there.
-template <int DT>
-__device__ __forceinline__ void four(const uint16_t *from, bool fours, int live, float *x)
-{
-    if (fours) {
-        uint2 v = make_uint2(0u, 0u);
-        if (live > 0)
-            v = __ldg(reinterpret_cast<const uint2 *>(from));
-        const float2 a = unpack2<DT>(v.x), b = unpack2<DT>(v.y);
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = i < live ? value<DT>(from + i) : 0.f;
-    }
-}
 
 // Eight lanes share a row of the state, each with J groups of four adjacent
 // keys 32 apart; a warp has RR times four rows, a block four warps.
@@ -71,7 +56,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __gri
             s[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (WHOLE) {
                 if (row < p.V && at < p.K)
-                    s[r][j] = *reinterpret_cast<const float4 *>(state + row * p.K + at);
+                    s[r][j] = __ldcs(reinterpret_cast<const float4 *>(state + row * p.K + at));
             } else if (row < p.V) {
                 float *e = reinterpret_cast<float *>(&s[r][j]);
 #pragma unroll
@@ -84,11 +69,11 @@ __global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __gri
     float q[4 * J], k[4 * J], sums[3] = {0.f, 0.f, 0.f};       // q.q, k.k, k.q
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int at = j * 32 + l8 * 4;
-        four<DT>(qp + at, p.fours, p.K - at, &q[4 * j]);
-        four<DT>(kp + at, p.fours, p.K - at, &k[4 * j]);
 #pragma unroll
         for (int e = 4 * j; e < 4 * j + 4; ++e) {
+            const int at = j * 32 + l8 * 4 + e % 4;
+            q[e] = at < p.K ? value<DT>(qp + at) : 0.f;
+            k[e] = at < p.K ? value<DT>(kp + at) : 0.f;
             sums[0] = fmaf(q[e], q[e], sums[0]);
             sums[1] = fmaf(k[e], k[e], sums[1]);
             sums[2] = fmaf(q[e], k[e], sums[2]);
@@ -137,7 +122,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __gri
                                          fmaf(uk, k[4 * j + 3], a * o.w));
             if (WHOLE) {
                 if (at < p.K)
-                    *reinterpret_cast<float4 *>(state + row * p.K + at) = n;
+                    __stcs(reinterpret_cast<float4 *>(state + row * p.K + at), n);
             } else {
                 const float e[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
@@ -175,9 +160,11 @@ int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream)
     p.H = (int32_t)a.H, p.G = (int32_t)a.G, p.K = (int32_t)a.K, p.V = (int32_t)a.V, p.flags = a.flags, p.scale = (float)a.scale;
     const bool whole = a.K % 4 == 0 && ((uintptr_t)a.state & 15u) == 0;
     const int64_t items = a.B * a.H;
-    p.fours = a.K % 4 == 0 && (((uintptr_t)a.q | (uintptr_t)a.k) & 7u) == 0 && ((a.q_strides[0] | a.q_strides[1] | a.k_strides[0] | a.k_strides[1]) & 3) == 0;
-    // eight rows to a warp where that still makes four blocks for each SM
-    const bool tall = items * ((a.V + 31) / 32) >= 4 * kNumSMs;
+    // Sixteen rows to a warp where that still makes four blocks for each SM: 256
+    // sequences of 16 heads of 128 x 128 take 80 us, 84 with eight rows, 93 with
+    // four; one sequence takes 2.8 us with four and has an eighth of the blocks
+    // with sixteen.
+    const bool tall = items * ((a.V + 63) / 64) >= 4 * kNumSMs;
     const auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const auto rows = [&](auto rr) {
@@ -186,7 +173,7 @@ int32_t launch_delta_step(const mcc1d_delta_step_args &a, cudaStream_t stream)
                    : a.K <= 64 ? step<DT, 2, RR>(p, items, whole, stream)
                                : step<DT, 4, RR>(p, items, whole, stream);
         };
-        return tall ? rows(std::integral_constant<int, 2>()) : rows(std::integral_constant<int, 1>());
+        return tall ? rows(std::integral_constant<int, 4>()) : rows(std::integral_constant<int, 1>());
     };
     return a.dtype == 0 ? go(std::integral_constant<int, 0>()) : go(std::integral_constant<int, 1>());
 }
