@@ -86,44 +86,44 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
         if (p.rows - first > step)
             ask(first + step);
         values<DT, R>(xr, x);
-        float s[2] = {0.f, 0.f};
+        values<DT, R>(gr, g);
+        // the gate z sigmoid(z), and grad_y times its derivative
+        float gz[R::E];
         if (p.z) {
             float z[R::E];
             values<DT, R>(zr, z);
-            values<DT, R>(gr, g);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e)
-                g[e] *= z[e] * sigmoid(z[e]);
-        } else {
-            values<DT, R>(gr, g);
+            for (int e = 0; e < R::E; e += 2) {
+                const float2 sig = sigmoid2(pair(z, e)), gate = mul2(pair(z, e), sig), one = make_float2(1.f, 1.f);
+                put(gz, e, mul2(pair(g, e), fma2(gate, sub2(one, sig), sig)));
+                put(g, e, mul2(pair(g, e), gate));
+            }
         }
+        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < R::E; ++e) {
-            s[0] = fmaf(x[e], x[e], s[0]);
-            s[1] = fmaf(g[e] * w[e], x[e], s[1]);
+        for (int e = 0; e < R::E; e += 2) {
+            s2[0] = fma2(pair(x, e), pair(x, e), s2[0]);
+            s2[1] = fma2(mul2(pair(g, e), pair(w, e)), pair(x, e), s2[1]);
         }
+        float s[2] = {s2[0].x + s2[0].y, s2[1].x + s2[1].y};
         row_sums<R>(s, &shared, turn);
         const float rms = inverse_root(fmaf(s[0], p.inv_D, p.eps));
         const float along = s[1] * p.inv_D * rms;      // mean(g weight n)
         if (there) {
+            const float2 r = make_float2(rms, rms);
 #pragma unroll
-            for (int e = 0; e < R::E; ++e) {
-                const float n = x[e] * rms;
-                gw[e] = fmaf(g[e], n, gw[e]);
-                g[e] = rms * fmaf(-n, along, g[e] * w[e]);
-                x[e] = n;
+            for (int e = 0; e < R::E; e += 2) {
+                const float2 n = mul2(pair(x, e), r);
+                put(gw, e, fma2(pair(g, e), n, pair(gw, e)));
+                put(g, e, mul2(r, fma2(n, make_float2(-along, -along), mul2(pair(g, e), pair(w, e)))));
+                put(x, e, n);
             }
             store_values<DT, R>(p.grad_x, (int64_t)row * p.D, p.D, g);
             if (p.grad_z) {
-                float z[R::E];
-                values<DT, R>(zr, z);
-                values<DT, R>(gr, g);
 #pragma unroll
-                for (int e = 0; e < R::E; ++e) {
-                    const float sig = sigmoid(z[e]);
-                    g[e] *= x[e] * w[e] * sig * fmaf(z[e], 1.f - sig, 1.f);
-                }
-                store_values<DT, R>(p.grad_z, (int64_t)row * p.D, p.D, g);
+                for (int e = 0; e < R::E; e += 2)
+                    put(gz, e, mul2(pair(gz, e), mul2(pair(x, e), pair(w, e))));
+                store_values<DT, R>(p.grad_z, (int64_t)row * p.D, p.D, gz);
             }
         }
     }
