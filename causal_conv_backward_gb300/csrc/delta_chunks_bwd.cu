@@ -446,7 +446,7 @@ __device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh,
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kThreads, 1) delta_chunks_bwd_kernel(const __grid_constant__ BackParams cp)
+__global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_chunks_bwd_rows(const __grid_constant__ BackParams cp)
 {
     extern __shared__ uint8_t raw_shared[];
     __shared__ BackShared sh;
@@ -506,13 +506,13 @@ int32_t chunks_of(const BackParams &p, cudaStream_t stream)
     // with: an increase past that would wait for ever
     static const bool fits = [] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, delta_chunks_bwd_kernel<DT, KP>) == cudaSuccess && fa.numRegs == kRegLaunch;
+        return cudaFuncGetAttributes(&fa, mcc1d_delta_chunks_bwd_rows<DT, KP>) == cudaSuccess && fa.numRegs == kRegLaunch;
     }();
     if (!fits)
         return kErrCuda;
-    if (cudaFuncSetAttribute(delta_chunks_bwd_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(mcc1d_delta_chunks_bwd_rows<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_chunks_bwd_kernel<DT, KP>, dim3((unsigned)blocks_of(p.seg, p.d, p.tiles)), kThreads, bytes, stream, p);
+    return launch(mcc1d_delta_chunks_bwd_rows<DT, KP>, dim3((unsigned)blocks_of(p.seg, p.d, p.tiles)), kThreads, bytes, stream, p);
 }
 
 }  // namespace

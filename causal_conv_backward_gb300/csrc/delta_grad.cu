@@ -186,7 +186,7 @@ __device__ __forceinline__ void three_products(uint32_t d, uint32_t a, uint32_t 
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ GradParams gp)
+__global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __grid_constant__ GradParams gp)
 {
     extern __shared__ uint8_t raw_shared[];
     __shared__ GradShared sh;
@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
                 x[e] = (four(sh.row[0], i) + four(sh.row[1], i)) - ((sh.col[0][i] + sh.col[1][i]) + (sh.col[2][i] + sh.col[3][i]));
                 x[e] += four(sh.dots[0], i) + sh.b[i] * sk - se;
                 sh.gb[i] = sh.dv[i] + sk + four(sh.low, i);
+                if (!ok)
+                    x[e] = sh.gb[i] = __uint_as_float(0x7FFFFFFFu);
                 all_e += se;
             }
             all_e = sum_of_lanes<32>(all_e);
@@ -657,9 +659,9 @@ template <int DT, int KP>
 int32_t grad(const GradParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Panels<KP>::kBytes + 1024;
-    if (cudaFuncSetAttribute(delta_grad_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(mcc1d_delta_grad_chunk<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_grad_kernel<DT, KP>, dim3((unsigned)blocks), kThreads, bytes, stream, p);
+    return launch(mcc1d_delta_grad_chunk<DT, KP>, dim3((unsigned)blocks), kThreads, bytes, stream, p);
 }
 
 }  // namespace

@@ -33,7 +33,7 @@ __device__ __forceinline__ void bring(float (*to)[KP + 4], const float *from, in
 }
 
 template <int KP, bool BACK>
-__global__ void __launch_bounds__(kThreads, 1) delta_join_kernel(const __grid_constant__ JoinParams p)
+__global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_join_segments(const __grid_constant__ JoinParams p)
 {
     extern __shared__ __align__(16) float shared[];
     typedef float Matrix[KP + 4];
@@ -97,9 +97,9 @@ template <int KP, bool BACK>
 int32_t join(const JoinParams &p, cudaStream_t stream)
 {
     constexpr int bytes = 2 * KP * (KP + 4) * 4;
-    if (cudaFuncSetAttribute(delta_join_kernel<KP, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(mcc1d_delta_join_segments<KP, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_join_kernel<KP, BACK>, dim3((unsigned)(p.heads * p.tiles)), kThreads, bytes, stream, p);
+    return launch(mcc1d_delta_join_segments<KP, BACK>, dim3((unsigned)(p.heads * p.tiles)), kThreads, bytes, stream, p);
 }
 
 }  // namespace

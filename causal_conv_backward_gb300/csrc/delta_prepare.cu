@@ -113,7 +113,7 @@ __device__ __forceinline__ float most_of_warp(float x)
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kThreads, 3) delta_prepare_kernel(const __grid_constant__ PrepareParams pp)
+__global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const __grid_constant__ PrepareParams pp)
 {
     extern __shared__ __align__(16) uint8_t raw_shared[];
     typedef PrepareShared<KP> Shared;
@@ -396,9 +396,9 @@ template <int DT, int KP>
 int32_t prepare(const PrepareParams &p, cudaStream_t stream)
 {
     constexpr int bytes = (int)sizeof(PrepareShared<KP>);
-    if (cudaFuncSetAttribute(delta_prepare_kernel<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(mcc1d_delta_prepare_chunk<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(delta_prepare_kernel<DT, KP>, dim3((unsigned)(p.chunks * p.d.B * p.d.H)), kThreads, bytes, stream, p);
+    return launch(mcc1d_delta_prepare_chunk<DT, KP>, dim3((unsigned)(p.chunks * p.d.B * p.d.H)), kThreads, bytes, stream, p);
 }
 
 }  // namespace

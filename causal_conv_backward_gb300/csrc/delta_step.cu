@@ -30,7 +30,7 @@ struct DeltaStepParams {
 constexpr int kStepWarps = 4;
 
 template <int DT, int J, int RR, bool WHOLE>
-__global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const __grid_constant__ DeltaStepParams p)
+__global__ void __launch_bounds__(kStepWarps * 32) mcc1d_delta_one_token(const __grid_constant__ DeltaStepParams p)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l8 = lane % 8;
     const uint32_t item = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
@@ -142,8 +142,8 @@ int32_t step(const DeltaStepParams &q, int64_t items, bool whole, cudaStream_t s
     DeltaStepParams p = q;
     p.tiles = (p.V + 4 * RR * kStepWarps - 1) / (4 * RR * kStepWarps);
     const dim3 grid((unsigned)(items * p.tiles));
-    return whole ? launch(delta_step_kernel<DT, J, RR, true>, grid, kStepWarps * 32, 0, stream, p)
-                 : launch(delta_step_kernel<DT, J, RR, false>, grid, kStepWarps * 32, 0, stream, p);
+    return whole ? launch(mcc1d_delta_one_token<DT, J, RR, true>, grid, kStepWarps * 32, 0, stream, p)
+                 : launch(mcc1d_delta_one_token<DT, J, RR, false>, grid, kStepWarps * 32, 0, stream, p);
 }
 
 }  // namespace

@@ -115,7 +115,7 @@ __device__ __forceinline__ void sum8(float (&x)[N])
 }
 
 template <int DT, int J>
-__global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_constant__ DeltaParams p)
+__global__ void __launch_bounds__(kWarps * 32) mcc1d_delta_tokens_rows(const __grid_constant__ DeltaParams p)
 {
     __shared__ TokenShared<32 * J> sh;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l8 = lane % 8;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(const __grid_
 // tokens: du = (G + gy q'^T) k', grad_v = b du, and before the token
 // G = a (G + gy q'^T - b du k'^T).
 template <int DT, int J>
-__global__ void __launch_bounds__(kWarps * 32) delta_tokens_bwd_kernel(const __grid_constant__ DeltaParams p)
+__global__ void __launch_bounds__(kWarps * 32) mcc1d_delta_tokens_bwd_rows(const __grid_constant__ DeltaParams p)
 {
     __shared__ TokenShared<32 * J> sh;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l8 = lane % 8;
@@ -241,8 +241,8 @@ int32_t launch_delta_tokens(const mcc1d_delta_args &a, const DeltaKept &kept, cu
     p.kept = kept;
     const auto go = [&](auto kernel) { return launch(kernel, token_grid(p), kWarps * 32, 0, stream, p); };
     if (a.dtype == 0)
-        return a.K <= 64 ? go(delta_tokens_kernel<0, 2>) : go(delta_tokens_kernel<0, 4>);
-    return a.K <= 64 ? go(delta_tokens_kernel<1, 2>) : go(delta_tokens_kernel<1, 4>);
+        return a.K <= 64 ? go(mcc1d_delta_tokens_rows<0, 2>) : go(mcc1d_delta_tokens_rows<0, 4>);
+    return a.K <= 64 ? go(mcc1d_delta_tokens_rows<1, 2>) : go(mcc1d_delta_tokens_rows<1, 4>);
 }
 
 int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, const DeltaKept &kept, cudaStream_t stream)
@@ -255,8 +255,8 @@ int32_t launch_delta_tokens_bwd(const mcc1d_delta_bwd_args &a, const DeltaKept &
         p.gy_s[i] = a.grad_y_strides[i];
     const auto go = [&](auto kernel) { return launch(kernel, token_grid(p), kWarps * 32, 0, stream, p); };
     if (a.fwd.dtype == 0)
-        return a.fwd.K <= 64 ? go(delta_tokens_bwd_kernel<0, 2>) : go(delta_tokens_bwd_kernel<0, 4>);
-    return a.fwd.K <= 64 ? go(delta_tokens_bwd_kernel<1, 2>) : go(delta_tokens_bwd_kernel<1, 4>);
+        return a.fwd.K <= 64 ? go(mcc1d_delta_tokens_bwd_rows<0, 2>) : go(mcc1d_delta_tokens_bwd_rows<0, 4>);
+    return a.fwd.K <= 64 ? go(mcc1d_delta_tokens_bwd_rows<1, 2>) : go(mcc1d_delta_tokens_bwd_rows<1, 4>);
 }
 
 }  // namespace mcc1d

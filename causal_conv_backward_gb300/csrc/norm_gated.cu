@@ -20,7 +20,7 @@ struct GatedParams {
 };
 
 template <int DT, class R>
-__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) gated_norm_kernel(const __grid_constant__ GatedParams p)
+__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) mcc1d_norm_gated_fwd(const __grid_constant__ GatedParams p)
 {
     __shared__ float shared[2][3][32];
     int turn = 0;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) gated_norm_kern
 //   grad_weight = sum of g n over the rows,  grad_z = grad_y n weight silu'(z),
 //   grad_x = r (g weight - n mean(g weight n))
 template <int DT, class R>
-__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREADS : 1) gated_norm_bwd_kernel(const __grid_constant__ GatedParams p)
+__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREADS : 1) mcc1d_norm_gated_bwd(const __grid_constant__ GatedParams p)
 {
     __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
 
 // out[c] = sum of part[p][c]: 32 columns to a block of 8 warps, each warp its
 // share of the parts, the warps' sums joined in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const __grid_constant__ ColumnSums s, int32_t parts, int32_t columns)
+__global__ void __launch_bounds__(256) mcc1d_norm_sums(const __grid_constant__ ColumnSums s, int32_t parts, int32_t columns)
 {
     __shared__ float joined[8][32];
     previous_done();
@@ -211,8 +211,8 @@ int32_t launch_gated_norm(const mcc1d_gated_norm_args &a, cudaStream_t stream)
     return with_row_shape(a.D, vectors(a, (uintptr_t)a.y, 0), [&](auto shape) {
         typedef decltype(shape) R;
         const dim3 grid((unsigned)((p.rows + R::ROWS - 1) / R::ROWS));
-        return a.dtype == 0 ? launch(gated_norm_kernel<0, R>, grid, R::THREADS, 0, stream, p)
-                            : launch(gated_norm_kernel<1, R>, grid, R::THREADS, 0, stream, p);
+        return a.dtype == 0 ? launch(mcc1d_norm_gated_fwd<0, R>, grid, R::THREADS, 0, stream, p)
+                            : launch(mcc1d_norm_gated_fwd<1, R>, grid, R::THREADS, 0, stream, p);
     });
 }
 
@@ -225,8 +225,8 @@ int32_t launch_gated_norm_bwd(const mcc1d_gated_norm_bwd_args &a, float *workspa
     const int64_t blocks = norm_bwd_blocks(p.rows, a.fwd.D, vec, kGatedThreads);
     const int32_t st = with_row_shape_bwd(a.fwd.D, vec, [&](auto shape) {
         typedef decltype(shape) R;
-        return a.fwd.dtype == 0 ? launch(gated_norm_bwd_kernel<0, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p)
-                                : launch(gated_norm_bwd_kernel<1, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p);
+        return a.fwd.dtype == 0 ? launch(mcc1d_norm_gated_bwd<0, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p)
+                                : launch(mcc1d_norm_gated_bwd<1, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p);
     });
     if (st != kOk)
         return st;
@@ -236,7 +236,7 @@ int32_t launch_gated_norm_bwd(const mcc1d_gated_norm_bwd_args &a, float *workspa
 
 int32_t launch_column_sums(const ColumnSums &s, int64_t parts, int64_t columns, int sums, cudaStream_t stream)
 {
-    return launch_as(true, column_sums_kernel, dim3((unsigned)((columns + 31) / 32), (unsigned)sums), 256, 0, stream, s, (int32_t)parts,
+    return launch_as(true, mcc1d_norm_sums, dim3((unsigned)((columns + 31) / 32), (unsigned)sums), 256, 0, stream, s, (int32_t)parts,
                      (int32_t)columns);
 }
 

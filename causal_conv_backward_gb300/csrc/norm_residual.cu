@@ -7,7 +7,7 @@ namespace {
 
 // RT: the residual stream's type.
 template <int DT, int RT, class R>
-__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) residual_norm_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(R::THREADS, 1024 / R::THREADS) mcc1d_norm_residual_fwd(const __grid_constant__ ResidualParams p)
 {
     __shared__ float shared[2][3][32];
     int turn = 0;
@@ -48,8 +48,8 @@ int32_t launch_residual_norm(const mcc1d_residual_norm_args &a, cudaStream_t str
         const dim3 grid((unsigned)((p.rows + R::ROWS - 1) / R::ROWS));
         const auto go = [&](auto kernel) { return launch(kernel, grid, R::THREADS, 0, stream, p); };
         if (a.flags & MCC1D_WIDE)
-            return a.dtype == 0 ? go(residual_norm_kernel<0, 2, R>) : go(residual_norm_kernel<1, 2, R>);
-        return a.dtype == 0 ? go(residual_norm_kernel<0, 0, R>) : go(residual_norm_kernel<1, 1, R>);
+            return a.dtype == 0 ? go(mcc1d_norm_residual_fwd<0, 2, R>) : go(mcc1d_norm_residual_fwd<1, 2, R>);
+        return a.dtype == 0 ? go(mcc1d_norm_residual_fwd<0, 0, R>) : go(mcc1d_norm_residual_fwd<1, 1, R>);
     });
 }
 

@@ -14,7 +14,7 @@ namespace mcc1d {
 namespace {
 
 template <int DT, int RT, class R>
-__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREADS : 1) residual_norm_bwd_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREADS : 1) mcc1d_norm_residual_bwd(const __grid_constant__ ResidualParams p)
 {
     __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
@@ -139,8 +139,8 @@ int32_t launch_residual_norm_bwd(const mcc1d_residual_norm_bwd_args &a, float *w
         typedef decltype(shape) R;
         const auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)blocks), R::THREADS, 0, stream, p); };
         if (f.flags & MCC1D_WIDE)
-            return f.dtype == 0 ? go(residual_norm_bwd_kernel<0, 2, R>) : go(residual_norm_bwd_kernel<1, 2, R>);
-        return f.dtype == 0 ? go(residual_norm_bwd_kernel<0, 0, R>) : go(residual_norm_bwd_kernel<1, 1, R>);
+            return f.dtype == 0 ? go(mcc1d_norm_residual_bwd<0, 2, R>) : go(mcc1d_norm_residual_bwd<1, 2, R>);
+        return f.dtype == 0 ? go(mcc1d_norm_residual_bwd<0, 0, R>) : go(mcc1d_norm_residual_bwd<1, 1, R>);
     });
     if (st != kOk)
         return st;

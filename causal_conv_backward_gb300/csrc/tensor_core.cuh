@@ -24,22 +24,6 @@ __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait:
 
 // Columns of this thread's lane. The loaded registers are valid after tmem_wait,
 // which names them so that nothing uses them earlier.
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(at)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 :
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[16])
 {
     asm volatile(
