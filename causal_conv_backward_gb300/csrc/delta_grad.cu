@@ -55,7 +55,9 @@ struct GradShared {
     float ch[kC], cl[kC], b[kC], dt[kC], raw[kC], fq[kC], fk[kC];    // fq, fk: of q, k as they are
     float xq[kC], xk[kC];                                           // of q, k as operands
     float gc[kC], gb[kC], dv[kC], dot[kThreads / 32];
-    float dots[3][kQuarters][kC], row[2][kQuarters][kC], low[kQuarters][kC], col[4][kC];
+    float dots[3][kQuarters][kC], low[kQuarters][kC];
+    int row[2][kQuarters][kC], col[4][kC];                           // sums over decayed pairs, in units of their warps
+    uint32_t exponent[kThreads / 32];
     float most[kQuarters][2 * kC], most_of_warps[kThreads / 32];
 };
 
@@ -158,7 +160,7 @@ __device__ __forceinline__ void ask_ahead(const GradParams &gp, int64_t chunk, i
 }
 
 // Sums of 16 values over the warp's lanes: lane l has that of value l / 2.
-__device__ __forceinline__ float sums16(float (&x)[16])
+__device__ __forceinline__ int sums16(int (&x)[16])
 {
     const int lane = threadIdx.x % 32;
 #pragma unroll
@@ -166,12 +168,20 @@ __device__ __forceinline__ float sums16(float (&x)[16])
         const bool upper = lane & d;
 #pragma unroll
         for (int e = 0; e < n; ++e) {
-            const float give = upper ? x[e] : x[e + n], keep = upper ? x[e + n] : x[e];
+            const int give = upper ? x[e] : x[e + n], keep = upper ? x[e + n] : x[e];
             x[e] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, d);
         }
     }
     return x[0] + __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
 }
+
+// What a warp's elements of magnitude up to `most` (its bits) are counted in:
+// 2^(e - 151) for the e of their exponent, 255 where one is not finite. 32 of
+// them stay within 2^30, and rounding to them is off by 2^-25 of the largest.
+__device__ __forceinline__ uint32_t exponent_of(uint32_t most) { return max(most >> 23, 24u); }
+__device__ __forceinline__ int counted(float x, uint32_t e) { return e >= 255 ? 0 : __float2int_rn(x * __uint_as_float((278u - e) << 23)); }
+// A warp's sum in units of 2^-16 of the largest warp's.
+__device__ __forceinline__ int64_t of_warp(int sum, uint32_t e, uint32_t most) { return ((int64_t)sum << 16) >> min(most - e, 63u); }
 
 // Adds A B^T, all of two terms but A's second times B's second, over 64 values
 // of the sum, by one thread.
@@ -465,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             uint32_t d[IC];
             tmem_load(lanes + kDK + quarter * IC, d);
             tmem_wait(d);
-            float E[IC], by_row[IC], row = 0.f, low = 0.f, most_row = 0.f, most_col = 0.f;
+            float E[IC], by_row[IC], low = 0.f, most_row = 0.f, most_col = 0.f;
+            uint32_t most_e = 0;
             const float th = sh.ch[t], tl = sh.cl[t], f = of_du ? sh.xk[t] : sh.xq[t], bt = of_du ? sh.b[t] : 1.f;
 #pragma unroll
             for (int c = 0; c < IC; ++c) {
@@ -473,17 +484,26 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
                 const bool in = of_du ? i < t : i <= t;
                 const float D = in ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) : 0.f, x = in ? PL[c] * D : 0.f;
                 const float xi = sh.xk[i], lk = x * (__uint_as_float(d[c]) * f * xi);
-                E[c] = bt * lk;
-                low += lk, row += E[c];
+                E[c] = i < t ? bt * lk : 0.f;      // no decay between a token and itself
+                low += lk, most_e = max(most_e, __float_as_uint(E[c]) & 0x7FFFFFFFu);
                 by_row[c] = bt * x * xi;
                 PL[c] = bt * x * f;
                 most_row = fmaxf(most_row, fabsf(by_row[c]));
                 most_col = fmaxf(most_col, fabsf(PL[c]));
             }
+            // a token's row less its column, summed from any token on, leaves out the
+            // pairs behind it: in integers nothing is left of them
+            const uint32_t exponent = exponent_of(__reduce_max_sync(0xFFFFFFFFu, most_e));
+            int counts[IC], row = 0;
+#pragma unroll
+            for (int c = 0; c < IC; ++c)
+                counts[c] = counted(E[c], exponent), row += counts[c];
             sh.row[of_du][quarter][t] = row;
             if (of_du)
                 sh.low[quarter][t] = low;
-            const float col = sums16(E);
+            const int col = sums16(counts);
+            if (lane == 0)
+                sh.exponent[warp] = exponent;
             if (lane % 2 == 0)
                 sh.col[warp % 4][quarter * IC + lane / 2] = col;
             most_col = most_of_lanes<32>(most_col);
@@ -548,39 +568,54 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
         if (warp == 0) {
             const float A = p.delta ? __ldg(p.A + h) : 0.f;
             const auto four = [](const float (&x)[kQuarters][kC], int i) { return (x[0][i] + x[1][i]) + (x[2][i] + x[3][i]); };
-            float x[2], all_e = 0.f;
+            // of pairs, in integers; of the end's products, which have the decays after
+            // their token; and of all others, which have those up to theirs
+            const uint32_t exponent = __reduce_max_sync(0xFFFFFFFFu, lane < kThreads / 32 ? sh.exponent[lane] : 0u);
+            int64_t pairs[2];
+            float x[2], e_of[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                const float se = four(sh.dots[2], i), sk = four(sh.dots[1], i);
-                x[e] = (four(sh.row[0], i) + four(sh.row[1], i)) - ((sh.col[0][i] + sh.col[1][i]) + (sh.col[2][i] + sh.col[3][i]));
-                x[e] += four(sh.dots[0], i) + sh.b[i] * sk - se;
+                pairs[e] = 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    pairs[e] += of_warp(sh.row[0][w][i], sh.exponent[4 * w + i / 32], exponent) + of_warp(sh.row[1][w][i], sh.exponent[4 * w + 2 + i / 32], exponent);
+                    pairs[e] -= of_warp(sh.col[w][i], sh.exponent[i / IC * 4 + w], exponent);
+                }
+                const float sk = four(sh.dots[1], i);
+                e_of[e] = four(sh.dots[2], i);
+                x[e] = four(sh.dots[0], i) + sh.b[i] * sk;
                 sh.gb[i] = sh.dv[i] + sk + four(sh.low, i);
                 if (!ok)
                     x[e] = sh.gb[i] = __uint_as_float(0x7FFFFFFFu);
-                all_e += se;
             }
-            all_e = sum_of_lanes<32>(all_e);
             if (lane == 31) {
                 float s = 0.f;
                 for (int w = 0; w < kThreads / 32; ++w)
                     s += sh.dot[w];
-                x[1] += fmaf(s, ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), all_e);
+                x[1] = fmaf(s, ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), x[1]);
             }
-            const float y = x[0] + x[1];
-            float s = y;      // sums to the end
+            int64_t s_pairs = pairs[0] + pairs[1];
+            float s = x[0] + x[1], s_e = e_of[0] + e_of[1];
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
-                const float o = __shfl_down_sync(0xFFFFFFFFu, s, d);
+                const int64_t op = __shfl_down_sync(0xFFFFFFFFu, s_pairs, d);
+                const float o = __shfl_down_sync(0xFFFFFFFFu, s, d), oe = __shfl_up_sync(0xFFFFFFFFu, s_e, d);
                 if (lane + d < 32)
-                    s += o;
+                    s += o, s_pairs += op;
+                if (lane >= d)
+                    s_e += oe;
             }
             const float o = __shfl_down_sync(0xFFFFFFFFu, s, 1), after = lane < 31 ? o : 0.f;
+            const float oe = __shfl_up_sync(0xFFFFFFFFu, s_e, 1), before = lane > 0 ? oe : 0.f;
+            // units of 2^(exponent - 151 - 16)
+            const float unit = exponent >= 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(exponent << 23);
             float sa = 0.f, sb = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                const float gl = i < n ? after + (e ? x[1] : y) : 0.f;
+                float gl = e ? after + x[1] + (before + e_of[0]) : after + (x[0] + x[1]) + before;
+                gl = i < n ? fmaf((float)(s_pairs - (e ? pairs[0] : 0)) * 0x1p-40f, unit, gl) : 0.f;
                 float graw = gl * A;
                 if (p.flags & MCC1D_SOFTPLUS)
                     graw *= sigmoid(sh.raw[i]);
