@@ -10,6 +10,11 @@
 // (their products are exact in fp32) and scaled afterwards. The inverse is that
 // of the 16-wide diagonal blocks by substitution, joined twice:
 // [[A,0],[C,B]]^-1 = [[A',0],[-B' C A',B']].
+//
+// A block has one chunk of one head, three blocks an SM: 2048 tokens of 8 x 16
+// heads of K = 128 take 163 us, where their 280 MB would take 41. The dependent
+// steps of the inverse and the barriers between its parts bound it, which three
+// blocks hide from one another in part.
 #include "delta_common.cuh"
 #include "tensor_core.cuh"
 

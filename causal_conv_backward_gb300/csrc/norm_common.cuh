@@ -203,8 +203,11 @@ __device__ __forceinline__ float inverse_root(float v)
 
 // ------------------------------------------------------------------ which threads
 // Threads for rows of D values: up to 1024 a warp or less, so that sums need
-// shuffles only; above, a block. Rows that cannot be read in 16-byte vectors
-// are read value by value.
+// shuffles only; above, a block. A thread's values past the row's end cost as much
+// as the others, so a shape is taken up to its full width: 2^27 values in rows of
+// 128, 256, 1024, 2048 and 4096 take 117 to 136 us in the gated norm so, and 212 to
+// 370 in the next wider shape. Rows that cannot be read in 16-byte vectors are read
+// value by value, 172 to 317 us at these widths.
 template <class F>
 int32_t with_row_shape(int64_t D, bool vectors, F &&f)
 {
@@ -215,24 +218,46 @@ int32_t with_row_shape(int64_t D, bool vectors, F &&f)
             return f(RowShape<8, 1, 16>());
         if (D <= 256)
             return f(RowShape<8, 1, 32>());
+        if (D <= 512)
+            return f(RowShape<8, 2, 32>());
         if (D <= 1024)
             return f(RowShape<8, 4, 32>());
+        if (D <= 1536)
+            return f(RowShape<8, 2, 96>());
         if (D <= 2048)
             return f(RowShape<8, 2, 128>());
+        if (D <= 2560)
+            return f(RowShape<8, 2, 160>());
         if (D <= 4096)
             return f(RowShape<8, 2, 256>());
-        return f(RowShape<8, 4, 512>());
+        if (D <= 8192)
+            return f(RowShape<8, 2, 512>());
+        return f(RowShape<8, 2, 1024>());
     }
+    if (D <= 64)
+        return f(RowShape<1, 2, 32>());
     if (D <= 128)
         return f(RowShape<1, 4, 32>());
+    if (D <= 256)
+        return f(RowShape<1, 8, 32>());
     if (D <= 512)
         return f(RowShape<1, 16, 32>());
+    if (D <= 1024)
+        return f(RowShape<1, 16, 64>());
     if (D <= 2048)
         return f(RowShape<1, 16, 128>());
-    return f(RowShape<1, 32, 512>());
+    if (D <= 4096)
+        return f(RowShape<1, 16, 256>());
+    if (D <= 8192)
+        return f(RowShape<1, 16, 512>());
+    return f(RowShape<1, 16, 1024>());
 }
 
-// The backwards hold sums and the next row too: half as many values to a thread.
+// The backwards hold sums and the next row too: half as many values to a thread
+// (rows of 2048 of the residual norm, 193 us with sixteen to a thread, 147 with
+// eight), up to 4096. Above, sixteen with the sums in shared memory: 2^27 values in
+// rows of 8192 take 302 us in the gated and 403 in the residual norm's gradients,
+// 1054 and 976 with sums and next row in registers, which overflow.
 template <class F>
 int32_t with_row_shape_bwd(int64_t D, bool vectors, F &&f)
 {
@@ -243,20 +268,36 @@ int32_t with_row_shape_bwd(int64_t D, bool vectors, F &&f)
             return f(RowShape<8, 1, 16>());
         if (D <= 256)
             return f(RowShape<8, 1, 32>());
+        if (D <= 512)
+            return f(RowShape<8, 1, 64>());
         if (D <= 1024)
             return f(RowShape<8, 1, 128>());
+        if (D <= 1536)
+            return f(RowShape<8, 1, 192>());
         if (D <= 2048)
             return f(RowShape<8, 1, 256>());
         if (D <= 4096)
             return f(RowShape<8, 1, 512>());
+        if (D <= 8192)
+            return f(RowShape<8, 2, 512>());
         return f(RowShape<8, 2, 1024>());
     }
+    if (D <= 64)
+        return f(RowShape<1, 2, 32>());
     if (D <= 128)
         return f(RowShape<1, 4, 32>());
+    if (D <= 256)
+        return f(RowShape<1, 8, 32>());
+    if (D <= 512)
+        return f(RowShape<1, 8, 64>());
     if (D <= 1024)
         return f(RowShape<1, 8, 128>());
+    if (D <= 2048)
+        return f(RowShape<1, 8, 256>());
     if (D <= 4096)
         return f(RowShape<1, 8, 512>());
+    if (D <= 8192)
+        return f(RowShape<1, 16, 512>());
     return f(RowShape<1, 16, 1024>());
 }
 
@@ -268,6 +309,55 @@ inline bool vectors_for(int64_t D, uintptr_t addresses, int64_t steps)
 }
 
 // ------------------------------------------------------------------ sums over rows
+// N sums of each of a thread's values over its rows: in registers, or, where the
+// rows are so long that these are needed for a row, in shared memory. Then the
+// next row is not asked for ahead either.
+template <class R, int N>
+struct Totals {
+    static constexpr bool HELD = R::E <= 8;
+    static constexpr int BYTES = HELD ? 0 : N * R::E * R::TPR * 4;
+    float held[N][HELD ? R::E : 2];
+    float2 *at;
+
+    __device__ __forceinline__ explicit Totals(uint8_t *shared) : at(reinterpret_cast<float2 *>(shared) + thread_of_row<R>())
+    {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int e = 0; e < R::E; e += 2)
+                if constexpr (HELD)
+                    put(held[k], e, make_float2(0.f, 0.f));
+                else
+                    at[(k * R::E + e) / 2 * R::TPR] = make_float2(0.f, 0.f);
+    }
+    __device__ __forceinline__ void add(int k, int e, float2 a, float2 b)
+    {
+        if constexpr (HELD) {
+            put(held[k], e, fma2(a, b, pair(held[k], e)));
+        } else {
+            float2 &x = at[(k * R::E + e) / 2 * R::TPR];
+            x = fma2(a, b, x);
+        }
+    }
+    __device__ __forceinline__ void get(int k, float (&x)[R::E]) const
+    {
+#pragma unroll
+        for (int e = 0; e < R::E; e += 2)
+            if constexpr (HELD)
+                put(x, e, pair(held[k], e));
+            else
+                put(x, e, at[(k * R::E + e) / 2 * R::TPR]);
+    }
+};
+template <class R, int N, class K, class P>
+int32_t launch_totals(K kernel, int64_t blocks, cudaStream_t stream, const P &p)
+{
+    constexpr int bytes = Totals<R, N>::BYTES;
+    if (bytes > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return kErrCuda;
+    return launch(kernel, dim3((unsigned)blocks), R::THREADS, bytes, stream, p);
+}
+
 // Each thread's sums over its rows, joined over the block's rows of threads and
 // written to part [blocks][D]: one barrier per use of `shared`.
 template <class R>

@@ -61,12 +61,12 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
 {
     __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
+    extern __shared__ uint8_t sums[];
     int turn = 0;
-    float w[R::E], gw[R::E];
+    float w[R::E];
     load_values<DT, R>(p.weight, 0, p.D, w);
-#pragma unroll
-    for (int e = 0; e < R::E; ++e)
-        gw[e] = 0.f;
+    typedef Totals<R, 1> Sums;
+    Sums gw(sums);
     // rows one ahead of their use
     Share<DT, R> xn, gn, zn;
     const auto ask = [&](uint32_t first) {
@@ -77,13 +77,16 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
             zn = load_share<DT, R>(p.z, p.order.at(p.zs, at), p.D);
     };
     const uint32_t step = gridDim.x * R::ROWS;
-    ask(blockIdx.x * R::ROWS);
+    if (Sums::HELD)
+        ask(blockIdx.x * R::ROWS);
     for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += step) {
         const uint32_t row = first + threadIdx.x / R::TPR;
         const bool there = row < p.rows;
         float x[R::E], g[R::E];
+        if (!Sums::HELD)
+            ask(first);
         const Share<DT, R> xr = xn, gr = gn, zr = zn;
-        if (p.rows - first > step)
+        if (Sums::HELD && p.rows - first > step)
             ask(first + step);
         values<DT, R>(xr, x);
         values<DT, R>(gr, g);
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
 #pragma unroll
             for (int e = 0; e < R::E; e += 2) {
                 const float2 n = mul2(pair(x, e), r);
-                put(gw, e, fma2(pair(g, e), n, pair(gw, e)));
+                gw.add(0, e, pair(g, e), n);
                 put(g, e, mul2(r, fma2(n, make_float2(-along, -along), mul2(pair(g, e), pair(w, e)))));
                 put(x, e, n);
             }
@@ -127,7 +130,8 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 256 ? 768 / R::THREA
             }
         }
     }
-    store_part<R>(gw, p.part, p.D, &joined);
+    gw.get(0, w);
+    store_part<R>(w, p.part, p.D, &joined);
 }
 
 // out[c] = sum of part[p][c]: 32 columns to a block of 8 warps, each warp its
@@ -225,8 +229,8 @@ int32_t launch_gated_norm_bwd(const mcc1d_gated_norm_bwd_args &a, float *workspa
     const int64_t blocks = norm_bwd_blocks(p.rows, a.fwd.D, vec, kGatedThreads);
     const int32_t st = with_row_shape_bwd(a.fwd.D, vec, [&](auto shape) {
         typedef decltype(shape) R;
-        return a.fwd.dtype == 0 ? launch(mcc1d_norm_gated_bwd<0, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p)
-                                : launch(mcc1d_norm_gated_bwd<1, R>, dim3((unsigned)blocks), R::THREADS, 0, stream, p);
+        return a.fwd.dtype == 0 ? launch_totals<R, 1>(mcc1d_norm_gated_bwd<0, R>, blocks, stream, p)
+                                : launch_totals<R, 1>(mcc1d_norm_gated_bwd<1, R>, blocks, stream, p);
     });
     if (st != kOk)
         return st;

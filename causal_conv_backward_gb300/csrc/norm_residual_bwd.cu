@@ -18,14 +18,13 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
 {
     __shared__ float shared[2][3][32];
     __shared__ float joined[R::ROWS > 1 ? R::ROWS * R::TPR * R::E : 1];
+    extern __shared__ uint8_t sums[];
     int turn = 0;
-    float gw[R::E], gs[R::E], gp[R::E];
     Branch<DT, R> b;
     b.weights(p);
     const auto wr = load_share<DT, R>(p.weight, 0, p.D);
-#pragma unroll
-    for (int e = 0; e < R::E; ++e)
-        gw[e] = gs[e] = gp[e] = 0.f;
+    typedef Totals<R, 3> Sums;      // of weight, post_weight, scale
+    Sums total(sums);
     // rows one ahead of their use
     Share<DT, R> xn, gn;
     Share<RT, R> rn, hn;
@@ -38,14 +37,17 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
             hn = load_share<RT, R>(p.grad_h, p.order.at(p.ghs, at), p.D);
     };
     const uint32_t step = gridDim.x * R::ROWS;
-    ask(blockIdx.x * R::ROWS);
+    if (Sums::HELD)
+        ask(blockIdx.x * R::ROWS);
     for (uint32_t first = blockIdx.x * R::ROWS; first < p.rows; first += step) {
         const uint32_t row = first + threadIdx.x / R::TPR;
         const bool there = row < p.rows;
         float x[R::E], h[R::E], g[R::E], w[R::E];
+        if (!Sums::HELD)
+            ask(first);
         const Share<DT, R> xr = xn, gr = gn;
         const Share<RT, R> rr = rn, hr = hn;
-        if (p.rows - first > step)
+        if (Sums::HELD && p.rows - first > step)
             ask(first + step);
         values<DT, R>(xr, x);
         values<RT, R>(rr, h);
@@ -65,7 +67,7 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
 #pragma unroll
         for (int e = 0; e < R::E; e += 2) {
             const float2 n = mul2(pair(h, e), make_float2(rh, rh));
-            put(gw, e, fma2(mul2(pair(g, e), make_float2(in, in)), n, pair(gw, e)));
+            total.add(0, e, mul2(pair(g, e), make_float2(in, in)), n);
             put(g, e, mul2(make_float2(rh, rh), fma2(n, make_float2(-along, -along), mul2(pair(g, e), pair(w, e)))));
         }
         if (p.grad_h) {
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
             values<2, R>(b.s, f);
 #pragma unroll
             for (int e = 0; e < R::E; e += 2) {
-                put(gs, e, fma2(mul2(pair(g, e), make_float2(in, in)), pair(m, e), pair(gs, e)));
+                total.add(2, e, mul2(pair(g, e), make_float2(in, in)), pair(m, e));
                 put(g, e, mul2(pair(g, e), pair(f, e)));
             }
         }
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
 #pragma unroll
             for (int e = 0; e < R::E; e += 2) {
                 put(x, e, mul2(pair(x, e), make_float2(b.r, b.r)));
-                put(gp, e, fma2(mul2(pair(g, e), make_float2(in, in)), pair(x, e), pair(gp, e)));
+                total.add(1, e, mul2(pair(g, e), make_float2(in, in)), pair(x, e));
                 put(g, e, mul2(pair(g, e), pair(pw, e)));
                 t2 = fma2(pair(g, e), pair(x, e), t2);
             }
@@ -108,11 +110,14 @@ __global__ void __launch_bounds__(R::THREADS, R::THREADS <= 512 ? 512 / R::THREA
         if (there)
             store_values<DT, R>(p.grad_x, (int64_t)row * p.D, p.D, g);
     }
-    store_part<R>(gw, p.part, p.D, &joined);
-    if (p.part_post)
-        store_part<R>(gp, p.part_post, p.D, &joined);
-    if (p.part_scale)
-        store_part<R>(gs, p.part_scale, p.D, &joined);
+    float *const parts[3] = {p.part, p.part_post, p.part_scale};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (parts[k]) {
+            float x[R::E];
+            total.get(k, x);
+            store_part<R>(x, parts[k], p.D, &joined);
+        }
 }
 
 }  // namespace
@@ -137,7 +142,7 @@ int32_t launch_residual_norm_bwd(const mcc1d_residual_norm_bwd_args &a, float *w
     p.part_scale = a.grad_scale ? workspace + 2 * blocks * f.H : nullptr;
     const int32_t st = with_row_shape_bwd(f.H, vec, [&](auto shape) {
         typedef decltype(shape) R;
-        const auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)blocks), R::THREADS, 0, stream, p); };
+        const auto go = [&](auto kernel) { return launch_totals<R, 3>(kernel, blocks, stream, p); };
         if (f.flags & MCC1D_WIDE)
             return f.dtype == 0 ? go(mcc1d_norm_residual_bwd<0, 2, R>) : go(mcc1d_norm_residual_bwd<1, 2, R>);
         return f.dtype == 0 ? go(mcc1d_norm_residual_bwd<0, 0, R>) : go(mcc1d_norm_residual_bwd<1, 1, R>);
