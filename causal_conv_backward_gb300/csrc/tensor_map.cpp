@@ -1,4 +1,4 @@
-// tensor_map.cpp - the driver's encoder of tile descriptors.
+// tensor_map.cpp - tile descriptors by the encoder that libcuda exports.
 #include "tensor_map.h"
 
 #include <cuda_runtime_api.h>

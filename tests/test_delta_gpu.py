@@ -305,3 +305,13 @@ def test_repeated_keys():
     loss = (ry * to64(gy)).sum() + (rf * to64(gf)).sum()
     for k, want in zip(got._fields, torch.autograd.grad(loss, [leaves[k] for k in got._fields])):
         check(getattr(got, k), want, S * 64, k)
+
+
+@pytest.mark.parametrize("S", [1, 17, 64, 100, 300])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 72)])
+def test_pairs_behind_a_token_cancel(S, K, V):
+    """The first token's decay multiplies an empty state: its gradient is a sum
+    of terms that cancel, all of the first chunk's pairs, and is zero exactly."""
+    t, _, gy, _ = inputs(S, 2, 4, 2, K, V, what="db")
+    g = m.gated_delta_backward(gy, **t, **FORMS)
+    assert g.delta[0].count_nonzero() == 0 and (S == 1 or g.delta[1:].count_nonzero() > 0)
