@@ -324,7 +324,9 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
 }
 
 // ------------------------------------------------------------------ products
-// One thread's. `y`: those of Y too.
+// One thread's, second terms first. Each of them is added with its last bits cut
+// off, towards zero, so the fewer to a sum of full size the better: with first and
+// second terms in turn states were 2e-7 too small. `y`: those of Y too.
 template <int KP>
 __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, int64_t chunks, bool y)
 {
@@ -334,20 +336,21 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, 
     const auto wait = [](uint64_t &bar, uint32_t parity) { return mbar_wait_bounded_inline(smem_u32(&bar), parity); };
     const auto with_state = [&](uint32_t d, uint32_t panels) {
 #pragma unroll
-        for (int j = 0; j < KP / 16; ++j) {
-            const uint64_t k = desc_rows(panels + (j / 4) * 2 * kPanelBytes) + 2 * (j % 4);
-            mma_ts(tmem + d, tmem + kSHi + 8 * j, k, by_rows, j > 0);
-            mma_ts(tmem + d, tmem + kSLo + 8 * j, k, by_rows, true);
-        }
+        for (int j = 0; j < KP / 16; ++j)
+            mma_ts(tmem + d, tmem + kSLo + 8 * j, desc_rows(panels + (j / 4) * 2 * kPanelBytes) + 2 * (j % 4), by_rows, j > 0);
+#pragma unroll
+        for (int j = 0; j < KP / 16; ++j)
+            mma_ts(tmem + d, tmem + kSHi + 8 * j, desc_rows(panels + (j / 4) * 2 * kPanelBytes) + 2 * (j % 4), by_rows, true);
     };
     const auto with_r = [&](uint32_t d, uint32_t panels) {
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t hi = desc_rows(panels) + 2 * j, lo = desc_rows(panels + (kPanelTLo - kPanelT) * kPanelBytes) + 2 * j;
-            mma_ts(tmem + d, tmem + kWHi + 8 * j, hi, by_rows, j > 0);
-            mma_ts(tmem + d, tmem + kWHi + 8 * j, lo, by_rows, true);
-            mma_ts(tmem + d, tmem + kWLo + 8 * j, hi, by_rows, true);
+            mma_ts(tmem + d, tmem + kWHi + 8 * j, desc_rows(panels + (kPanelTLo - kPanelT) * kPanelBytes) + 2 * j, by_rows, j > 0);
+            mma_ts(tmem + d, tmem + kWLo + 8 * j, desc_rows(panels) + 2 * j, by_rows, true);
         }
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + d, tmem + kWHi + 8 * j, desc_rows(panels) + 2 * j, by_rows, true);
     };
     for (int64_t i = 0; i < chunks; ++i) {
         const uint32_t parity = (uint32_t)(i & 1), tile = tiles + (uint32_t)(i % kTiles) * Tl::kBytes;
@@ -375,12 +378,13 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, 
         if (!wait(sh.v, parity))
             break;
         tmem_fence_after();
+        const uint64_t k = desc_columns(tile + Tl::K, 2 * kPanelBytes);
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t k = desc_columns(tile + Tl::K, 2 * kPanelBytes) + (uint64_t)(2048 * j >> 4);
-            mma_ts(tmem + kUpdate, tmem + kVHi + 8 * j, k, by_columns, j > 0);
-            mma_ts(tmem + kUpdate, tmem + kVLo + 8 * j, k, by_columns, true);
-        }
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + kUpdate, tmem + kVLo + 8 * j, k + (uint64_t)(2048 * j >> 4), by_columns, j > 0);
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + kUpdate, tmem + kVHi + 8 * j, k + (uint64_t)(2048 * j >> 4), by_columns, true);
         mma_commit(smem_u32(&sh.end));
         mma_commit(smem_u32(&sh.tile_free[i % kTiles]));
         mma_commit(smem_u32(&sh.prepared_free[i % kPrepareds]));

@@ -271,6 +271,7 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
 }
 
 // ------------------------------------------------------------------ products
+// Second terms first, as in delta_chunks.cu.
 template <int KP>
 __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, int64_t chunks, bool out)
 {
@@ -285,45 +286,47 @@ __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, 
             break;
         tmem_fence_after();
 #pragma unroll
-        for (int j = 0; j < KP / 16; ++j) {
-            const uint64_t k = desc_rows(stage + St::K + (j / 4) * kPanelBytes) + 2 * (j % 4);
-            mma_ts(tmem + kX, tmem + kGHi + 8 * j, k, by_rows, j > 0);
-            mma_ts(tmem + kX, tmem + kGLo + 8 * j, k, by_rows, true);
-        }
-        mma_commit(smem_u32(&sh.x));
+        for (int j = 0; j < KP / 16; ++j)
+            mma_ts(tmem + kX, tmem + kGLo + 8 * j, desc_rows(stage + St::K + (j / 4) * kPanelBytes) + 2 * (j % 4), by_rows, j > 0);
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t step = (uint64_t)(2048 * j >> 4), y = desc_columns(stage + St::Y, kPanelBytes) + step;
-            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + kPanelPT * kPanelBytes, kPanelBytes) + step, y_tokens, j > 0);
-            mma_ss(tmem + kYP, y, desc_columns(stage + St::kPrepared + kPanelPTLo * kPanelBytes, kPanelBytes) + step, y_tokens, true);
-        }
+        for (int j = 0; j < KP / 16; ++j)
+            mma_ts(tmem + kX, tmem + kGHi + 8 * j, desc_rows(stage + St::K + (j / 4) * kPanelBytes) + 2 * (j % 4), by_rows, true);
+        mma_commit(smem_u32(&sh.x));
+        constexpr uint64_t step = 2048 >> 4;                // sixteen rows
+        const uint64_t y = desc_columns(stage + St::Y, kPanelBytes);
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kPanelPTLo * kPanelBytes, kPanelBytes) + step * j, y_tokens, j > 0);
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kPanelPT * kPanelBytes, kPanelBytes) + step * j, y_tokens, true);
         if (!wait(sh.r, parity))
             break;
         tmem_fence_after();
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t step = (uint64_t)(2048 * j >> 4), hi = desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step;
-            const uint64_t lo = desc_columns(stage + St::kPrepared + kPanelTLo * kPanelBytes, kPanelBytes) + step;
-            mma_ts(tmem + kU, tmem + kWHi + 8 * j, hi, tokens_by_columns, j > 0);
-            mma_ts(tmem + kU, tmem + kWHi + 8 * j, lo, tokens_by_columns, true);
-            mma_ts(tmem + kU, tmem + kWLo + 8 * j, hi, tokens_by_columns, true);
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kPanelTLo * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, j > 0);
+            mma_ts(tmem + kU, tmem + kWLo + 8 * j, desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, true);
         }
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, true);
         mma_commit(smem_u32(&sh.u));
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t step = (uint64_t)(2048 * j >> 4), y = desc_columns(stage + St::Y, kPanelBytes) + step;
-            mma_ss(tmem + kYQ, y, desc_columns(stage + St::QHi, kPanelBytes) + step, y_keys, j > 0);
-            mma_ss(tmem + kYQ, y, desc_columns(stage + St::QLo, kPanelBytes) + step, y_keys, true);
-        }
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ss(tmem + kYQ, y + step * j, desc_columns(stage + St::QLo, kPanelBytes) + step * j, y_keys, j > 0);
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ss(tmem + kYQ, y + step * j, desc_columns(stage + St::QHi, kPanelBytes) + step * j, y_keys, true);
         if (!wait(sh.v, parity) || (out && !wait(sh.out, parity)))
             break;
         tmem_fence_after();
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j) {
-            const uint64_t k = desc_columns(stage + St::K, kPanelBytes) + (uint64_t)(2048 * j >> 4);
-            mma_ts(tmem + kX, tmem + kWHi + 8 * j, k, by_columns, j > 0);
-            mma_ts(tmem + kX, tmem + kWLo + 8 * j, k, by_columns, true);
-        }
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + kX, tmem + kWLo + 8 * j, desc_columns(stage + St::K, kPanelBytes) + step * j, by_columns, j > 0);
+#pragma unroll
+        for (int j = 0; j < kC / 16; ++j)
+            mma_ts(tmem + kX, tmem + kWHi + 8 * j, desc_columns(stage + St::K, kPanelBytes) + step * j, by_columns, true);
         mma_commit(smem_u32(&sh.end));
         mma_commit(smem_u32(&sh.empty[i % kStages]));
     }

@@ -187,15 +187,17 @@ __device__ __forceinline__ int counted(float x, uint32_t e) { return e >= 255 ? 
 __device__ __forceinline__ int64_t of_warp(int sum, uint32_t e, uint32_t most) { return ((int64_t)sum << 16) >> min(most - e, 63u); }
 
 // Adds A B^T, all of two terms but A's second times B's second, over 64 values
-// of the sum, by one thread.
+// of the sum, by one thread; second terms first, as in delta_chunks.cu.
 __device__ __forceinline__ void three_products(uint32_t d, uint32_t a, uint32_t a_lo, uint32_t b, uint32_t b_lo, uint32_t kind)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         mma_ss(d, desc_rows(a) + 2 * j, desc_rows(b_lo) + 2 * j, kind, j > 0);
         mma_ss(d, desc_rows(a_lo) + 2 * j, desc_rows(b) + 2 * j, kind, true);
-        mma_ss(d, desc_rows(a) + 2 * j, desc_rows(b) + 2 * j, kind, true);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        mma_ss(d, desc_rows(a) + 2 * j, desc_rows(b) + 2 * j, kind, true);
 }
 
 template <int DT, int KP>
@@ -535,17 +537,17 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             if (tid == 0) {
                 const uint32_t qk = at_panels + Pn::QK;
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t step = (uint64_t)(2048 * j >> 4);
-                    const uint64_t q = desc_columns(qk, Pn::kQK) + step, k = desc_columns(qk + kPanelBytes, Pn::kQK) + step;
-                    mma_ss(tmem + kDG, desc_rows(at_panels + Pn::XLo) + 2 * j, k, keys_by_columns, j > 0);
-                    mma_ss(tmem + kDG, desc_rows(at_panels + Pn::X) + 2 * j, k, keys_by_columns, true);
-                    // 128 columns to the product, of the panel before too: the second half's rows are read
-                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::PCLo - kPanelBytes, kPanelBytes) + step, q, both_by_columns, j > 0);
-                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::LCLo - kPanelBytes, kPanelBytes) + step, k, both_by_columns, true);
-                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::PC - kPanelBytes, kPanelBytes) + step, q, both_by_columns, true);
-                    mma_ss(tmem + kDS, desc_columns(at_panels + Pn::LC - kPanelBytes, kPanelBytes) + step, k, both_by_columns, true);
-                }
+                for (int lo = 1; lo >= 0; --lo)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j) {
+                        const uint64_t step = (uint64_t)(2048 * j >> 4);
+                        const uint64_t q = desc_columns(qk, Pn::kQK) + step, k = desc_columns(qk + kPanelBytes, Pn::kQK) + step;
+                        const bool add = !lo || j > 0;
+                        mma_ss(tmem + kDG, desc_rows(at_panels + (lo ? Pn::XLo : Pn::X)) + 2 * j, k, keys_by_columns, add);
+                        // 128 columns to the product, of the panel before too: the second half's rows are read
+                        mma_ss(tmem + kDS, desc_columns(at_panels + (lo ? Pn::PCLo : Pn::PC) - kPanelBytes, kPanelBytes) + step, q, both_by_columns, add);
+                        mma_ss(tmem + kDS, desc_columns(at_panels + (lo ? Pn::LCLo : Pn::LC) - kPanelBytes, kPanelBytes) + step, k, both_by_columns, true);
+                    }
                 mma_commit(smem_u32(&sh.done));
             }
             ok = ok && mbar_wait_bounded(smem_u32(&sh.done), parity);
