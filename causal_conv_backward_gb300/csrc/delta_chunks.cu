@@ -16,7 +16,7 @@
 // The chunks of one head follow on one another, X - R - U - S, and bound the
 // kernel: the products' time and the conversions between them, for which a
 // scheduler has four warps of rows: 4096 tokens of 8 x 16 heads of 128 x 128 take
-// 225 us, 3.5 us a chunk; q, k, v, y and the factors would take 1.9 at the
+// 247 us, 3.9 us a chunk; q, k, v, y and the factors would take 1.9 at the
 // copy bandwidth. Y is taken in the gaps and leaves through
 // warps of its own. Warps 0 to 15 hold the rows, 16 to 19 write Y, 20 issues the
 // products, 21 copies the tokens of the chunk after the next, 22 to 27 make
@@ -326,7 +326,7 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
 // ------------------------------------------------------------------ products
 // One thread's, second terms first. Each of them is added with its last bits cut
 // off, towards zero, so the fewer to a sum of full size the better: with first and
-// second terms in turn states were 2e-7 too small. `y`: those of Y too.
+// second terms in turn states were 2e-7 too small (and the kernel took 225 us). `y`: those of Y too.
 template <int KP>
 __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, int64_t chunks, bool y)
 {

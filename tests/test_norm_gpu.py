@@ -194,3 +194,12 @@ def test_same_bits_every_time_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+# both sides of the shapes' widths, with more rows than blocks
+@pytest.mark.parametrize("D", [257, 512, 520, 1025, 1536, 1544, 2560, 4097, 4104, 8191, 8192, 8193, 8200, 16383, 16384])
+def test_many_rows_of_each_shape(D):
+    x, z, w, gy = rand(107, 3, 1, D, seed=1), rand(107, 3, 1, D, seed=2), rand(D, seed=3, add=1), rand(107, 3, 1, D, seed=4)
+    check_gated(x, z, w, gy, EPS)
+    check_residual(*residual_inputs(107, 3, D, BF16, True, "ps"), True)
+    check_residual(*residual_inputs(107, 3, D, FP16, False, ""), False)
