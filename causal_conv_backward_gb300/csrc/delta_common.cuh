@@ -55,6 +55,31 @@ __device__ __forceinline__ Gates gates_of(int flags, bool decays, float delta, f
     return g;
 }
 
+// 2^x for a decay that a state is multiplied by again and again, token after token
+// or chunk after chunk: a bias of its last bit would add up where rounding cancels.
+// ex2.approx is low by 0.6e-8 on average at exponents of -1e-5 to -1e-3, by 2e-8 at
+// -0.01 to -1, so that no shift of the exponent suits both (3000 steps left a state
+// 1.7e-5 too small, with the scan's shift 2.5e-5 too large). This is the exponential
+// series of f ln 2 for the f of -1/2..1/2 beside a whole power, off by 5e-9 at its
+// end, and 1 exactly for x = 0. NaN stays NaN, and what fp32 cannot hold is 0 or
+// infinity.
+__device__ __forceinline__ float decay_of(float x)
+{
+    if (x < -126.f)
+        return 0.f;
+    if (x >= 128.f)
+        return INFINITY;
+    const float n = fminf(rintf(x), 127.f), f = x - n;
+    float r = 1.5252734e-5f;          // (ln 2)^7 / 7!, and so on
+    r = fmaf(r, f, 1.5403530e-4f);
+    r = fmaf(r, f, 1.3333558e-3f);
+    r = fmaf(r, f, 9.6181291e-3f);
+    r = fmaf(r, f, 5.5504109e-2f);
+    r = fmaf(r, f, 2.4022651e-1f);
+    r = fmaf(r, f, 6.9314718e-1f);
+    return fmaf(r, f, 1.f) * __uint_as_float((uint32_t)((int)n + 127) << 23);
+}
+
 // What q or k is multiplied by, from its squared length.
 __device__ __forceinline__ float unit_factor(int flags, float squares)
 {

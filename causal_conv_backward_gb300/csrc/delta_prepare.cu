@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
     }
     __syncthreads();
     if (tid < 8) {
-        const float *e = sh.most_p, of[8] = {ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), e[0], e[1], e[2], e[3],
+        const float *e = sh.most_p, of[8] = {decay_of(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), e[0], e[1], e[2], e[3],
                                              e[4] * (kC * e[5]) * e[6], kC * most_p * e[6], e[7]};
 #pragma unroll
         for (int j = 0; j < 8; ++j)

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) mcc1d_delta_one_token(const _
         }
     }
     const float fq = unit_factor(p.flags, sums[0]) * p.scale, fk = unit_factor(p.flags, sums[1]);
-    const float a = ex2(gate.log2a), kq = sums[2] * fq * fk;
+    const float a = decay_of(gate.log2a), kq = sums[2] * fq * fk;
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
         const int row = row0 + 4 * r;

@@ -63,7 +63,7 @@ __device__ __forceinline__ void stage(const DeltaParams &p, TokenShared<KP> &s, 
                 gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + t * p.delta_s[0] + b * p.delta_s[1] + h) : 0.f,
                                 p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
                                 value<DT>(p.beta + t * p.beta_s[0] + b * p.beta_s[1] + h));
-            s.a[i] = p.delta && live ? ex2(gate.log2a + kDecayShift) : 1.f;
+            s.a[i] = decay_of(gate.log2a);
             s.b[i] = gate.b;
             s.kq[i] = sums[2] * fq * fk;
         }
