@@ -38,15 +38,20 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a);
 // What the products of a chunk need beside q, k and v, for each (b, h, chunk):
 // T and P T as fp16 terms in the panels that the tensor cores read, the factors
 // of its tokens, and in the row kFactorEnd what is one value (delta_prepare.cu).
-constexpr int kPanelBytes = kChunk * 128;
-enum { kPanelT, kPanelPT, kPanelTLo, kPanelPTLo };            // T and P T meet the same rows
+// The forward's: T, factors, and for y P T; behind it the backward's: T, P T, factors.
+constexpr int kPanelBytes = kChunk * 128, kFactorRows = 12, kFactorBytes = kFactorRows * kChunk * 4;
+constexpr int kAtT = 0, kAtTLo = kPanelBytes, kAtFactors = 2 * kPanelBytes, kStatesBytes = kAtFactors + kFactorBytes, kAtPT = kStatesBytes,
+              kAtPTLo = kAtPT + kPanelBytes, kForwardBytes = kAtPTLo + kPanelBytes;
+constexpr int kAtBackT = 0, kAtBackTLo = kPanelBytes, kAtBackPT = 2 * kPanelBytes, kAtBackPTLo = 3 * kPanelBytes, kAtBackFactors = 4 * kPanelBytes,
+              kBackBytes = kAtBackFactors + kFactorBytes;
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
        kFactorT, kFactors };
-// In that row: the chunk's decay; what bounds a row's R (of its v and state), U
+static_assert(kFactors <= kFactorRows && kAtPT % 1024 == 0 && kForwardBytes % 1024 == 0 && kBackBytes % 1024 == 0, "panels on 1024 bytes");
+// In that row: the chunk's decay; what bounds the state's part of a row's R, U
 // (of R), and backwards the state's part of du and of du as an operand, grad_y's
 // part of that; the largest factor of q.
-enum { kEndDecay, kEndOfV, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
-constexpr int kChunkBytes = 4 * kPanelBytes + kFactors * kChunk * 4;
+enum { kEndDecay, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
+constexpr int kBothBytes = kStatesBytes + kBackBytes;        // of a chunk in a backward; kForwardBytes in a forward
 
 struct DeltaPlan {
     bool tokens;                           // token by token, no workspace
@@ -54,10 +59,10 @@ struct DeltaPlan {
     int32_t segments;                      // of the time axis that are taken at once
     uint64_t off_prepared, off_states, off_turns, bytes;
 };
-DeltaPlan delta_plan(const mcc1d_delta_args &a);
+DeltaPlan delta_plan(const mcc1d_delta_args &a, bool back);       // back: of a backward's forward
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream);
-int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream);
+int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, bool back, cudaStream_t stream);
 int32_t launch_delta_chunks_bwd(const mcc1d_delta_bwd_args &a, const DeltaPlan &plan, const uint8_t *forward, float *grads, const DeltaKept &kept,
                                 cudaStream_t stream);
 int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, uint8_t *workspace, const DeltaKept &kept, cudaStream_t stream);

@@ -121,7 +121,7 @@ extern "C" int32_t mcc1d_delta_workspace_size(const mcc1d_delta_args *a, uint64_
         return kErrNull;
     const int32_t st = check(a, true);
     if (st == kOk)
-        *bytes_out = delta_plan(*a).bytes;
+        *bytes_out = delta_plan(*a, false).bytes;
     return st;
 }
 
@@ -130,7 +130,7 @@ extern "C" int32_t mcc1d_delta(const mcc1d_delta_args *a, void *workspace, uint6
     int32_t st = check(a, true);
     if (st != kOk)
         return st;
-    const uint64_t bytes = delta_plan(*a).bytes;
+    const uint64_t bytes = delta_plan(*a, false).bytes;
     st = check_workspace(workspace, workspace_bytes, bytes);
     if (st == kOk)
         st = check_apart(*a, workspace, bytes);

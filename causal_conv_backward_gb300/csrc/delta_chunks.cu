@@ -8,7 +8,8 @@
 //   X = S K^T        R = b V - e^c X          (A: the state, from tensor memory)
 //   U = R T^T        Y = e^c S Q^T + R (PT)^T
 //   S = e^c(end) S + (U e^(c(end)-c)) K
-// with tokens along the columns. Operands in tensor memory are two fp16 terms of
+// with tokens along the columns; R is taken without each token's growth, which T's
+// and P T's columns put back (growth_of in delta_prepare.cu). Operands in tensor memory are two fp16 terms of
 // fp32 rows scaled by a power of two, 22 bits; K and Q are exact in fp16 (rows
 // scaled by a power of two), so those products take two terms and those
 // with T and P T three. Sums are fp32.
@@ -38,6 +39,7 @@ struct ChunkParams {
     CUtensorMap map_q, map_k, map_v;    // where rows can be copied as tiles
     DeltaParams d;
     const uint8_t *prepared;
+    int32_t record;           // bytes of a chunk's there
     int64_t chunks;
     int32_t tiles;            // of 128 rows of V
     bool vectors_q, vectors_k, vectors_v, vectors_s;
@@ -53,7 +55,7 @@ struct Tile {
     static constexpr int K = 0, Q = kPanelBytes, V = 2 * kPanels, kBytes = V + kRows / 64 * kPanelBytes;
     static constexpr int kAll = kTiles * kBytes;
 };
-constexpr int kPreparedBytes = (kChunkBytes + 1023) / 1024 * 1024;
+constexpr int kPreparedBytes = kForwardBytes;
 
 // Columns of tensor memory: sums, then operands (pairs of fp16). The state's
 // update is summed over X and U.
@@ -156,17 +158,17 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
         if (i >= chunks)
             break;
         const uint8_t *prepared = tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes;
-        const float *f = reinterpret_cast<const float *>(prepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
+        const float *f = reinterpret_cast<const float *>(prepared + kAtFactors), *ends = f + kFactorEnd * kC;
         const uint16_t *v = reinterpret_cast<const uint16_t *>(tiles + (i % kTiles) * Tl::kBytes + Tl::V + (r / 64) * kPanelBytes) + part * HC * 64 + r % 64;
         f += part * HC;
         // the products wait for the chunk's tiles too, but this thread reads some itself
         ok = warp_wait(sh.full[i % kTiles], (uint32_t)(i / kTiles) & 1);
-        float most_v = 0.f;
+        float most_v = 0.f;          // as R has them
         uint32_t pairs[HC / 2];      // of tokens
 #pragma unroll
         for (int t = 0; t < HC; t += 2) {
             pairs[t / 2] = v[t * 64] | (uint32_t)v[(t + 1) * 64] << 16;
-            const float2 x = unpack2<DT>(pairs[t / 2]);
+            const float2 x = mul2(*reinterpret_cast<const float2 *>(f + kFactorB * kC + t), unpack2<DT>(pairs[t / 2]));
             most_v = fmaxf(most_v, fmaxf(fabsf(x.x), fabsf(x.y)));
         }
         sh.most[part][r] = most_of(s);
@@ -178,8 +180,9 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
             continue;
         }
         const float of_s = inverse_scale(scale_s), most_s = most_of_parts(sh.most, r) * of_s;
-        const float bound_r = fmaf(ends[kEndOfV], most_of_parts(sh.most_v, r), ends[kEndOfState] * most_s);
-        const float scale_r = scale_for(bound_r), of_r = inverse_scale(scale_r);
+        const float bound_r = fmaf(ends[kEndOfState], most_s, most_of_parts(sh.most_v, r));
+        // times b 2^17 at most, and still a number; rows below 2^-86 are held to 2^-126 so
+        const float scale_r = fminf(scale_for(bound_r), 0x1p100f), of_r = inverse_scale(scale_r);
         const float scale_u = scale_for(bound_r * ends[kEndOfR]), of_u = inverse_scale(scale_u), end = ends[kEndDecay];
         if (part == 0)
             sh.of_r[parity][r] = of_r;
@@ -342,10 +345,10 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, 
         for (int j = 0; j < KP / 16; ++j)
             mma_ts(tmem + d, tmem + kSHi + 8 * j, desc_rows(panels + (j / 4) * 2 * kPanelBytes) + 2 * (j % 4), by_rows, true);
     };
-    const auto with_r = [&](uint32_t d, uint32_t panels) {
+    const auto with_r = [&](uint32_t d, uint32_t panels) {        // first terms, second ones behind them
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            mma_ts(tmem + d, tmem + kWHi + 8 * j, desc_rows(panels + (kPanelTLo - kPanelT) * kPanelBytes) + 2 * j, by_rows, j > 0);
+            mma_ts(tmem + d, tmem + kWHi + 8 * j, desc_rows(panels + kPanelBytes) + 2 * j, by_rows, j > 0);
             mma_ts(tmem + d, tmem + kWLo + 8 * j, desc_rows(panels) + 2 * j, by_rows, true);
         }
 #pragma unroll
@@ -369,10 +372,10 @@ __device__ __forceinline__ void issue_products(ChunkShared &sh, uint32_t tiles, 
         if (!wait(sh.r, parity))
             break;
         tmem_fence_after();
-        with_r(kU, prepared + kPanelT * kPanelBytes);
+        with_r(kU, prepared + kAtT);
         mma_commit(smem_u32(&sh.u));
         if (y) {
-            with_r(kPR, prepared + kPanelPT * kPanelBytes);
+            with_r(kPR, prepared + kAtPT);
             mma_commit(smem_u32(&sh.y));
         }
         if (!wait(sh.v, parity))
@@ -428,9 +431,10 @@ __device__ __forceinline__ void copy_tiles(const ChunkParams &cp, ChunkShared &s
             return;
         if (threadIdx.x % 32 == 0) {
             const uint32_t ready = smem_u32(&sh.prepared[i % kPrepareds]);
-            mbar_arrive_expect_tx(ready, kChunkBytes);
-            bulk_g2s(smem_u32(tiles) + Tl::kAll + (uint32_t)(i % kPrepareds) * kPreparedBytes, cp.prepared + (pt.item * cp.chunks + pt.first + i) * kChunkBytes,
-                     kChunkBytes, ready);
+            const uint32_t bytes = p.y ? kForwardBytes : kStatesBytes;
+            mbar_arrive_expect_tx(ready, bytes);
+            bulk_g2s(smem_u32(tiles) + Tl::kAll + (uint32_t)(i % kPrepareds) * kPreparedBytes, cp.prepared + (pt.item * cp.chunks + pt.first + i) * cp.record,
+                     bytes, ready);
         }
         __syncwarp();
     }
@@ -448,7 +452,7 @@ __device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &s
         const int64_t t0 = (pt.first + i) * kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC);
         uint8_t *tile = tiles + (i % kTiles) * Tl::kBytes;
-        const float *f = reinterpret_cast<const float *>(tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes + 4 * kPanelBytes);
+        const float *f = reinterpret_cast<const float *>(tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes + kAtFactors);
         if (!warp_wait(sh.tiles[i % kTiles], (uint32_t)(i / kTiles) & 1) || !warp_wait(sh.prepared[i % kPrepareds], (uint32_t)(i / kPrepareds) & 1))
             break;
         make_panels<DT, KP>(tile + Tl::K, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k, live, thread);
@@ -561,7 +565,7 @@ int32_t delta_segments(int64_t chunks, int64_t heads, int64_t tiles)
 // Prompts of less than half a chunk go token by token. 8 sequences of 16 heads of
 // 128 x 128 take 18 us so and 36 in a chunk at 16 tokens, 32 and 36 at 31, 47 and
 // 36 at 48; with gradients 58 and 85, 83 and 86, 109 and 87.
-DeltaPlan delta_plan(const mcc1d_delta_args &a)
+DeltaPlan delta_plan(const mcc1d_delta_args &a, bool back)
 {
     DeltaPlan p = {};
     p.chunks = (a.S + kChunk - 1) / kChunk;
@@ -573,7 +577,7 @@ DeltaPlan delta_plan(const mcc1d_delta_args &a)
         p.bytes += (bytes + 255) / 256 * 256;
         return at;
     };
-    p.off_prepared = take((uint64_t)(p.chunks * a.B * a.H) * kChunkBytes);
+    p.off_prepared = take((uint64_t)(p.chunks * a.B * a.H) * (back ? kBothBytes : kForwardBytes));
     p.segments = delta_segments(p.chunks, a.B * a.H, (a.V + kRows - 1) / kRows);
     if (p.segments > 1) {
         const uint64_t joins = (uint64_t)(p.segments - 1) * a.B * a.H * a.K * 4;
@@ -586,7 +590,7 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, ui
 {
     ChunkParams p = {};
     p.d = delta_params(a);
-    p.prepared = workspace + plan.off_prepared;
+    p.prepared = workspace + plan.off_prepared, p.record = kept.u ? kBothBytes : kForwardBytes;
     p.chunks = plan.chunks;
     p.tiles = (int32_t)((a.V + kRows - 1) / kRows);
     p.vectors_q = token_tiles(&p.map_q, a.q, a.S, a.B, a.G, a.K, a.q_strides, true);
@@ -622,11 +626,11 @@ int32_t launch_delta_chunks(const mcc1d_delta_args &a, const DeltaPlan &plan, ui
 
 int32_t launch_delta(const mcc1d_delta_args &a, void *workspace, cudaStream_t stream)
 {
-    const DeltaPlan plan = delta_plan(a);
+    const DeltaPlan plan = delta_plan(a, false);
     if (plan.tokens)
         return launch_delta_tokens(a, DeltaKept(), stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int32_t st = launch_delta_prepare(a, ws + plan.off_prepared, stream);
+    const int32_t st = launch_delta_prepare(a, ws + plan.off_prepared, false, stream);
     return st == kOk ? launch_delta_chunks(a, plan, ws, DeltaKept(), stream) : st;
 }
 

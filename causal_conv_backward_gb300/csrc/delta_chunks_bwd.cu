@@ -41,7 +41,7 @@ template <int KP>
 struct Stage {
     static constexpr int kPanels = KP / 64 * kPanelBytes;
     static constexpr int K = 0, QHi = kPanels, QLo = 2 * kPanels, Y = 3 * kPanels, kPrepared = Y + kRows / 64 * kPanelBytes;
-    static constexpr int kBytes = kPrepared + (kChunkBytes + 1023) / 1024 * 1024;
+    static constexpr int kBytes = kPrepared + kBackBytes;
     static_assert(kBytes % 1024 == 0, "panels on 1024 bytes");
 };
 
@@ -114,7 +114,7 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
             break;
         }
         const uint8_t *stage = stages + (i % kStages) * St::kBytes;
-        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes), *ends = f + kFactorEnd * kC;
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + kAtBackFactors), *ends = f + kFactorEnd * kC;
         f += part * HC;
         ok = warp_wait(sh.full[i % kStages], (uint32_t)(i / kStages) & 1);
         sh.most[part][r] = most_of(s);
@@ -296,21 +296,21 @@ __device__ __forceinline__ void issue_products(BackShared &sh, uint32_t stages, 
         const uint64_t y = desc_columns(stage + St::Y, kPanelBytes);
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j)
-            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kPanelPTLo * kPanelBytes, kPanelBytes) + step * j, y_tokens, j > 0);
+            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kAtBackPTLo, kPanelBytes) + step * j, y_tokens, j > 0);
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j)
-            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kPanelPT * kPanelBytes, kPanelBytes) + step * j, y_tokens, true);
+            mma_ss(tmem + kYP, y + step * j, desc_columns(stage + St::kPrepared + kAtBackPT, kPanelBytes) + step * j, y_tokens, true);
         if (!wait(sh.r, parity))
             break;
         tmem_fence_after();
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j) {
-            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kPanelTLo * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, j > 0);
-            mma_ts(tmem + kU, tmem + kWLo + 8 * j, desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, true);
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kAtBackTLo, kPanelBytes) + step * j, tokens_by_columns, j > 0);
+            mma_ts(tmem + kU, tmem + kWLo + 8 * j, desc_columns(stage + St::kPrepared + kAtBackT, kPanelBytes) + step * j, tokens_by_columns, true);
         }
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j)
-            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kPanelT * kPanelBytes, kPanelBytes) + step * j, tokens_by_columns, true);
+            mma_ts(tmem + kU, tmem + kWHi + 8 * j, desc_columns(stage + St::kPrepared + kAtBackT, kPanelBytes) + step * j, tokens_by_columns, true);
         mma_commit(smem_u32(&sh.u));
 #pragma unroll
         for (int j = 0; j < kC / 16; ++j)
@@ -348,8 +348,8 @@ __device__ __forceinline__ void copy_tiles(const BackParams &cp, BackShared &sh,
             const int64_t chunk = pt.first + chunks - 1 - i;
             const uint32_t stage = smem_u32(stages) + (uint32_t)(i % kStages) * St::kBytes, bar = smem_u32(&sh.tiles[i % kStages]);
             const int t0 = (int)(chunk * kC), values = p.V - v0 > 64 ? 2 : 1;
-            mbar_arrive_expect_tx(bar, kChunkBytes + ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (y ? values : 0)) * kPanelBytes);
-            bulk_g2s(stage + St::kPrepared, cp.prepared + (pt.item * cp.chunks + chunk) * kChunkBytes, kChunkBytes, bar);
+            mbar_arrive_expect_tx(bar, kBackBytes + ((k ? KP / 64 : 0) + (q ? KP / 64 : 0) + (y ? values : 0)) * kPanelBytes);
+            bulk_g2s(stage + St::kPrepared, cp.prepared + (pt.item * cp.chunks + chunk) * kBothBytes + kStatesBytes, kBackBytes, bar);
             for (int j = 0; j < KP / 64; ++j) {
                 if (k)
                     tile_g2s(stage + St::K + j * kPanelBytes, &cp.map_k, 64 * j, t0, g, b, bar);
@@ -385,7 +385,7 @@ __device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh,
         const int64_t t0 = (pt.first + chunks - 1 - i) * kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC);
         uint8_t *stage = stages + (i % kStages) * St::kBytes;
-        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + 4 * kPanelBytes);
+        const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + kAtBackFactors);
         if (!warp_wait(sh.tiles[i % kStages], (uint32_t)(i / kStages) & 1))
             break;
         // grad_y: its largest value first

@@ -712,7 +712,7 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a)
     DeltaBwdPlan p = {};
     p.chunks = (f.S + kChunk - 1) / kChunk;
     p.Vp = (int32_t)((f.V + 3) / 4 * 4);
-    p.tokens = delta_plan(f).tokens;
+    p.tokens = delta_plan(f, true).tokens;
     const auto take = [&](uint64_t bytes) {
         const uint64_t at = p.bytes;
         p.bytes += (bytes + 255) / 256 * 256;
@@ -722,7 +722,7 @@ DeltaBwdPlan delta_bwd_plan(const mcc1d_delta_bwd_args &a)
     p.off_u = take(4 * tokens), p.off_du = take(4 * tokens);
     p.off_s = take(4 * states), p.off_g = take(4 * states);
     p.off_sums = take(4 * (uint64_t)(2 * p.chunks * f.B * f.H));
-    const DeltaPlan forward = delta_plan(f);
+    const DeltaPlan forward = delta_plan(f, true);
     p.off_forward = take(forward.bytes);
     p.off_grads = take(4 * (uint64_t)(forward.segments > 1 ? forward.segments - 1 : 0) * (uint64_t)(f.B * f.H * f.V * f.K));
     return p;
@@ -743,8 +743,8 @@ int32_t launch_delta_bwd(const mcc1d_delta_bwd_args &a, void *workspace, cudaStr
         if (st == kOk)
             st = launch_delta_tokens_bwd(a, back, stream);
     } else {
-        const DeltaPlan forward = delta_plan(f);
-        st = launch_delta_prepare(in, ws + plan.off_forward + forward.off_prepared, stream);
+        const DeltaPlan forward = delta_plan(f, true);
+        st = launch_delta_prepare(in, ws + plan.off_forward + forward.off_prepared, true, stream);
         if (st == kOk)
             st = launch_delta_chunks(in, forward, ws + plan.off_forward, kept, stream);
         if (st == kOk)

@@ -1,10 +1,13 @@
 // delta_prepare.cu - a chunk's products of tokens with tokens.
 //
 // With c(t) the running sum of log a, D(t,i) = exp(c(t) - c(i)):
-//   L(t,i) = b(t) D (k'(t).k'(i)), i < t;   P(t,i) = D (q'(t).k'(i)), i <= t
-//   T = (I + L)^-1,   so that U = T R for R = b (V - e^c K' S^T),  and P U = (P T) R
-// T and P T leave as two fp16 terms each (22 bits), rows scaled by powers of two,
-// in the layout that delta_chunks.cu multiplies from.
+//   L(t,i) = b(t) (k'(t).k'(i)), i < t;   P(t,i) = q'(t).k'(i), i <= t
+//   T = (I + L)^-1,   so that U = (D T) R for R = b (V - e^c K' S^T),  and the tokens' part
+//   of Y is (D P T) R: each path from i to t passes through the same decays, so that
+//   they multiply the finished matrices, value by value.
+// D T and D P T (T and P T elsewhere) leave as two fp16 terms each (22 bits), rows
+// scaled by powers of two, in the layout that delta_chunks.cu multiplies from, for an
+// R that a token's growth has been taken out of (growth_of).
 //
 // k'.k' and q'.k' are taken of the 16-bit tensors themselves on the tensor cores
 // (their products are exact in fp32) and scaled afterwards. The inverse is that
@@ -43,7 +46,7 @@ struct PrepareShared {
         };
     };
     float L[kC][kRow], P[kC][kRow];
-    float ch[kC], cl[kC], b[kC], f[2][kC], m[2][kC], lk[kC], ends[8][kC], most_p[kThreads / 32];
+    float ch[kC], cl[kC], rest[kC], b[kC], f[2][kC], m[2][kC], lk[kC], ends[7][kC], most_p[kThreads / 32];
     bool zero_q[kC];
 };
 
@@ -116,8 +119,32 @@ __device__ __forceinline__ float most_of_warp(float x)
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
     return x;
 }
+// The largest of a row over its four threads, and the sum of all.
+__device__ __forceinline__ float most_of_row(const float (&x)[16], float &sum)
+{
+    float most = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        most = fmaxf(most, fabsf(x[j])), sum += fabsf(x[j]);
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2)
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d)), sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    return most;
+}
 
-template <int DT, int KP>
+// What is taken out of a token's R and put back by its column of T and P T, as a
+// power of two, from the logarithm c of all decays up to it. Two terms hold a row to
+// 2^-40 of its largest value, and a token's R has two parts, its value and the
+// state's, e^c S k. All of a growth (c > 0), which else only the last tokens would be
+// seen of; half of a decay, up to 2^17, so that where values are small both R, which
+// falls by the other half, and T keep their bits.
+__device__ __forceinline__ float growth_of(float c)
+{
+    return c > 0.f ? fminf(rintf(c), 126.f) : fmaxf(rintf(0.5f * c), -17.f);
+}
+
+template <int DT, int KP, bool BACK>
 __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const __grid_constant__ PrepareParams pp)
 {
     extern __shared__ __align__(16) uint8_t raw_shared[];
@@ -132,8 +159,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         return;
     const int n = (int)(length - t0 < kC ? length - t0 : kC);
     const int64_t item = (int64_t)b * p.H + h;
-    uint8_t *out = pp.out + (item * pp.chunks + chunk) * kChunkBytes;
-    float *factors = reinterpret_cast<float *>(out + 4 * kPanelBytes);
+    uint8_t *out = pp.out + (item * pp.chunks + chunk) * (BACK ? kBothBytes : kForwardBytes);
 
     // rows of q and k, all of a thread's loads in flight together
     constexpr int PIECES = KP / 8, STEP = kThreads / PIECES, N = kC / STEP;
@@ -221,6 +247,8 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         }
     }
     __syncthreads();
+    if (tid < kC)
+        sh.rest[tid] = sh.ch[tid] - growth_of(sh.ch[tid] + sh.cl[tid]);
     {   // 16 rows and 32 columns of both products to a warp
         const int r0 = 16 * (warp % 4), c0 = 32 * (warp / 4), row = lane / 4, col = 2 * (lane % 4);
         float kk[4][4] = {}, qk[4][4] = {};
@@ -246,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = r0 + row + 8 * half;
-            const float th = sh.ch[t], tl = sh.cl[t], lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
+            const float lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (c0 + 8 * j > r0 + 15)          // above the diagonal: read by nothing
@@ -255,9 +283,8 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = c0 + 8 * j + col + e;
-                    const float D = i <= t ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) * sh.f[1][i] : 0.f;
-                    l[e] = i < t ? kk[j][2 * half + e] * (D * lt) : 0.f;
-                    x[e] = i <= t ? qk[j][2 * half + e] * (D * pt) : 0.f;
+                    l[e] = i < t ? kk[j][2 * half + e] * (sh.f[1][i] * lt) : 0.f;
+                    x[e] = i <= t ? qk[j][2 * half + e] * (sh.f[1][i] * pt) : 0.f;
                 }
                 *reinterpret_cast<float2 *>(&sh.L[t][c0 + 8 * j + col]) = make_float2(l[0], l[1]);
                 *reinterpret_cast<float2 *>(&sh.P[t][c0 + 8 * j + col]) = make_float2(x[0], x[1]);
@@ -323,101 +350,133 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                 *reinterpret_cast<float2 *>(&sh.X[r0 + row + 8 * e][8 * (2 * j + warp / 4) + 2 * col]) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
     }
     __syncthreads();
-    // T by rows, P T as a whole scaled to fp16's range; four threads to a row
+    // four threads to a row; the decays come in here
     const int t = tid / 4, part = tid % 4;
-    float xt[16], xp[16], most_t = 0.f, sum_t = 0.f, most_p = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(&sh.T[t][16 * part + j]), w = *reinterpret_cast<const float4 *>(&sh.X[t][16 * part + j]);
-        xt[j] = v.x, xt[j + 1] = v.y, xt[j + 2] = v.z, xt[j + 3] = v.w;
-        xp[j] = w.x, xp[j + 1] = w.y, xp[j + 2] = w.z, xp[j + 3] = w.w;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        if (16 * part + j > t)         // never written
-            xt[j] = 0.f;
-        most_t = fmaxf(most_t, fabsf(xt[j])), sum_t += fabsf(xt[j]);
-        most_p = fmaxf(most_p, fabsf(xp[j]));
-    }
-#pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
-        most_t = fmaxf(most_t, __shfl_xor_sync(0xFFFFFFFFu, most_t, d));
-        sum_t += __shfl_xor_sync(0xFFFFFFFFu, sum_t, d);
-    }
-    most_p = most_of_warp(most_p);
-    if (lane == 0)
-        sh.most_p[warp] = most_p;
-    const float scale_t = scale_for(most_t), of_t = inverse_scale(scale_t);
-    store_terms(xt, scale_t, out + kPanelT * kPanelBytes, out + kPanelTLo * kPanelBytes, t, part);
-    const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
+    const float th = sh.ch[t], tl = sh.cl[t], growth = th - sh.rest[t];
+    const float ec = ex2(fminf(th + tl, 127.f)), el = ex2(fminf((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl), 127.f));
     // a row of zeros adds nothing, and must not lower the others' scale
     const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
     const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
-    const float fx = sh.b[t] * ec * k;
-    __syncthreads();
-    most_p = sh.most_p[0];
+    const float reach = sh.lk[t] * sqrtf((float)p.K);                  // |S k'| <= sqrt(K) |k'| max |S|
+    const auto row_of = [&](const float (*m)[kRow], const float *less, float (&x)[16]) {      // times e^(c(t) - less(i)), zeros behind the diagonal
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w)
-        most_p = fmaxf(most_p, sh.most_p[w]);
-    const float scale_p = scale_for(most_p);
-    store_terms(xp, scale_p, out + kPanelPT * kPanelBytes, out + kPanelPTLo * kPanelBytes, t, part);
-    if (part == 0) {
-        factors[kFactorB * kC + t] = sh.b[t];
-        factors[kFactorX * kC + t] = fx;
-        factors[kFactorU * kC + t] = of_t * el * k;
-        factors[kFactorQ * kC + t] = ec * q;
-        factors[kFactorP * kC + t] = inverse_scale(scale_p);
-        factors[kFactorT * kC + t] = of_t;
-        factors[kFactorScaleK * kC + t] = sh.m[1][t];
-        factors[kFactorScaleQ * kC + t] = sh.m[0][t];
-        float (*ends)[kC] = sh.ends;
-        ends[0][t] = fabsf(sh.b[t]);
-        ends[1][t] = fabsf(sh.b[t]) * ec * sh.lk[t] * sqrtf((float)p.K);      // |S k'| <= sqrt(K) |k'| max |S|
-        ends[2][t] = sum_t * el * fabsf(k);
-        ends[3][t] = el * sh.lk[t] * sqrtf((float)p.K) * of_t;
-        ends[4][t] = el * sh.lk[t] * sqrtf((float)p.K);
-        ends[5][t] = most_t;
-        ends[6][t] = fabsf(fx);
-        ends[7][t] = fabsf(ec * q);
+        for (int j = 0; j < 16; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]);
+            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int i = 16 * part + j;
+            x[j] = i <= t ? x[j] * ex2(fminf((th - less[i]) + (tl - sh.cl[i]), 127.f)) : 0.f;
+        }
+    };
+    float x[16];
+    {
+        // T for rows that their growth has been taken out of, each row scaled
+        row_of(sh.T, sh.rest, x);
+        float sum = 0.f, scale = scale_for(most_of_row(x, sum)), of = inverse_scale(scale);
+        store_terms(x, scale, out + kAtT, out + kAtTLo, t, part);
+        float scale_p = 1.f;
+        if (!BACK) {
+            float unused = 0.f;
+            row_of(sh.X, sh.rest, x);
+            scale_p = scale_for(most_of_row(x, unused));
+            store_terms(x, scale_p, out + kAtPT, out + kAtPTLo, t, part);
+        }
+        if (part == 0) {
+            float *factors = reinterpret_cast<float *>(out + kAtFactors);
+            const float fx = sh.b[t] * ex2(fminf(sh.rest[t] + tl, 127.f)) * k;
+            factors[kFactorB * kC + t] = sh.b[t] * ex2(-growth);
+            factors[kFactorX * kC + t] = fx;
+            factors[kFactorU * kC + t] = of * el * k;
+            factors[kFactorQ * kC + t] = ec * q;
+            factors[kFactorP * kC + t] = inverse_scale(scale_p);
+            factors[kFactorT * kC + t] = of;
+            factors[kFactorScaleK * kC + t] = sh.m[1][t];
+            factors[kFactorScaleQ * kC + t] = sh.m[0][t];
+            sh.ends[0][t] = fabsf(sh.b[t]) * ex2(fminf(sh.rest[t] + tl, 127.f)) * reach;
+            sh.ends[1][t] = sum * el * fabsf(k);
+        }
+    }
+    float most_p = 0.f;
+    if (BACK) {
+        float unused = 0.f;
+        row_of(sh.X, sh.ch, x);
+        most_p = most_of_warp(most_of_row(x, unused));
+        if (lane == 0)
+            sh.most_p[warp] = most_p;
+        __syncthreads();
+        most_p = sh.most_p[0];
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w)
+            most_p = fmaxf(most_p, sh.most_p[w]);
+        const float scale_p = scale_for(most_p);
+        uint8_t *back = out + kStatesBytes;
+        store_terms(x, scale_p, back + kAtBackPT, back + kAtBackPTLo, t, part);
+        row_of(sh.T, sh.ch, x);
+        const float most_t = most_of_row(x, unused), scale = scale_for(most_t), of = inverse_scale(scale);
+        store_terms(x, scale, back + kAtBackT, back + kAtBackTLo, t, part);
+        if (part == 0) {
+            float *factors = reinterpret_cast<float *>(back + kAtBackFactors);
+            const float fx = sh.b[t] * ec * k;
+            factors[kFactorB * kC + t] = sh.b[t];
+            factors[kFactorX * kC + t] = fx;
+            factors[kFactorU * kC + t] = of * el * k;
+            factors[kFactorQ * kC + t] = ec * q;
+            factors[kFactorP * kC + t] = inverse_scale(scale_p);
+            factors[kFactorScaleK * kC + t] = sh.m[1][t];
+            factors[kFactorScaleQ * kC + t] = sh.m[0][t];
+            sh.ends[2][t] = el * reach * of;
+            sh.ends[3][t] = el * reach;
+            sh.ends[4][t] = most_t;
+            sh.ends[5][t] = fabsf(fx);
+            sh.ends[6][t] = fabsf(ec * q);
+        }
     }
     __syncthreads();
-    {
+    if (warp < (BACK ? 7 : 2)) {
         const float most = most_of_warp(fmaxf(sh.ends[warp][lane], sh.ends[warp][lane + 32]));
         if (lane == 0)
             sh.most_p[warp] = most;
     }
     __syncthreads();
-    if (tid < 8) {
-        const float *e = sh.most_p, of[8] = {decay_of(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), e[0], e[1], e[2], e[3],
-                                             e[4] * (kC * e[5]) * e[6], kC * most_p * e[6], e[7]};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (tid == j)
-                factors[kFactorEnd * kC + j] = of[j];
+    if (tid == 0) {
+        const float *e = sh.most_p, decay = decay_of(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
+        float *ends = reinterpret_cast<float *>(out + kAtFactors) + kFactorEnd * kC;
+        ends[kEndDecay] = decay, ends[kEndOfState] = e[0], ends[kEndOfR] = e[1];
+        if (BACK) {
+            ends = reinterpret_cast<float *>(out + kStatesBytes + kAtBackFactors) + kFactorEnd * kC;
+            ends[kEndDecay] = decay, ends[kEndOfGrad] = e[2], ends[kEndDuOfGrad] = e[3] * (kC * e[4]) * e[5], ends[kEndDuOfY] = kC * most_p * e[5];
+            ends[kEndMostQ] = e[6];
+        }
     }
 }
 
-template <int DT, int KP>
+template <int DT, int KP, bool BACK>
 int32_t prepare(const PrepareParams &p, cudaStream_t stream)
 {
     constexpr int bytes = (int)sizeof(PrepareShared<KP>);
-    if (cudaFuncSetAttribute(mcc1d_delta_prepare_chunk<DT, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(mcc1d_delta_prepare_chunk<DT, KP, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return kErrCuda;
-    return launch(mcc1d_delta_prepare_chunk<DT, KP>, dim3((unsigned)(p.chunks * p.d.B * p.d.H)), kThreads, bytes, stream, p);
+    return launch(mcc1d_delta_prepare_chunk<DT, KP, BACK>, dim3((unsigned)(p.chunks * p.d.B * p.d.H)), kThreads, bytes, stream, p);
 }
 
 }  // namespace
 
-int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, cudaStream_t stream)
+int32_t launch_delta_prepare(const mcc1d_delta_args &a, uint8_t *prepared, bool back, cudaStream_t stream)
 {
     PrepareParams p = {};
     p.d = delta_params(a);
     p.out = prepared, p.chunks = (a.S + kChunk - 1) / kChunk;
     p.vectors_q = vectors_for(a.K, (uintptr_t)a.q, a.q_strides[0] | a.q_strides[1] | a.q_strides[2]);
     p.vectors_k = vectors_for(a.K, (uintptr_t)a.k, a.k_strides[0] | a.k_strides[1] | a.k_strides[2]);
-    if (a.dtype == 0)
-        return a.K <= 64 ? prepare<0, 64>(p, stream) : prepare<0, 128>(p, stream);
-    return a.K <= 64 ? prepare<1, 64>(p, stream) : prepare<1, 128>(p, stream);
+    const auto go = [&](auto dt, auto b) {
+        constexpr int DT = decltype(dt)::value;
+        constexpr bool BACK = decltype(b)::value;
+        return a.K <= 64 ? prepare<DT, 64, BACK>(p, stream) : prepare<DT, 128, BACK>(p, stream);
+    };
+    const auto type = [&](auto b) { return a.dtype == 0 ? go(std::integral_constant<int, 0>(), b) : go(std::integral_constant<int, 1>(), b); };
+    return back ? type(std::true_type()) : type(std::false_type());
 }
 
 }  // namespace mcc1d
