@@ -45,11 +45,11 @@ constexpr int kAtT = 0, kAtTLo = kPanelBytes, kAtFactors = 2 * kPanelBytes, kSta
 constexpr int kAtBackT = 0, kAtBackTLo = kPanelBytes, kAtBackPT = 2 * kPanelBytes, kAtBackPTLo = 3 * kPanelBytes, kAtBackFactors = 4 * kPanelBytes,
               kBackBytes = kAtBackFactors + kFactorBytes;
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
-       kFactorT, kFactors };
+       kFactorT, kFactorXY, kFactorY, kFactors };
 static_assert(kFactors <= kFactorRows && kAtPT % 1024 == 0 && kForwardBytes % 1024 == 0 && kBackBytes % 1024 == 0, "panels on 1024 bytes");
 // In that row: the chunk's decay; what bounds the state's part of a row's R, U
-// (of R), and backwards the state's part of du and of du as an operand, grad_y's
-// part of that; the largest factor of q.
+// (of R), and backwards what the state's gradient is multiplied with first, its part
+// and grad_y's of du as an operand; the largest factor of q.
 enum { kEndDecay, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
 constexpr int kBothBytes = kStatesBytes + kBackBytes;        // of a chunk in a backward; kForwardBytes in a forward
 

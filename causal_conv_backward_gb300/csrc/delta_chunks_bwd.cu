@@ -3,11 +3,13 @@
 //
 // A block has up to 128 rows of one head's gradient G [V,K] of the state after
 // the chunk, as delta_chunks.cu has the state. With the factors of
-// delta_prepare.cu, D0 = e^(c(end)-c) G K^T, every chunk is
-//   dU through the later tokens: dR = D0 T + grad_y (P T)    (tokens along the columns)
+// delta_prepare.cu, T without the decays (which G's part passes all of, whatever
+// token it goes through: none of its bits are lost where they are small), every chunk is
+//   D0 = G K^T,  dU through the later tokens: dR = e^(c(end)-c) D0 T + grad_y (P T)    (tokens along the columns)
 //   grad_v = b dR
 //   G = e^c(end) G + grad_y^T (e^c Q) - (dR b e^c) K
-// grad_y is exact in fp16 (a chunk's values scaled by a power of two) and is
+// grad_y is exact in fp16 (a chunk's values scaled by a power of two, rows that grow
+// on their way to the end or fade by another: growth_of in delta_prepare.cu) and is
 // multiplied from shared memory; e^c Q is two fp16 terms there. The chain is
 // G - D0 - dR - G, and bounds the kernel; the products with grad_y run in its gaps.
 // 2048 tokens of 8 x 16 heads of 128 x 128 take 193 us, 6 us a chunk, of which the
@@ -52,8 +54,8 @@ enum { kX = 0, kU = 64, kYP = 128, kYQ = 192, kGHi = 320, kGLo = 384, kWHi = 448
 struct BackShared {
     uint64_t full[kStages], empty[kStages], tiles[kStages], x, r, u, v, s, end, out;
     float of_u[2][kRows];                       // of the last two chunks: what a row's sums are multiplied by
-    float of_out[4][kC], of_p[4];               // of the last four chunks: b, and the factor of grad_y (P T)
-    float of_y[4], of_yq[4], most_y[4];         // grad_y's factor, that of grad_y Q, the largest |grad_y|
+    alignas(8) float of_out[4][3 * kC];                    // of the last four chunks: the factors of G's and of grad_y's part of dR, b
+    float of_y[4], of_q[4], most_y[4];          // grad_y's factor (0 where there is none), Q's, the largest |grad_y|
     float most[kParts][kRows], sum_r[kParts][kRows];
     float most_of_warps[2][kLoadWarps];
     uint32_t tmem, failed;
@@ -124,10 +126,9 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
             i = chunks - 1;
             continue;
         }
-        const float of_s = inverse_scale(scale_s), most_s = most_of_parts(sh.most, r) * of_s, most_y = sh.most_y[i & 3];
+        const float of_s = inverse_scale(scale_s), most_s = most_of_parts(sh.most, r) * of_s;
         const float scale_u = scale_for(ends[kEndOfGrad] * most_s), of_u = inverse_scale(scale_u);
-        const float scale_r = scale_for(fmaf(ends[kEndDuOfGrad], most_s, ends[kEndDuOfY] * most_y)), of_r = inverse_scale(scale_r);
-        const float of_yp = sh.of_y[i & 3] * f[kFactorP * kC], of_yq = sh.of_yq[i & 3], end = ends[kEndDecay];
+        const float scale_r = scale_for(fmaf(ends[kEndDuOfGrad], most_s, ends[kEndDuOfY] * sh.most_y[i & 3])), of_r = inverse_scale(scale_r);
         if (part == 0)
             sh.of_u[parity][r] = of_u;
         ok = ok && warp_wait(sh.x, parity);
@@ -155,12 +156,14 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
             tmem_load(lanes + kU + HC * part, raw);
             tmem_load(lanes + kYP + HC * part, yp);
             tmem_wait(raw), tmem_wait(yp);
-            const float2 mu = make_float2(-of_u * scale_r, -of_u * scale_r), my = make_float2(-of_yp * scale_r, -of_yp * scale_r);
+            const float2 mu = make_float2(-of_u * scale_r, -of_u * scale_r);
+            const float of_y = -sh.of_y[i & 3] * scale_r;
+            const float2 my = make_float2(of_y, of_y);
 #pragma unroll
             for (int t = 0; t < HC; t += 2) {
-                const float2 ft = *reinterpret_cast<const float2 *>(f + kFactorX * kC + t);
-                const float2 a = mul2(ft, fma2(mu, make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])),
-                                               mul2(my, make_float2(__uint_as_float(yp[t]), __uint_as_float(yp[t + 1])))));
+                const float2 fg = *reinterpret_cast<const float2 *>(f + kFactorX * kC + t), fy = *reinterpret_cast<const float2 *>(f + kFactorXY * kC + t);
+                const float2 a = fma2(mul2(fg, mu), make_float2(__uint_as_float(raw[t]), __uint_as_float(raw[t + 1])),
+                                      mul2(mul2(fy, my), make_float2(__uint_as_float(yp[t]), __uint_as_float(yp[t + 1]))));
                 sum = add2(sum, make_float2(fabsf(a.x), fabsf(a.y)));
                 x[t] = a.x, x[t + 1] = a.y;
             }
@@ -168,13 +171,13 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
         sh.sum_r[part][r] = sum.x + sum.y;
         put_terms<HC>(x, terms_w, terms_w + (kWLo - kWHi));
         terms_done(sh.v);
-        warp_arrive(sh.empty[i % kStages]);
         rows_meet();     // for sum_r, while the products run
         // |G| <= e^c(end) |G| + sum of |dR k| + 64 |grad_y| |q|, and no |k|, |q| is above 2^16 as an operand
-        const float before = scale_s;
+        const float before = scale_s, end = ends[kEndDecay], of_q = sh.of_q[i & 3], of_yq = sh.of_y[i & 3] * of_q;
         scale_s = scale_for(fmaf(fabsf(end), most_s, ((sh.sum_r[0][r] + sh.sum_r[1][r]) + (sh.sum_r[2][r] + sh.sum_r[3][r])) * of_r * 65536.f) +
-                            most_y * (kC * 65536.f) * (of_yq / sh.of_y[i & 3]));
+                            sh.most_y[i & 3] * (kC * 65536.f) * of_q);
         const float2 keep = make_float2(end * inverse_scale(before) * scale_s, end * inverse_scale(before) * scale_s);
+        warp_arrive(sh.empty[i % kStages]);
         const float2 add = make_float2(of_r * scale_s, of_r * scale_s), add_y = make_float2(of_yq * scale_s, of_yq * scale_s);
         ok = ok && warp_wait(sh.end, parity);
         tmem_fence_after();
@@ -220,8 +223,8 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
             break;
         tmem_fence_after();
         const int64_t t0 = (pt.first + chunks - 1 - i) * kC;
-        const float of_u = sh.of_u[i & 1][r], of_p = sh.of_p[i & 3];
-        const float *bt = sh.of_out[i & 3];
+        const float of_u = sh.of_u[i & 1][r], of_y = sh.of_y[i & 3];
+        const float *fg = sh.of_out[i & 3], *fy = fg + kC, *bt = fy + kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC), rows = (int)(p.S - t0 < kC ? p.S - t0 : kC);
         const bool whole = cp.pairs_v && rows == kC && live == kC;
         uint32_t dr[4][16];
@@ -232,8 +235,12 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
             tmem_load(lanes + kYP + 16 * c, y);
             tmem_wait(dr[c]), tmem_wait(y);
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-                dr[c][t] = __float_as_uint(fmaf(of_u, __uint_as_float(dr[c][t]), of_p * __uint_as_float(y[t])));
+            for (int t = 0; t < 16; t += 2) {
+                const float2 g = *reinterpret_cast<const float2 *>(fg + 16 * c + t), f = *reinterpret_cast<const float2 *>(fy + 16 * c + t);
+                const float2 a = fma2(mul2(g, make_float2(of_u, of_u)), make_float2(__uint_as_float(dr[c][t]), __uint_as_float(dr[c][t + 1])),
+                                      mul2(mul2(f, make_float2(of_y, of_y)), make_float2(__uint_as_float(y[t]), __uint_as_float(y[t + 1]))));
+                dr[c][t] = __float_as_uint(a.x), dr[c][t + 1] = __float_as_uint(a.y);
+            }
         }
         tmem_fence_before();
         warp_arrive(sh.out);
@@ -247,7 +254,7 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
                     const float a = __uint_as_float(dr[c][t]), e = __uint_as_float(dr[c][t + 1]);
                     if (mine)
                         to_u[0] = a, to_u[step_u] = e;
-                    const uint32_t both = pack2<DT>(make_float2(a * bt[16 * c + t], e * bt[16 * c + t + 1]));
+                    const uint32_t both = pack2<DT>(mul2(make_float2(a, e), *reinterpret_cast<const float2 *>(bt + 16 * c + t)));
                     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, both, 1);
                     if (mine)       // two rows of one token: even lanes the first, odd lanes the second
                         *reinterpret_cast<uint32_t *>(pair) = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
@@ -397,11 +404,10 @@ __device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh,
 #pragma unroll 2
         for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
             uint8_t *at = panel_y + panel_at(t, piece_y % 8);
-            float2 x[4];
-            unpack8<DT>(piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                most = fmaxf(most, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+            // magnitudes are in the order of their bits
+            const uint4 v = piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0);
+            const float2 two = unpack2<DT>(__vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            most = fmaxf(most, fmaxf(two.x, two.y) * f[kFactorY * kC + t]);
         }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
@@ -413,20 +419,19 @@ __device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh,
 #pragma unroll
         for (int w = 1; w < kLoadWarps; ++w)
             most = fmaxf(most, sh.most_of_warps[i & 1][w]);
-        const float scale_y = scale_for(most);
+        const float scale_y = fminf(scale_for(most), 0x1p100f);      // times a token's factor, and still a number
         const float scale_q = scale_for(f[kFactorEnd * kC + kEndMostQ] * 32768.f);       // rows of q are below 2^15 as operands
         if (thread == 0) {
-            sh.of_y[i & 3] = inverse_scale(scale_y), sh.of_yq[i & 3] = inverse_scale(scale_y) * inverse_scale(scale_q), sh.most_y[i & 3] = most;
-            sh.of_p[i & 3] = inverse_scale(scale_y) * f[kFactorP * kC];
+            sh.of_y[i & 3] = most == 0.f ? 0.f : inverse_scale(scale_y), sh.of_q[i & 3] = inverse_scale(scale_q), sh.most_y[i & 3] = most;
         }
-        if (thread < kC)
-            sh.of_out[i & 3][thread] = f[kFactorB * kC + thread];
+        if (thread < 3 * kC)
+            sh.of_out[i & 3][thread] = f[(thread < kC ? kFactorT : thread < 2 * kC ? kFactorP : kFactorB) * kC + thread % kC];
 #pragma unroll 2
         for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
             uint8_t *at = panel_y + panel_at(t, piece_y % 8);
             float2 x[4];
             unpack8<DT>(piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
-            *reinterpret_cast<uint4 *>(at) = scaled_half(x, scale_y);
+            *reinterpret_cast<uint4 *>(at) = scaled_half(x, scale_y * f[kFactorY * kC + t]);
         }
         const int piece = thread % PIECES, live_k = p.K - 8 * piece;
         const uint16_t *k = p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] + 8 * piece, *q = p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2] + 8 * piece;

@@ -46,7 +46,7 @@ struct PrepareShared {
         };
     };
     float L[kC][kRow], P[kC][kRow];
-    float ch[kC], cl[kC], rest[kC], b[kC], f[2][kC], m[2][kC], lk[kC], ends[7][kC], most_p[kThreads / 32];
+    float ch[kC], cl[kC], rest[kC], b[kC], f[2][kC], m[2][kC], lk[kC], late[kC], of_t[kC], sum_t[kC], of_p[kC], ends[4][8];
     bool zero_q[kC];
 };
 
@@ -351,103 +351,142 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
     }
     __syncthreads();
     // four threads to a row; the decays come in here
-    const int t = tid / 4, part = tid % 4;
-    const float th = sh.ch[t], tl = sh.cl[t], growth = th - sh.rest[t];
-    const float ec = ex2(fminf(th + tl, 127.f)), el = ex2(fminf((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl), 127.f));
-    // a row of zeros adds nothing, and must not lower the others' scale
-    const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
-    const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
-    const float reach = sh.lk[t] * sqrtf((float)p.K);                  // |S k'| <= sqrt(K) |k'| max |S|
-    const auto row_of = [&](const float (*m)[kRow], const float *less, float (&x)[16]) {      // times e^(c(t) - less(i)), zeros behind the diagonal
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]);
-            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int i = 16 * part + j;
-            x[j] = i <= t ? x[j] * ex2(fminf((th - less[i]) + (tl - sh.cl[i]), 127.f)) : 0.f;
-        }
-    };
-    float x[16];
     {
-        // T for rows that their growth has been taken out of, each row scaled
-        row_of(sh.T, sh.rest, x);
-        float sum = 0.f, scale = scale_for(most_of_row(x, sum)), of = inverse_scale(scale);
-        store_terms(x, scale, out + kAtT, out + kAtTLo, t, part);
-        float scale_p = 1.f;
-        if (!BACK) {
-            float unused = 0.f;
-            row_of(sh.X, sh.rest, x);
-            scale_p = scale_for(most_of_row(x, unused));
-            store_terms(x, scale_p, out + kAtPT, out + kAtPTLo, t, part);
-        }
-        if (part == 0) {
-            float *factors = reinterpret_cast<float *>(out + kAtFactors);
-            const float fx = sh.b[t] * ex2(fminf(sh.rest[t] + tl, 127.f)) * k;
-            factors[kFactorB * kC + t] = sh.b[t] * ex2(-growth);
-            factors[kFactorX * kC + t] = fx;
-            factors[kFactorU * kC + t] = of * el * k;
-            factors[kFactorQ * kC + t] = ec * q;
-            factors[kFactorP * kC + t] = inverse_scale(scale_p);
-            factors[kFactorT * kC + t] = of;
-            factors[kFactorScaleK * kC + t] = sh.m[1][t];
-            factors[kFactorScaleQ * kC + t] = sh.m[0][t];
-            sh.ends[0][t] = fabsf(sh.b[t]) * ex2(fminf(sh.rest[t] + tl, 127.f)) * reach;
-            sh.ends[1][t] = sum * el * fabsf(k);
-        }
-    }
-    float most_p = 0.f;
-    if (BACK) {
-        float unused = 0.f;
-        row_of(sh.X, sh.ch, x);
-        most_p = most_of_warp(most_of_row(x, unused));
-        if (lane == 0)
-            sh.most_p[warp] = most_p;
-        __syncthreads();
-        most_p = sh.most_p[0];
+        const int t = tid / 4, part = tid % 4;
+        const float th = sh.ch[t], tl = sh.cl[t];
+        float x[16], D[16];
+        const auto row_of = [&](const float (*m)[kRow], const float (&by)[16]) {
 #pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w)
-            most_p = fmaxf(most_p, sh.most_p[w]);
-        const float scale_p = scale_for(most_p);
-        uint8_t *back = out + kStatesBytes;
-        store_terms(x, scale_p, back + kAtBackPT, back + kAtBackPTLo, t, part);
-        row_of(sh.T, sh.ch, x);
-        const float most_t = most_of_row(x, unused), scale = scale_for(most_t), of = inverse_scale(scale);
-        store_terms(x, scale, back + kAtBackT, back + kAtBackTLo, t, part);
-        if (part == 0) {
-            float *factors = reinterpret_cast<float *>(back + kAtBackFactors);
-            const float fx = sh.b[t] * ec * k;
-            factors[kFactorB * kC + t] = sh.b[t];
-            factors[kFactorX * kC + t] = fx;
-            factors[kFactorU * kC + t] = of * el * k;
-            factors[kFactorQ * kC + t] = ec * q;
-            factors[kFactorP * kC + t] = inverse_scale(scale_p);
-            factors[kFactorScaleK * kC + t] = sh.m[1][t];
-            factors[kFactorScaleQ * kC + t] = sh.m[0][t];
-            sh.ends[2][t] = el * reach * of;
-            sh.ends[3][t] = el * reach;
-            sh.ends[4][t] = most_t;
-            sh.ends[5][t] = fabsf(fx);
-            sh.ends[6][t] = fabsf(ec * q);
+            for (int j = 0; j < 16; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]);
+                x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[j] = 16 * part + j <= t ? x[j] * by[j] : 0.f;       // nothing is written behind the diagonal
+        };
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            D[j] = ex2(fminf((th - sh.rest[16 * part + j]) + (tl - sh.cl[16 * part + j]), 127.f));
+        row_of(sh.T, D);
+        float sum, scale = scale_for(most_of_row(x, sum));
+        store_terms(x, scale, out + kAtT, out + kAtTLo, t, part);
+        if (part == 0)
+            sh.of_t[t] = inverse_scale(scale), sh.sum_t[t] = sum;
+        if (!BACK) {
+            row_of(sh.X, D);
+            scale = scale_for(most_of_row(x, sum));
+            store_terms(x, scale, out + kAtPT, out + kAtPTLo, t, part);
+            if (part == 0)
+                sh.of_p[t] = inverse_scale(scale);
         }
     }
-    __syncthreads();
-    if (warp < (BACK ? 7 : 2)) {
-        const float most = most_of_warp(fmaxf(sh.ends[warp][lane], sh.ends[warp][lane + 32]));
-        if (lane == 0)
-            sh.most_p[warp] = most;
+    if (BACK) {
+        // T as it is and P T with the decays behind it; these sum over their rows, so
+        // that each column is scaled. What takes a growth out of grad_y's rows
+        // (from the token to the end) is put into those of P T.
+        float (*most)[kRow] = sh.L, (*scales)[kRow] = sh.L + 8;          // L is not read any more
+        const int i = tid % kC, first = 16 * (tid / kC);
+        if (tid < kC)
+            sh.late[tid] = growth_of((sh.ch[kC - 1] - sh.ch[tid]) + (sh.cl[kC - 1] - sh.cl[tid]));
+        __syncthreads();
+        {
+            float most_t = 0.f, most_p = 0.f;
+            if (first + 15 >= i) {
+                const float ih = sh.ch[i], il = sh.cl[i];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = first + e;
+                    if (j >= i) {
+                        const float v = sh.X[j][i] * ex2(fminf((sh.ch[j] + sh.late[j] - ih) + (sh.cl[j] - il), 127.f));
+                        most_t = fmaxf(most_t, fabsf(sh.T[j][i])), most_p = fmaxf(most_p, fabsf(v));
+                        sh.X[j][i] = v;
+                    }
+                }
+            }
+            most[tid / kC][i] = most_t, most[4 + tid / kC][i] = most_p;
+        }
+        __syncthreads();
+        if (tid < 2 * kC) {
+            const int w = tid / kC;
+            most[4 * w][i] = fmaxf(fmaxf(most[4 * w][i], most[4 * w + 1][i]), fmaxf(most[4 * w + 2][i], most[4 * w + 3][i]));
+            scales[w][i] = scale_for(most[4 * w][i]);
+        }
+        __syncthreads();
+        const int t = tid / 4, part = tid % 4;
+        uint8_t *back = out + kStatesBytes;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const float (*m)[kRow] = w ? sh.X : sh.T;
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]), f = *reinterpret_cast<const float4 *>(&scales[w][16 * part + j]);
+                x[j] = v.x * f.x, x[j + 1] = v.y * f.y, x[j + 2] = v.z * f.z, x[j + 3] = v.w * f.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[j] = 16 * part + j <= t ? x[j] : 0.f;
+            store_terms(x, 1.f, back + (w ? kAtBackPT : kAtBackT), back + (w ? kAtBackPTLo : kAtBackTLo), t, part);
+        }
+    } else {
+        __syncthreads();
+    }
+    // the tokens' factors: two warps the forward's, two the backward's
+    if (warp < (BACK ? 4 : 2)) {
+        const int t = tid % kC;
+        const bool back = warp >= 2;
+        const float th = sh.ch[t], tl = sh.cl[t], b = sh.b[t], end = sh.ch[kC - 1] + sh.cl[kC - 1];
+        const float ec = ex2(fminf(th + tl, 127.f)), el = ex2(fminf((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl), 127.f)), decay = decay_of(fminf(end, 127.f));
+        // a row of zeros adds nothing, and must not lower the others' scale
+        const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
+        const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
+        const float reach = sh.lk[t] * sqrtf((float)p.K);                  // |S k'| <= sqrt(K) |k'| max |S|
+        float *to = reinterpret_cast<float *>(out + (back ? kStatesBytes + kAtBackFactors : kAtFactors)) + t;
+        to[kFactorScaleK * kC] = sh.m[1][t];
+        to[kFactorScaleQ * kC] = sh.m[0][t];
+        if (!back) {
+            const float rest = ex2(fminf(sh.rest[t] + tl, 127.f)), of = sh.of_t[t];
+            to[kFactorB * kC] = b * ex2(sh.rest[t] - th);
+            to[kFactorX * kC] = b * rest * k;
+            to[kFactorU * kC] = of * el * k;
+            to[kFactorT * kC] = of;
+            if (!BACK) {
+                to[kFactorQ * kC] = ec * q;
+                to[kFactorP * kC] = sh.of_p[t];
+            }
+            const float most[2] = {most_of_warp(fabsf(b) * rest * reach), most_of_warp(sh.sum_t[t] * el * fabsf(k))};
+            if (lane == 0)
+                sh.ends[warp][0] = most[0], sh.ends[warp][1] = most[1], sh.ends[warp][5] = decay;
+        } else {
+            const float most_t = sh.L[0][t], of_t = inverse_scale(sh.L[8][t]), of_p = inverse_scale(sh.L[9][t]), bk = b * k;
+            const float fq = ex2(fminf(th + sh.late[t] + tl, 127.f)) * q;
+            to[kFactorB * kC] = b;
+            to[kFactorX * kC] = bk * decay * of_t;
+            to[kFactorXY * kC] = bk * ec * of_p;
+            to[kFactorU * kC] = k;
+            to[kFactorT * kC] = el * of_t;
+            to[kFactorP * kC] = of_p;
+            to[kFactorQ * kC] = fq;
+            to[kFactorY * kC] = ex2(-sh.late[t]);
+            const float most[5] = {most_of_warp(reach), most_of_warp(most_t), most_of_warp(fabsf(bk) * decay), most_of_warp(fabsf(bk) * ec * (kC * sh.L[4][t])),
+                                   most_of_warp(fabsf(fq))};
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < 5; ++j)
+                    sh.ends[warp][j] = most[j];
+        }
     }
     __syncthreads();
     if (tid == 0) {
-        const float *e = sh.most_p, decay = decay_of(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f));
+        const auto most = [&](int w, int j) { return fmaxf(sh.ends[w][j], sh.ends[w + 1][j]); };
+        const float decay = sh.ends[0][5];
         float *ends = reinterpret_cast<float *>(out + kAtFactors) + kFactorEnd * kC;
-        ends[kEndDecay] = decay, ends[kEndOfState] = e[0], ends[kEndOfR] = e[1];
+        ends[kEndDecay] = decay, ends[kEndOfState] = most(0, 0), ends[kEndOfR] = most(0, 1);
         if (BACK) {
             ends = reinterpret_cast<float *>(out + kStatesBytes + kAtBackFactors) + kFactorEnd * kC;
-            ends[kEndDecay] = decay, ends[kEndOfGrad] = e[2], ends[kEndDuOfGrad] = e[3] * (kC * e[4]) * e[5], ends[kEndDuOfY] = kC * most_p * e[5];
-            ends[kEndMostQ] = e[6];
+            ends[kEndDecay] = decay, ends[kEndOfGrad] = most(2, 0), ends[kEndDuOfGrad] = most(2, 0) * (kC * most(2, 1)) * most(2, 2);
+            ends[kEndDuOfY] = most(2, 3), ends[kEndMostQ] = most(2, 4);
         }
     }
 }

@@ -58,7 +58,7 @@ def exact(t):
     return d, y, final
 
 
-OUT = ("y", "final")
+OUT, STATES = ("y", "final"), ("grad v", "grad state")
 
 
 def run(t, gy, gf, what):
@@ -71,19 +71,20 @@ def run(t, gy, gf, what):
         near(y, ry, K + 256, of_row(ry), "y")
     if "final" in what:
         near(final, rf, K + 256, rf.abs().amax((-1, -2), keepdim=True), "final state")
-    if "grads" not in what:
+    if not any(k.startswith("grad") for k in what):
         return
     got = m.gated_delta_backward(gy if gy is not None else torch.zeros_like(t["v"]), *args, state=t["state"], grad_final_state=gf, **FORMS)
     loss = ((ry * to64(gy)).sum() if gy is not None else 0) + ((rf * to64(gf)).sum() if gf is not None else 0)
     names = ("q", "k", "v", "delta", "beta", "A", "state")
     want = dict(zip(names, torch.autograd.grad(loss, [leaves[k] for k in names], allow_unused=True)))
     want = {k: torch.zeros_like(leaves[k]) if w is None else w for k, w in want.items()}
-    for k in ("q", "k", "v"):
-        near(getattr(got, k), want[k], 2 * V * K + 256, of_row(want[k]), "grad " + k)
-    for k in ("delta", "beta"):
-        near(getattr(got, k), want[k], K * V, of_neighbours(want[k]), "grad " + k)
-    near(got.state, want["state"], K + 256, want["state"].abs().amax((-1, -2), keepdim=True), "grad state")
-    near(got.A, want["A"], S * B * 64, (want["delta"] * to64(t["delta"])).abs().sum((0, 1)), "grad A")
+    gates = {k: of_neighbours(want[k]) for k in ("delta", "beta")}
+    size = {"q": of_row(want["q"]), "k": of_row(want["k"]), "v": of_row(want["v"]), "state": want["state"].abs().amax((-1, -2), keepdim=True), **gates,
+            "A": (gates["delta"] * to64(t["delta"]).abs()).sum((0, 1))}
+    terms = {"delta": K * V, "beta": K * V, "A": S * B * 64, "state": K + 256}
+    for k in names:
+        if "grad " + k in what:
+            near(getattr(got, k), want[k], terms.get(k, 2 * V * K + 256), size[k], "grad " + k)
 
 
 def growing(S, log2, K, V):
@@ -97,6 +98,7 @@ def growing(S, log2, K, V):
 
 GROWTH = pytest.mark.parametrize("S,log2", [(16, 30), (200, 5), (200, 10), (200, 17), (200, 30), (96, 60), (64, 100), (64, 120)])
 SHAPES = pytest.mark.parametrize("K,V", [(32, 24), (128, 72)])
+GRADIENTS = pytest.mark.parametrize("part", [STATES], ids=["states"])
 
 
 @GROWTH
@@ -115,8 +117,40 @@ def test_growth_and_decay_in_one_chunk(path):
     run(*inputs(PATHS[path] + [0.0] * 20), OUT)
 
 
+@GROWTH
+@SHAPES
+@GRADIENTS
+def test_gradients_of_growth(S, log2, K, V, part):
+    run(*growing(S, log2, K, V), part)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@GRADIENTS
+def test_gradients_of_growth_and_decay_in_one_chunk(path, part):
+    run(*inputs(PATHS[path] + [0.0] * 20), part)
+
+
 # what is left of a state or of a gradient after 200 tokens: 2^-20 to 2^-100 of it
 RATES = [-0.1, -0.3, -0.5]
+
+
+@pytest.mark.parametrize("rate", RATES)
+@SHAPES
+@pytest.mark.parametrize("where", ["last chunk", "last token", "final state"])
+@GRADIENTS
+def test_gradients_that_come_from_the_end_only(rate, K, V, where, part):
+    t, gy, gf = inputs([rate] * 200, K=K, V=V)
+    if where == "final state":
+        return run(t, None, gf, part)
+    gy[:192 if where == "last chunk" else 199] = 0
+    run(t, gy, None, part)
+
+
+@pytest.mark.parametrize("S,rate", [(40, -2.0), (64, -1.5)])
+@GRADIENTS
+def test_gradients_of_a_final_state_that_has_faded_in_a_chunk(S, rate, part):
+    t, _, gf = inputs([rate] * S)
+    run(t, None, gf, part)
 
 
 @pytest.mark.parametrize("rate", RATES)
