@@ -59,9 +59,9 @@ struct GradShared {
     float xq[kC], xk[kC];                                           // of q, k as operands
     float gc[kC], gb[kC], dv[kC], dot[kThreads / 32];
     float dots[3][kQuarters][kC], low[kQuarters][kC];
-    int row[2][kQuarters][kC], col[4][kC];                           // sums over decayed pairs, in units of their warps
-    uint32_t exponent[kThreads / 32];
-    float most[kQuarters][2 * kC], most_of_warps[kThreads / 32];
+    float cross[2][kQuarters][kC], later[2][kC / 2];                 // sums over decayed pairs
+    float most[kQuarters][2 * kC];
+    float4 most_col[kC];                                             // of the four warps of a column
 };
 
 // Columns of tensor memory: [grad_y; du] S, [grad_y; du] u, [du; u] G, [q; k] k;
@@ -162,8 +162,9 @@ __device__ __forceinline__ void ask_ahead(const GradParams &gp, int64_t chunk, i
     }
 }
 
-// Sums of 16 values over the warp's lanes: lane l has that of value l / 2.
-__device__ __forceinline__ int sums16(int (&x)[16])
+// Sums (or the largest) of 16 values over the warp's lanes: lane l has that of value l / 2.
+template <class F>
+__device__ __forceinline__ float of16(float (&x)[16], F &&join)
 {
     const int lane = threadIdx.x % 32;
 #pragma unroll
@@ -171,20 +172,23 @@ __device__ __forceinline__ int sums16(int (&x)[16])
         const bool upper = lane & d;
 #pragma unroll
         for (int e = 0; e < n; ++e) {
-            const int give = upper ? x[e] : x[e + n], keep = upper ? x[e + n] : x[e];
-            x[e] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, d);
+            const float give = upper ? x[e] : x[e + n], keep = upper ? x[e + n] : x[e];
+            x[e] = join(keep, __shfl_xor_sync(0xFFFFFFFFu, give, d));
         }
     }
-    return x[0] + __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
+    return join(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 1));
 }
-
-// What a warp's elements of magnitude up to `most` (its bits) are counted in:
-// 2^(e - 151) for the e of their exponent, 255 where one is not finite. 32 of
-// them stay within 2^30, and rounding to them is off by 2^-25 of the largest.
-__device__ __forceinline__ uint32_t exponent_of(uint32_t most) { return max(most >> 23, 24u); }
-__device__ __forceinline__ int counted(float x, uint32_t e) { return e >= 255 ? 0 : __float2int_rn(x * __uint_as_float((278u - e) << 23)); }
-// A warp's sum in units of 2^-16 of the largest warp's.
-__device__ __forceinline__ int64_t of_warp(int sum, uint32_t e, uint32_t most) { return ((int64_t)sum << 16) >> min(most - e, 63u); }
+// A sum over this lane and those after it.
+__device__ __forceinline__ float from_lane_on(float x)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const float o = __shfl_down_sync(0xFFFFFFFFu, x, d);
+        if (threadIdx.x % 32 + d < 32)
+            x += o;
+    }
+    return x;
+}
 
 // Adds A B^T, all of two terms but A's second times B's second, over 64 values
 // of the sum, by one thread; second terms first, as in delta_chunks.cu.
@@ -480,8 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             uint32_t d[IC];
             tmem_load(lanes + kDK + quarter * IC, d);
             tmem_wait(d);
-            float E[IC], by_row[IC], low = 0.f, most_row = 0.f, most_col = 0.f;
-            uint32_t most_e = 0;
+            float E[IC], by_row[IC], low = 0.f, most_row = 0.f;
             const float th = sh.ch[t], tl = sh.cl[t], f = of_du ? sh.xk[t] : sh.xq[t], bt = of_du ? sh.b[t] : 1.f;
 #pragma unroll
             for (int c = 0; c < IC; ++c) {
@@ -490,45 +493,67 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
                 const float D = in ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) : 0.f, x = in ? PL[c] * D : 0.f;
                 const float xi = sh.xk[i], lk = x * (__uint_as_float(d[c]) * f * xi);
                 E[c] = i < t ? bt * lk : 0.f;      // no decay between a token and itself
-                low += lk, most_e = max(most_e, __float_as_uint(E[c]) & 0x7FFFFFFFu);
+                low += lk;
                 by_row[c] = bt * x * xi;
                 PL[c] = bt * x * f;
                 most_row = fmaxf(most_row, fabsf(by_row[c]));
-                most_col = fmaxf(most_col, fabsf(PL[c]));
             }
-            // a token's row less its column, summed from any token on, leaves out the
-            // pairs behind it: in integers nothing is left of them
-            const uint32_t exponent = exponent_of(__reduce_max_sync(0xFFFFFFFFu, most_e));
-            int counts[IC], row = 0;
+            // The pairs (t, i) whose decay a token has part in are those with i before it and t
+            // not. Only they are summed: pairs behind it, however much larger, would leave
+            // their rounding. A warp has 32 t and 16 i; behind all of its i a token has
+            // the whole rows from it on, within them those rows' sums up to it.
+            {
+                const bool within = quarter / 2 == warp % 2;
+                const auto sum = [](float x, float y) { return x + y; };
+                float rows = 0.f;
+                if (within) {
 #pragma unroll
-            for (int c = 0; c < IC; ++c)
-                counts[c] = counted(E[c], exponent), row += counts[c];
-            sh.row[of_du][quarter][t] = row;
+                    for (int c = 0; c < IC; ++c) {
+                        rows += E[c];
+                        E[c] = t > quarter * IC + c ? rows : 0.f;      // for the token after c
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < IC; ++c)
+                        rows += E[c];
+                }
+                rows = from_lane_on(rows);
+                const float sums = of16(E, sum);
+                const int at = quarter * IC + lane / 2;
+                if (!within || t <= quarter * IC || t > quarter * IC + IC)
+                    sh.cross[of_du][quarter][t] = quarter * IC < t ? rows : 0.f;
+                if (lane % 2 == 0 && within && (at + 1) / 32 == warp % 2)
+                    sh.cross[of_du][quarter][at + 1] = sums;
+                if (lane % 2 == 0 && quarter / 2 < warp % 2)           // of tokens in the other half
+                    sh.later[of_du][at] = sums;
+            }
             if (of_du)
                 sh.low[quarter][t] = low;
-            const int col = sums16(counts);
-            if (lane == 0)
-                sh.exponent[warp] = exponent;
+            // a column's pairs, of rows that P' and L' fade or grow along, are a sum of their own
+#pragma unroll
+            for (int c = 0; c < IC; ++c)
+                E[c] = fabsf(PL[c]);
+            const float most_col = of16(E, [](float x, float y) { return fmaxf(x, y); });
             if (lane % 2 == 0)
-                sh.col[warp % 4][quarter * IC + lane / 2] = col;
-            most_col = most_of_lanes<32>(most_col);
-            if (lane == 0)
-                sh.most_of_warps[warp] = most_col;
+                reinterpret_cast<float *>(&sh.most_col[quarter * IC + lane / 2])[warp % 4] = most_col;
             sh.most[quarter][r] = most_row;
             tmem_fence_before();
             __syncthreads();
             tmem_fence_after();
             most_row = fmaxf(fmaxf(sh.most[0][r], sh.most[1][r]), fmaxf(sh.most[2][r], sh.most[3][r]));
-            most_col = sh.most_of_warps[0];
+            const auto scale_of = [&](int i) {
+                const float4 m = sh.most_col[i];
+                return scale_for(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+            };
+            const float scale_row = scale_for(most_row), scale_lane = scale_of(quarter * IC + lane % IC);
 #pragma unroll
-            for (int w = 1; w < kThreads / 32; ++w)
-                most_col = fmaxf(most_col, sh.most_of_warps[w]);
-            const float scale_row = scale_for(most_row), scale_col = scale_for(most_col);
+            for (int c = 0; c < IC; ++c)
+                PL[c] *= __shfl_sync(0xFFFFFFFFu, scale_lane, c);
             uint8_t *hi = panels + (of_du ? Pn::LC : Pn::PC), *lo = panels + (of_du ? Pn::LCLo : Pn::PCLo);
 #pragma unroll
             for (int e = 0; e < IC / 8; ++e) {
                 put8(panels + Pn::X, panels + Pn::XLo, panel_at(r, quarter * (IC / 8) + e), by_row + 8 * e, scale_row);
-                put8(hi, lo, panel_at(t, quarter * (IC / 8) + e), PL + 8 * e, scale_col);
+                put8(hi, lo, panel_at(t, quarter * (IC / 8) + e), PL + 8 * e, 1.f);
             }
             shared_to_async();
             tmem_fence_before();
@@ -554,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             parity ^= 1;
             tmem_fence_after();
             __syncwarp();
-            const float of_x = inverse_scale(scale_row), of_c = of_du ? inverse_scale(scale_col) : 0.f;
+            const float of_x = inverse_scale(scale_row), of_c = of_du ? inverse_scale(scale_of(t)) : 0.f;
 #pragma unroll
             for (int c = 0; c < KC; c += UNIT) {
                 uint32_t x[UNIT], y[UNIT];
@@ -573,20 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
         if (warp == 0) {
             const float A = p.delta ? __ldg(p.A + h) : 0.f;
             const auto four = [](const float (&x)[kQuarters][kC], int i) { return (x[0][i] + x[1][i]) + (x[2][i] + x[3][i]); };
-            // of pairs, in integers; of the end's products, which have the decays after
-            // their token; and of all others, which have those up to theirs
-            const uint32_t exponent = __reduce_max_sync(0xFFFFFFFFu, lane < kThreads / 32 ? sh.exponent[lane] : 0u);
-            int64_t pairs[2];
-            float x[2], e_of[2];
+            // of pairs; of the end's products, which have the decays after their token; and
+            // of all others, which have those up to theirs
+            float pairs[2], x[2], e_of[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                pairs[e] = 0;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    pairs[e] += of_warp(sh.row[0][w][i], sh.exponent[4 * w + i / 32], exponent) + of_warp(sh.row[1][w][i], sh.exponent[4 * w + 2 + i / 32], exponent);
-                    pairs[e] -= of_warp(sh.col[w][i], sh.exponent[i / IC * 4 + w], exponent);
-                }
+                pairs[e] = four(sh.cross[0], i) + four(sh.cross[1], i);
                 const float sk = four(sh.dots[1], i);
                 e_of[e] = four(sh.dots[2], i);
                 x[e] = four(sh.dots[0], i) + sh.b[i] * sk;
@@ -594,33 +612,43 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
                 if (!ok)
                     x[e] = sh.gb[i] = __uint_as_float(0x7FFFFFFFu);
             }
+            {       // tokens of the first half: the second half's pairs with those before them
+                const int i = 2 * lane;
+                const float l0 = lane < 16 ? sh.later[0][i] + sh.later[1][i] : 0.f, l1 = lane < 16 ? sh.later[0][i + 1] + sh.later[1][i + 1] : 0.f;
+                float to = l0 + l1;
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) {
+                    const float o = __shfl_up_sync(0xFFFFFFFFu, to, d);
+                    if (lane >= d)
+                        to += o;
+                }
+                const float o = __shfl_up_sync(0xFFFFFFFFu, to, 1), before = lane > 0 ? o : 0.f;
+                if (lane < 16)
+                    pairs[0] += before, pairs[1] += before + l0;
+            }
             if (lane == 31) {
                 float s = 0.f;
                 for (int w = 0; w < kThreads / 32; ++w)
                     s += sh.dot[w];
                 x[1] = fmaf(s, ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), x[1]);
             }
-            int64_t s_pairs = pairs[0] + pairs[1];
             float s = x[0] + x[1], s_e = e_of[0] + e_of[1];
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
-                const int64_t op = __shfl_down_sync(0xFFFFFFFFu, s_pairs, d);
                 const float o = __shfl_down_sync(0xFFFFFFFFu, s, d), oe = __shfl_up_sync(0xFFFFFFFFu, s_e, d);
                 if (lane + d < 32)
-                    s += o, s_pairs += op;
+                    s += o;
                 if (lane >= d)
                     s_e += oe;
             }
             const float o = __shfl_down_sync(0xFFFFFFFFu, s, 1), after = lane < 31 ? o : 0.f;
             const float oe = __shfl_up_sync(0xFFFFFFFFu, s_e, 1), before = lane > 0 ? oe : 0.f;
-            // units of 2^(exponent - 151 - 16)
-            const float unit = exponent >= 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(exponent << 23);
             float sa = 0.f, sb = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
                 float gl = e ? after + x[1] + (before + e_of[0]) : after + (x[0] + x[1]) + before;
-                gl = i < n ? fmaf((float)(s_pairs - (e ? pairs[0] : 0)) * 0x1p-40f, unit, gl) : 0.f;
+                gl = i < n ? gl + pairs[e] : 0.f;
                 float graw = gl * A;
                 if (p.flags & MCC1D_SOFTPLUS)
                     graw *= sigmoid(sh.raw[i]);

@@ -58,7 +58,7 @@ def exact(t):
     return d, y, final
 
 
-OUT, STATES = ("y", "final"), ("grad v", "grad state")
+OUT, STATES, TOKENS = ("y", "final"), ("grad v", "grad state"), ("grad q", "grad k", "grad delta", "grad beta", "grad A")
 
 
 def run(t, gy, gf, what):
@@ -98,7 +98,7 @@ def growing(S, log2, K, V):
 
 GROWTH = pytest.mark.parametrize("S,log2", [(16, 30), (200, 5), (200, 10), (200, 17), (200, 30), (96, 60), (64, 100), (64, 120)])
 SHAPES = pytest.mark.parametrize("K,V", [(32, 24), (128, 72)])
-GRADIENTS = pytest.mark.parametrize("part", [STATES], ids=["states"])
+GRADIENTS = pytest.mark.parametrize("part", [STATES, TOKENS], ids=["states", "tokens"])
 
 
 @GROWTH
