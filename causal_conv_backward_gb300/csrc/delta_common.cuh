@@ -37,6 +37,11 @@ inline DeltaParams delta_params(const mcc1d_delta_args &a)
     return p;
 }
 
+// The log2 of one decay as the chunks take it, and 2^x for sums of them, no more than
+// 2^127. By comparisons, not by the smaller and larger of two: a NaN stays one.
+__device__ __forceinline__ float held_log2(float x) { return x < -255.f ? -255.f : x > 255.f ? 255.f : x; }
+__device__ __forceinline__ float ex2_held(float x) { return ex2(x > 127.f ? 127.f : x); }
+
 // One 16-bit value.
 template <int DT>
 __device__ __forceinline__ float value(const uint16_t *p) { return unpack2<DT>(__ldg(p)).x; }

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
                     if (i < n)
                         gate = gates_of(p.flags, p.delta != nullptr, raw_delta[e], p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
                                         raw_beta[e]);
-                    const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f);
+                    const float l = held_log2(gate.log2a);
                     hi[e] = rintf(l * 512.f) * (1.f / 512.f), lo[e] = l - hi[e];
                     sh.b[i] = gate.b, sh.dt[i] = gate.dt, sh.raw[i] = gate.raw;
                 }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             tmem_fence_after();
             __syncwarp();
             const float of_row = sh.of_rows[r], bt = sh.b[t];
-            const float ec = ex2(fminf(sh.ch[t] + sh.cl[t], 127.f)), el = ex2(fminf((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]), 127.f));
+            const float ec = ex2_held(sh.ch[t] + sh.cl[t]), el = ex2_held((sh.ch[kC - 1] - sh.ch[t]) + (sh.cl[kC - 1] - sh.cl[t]));
             const float add = (of_du ? -ec : ec) * of_row, to_acc = of_du ? bt : 1.f, add_g = of_du ? el * sh.of_rows[kC + r] : 0.f;
 #pragma unroll
             for (int c = 0; c < KC; c += UNIT) {
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
             for (int c = 0; c < IC; ++c) {
                 const int i = quarter * IC + c;
                 const bool in = of_du ? i < t : i <= t;
-                const float D = in ? ex2(fminf((th - sh.ch[i]) + (tl - sh.cl[i]), 127.f)) : 0.f, x = in ? PL[c] * D : 0.f;
+                const float D = in ? ex2_held((th - sh.ch[i]) + (tl - sh.cl[i])) : 0.f, x = in ? PL[c] * D : 0.f;
                 const float xi = sh.xk[i], lk = x * (__uint_as_float(d[c]) * f * xi);
                 E[c] = i < t ? bt * lk : 0.f;      // no decay between a token and itself
                 low += lk;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
                 float s = 0.f;
                 for (int w = 0; w < kThreads / 32; ++w)
                     s += sh.dot[w];
-                x[1] = fmaf(s, ex2(fminf(sh.ch[kC - 1] + sh.cl[kC - 1], 127.f)), x[1]);
+                x[1] = fmaf(s, ex2_held(sh.ch[kC - 1] + sh.cl[kC - 1]), x[1]);
             }
             float s = x[0] + x[1], s_e = e_of[0] + e_of[1];
 #pragma unroll

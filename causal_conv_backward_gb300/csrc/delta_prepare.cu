@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                 gate = gates_of(p.flags, p.delta != nullptr, p.delta ? value<DT>(p.delta + t * p.delta_s[0] + b * p.delta_s[1] + h) : 0.f,
                                 p.delta_bias ? __ldg(p.delta_bias + h) : 0.f, p.delta ? __ldg(p.A + h) : 0.f,
                                 value<DT>(p.beta + t * p.beta_s[0] + b * p.beta_s[1] + h));
-            const float l = fminf(fmaxf(gate.log2a, -255.f), 255.f), hi = rintf(l * 512.f) * (1.f / 512.f);
+            const float l = held_log2(gate.log2a), hi = rintf(l * 512.f) * (1.f / 512.f);
             sh.ch[tid] = hi, sh.cl[tid] = l - hi, sh.b[tid] = gate.b;
         }
 #pragma unroll
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         };
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            D[j] = ex2(fminf((th - sh.rest[16 * part + j]) + (tl - sh.cl[16 * part + j]), 127.f));
+            D[j] = ex2_held((th - sh.rest[16 * part + j]) + (tl - sh.cl[16 * part + j]));
         row_of(sh.T, D);
         float sum, scale = scale_for(most_of_row(x, sum));
         store_terms(x, scale, out + kAtT, out + kAtTLo, t, part);
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                 for (int e = 0; e < 16; ++e) {
                     const int j = first + e;
                     if (j >= i) {
-                        const float v = sh.X[j][i] * ex2(fminf((sh.ch[j] + sh.late[j] - ih) + (sh.cl[j] - il), 127.f));
+                        const float v = sh.X[j][i] * ex2_held((sh.ch[j] + sh.late[j] - ih) + (sh.cl[j] - il));
                         most_t = fmaxf(most_t, fabsf(sh.T[j][i])), most_p = fmaxf(most_p, fabsf(v));
                         sh.X[j][i] = v;
                     }
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         const int t = tid % kC;
         const bool back = warp >= 2;
         const float th = sh.ch[t], tl = sh.cl[t], b = sh.b[t], end = sh.ch[kC - 1] + sh.cl[kC - 1];
-        const float ec = ex2(fminf(th + tl, 127.f)), el = ex2(fminf((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl), 127.f)), decay = decay_of(fminf(end, 127.f));
+        const float ec = ex2_held(th + tl), el = ex2_held((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl)), decay = decay_of(end > 127.f ? 127.f : end);
         // a row of zeros adds nothing, and must not lower the others' scale
         const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
         const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         to[kFactorScaleK * kC] = sh.m[1][t];
         to[kFactorScaleQ * kC] = sh.m[0][t];
         if (!back) {
-            const float rest = ex2(fminf(sh.rest[t] + tl, 127.f)), of = sh.of_t[t];
+            const float rest = ex2_held(sh.rest[t] + tl), of = sh.of_t[t];
             to[kFactorB * kC] = b * ex2(sh.rest[t] - th);
             to[kFactorX * kC] = b * rest * k;
             to[kFactorU * kC] = of * el * k;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                 sh.ends[warp][0] = most[0], sh.ends[warp][1] = most[1], sh.ends[warp][5] = decay;
         } else {
             const float most_t = sh.L[0][t], of_t = inverse_scale(sh.L[8][t]), of_p = inverse_scale(sh.L[9][t]), bk = b * k;
-            const float fq = ex2(fminf(th + sh.late[t] + tl, 127.f)) * q;
+            const float fq = ex2_held(th + sh.late[t] + tl) * q;
             to[kFactorB * kC] = b;
             to[kFactorX * kC] = bk * decay * of_t;
             to[kFactorXY * kC] = bk * ec * of_p;
