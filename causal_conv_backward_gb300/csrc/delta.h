@@ -47,10 +47,11 @@ constexpr int kAtBackT = 0, kAtBackTLo = kPanelBytes, kAtBackPT = 2 * kPanelByte
 enum { kFactorB, kFactorX, kFactorU, kFactorQ, kFactorP, kFactorScaleK, kFactorScaleQ, kFactorEnd,
        kFactorT, kFactorXY, kFactorY, kFactors };
 static_assert(kFactors <= kFactorRows && kAtPT % 1024 == 0 && kForwardBytes % 1024 == 0 && kBackBytes % 1024 == 0, "panels on 1024 bytes");
-// In that row: the chunk's decay; what bounds the state's part of a row's R, U
-// (of R), and backwards what the state's gradient is multiplied with first, its part
-// and grad_y's of du as an operand; the largest factor of q.
-enum { kEndDecay, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
+// In that row: how many tokens come before the first whose k or gates are not
+// finite; the chunk's decay; what bounds the state's part of a row's R, U (of R), and
+// backwards what the state's gradient is multiplied with first, its part and grad_y's
+// of du as an operand; the largest factor of q.
+enum { kEndGood, kEndDecay, kEndOfState, kEndOfR, kEndOfGrad, kEndDuOfGrad, kEndDuOfY, kEndMostQ };
 constexpr int kBothBytes = kStatesBytes + kBackBytes;        // of a chunk in a backward; kForwardBytes in a forward
 
 struct DeltaPlan {

@@ -22,6 +22,8 @@
 // warps of its own. Warps 0 to 15 hold the rows, 16 to 19 write Y, 20 issues the
 // products, 21 copies the tokens of the chunk after the next, 22 to 27 make
 // panels of the next one's.
+#include <limits.h>
+
 #include <utility>
 
 #include "delta_chunks.cuh"
@@ -66,6 +68,7 @@ struct ChunkShared {
     float of_s[2][kRows], of_r[2][kRows];       // of the last two chunks: what rows' terms are multiplied by
     float of_y[4][2 * kC];                      // the factors of Y of the last four chunks
     float most[kParts][kRows], most_v[kParts][kRows], sum_u[kParts][kRows];      // of the parts of a row
+    int bad[kRows];                              // the first token whose value is not finite, of rows that have one
     uint32_t tmem, failed;
 };
 
@@ -98,6 +101,37 @@ __device__ __forceinline__ void fill_values(uint8_t *values, const uint16_t *fro
         if (!vectors || t >= n || live <= 0)
             *reinterpret_cast<uint4 *>(values + (piece / 8) * kPanelBytes + t * 128 + 16 * (piece % 8)) =
                 piece_of(nullptr, from + t * step + 8 * piece, false, t < n && !vectors ? live : 0);
+}
+
+// Values that are not finite become zeros where they lie: in a row's operands they
+// would, times zeros of T, make NaN of earlier tokens too. A row's first of them is
+// noted (`first`: the chunk's first token), and its outputs from there on and its state
+// become NaN. The threads have the pieces that they have in fill_values.
+template <int DT>
+__device__ __forceinline__ void leave_out(uint8_t *values, int V, int n, int first, int *bad, int thread)
+{
+    constexpr int PIECES = kRows / 8, STEP = kLoadThreads / PIECES;
+    constexpr uint32_t INF = DT == 0 ? 0x7F80u : 0x7C00u;
+    const int piece = thread % PIECES;
+    if (V - 8 * piece <= 0)
+        return;
+    uint8_t *at = values + (piece / 8) * kPanelBytes + 16 * (piece % 8);
+    uint32_t most = 0u;           // magnitudes are in the order of their bits
+#pragma unroll 2
+    for (int t = thread / PIECES; t < n; t += STEP) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(at + t * 128);
+        most = __vmaxu2(__vmaxu2(most, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    }
+    if ((most & 0xFFFFu) < INF && most >> 16 < INF)
+        return;
+#pragma unroll 1
+    for (int t = thread / PIECES; t < n; t += STEP)
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+            uint16_t &x = reinterpret_cast<uint16_t *>(at + t * 128)[e];
+            if ((x & 0x7FFFu) >= INF)
+                x = 0, atomicMin(bad + 8 * piece + e, first + t);
+        }
 }
 
 // ------------------------------------------------------------------ the rows
@@ -240,8 +274,8 @@ __device__ __forceinline__ void hold_rows(const ChunkParams &cp, ChunkShared &sh
         // |S| <= e^c(end) |S| + sum of |U k|, and no |k| is above 2^16 as an operand
         const float before = scale_s;
         scale_s = scale_for(fmaf(fabsf(end), most_s, ((sh.sum_u[0][r] + sh.sum_u[1][r]) + (sh.sum_u[2][r] + sh.sum_u[3][r])) * of_u * 65536.f));
-        const float2 keep = make_float2(end * inverse_scale(before) * scale_s, end * inverse_scale(before) * scale_s);
-        const float2 add = make_float2(of_u * scale_s, of_u * scale_s);
+        const float kept = sh.bad[r] < (int)(pt.first + i + 1) * kC ? __uint_as_float(0x7FFFFFFFu) : end * inverse_scale(before) * scale_s;
+        const float2 keep = make_float2(kept, kept), add = make_float2(of_u * scale_s, of_u * scale_s);
         if (part == 0)
             sh.of_s[parity ^ 1][r] = inverse_scale(scale_s);
         ok = ok && warp_wait(sh.end, parity);
@@ -288,6 +322,7 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
         const int64_t t1 = (pt.first + i) * kC;
         const int live = (int)(n - t1 < kC ? n - t1 : kC), rows = (int)(p.S - t1 < kC ? p.S - t1 : kC);
         const bool whole = cp.pairs_y && rows == kC && live == kC;
+        const int good = sh.bad[r] - (int)t1;
 #pragma unroll 1
         for (int t0 = 0; t0 < kC; t0 += 16) {
             uint32_t a[16], c[16], y[8];
@@ -304,6 +339,11 @@ __device__ __forceinline__ void write_y(const ChunkParams &cp, ChunkShared &sh, 
                 y[t / 2] = pack2<DT>(fma2(mul2(pr, of_r), make_float2(__uint_as_float(c[t]), __uint_as_float(c[t + 1])),
                                           mul2(mul2(q, of_s), make_float2(__uint_as_float(a[t]), __uint_as_float(a[t + 1])))));
             }
+            if (good < t0 + 16)
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (t0 + t >= good)
+                        y[t / 2] |= t % 2 ? 0x7FFF0000u : 0x00007FFFu;
             if (whole) {        // two rows of one token: even lanes the first, odd lanes the second
 #pragma unroll
                 for (int t = 0; t < 8; ++t, pair += 2 * step) {
@@ -455,7 +495,8 @@ __device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &s
         const float *f = reinterpret_cast<const float *>(tiles + Tl::kAll + (i % kPrepareds) * kPreparedBytes + kAtFactors);
         if (!warp_wait(sh.tiles[i % kTiles], (uint32_t)(i / kTiles) & 1) || !warp_wait(sh.prepared[i % kPrepareds], (uint32_t)(i / kPrepareds) & 1))
             break;
-        make_panels<DT, KP>(tile + Tl::K, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k, live, thread);
+        make_panels<DT, KP>(tile + Tl::K, p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2], p.k_s[0], f + kFactorScaleK * kC, p.K, cp.vectors_k,
+                            min(live, (int)f[kFactorEnd * kC + kEndGood]), thread);
         if (p.y) {
             make_panels<DT, KP>(tile + Tl::Q, p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2], p.q_s[0], f + kFactorScaleQ * kC, p.K, cp.vectors_q, live,
                                 thread);
@@ -464,6 +505,7 @@ __device__ __forceinline__ void make_tiles(const ChunkParams &cp, ChunkShared &s
         }
         if (live < kC || !cp.vectors_v || pt.unit || p.V - v0 < kRows)
             fill_values(tile + Tl::V, p.v + t0 * p.v_s[0] + b * p.v_s[1] + h * p.v_s[2] + v0, p.v_s[0], pt.unit ? 0 : p.V - v0, cp.vectors_v, live, thread);
+        leave_out<DT>(tile + Tl::V, pt.unit ? 0 : p.V - v0, live, (int)t0, sh.bad, thread);
         shared_to_async();
         warp_arrive(sh.full[i % kTiles]);
     }
@@ -482,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_chunks_rows(const __g
     if (!part_of(cp.seg, p, cp.tiles, p.state, p.final_state, pt, n))
         return;
 
+    if (tid < kRows)
+        sh.bad[tid] = INT_MAX;
     if (tid == 0) {
         sh.failed = 0;
         for (int i = 0; i < kTiles; ++i)
@@ -519,6 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_chunks_rows(const __g
     if (warp == kProductWarp) {
         tmem_fence_after();
         tmem_free(sh.tmem, kColumns);
+    }
+    if (p.kept.u && tid < kRows && pt.v0 + tid < p.V) {
+        const int64_t end = (pt.first + pt.chunks) * kC;
+        for (int64_t t = sh.bad[tid]; t < n && t < end; ++t)
+            p.kept.u[(t * p.B * p.H + pt.item) * p.kept.Vp + pt.v0 + tid] = __uint_as_float(0x7FFFFFFFu);
     }
 }
 

@@ -48,6 +48,8 @@ struct PrepareShared {
     float L[kC][kRow], P[kC][kRow];
     float ch[kC], cl[kC], rest[kC], b[kC], f[2][kC], m[2][kC], lk[kC], late[kC], of_t[kC], sum_t[kC], of_p[kC], ends[4][8];
     bool zero_q[kC];
+    uint32_t bad_gates[2];
+    int bad_k[4];
 };
 
 template <int DT>
@@ -199,6 +201,9 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                                 value<DT>(p.beta + t * p.beta_s[0] + b * p.beta_s[1] + h));
             const float l = held_log2(gate.log2a), hi = rintf(l * 512.f) * (1.f / 512.f);
             sh.ch[tid] = hi, sh.cl[tid] = l - hi, sh.b[tid] = gate.b;
+            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !(l == l && fabsf(gate.b) < INFINITY));
+            if (lane == 0)
+                sh.bad_gates[warp] = bad;
         }
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -237,6 +242,9 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        const uint32_t bad = __ballot_sync(0xFFFFFFFFu, !(sum == sum && most < INFINITY));
+        if (w == 1 && lane == 0)
+            sh.bad_k[warp - 4] = bad ? 16 * (warp - 4) + (__ffs(bad) - 1) / 2 : kC;
         if (half == 0) {
             const float f = unit_factor(p.flags, sum);
             sh.f[w][t] = f, sh.m[w][t] = scale_for(most);
@@ -247,6 +255,12 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         }
     }
     __syncthreads();
+    // From the first token on whose k or gates are not finite all outputs are NaN, and
+    // so is the state; the tokens before it know nothing of them: no zero of T meets
+    // them. (Gradients do not keep to that: theirs are NaN for the whole chunk.)
+    int good = min(min(sh.bad_k[0], sh.bad_k[1]), min(sh.bad_k[2], sh.bad_k[3]));
+    if (sh.bad_gates[0] | sh.bad_gates[1])
+        good = min(good, sh.bad_gates[0] ? __ffs(sh.bad_gates[0]) - 1 : 31 + __ffs(sh.bad_gates[1]));
     if (tid < kC)
         sh.rest[tid] = sh.ch[tid] - growth_of(sh.ch[tid] + sh.cl[tid]);
     {   // 16 rows and 32 columns of both products to a warp
@@ -283,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = c0 + 8 * j + col + e;
-                    l[e] = i < t ? kk[j][2 * half + e] * (sh.f[1][i] * lt) : 0.f;
-                    x[e] = i <= t ? qk[j][2 * half + e] * (sh.f[1][i] * pt) : 0.f;
+                    l[e] = i < t && t < good ? kk[j][2 * half + e] * (sh.f[1][i] * lt) : 0.f;
+                    x[e] = i <= t && t < good ? qk[j][2 * half + e] * (sh.f[1][i] * pt) : 0.f;
                 }
                 *reinterpret_cast<float2 *>(&sh.L[t][c0 + 8 * j + col]) = make_float2(l[0], l[1]);
                 *reinterpret_cast<float2 *>(&sh.P[t][c0 + 8 * j + col]) = make_float2(x[0], x[1]);
@@ -437,7 +451,10 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         const int t = tid % kC;
         const bool back = warp >= 2;
         const float th = sh.ch[t], tl = sh.cl[t], b = sh.b[t], end = sh.ch[kC - 1] + sh.cl[kC - 1];
-        const float ec = ex2_held(th + tl), el = ex2_held((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl)), decay = decay_of(end > 127.f ? 127.f : end);
+        const float none = __uint_as_float(0x7FFFFFFFu);
+        const bool there = t < good;
+        const float ec = ex2_held(th + tl), decay = good < kC ? none : decay_of(end > 127.f ? 127.f : end);
+        const float el = back && good < kC ? none : ex2_held((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl));
         // a row of zeros adds nothing, and must not lower the others' scale
         const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
         const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
@@ -447,19 +464,19 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         to[kFactorScaleQ * kC] = sh.m[0][t];
         if (!back) {
             const float rest = ex2_held(sh.rest[t] + tl), of = sh.of_t[t];
-            to[kFactorB * kC] = b * ex2(sh.rest[t] - th);
-            to[kFactorX * kC] = b * rest * k;
+            to[kFactorB * kC] = there ? b * ex2(sh.rest[t] - th) : 0.f;
+            to[kFactorX * kC] = there ? b * rest * k : 0.f;
             to[kFactorU * kC] = of * el * k;
-            to[kFactorT * kC] = of;
+            to[kFactorT * kC] = there ? of : none;
             if (!BACK) {
-                to[kFactorQ * kC] = ec * q;
+                to[kFactorQ * kC] = there ? ec * q : none;
                 to[kFactorP * kC] = sh.of_p[t];
             }
-            const float most[2] = {most_of_warp(fabsf(b) * rest * reach), most_of_warp(sh.sum_t[t] * el * fabsf(k))};
+            const float most[2] = {most_of_warp(there ? fabsf(b) * rest * reach : 0.f), most_of_warp(sh.sum_t[t] * el * fabsf(k))};
             if (lane == 0)
                 sh.ends[warp][0] = most[0], sh.ends[warp][1] = most[1], sh.ends[warp][5] = decay;
         } else {
-            const float most_t = sh.L[0][t], of_t = inverse_scale(sh.L[8][t]), of_p = inverse_scale(sh.L[9][t]), bk = b * k;
+            const float most_t = sh.L[0][t], of_t = inverse_scale(sh.L[8][t]), of_p = good < kC ? none : inverse_scale(sh.L[9][t]), bk = b * k;
             const float fq = ex2_held(th + sh.late[t] + tl) * q;
             to[kFactorB * kC] = b;
             to[kFactorX * kC] = bk * decay * of_t;
@@ -482,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         const auto most = [&](int w, int j) { return fmaxf(sh.ends[w][j], sh.ends[w + 1][j]); };
         const float decay = sh.ends[0][5];
         float *ends = reinterpret_cast<float *>(out + kAtFactors) + kFactorEnd * kC;
-        ends[kEndDecay] = decay, ends[kEndOfState] = most(0, 0), ends[kEndOfR] = most(0, 1);
+        ends[kEndGood] = (float)good, ends[kEndDecay] = decay, ends[kEndOfState] = most(0, 0), ends[kEndOfR] = most(0, 1);
         if (BACK) {
             ends = reinterpret_cast<float *>(out + kStatesBytes + kAtBackFactors) + kFactorEnd * kC;
             ends[kEndDecay] = decay, ends[kEndOfGrad] = most(2, 0), ends[kEndDuOfGrad] = most(2, 0) * (kC * most(2, 1)) * most(2, 2);

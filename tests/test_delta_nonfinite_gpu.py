@@ -1,5 +1,5 @@
-"""NaN in the gated delta rule's inputs comes out of every token that depends on
-it, by whichever path."""
+"""NaN and infinity in the gated delta rule's inputs: they come out of every
+token that depends on them, by whichever path, and out of no other's."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -7,9 +7,10 @@ pytestmark = pytest.mark.gpu
 
 import causal_conv_backward_gb300 as m  # noqa: E402
 import delta_reference as ref  # noqa: E402
-from ssm_reference import to64  # noqa: E402
+from ssm_reference import check, to64  # noqa: E402
 from test_delta_gpu import FORMS, NAN, cuda_ready, inputs, lens  # noqa: E402,F401
 
+INF = float("inf")
 TOKENS = ("q", "k", "v", "delta", "beta")
 SHAPE = dict(B=2, H=4, G=2, K=32, V=24)
 
@@ -22,6 +23,13 @@ def run(t, lengths=None):
 def exact(t, lengths=None, grad=False):
     d = {k: to64(v, grad=grad) for k, v in t.items()}
     return d, *ref.delta_rule(*[d[k] for k in TOKENS + ("A", "delta_bias")], lengths=lengths, state=d["state"])
+
+
+def same_where_finite(got, bad, clean, what):
+    """Not finite exactly where the definition is not; `clean`, without the value, elsewhere."""
+    bad = bad.detach()
+    assert torch.equal(torch.isfinite(got.cpu()), torch.isfinite(bad)), what
+    check(torch.where(torch.isfinite(bad).cuda(), got, 0), torch.where(torch.isfinite(bad), clean, 0), 32 + 256, what)
 
 
 def spoil(t, name, at, value):
@@ -55,6 +63,21 @@ def test_a_gate_that_is_nan(S, at, name):
         assert not torch.isfinite(getattr(got, k).cpu())[~torch.isfinite(want)].any(), k
 
 
+@pytest.mark.parametrize("S,at", PLACES)
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "delta"])
+def test_earlier_tokens_and_other_rows_keep_their_values(S, at, name, value):
+    if name in ("beta", "delta") and value == INF:
+        value = NAN             # a gate of one, or no state left: finite
+    t, _, _, _ = inputs(S, **SHAPE)
+    bad = spoil(t, name, (at, 0, 1) if name in ("beta", "delta") else (at, 0, 1, 3), value)
+    y, final = run(bad)
+    _, ry, rf = exact(bad)
+    _, cy, cf = exact(t)
+    same_where_finite(y, ry, cy, "y")
+    same_where_finite(final, rf, cf, "final state")
+
+
 @pytest.mark.parametrize("S", [16, 100])
 def test_what_a_length_leaves_out_spoils_nothing(S):
     """The first value that is not finite is the first one behind the end."""
@@ -66,6 +89,21 @@ def test_what_a_length_leaves_out_spoils_nothing(S):
     y, final = run(bad, n)
     clean, state = run(t, n)
     assert torch.equal(y, clean) and torch.equal(final, state)
+
+
+@pytest.mark.parametrize("name", TOKENS + ("state",))
+def test_long_prompts_in_segments(name):
+    """One head, its time axis cut into segments: a value that is not finite
+    reaches all tokens after it, and none before."""
+    S, at = 2600, 1000
+    t, _, _, _ = inputs(S, 1, 1, 1, 16, 8, what="dbs")
+    where = {"q": (at, 0, 0, 3), "k": (at, 0, 0, 3), "v": (at, 0, 0, 3), "delta": (at, 0, 0), "beta": (at, 0, 0), "state": (0, 0, 3)}[name]
+    bad = spoil(t, name, where, NAN)
+    y, final = run(bad)
+    _, ry, rf = exact(bad)
+    _, cy, cf = exact(t)
+    same_where_finite(y, ry, cy, "y")
+    same_where_finite(final, rf, cf, "final state")
 
 
 @pytest.mark.parametrize("name", ["q", "k", "v", "beta"])
