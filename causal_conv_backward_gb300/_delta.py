@@ -82,7 +82,7 @@ def gated_delta(q, k, v, delta, beta, A=None, delta_bias=None, *, delta_softplus
                 scale=None, lengths=None, state=None, return_state=False, y=None, stream=None):
     """S_t = a_t S_{t-1} + u_t k_t^T,  u_t = b_t (v_t - a_t S_{t-1} k_t),  y_t = S_t (scale q_t)
     with a = exp(A dt), dt = delta + delta_bias, through softplus if
-    ``delta_softplus`` (a = 1 without delta), b = beta, through a sigmoid if
+    ``delta_softplus`` (without delta a = 1, whatever A and delta_bias), b = beta, through a sigmoid if
     ``beta_sigmoid``, and with ``qk_norm`` q / sqrt(|q|^2 + 1e-6) and
     k / sqrt(|k|^2 + 1e-6) for q and k. ``scale`` is K ** -0.5 unless given.
 
@@ -113,13 +113,12 @@ def gated_delta_backward(grad_y, q, k, v, delta, beta, A=None, delta_bias=None, 
     """Gradients of ``gated_delta`` (same arguments) for grad_y [S,B,H,V] and, if
     the final state went into the loss, grad_final_state [B,H,V,K]. Returns
     ``GatedDeltaGrads(q, k, v, delta, beta, A, delta_bias, state)`` with None
-    where the argument was None; A, delta_bias and state are fp32."""
+    where the argument was None; A, delta_bias and state are fp32. Without delta
+    nothing depends on A and delta_bias: zeros."""
     _load()
     fwd = _fields(q, k, v, delta, beta, A, delta_bias, delta_softplus, beta_sigmoid, qk_norm, scale, lengths, state, None, None)
     (S, B), G, K, H, V, _, index = _leading(q, v, 4)
     device, dt, f32 = q.device, q.dtype, _base._torch.float32
-    if delta_bias is not None and delta is None:
-        raise ValueError("delta_bias needs delta")
     handle, stream = _stream(stream, index)
     at = _rows(grad_y, "grad_y", (S, B, H, V), dt, index), *grad_y.stride()[:3]
     at_final = _optional(grad_final_state, "grad_final_state", (B, H, V, K), f32, index)
@@ -128,9 +127,15 @@ def gated_delta_backward(grad_y, q, k, v, delta, beta, A=None, delta_bias=None, 
         return _empty(shape, dtype, device, stream) if like is not None else None
 
     g = GatedDeltaGrads(out(q, (S, B, G, K), dt), out(k, (S, B, G, K), dt), out(v, (S, B, H, V), dt), out(delta, (S, B, H), dt),
-                        out(beta, (S, B, H), dt), out(delta, (H,), f32), out(delta_bias, (H,), f32), out(state, (B, H, V, K), f32))
-    args = _pack_bwd(*fwd, *at, at_final, *[0 if t is None else t.data_ptr() for t in g])
+                        out(beta, (S, B, H), dt), out(A, (H,), f32), out(delta_bias, (H,), f32), out(state, (B, H, V, K), f32))
+    made = g if delta is not None else g._replace(A=None, delta_bias=None)      # without delta nothing depends on them
+    args = _pack_bwd(*fwd, *at, at_final, *[0 if t is None else t.data_ptr() for t in made])
     _call_ws("mcc1d_delta_bwd", args, handle, stream, device)
+    if delta is None and (A is not None or delta_bias is not None):
+        with _base._torch.cuda.stream(stream):      # None: the current one
+            for t in (g.A, g.delta_bias):
+                if t is not None:
+                    t.zero_()
     if stream is not None:
         _record(stream, index, (grad_y, q, k, v, delta, beta, A, delta_bias, lengths, state, grad_final_state), g)
     return g

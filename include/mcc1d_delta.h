@@ -7,7 +7,7 @@
  * heads of queries and keys. For every sequence and head, token by token:
  *
  *   a(t) = exp(A dt(t)),  dt(t) = softplus(delta(t) + delta_bias)   (MCC1D_SOFTPLUS),
- *          or delta(t) + delta_bias; 1 without delta
+ *          or delta(t) + delta_bias; 1 without delta (A and delta_bias are not read)
  *   b(t) = sigmoid(beta(t))   (MCC1D_SIGMOID), or beta(t)
  *   k'(t) = k(t) / sqrt(|k(t)|^2 + 1e-6),  q'(t) = scale q(t) / sqrt(|q(t)|^2 + 1e-6)
  *          (MCC1D_QK_NORM), or k(t) and scale q(t)
