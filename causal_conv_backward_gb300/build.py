@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 
@@ -42,6 +43,22 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def launch_registers(src: str) -> int:
+    """The registers a thread that a source's kernels start with and share out again
+    (setmaxnreg), 0 for sources that leave them as they are."""
+    with open(src) as f:
+        m = re.search(r"\bkRegLaunch = (\d+)", f.read())
+    return int(m.group(1)) if m else 0
+
+
+def check_registers(src: str, log: str) -> None:
+    """Such kernels refuse to be launched with any other number: one that the
+    compiler gave another fails here, not at its first call."""
+    want, used = launch_registers(src), [int(n) for n in re.findall(r"Used (\d+) registers", log)]
+    if want and (not used or any(n != want for n in used)):
+        raise RuntimeError(f"{os.path.basename(src)}: its kernels are written for {want} registers a thread, the compiler used {used}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA/C++ source of the library for sm_103a; returns the .so path."""
     if not force and not _stale():
@@ -52,7 +69,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmds = []
     for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        extra = ["-Xptxas", "-v"] if (verbose and src.endswith(".cu")) else []
+        extra = ["-Xptxas", "-v"] if src.endswith(".cu") and (verbose or launch_registers(src)) else []
         cmds.append([nvcc, *ARCH, *COMMON, *extra, "-c", src, "-o", obj])
         objs.append(obj)
 
@@ -63,11 +80,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return r.stdout + r.stderr
 
     # biggest translation units first, so they start early
-    order = sorted(range(len(cmds)), key=lambda k: -os.path.getsize(sources()[k]))
+    srcs = sources()
+    order = sorted(range(len(cmds)), key=lambda k: -os.path.getsize(srcs[k]))
     cmds = [cmds[k] for k in order]
     objs = [objs[k] for k in order]
     with cf.ThreadPoolExecutor(max_workers=len(cmds)) as ex:
         logs = list(ex.map(run, cmds))
+    for k, log in zip(order, logs):
+        check_registers(srcs[k], log)
     if verbose:
         print("".join(logs))
     tmp = LIB + f".tmp{os.getpid()}"
