@@ -1,13 +1,12 @@
 // delta_prepare.cu - a chunk's products of tokens with tokens.
 //
 // With c(t) the running sum of log a, D(t,i) = exp(c(t) - c(i)):
-//   L(t,i) = b(t) (k'(t).k'(i)), i < t;   P(t,i) = q'(t).k'(i), i <= t
-//   T = (I + L)^-1,   so that U = (D T) R for R = b (V - e^c K' S^T),  and the tokens' part
-//   of Y is (D P T) R: each path from i to t passes through the same decays, so that
-//   they multiply the finished matrices, value by value.
-// D T and D P T (T and P T elsewhere) leave as two fp16 terms each (22 bits), rows
-// scaled by powers of two, in the layout that delta_chunks.cu multiplies from, for an
-// R that a token's growth has been taken out of (growth_of).
+//   L(t,i) = b(t) D (k'(t).k'(i)), i < t;   P(t,i) = D (q'(t).k'(i)), i <= t
+//   T = (I + L)^-1,   so that U = T R for R = b (V - e^c K' S^T),  and P U = (P T) R
+// T and P T leave as two fp16 terms each (22 bits), rows scaled by powers of two,
+// in the layout that delta_chunks.cu multiplies from, for an R that a token's growth
+// has been taken out of (growth_of). All paths from i to t pass the same decays, so that
+// powers of two by token change those of T and P T value by value.
 //
 // k'.k' and q'.k' are taken of the 16-bit tensors themselves on the tensor cores
 // (their products are exact in fp32) and scaled afterwards. The inverse is that
@@ -46,7 +45,7 @@ struct PrepareShared {
         };
     };
     float L[kC][kRow], P[kC][kRow];
-    float ch[kC], cl[kC], rest[kC], b[kC], f[2][kC], m[2][kC], lk[kC], late[kC], of_t[kC], sum_t[kC], of_p[kC], ends[4][8];
+    float ch[kC], cl[kC], rest[kC], grown[kC], b[kC], f[2][kC], m[2][kC], lk[kC], late[kC], whole[kC], of_t[kC], sum_t[kC], of_p[kC], ends[4][8];
     bool zero_q[kC];
     uint32_t bad_gates[2];
     int bad_k[4];
@@ -135,6 +134,8 @@ __device__ __forceinline__ float most_of_row(const float (&x)[16], float &sum)
     return most;
 }
 
+// The whole powers of two of e^c, of which T is a quotient.
+__device__ __forceinline__ float whole_of(float c) { return fminf(fmaxf(rintf(c), -100.f), 126.f); }
 // What is taken out of a token's R and put back by its column of T and P T, as a
 // power of two, from the logarithm c of all decays up to it. Two terms hold a row to
 // 2^-40 of its largest value, and a token's R has two parts, its value and the
@@ -261,8 +262,10 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
     int good = min(min(sh.bad_k[0], sh.bad_k[1]), min(sh.bad_k[2], sh.bad_k[3]));
     if (sh.bad_gates[0] | sh.bad_gates[1])
         good = min(good, sh.bad_gates[0] ? __ffs(sh.bad_gates[0]) - 1 : 31 + __ffs(sh.bad_gates[1]));
-    if (tid < kC)
-        sh.rest[tid] = sh.ch[tid] - growth_of(sh.ch[tid] + sh.cl[tid]);
+    if (tid < kC) {
+        const float growth = growth_of(sh.ch[tid] + sh.cl[tid]);
+        sh.rest[tid] = sh.ch[tid] - growth, sh.grown[tid] = ex2(growth);
+    }
     {   // 16 rows and 32 columns of both products to a warp
         const int r0 = 16 * (warp % 4), c0 = 32 * (warp / 4), row = lane / 4, col = 2 * (lane % 4);
         float kk[4][4] = {}, qk[4][4] = {};
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = r0 + row + 8 * half;
-            const float lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
+            const float th = sh.ch[t], tl = sh.cl[t], lt = sh.b[t] * sh.f[1][t], pt = p.scale * sh.f[0][t];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (c0 + 8 * j > r0 + 15)          // above the diagonal: read by nothing
@@ -297,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = c0 + 8 * j + col + e;
-                    l[e] = i < t && t < good ? kk[j][2 * half + e] * (sh.f[1][i] * lt) : 0.f;
-                    x[e] = i <= t && t < good ? qk[j][2 * half + e] * (sh.f[1][i] * pt) : 0.f;
+                    const float D = i <= t ? ex2_held((th - sh.ch[i]) + (tl - sh.cl[i])) * sh.f[1][i] : 0.f;
+                    l[e] = i < t && t < good ? kk[j][2 * half + e] * (D * lt) : 0.f;
+                    x[e] = i <= t && t < good ? qk[j][2 * half + e] * (D * pt) : 0.f;
                 }
                 *reinterpret_cast<float2 *>(&sh.L[t][c0 + 8 * j + col]) = make_float2(l[0], l[1]);
                 *reinterpret_cast<float2 *>(&sh.P[t][c0 + 8 * j + col]) = make_float2(x[0], x[1]);
@@ -364,31 +368,27 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
                 *reinterpret_cast<float2 *>(&sh.X[r0 + row + 8 * e][8 * (2 * j + warp / 4) + 2 * col]) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
     }
     __syncthreads();
-    // four threads to a row; the decays come in here
+    // four threads to a row
     {
         const int t = tid / 4, part = tid % 4;
-        const float th = sh.ch[t], tl = sh.cl[t];
-        float x[16], D[16];
-        const auto row_of = [&](const float (*m)[kRow], const float (&by)[16]) {
+        float x[16];
+        const auto row_of = [&](const float (*m)[kRow]) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]);
-                x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+                const float4 v = *reinterpret_cast<const float4 *>(&m[t][16 * part + j]), f = *reinterpret_cast<const float4 *>(&sh.grown[16 * part + j]);
+                x[j] = v.x * f.x, x[j + 1] = v.y * f.y, x[j + 2] = v.z * f.z, x[j + 3] = v.w * f.w;
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                x[j] = 16 * part + j <= t ? x[j] * by[j] : 0.f;       // nothing is written behind the diagonal
+                x[j] = 16 * part + j <= t ? x[j] : 0.f;       // nothing is written behind the diagonal
         };
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            D[j] = ex2_held((th - sh.rest[16 * part + j]) + (tl - sh.cl[16 * part + j]));
-        row_of(sh.T, D);
+        row_of(sh.T);
         float sum, scale = scale_for(most_of_row(x, sum));
         store_terms(x, scale, out + kAtT, out + kAtTLo, t, part);
         if (part == 0)
             sh.of_t[t] = inverse_scale(scale), sh.sum_t[t] = sum;
         if (!BACK) {
-            row_of(sh.X, D);
+            row_of(sh.X);
             scale = scale_for(most_of_row(x, sum));
             store_terms(x, scale, out + kAtPT, out + kAtPTLo, t, part);
             if (part == 0)
@@ -396,25 +396,30 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         }
     }
     if (BACK) {
-        // T as it is and P T with the decays behind it; these sum over their rows, so
-        // that each column is scaled. What takes a growth out of grad_y's rows
-        // (from the token to the end) is put into those of P T.
+        // T without the decays (G's part passes all of them, whatever token it goes
+        // through) and P T; these sum over their rows, so that each column is scaled. What
+        // takes a growth out of grad_y's rows (from the token to the end) is put into
+        // those of P T, and the decays' powers of two taken out of T, as far as 2^-100.
         float (*most)[kRow] = sh.L, (*scales)[kRow] = sh.L + 8;          // L is not read any more
         const int i = tid % kC, first = 16 * (tid / kC);
-        if (tid < kC)
+        float *late = sh.L[10], *by = sh.L[11], *to = sh.L[12];
+        if (tid < kC) {
+            const float w = whole_of(sh.ch[tid] + sh.cl[tid]);
             sh.late[tid] = growth_of((sh.ch[kC - 1] - sh.ch[tid]) + (sh.cl[kC - 1] - sh.cl[tid]));
+            late[tid] = ex2(sh.late[tid]), sh.whole[tid] = w, by[tid] = ex2(-w), to[tid] = ex2(w);
+        }
         __syncthreads();
         {
             float most_t = 0.f, most_p = 0.f;
             if (first + 15 >= i) {
-                const float ih = sh.ch[i], il = sh.cl[i];
+                const float to_i = to[i];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = first + e;
                     if (j >= i) {
-                        const float v = sh.X[j][i] * ex2_held((sh.ch[j] + sh.late[j] - ih) + (sh.cl[j] - il));
-                        most_t = fmaxf(most_t, fabsf(sh.T[j][i])), most_p = fmaxf(most_p, fabsf(v));
-                        sh.X[j][i] = v;
+                        const float v = sh.T[j][i] * by[j] * to_i, w = sh.X[j][i] * late[j];
+                        most_t = fmaxf(most_t, fabsf(v)), most_p = fmaxf(most_p, fabsf(w));
+                        sh.T[j][i] = v, sh.X[j][i] = w;
                     }
                 }
             }
@@ -454,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         const float none = __uint_as_float(0x7FFFFFFFu);
         const bool there = t < good;
         const float ec = ex2_held(th + tl), decay = good < kC ? none : decay_of(end > 127.f ? 127.f : end);
-        const float el = back && good < kC ? none : ex2_held((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl));
         // a row of zeros adds nothing, and must not lower the others' scale
         const float k = sh.lk[t] != 0.f ? sh.f[1][t] * inverse_scale(sh.m[1][t]) : 0.f;
         const float q = sh.zero_q[t] ? 0.f : sh.f[0][t] * p.scale * inverse_scale(sh.m[0][t]);
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
         to[kFactorScaleK * kC] = sh.m[1][t];
         to[kFactorScaleQ * kC] = sh.m[0][t];
         if (!back) {
-            const float rest = ex2_held(sh.rest[t] + tl), of = sh.of_t[t];
+            const float rest = ex2_held(sh.rest[t] + tl), el = ex2_held((sh.ch[kC - 1] - th) + (sh.cl[kC - 1] - tl)), of = sh.of_t[t];
             to[kFactorB * kC] = there ? b * ex2(sh.rest[t] - th) : 0.f;
             to[kFactorX * kC] = there ? b * rest * k : 0.f;
             to[kFactorU * kC] = of * el * k;
@@ -476,17 +480,18 @@ __global__ void __launch_bounds__(kThreads, 3) mcc1d_delta_prepare_chunk(const _
             if (lane == 0)
                 sh.ends[warp][0] = most[0], sh.ends[warp][1] = most[1], sh.ends[warp][5] = decay;
         } else {
-            const float most_t = sh.L[0][t], of_t = inverse_scale(sh.L[8][t]), of_p = good < kC ? none : inverse_scale(sh.L[9][t]), bk = b * k;
-            const float fq = ex2_held(th + sh.late[t] + tl) * q;
+            const float most_t = sh.L[0][t], of_t = good < kC ? none : inverse_scale(sh.L[8][t]), of_p = good < kC ? none : inverse_scale(sh.L[9][t]), bk = b * k;
+            const float fq = ex2_held(th + sh.late[t] + tl) * q, w = sh.whole[t], w_end = sh.whole[kC - 1];
+            const float fx = bk * ex2_held(th - w + w_end + tl), fu = ex2_held(((sh.ch[kC - 1] - w_end) - (th - w)) + (sh.cl[kC - 1] - tl));
             to[kFactorB * kC] = b;
-            to[kFactorX * kC] = bk * decay * of_t;
+            to[kFactorX * kC] = fx * of_t;
             to[kFactorXY * kC] = bk * ec * of_p;
-            to[kFactorU * kC] = k;
-            to[kFactorT * kC] = el * of_t;
+            to[kFactorU * kC] = fu * k;
+            to[kFactorT * kC] = ex2_held(w_end - w) * of_t;
             to[kFactorP * kC] = of_p;
             to[kFactorQ * kC] = fq;
             to[kFactorY * kC] = ex2(-sh.late[t]);
-            const float most[5] = {most_of_warp(reach), most_of_warp(most_t), most_of_warp(fabsf(bk) * decay), most_of_warp(fabsf(bk) * ec * (kC * sh.L[4][t])),
+            const float most[5] = {most_of_warp(fu * reach), most_of_warp(most_t), most_of_warp(fabsf(fx)), most_of_warp(fabsf(bk) * ec * (kC * sh.L[4][t])),
                                    most_of_warp(fabsf(fq))};
             if (lane == 0)
 #pragma unroll

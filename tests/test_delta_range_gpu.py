@@ -174,3 +174,27 @@ def test_states_that_fade_to_nothing(rate):
     near(y[500:], late, 32 + 256, of_row(late), "y")
     near(final, rf, 32 + 256, rf.abs().amax((-1, -2), keepdim=True), "final state")
     assert (to64(y[:500]) - ry[:500].detach()).abs().max() < 2.0 ** -8 * float(ry[:500].detach().abs().max())
+
+
+@pytest.mark.parametrize("what", ["one key", "any keys"])
+@pytest.mark.parametrize("S", [64, 150])
+def test_keys_that_decays_hold(what, S):
+    """Keys that are not divided by their lengths: b |k|^2 = 6 turns a state along
+    the key round to five times itself, 2^148 in a chunk of one key, and the decay
+    of 1/8 a token holds it."""
+    t, gy, gf = inputs([-3.0] * S)
+    t["k"] = (t["k"].float() / t["k"].float().norm(dim=-1, keepdim=True) * 6 ** 0.5).to(BF16)
+    if what == "one key":
+        t["k"] = t["k"][:1].expand_as(t["k"])
+    t["beta"], forms = torch.ones_like(t["beta"]), dict(delta_softplus=False, beta_sigmoid=False, qk_norm=False)
+    K, V = 32, 24
+    args = [t[k] for k in ("q", "k", "v", "delta", "beta", "A")]
+    d = {k: to64(v, grad=True) for k, v in t.items()}
+    ry, rf = ref.delta_rule(d["q"], d["k"], d["v"], d["delta"], d["beta"], d["A"], None, False, False, False, state=d["state"])
+    y, final = m.gated_delta(*args, state=t["state"], return_state=True, **forms)
+    near(y, ry, K + 256, of_row(ry), "y")
+    near(final, rf, K + 256, rf.abs().amax((-1, -2), keepdim=True), "final state")
+    got = m.gated_delta_backward(gy, *args, state=t["state"], grad_final_state=gf, **forms)
+    names = ("q", "k", "v", "state")
+    for k, want in zip(names, torch.autograd.grad((ry * to64(gy)).sum() + (rf * to64(gf)).sum(), [d[k] for k in names])):
+        near(getattr(got, k), want, 2 * V * K + 256, of_row(want) if k != "state" else want.abs().amax((-1, -2), keepdim=True), "grad " + k)
