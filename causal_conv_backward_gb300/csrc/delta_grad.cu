@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) mcc1d_delta_grad_chunk(const __gr
     const float f = of_du ? sh.fk[t] : sh.fq[t], fx = of_du ? sh.xk[t] : sh.xq[t];
     dot = (sh.most[0][r] + sh.most[1][r]) + (sh.most[2][r] + sh.most[3][r]);
     // q' is scale times a unit vector
-    const float unit = of_du ? 1.f : p.scale != 0.f ? 1.f / (p.scale * p.scale) : 0.f;
-    const float back = p.flags & MCC1D_QK_NORM ? -dot * fx * fx * unit : 0.f;
+    const float along = of_du ? fx : p.scale != 0.f ? fx / p.scale : 0.f;
+    const float back = p.flags & MCC1D_QK_NORM ? -dot * along * along : 0.f;
     if (t < there) {
         uint16_t *to = (of_du ? gp.grad_k : gp.grad_q) + (((t0 + t) * p.B + b) * p.G + g) * p.K;
 #pragma unroll
