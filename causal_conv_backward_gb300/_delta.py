@@ -55,6 +55,10 @@ def _flags(delta_softplus, beta_sigmoid, qk_norm):
     return (SOFTPLUS if delta_softplus else 0) | (SIGMOID if beta_sigmoid else 0) | (QK_NORM if qk_norm else 0)
 
 
+def _scale(K, scale):
+    return scale if scale is not None else K ** -0.5 if K else 1.0      # no keys: refused below
+
+
 def _leading(q, v, dims):
     """The sizes S, B (of prompts), G, K, H, V in front, and q's dtype code and device."""
     shape, code, index = _first(q, "q", dims)
@@ -74,7 +78,7 @@ def _fields(q, k, v, delta, beta, A, delta_bias, softplus, sigmoid, norm, scale,
             _rows(beta, "beta", (S, B, H), dt, index), beta.stride(0), beta.stride(1), _optional(A, "A", (H,), f32, index),
             _optional(delta_bias, "delta_bias", (H,), f32, index), _optional(state, "state", (B, H, V, K), f32, index),
             _optional(lengths, "lengths", (B,), _base._torch.int32, index), _optional(y, "y", (S, B, H, V), dt, index),
-            0 if final is None else final.data_ptr(), S, B, H, G, K, V, K ** -0.5 if scale is None else scale, code,
+            0 if final is None else final.data_ptr(), S, B, H, G, K, V, _scale(K, scale), code,
             _flags(softplus, sigmoid, norm))
 
 
@@ -163,7 +167,7 @@ def gated_delta_step(q, k, v, delta, beta, state, A=None, delta_bias=None, *, de
                       *((0, 0) if delta is None else (_rows(delta, "delta", (B, H), dt, index), delta.stride(0))),
                       _rows(beta, "beta", (B, H), dt, index), beta.stride(0), _optional(A, "A", (H,), f32, index),
                       _optional(delta_bias, "delta_bias", (H,), f32, index), cache, at, _dense(y, "y", (B, H, V), dt, index),
-                      rows, B, H, G, K, V, K ** -0.5 if scale is None else scale, code, _flags(delta_softplus, beta_sigmoid, qk_norm))
+                      rows, B, H, G, K, V, _scale(K, scale), code, _flags(delta_softplus, beta_sigmoid, qk_norm))
     _call("mcc1d_delta_step", args, handle)
     if stream is not None:
         _record(stream, index, (q, k, v, delta, beta, state, A, delta_bias, slots), (y,))

@@ -25,7 +25,7 @@ int32_t check(const mcc1d_delta_args *a, bool out)
 {
     if (!a || !a->q || !a->k || !a->v || !a->beta || (a->delta && !a->A) || (out && !a->y))
         return kErrNull;
-    if ((a->dtype != 0 && a->dtype != 1) || (a->flags & ~kFlags) || !std::isfinite(a->scale))
+    if ((a->dtype != 0 && a->dtype != 1) || (a->flags & ~kFlags) || !std::isfinite((float)a->scale))
         return kErrInvalid;
     if (!shape_ok(a->S, a->B, a->H) || !heads_ok(a->B, a->H, a->G, a->K, a->V))
         return kErrShape;
@@ -58,7 +58,7 @@ int32_t check(const mcc1d_delta_step_args *a)
 {
     if (!a || !a->q || !a->k || !a->v || !a->beta || (a->delta && !a->A) || !a->state || !a->y)
         return kErrNull;
-    if ((a->dtype != 0 && a->dtype != 1) || (a->flags & ~kFlags) || !std::isfinite(a->scale))
+    if ((a->dtype != 0 && a->dtype != 1) || (a->flags & ~kFlags) || !std::isfinite((float)a->scale))
         return kErrInvalid;
     if (!shape_ok(1, a->B, a->H) || !heads_ok(a->B, a->H, a->G, a->K, a->V) || a->cache_rows < 1 || (!a->slots && a->cache_rows < a->B))
         return kErrShape;

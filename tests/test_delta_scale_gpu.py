@@ -24,3 +24,13 @@ def test_scales(S, scale):
     got = m.gated_delta_backward(gy, *args, state=t["state"], scale=scale, **FORMS)
     for k, want in zip(NAMES, torch.autograd.grad((ry * to64(gy)).sum(), [leaves[k] for k in NAMES])):
         check(getattr(got, k), want, S * B * 64 if k in ("A", "delta_bias") else K * V + 256, k)
+
+
+def test_no_keys_are_refused():
+    t, _, _, _ = inputs(9, 2, 4, 2, 16, 16)
+    q = t["q"][..., :0]
+    for call in (lambda: m.gated_delta(q, q, t["v"], t["delta"], t["beta"], t["A"]),
+                 lambda: m.gated_delta_backward(t["v"], q, q, t["v"], t["delta"], t["beta"], t["A"]),
+                 lambda: m.gated_delta_step(q[0], q[0], t["v"][0], t["delta"][0], t["beta"][0], t["state"][..., :0], t["A"])):
+        with pytest.raises(m.Mcc1dError):
+            call()
