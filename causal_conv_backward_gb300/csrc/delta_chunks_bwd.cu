@@ -8,7 +8,7 @@
 //   D0 = G K^T,  dU through the later tokens: dR = e^(c(end)-c) D0 T + grad_y (P T)    (tokens along the columns)
 //   grad_v = b dR
 //   G = e^c(end) G + grad_y^T (e^c Q) - (dR b e^c) K
-// grad_y is exact in fp16 (a chunk's values scaled by a power of two, rows that grow
+// grad_y is exact in fp16 (each row's values scaled by a power of two, tokens that grow
 // on their way to the end or fade by another: growth_of in delta_prepare.cu) and is
 // multiplied from shared memory; e^c Q is two fp16 terms there. The chain is
 // G - D0 - dR - G, and bounds the kernel; the products with grad_y run in its gaps.
@@ -54,10 +54,11 @@ enum { kX = 0, kU = 64, kYP = 128, kYQ = 192, kGHi = 320, kGLo = 384, kWHi = 448
 struct BackShared {
     uint64_t full[kStages], empty[kStages], tiles[kStages], x, r, u, v, s, end, out;
     float of_u[2][kRows];                       // of the last two chunks: what a row's sums are multiplied by
-    alignas(8) float of_out[4][3 * kC];                    // of the last four chunks: the factors of G's and of grad_y's part of dR, b
-    float of_y[4], of_q[4], most_y[4];          // grad_y's factor (0 where there is none), Q's, the largest |grad_y|
+    alignas(16) float of_out[4][3 * kC];                   // of the last four chunks: the factors of G's and of grad_y's part of dR, b
+    alignas(16) float of_y[4][kRows], most_y[4][kRows];     // grad_y's factor (0 where there is none), and its largest, by rows
+    float of_q[4];                              // Q's factor
     float most[kParts][kRows], sum_r[kParts][kRows];
-    float most_of_warps[2][kLoadWarps];
+    alignas(16) float most_of_warps[2][kLoadWarps][kRows];
     uint32_t tmem, failed;
 };
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
         }
         const float of_s = inverse_scale(scale_s), most_s = most_of_parts(sh.most, r) * of_s;
         const float scale_u = scale_for(ends[kEndOfGrad] * most_s), of_u = inverse_scale(scale_u);
-        const float scale_r = scale_for(fmaf(ends[kEndDuOfGrad], most_s, ends[kEndDuOfY] * sh.most_y[i & 3])), of_r = inverse_scale(scale_r);
+        const float scale_r = scale_for(fmaf(ends[kEndDuOfGrad], most_s, ends[kEndDuOfY] * sh.most_y[i & 3][r])), of_r = inverse_scale(scale_r);
         if (part == 0)
             sh.of_u[parity][r] = of_u;
         ok = ok && warp_wait(sh.x, parity);
@@ -157,7 +158,7 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
             tmem_load(lanes + kYP + HC * part, yp);
             tmem_wait(raw), tmem_wait(yp);
             const float2 mu = make_float2(-of_u * scale_r, -of_u * scale_r);
-            const float of_y = -sh.of_y[i & 3] * scale_r;
+            const float of_y = -sh.of_y[i & 3][r] * scale_r;
             const float2 my = make_float2(of_y, of_y);
 #pragma unroll
             for (int t = 0; t < HC; t += 2) {
@@ -173,9 +174,9 @@ __device__ __forceinline__ void hold_rows(const BackParams &cp, BackShared &sh, 
         terms_done(sh.v);
         rows_meet();     // for sum_r, while the products run
         // |G| <= e^c(end) |G| + sum of |dR k| + 64 |grad_y| |q|, and no |k|, |q| is above 2^16 as an operand
-        const float before = scale_s, end = ends[kEndDecay], of_q = sh.of_q[i & 3], of_yq = sh.of_y[i & 3] * of_q;
+        const float before = scale_s, end = ends[kEndDecay], of_q = sh.of_q[i & 3], of_yq = sh.of_y[i & 3][r] * of_q;
         scale_s = scale_for(fmaf(fabsf(end), most_s, ((sh.sum_r[0][r] + sh.sum_r[1][r]) + (sh.sum_r[2][r] + sh.sum_r[3][r])) * of_r * 65536.f) +
-                            sh.most_y[i & 3] * (kC * 65536.f) * of_q);
+                            sh.most_y[i & 3][r] * (kC * 65536.f) * of_q);
         const float2 keep = make_float2(end * inverse_scale(before) * scale_s, end * inverse_scale(before) * scale_s);
         warp_arrive(sh.empty[i % kStages]);
         const float2 add = make_float2(of_r * scale_s, of_r * scale_s), add_y = make_float2(of_yq * scale_s, of_yq * scale_s);
@@ -223,7 +224,7 @@ __device__ __forceinline__ void write_rows(const BackParams &cp, BackShared &sh,
             break;
         tmem_fence_after();
         const int64_t t0 = (pt.first + chunks - 1 - i) * kC;
-        const float of_u = sh.of_u[i & 1][r], of_y = sh.of_y[i & 3];
+        const float of_u = sh.of_u[i & 1][r], of_y = sh.of_y[i & 3][r];
         const float *fg = sh.of_out[i & 3], *fy = fg + kC, *bt = fy + kC;
         const int live = (int)(n - t0 < kC ? n - t0 : kC), rows = (int)(p.S - t0 < kC ? p.S - t0 : kC);
         const bool whole = cp.pairs_v && rows == kC && live == kC;
@@ -395,43 +396,67 @@ __device__ __forceinline__ void make_tiles(const BackParams &cp, BackShared &sh,
         const float *f = reinterpret_cast<const float *>(stage + St::kPrepared + kAtBackFactors);
         if (!warp_wait(sh.tiles[i % kStages], (uint32_t)(i / kStages) & 1))
             break;
-        // grad_y: its largest value first
+        // grad_y: the largest value of each row first; a thread has eight rows of every STEP_Yth token
         constexpr int PIECES_Y = kRows / 8, STEP_Y = kLoadThreads / PIECES_Y, PIECES = KP / 8, STEP = kLoadThreads / PIECES;
+        static_assert(PIECES_Y == 16, "two lanes of a warp to the same rows");
         const uint16_t *gy = p.grad_y + t0 * p.gy_s[0] + b * p.gy_s[1] + h * p.gy_s[2] + v0;
         const int piece_y = thread % PIECES_Y, live_y = p.V - v0 - 8 * piece_y;
         uint8_t *panel_y = stage + St::Y + (piece_y / 8) * kPanelBytes;
-        float most = 0.f;
-#pragma unroll 2
-        for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
-            uint8_t *at = panel_y + panel_at(t, piece_y % 8);
-            // magnitudes are in the order of their bits
-            const uint4 v = piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0);
-            const float2 two = unpack2<DT>(__vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-            most = fmaxf(most, fmaxf(two.x, two.y) * f[kFactorY * kC + t]);
+        float2 scale[4];
+        {
+            float2 most[4] = {};
+#pragma unroll 1
+            for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
+                float2 x[4];
+                unpack8<DT>(piece_of(panel_y + panel_at(t, piece_y % 8), gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
+                const float2 by = make_float2(f[kFactorY * kC + t], f[kFactorY * kC + t]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = mul2(x[e], by);
+                    most[e] = make_float2(fmaxf(most[e].x, fabsf(x[e].x)), fmaxf(most[e].y, fabsf(x[e].y)));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                most[e] = make_float2(fmaxf(most[e].x, __shfl_xor_sync(0xFFFFFFFFu, most[e].x, 16)), fmaxf(most[e].y, __shfl_xor_sync(0xFFFFFFFFu, most[e].y, 16)));
+            float4 *to = reinterpret_cast<float4 *>(&sh.most_of_warps[i & 1][thread / 32][8 * piece_y]);
+            if (thread % 32 < 16)
+                to[0] = make_float4(most[0].x, most[0].y, most[1].x, most[1].y), to[1] = make_float4(most[2].x, most[2].y, most[3].x, most[3].y);
+            asm volatile("bar.sync 2, %0;" ::"n"(kLoadThreads) : "memory");
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kLoadWarps; ++w) {
+                    const float4 o = reinterpret_cast<const float4 *>(&sh.most_of_warps[i & 1][w][8 * piece_y])[half];
+                    m = make_float4(fmaxf(m.x, o.x), fmaxf(m.y, o.y), fmaxf(m.z, o.z), fmaxf(m.w, o.w));
+                }
+                // times a token's factor, and still a number
+                const auto of = [](float most) { return fminf(scale_for(most), 0x1p100f); };
+                scale[2 * half] = make_float2(of(m.x), of(m.y)), scale[2 * half + 1] = make_float2(of(m.z), of(m.w));
+                if (thread < PIECES_Y) {
+                    const auto back = [](float most, float scale) { return most == 0.f ? 0.f : inverse_scale(scale); };
+                    reinterpret_cast<float4 *>(&sh.most_y[i & 3][8 * piece_y])[half] = m;
+                    reinterpret_cast<float4 *>(&sh.of_y[i & 3][8 * piece_y])[half] =
+                        make_float4(back(m.x, scale[2 * half].x), back(m.y, scale[2 * half].y), back(m.z, scale[2 * half + 1].x), back(m.w, scale[2 * half + 1].y));
+                }
+            }
         }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2)
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        if (thread % 32 == 0)
-            sh.most_of_warps[i & 1][thread / 32] = most;
-        asm volatile("bar.sync 2, %0;" ::"n"(kLoadThreads) : "memory");
-        most = sh.most_of_warps[i & 1][0];
-#pragma unroll
-        for (int w = 1; w < kLoadWarps; ++w)
-            most = fmaxf(most, sh.most_of_warps[i & 1][w]);
-        const float scale_y = fminf(scale_for(most), 0x1p100f);      // times a token's factor, and still a number
         const float scale_q = scale_for(f[kFactorEnd * kC + kEndMostQ] * 32768.f);       // rows of q are below 2^15 as operands
-        if (thread == 0) {
-            sh.of_y[i & 3] = most == 0.f ? 0.f : inverse_scale(scale_y), sh.of_q[i & 3] = inverse_scale(scale_q), sh.most_y[i & 3] = most;
-        }
+        if (thread == 0)
+            sh.of_q[i & 3] = inverse_scale(scale_q);
         if (thread < 3 * kC)
             sh.of_out[i & 3][thread] = f[(thread < kC ? kFactorT : thread < 2 * kC ? kFactorP : kFactorB) * kC + thread % kC];
-#pragma unroll 2
+#pragma unroll 1
         for (int t = thread / PIECES_Y; t < kC; t += STEP_Y) {
             uint8_t *at = panel_y + panel_at(t, piece_y % 8);
             float2 x[4];
             unpack8<DT>(piece_of(at, gy + t * p.gy_s[0] + 8 * piece_y, cp.vectors_y, t < live ? live_y : 0), x);
-            *reinterpret_cast<uint4 *>(at) = scaled_half(x, scale_y * f[kFactorY * kC + t]);
+            const float2 by = make_float2(f[kFactorY * kC + t], f[kFactorY * kC + t]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = mul2(x[e], mul2(scale[e], by));
+            *reinterpret_cast<uint4 *>(at) = make_uint4(pack_half2(x[0]), pack_half2(x[1]), pack_half2(x[2]), pack_half2(x[3]));
         }
         const int piece = thread % PIECES, live_k = p.K - 8 * piece;
         const uint16_t *k = p.k + t0 * p.k_s[0] + b * p.k_s[1] + g * p.k_s[2] + 8 * piece, *q = p.q + t0 * p.q_s[0] + b * p.q_s[1] + g * p.q_s[2] + 8 * piece;
