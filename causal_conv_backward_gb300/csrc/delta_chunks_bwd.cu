@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kStages = 2;
 // Registers by warpgroup: rows (four), the ones that write, and two for the rest.
-constexpr int kRegRows = 72, kRegOut = 112, kRegRest = 48, kRegLaunch = 72;
+constexpr int kRegRows = 72, kRegOut = 96, kRegRest = 56, kRegLaunch = 72;
 static_assert(kParts * kRegRows + kRegOut + 2 * kRegRest <= kThreads / 128 * kRegLaunch && kRegRows == kRegLaunch, "what the block is launched with");
 
 struct BackParams {
