@@ -151,14 +151,15 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 }
 
 // ------------------------------------------------------------------ two terms
-// The power of two that takes a largest magnitude to 2^14..2^15 (1 for zero,
-// infinity and NaN), and its reciprocal. A value times it is hi + lo, two fp16
+// The power of two that takes a largest magnitude to 2^14..2^15 (1 for zero; for
+// infinity, which a bound may be where no value is, what takes the largest number
+// there), and its reciprocal. A value times it is hi + lo, two fp16
 // numbers, with 22 bits from the largest down to 2^-24 of it, and an absolute
 // error of 2^-40 of the largest below.
 __device__ __forceinline__ float scale_for(float largest)
 {
     const int e = (int)(__float_as_uint(largest) >> 23);         // sign 0
-    return e == 0 || e >= 255 ? 1.f : __uint_as_float((uint32_t)min(268 - e, 253) << 23);
+    return e == 0 ? 1.f : __uint_as_float((uint32_t)min(268 - min(e, 254), 253) << 23);
 }
 __device__ __forceinline__ float inverse_scale(float scale)
 {

@@ -198,3 +198,17 @@ def test_keys_that_decays_hold(what, S):
     names = ("q", "k", "v", "state")
     for k, want in zip(names, torch.autograd.grad((ry * to64(gy)).sum() + (rf * to64(gf)).sum(), [d[k] for k in names])):
         near(getattr(got, k), want, 2 * V * K + 256, of_row(want) if k != "state" else want.abs().amax((-1, -2), keepdim=True), "grad " + k)
+
+
+@SHAPES
+@pytest.mark.parametrize("part", [OUT, STATES], ids=["outputs", "states"])
+@pytest.mark.parametrize("size", [100, 110, 116, 120])
+def test_states_near_the_largest(K, V, part, size):
+    """States and gradients some 2^5 to 2^26 below fp32's largest value: what bounds
+    their rows passes it, the rows themselves do not."""
+    t, gy, gf = inputs([-0.01] * 200, K=K, V=V)
+    if part is OUT:
+        t["v"], t["state"] = t["v"] * 2.0 ** size, t["state"] * 2.0 ** size
+    else:
+        gy, gf = gy * 2.0 ** size, gf * 2.0 ** size
+    run(t, gy, gf, part)
