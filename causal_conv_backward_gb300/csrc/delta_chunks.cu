@@ -9,19 +9,20 @@
 //   U = R T^T        Y = e^c S Q^T + R (PT)^T
 //   S = e^c(end) S + (U e^(c(end)-c)) K
 // with tokens along the columns; R is taken without each token's growth, which T's
-// and P T's columns put back (growth_of in delta_prepare.cu). Operands in tensor memory are two fp16 terms of
-// fp32 rows scaled by a power of two, 22 bits; K and Q are exact in fp16 (rows
-// scaled by a power of two), so those products take two terms and those
-// with T and P T three. Sums are fp32.
+// and P T's columns put back (growth_of in delta_prepare.cu). Operands in tensor
+// memory are two fp16 terms of fp32 rows scaled by a power of two, 22 bits; K and Q
+// are exact in fp16 (rows scaled by a power of two), so those products take two
+// terms and those with T and P T three. Sums are fp32.
 //
 // The chunks of one head follow on one another, X - R - U - S, and bound the
 // kernel: the products' time and the conversions between them, for which a
 // scheduler has four warps of rows: 4096 tokens of 8 x 16 heads of 128 x 128 take
-// 247 us, 3.9 us a chunk; q, k, v, y and the factors would take 1.9 at the
+// 243 us, 3.8 us a chunk; q, k, v, y and the factors would take 1.9 at the
 // copy bandwidth. Y is taken in the gaps and leaves through
 // warps of its own. Warps 0 to 15 hold the rows, 16 to 19 write Y, 20 issues the
 // products, 21 copies the tokens of the chunk after the next, 22 to 27 make
-// panels of the next one's.
+// panels of the next one's and look for values that are not finite (looked for by the
+// rows' threads, on the chain, it cost 8 us of 34 over eight chunks).
 #include <limits.h>
 
 #include <utility>
@@ -596,7 +597,8 @@ int32_t chunks_of(const ChunkParams &p, cudaStream_t stream)
 // from the unit matrix; a join passes the states on; a second pass takes all
 // segments at once. In units of a chunk's time, with waves of 152 blocks and two
 // units for each join, the shortest division is taken, if it saves a fifth: 65536
-// tokens of 6 heads of 64 take 3160 us in one piece and 400 us in 25.
+// tokens of 6 heads of 64 take 3160 us in one piece and 418 us in 25 (241 + 36 + 141).
+// Measured at that case only; a join of K = 128 reads four times as much.
 static int64_t waves(int64_t blocks) { return (blocks + kNumSMs - 1) / kNumSMs; }
 
 int32_t delta_segments(int64_t chunks, int64_t heads, int64_t tiles)
@@ -611,9 +613,11 @@ int32_t delta_segments(int64_t chunks, int64_t heads, int64_t tiles)
     return (int32_t)best;
 }
 
-// Prompts of less than half a chunk go token by token. 8 sequences of 16 heads of
-// 128 x 128 take 18 us so and 36 in a chunk at 16 tokens, 32 and 36 at 31, 47 and
-// 36 at 48; with gradients 58 and 85, 83 and 86, 109 and 87.
+// Prompts of less than half a chunk go token by token and take no workspace. 8
+// sequences of 16 heads of 128 x 128 take 16 us so at 16 tokens and 30 at 31, and in a
+// chunk 23 at any number up to 64; with gradients 56 and 81, and 63. The sides are even
+// at about 22 tokens; 64 sequences take 35 us at 4 tokens and 166 at 31, where reading
+// and writing the states would take 20.
 DeltaPlan delta_plan(const mcc1d_delta_args &a, bool back)
 {
     DeltaPlan p = {};

@@ -12,9 +12,10 @@
 // on their way to the end or fade by another: growth_of in delta_prepare.cu) and is
 // multiplied from shared memory; e^c Q is two fp16 terms there. The chain is
 // G - D0 - dR - G, and bounds the kernel; the products with grad_y run in its gaps.
-// 2048 tokens of 8 x 16 heads of 128 x 128 take 193 us, 6 us a chunk, of which the
-// operands of the two tiles that fit beside one another take most: grad_y by rows
-// and by columns, e^c Q in two terms. Warps 0 to 15 hold
+// 2048 tokens of 8 x 16 heads of 128 x 128 take 205 us, 6.4 us a chunk, of which the
+// operands of the two tiles that fit beside one another take most: grad_y with its
+// rows' scales, e^c Q in two terms (one scale for all rows: 216 us with the same
+// registers, 205 with 8 more for the warps that make operands). Warps 0 to 15 hold
 // the rows, 16 to 19 write dR and grad_v, 20 issues the products, 21 copies the
 // tiles, 22 to 27 make operands of them where they lie.
 #include "delta_chunks.cuh"

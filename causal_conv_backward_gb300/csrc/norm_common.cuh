@@ -204,10 +204,13 @@ __device__ __forceinline__ float inverse_root(float v)
 // ------------------------------------------------------------------ which threads
 // Threads for rows of D values: up to 1024 a warp or less, so that sums need
 // shuffles only; above, a block. A thread's values past the row's end cost as much
-// as the others, so a shape is taken up to its full width: 2^27 values in rows of
-// 128, 256, 1024, 2048 and 4096 take 117 to 136 us in the gated norm so, and 212 to
-// 370 in the next wider shape. Rows that cannot be read in 16-byte vectors are read
-// value by value, 172 to 317 us at these widths.
+// as the others: 2^27 values in rows of 128, 256, 1024, 2048 and 4096 take 117 to 136
+// us in the gated norm in shapes of their width, and 212 to 370 in the next wider one.
+// So there is a shape for every power of two, and two between (up to 1536 and 2560),
+// and other widths have up to half of a shape idle. Rows of 513 to 1024 values with an
+// fp32 residual do not fit the residual norm's registers whole (0.7 KB a thread
+// spilled), nor do rows above 8192 in the gradients (0.4 KB). Rows that cannot be read
+// in 16-byte vectors are read value by value, 172 to 317 us at these widths.
 template <class F>
 int32_t with_row_shape(int64_t D, bool vectors, F &&f)
 {

@@ -40,14 +40,31 @@
  *    their element. Outputs must not overlap inputs or each other (a step's
  *    `state` is both). The library allocates nothing and keeps nothing between
  *    calls; what a call needs is in `workspace` (16-byte aligned), sized by the
- *    *_workspace_size call, whose contents on entry are ignored.
+ *    *_workspace_size call, whose contents on entry are ignored. With c chunks of 64
+ *    tokens it is 35840 c B H bytes for prompts (none below 32 tokens), and 8 S B H V
+ *    + c B H (8 K V + 55296) for gradients: 1.0 GB for 16 K tokens of 16 heads of 128
+ *    x 128. Where B H is small, up to 63 states and K x K matrices of each are added.
  *  - Every call enqueues on `stream` of the current device and returns without
  *    waiting. Results are deterministic: no floating-point atomics, every sum
  *    in an order that depends on the shape only.
  *  - Limits: 1 <= S <= 2^31 - 4096, 1 <= B <= 65535, 1 <= H <= 2^20,
  *    H % G == 0, 1 <= K <= 128, 1 <= V <= 1024, and B*H*V*K, B*H*V and a
- *    grid's blocks below 2^31. A decay above one is taken, as long as 64 tokens
- *    together grow a state by less than 2^126.
+ *    grid's blocks below 2^31; scale is a number in fp32.
+ *  - Range: a decay above one is taken, as long as 64 tokens together grow a state
+ *    by less than 2^126; a token's decay counts as 2^-255 at least. Prompts of 32
+ *    tokens or more go in chunks of 64 through the tensor cores, in rows of 22 bits:
+ *    a row of a state keeps its accuracy beside louder rows, and while it grows, or
+ *    fades by up to 2^34 in a chunk. What is left of it, of a value or of grad_y
+ *    after it has faded by more within one chunk, with nothing added since, is off
+ *    by up to 2^-57 of what it was (a gradient of the state on its way through the
+ *    chunk by its own rounding, however small it has become). Values below 2^-100
+ *    are off by up to 2^-125, keys of one token by 2^-40 of the largest of them.
+ *    Squares of q and k (MCC1D_QK_NORM) are summed in fp32.
+ *  - Values that are not finite make NaN or infinity of the outputs that depend on
+ *    them, and of no others: of a token's q of its y; of its v of one row of y and
+ *    the state from that token on; of k, delta, beta, A and delta_bias of all rows of
+ *    the head from there on. Gradients hide none, but may be NaN for the chunk of 64
+ *    tokens where the definition's are not yet.
  *
  * Errors as in mcc1d_ssm.h.
  */

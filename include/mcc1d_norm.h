@@ -34,7 +34,8 @@
  *    that depends on the shape only.
  *  - Limits: 1 <= S <= 2^31 - 4096, 1 <= B <= 65535, 1 <= H <= 2^20, rows
  *    (S*B*H of the gated norm, S*B of the residual norm) below 2^31, and rows
- *    of 1 to 16384 values; eps finite and not negative.
+ *    of 1 to 16384 values; eps finite and not negative. Squares are summed in
+ *    fp32: rows of values above some 1e18 / sqrt(their number) are past it.
  *
  * Errors as in mcc1d_ssm.h.
  */
