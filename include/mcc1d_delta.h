@@ -53,11 +53,11 @@
  *  - Range: a decay above one is taken, as long as 64 tokens together grow a state
  *    by less than 2^126; a token's decay counts as 2^-255 at least. Prompts of 32
  *    tokens or more go in chunks of 64 through the tensor cores, in rows of 22 bits.
- *    With growth, outputs are as accurate as what the decays alone make of states
- *    and values, also where keys overwrite most of it token by token (one key, or
- *    few); b |k|^2 above 2, which turns a state over on itself, is growth too.
- *    A row of a state keeps its accuracy beside louder rows, and while it fades by up
- *    to 2^34 in a chunk. What is left of it, of a value or of grad_y
+ *    With growth, outputs are off by the rounding of what the decays alone would
+ *    make of states and values, also where keys overwrite most of it token by token
+ *    (one key, or few); b |k|^2 above 2, which turns a state over on itself, is
+ *    growth too. A row of a state keeps its accuracy beside louder rows, and while
+ *    it fades by up to 2^34 in a chunk. What is left of it, of a value or of grad_y
  *    after it has faded by more within one chunk, with nothing added since, is off
  *    by up to 2^-57 of what it was (a gradient of the state on its way through the
  *    chunk by its own rounding, however small it has become). Values below 2^-100
